@@ -206,16 +206,20 @@ def _plain_gate(st):
     l, s = _plain_scores(st["logits"], c["score"])
     bias = st["bias"]
     v = s if bias is None else s + bias.double()
+    v = v.masked_fill(l == -math.inf, -math.inf)
     rank = l if bias is None else v
     if c["n_group"] > 1:
         size = E // c["n_group"]
         best = v.view(T, c["n_group"], size).sort(dim=2, descending=True).values
-        groups = best[:, :, :c["group_topk"]].sum(dim=2)
+        groups = best[:, :, :c["group_topk"]].clone()
+        groups[:, :, 1:].masked_fill_(groups[:, :, 1:] == -math.inf, 0.0)
+        groups = groups.sum(dim=2)
         kept = groups.sort(dim=1, descending=True, stable=True).indices[:, :c["topk_group"]]
         keep = torch.zeros((T, c["n_group"]), dtype=torch.bool, device=l.device)
         keep.scatter_(1, kept, True)
-        out = ~keep.repeat_interleave(size, dim=1)
-        rank = rank.masked_fill(out, -math.inf)
+        # what is masked ranks last, and before what its group excludes
+        rank = rank.masked_fill(rank == -math.inf, -1e308)
+        rank = rank.masked_fill(~keep.repeat_interleave(size, dim=1), -math.inf)
     ids = rank.sort(dim=1, descending=True, stable=True).indices[:, :k]
     _, w = _plain_weights(l, s, c, ids, None if bias is None else bias[ids])
     counts = torch.bincount(ids.reshape(-1), minlength=E)
