@@ -517,6 +517,200 @@ moe_status moe_expert_backward_mxfp8(const void* dy, const void* x, const uint8_
                                      float* dprobs, int accumulate_dw, void* workspace,
                                      size_t ws_bytes, const moe_config* cfg, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Operators of the layer around the block: the balanced gate, the norms
+ * before and after the block, and the clip of all gradients by one norm.
+ * The pages name them without spelling them out (the gate as the first part
+ * of a training step, the fused norm + residual of the MindSpeed article);
+ * the formulas are stated here in full. All of them are deterministic: the
+ * same inputs give the same bits, and no result depends on an atomic's order.
+ * ------------------------------------------------------------------------ */
+
+/* Element types of the arguments that come in more than one. */
+typedef enum moe_type { MOE_TYPE_F32 = 0, MOE_TYPE_BF16 = 1 } moe_type;
+
+typedef enum moe_score { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+
+/* How the gate scores, chooses and weighs. moe_gate_config_init() fills the
+ * defaults: softmax, one group, renormalised, scale 1 (the gate of
+ * moe_route_topk); a NULL pointer means the defaults. */
+typedef struct moe_gate_config {
+  int score;        /* moe_score                                                        */
+  int n_group;      /* equal groups of consecutive experts: divides E, 1..32             */
+  int topk_group;   /* groups kept: 1..n_group, with topk_group * (E / n_group) >= k     */
+  int group_topk;   /* 1 or 2: best experts of a group that make its score               */
+  int renormalise;  /* 1: the weights sum to scale; 0: the scores themselves times scale */
+  float scale;      /* factor of the weights (finite)                                   */
+} moe_gate_config;
+
+void moe_gate_config_init(moe_gate_config* cfg);
+
+/* ------------------------------------------------------------------------
+ * moe_route_gate - top-k gate with softmax or sigmoid scores, a bias for
+ * balance, groups and renormalised weights, with the counts and offsets of
+ * the choice. For every token, in exact arithmetic:
+ *   l_e = the logit (NaN counts as -inf, +inf as the largest float)
+ *   s_e = 1 / (1 + exp(-l_e)), or exp(l_e) / sum_i exp(l_i)
+ *   v_e = s_e + bias_e; -inf (masked) where l_e is -inf or bias_e is -inf or
+ *         NaN (a bias of +inf counts as the largest float)
+ *   groups: each scores the sum of its group_topk largest unmasked v_e
+ *         (-inf with none); the topk_group largest scores are kept
+ *   ids = the k largest v_e of the kept groups in descending order; without
+ *         a bias the k largest l_e
+ *   w_j = scale * s_j, or scale * s_j / sum_i s_i over the chosen; a masked
+ *         expert (chosen only when no other is left) has s_j = 0, and
+ *         weights without a positive sum are 0
+ * Ties go to the lower index, of experts and of groups. The order is that of
+ * the values in double: where float cannot tell two of them apart, the
+ * kernel computes them in double. The bias enters the choice only.
+ *
+ *  logits      float or bf16 [T, E] (logits_type, a moe_type), aligned to its
+ *              element
+ *  bias        float [E] or NULL
+ *  expert_ids  int32 [T, k]   out
+ *  probs       float [T, k]   out: w
+ *  counts      int32 [E], offsets int32 [E + 1]   out, as moe_counts
+ *  workspace   >= moe_route_gate_workspace_size(T, k, E) bytes, 16-byte
+ *              aligned; every call overwrites what it uses
+ * Requires 1 <= k <= E <= 1024, k <= 32 and T * k < 2^31. T = 0 gives zero
+ * counts and offsets. Never reports a device error.
+ * ------------------------------------------------------------------------ */
+size_t moe_route_gate_workspace_size(int64_t T, int k, int E);
+moe_status moe_route_gate(const void* logits, int logits_type, const float* bias, int64_t T, int E,
+                          int k, const moe_gate_config* cfg, int32_t* expert_ids, float* probs,
+                          int32_t* counts, int32_t* offsets, void* workspace, size_t ws_bytes,
+                          void* stream);
+
+/* ------------------------------------------------------------------------
+ * moe_route_gate_backward - the gradient of the gate's weights with respect
+ * to its logits, for the choice that the forward made (the choice itself has
+ * no gradient, and the bias none at all). With u_j = w_j / scale and
+ * d = sum_j dprobs_j u_j over the chosen:
+ *   softmax, renormalised   dl_j = scale u_j (dprobs_j - d)
+ *   sigmoid, renormalised   dl_j = scale u_j (1 - s_j) (dprobs_j - d)
+ *   sigmoid                 dl_j = scale s_j (1 - s_j) dprobs_j
+ *   softmax                 dl_e = scale s_e ([e chosen] dprobs_e - d), every e
+ * and 0 where nothing is said. A masked slot has no gradient.
+ *
+ *  dprobs      float [T, k]
+ *  logits, logits_type, bias, expert_ids: as the forward had and wrote them
+ *  cfg         the forward's (its groups are not read)
+ *  dlogits     [T, E] of the logits' type   out, every element written
+ * An id outside [0, E) has no gradient and raises MOE_ERR_BAD_EXPERT_ID.
+ * Same limits as moe_route_gate. T = 0 does nothing.
+ * ------------------------------------------------------------------------ */
+moe_status moe_route_gate_backward(const float* dprobs, const void* logits, int logits_type,
+                                   const float* bias, const int32_t* expert_ids, int64_t T, int E,
+                                   int k, const moe_gate_config* cfg, void* dlogits, void* stream);
+
+/* Scalars and types of the norms around the block. moe_norm_config_init()
+ * fills the defaults: eps 1e-6, both scales 1, a bf16 stream and bf16
+ * weights; a NULL pointer means the defaults. */
+typedef struct moe_norm_config {
+  float eps;             /* >= 0, added to the mean square                     */
+  float residual_scale;  /* a: factor of the residual stream                   */
+  float branch_scale;    /* b: factor of the block's output                    */
+  int stream_type;       /* moe_type of x, out, d_out and dx                   */
+  int weight_type;       /* moe_type of w_post, gate and w_next                */
+} moe_norm_config;
+
+void moe_norm_config_init(moe_norm_config* cfg);
+
+/* ------------------------------------------------------------------------
+ * moe_norm_residual - the norm after the block, its gate, the scaled
+ * residual and the norm before the next block, in one pass:
+ *   z_t   = w_post * y_t * rstd_y_t          (w_post NULL: z_t = y_t)
+ *   out_t = a x_t + b g_t * z_t              (gate NULL: g_t = 1)
+ *   n_t   = w_next * out_t * rstd_out_t      (w_next NULL: not computed)
+ *   rstd_y_t = 1 / sqrt(mean(y_t^2) + eps), rstd_out_t of out_t likewise
+ * in float, each result rounded once (n and rstd_out come from out before it
+ * is rounded). With y NULL it is the norm alone, of x: n_t = w_next * x_t *
+ * rstd_out_t; w_post, gate and out must then be NULL, and a and b are not used.
+ *
+ *  x       [T, H] residual stream (cfg->stream_type)
+ *  y       bf16 [T, H] the block's output
+ *  w_post, w_next  [H];  gate  [gate_rows, H]  (cfg->weight_type); token t
+ *          takes gate row t / (T / gate_rows): gate_rows = 1 is a gate for
+ *          each channel, the number of sequences one for each of them, T one
+ *          for each token. gate_rows >= 1 divides T (0 with gate NULL).
+ *  out     [T, H] of the stream's type   out; may be x itself
+ *  n       bf16 [T, H]   out
+ *  rstd_y  float [T]     out with w_post, else not written (may be NULL)
+ *  rstd_out float [T]    out with w_next, else not written (may be NULL)
+ * Any H from 1 to 65536; with H % 8 == 0 and at most 16384 (8192 with a
+ * float stream) rows are read once. T = 0 does nothing.
+ * ------------------------------------------------------------------------ */
+moe_status moe_norm_residual(const void* x, const void* y, const void* w_post, const void* gate,
+                             int64_t gate_rows, const void* w_next, int64_t T, int H,
+                             const moe_norm_config* cfg, void* out, void* n, float* rstd_y,
+                             float* rstd_out, void* stream);
+
+/* ------------------------------------------------------------------------
+ * moe_norm_residual_backward - the gradients of moe_norm_residual. With
+ * o_t = out_t rstd_out_t, yh_t = y_t rstd_y_t (w_post NULL: y_t), m(.) the
+ * mean over a row:
+ *   D_t   = d_out_t + rstd_out_t (q_t - o_t m(q_t * o_t)),  q_t = d_n_t * w_next
+ *   dw_next = sum_t d_n_t * o_t
+ *   dx_t  = a D_t                                (y NULL: dx_t = D_t)
+ *   dgate_r = b w_post * sum_t D_t * yh_t        over the tokens of gate row r
+ *   dw_post = b sum_t g_t * D_t * yh_t
+ *   dy_t  = rstd_y_t (p_t - yh_t m(p_t * yh_t)),  p_t = b g_t * w_post * D_t
+ *           (w_post NULL: dy_t = b g_t * D_t)
+ *
+ *  d_out   [T, H] of the stream's type: the gradient of out; NULL: none
+ *  d_n     bf16 [T, H]: the gradient of n (needs w_next); NULL: none. One of
+ *          the two at least is given.
+ *  out     [T, H] the forward's out (with y NULL its x); read with d_n only
+ *  y, w_post, gate, gate_rows, w_next: the forward's
+ *  rstd_y, rstd_out  float [T] as the forward wrote them
+ *  dx      [T, H] of the stream's type   out; may be d_out itself
+ *  dy      bf16 [T, H]                   out (NULL with y NULL)
+ *  dw_post, dw_next float [H], dgate float [gate_rows, H]   out, each where
+ *          its weight is given (dw_next: and d_n); added to what is there
+ *          when accumulate_dw
+ *  workspace >= moe_norm_residual_backward_workspace_size(T, H, gate_rows)
+ *          bytes, 16-byte aligned
+ * Same limits as moe_norm_residual. T = 0 writes zero weight gradients (or
+ * leaves them when accumulating).
+ * ------------------------------------------------------------------------ */
+size_t moe_norm_residual_backward_workspace_size(int64_t T, int H, int64_t gate_rows);
+moe_status moe_norm_residual_backward(const void* d_out, const void* d_n, const void* out,
+                                      const void* y, const void* w_post, const void* gate,
+                                      int64_t gate_rows, const void* w_next, const float* rstd_y,
+                                      const float* rstd_out, int64_t T, int H,
+                                      const moe_norm_config* cfg, void* dx, void* dy,
+                                      float* dw_post, float* dgate, float* dw_next,
+                                      int accumulate_dw, void* workspace, size_t ws_bytes,
+                                      void* stream);
+
+/* ------------------------------------------------------------------------
+ * moe_clip_grad_norm - one norm over many gradients, and all of them scaled
+ * by it: with norm = sqrt(sum of all g^2) (norm_kind 0) or max |g| (1),
+ *   coef = min(1, max_norm / (norm + eps)),   g <- g * coef
+ * A NaN among the gradients gives norm = coef = NaN, an infinity norm = inf
+ * and coef = 0 (so that finite gradients become 0 and infinite ones NaN).
+ * With max_norm < 0 only the norm is computed (coef = 1).
+ *
+ *  grads    HOST array of n_tensors device pointers, each aligned to its
+ *           element; the arrays are read before the call returns
+ *  outs     HOST array of n_tensors device pointers of the same types, or
+ *           NULL: in place. In place nothing is written when coef = 1; out of
+ *           place every element is. outs[i] is grads[i] or overlaps no input.
+ *  numels   HOST array of element counts (>= 0; 0 allows a null pointer)
+ *  types    HOST array of moe_type
+ *  norm_coef float [2] device memory   out: norm, coef
+ *  workspace >= moe_clip_grad_norm_workspace_size() bytes, 16-byte aligned;
+ *           every call overwrites what it uses
+ * n_tensors <= 1048576. Squares are summed in float over short runs and in
+ * double beyond: elements between 1e-18 and 1e18 in magnitude count in full.
+ * No tensors, or only empty ones: norm = 0, coef = min(1, max_norm / eps).
+ * ------------------------------------------------------------------------ */
+size_t moe_clip_grad_norm_workspace_size(void);
+moe_status moe_clip_grad_norm(const void* const* grads, void* const* outs, const int64_t* numels,
+                              const int* types, int64_t n_tensors, float max_norm, int norm_kind,
+                              float eps, float* norm_coef, void* workspace, size_t ws_bytes,
+                              void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -7,7 +7,9 @@ fallback: importing this package without the built library raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import math
 import os
 
 import torch
@@ -49,6 +51,19 @@ class moe_config(ctypes.Structure):
                 ("mxfp8_tile_n", ctypes.c_int),
                 ("cta_pairs", ctypes.c_int),
                 ("mx_scales_pretiled", ctypes.c_int)]
+
+
+class moe_gate_config(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int), ("n_group", ctypes.c_int), ("topk_group", ctypes.c_int),
+                ("group_topk", ctypes.c_int), ("renormalise", ctypes.c_int),
+                ("scale", ctypes.c_float)]
+
+
+class moe_norm_config(ctypes.Structure):
+    _fields_ = [("eps", ctypes.c_float), ("residual_scale", ctypes.c_float),
+                ("branch_scale", ctypes.c_float), ("stream_type", ctypes.c_int),
+                ("weight_type", ctypes.c_int)]
+
 
 STEP_EVENTS = 5       # forward: start, routing, fc1+SwiGLU, fc2, unpermute
 BWD_STEP_EVENTS = 7   # backward: start, dO+dprobs, dH, dXp, dX, dW1, dW2
@@ -100,6 +115,22 @@ _sig("moe_expert_forward_mxfp8", _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _
      _i32, _i32, _i32, _vp, _vp, _sz, ctypes.POINTER(moe_config), _vp)
 _sig("moe_tile_weight_scales_mxfp8", _i32, _vp, _vp, _vp, _i32, _i32, _i32,
      ctypes.POINTER(moe_config), _vp, _vp, _vp)
+
+_sig("moe_gate_config_init", None, ctypes.POINTER(moe_gate_config))
+_sig("moe_route_gate_workspace_size", _sz, _i64, _i32, _i32)
+_sig("moe_route_gate", _i32, _vp, _i32, _vp, _i64, _i32, _i32, ctypes.POINTER(moe_gate_config),
+     _vp, _vp, _vp, _vp, _vp, _sz, _vp)
+_sig("moe_route_gate_backward", _i32, _vp, _vp, _i32, _vp, _vp, _i64, _i32, _i32,
+     ctypes.POINTER(moe_gate_config), _vp, _vp)
+_sig("moe_norm_config_init", None, ctypes.POINTER(moe_norm_config))
+_sig("moe_norm_residual", _i32, _vp, _vp, _vp, _vp, _i64, _vp, _i64, _i32,
+     ctypes.POINTER(moe_norm_config), _vp, _vp, _vp, _vp, _vp)
+_sig("moe_norm_residual_backward_workspace_size", _sz, _i64, _i32, _i64)
+_sig("moe_norm_residual_backward", _i32, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _i64,
+     _i32, ctypes.POINTER(moe_norm_config), _vp, _vp, _vp, _vp, _vp, _i32, _vp, _sz, _vp)
+_sig("moe_clip_grad_norm_workspace_size", _sz)
+_sig("moe_clip_grad_norm", _i32, ctypes.POINTER(_vp), ctypes.POINTER(_vp), ctypes.POINTER(_i64),
+     ctypes.POINTER(_i32), _i64, ctypes.c_float, _i32, ctypes.c_float, _vp, _vp, _sz, _vp)
 
 
 class MoeError(RuntimeError):
@@ -695,3 +726,307 @@ def moe_expert_backward_mxfp8(dy, x, w1g_q, w1g_s, w1u_q, w1u_s, w2_q, w2_s, exp
                                               ctypes.byref(c), _stream(stream, dev)),
                "moe_expert_backward_mxfp8")
     return dict(dx=dx, dw_gate_t=dw_gate_t, dw_up_t=dw_up_t, dw_down_t=dw_down_t, dprobs=dprobs)
+
+
+# ------------------------------------------------------------------ the layer around the block
+
+_TYPES = {torch.float32: 0, torch.bfloat16: 1}
+_SCORES = {"softmax": 0, "sigmoid": 1}
+_NO_GUARD = contextlib.nullcontext()
+
+
+def _guard(dev):
+    """Makes dev current for the call; free where it is already."""
+    return _NO_GUARD if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream, dev):
+    """_stream as a plain integer."""
+    if stream is None:
+        return torch.cuda.current_stream(dev).cuda_stream
+    if stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+    return stream.cuda_stream
+
+
+def _typed(t, name):
+    """The moe_type of a tensor that may be float32 or bfloat16."""
+    code = _TYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be torch.float32 or torch.bfloat16, got {t.dtype}")
+    return code
+
+
+def _shaped(t, name, *shape):
+    if t is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+
+
+def _gate_config(score, n_group, topk_group, group_topk, renormalise, scale):
+    if score not in _SCORES:
+        raise ValueError(f"score must be 'softmax' or 'sigmoid', got {score!r}")
+    return moe_gate_config(_SCORES[score], n_group, topk_group, group_topk, bool(renormalise),
+                           scale)
+
+
+def moe_route_gate(logits: torch.Tensor, k: int, bias=None, score="softmax", n_group=1,
+                   topk_group=1, group_topk=1, renormalise=True, scale=1.0, expert_ids=None,
+                   probs=None, counts=None, offsets=None, workspace=None, stream=None):
+    """The top-k gate with softmax or sigmoid scores, a balance bias float32 [E]
+    that enters the choice only, groups (the topk_group of n_group groups with
+    the largest sum of their group_topk best experts) and weights that are
+    renormalised over the chosen and scaled: (expert_ids int32 [T, k], probs
+    float32 [T, k], counts int32 [E], offsets int32 [E+1]) of float32 or
+    bfloat16 logits [T, E]."""
+    _cuda(logits, "logits")
+    lt = _typed(logits, "logits")
+    T, E = logits.shape
+    _cuda(bias, "bias", torch.float32)
+    _shaped(bias, "bias", E)
+    _cuda(expert_ids, "expert_ids", torch.int32, T * k)
+    _cuda(probs, "probs", torch.float32, T * k)
+    _cuda(counts, "counts", torch.int32, E)
+    _cuda(offsets, "offsets", torch.int32, E + 1)
+    _cuda(workspace, "workspace")
+    dev = _device(("logits", logits), ("bias", bias), ("expert_ids", expert_ids),
+                  ("probs", probs), ("counts", counts), ("offsets", offsets),
+                  ("workspace", workspace))
+    cfg = _gate_config(score, n_group, topk_group, group_topk, renormalise, scale)
+    with _guard(dev):
+        if expert_ids is None:
+            expert_ids = torch.empty((T, max(k, 0)), dtype=torch.int32, device=dev)
+        if probs is None:
+            probs = torch.empty((T, max(k, 0)), dtype=torch.float32, device=dev)
+        if counts is None:
+            counts = torch.empty(E, dtype=torch.int32, device=dev)
+        if offsets is None:
+            offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
+        if workspace is None:
+            workspace = _workspace(_lib.moe_route_gate_workspace_size(T, k, E), dev)
+        _check(_lib.moe_route_gate(logits.data_ptr(), lt, _ptr(bias), T, E, k, cfg,
+                                   expert_ids.data_ptr(), probs.data_ptr(), counts.data_ptr(),
+                                   offsets.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+                                   _raw_stream(stream, dev)), "moe_route_gate")
+    return expert_ids, probs, counts, offsets
+
+
+def moe_route_gate_backward(dprobs, logits, expert_ids, bias=None, score="softmax",
+                            renormalise=True, scale=1.0, dlogits=None, stream=None):
+    """dlogits [T, E], of the logits' type, of moe_route_gate's weights for the
+    choice expert_ids that it made; bias, score, renormalise and scale as there."""
+    _cuda(dprobs, "dprobs", torch.float32)
+    _cuda(logits, "logits")
+    lt = _typed(logits, "logits")
+    _cuda(expert_ids, "expert_ids", torch.int32)
+    T, E = logits.shape
+    k = expert_ids.shape[1]
+    _shaped(expert_ids, "expert_ids", T, k)
+    _shaped(dprobs, "dprobs", T, k)
+    _cuda(bias, "bias", torch.float32)
+    _shaped(bias, "bias", E)
+    _cuda(dlogits, "dlogits", logits.dtype, T * E)
+    dev = _device(("dprobs", dprobs), ("logits", logits), ("expert_ids", expert_ids),
+                  ("bias", bias), ("dlogits", dlogits))
+    cfg = _gate_config(score, 1, 1, 1, renormalise, scale)
+    with _guard(dev):
+        dlogits = torch.empty_like(logits) if dlogits is None else dlogits
+        _check(_lib.moe_route_gate_backward(dprobs.data_ptr(), logits.data_ptr(), lt, _ptr(bias),
+                                            expert_ids.data_ptr(), T, E, k, cfg,
+                                            dlogits.data_ptr(), _raw_stream(stream, dev)),
+               "moe_route_gate_backward")
+    return dlogits
+
+
+def _norm_weights(H, **named):
+    """(moe_type of the weights, rows of the gate) of the given w_post, gate, w_next."""
+    wt, first = None, None
+    for name, t in named.items():
+        if t is None:
+            continue
+        _cuda(t, name)
+        code = _typed(t, name)
+        if wt is not None and code != wt:
+            raise ValueError(f"{name} is {t.dtype} but {first} is not: the weights share one type")
+        wt, first = code, name
+        if name != "gate":
+            _shaped(t, name, H)
+        elif t.dim() not in (1, 2) or t.shape[-1] != H:
+            raise ValueError(f"gate must have shape [{H}] or [rows, {H}], got {list(t.shape)}")
+    gate = named["gate"]
+    return (1 if wt is None else wt,
+            0 if gate is None else 1 if gate.dim() == 1 else gate.shape[0])
+
+
+def moe_norm_residual(x, y=None, w_post=None, gate=None, w_next=None, eps=1e-6,
+                      residual_scale=1.0, branch_scale=1.0, out=None, n=None, rstd_y=None,
+                      rstd_out=None, stream=None):
+    """The norm after the block, its gate, the scaled residual and the norm
+    before the next block in one pass over x [T, H] (float32 or bfloat16) and
+    the block's output y (bfloat16 [T, H]):
+      out = residual_scale * x + branch_scale * gate * (w_post * rmsnorm(y))
+      n = w_next * rmsnorm(out)
+    Without w_post y enters as it is, without gate (of [H], or [rows, H] with T
+    / rows consecutive tokens to a row) it is 1, without w_next n is left out.
+    Without y it is the norm alone, of x. Returns dict(out, n, rstd_y,
+    rstd_out), None where nothing was computed; out may be x itself."""
+    _cuda(x, "x")
+    st = _typed(x, "x")
+    T, H = x.shape
+    _cuda(y, "y", torch.bfloat16)
+    _shaped(y, "y", T, H)
+    wt, rows = _norm_weights(H, w_post=w_post, gate=gate, w_next=w_next)
+    _cuda(out, "out", x.dtype, T * H)
+    _cuda(n, "n", torch.bfloat16, T * H)
+    _cuda(rstd_y, "rstd_y", torch.float32, T)
+    _cuda(rstd_out, "rstd_out", torch.float32, T)
+    dev = _device(("x", x), ("y", y), ("w_post", w_post), ("gate", gate), ("w_next", w_next),
+                  ("out", out), ("n", n), ("rstd_y", rstd_y), ("rstd_out", rstd_out))
+    cfg = moe_norm_config(eps, residual_scale, branch_scale, st, wt)
+    with _guard(dev):
+        if y is None:
+            out = None
+        elif out is None:
+            out = torch.empty_like(x)
+        if w_post is None:
+            rstd_y = None
+        elif rstd_y is None:
+            rstd_y = torch.empty(T, dtype=torch.float32, device=dev)
+        if w_next is None:
+            n = rstd_out = None
+        else:
+            if n is None:
+                n = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+            if rstd_out is None:
+                rstd_out = torch.empty(T, dtype=torch.float32, device=dev)
+        _check(_lib.moe_norm_residual(x.data_ptr(), _ptr(y), _ptr(w_post), _ptr(gate), rows,
+                                      _ptr(w_next), T, H, cfg, _ptr(out), _ptr(n), _ptr(rstd_y),
+                                      _ptr(rstd_out), _raw_stream(stream, dev)),
+               "moe_norm_residual")
+    return dict(out=out, n=n, rstd_y=rstd_y, rstd_out=rstd_out)
+
+
+def moe_norm_residual_backward(d_out, d_n, out, y=None, w_post=None, gate=None, w_next=None,
+                               rstd_y=None, rstd_out=None, eps=1e-6, residual_scale=1.0,
+                               branch_scale=1.0, dx=None, dy=None, dw_post=None, dgate=None,
+                               dw_next=None, accumulate_dw=False, workspace=None, stream=None):
+    """Gradients of moe_norm_residual from d_out (of x's type) and d_n
+    (bfloat16), either of them None for no gradient. out is the forward's (its
+    x where y is None); y, the weights, rstd_y, rstd_out and the scalars are the
+    forward's. Returns dict(dx, dy, dw_post, dgate, dw_next), the last three in
+    float32 and, with accumulate_dw, added to what the given tensors hold; None
+    where there is no such input. dx may be d_out itself."""
+    _cuda(out, "out")
+    st = _typed(out, "out")
+    T, H = out.shape
+    _cuda(d_out, "d_out", out.dtype)
+    _shaped(d_out, "d_out", T, H)
+    _cuda(d_n, "d_n", torch.bfloat16)
+    _shaped(d_n, "d_n", T, H)
+    _cuda(y, "y", torch.bfloat16)
+    _shaped(y, "y", T, H)
+    wt, rows = _norm_weights(H, w_post=w_post, gate=gate, w_next=w_next)
+    for t, name in ((rstd_y, "rstd_y"), (rstd_out, "rstd_out")):
+        _cuda(t, name, torch.float32, T)
+    _cuda(dx, "dx", out.dtype, T * H)
+    _cuda(dy, "dy", torch.bfloat16, T * H)
+    for t, name, m in ((dw_post, "dw_post", H), (dgate, "dgate", rows * H),
+                       (dw_next, "dw_next", H)):
+        _cuda(t, name, torch.float32, m)
+    _cuda(workspace, "workspace")
+    dev = _device(("out", out), ("d_out", d_out), ("d_n", d_n), ("y", y), ("w_post", w_post),
+                  ("gate", gate), ("w_next", w_next), ("rstd_y", rstd_y),
+                  ("rstd_out", rstd_out), ("dx", dx), ("dy", dy), ("dw_post", dw_post),
+                  ("dgate", dgate), ("dw_next", dw_next), ("workspace", workspace))
+    if accumulate_dw and any(w is not None and g is None for w, g in (
+            (w_post, dw_post), (gate, dgate), (w_next if d_n is not None else None, dw_next))):
+        raise ValueError("accumulate_dw adds to dw_post, dgate and dw_next: pass them")
+    cfg = moe_norm_config(eps, residual_scale, branch_scale, st, wt)
+    f32 = dict(dtype=torch.float32, device=dev)
+    with _guard(dev):
+        dx = torch.empty_like(out) if dx is None else dx
+        if y is None:
+            dy = None
+        elif dy is None:
+            dy = torch.empty_like(y)
+        if w_post is None:
+            dw_post = None
+        elif dw_post is None:
+            dw_post = torch.empty(H, **f32)
+        if gate is None:
+            dgate = None
+        elif dgate is None:
+            dgate = torch.empty(gate.shape, **f32)
+        if w_next is None or d_n is None:
+            dw_next = None
+        elif dw_next is None:
+            dw_next = torch.empty(H, **f32)
+        if workspace is None:
+            workspace = _workspace(
+                _lib.moe_norm_residual_backward_workspace_size(T, H, rows), dev)
+        _check(_lib.moe_norm_residual_backward(
+            _ptr(d_out), _ptr(d_n), out.data_ptr(), _ptr(y), _ptr(w_post), _ptr(gate), rows,
+            _ptr(w_next), _ptr(rstd_y), _ptr(rstd_out), T, H, cfg, dx.data_ptr(), _ptr(dy),
+            _ptr(dw_post), _ptr(dgate), _ptr(dw_next), bool(accumulate_dw), workspace.data_ptr(),
+            workspace.nbytes, _raw_stream(stream, dev)), "moe_norm_residual_backward")
+    return dict(dx=dx, dy=dy, dw_post=dw_post, dgate=dgate, dw_next=dw_next)
+
+
+def moe_clip_grad_norm(grads, max_norm, out=None, norm_type=2.0, eps=1e-6, norm_coef=None,
+                       workspace=None, stream=None):
+    """One norm over a list of gradients (float32 or bfloat16, contiguous), and
+    every one of them scaled by coef = min(1, max_norm / (norm + eps)): in place,
+    or into the tensors of the list out (same types and sizes). norm_type is 2.0
+    or math.inf; max_norm None computes the norm alone. Returns (norm, coef), two
+    float32 tensors of one element; nothing is read back to the host."""
+    grads = list(grads)
+    if norm_type not in (2.0, math.inf):
+        raise ValueError(f"norm_type must be 2.0 or inf, got {norm_type}")
+    if max_norm is not None and not max_norm >= 0:
+        raise ValueError(f"max_norm must be None or >= 0, got {max_norm}")
+    if max_norm is None and out is not None:
+        raise ValueError("out is written when gradients are clipped: max_norm is None")
+    dev = grads[0].device if grads else None if norm_coef is None else norm_coef.device
+    if dev is None:
+        raise ValueError("no gradients: pass norm_coef to say where the norm goes")
+    for i, g in enumerate(grads):
+        if g.dtype not in _TYPES or g.device != dev or not g.is_contiguous():
+            raise ValueError(f"grads[{i}] must be a contiguous float32 or bfloat16 tensor on {dev}")
+    if dev.type != "cuda":
+        raise ValueError("grads must be CUDA tensors")
+    n = len(grads)
+    outs = None
+    if out is not None:
+        out = list(out)
+        if len(out) != n:
+            raise ValueError(f"out holds {len(out)} tensors, grads {n}")
+        for i, (g, o) in enumerate(zip(grads, out)):
+            if o.dtype != g.dtype or o.device != dev or not o.is_contiguous() or \
+                    o.numel() != g.numel():
+                raise ValueError(f"out[{i}] must be as grads[{i}]: same type, device and size")
+        outs = (_vp * n)(*[o.data_ptr() for o in out])
+    _cuda(norm_coef, "norm_coef", torch.float32, 2)
+    _cuda(workspace, "workspace")
+    _device(("grads", grads[0] if grads else None), ("norm_coef", norm_coef),
+            ("workspace", workspace))
+    with _guard(dev):
+        if norm_coef is None:
+            norm_coef = torch.empty(2, dtype=torch.float32, device=dev)
+        if workspace is None:
+            workspace = _workspace(_lib.moe_clip_grad_norm_workspace_size(), dev)
+        _check(_lib.moe_clip_grad_norm(
+            (_vp * n)(*[g.data_ptr() for g in grads]), outs,
+            (_i64 * n)(*[g.numel() for g in grads]), (_i32 * n)(*[_TYPES[g.dtype] for g in grads]),
+            n, -1.0 if max_norm is None else max_norm, int(norm_type == math.inf), eps,
+            norm_coef.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+            _raw_stream(stream, dev)), "moe_clip_grad_norm")
+    return norm_coef[0:1], norm_coef[1:2]
+
+
+def moe_grad_norm(grads, norm_type=2.0, norm_coef=None, workspace=None, stream=None):
+    """The norm alone of a list of gradients: a float32 tensor of one element."""
+    return moe_clip_grad_norm(grads, None, norm_type=norm_type, norm_coef=norm_coef,
+                              workspace=workspace, stream=stream)[0]
