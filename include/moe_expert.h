@@ -571,7 +571,8 @@ void moe_gate_config_init(moe_gate_config* cfg);
  *  probs       float [T, k]   out: w
  *  counts      int32 [E], offsets int32 [E + 1]   out, as moe_counts
  *  workspace   >= moe_route_gate_workspace_size(T, k, E) bytes, 16-byte
- *              aligned; every call overwrites what it uses
+ *              aligned; every call overwrites what it uses. 0 bytes, and NULL
+ *              allowed, for the small batches that one cluster counts
  * Requires 1 <= k <= E <= 1024, k <= 32 and T * k < 2^31. T = 0 gives zero
  * counts and offsets. Never reports a device error.
  * ------------------------------------------------------------------------ */

@@ -7,7 +7,6 @@ fallback: importing this package without the built library raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import os
@@ -732,12 +731,30 @@ def moe_expert_backward_mxfp8(dy, x, w1g_q, w1g_s, w1u_q, w1u_s, w2_q, w2_s, exp
 
 _TYPES = {torch.float32: 0, torch.bfloat16: 1}
 _SCORES = {"softmax": 0, "sigmoid": 1}
-_NO_GUARD = contextlib.nullcontext()
+# the current stream of a device as an integer, without a Stream object
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _guard(dev):
-    """Makes dev current for the call; free where it is already."""
-    return _NO_GUARD if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+def _fit(dev, *named):
+    """Checks (tensor or None, name, dtype, least number of elements) on dev:
+    these calls are short, so one pass looks at everything and the messages
+    are made only where something is wrong."""
+    index = dev.index
+    for t, name, dtype, least in named:
+        if t is not None and (t.get_device() != index or t.dtype != dtype
+                              or not t.is_contiguous() or t.numel() < least):
+            _cuda(t, name, dtype, least)
+            raise ValueError(f"{name} is on {t.device} but the call's first tensor on {dev}: "
+                             "all tensors of a call must share one device")
+
+
+def _on(dev, fn, *args):
+    """fn(*args) with dev current."""
+    if dev.index == torch.cuda.current_device():
+        return fn(*args)
+    with torch.cuda.device(dev):
+        return fn(*args)
 
 
 def _ptr(t):
@@ -747,10 +764,20 @@ def _ptr(t):
 def _raw_stream(stream, dev):
     """_stream as a plain integer."""
     if stream is None:
-        return torch.cuda.current_stream(dev).cuda_stream
+        return _current_raw_stream(dev.index)
     if stream.device != dev:
         raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
     return stream.cuda_stream
+
+
+def _scratch(workspace, need, dev):
+    """(the given workspace or a new one, its bytes); None where none is needed."""
+    if workspace is not None:
+        _fit(dev, (workspace, "workspace", workspace.dtype, 0))
+        return workspace, workspace.nbytes
+    if not need:
+        return None, 0
+    return torch.empty(need, dtype=torch.uint8, device=dev), need
 
 
 def _typed(t, name):
@@ -782,35 +809,26 @@ def moe_route_gate(logits: torch.Tensor, k: int, bias=None, score="softmax", n_g
     renormalised over the chosen and scaled: (expert_ids int32 [T, k], probs
     float32 [T, k], counts int32 [E], offsets int32 [E+1]) of float32 or
     bfloat16 logits [T, E]."""
-    _cuda(logits, "logits")
     lt = _typed(logits, "logits")
     T, E = logits.shape
-    _cuda(bias, "bias", torch.float32)
+    dev = logits.device
+    _fit(dev, (logits, "logits", logits.dtype, 0), (bias, "bias", torch.float32, 0),
+         (expert_ids, "expert_ids", torch.int32, T * k), (probs, "probs", torch.float32, T * k),
+         (counts, "counts", torch.int32, E), (offsets, "offsets", torch.int32, E + 1))
     _shaped(bias, "bias", E)
-    _cuda(expert_ids, "expert_ids", torch.int32, T * k)
-    _cuda(probs, "probs", torch.float32, T * k)
-    _cuda(counts, "counts", torch.int32, E)
-    _cuda(offsets, "offsets", torch.int32, E + 1)
-    _cuda(workspace, "workspace")
-    dev = _device(("logits", logits), ("bias", bias), ("expert_ids", expert_ids),
-                  ("probs", probs), ("counts", counts), ("offsets", offsets),
-                  ("workspace", workspace))
     cfg = _gate_config(score, n_group, topk_group, group_topk, renormalise, scale)
-    with _guard(dev):
-        if expert_ids is None:
-            expert_ids = torch.empty((T, max(k, 0)), dtype=torch.int32, device=dev)
-        if probs is None:
-            probs = torch.empty((T, max(k, 0)), dtype=torch.float32, device=dev)
-        if counts is None:
-            counts = torch.empty(E, dtype=torch.int32, device=dev)
-        if offsets is None:
-            offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
-        if workspace is None:
-            workspace = _workspace(_lib.moe_route_gate_workspace_size(T, k, E), dev)
-        _check(_lib.moe_route_gate(logits.data_ptr(), lt, _ptr(bias), T, E, k, cfg,
-                                   expert_ids.data_ptr(), probs.data_ptr(), counts.data_ptr(),
-                                   offsets.data_ptr(), workspace.data_ptr(), workspace.nbytes,
-                                   _raw_stream(stream, dev)), "moe_route_gate")
+    if expert_ids is None:
+        expert_ids = torch.empty((T, max(k, 0)), dtype=torch.int32, device=dev)
+    if probs is None:
+        probs = torch.empty((T, max(k, 0)), dtype=torch.float32, device=dev)
+    if counts is None:
+        counts = torch.empty(E, dtype=torch.int32, device=dev)
+    if offsets is None:
+        offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
+    ws, ws_bytes = _scratch(workspace, _lib.moe_route_gate_workspace_size(T, k, E), dev)
+    _check(_on(dev, _lib.moe_route_gate, logits.data_ptr(), lt, _ptr(bias), T, E, k, cfg,
+               expert_ids.data_ptr(), probs.data_ptr(), counts.data_ptr(), offsets.data_ptr(),
+               _ptr(ws), ws_bytes, _raw_stream(stream, dev)), "moe_route_gate")
     return expert_ids, probs, counts, offsets
 
 
@@ -818,47 +836,43 @@ def moe_route_gate_backward(dprobs, logits, expert_ids, bias=None, score="softma
                             renormalise=True, scale=1.0, dlogits=None, stream=None):
     """dlogits [T, E], of the logits' type, of moe_route_gate's weights for the
     choice expert_ids that it made; bias, score, renormalise and scale as there."""
-    _cuda(dprobs, "dprobs", torch.float32)
-    _cuda(logits, "logits")
     lt = _typed(logits, "logits")
-    _cuda(expert_ids, "expert_ids", torch.int32)
     T, E = logits.shape
     k = expert_ids.shape[1]
+    dev = logits.device
+    _fit(dev, (logits, "logits", logits.dtype, 0), (dprobs, "dprobs", torch.float32, 0),
+         (expert_ids, "expert_ids", torch.int32, 0), (bias, "bias", torch.float32, 0),
+         (dlogits, "dlogits", logits.dtype, T * E))
     _shaped(expert_ids, "expert_ids", T, k)
     _shaped(dprobs, "dprobs", T, k)
-    _cuda(bias, "bias", torch.float32)
     _shaped(bias, "bias", E)
-    _cuda(dlogits, "dlogits", logits.dtype, T * E)
-    dev = _device(("dprobs", dprobs), ("logits", logits), ("expert_ids", expert_ids),
-                  ("bias", bias), ("dlogits", dlogits))
     cfg = _gate_config(score, 1, 1, 1, renormalise, scale)
-    with _guard(dev):
-        dlogits = torch.empty_like(logits) if dlogits is None else dlogits
-        _check(_lib.moe_route_gate_backward(dprobs.data_ptr(), logits.data_ptr(), lt, _ptr(bias),
-                                            expert_ids.data_ptr(), T, E, k, cfg,
-                                            dlogits.data_ptr(), _raw_stream(stream, dev)),
-               "moe_route_gate_backward")
+    if dlogits is None:
+        dlogits = torch.empty_like(logits)
+    _check(_on(dev, _lib.moe_route_gate_backward, dprobs.data_ptr(), logits.data_ptr(), lt,
+               _ptr(bias), expert_ids.data_ptr(), T, E, k, cfg, dlogits.data_ptr(),
+               _raw_stream(stream, dev)), "moe_route_gate_backward")
     return dlogits
 
 
-def _norm_weights(H, **named):
-    """(moe_type of the weights, rows of the gate) of the given w_post, gate, w_next."""
-    wt, first = None, None
-    for name, t in named.items():
-        if t is None:
-            continue
-        _cuda(t, name)
-        code = _typed(t, name)
-        if wt is not None and code != wt:
-            raise ValueError(f"{name} is {t.dtype} but {first} is not: the weights share one type")
-        wt, first = code, name
-        if name != "gate":
-            _shaped(t, name, H)
-        elif t.dim() not in (1, 2) or t.shape[-1] != H:
-            raise ValueError(f"gate must have shape [{H}] or [rows, {H}], got {list(t.shape)}")
-    gate = named["gate"]
-    return (1 if wt is None else wt,
-            0 if gate is None else 1 if gate.dim() == 1 else gate.shape[0])
+def _norm_weights(dev, H, w_post, gate, w_next):
+    """(moe_type of the weights, rows of the gate)."""
+    first = w_post if w_post is not None else gate if gate is not None else w_next
+    if first is None:
+        return 1, 0
+    wt = _typed(first, "weights")
+    if any(t is not None and t.dtype != first.dtype for t in (gate, w_next)):
+        raise ValueError("w_post, gate and w_next share one type: got "
+                         f"{[t.dtype for t in (w_post, gate, w_next) if t is not None]}")
+    _fit(dev, (w_post, "w_post", first.dtype, 0), (gate, "gate", first.dtype, 0),
+         (w_next, "w_next", first.dtype, 0))
+    _shaped(w_post, "w_post", H)
+    _shaped(w_next, "w_next", H)
+    if gate is None:
+        return wt, 0
+    if gate.dim() not in (1, 2) or gate.shape[-1] != H:
+        raise ValueError(f"gate must have shape [{H}] or [rows, {H}], got {list(gate.shape)}")
+    return wt, 1 if gate.dim() == 1 else gate.shape[0]
 
 
 def moe_norm_residual(x, y=None, w_post=None, gate=None, w_next=None, eps=1e-6,
@@ -873,39 +887,33 @@ def moe_norm_residual(x, y=None, w_post=None, gate=None, w_next=None, eps=1e-6,
     / rows consecutive tokens to a row) it is 1, without w_next n is left out.
     Without y it is the norm alone, of x. Returns dict(out, n, rstd_y,
     rstd_out), None where nothing was computed; out may be x itself."""
-    _cuda(x, "x")
     st = _typed(x, "x")
     T, H = x.shape
-    _cuda(y, "y", torch.bfloat16)
+    dev = x.device
+    _fit(dev, (x, "x", x.dtype, 0), (y, "y", torch.bfloat16, 0), (out, "out", x.dtype, T * H),
+         (n, "n", torch.bfloat16, T * H), (rstd_y, "rstd_y", torch.float32, T),
+         (rstd_out, "rstd_out", torch.float32, T))
     _shaped(y, "y", T, H)
-    wt, rows = _norm_weights(H, w_post=w_post, gate=gate, w_next=w_next)
-    _cuda(out, "out", x.dtype, T * H)
-    _cuda(n, "n", torch.bfloat16, T * H)
-    _cuda(rstd_y, "rstd_y", torch.float32, T)
-    _cuda(rstd_out, "rstd_out", torch.float32, T)
-    dev = _device(("x", x), ("y", y), ("w_post", w_post), ("gate", gate), ("w_next", w_next),
-                  ("out", out), ("n", n), ("rstd_y", rstd_y), ("rstd_out", rstd_out))
-    cfg = moe_norm_config(eps, residual_scale, branch_scale, st, wt)
-    with _guard(dev):
-        if y is None:
-            out = None
-        elif out is None:
-            out = torch.empty_like(x)
-        if w_post is None:
-            rstd_y = None
-        elif rstd_y is None:
-            rstd_y = torch.empty(T, dtype=torch.float32, device=dev)
-        if w_next is None:
-            n = rstd_out = None
-        else:
-            if n is None:
-                n = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
-            if rstd_out is None:
-                rstd_out = torch.empty(T, dtype=torch.float32, device=dev)
-        _check(_lib.moe_norm_residual(x.data_ptr(), _ptr(y), _ptr(w_post), _ptr(gate), rows,
-                                      _ptr(w_next), T, H, cfg, _ptr(out), _ptr(n), _ptr(rstd_y),
-                                      _ptr(rstd_out), _raw_stream(stream, dev)),
-               "moe_norm_residual")
+    wt, rows = _norm_weights(dev, H, w_post, gate, w_next)
+    if y is None:
+        out = None
+    elif out is None:
+        out = torch.empty_like(x)
+    if w_post is None:
+        rstd_y = None
+    elif rstd_y is None:
+        rstd_y = torch.empty(T, dtype=torch.float32, device=dev)
+    if w_next is None:
+        n = rstd_out = None
+    else:
+        if n is None:
+            n = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+        if rstd_out is None:
+            rstd_out = torch.empty(T, dtype=torch.float32, device=dev)
+    _check(_on(dev, _lib.moe_norm_residual, x.data_ptr(), _ptr(y), _ptr(w_post), _ptr(gate), rows,
+               _ptr(w_next), T, H, moe_norm_config(eps, residual_scale, branch_scale, st, wt),
+               _ptr(out), _ptr(n), _ptr(rstd_y), _ptr(rstd_out), _raw_stream(stream, dev)),
+           "moe_norm_residual")
     return dict(out=out, n=n, rstd_y=rstd_y, rstd_out=rstd_out)
 
 
@@ -919,59 +927,48 @@ def moe_norm_residual_backward(d_out, d_n, out, y=None, w_post=None, gate=None, 
     forward's. Returns dict(dx, dy, dw_post, dgate, dw_next), the last three in
     float32 and, with accumulate_dw, added to what the given tensors hold; None
     where there is no such input. dx may be d_out itself."""
-    _cuda(out, "out")
     st = _typed(out, "out")
     T, H = out.shape
-    _cuda(d_out, "d_out", out.dtype)
+    dev = out.device
+    bf16, f32 = torch.bfloat16, torch.float32
+    _fit(dev, (out, "out", out.dtype, 0), (d_out, "d_out", out.dtype, 0), (d_n, "d_n", bf16, 0),
+         (y, "y", bf16, 0), (rstd_y, "rstd_y", f32, T), (rstd_out, "rstd_out", f32, T),
+         (dx, "dx", out.dtype, T * H), (dy, "dy", bf16, T * H))
     _shaped(d_out, "d_out", T, H)
-    _cuda(d_n, "d_n", torch.bfloat16)
     _shaped(d_n, "d_n", T, H)
-    _cuda(y, "y", torch.bfloat16)
     _shaped(y, "y", T, H)
-    wt, rows = _norm_weights(H, w_post=w_post, gate=gate, w_next=w_next)
-    for t, name in ((rstd_y, "rstd_y"), (rstd_out, "rstd_out")):
-        _cuda(t, name, torch.float32, T)
-    _cuda(dx, "dx", out.dtype, T * H)
-    _cuda(dy, "dy", torch.bfloat16, T * H)
-    for t, name, m in ((dw_post, "dw_post", H), (dgate, "dgate", rows * H),
-                       (dw_next, "dw_next", H)):
-        _cuda(t, name, torch.float32, m)
-    _cuda(workspace, "workspace")
-    dev = _device(("out", out), ("d_out", d_out), ("d_n", d_n), ("y", y), ("w_post", w_post),
-                  ("gate", gate), ("w_next", w_next), ("rstd_y", rstd_y),
-                  ("rstd_out", rstd_out), ("dx", dx), ("dy", dy), ("dw_post", dw_post),
-                  ("dgate", dgate), ("dw_next", dw_next), ("workspace", workspace))
+    wt, rows = _norm_weights(dev, H, w_post, gate, w_next)
+    _fit(dev, (dw_post, "dw_post", f32, H), (dgate, "dgate", f32, rows * H),
+         (dw_next, "dw_next", f32, H))
     if accumulate_dw and any(w is not None and g is None for w, g in (
             (w_post, dw_post), (gate, dgate), (w_next if d_n is not None else None, dw_next))):
         raise ValueError("accumulate_dw adds to dw_post, dgate and dw_next: pass them")
-    cfg = moe_norm_config(eps, residual_scale, branch_scale, st, wt)
-    f32 = dict(dtype=torch.float32, device=dev)
-    with _guard(dev):
-        dx = torch.empty_like(out) if dx is None else dx
-        if y is None:
-            dy = None
-        elif dy is None:
-            dy = torch.empty_like(y)
-        if w_post is None:
-            dw_post = None
-        elif dw_post is None:
-            dw_post = torch.empty(H, **f32)
-        if gate is None:
-            dgate = None
-        elif dgate is None:
-            dgate = torch.empty(gate.shape, **f32)
-        if w_next is None or d_n is None:
-            dw_next = None
-        elif dw_next is None:
-            dw_next = torch.empty(H, **f32)
-        if workspace is None:
-            workspace = _workspace(
-                _lib.moe_norm_residual_backward_workspace_size(T, H, rows), dev)
-        _check(_lib.moe_norm_residual_backward(
-            _ptr(d_out), _ptr(d_n), out.data_ptr(), _ptr(y), _ptr(w_post), _ptr(gate), rows,
-            _ptr(w_next), _ptr(rstd_y), _ptr(rstd_out), T, H, cfg, dx.data_ptr(), _ptr(dy),
-            _ptr(dw_post), _ptr(dgate), _ptr(dw_next), bool(accumulate_dw), workspace.data_ptr(),
-            workspace.nbytes, _raw_stream(stream, dev)), "moe_norm_residual_backward")
+    if dx is None:
+        dx = torch.empty_like(out)
+    if y is None:
+        dy = None
+    elif dy is None:
+        dy = torch.empty_like(y)
+    if w_post is None:
+        dw_post = None
+    elif dw_post is None:
+        dw_post = torch.empty(H, dtype=f32, device=dev)
+    if gate is None:
+        dgate = None
+    elif dgate is None:
+        dgate = torch.empty(gate.shape, dtype=f32, device=dev)
+    if w_next is None or d_n is None:
+        dw_next = None
+    elif dw_next is None:
+        dw_next = torch.empty(H, dtype=f32, device=dev)
+    ws, ws_bytes = _scratch(workspace, _on(
+        dev, _lib.moe_norm_residual_backward_workspace_size, T, H, rows), dev)
+    _check(_on(dev, _lib.moe_norm_residual_backward, _ptr(d_out), _ptr(d_n), out.data_ptr(),
+               _ptr(y), _ptr(w_post), _ptr(gate), rows, _ptr(w_next), _ptr(rstd_y),
+               _ptr(rstd_out), T, H, moe_norm_config(eps, residual_scale, branch_scale, st, wt),
+               dx.data_ptr(), _ptr(dy), _ptr(dw_post), _ptr(dgate), _ptr(dw_next),
+               bool(accumulate_dw), _ptr(ws), ws_bytes, _raw_stream(stream, dev)),
+           "moe_norm_residual_backward")
     return dict(dx=dx, dy=dy, dw_post=dw_post, dgate=dgate, dw_next=dw_next)
 
 
@@ -1008,21 +1005,16 @@ def moe_clip_grad_norm(grads, max_norm, out=None, norm_type=2.0, eps=1e-6, norm_
                     o.numel() != g.numel():
                 raise ValueError(f"out[{i}] must be as grads[{i}]: same type, device and size")
         outs = (_vp * n)(*[o.data_ptr() for o in out])
-    _cuda(norm_coef, "norm_coef", torch.float32, 2)
-    _cuda(workspace, "workspace")
-    _device(("grads", grads[0] if grads else None), ("norm_coef", norm_coef),
-            ("workspace", workspace))
-    with _guard(dev):
-        if norm_coef is None:
-            norm_coef = torch.empty(2, dtype=torch.float32, device=dev)
-        if workspace is None:
-            workspace = _workspace(_lib.moe_clip_grad_norm_workspace_size(), dev)
-        _check(_lib.moe_clip_grad_norm(
-            (_vp * n)(*[g.data_ptr() for g in grads]), outs,
-            (_i64 * n)(*[g.numel() for g in grads]), (_i32 * n)(*[_TYPES[g.dtype] for g in grads]),
-            n, -1.0 if max_norm is None else max_norm, int(norm_type == math.inf), eps,
-            norm_coef.data_ptr(), workspace.data_ptr(), workspace.nbytes,
-            _raw_stream(stream, dev)), "moe_clip_grad_norm")
+    _fit(dev, (norm_coef, "norm_coef", torch.float32, 2))
+    if norm_coef is None:
+        norm_coef = torch.empty(2, dtype=torch.float32, device=dev)
+    ws, ws_bytes = _scratch(workspace, _lib.moe_clip_grad_norm_workspace_size(), dev)
+    _check(_on(dev, _lib.moe_clip_grad_norm, (_vp * n)(*[g.data_ptr() for g in grads]), outs,
+               (_i64 * n)(*[g.numel() for g in grads]),
+               (_i32 * n)(*[_TYPES[g.dtype] for g in grads]), n,
+               -1.0 if max_norm is None else max_norm, int(norm_type == math.inf), eps,
+               norm_coef.data_ptr(), _ptr(ws), ws_bytes, _raw_stream(stream, dev)),
+           "moe_clip_grad_norm")
     return norm_coef[0:1], norm_coef[1:2]
 
 

@@ -37,7 +37,8 @@ __device__ __forceinline__ float load_logit<__nv_bfloat16>(const __nv_bfloat16* 
 }
 
 // NaN counts as -inf, +inf as the largest float.
-__device__ __forceinline__ float clean(float l) { return isnan(l) ? -INFINITY : fminf(l, kFloatMax); }
+// (fmaxf drops a NaN)
+__device__ __forceinline__ float clean(float l) { return fminf(fmaxf(l, -INFINITY), kFloatMax); }
 
 // W consecutive lanes share a token: sums, maxima over them.
 template <int W, typename V>
@@ -60,9 +61,9 @@ __device__ __forceinline__ unsigned seg_max_key(unsigned v) {
   return v;
 }
 
-// Unsigned keys in the order of the floats (-0.0 entered as +0.0), and back.
+// Unsigned keys in the order of the floats (-0.0 below +0.0), and back.
 __device__ __forceinline__ unsigned key_of(float v) {
-  const int b = __float_as_int(v + 0.0f);
+  const int b = __float_as_int(v);
   return static_cast<unsigned>(b) ^ (static_cast<unsigned>(b >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float float_of(unsigned k) {
@@ -82,7 +83,7 @@ __device__ __forceinline__ float fast_sigmoid(float l) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + fast_exp(-l)));
   return r;
 }
-__device__ __forceinline__ float sigmoid(float l) { return 1.0f / (1.0f + expf(-l)); }
+__device__ __forceinline__ float sigmoid(float l) { return __fdividef(1.0f, 1.0f + expf(-l)); }
 
 // Whether x, that ranks before y, is larger by more than both may be off.
 __device__ __forceinline__ bool apart(float x, float y, float abs_off, float rel_off) {
@@ -118,13 +119,28 @@ __device__ __forceinline__ void sort_desc(unsigned (&a)[N]) {
 
 // ------------------------------------------------------------------ one token in double
 
-__device__ __forceinline__ double warp_sum(double v) { return seg_sum<32>(v); }
+// One chosen expert: its key in the order, whose low bits count the lane's
+// experts down, and its lane's first expert.
+struct Pick {
+  unsigned key;
+  int e;
+};
+template <int C>
+__device__ __forceinline__ int expert_of(const Pick& q) {
+  return q.e + static_cast<int>(C - 1u - (q.key & (C - 1u)));
+}
 
-// The larger value first, equal values to the lower index.
-__device__ __forceinline__ void warp_argmax(double& v, int& e) {
+// Signed keys in the order of the doubles (-0.0 entered as +0.0).
+__device__ __forceinline__ long long order_of(double v) {
+  const long long b = __double_as_longlong(v + 0.0);
+  return b ^ static_cast<long long>(static_cast<unsigned long long>(b >> 63) >> 1);
+}
+constexpr long long kLowest = LLONG_MIN;
+
+__device__ __forceinline__ void warp_argmax(long long& v, int& e) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    const double ov = __shfl_xor_sync(kAll, v, o);
+    const long long ov = __shfl_xor_sync(kAll, v, o);
     const int oe = __shfl_xor_sync(kAll, e, o);
     if (ov > v || (ov == v && oe < e)) {
       v = ov;
@@ -133,13 +149,9 @@ __device__ __forceinline__ void warp_argmax(double& v, int& e) {
   }
 }
 
-struct Pick {                // one chosen expert: its key in the order, and its index
-  unsigned key;
-  int e;
-};
-
 // The choice of one token by a whole warp with every value in double (v: E
-// doubles of shared memory): for the tokens whose order float leaves open.
+// values of shared memory): for the few tokens that neither reorder nor
+// groups_in_double can settle. Some 20 us, most of it the exponentials.
 template <typename L>
 __device__ __noinline__ void choose_in_double(const GateParams& p, const L* row, double* v,
                                               Pick* pick) {
@@ -152,17 +164,19 @@ __device__ __noinline__ void choose_in_double(const GateParams& p, const L* row,
     m = seg_max<32>(m);
     top = m == -INFINITY ? 0.0 : static_cast<double>(m);
     double sum = 0.0;
+#pragma unroll 4
     for (int e = lane; e < p.E; e += 32) sum += exp(clean(load_logit(row + e)) - top);
-    sum = warp_sum(sum);
+    sum = seg_sum<32>(sum);
     inv = sum > 0.0 ? 1.0 / sum : 0.0;
   }
   __syncwarp();
+#pragma unroll 4
   for (int e = lane; e < p.E; e += 32) {
     const float l = clean(load_logit(row + e));
     const float b = p.bias ? clean(__ldg(p.bias + e)) : 0.0f;
-    v[e] = l == -INFINITY || b == -INFINITY   ? -INFINITY
-           : p.score == MOE_SCORE_SOFTMAX     ? exp(l - top) * inv + b
-                                              : 1.0 / (1.0 + exp(-static_cast<double>(l))) + b;
+    const double ex = exp(p.score == MOE_SCORE_SOFTMAX ? l - top : -static_cast<double>(l));
+    const double s = p.score == MOE_SCORE_SOFTMAX ? ex * inv : 1.0 / (1.0 + ex);
+    v[e] = l == -INFINITY || b == -INFINITY ? -INFINITY : s + b;
   }
   __syncwarp();
   unsigned kept = kAll;
@@ -170,14 +184,11 @@ __device__ __noinline__ void choose_in_double(const GateParams& p, const L* row,
     double g = -INFINITY;
     if (lane < p.n_group) {
       double a = -INFINITY, b = -INFINITY;
-      for (int e = lane * size; e < (lane + 1) * size; ++e) {
-        const double x = v[e];
-        if (x > a) {
-          b = a;
-          a = x;
-        } else if (x > b) {
-          b = x;
-        }
+#pragma unroll 4
+      for (int i = 0; i < size; ++i) {
+        const double x = v[lane * size + i];
+        b = order_of(x) > order_of(a) ? a : order_of(x) > order_of(b) ? x : b;
+        a = order_of(x) > order_of(a) ? x : a;
       }
       g = a;
       if (p.group_topk == 2 && b != -INFINITY) g += b;
@@ -185,56 +196,160 @@ __device__ __noinline__ void choose_in_double(const GateParams& p, const L* row,
     kept = 0u;
     for (int j = 0; j < p.topk_group; ++j) {
       const bool open = lane < p.n_group && !((kept >> lane) & 1u);
-      double bv = open ? g : -INFINITY;
+      long long bv = open ? order_of(g) : kLowest;
       int be = open ? lane : INT_MAX;
       warp_argmax(bv, be);
       kept |= 1u << be;                             // topk_group <= n_group: one is open
     }
   }
-  unsigned taken = 0u;                              // bit i: expert lane + 32 i
-  for (int j = 0; j < p.k; ++j) {
-    double bv = -INFINITY;
-    int be = INT_MAX;
-    for (int i = 0, e = lane; e < p.E; ++i, e += 32) {
-      if (((taken >> i) & 1u) || !((kept >> (e / size)) & 1u)) continue;
-      const double x = v[e] == -INFINITY ? -INFINITY
-                       : p.bias          ? v[e]
-                                         : static_cast<double>(clean(load_logit(row + e)));
-      if (x > bv || be == INT_MAX) {
-        bv = x;
-        be = e;
-      }
-    }
-    warp_argmax(bv, be);
-    if ((be & 31) == lane) taken |= 1u << (be >> 5);
-    if (lane == 0) pick[j].e = be;
+  __syncwarp();
+  // the values' order in place of the values
+  long long* o = reinterpret_cast<long long*>(v);
+  for (int e = lane; e < p.E; e += 32) {
+    const double x = v[e] == -INFINITY || p.bias ? v[e]
+                                                 : static_cast<double>(clean(load_logit(row + e)));
+    o[e] = (kept >> (e / size)) & 1u ? order_of(x) : kLowest;
   }
   __syncwarp();
+  for (int j = 0; j < p.k; ++j) {
+    long long bv = kLowest;
+    int be = INT_MAX;
+#pragma unroll 4
+    for (int e = lane; e < p.E; e += 32)
+      if (o[e] > bv) {
+        bv = o[e];
+        be = e;
+      }
+    warp_argmax(bv, be);                            // k experts at least are kept
+    if ((be & 31) == lane) o[be] = kLowest;
+    if (lane == 0) pick[j] = Pick{kAll, be};         // low bits all set: nothing to add
+    __syncwarp();
+  }
 }
 
-// The same k experts in the order of their values in double: where only the
-// order among them is open, and a value needs no sum over the others.
+// The groups that a token keeps (a bit each), by a whole warp, where sigmoid
+// scores leave two groups at the border too close for float: only the groups
+// there, and of them only the experts that may be among their best, are
+// computed in double, one by each lane. 0 with more of them than lanes.
+// row_v: 2 E floats of shared memory; off: what a score may be off.
 template <typename L>
-__device__ __noinline__ void reorder_in_double(const GateParams& p, const L* row, Pick* pick) {
-  const int lane = lane_id();
-  int e = INT_MAX;
-  double v = -INFINITY;
-  if (lane < p.k) {
-    e = pick[lane].e;
+__device__ __noinline__ unsigned groups_in_double(const GateParams& p, const L* row, float* row_v,
+                                                  float off) {
+  const int lane = lane_id(), size = p.E / p.n_group;
+  int* list = reinterpret_cast<int*>(row_v + p.E);
+  __syncwarp();
+  for (int e = lane; e < p.E; e += 32) {
     const float l = clean(load_logit(row + e));
     const float b = p.bias ? clean(__ldg(p.bias + e)) : 0.0f;
-    if (l != -INFINITY && b != -INFINITY)
-      v = p.bias ? 1.0 / (1.0 + exp(-static_cast<double>(l))) + b : static_cast<double>(l);
+    row_v[e] = l == -INFINITY || b == -INFINITY ? -INFINITY : fast_sigmoid(l) + b;
+  }
+  __syncwarp();
+  float a = -INFINITY, c = -INFINITY;
+  if (lane < p.n_group)
+    for (int i = 0, at = lane % size; i < size; ++i, at = at + 1 == size ? 0 : at + 1) {
+      const float x = row_v[lane * size + at];
+      c = fmaxf(c, fminf(a, x));
+      a = fmaxf(a, x);
+    }
+  const bool two = p.group_topk == 2 && c != -INFINITY;
+  const float g = two ? a + c : a;
+  int rank = 0;
+  for (int j = 0; j < p.n_group; ++j) {
+    const float o = __shfl_sync(kAll, g, j);
+    rank += o > g || (o == g && j < lane);
+  }
+  const bool in = lane < p.n_group && rank < p.topk_group;
+  const float low = -seg_max<32>(in ? -g : -INFINITY);
+  const float high = seg_max<32>(in || lane >= p.n_group ? -INFINITY : g);
+  const bool open = lane < p.n_group && !(in ? apart(g, high, 4.0f * off, 0x1p-22f)
+                                             : apart(low, g, 4.0f * off, 0x1p-22f));
+  const unsigned opens = __ballot_sync(kAll, open);
+  unsigned kept = __ballot_sync(kAll, in && !open);
+  const float least = two ? c : a;                 // what a group's best may be level with
+  int n = 0;
+  for (int e1 = 0; e1 < p.E; e1 += 32) {
+    const int e = e1 + lane;
+    const int of = e < p.E ? e / size : 0;
+    const float bar = __shfl_sync(kAll, least, of);
+    const bool may = e < p.E && ((opens >> of) & 1u) && row_v[e] != -INFINITY &&
+                     !apart(bar, row_v[e], 2.0f * off, 0x1p-22f);
+    const unsigned m = __ballot_sync(kAll, may);
+    const int at = n + __popc(m & ((1u << lane) - 1u));
+    if (may && at < 32) list[at] = e;
+    n += __popc(m);
+  }
+  __syncwarp();
+  if (n > 32) return 0u;
+  int mine = -1;
+  double x = 0.0;
+  if (lane < n) {
+    const int e = list[lane];
+    mine = e / size;
+    x = 1.0 / (1.0 + exp(-static_cast<double>(clean(load_logit(row + e))))) +
+        (p.bias ? clean(__ldg(p.bias + e)) : 0.0f);
+  }
+  double best = -INFINITY, next = -INFINITY;
+  for (int j = 0; j < n; ++j) {
+    const double o = __shfl_sync(kAll, x, j);
+    const int of = __shfl_sync(kAll, mine, j);
+    if (of != lane) continue;
+    next = o > best ? best : o > next ? o : next;
+    best = o > best ? o : best;
+  }
+  if (p.group_topk == 2 && next != -INFINITY) best += next;
+  for (int j = __popc(kept); j < p.topk_group; ++j) {
+    const bool free = open && !((kept >> lane) & 1u);
+    long long bv = free ? order_of(best) : kLowest;
+    int be = free ? lane : INT_MAX;
+    warp_argmax(bv, be);
+    kept |= 1u << be;                              // the open groups are enough
+  }
+  __syncwarp();
+  return kept;
+}
+
+// The first k of n <= 32 candidates in their right order, by a whole warp.
+// Where neighbours that are close are all the same pair of logit and bias,
+// only their indices tell them apart; else every value is computed in double,
+// one by each lane. False where that would need the softmax's sum.
+template <typename L, int C>
+__device__ __noinline__ bool reorder(const GateParams& p, const L* row, Pick* pick, int n,
+                                     float abs_off) {
+  const int lane = lane_id();
+  const bool soft = p.score == MOE_SCORE_SOFTMAX;
+  unsigned key = 0u;
+  int e = INT_MAX;
+  float l = -INFINITY, b = 0.0f;
+  if (lane < n && pick[lane].key != 0u) {
+    key = pick[lane].key & ~(C - 1u);
+    e = expert_of<C>(pick[lane]);
+    l = clean(load_logit(row + e));
+    if (p.bias) b = clean(__ldg(p.bias + e));
+  }
+  const unsigned next = __shfl_down_sync(kAll, key, 1);
+  const float nl = __shfl_down_sync(kAll, l, 1), nb = __shfl_down_sync(kAll, b, 1);
+  const bool differ = lane + 1 < n && next != 0u && !(l == nl && b == nb) &&
+                      !apart(float_of(key), float_of(next), abs_off, C * 0x1.2p-23f);
+  const bool compute = __any_sync(kAll, differ);
+  if (compute && soft && p.bias) return false;
+  long long v = key;                                // equal for the same pair
+  if (compute && key != 0u) {
+    double x = l;
+    if (p.bias) x = 1.0 / (1.0 + exp(-static_cast<double>(l))) + b;
+    v = order_of(l == -INFINITY || b == -INFINITY ? -INFINITY : x);
+  } else if (compute) {
+    v = kLowest;
   }
   int rank = 0;
-  for (int j = 0; j < p.k; ++j) {
-    const double ov = __shfl_sync(kAll, v, j);
+  for (int j = 0; j < n; ++j) {
+    const long long ov = __shfl_sync(kAll, v, j);
     const int oe = __shfl_sync(kAll, e, j);
     rank += ov > v || (ov == v && oe < e);
   }
   __syncwarp();
-  if (lane < p.k) pick[rank].e = e;
+  if (rank < p.k && lane < n) pick[rank] = Pick{kAll, e};
   __syncwarp();
+  return true;
 }
 
 // ------------------------------------------------------------------ weights of the chosen
@@ -254,10 +369,13 @@ __device__ __forceinline__ void slot_weights(const GateParams& p, const float (&
                                              float inv, float (&u)[S]) {
   if (!p.renorm) {
 #pragma unroll
-    for (int i = 0; i < S; ++i)
+    for (int i = 0; i < S; ++i) {
+      u[i] = 0.0f;
+      if (W * i >= p.k) continue;                   // the same for every lane
       u[i] = l[i] == -INFINITY               ? 0.0f
              : p.score == MOE_SCORE_SOFTMAX  ? expf(l[i] - top) * inv
                                              : sigmoid(l[i]);
+    }
     return;
   }
   float sum = 0.0f;
@@ -268,6 +386,8 @@ __device__ __forceinline__ void slot_weights(const GateParams& p, const float (&
     m = seg_max<W>(m);
 #pragma unroll
     for (int i = 0; i < S; ++i) {
+      u[i] = 0.0f;
+      if (W * i >= p.k) continue;
       u[i] = l[i] == -INFINITY ? 0.0f : expf(l[i] - m);
       sum += u[i];
     }
@@ -275,6 +395,8 @@ __device__ __forceinline__ void slot_weights(const GateParams& p, const float (&
   } else {
 #pragma unroll
     for (int i = 0; i < S; ++i) {
+      u[i] = 0.0f;
+      if (W * i >= p.k) continue;
       u[i] = l[i] == -INFINITY ? 0.0f : sigmoid(l[i]);
       sum += u[i];
     }
@@ -291,7 +413,8 @@ __device__ __forceinline__ void slot_weights(const GateParams& p, const float (&
     }
   }
 #pragma unroll
-  for (int i = 0; i < S; ++i) u[i] = sum > 0.0f ? u[i] / sum : 0.0f;
+  for (int i = 0; i < S; ++i)
+    if (W * i < p.k) u[i] = sum > 0.0f ? __fdividef(u[i], sum) : 0.0f;
 }
 
 // The softmax's largest logit (0 for a row of -inf) and the reciprocal of
@@ -347,8 +470,10 @@ template <int W, int C>
 struct GateShape {
   static constexpr int kWarps = C > 16 ? 4 : 8;
   static constexpr int kTokens = 32 / W;                       // of a warp
-  static constexpr int kPicks = (W * C < 32 ? W * C : 32) + 1; // k, and the first one left out
-  static constexpr int kSlots = 32 / W < 8 ? 32 / W : 8;       // k <= min(32, W * C) over W lanes
+  static constexpr int kMost = W * C < 32 ? W * C : 32;        // the largest k
+  static constexpr int kPicks = kMost + 1;                     // and the first one left out
+  static constexpr int kSlots = (kMost + W - 1) / W;           // k over W lanes
+  static constexpr int kCtas = C > 16 ? 2 : C > 8 ? 3 : 4;     // of an SM, by registers
 };
 
 // ------------------------------------------------------------------ forward
@@ -364,13 +489,14 @@ struct GateShape {
 // and rcp.approx within 2^-22 and 2^-23, and s (1 - s) <= 1/4), a choice
 // value by 2^-24 of itself more, and its key by the C - 1 units that its low
 // bits hold. Only tokens with two neighbours in the order closer than that
-// (some 0.2% with scores of 256 experts) are ordered again in double. bf16
+// (some 0.3% with scores of 256 experts) are looked at again: for ties and
+// most others in the order of the candidates alone (reorder). bf16
 // logits that rank by themselves leave room for the whole index in the key,
 // and need no second look at all (kScored false: no bias and no groups).
 //
-// Bound by instruction issue (some 400 warp instructions for 256 experts).
+// Bound by instruction issue.
 template <typename L, int W, int C, bool kScored>
-__global__ void __launch_bounds__((GateShape<W, C>::kWarps * 32), (C > 8 ? 2 : 4))
+__global__ void __launch_bounds__((GateShape<W, C>::kWarps * 32), (GateShape<W, C>::kCtas))
     gate_kernel(const __grid_constant__ GateParams p, int32_t* __restrict__ ids, float* __restrict__ probs,
                 int32_t* __restrict__ counts, int32_t* __restrict__ offsets,
                 int32_t* __restrict__ scratch, int clustered) {
@@ -378,25 +504,23 @@ __global__ void __launch_bounds__((GateShape<W, C>::kWarps * 32), (C > 8 ? 2 : 4
   extern __shared__ __align__(16) unsigned char smem[];
   double* sh_v = reinterpret_cast<double*>(smem);              // [warps][E]
   int* hist = reinterpret_cast<int*>(sh_v + static_cast<size_t>(G::kWarps) * p.E);   // [E]
+  __shared__ __align__(16) float sh_bias[kScored ? W * C : 4];
   __shared__ Pick sh_pick[G::kWarps][G::kTokens][G::kPicks];
-  __shared__ float sh_group[G::kWarps][G::kTokens][G::kPicks - 1];
+  __shared__ float sh_group[kScored ? G::kWarps : 1][G::kTokens][G::kMost];
   const int lane = lane_id(), w = threadIdx.x >> 5;
   const int sub = lane & (W - 1), tok = lane / W, e0 = sub * C;
   const unsigned seg = static_cast<unsigned>((1ull << W) - 1ull) << (lane & ~(W - 1));
+  const unsigned before = (1u << lane) - 1u;                   // lower lanes
   for (int e = threadIdx.x; e < p.E; e += blockDim.x) hist[e] = 0;
+  if (kScored && p.bias)                                       // out of E: masked
+    for (int e = threadIdx.x; e < W * C; e += blockDim.x)
+      sh_bias[e] = e < p.E ? clean(__ldg(p.bias + e)) : -INFINITY;
   __syncthreads();
 
   const bool biased = kScored && p.bias != nullptr, grouped = kScored && p.n_group > 1;
   const bool soft = p.score == MOE_SCORE_SOFTMAX;
   constexpr bool exact = sizeof(L) == 2 && !kScored;           // keys that hold the index whole
   const int size = p.E / p.n_group;
-  float b[C];
-  if (biased) {
-    load_row<C>(p.bias, e0, p.E, (reinterpret_cast<uintptr_t>(p.bias) & 15) == 0 && p.E % 4 == 0,
-                -INFINITY, b);
-#pragma unroll
-    for (int i = 0; i < C; ++i) b[i] = clean(b[i]);
-  }
   Pick* pick = sh_pick[w][tok];
   const int64_t step = static_cast<int64_t>(gridDim.x) * G::kWarps * G::kTokens;
   // the trip count is the same for every lane of a warp
@@ -410,7 +534,7 @@ __global__ void __launch_bounds__((GateShape<W, C>::kWarps * 32), (C > 8 ? 2 : 4
     if (exact) {
 #pragma unroll
       for (int i = 0; i < C; ++i)
-        key[i] = (key_of(isnan(l[i]) ? -INFINITY : l[i]) & 0xffff0000u) | (0xffffu - e0 - i);
+        key[i] = (key_of(fmaxf(l[i], -INFINITY) + 0.0f) & 0xffff0000u) | (0xffffu - e0 - i);
     }
 #pragma unroll
     for (int i = 0; i < C; ++i) l[i] = clean(l[i]);
@@ -418,21 +542,53 @@ __global__ void __launch_bounds__((GateShape<W, C>::kWarps * 32), (C > 8 ? 2 : 4
     if (soft && (kScored || !p.renorm)) softmax_of<W, C>(l, &top, &inv);
     float v[C];
     if (kScored) {
+      if (soft) {
 #pragma unroll
-      for (int i = 0; i < C; ++i) {
-        v[i] = soft ? fast_exp(l[i] - top) * inv : fast_sigmoid(l[i]);
-        if (biased) v[i] = b[i] == -INFINITY ? -INFINITY : v[i] + b[i];
-        if (l[i] == -INFINITY) v[i] = -INFINITY;
+        for (int i = 0; i < C; ++i) v[i] = fast_exp(l[i] - top) * inv;
+      } else {
+#pragma unroll
+        for (int i = 0; i < C; ++i) v[i] = fast_sigmoid(l[i]);
+      }
+      if (biased) {
+#pragma unroll
+        for (int i = 0; i < C; i += 4) {
+          const float4 b = *reinterpret_cast<const float4*>(sh_bias + e0 + i);
+          v[i] += b.x;
+          v[i + 1] += b.y;
+          v[i + 2] += b.z;
+          v[i + 3] += b.w;
+        }
+      }
+      float least = l[0];
+#pragma unroll
+      for (int i = 1; i < C; ++i) least = fminf(least, l[i]);
+      if (__any_sync(kAll, least == -INFINITY)) {
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+          if (l[i] == -INFINITY) v[i] = -INFINITY;
       }
     }
     if (!exact) {
 #pragma unroll
       for (int i = 0; i < C; ++i)
-        key[i] = (key_of(biased ? v[i] : l[i]) & ~(C - 1u)) | (C - 1u - i);
+        key[i] = (key_of((biased ? v[i] : l[i]) + 0.0f) & ~(C - 1u)) | (C - 1u - i);   // one zero
     }
     // how far a score may be off (logits that rank by themselves: only by their key)
     const float off = soft ? inv * 0x1p-19f : 0x1p-21f;
     bool open_set = false;                                     // the k experts are not certain
+    // the groups of the warp's tokens that opens names, in double; 0: not settled
+    auto settle_groups = [&](unsigned opens) {
+      unsigned right = 0u;
+      for (int q = 0; q < G::kTokens && !soft; ++q) {
+        const unsigned mine = static_cast<unsigned>((1ull << W) - 1ull) << (q * W);
+        if (!(opens & mine)) continue;
+        const unsigned kept =
+            groups_in_double(p, static_cast<const L*>(p.logits) + min(t0 + q, p.T - 1) * p.E,
+                             reinterpret_cast<float*>(sh_v + static_cast<size_t>(w) * p.E), off);
+        if (tok == q) right = kept;
+      }
+      return right;
+    };
     if (grouped) {
       // a group's score, its rank, and the lanes' experts that it leaves out
       if (p.E == W * C && p.n_group <= W) {
@@ -449,16 +605,25 @@ __global__ void __launch_bounds__((GateShape<W, C>::kWarps * 32), (C > 8 ? 2 : 4
           a = fmaxf(a, oa);
         }
         const float g = p.group_topk == 2 && c != -INFINITY ? a + c : a;
-        int rank = 0;
-        for (int o = lanes; o < W; o += lanes) {
-          const int from = sub ^ o;                            // every other group once
-          const float og = __shfl_xor_sync(kAll, g, o);
-          rank += og > g || (og == g && from < sub);
+        // topk_group rounds of the largest; groups of one score go together,
+        // and are then too close to be certain
+        unsigned gk = key_of(g + 0.0f), low = 0u, high = 0u;
+        for (int j = 0; j <= p.topk_group; ++j) {
+          low = high;
+          high = seg_max_key<W>(gk);
+          if (j < p.topk_group && gk == high) gk = 0u;
         }
-        const bool kept = rank < p.topk_group;
-        const float low = -seg_max<W>(kept ? -g : -INFINITY);
-        const float high = seg_max<W>(kept ? -INFINITY : g);
-        open_set = p.topk_group < p.n_group && !apart(low, high, 4.0f * off, 0x1p-22f);
+        bool kept = gk == 0u;
+        const int of = __popc(__ballot_sync(kAll, kept) & seg);
+        open_set = of != p.topk_group * lanes ||
+                   (high != 0u && !apart(float_of(low), float_of(high), 4.0f * off, 0x1p-22f));
+        if (const unsigned opens = __ballot_sync(kAll, open_set)) {
+          const unsigned right = settle_groups(opens);
+          if (right) {
+            kept = (right >> (sub / lanes)) & 1u;
+            open_set = false;
+          }
+        }
         if (!kept) {
 #pragma unroll
           for (int i = 0; i < C; ++i) key[i] = 0u;
@@ -505,52 +670,74 @@ __global__ void __launch_bounds__((GateShape<W, C>::kWarps * 32), (C > 8 ? 2 : 4
         low = -seg_max<W>(-low);
         high = seg_max<W>(high);
         open_set = p.topk_group < p.n_group && !apart(low, high, 4.0f * off, 0x1p-22f);
+        if (const unsigned opens = __ballot_sync(kAll, open_set)) {
+          const unsigned right = settle_groups(opens);
+          if (right) {
+            kept = right;
+            open_set = false;
+          }
+        }
 #pragma unroll
         for (int i = 0; i < C; ++i)
           if (e0 + i >= p.E || !((kept >> ((e0 + i) / size)) & 1u)) key[i] = 0u;
         __syncwarp();
       }
     }
+    if (p.E != W * C) {
 #pragma unroll
-    for (int i = 0; i < C; ++i)
-      if (e0 + i >= p.E) key[i] = 0u;
+      for (int i = 0; i < C; ++i)
+        if (e0 + i >= p.E) key[i] = 0u;
+    }
     sort_desc<0, C>(key);
     __syncwarp();                                              // the last token's picks are read
-    for (int j = 0; j <= p.k; ++j) {
+    auto pop = [&](int j) {
       const unsigned best = seg_max_key<W>(key[0]);
-      const unsigned same = __ballot_sync(kAll, key[0] == best) & seg;
-      if (lane == __ffs(same) - 1) {
-        pick[j].key = best;
-        pick[j].e = exact ? static_cast<int>(0xffffu - (best & 0xffffu))
-                          : e0 + static_cast<int>(C - 1u - (best & (C - 1u)));
+      bool won = key[0] == best;
+      if (!exact) {
+        const unsigned same = __ballot_sync(kAll, won);        // every lane votes
+        won = won && !(same & seg & before);                   // the lowest of equal lanes
+      }
+      if (won) {
+        pick[j] = Pick{best, e0};
 #pragma unroll
         for (int i = 0; i + 1 < C; ++i) key[i] = key[i + 1];
         key[C - 1] = 0u;
       }
-    }
+    };
+    for (int j = 0; j <= p.k; ++j) pop(j);
     __syncwarp();
-    // neighbours too close for float
-    bool open_order = false;
     if (!exact) {
-      for (int j = sub; j < p.k; j += W) {
-        const unsigned ka = pick[j].key & ~(C - 1u), kb = pick[j + 1].key & ~(C - 1u);
-        if (kb == 0u) continue;                                // nothing is left out
-        const float x = float_of(ka), y = float_of(kb);
-        const bool close = !apart(x, y, biased ? 2.0f * off : 1e-43f, C * 0x1.2p-23f);
-        if (close && j + 1 == p.k) open_set = true;
-        if (close && j + 1 < p.k) open_order = true;
-      }
-    }
-    const unsigned sets = __ballot_sync(kAll, open_set || (open_order && soft && biased));
-    const unsigned orders = __ballot_sync(kAll, open_order);
-    if (sets | orders) {
-      for (int q = 0; q < G::kTokens; ++q) {
-        const unsigned mine = static_cast<unsigned>((1ull << W) - 1ull) << (q * W);
-        const L* its = static_cast<const L*>(p.logits) + min(t0 + q, p.T - 1) * p.E;
-        if (sets & mine)
-          choose_in_double(p, its, sh_v + static_cast<size_t>(w) * p.E, sh_pick[w][q]);
-        else if (orders & mine)
-          reorder_in_double(p, its, sh_pick[w][q]);
+      // neighbours too close for float: among the k, or at their end
+      const float abs_off = biased ? 2.0f * off : 1e-43f;
+      auto close = [&](int i, int j) {
+        const unsigned ka = pick[i].key & ~(C - 1u), kb = pick[j].key & ~(C - 1u);
+        return kb != 0u && !apart(float_of(ka), float_of(kb), abs_off, C * 0x1.2p-23f);
+      };
+      bool open_order = false, open_end = false;
+      for (int j = sub; j < p.k; j += W)
+        if (close(j, j + 1)) (j + 1 < p.k ? open_order : open_end) = true;
+      if (__any_sync(kAll, open_order || open_end || open_set)) {
+        int n = p.k;
+        if (unsigned ends = __ballot_sync(kAll, open_end)) {
+          // more candidates, until one is apart from the k-th
+          const int most = G::kPicks < 32 ? G::kPicks : 32;
+          for (n = p.k + 1; ends && n < most; ++n) {
+            pop(n);
+            __syncwarp();
+            ends = __ballot_sync(kAll, (ends & seg) && close(p.k - 1, n));
+          }
+          if (ends & seg) open_set = true;
+          n = min(n, 32);
+        }
+        const unsigned sets = __ballot_sync(kAll, open_set);
+        const unsigned orders = __ballot_sync(kAll, open_order || open_end);
+        for (int q = 0; q < G::kTokens; ++q) {
+          const unsigned mine = static_cast<unsigned>((1ull << W) - 1ull) << (q * W);
+          if (!((sets | orders) & mine)) continue;
+          const L* its = static_cast<const L*>(p.logits) + min(t0 + q, p.T - 1) * p.E;
+          if ((sets & mine) || !reorder<L, C>(p, its, sh_pick[w][q], n, abs_off))
+            choose_in_double(p, its, sh_v + static_cast<size_t>(w) * p.E, sh_pick[w][q]);
+        }
       }
     }
     // weights
@@ -560,17 +747,17 @@ __global__ void __launch_bounds__((GateShape<W, C>::kWarps * 32), (C > 8 ? 2 : 4
     for (int i = 0; i < G::kSlots; ++i) {
       const int j = sub + W * i;
       lj[i] = -INFINITY;
-      if (j < p.k) {
-        ej[i] = pick[j].e;
+      if (W * i < p.k && j < p.k) {
+        ej[i] = exact ? static_cast<int>(0xffffu - (pick[j].key & 0xffffu)) : expert_of<C>(pick[j]);
         lj[i] = clean(load_logit(row + ej[i]));
-        if (biased && clean(__ldg(p.bias + ej[i])) == -INFINITY) lj[i] = -INFINITY;
+        if (biased && sh_bias[ej[i]] == -INFINITY) lj[i] = -INFINITY;
       }
     }
     slot_weights<W>(p, lj, top, inv, u);
 #pragma unroll
     for (int i = 0; i < G::kSlots; ++i) {
       const int j = sub + W * i;
-      if (j < p.k && t0 + tok < p.T) {
+      if (W * i < p.k && j < p.k && t0 + tok < p.T) {
         ids[t * p.k + j] = ej[i];
         probs[t * p.k + j] = p.scale * u[i];
         atomicAdd(hist + ej[i], 1);
@@ -628,7 +815,7 @@ __global__ void __launch_bounds__((GateShape<W, C>::kWarps * 32), (C > 8 ? 2 : 4
 // through a row of shared memory, zero between tokens, to the lanes that own
 // their experts; every lane then writes its C columns.
 template <typename L, int W, int C>
-__global__ void __launch_bounds__((GateShape<W, C>::kWarps * 32), (C > 8 ? 2 : 4))
+__global__ void __launch_bounds__((GateShape<W, C>::kWarps * 32), (GateShape<W, C>::kCtas))
     gate_backward_kernel(const __grid_constant__ GateParams p, const float* __restrict__ dprobs,
                          const int32_t* __restrict__ ids, L* __restrict__ dlogits, int vec_out,
                          int* err) {
@@ -664,7 +851,7 @@ __global__ void __launch_bounds__((GateShape<W, C>::kWarps * 32), (C > 8 ? 2 : 4
       lj[i] = -INFINITY;
       dp[i] = 0.0f;
       ej[i] = -1;
-      if (j < p.k) {
+      if (W * i < p.k && j < p.k) {
         ej[i] = __ldg(ids + t * p.k + j);
         if (ej[i] < 0 || ej[i] >= p.E) {
           report_error(err, kErrBadId);
@@ -696,6 +883,7 @@ __global__ void __launch_bounds__((GateShape<W, C>::kWarps * 32), (C > 8 ? 2 : 4
     float g[G::kSlots];
 #pragma unroll
     for (int i = 0; i < G::kSlots; ++i) {
+      if (W * i >= p.k) continue;
       const float far = sigm ? 1.0f / (1.0f + expf(lj[i])) : 1.0f;     // 1 - s
       g[i] = lj[i] == -INFINITY ? 0.0f : u[i] * far * (p.renorm ? dp[i] - d : dp[i]);
       if (ej[i] >= 0) mine[ej[i]] = any_twice ? 0.0f : g[i];
@@ -777,12 +965,21 @@ moe_status gate_params(GateParams* p, const void* logits, int type, const float*
 // Head of the workspace (the ticket, 256 bytes) and one total per expert.
 size_t gate_scratch_bytes(int E) { return 256 + static_cast<size_t>(E) * sizeof(int32_t); }
 
+// CTAs that hold all tokens at once.
+struct GateCtas {
+  int64_t T;
+  template <int W, int C>
+  int64_t operator()() const {
+    const int64_t per = GateShape<W, C>::kWarps * GateShape<W, C>::kTokens;
+    return T > 0 ? (T + per - 1) / per : 1;
+  }
+};
+
 template <typename L, int W, int C>
 cudaError_t launch_gate(const GateParams& p, int32_t* ids, float* probs, int32_t* counts,
                         int32_t* offsets, int32_t* scratch, cudaStream_t st) {
   using G = GateShape<W, C>;
-  const int64_t per = G::kWarps * G::kTokens;
-  const int64_t want = p.T > 0 ? (p.T + per - 1) / per : 1;
+  const int64_t want = GateCtas{p.T}.operator()<W, C>();
   const size_t smem = static_cast<size_t>(G::kWarps) * p.E * sizeof(double) + p.E * sizeof(int);
   auto* kernel = p.bias || p.n_group > 1 ? gate_kernel<L, W, C, true> : gate_kernel<L, W, C, false>;
   if (want <= kMaxCluster) {
@@ -801,7 +998,7 @@ cudaError_t launch_gate(const GateParams& p, int32_t* ids, float* probs, int32_t
   }
   cudaError_t e = cudaMemsetAsync(scratch, 0, gate_scratch_bytes(p.E), st);
   if (e != cudaSuccess) return e;
-  const int64_t cap = static_cast<int64_t>(device_sm_count()) * 4;
+  const int64_t cap = static_cast<int64_t>(device_sm_count()) * G::kCtas;
   kernel<<<static_cast<unsigned>(want < cap ? want : cap), G::kWarps * 32, smem, st>>>(
       p, ids, probs, counts, offsets, scratch, 0);
   return cudaGetLastError();
@@ -822,16 +1019,17 @@ cudaError_t launch_gate_backward(const GateParams& p, const float* dprobs, const
   return cudaGetLastError();
 }
 
-// Calls f with the lanes per token and the experts per lane that hold E:
-// eight experts a lane, as many tokens a warp as that leaves room for.
+// Calls f with the lanes per token and the experts per lane that hold E. Most
+// instructions are a token's, not an expert's, and a warp issues them once for
+// all its tokens: sixteen experts a lane where there are that many to hold.
 template <typename F>
-cudaError_t with_shape(int E, F&& f) {
+auto with_shape(int E, F&& f) {
   if (E <= 8) return f.template operator()<1, 8>();
   if (E <= 16) return f.template operator()<2, 8>();
   if (E <= 32) return f.template operator()<4, 8>();
-  if (E <= 64) return f.template operator()<8, 8>();
-  if (E <= 128) return f.template operator()<16, 8>();
-  if (E <= 256) return f.template operator()<32, 8>();
+  if (E <= 64) return f.template operator()<4, 16>();
+  if (E <= 128) return f.template operator()<8, 16>();
+  if (E <= 256) return f.template operator()<16, 16>();
   if (E <= 512) return f.template operator()<32, 16>();
   return f.template operator()<32, 32>();
 }
@@ -876,7 +1074,7 @@ void moe_gate_config_init(moe_gate_config* cfg) {
 
 size_t moe_route_gate_workspace_size(int64_t T, int k, int E) {
   if (T < 0 || k < 1 || E < 1 || T > ((static_cast<int64_t>(1) << 31) - 1) / k) return 0;
-  return gate_scratch_bytes(E);
+  return with_shape(E, GateCtas{T}) <= kMaxCluster ? 0 : gate_scratch_bytes(E);
 }
 
 moe_status moe_route_gate(const void* logits, int logits_type, const float* bias, int64_t T, int E,
@@ -889,8 +1087,8 @@ moe_status moe_route_gate(const void* logits, int logits_type, const float* bias
   if (s != MOE_OK) return s;
   if ((T > 0 && (!logits || !expert_ids || !probs)) || !counts || !offsets)
     return MOE_ERR_INVALID_ARG;
-  if (!workspace || ws_bytes < moe_route_gate_workspace_size(T, k, E) ||
-      (reinterpret_cast<uintptr_t>(workspace) & 15))
+  const size_t need = moe_route_gate_workspace_size(T, k, E);
+  if (need > 0 && (!workspace || ws_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 15)))
     return MOE_ERR_WORKSPACE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   int32_t* scratch = static_cast<int32_t*>(workspace);

@@ -250,7 +250,7 @@ def test_gate_refusals():
             call()
         assert e.value.status == 1
     with pytest.raises(m.MoeError) as e:
-        m.moe_route_gate(logits, 2, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+        m.moe_route_gate(dev(torch.zeros((9999, 8))), 2, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     assert e.value.status == 4
     with pytest.raises(ValueError, match="contiguous"):
         m.moe_route_gate(dev(torch.zeros((8, 4))).t(), 2)

@@ -164,6 +164,7 @@ def test_config_defaults(m):
 def test_workspace_sizes(m):
     L = m._lib
     assert L.moe_route_gate_workspace_size(4096, 8, 256) > 0
+    assert L.moe_route_gate_workspace_size(4, 8, 256) == 0        # one cluster needs none
     assert L.moe_route_gate_workspace_size(1 << 62, 32, 64) == 0
     assert L.moe_route_gate_workspace_size(-1, 2, 8) == 0
     assert L.moe_norm_residual_backward_workspace_size(4096, 4096, 1) > 0
@@ -240,9 +241,9 @@ def test_entry_points_refuse_before_any_launch(m):
         ("gate: group_topk = 3", INV, lambda: gate(cfg=gcfg(group_topk=3))),
         ("gate: scale", INV, lambda: gate(cfg=gcfg(scale=inf))),
         ("gate: no counts", INV, lambda: gate(counts=None)),
-        ("gate: no workspace", WS, lambda: gate(ws=None)),
-        ("gate: small workspace", WS, lambda: gate(wsb=8)),
-        ("gate: unaligned workspace", WS, lambda: gate(ws=U)),
+        ("gate: no workspace", WS, lambda: gate(T=9999, ws=None)),
+        ("gate: small workspace", WS, lambda: gate(T=9999, wsb=8)),
+        ("gate: unaligned workspace", WS, lambda: gate(T=9999, ws=U)),
         ("gate backward: no ids", INV, lambda: gate_b(ids=None)),
         ("gate backward: no dlogits", INV, lambda: gate_b(dl=None)),
         ("gate backward: unaligned dlogits", INV, lambda: gate_b(dl=O)),
