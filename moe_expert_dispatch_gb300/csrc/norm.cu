@@ -1,33 +1,12 @@
 // norm.cu - moe_norm_residual and its backward: the norm after the block,
 // its gate, the scaled residual and the norm before the next block.
-#include "common.cuh"
-#include "internal.h"
+#include "norm.cuh"
 
 namespace moe {
-
-int* device_error_word();
-
 namespace {
 
 constexpr int kNormThreads = 256;
 constexpr int kMaxNormH = 65536;
-
-struct NormParams {
-  const void* x;        // forward: the stream; backward: d_out (may be null)
-  const void* out;      // backward: the forward's out
-  const __nv_bfloat16* y;
-  const __nv_bfloat16* d_n;
-  const void* w_post;
-  const void* gate;
-  const void* w_next;
-  const float* rstd_y;
-  const float* rstd_out;
-  int64_t T;
-  int64_t gate_span;    // tokens that share a gate row
-  int H;
-  float eps, a, b;
-  float inv_h;
-};
 
 template <typename E>
 __device__ __forceinline__ float ld(const void* p, int64_t i);
@@ -229,299 +208,6 @@ __global__ void __launch_bounds__(1024)
   }
 }
 
-// ------------------------------------------------------------------ backward, rows through shared memory
-
-// Rows of strip i of n: [i T / n, (i + 1) T / n); the strip of a row.
-__host__ __device__ __forceinline__ int64_t strip_row(int64_t T, int n, int64_t i) {
-  return i * T / n;
-}
-__device__ __forceinline__ int64_t strip_of(int64_t T, int n, int64_t row) {
-  return ((row + 1) * n - 1) / T;
-}
-
-struct BackwardParams {
-  NormParams n;
-  void* dx;
-  __nv_bfloat16* dy;
-  float* dgate;
-  float* part_post;      // [CTAs, H] sum of D yh (kMany: of g D yh), without b
-  float* part_next;      // [CTAs, H] sum of d_n o
-  float* part_gate;      // kMany: two pieces of [H] for every strip
-  int strips, group, groups, stages, row_bytes, accumulate;
-  int weights_f32;
-  int* err;
-};
-
-// The sum of v over a group of `group` threads (whole warps) to each of them.
-__device__ __forceinline__ float group_sum(float v, float* red, int bar, int group) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if (lane_id() == 0) red[threadIdx.x % group >> 5] = v;
-  asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(group) : "memory");
-  v = lane_id() < (group >> 5) ? red[lane_id()] : 0.0f;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-
-__device__ __forceinline__ void weights4(const BackwardParams& p, const void* w, int64_t i,
-                                         float* f) {
-  float q[4];
-  if (p.weights_f32)
-    load_weights<float, 4>(w, i, q);
-  else
-    load_weights<__nv_bfloat16, 4>(w, i, q);
-#pragma unroll
-  for (int h = 0; h < 4; ++h) f[h] = q[h];
-}
-
-// Four consecutive elements of a row in shared memory.
-template <typename T>
-__device__ __forceinline__ void row4(const unsigned char* row, int i, float (&f)[4]) {
-  if constexpr (sizeof(T) == 4) {
-    const float4 q = *reinterpret_cast<const float4*>(row + i * 4);
-    f[0] = q.x;
-    f[1] = q.y;
-    f[2] = q.z;
-    f[3] = q.w;
-  } else {
-    const uint2 q = *reinterpret_cast<const uint2*>(row + i * 2);
-    unpack<4>(Raw<4>{{q.x, q.y}}, f);
-  }
-}
-
-// A group of threads walks a strip of consecutive rows, every thread with
-// eight fixed columns (two vectors of four, so that all accesses are
-// coalesced): the column sums of the weight gradients stay in its registers,
-// and each row's tensors, which bulk copies bring into a ring of shared
-// memory ahead of it, are read once. A CTA has as many groups as 1024 threads
-// hold, each with its own ring and barriers, and adds their sums up at the
-// end, so that norm_finish_kernel has one row of partial sums an SM to add.
-//
-// kBranch: with y. kPost: with w_post. kNext: with d_n. kMany: with more than
-// one gate row; else S = sum D yh gives both dw_post = b g S and dgate =
-// b w_post S. Bound by HBM: 18 bytes an element with a float stream.
-template <typename ST, bool kBranch, bool kPost, bool kNext, bool kMany>
-__global__ void __launch_bounds__(1024, 1) norm_backward_kernel(const __grid_constant__ BackwardParams p) {
-  extern __shared__ __align__(128) unsigned char ring_all[];
-  __shared__ float red_all[8][4][32];
-  __shared__ __align__(8) uint64_t full_all[8][4];
-  __shared__ int abort_wait;
-  const NormParams& q = p.n;
-  const int g = threadIdx.x / p.group, tid = threadIdx.x % p.group, H = q.H;
-  const int strip = blockIdx.x * p.groups + g;
-  int64_t lo = 0, hi = 0;
-  if (strip < p.strips) {
-    lo = strip_row(q.T, p.strips, strip);
-    hi = strip_row(q.T, p.strips, strip + 1);
-  }
-  unsigned char* ring = ring_all + static_cast<size_t>(g) * p.stages * p.row_bytes;
-  const uint32_t full = smem_u32(&full_all[g][0]);
-  if (threadIdx.x == 0) abort_wait = 0;
-  if (tid == 0) {
-    for (int i = 0; i < p.stages; ++i) mbar_init(full + 8 * i, 1);
-    fence_mbar_init();
-  }
-  __syncthreads();
-
-  // a stage: d_out, out (kNext), y (kBranch), d_n (kNext)
-  const int wide = H * static_cast<int>(sizeof(ST)), half = H * 2;
-  const int at_out = q.x ? wide : 0, at_y = at_out + (kNext ? wide : 0),
-            at_dn = at_y + (kBranch ? half : 0);
-  auto issue = [&](int64_t t, int stage) {
-    const uint32_t bar = full + 8 * stage, to = smem_u32(ring) + stage * p.row_bytes;
-    const int64_t at = t * H;
-    mbar_arrive_expect_tx(bar, p.row_bytes);
-    if (q.x) bulk_copy_g2s(to, static_cast<const ST*>(q.x) + at, wide, bar);
-    if (kNext) bulk_copy_g2s(to + at_out, static_cast<const ST*>(q.out) + at, wide, bar);
-    if (kBranch) bulk_copy_g2s(to + at_y, q.y + at, half, bar);
-    if (kNext) bulk_copy_g2s(to + at_dn, q.d_n + at, half, bar);
-  };
-  if (tid == 0)
-    for (int i = 0; i < p.stages && lo + i < hi; ++i) issue(lo + i, i);
-
-  const int col[2] = {4 * tid, 4 * (tid + p.group)};
-  float gw[8], wn[8], sum_s[8], sum_w[8], sum_n[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    gw[i] = q.b;
-    wn[i] = sum_s[i] = sum_w[i] = sum_n[i] = 0.0f;
-  }
-  auto times = [&](const void* w, int64_t row, float (&f)[8]) {
-    float m[4];
-#pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      if (col[v] >= H) continue;
-      weights4(p, w, row + col[v], m);
-#pragma unroll
-      for (int h = 0; h < 4; ++h) f[4 * v + h] *= m[h];
-    }
-  };
-  if (kNext) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) wn[i] = 1.0f;
-    times(q.w_next, 0, wn);
-  }
-  if (kBranch && !kMany) {
-    if (kPost) times(q.w_post, 0, gw);
-    if (q.gate) times(q.gate, 0, gw);
-  }
-
-  unsigned long long limit = kDefaultWaitNs;
-  float next_ro = 0.0f, next_ry = 1.0f;
-  if (lo < hi) {
-    if (kNext) next_ro = q.rstd_out[lo];
-    if (kPost) next_ry = q.rstd_y[lo];
-  }
-  int stage = 0, parity = 0, odd = 0;
-  for (int64_t t = lo; t < hi; ++t) {
-    const float ro = next_ro, ry = next_ry;
-    if (t + 1 < hi) {
-      if (kNext) next_ro = q.rstd_out[t + 1];
-      if (kPost) next_ry = q.rstd_y[t + 1];
-    }
-    if (kMany && (t == lo || t % q.gate_span == 0)) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        gw[i] = q.b;
-        sum_s[i] = 0.0f;
-      }
-      if (kPost) times(q.w_post, 0, gw);
-      times(q.gate, t / q.gate_span * H, gw);
-    }
-    if (!mbar_wait(full + 8 * stage, parity, limit, &abort_wait)) {
-      // no wait of this length is legitimate: report it, and wait no more
-      report_error(p.err, kErrTimeout);
-      limit = 0;
-    }
-    const unsigned char* row = ring + stage * p.row_bytes;
-    float d[8], f[4], u[4];
-    if (kNext) {
-      float s = 0.0f;
-#pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        if (col[v] >= H) continue;
-        row4<__nv_bfloat16>(row + at_dn, col[v], f);
-        row4<ST>(row + at_out, col[v], u);
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          const float o = u[h] * ro;
-          sum_n[4 * v + h] = fmaf(f[h], o, sum_n[4 * v + h]);
-          s = fmaf(f[h] * wn[4 * v + h], o, s);
-        }
-      }
-      const float c = group_sum(s, red_all[g][odd], g + 1, p.group) * q.inv_h;
-#pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        if (col[v] >= H) continue;
-        row4<__nv_bfloat16>(row + at_dn, col[v], f);
-        row4<ST>(row + at_out, col[v], u);
-#pragma unroll
-        for (int h = 0; h < 4; ++h)
-          d[4 * v + h] = ro * (f[h] * wn[4 * v + h] - u[h] * ro * c);
-      }
-    }
-#pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      if (col[v] >= H) continue;
-      if (q.x) row4<ST>(row, col[v], f);
-#pragma unroll
-      for (int h = 0; h < 4; ++h)
-        d[4 * v + h] = kNext ? (q.x ? d[4 * v + h] + f[h] : d[4 * v + h]) : f[h];
-    }
-    float yh[8], m = 0.0f;
-    if (kBranch) {
-      float s = 0.0f;
-#pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        if (col[v] >= H) continue;
-        row4<__nv_bfloat16>(row + at_y, col[v], f);
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          const int i = 4 * v + h;
-          yh[i] = kPost ? f[h] * ry : f[h];
-          sum_s[i] = fmaf(d[i], yh[i], sum_s[i]);
-          if (kPost) s = fmaf(gw[i] * d[i], yh[i], s);
-        }
-      }
-      if (kPost) m = group_sum(s, red_all[g][2 + odd], g + 1, p.group) * q.inv_h;
-    }
-    if (!(kBranch && kPost)) asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "r"(p.group) : "memory");
-    // every thread has the row in registers: its stage takes another
-    if (tid == 0 && t + p.stages < hi) issue(t + p.stages, stage);
-    const int64_t at = t * H;
-#pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      if (col[v] >= H) continue;
-      if (kBranch) {
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          const int i = 4 * v + h;
-          f[h] = kPost ? ry * (gw[i] * d[i] - yh[i] * m) : gw[i] * d[i];
-        }
-        store_bf16<4>(p.dy + at + col[v], f);
-      }
-      const float a = kBranch ? q.a : 1.0f;
-#pragma unroll
-      for (int h = 0; h < 4; ++h) f[h] = a * d[4 * v + h];
-      ST* to = static_cast<ST*>(p.dx) + at + col[v];
-      if constexpr (sizeof(ST) == 4)
-        *reinterpret_cast<float4*>(to) = make_float4(f[0], f[1], f[2], f[3]);
-      else
-        store_bf16<4>(to, f);
-    }
-    if (kMany && (t + 1 == hi || (t + 1) % q.gate_span == 0)) {
-      const int64_t r = t / q.gate_span, first = r * q.gate_span;
-      const bool whole = first >= lo && first + q.gate_span <= hi;
-      float* to = whole ? p.dgate + r * H
-                        : p.part_gate + (static_cast<int64_t>(strip) * 2 + (first >= lo)) * H;
-#pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        if (col[v] >= H) continue;
-        float gt[4], wp[4];
-        weights4(p, q.gate, r * H + col[v], gt);
-        if (kPost) weights4(p, q.w_post, col[v], wp);
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          const int i = 4 * v + h;
-          sum_w[i] = fmaf(gt[h], sum_s[i], sum_w[i]);
-          float z = sum_s[i];
-          if (whole) {
-            z *= kPost ? q.b * wp[h] : q.b;
-            if (p.accumulate) z += to[col[v] + h];
-          }
-          to[col[v] + h] = z;
-        }
-      }
-    }
-    odd ^= 1;
-    if (++stage == p.stages) {
-      stage = 0;
-      parity ^= 1;
-    }
-  }
-
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  // the groups' sums, in order
-  auto add_up = [&](const float (&sum)[8], float* part) {
-    float* all = reinterpret_cast<float*>(ring_all);
-    __syncthreads();
-#pragma unroll
-    for (int v = 0; v < 2; ++v)
-      if (col[v] < H)
-        *reinterpret_cast<float4*>(all + static_cast<size_t>(g) * H + col[v]) =
-            make_float4(sum[4 * v], sum[4 * v + 1], sum[4 * v + 2], sum[4 * v + 3]);
-    __syncthreads();
-    for (int h = threadIdx.x; h < H; h += blockDim.x) {
-      float z = 0.0f;
-      for (int i = 0; i < p.groups; ++i) z += all[static_cast<size_t>(i) * H + h];
-      part[static_cast<int64_t>(blockIdx.x) * H + h] = z;
-    }
-  };
-  if (kBranch && p.part_post) add_up(kMany ? sum_w : sum_s, p.part_post);
-  if (kNext) add_up(sum_n, p.part_next);
-}
-
 // ------------------------------------------------------------------ any H, any alignment
 
 // One CTA per row, three passes over it (the later two from L1/L2).
@@ -689,45 +375,49 @@ struct FinishParams {
   float b;
 };
 
-__global__ void __launch_bounds__(512) norm_finish_kernel(const __grid_constant__ FinishParams p) {
-  __shared__ float sh[16][33];
+__global__ void __launch_bounds__(1024) norm_finish_kernel(const __grid_constant__ FinishParams p) {
+  __shared__ float sh[32][33];
   const int lane = lane_id(), w = threadIdx.x >> 5;
   const int h = blockIdx.x * 32 + lane;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  auto weight = [&](const void* q, int64_t i) {
-    return p.weights_f32 ? static_cast<const float*>(q)[i]
-                         : __bfloat162float(static_cast<const __nv_bfloat16*>(q)[i]);
-  };
   for (int64_t what = blockIdx.y; what < 2 + p.gate_rows; what += gridDim.y) {
     const bool of_gate = what >= 2;
     const int64_t r = what - 2;
-    // one gate row: its sum is the one behind dw_post
-    const bool from_post = what == 0 || (of_gate && p.one_gate);
     if (!of_gate && !(what == 0 ? p.dw_post : p.dw_next)) continue;
+    // one gate row: its sum is the one behind dw_post
+    const bool pieces = of_gate && !p.one_gate;
+    const float* part = what == 1 ? p.part_next : pieces ? p.part_gate : p.part_post;
     int64_t i0 = 0, i1 = p.parts;
-    const float* part = from_post ? p.part_post : what == 1 ? p.part_next : p.part_gate;
-    if (of_gate && !p.one_gate && p.strips > 0) {
+    if (pieces && p.strips > 0) {
       i0 = strip_of(p.T, p.strips, r * p.gate_span);
       i1 = strip_of(p.T, p.strips, (r + 1) * p.gate_span - 1) + 1;
       if (i1 - i0 == 1) continue;                  // written by its strip
     }
-    const bool pieces = of_gate && !p.one_gate;
     float s = 0.0f;
     if (h < p.H)
-#pragma unroll 4
-      for (int64_t i = i0 + w; i < i1; i += 16)
-        s += part[(pieces ? i * 2 + (i == i0) : i) * p.H + h];
+      for (int64_t i = i0 + w; i < i1; i += 32 * 8) {
+        float f[8];                                // eight loads on their way
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int64_t j = i + 32 * u;
+          f[u] = j < i1 ? part[(pieces ? j * 2 + (j == i0) : j) * p.H + h] : 0.0f;
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) s += f[u];
+      }
     __syncthreads();
     sh[w][lane] = s;
     __syncthreads();
-    if (w == 0 && h < p.H) {
-      s = 0.0f;
+    // a warp a column of sh, each 32 parts: in a fixed order
+    s = sh[lane][w];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) s += sh[i][lane];
-      float* to = (of_gate ? p.dgate + r * p.H : what == 0 ? p.dw_post : p.dw_next) + h;
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    const int c = blockIdx.x * 32 + w;
+    if (lane == 0 && c < p.H) {
+      float* to = (of_gate ? p.dgate + r * p.H : what == 0 ? p.dw_post : p.dw_next) + c;
       if (what != 1) s *= p.b;
-      if (of_gate && p.w_post) s *= weight(p.w_post, h);
-      if (what == 0 && p.one_gate) s *= weight(p.gate, h);
+      if (of_gate && p.w_post) s *= weight_at(p.w_post, p.weights_f32, c);
+      if (what == 0 && p.one_gate) s *= weight_at(p.gate, p.weights_f32, c);
       *to = p.accumulate ? *to + s : s;
     }
   }
@@ -767,6 +457,19 @@ int forward_threads(int H, int W, int V) {
 template <typename ST, typename WT>
 cudaError_t forward(const NormParams& p, void* out, void* n, float* rstd_y, float* rstd_out,
                     cudaStream_t s) {
+  // up to one row an SM the kernel without a ring is shorter (1 x 7168: 3.8
+  // against 4.4 us); beyond, rows through shared memory (4096 x 4096: 31
+  // against 37 us)
+  const int row_bytes = p.H * static_cast<int>(sizeof(ST) + (p.y ? 2 : 0));
+  const RingShape r = ring_shape(p.T, p.H, row_bytes);
+  if (r.groups > 0 && p.T > device_sm_count()) {
+    RingOut ro = {};
+    ro.stream = out;
+    ro.branch = static_cast<__nv_bfloat16*>(n);
+    ro.rstd_y = rstd_y;
+    ro.rstd_out = rstd_out;
+    return launch_norm_ring(p, r, ro, sizeof(ST) == 4, false, row_bytes, s);
+  }
   constexpr int W = sizeof(ST) == 4 ? 4 : 8;
   ST* o = static_cast<ST*>(out);
   __nv_bfloat16* nn = static_cast<__nv_bfloat16*>(n);
@@ -795,64 +498,6 @@ struct NormGrads {
   int accumulate;
 };
 
-// How a backward call is laid out; groups 0: the kernels for any H.
-struct BackwardShape {
-  int groups, group, stages, ctas, strips;
-};
-
-constexpr int kRingBytes = 216 * 1024;
-
-BackwardShape backward_shape(int64_t T, int H, int row_bytes) {
-  BackwardShape b = {};
-  if (T == 0) return b;
-  const int sms = device_sm_count();
-  b.group = (H / 8 + 31) / 32 * 32;
-  if (H % 8 == 0 && b.group <= 1024 && 2 * row_bytes <= kRingBytes) {
-    b.groups = 1024 / b.group < 8 ? 1024 / b.group : 8;
-    while (b.groups > 1 && (b.groups * 2 * row_bytes > kRingBytes ||
-                            T <= static_cast<int64_t>(sms) * (b.groups - 1)))
-      --b.groups;
-    b.stages = kRingBytes / (b.groups * row_bytes);
-    if (b.stages > 4) b.stages = 4;
-    const int64_t most = static_cast<int64_t>(sms) * b.groups;
-    b.strips = static_cast<int>(T < most ? T : most);
-    b.ctas = (b.strips + b.groups - 1) / b.groups;
-  } else {
-    const int64_t most = static_cast<int64_t>(sms) * 2;
-    b.strips = b.ctas = static_cast<int>(T < most ? T : most);
-  }
-  return b;
-}
-
-template <typename K>
-cudaError_t launch_backward(K* kernel, const BackwardParams& p, const BackwardShape& b, size_t smem,
-                            cudaStream_t s) {
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(smem));
-  if (e != cudaSuccess) return e;
-  kernel<<<b.ctas, b.groups * b.group, smem, s>>>(p);
-  return cudaGetLastError();
-}
-
-template <typename ST>
-cudaError_t fast_backward(const BackwardParams& p, const BackwardShape& b, cudaStream_t s) {
-  const size_t ring = static_cast<size_t>(b.groups) * b.stages * p.row_bytes;
-  const size_t sums = static_cast<size_t>(b.groups) * p.n.H * sizeof(float);
-  const size_t smem = ring > sums ? ring : sums;
-  const bool post = p.n.w_post, next = p.n.d_n, many = p.n.gate && p.n.gate_span < p.n.T;
-  if (!p.n.y) return launch_backward(norm_backward_kernel<ST, false, false, true, false>, p, b, smem, s);
-  auto* kernel =
-      many ? (post ? (next ? norm_backward_kernel<ST, true, true, true, true>
-                           : norm_backward_kernel<ST, true, true, false, true>)
-                   : (next ? norm_backward_kernel<ST, true, false, true, true>
-                           : norm_backward_kernel<ST, true, false, false, true>))
-           : (post ? (next ? norm_backward_kernel<ST, true, true, true, false>
-                           : norm_backward_kernel<ST, true, true, false, false>)
-                   : (next ? norm_backward_kernel<ST, true, false, true, false>
-                           : norm_backward_kernel<ST, true, false, false, false>));
-  return launch_backward(kernel, p, b, smem, s);
-}
-
 int row_bytes_of(const NormParams& p, int stream_size) {
   return p.H * ((p.x ? stream_size : 0) + (p.d_n ? stream_size + 2 : 0) + (p.y ? 2 : 0));
 }
@@ -861,34 +506,28 @@ template <typename ST, typename WT>
 cudaError_t backward(const NormParams& p, const NormGrads& g, void* ws, cudaStream_t s) {
   const bool one_gate = p.gate && p.T > 0 && p.gate_span == p.T;
   const int row_bytes = row_bytes_of(p, sizeof(ST));
-  // without y and d_n there is nothing to reduce: the plain kernels do
-  const BackwardShape b = p.y || p.d_n ? backward_shape(p.T, p.H, row_bytes)
-                                       : backward_shape(p.T, 1, 1 << 30);
+  RingShape b = ring_shape(p.T, p.H, row_bytes);
+  if (b.groups == 0) {
+    const int64_t most = static_cast<int64_t>(device_sm_count()) * 2;
+    b.strips = b.ctas = static_cast<int>(p.T < most ? p.T : most);
+  }
   float* c_of = static_cast<float*>(ws);
   float* part = c_of + (p.T + 63) / 64 * 64;
-  const int64_t one = static_cast<int64_t>(b.strips) * p.H;
+  const int64_t one = static_cast<int64_t>(b.ctas) * p.H;
   float* part_post = (g.dw_post || one_gate) && b.strips ? part : nullptr;
   float* part_next = g.dw_next && b.strips ? part + one : nullptr;
   float* part_gate = part + 2 * one;
   cudaError_t e = cudaSuccess;
   if (b.groups > 0) {
-    BackwardParams q = {};
-    q.n = p;
-    q.dx = g.dx;
-    q.dy = static_cast<__nv_bfloat16*>(g.dy);
-    q.dgate = g.dgate;
-    q.part_post = part_post;
-    q.part_next = part_next;
-    q.part_gate = part_gate;
-    q.strips = b.strips;
-    q.group = b.group;
-    q.groups = b.groups;
-    q.stages = b.stages;
-    q.row_bytes = row_bytes;
-    q.accumulate = g.accumulate;
-    q.weights_f32 = sizeof(WT) == 4;
-    q.err = device_error_word();
-    e = fast_backward<ST>(q, b, s);
+    RingOut o = {};
+    o.stream = g.dx;
+    o.branch = static_cast<__nv_bfloat16*>(g.dy);
+    o.dgate = g.dgate;
+    o.part_post = part_post;
+    o.part_next = part_next;
+    o.part_gate = part_gate;
+    o.accumulate = g.accumulate;
+    e = launch_norm_ring(p, b, o, sizeof(ST) == 4, true, row_bytes, s);
   } else if (p.T > 0) {
     const unsigned cols = static_cast<unsigned>((p.H + 127) / 128);
     norm_rows_backward_kernel<ST, WT, true><<<rows_grid(p.T), kNormThreads, 0, s>>>(
@@ -914,7 +553,7 @@ cudaError_t backward(const NormParams& p, const NormGrads& g, void* ws, cudaStre
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3(static_cast<unsigned>((p.H + 31) / 32),
                      static_cast<unsigned>(want < 1024 ? want : 1024));
-  cfg.blockDim = dim3(512);
+  cfg.blockDim = dim3(1024);
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
@@ -961,6 +600,7 @@ moe_status moe_norm_residual(const void* x, const void* y, const void* w_post, c
   p.a = c.residual_scale;
   p.b = c.branch_scale;
   p.inv_h = 1.0f / H;
+  p.weights_f32 = c.weight_type == MOE_TYPE_F32;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool sf = c.stream_type == MOE_TYPE_F32, wf = c.weight_type == MOE_TYPE_F32;
   auto* run = sf ? (wf ? forward<float, float> : forward<float, __nv_bfloat16>)
@@ -971,11 +611,12 @@ moe_status moe_norm_residual(const void* x, const void* y, const void* w_post, c
 size_t moe_norm_residual_backward_workspace_size(int64_t T, int H, int64_t gate_rows) {
   if (T < 0 || H < 1 || H > kMaxNormH || gate_rows < 0 || T > (static_cast<int64_t>(1) << 40))
     return 0;
-  // strips of the layout with the most of them, whatever a call's tensors are
-  const int64_t most = static_cast<int64_t>(device_sm_count()) * 8;
-  const int64_t strips = T < most ? T : most;
+  // the layout with the most CTAs and strips, whatever a call's tensors are
+  const int64_t sms = device_sm_count(), groups = max_ring_groups(ring_group(H));
+  const int64_t ctas = T < 2 * sms ? T : 2 * sms;
+  const int64_t most = sms * (groups > 2 ? groups : 2), strips = T < most ? T : most;
   return static_cast<size_t>((T + 63) / 64 * 64) * sizeof(float) +
-         (gate_rows > 1 ? 4 : 2) * static_cast<size_t>(strips) * H * sizeof(float) + 256;
+         2 * static_cast<size_t>(ctas + (gate_rows > 1 ? strips : 0)) * H * sizeof(float) + 256;
 }
 
 moe_status moe_norm_residual_backward(const void* d_out, const void* d_n, const void* out,
@@ -1024,6 +665,7 @@ moe_status moe_norm_residual_backward(const void* d_out, const void* d_n, const 
   p.a = c.residual_scale;
   p.b = c.branch_scale;
   p.inv_h = 1.0f / H;
+  p.weights_f32 = c.weight_type == MOE_TYPE_F32;
   const NormGrads g{dx, dy, dw_post, dgate, dw_next, gate_rows, accumulate_dw};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool sf = c.stream_type == MOE_TYPE_F32, wf = c.weight_type == MOE_TYPE_F32;
