@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(128)
   if (part_next) part_next[strip * p.H + h] = sum_next;
 }
 
-// The partial sums, in order: 32 columns a CTA, its warps taking the parts in
+// The partial sums, in order: 128 columns a CTA, its warps taking the parts in
 // turn. blockIdx.y 0: dw_post, 1: dw_next, 2 + r: gate row r, from the pieces of
 // the strips that share it. scale_*: weights that the parts were left without.
 struct FinishParams {
@@ -375,10 +375,12 @@ struct FinishParams {
   float b;
 };
 
-__global__ void __launch_bounds__(1024) norm_finish_kernel(const __grid_constant__ FinishParams p) {
-  __shared__ float sh[32][33];
+__global__ void __launch_bounds__(256) norm_finish_kernel(const __grid_constant__ FinishParams p) {
+  constexpr int kWarps = 8, kLoads = 10;
+  __shared__ float4 sh[kWarps][32];
   const int lane = lane_id(), w = threadIdx.x >> 5;
-  const int h = blockIdx.x * 32 + lane;
+  const int h = blockIdx.x * 128 + lane * 4;       // the lane's four columns
+  const bool vec = p.H % 4 == 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   for (int64_t what = blockIdx.y; what < 2 + p.gate_rows; what += gridDim.y) {
     const bool of_gate = what >= 2;
@@ -387,38 +389,53 @@ __global__ void __launch_bounds__(1024) norm_finish_kernel(const __grid_constant
     // one gate row: its sum is the one behind dw_post
     const bool pieces = of_gate && !p.one_gate;
     const float* part = what == 1 ? p.part_next : pieces ? p.part_gate : p.part_post;
-    int64_t i0 = 0, i1 = p.parts;
+    int i0 = 0, i1 = p.parts;
     if (pieces && p.strips > 0) {
-      i0 = strip_of(p.T, p.strips, r * p.gate_span);
-      i1 = strip_of(p.T, p.strips, (r + 1) * p.gate_span - 1) + 1;
+      i0 = static_cast<int>(strip_of(p.T, p.strips, r * p.gate_span));
+      i1 = static_cast<int>(strip_of(p.T, p.strips, (r + 1) * p.gate_span - 1)) + 1;
       if (i1 - i0 == 1) continue;                  // written by its strip
     }
-    float s = 0.0f;
-    if (h < p.H)
-      for (int64_t i = i0 + w; i < i1; i += 32 * 8) {
-        float f[8];                                // eight loads on their way
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int i = i0 + w; i < i1; i += kWarps * kLoads) {
+      float4 f[kLoads];                            // as many loads on their way
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int64_t j = i + 32 * u;
-          f[u] = j < i1 ? part[(pieces ? j * 2 + (j == i0) : j) * p.H + h] : 0.0f;
+      for (int u = 0; u < kLoads; ++u) {
+        const int j = i + kWarps * u;
+        const float* at = part + static_cast<int64_t>(pieces ? j * 2 + (j == i0) : j) * p.H + h;
+        f[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (j < i1 && h < p.H) {
+          if (vec) {
+            f[u] = *reinterpret_cast<const float4*>(at);
+          } else {
+            f[u].x = at[0];
+            if (h + 1 < p.H) f[u].y = at[1];
+            if (h + 2 < p.H) f[u].z = at[2];
+            if (h + 3 < p.H) f[u].w = at[3];
+          }
         }
-#pragma unroll
-        for (int u = 0; u < 8; ++u) s += f[u];
       }
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u) {
+        s.x += f[u].x;
+        s.y += f[u].y;
+        s.z += f[u].z;
+        s.w += f[u].w;
+      }
+    }
     __syncthreads();
     sh[w][lane] = s;
     __syncthreads();
-    // a warp a column of sh, each 32 parts: in a fixed order
-    s = sh[lane][w];
+    const int c = blockIdx.x * 128 + threadIdx.x;
+    if (threadIdx.x < 128 && c < p.H) {
+      const float* all = reinterpret_cast<const float*>(sh);
+      float z = 0.0f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    const int c = blockIdx.x * 32 + w;
-    if (lane == 0 && c < p.H) {
+      for (int i = 0; i < kWarps; ++i) z += all[i * 128 + threadIdx.x];
       float* to = (of_gate ? p.dgate + r * p.H : what == 0 ? p.dw_post : p.dw_next) + c;
-      if (what != 1) s *= p.b;
-      if (of_gate && p.w_post) s *= weight_at(p.w_post, p.weights_f32, c);
-      if (what == 0 && p.one_gate) s *= weight_at(p.gate, p.weights_f32, c);
-      *to = p.accumulate ? *to + s : s;
+      if (what != 1) z *= p.b;
+      if (of_gate && p.w_post) z *= weight_at(p.w_post, p.weights_f32, c);
+      if (what == 0 && p.one_gate) z *= weight_at(p.gate, p.weights_f32, c);
+      *to = p.accumulate ? *to + z : z;
     }
   }
 }
@@ -461,7 +478,7 @@ cudaError_t forward(const NormParams& p, void* out, void* n, float* rstd_y, floa
   // against 4.4 us); beyond, rows through shared memory (4096 x 4096: 31
   // against 37 us)
   const int row_bytes = p.H * static_cast<int>(sizeof(ST) + (p.y ? 2 : 0));
-  const RingShape r = ring_shape(p.T, p.H, row_bytes);
+  const RingShape r = ring_shape(p.T, p.H, row_bytes, false, false);
   if (r.groups > 0 && p.T > device_sm_count()) {
     RingOut ro = {};
     ro.stream = out;
@@ -506,7 +523,7 @@ template <typename ST, typename WT>
 cudaError_t backward(const NormParams& p, const NormGrads& g, void* ws, cudaStream_t s) {
   const bool one_gate = p.gate && p.T > 0 && p.gate_span == p.T;
   const int row_bytes = row_bytes_of(p, sizeof(ST));
-  RingShape b = ring_shape(p.T, p.H, row_bytes);
+  RingShape b = ring_shape(p.T, p.H, row_bytes, true, p.gate && !one_gate);
   if (b.groups == 0) {
     const int64_t most = static_cast<int64_t>(device_sm_count()) * 2;
     b.strips = b.ctas = static_cast<int>(p.T < most ? p.T : most);
@@ -551,9 +568,9 @@ cudaError_t backward(const NormParams& p, const NormGrads& g, void* ws, cudaStre
   // for the whole grid before they read
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>((p.H + 31) / 32),
+  cfg.gridDim = dim3(static_cast<unsigned>((p.H + 127) / 128),
                      static_cast<unsigned>(want < 1024 ? want : 1024));
-  cfg.blockDim = dim3(1024);
+  cfg.blockDim = dim3(256);
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
@@ -612,7 +629,7 @@ size_t moe_norm_residual_backward_workspace_size(int64_t T, int H, int64_t gate_
   if (T < 0 || H < 1 || H > kMaxNormH || gate_rows < 0 || T > (static_cast<int64_t>(1) << 40))
     return 0;
   // the layout with the most CTAs and strips, whatever a call's tensors are
-  const int64_t sms = device_sm_count(), groups = max_ring_groups(ring_group(H));
+  const int64_t sms = device_sm_count(), groups = most_ring_groups(H);
   const int64_t ctas = T < 2 * sms ? T : 2 * sms;
   const int64_t most = sms * (groups > 2 ? groups : 2), strips = T < most ? T : most;
   return static_cast<size_t>((T + 63) / 64 * 64) * sizeof(float) +

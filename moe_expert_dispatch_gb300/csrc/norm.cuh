@@ -34,12 +34,11 @@ __device__ __forceinline__ int64_t strip_of(int64_t T, int n, int64_t row) {
 
 // How a call's rows lie on the ring kernels; groups 0: another length of a row.
 struct RingShape {
-  int groups, group, stages, ctas, strips;
+  int groups, group, stages, ctas, strips, tail_bytes;
 };
 constexpr int kMaxRingGroups = 15;       // a named barrier each, beside the CTA's own
-RingShape ring_shape(int64_t T, int H, int row_bytes);
-int ring_group(int H);                   // threads that share a row; 0: not on the ring kernels
-int max_ring_groups(int group);
+RingShape ring_shape(int64_t T, int H, int row_bytes, bool backward, bool many);
+int most_ring_groups(int H);             // of a CTA of the backward; 0: not on the ring kernels
 
 struct RingOut {
   void* stream;                  // out, or dx
