@@ -702,8 +702,9 @@ moe_status moe_norm_residual_backward(const void* d_out, const void* d_n, const 
  *  norm_coef float [2] device memory   out: norm, coef
  *  workspace >= moe_clip_grad_norm_workspace_size() bytes, 16-byte aligned;
  *           every call overwrites what it uses
- * n_tensors <= 1048576. Squares are summed in float over short runs and in
- * double beyond: elements between 1e-18 and 1e18 in magnitude count in full.
+ * n_tensors <= 1048576, numels[i] <= 2^40. Squares are summed in float over
+ * runs of at most 32 and to twice its precision beyond: elements between 1e-18
+ * and 1e18 in magnitude count in full.
  * No tensors, or only empty ones: norm = 0, coef = min(1, max_norm / eps).
  * ------------------------------------------------------------------------ */
 size_t moe_clip_grad_norm_workspace_size(void);

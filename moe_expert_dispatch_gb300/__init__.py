@@ -7,6 +7,7 @@ fallback: importing this package without the built library raises.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import math
 import os
@@ -128,8 +129,8 @@ _sig("moe_norm_residual_backward_workspace_size", _sz, _i64, _i32, _i64)
 _sig("moe_norm_residual_backward", _i32, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _i64,
      _i32, ctypes.POINTER(moe_norm_config), _vp, _vp, _vp, _vp, _vp, _i32, _vp, _sz, _vp)
 _sig("moe_clip_grad_norm_workspace_size", _sz)
-_sig("moe_clip_grad_norm", _i32, ctypes.POINTER(_vp), ctypes.POINTER(_vp), ctypes.POINTER(_i64),
-     ctypes.POINTER(_i32), _i64, ctypes.c_float, _i32, ctypes.c_float, _vp, _vp, _sz, _vp)
+_sig("moe_clip_grad_norm", _i32, _vp, _vp, _vp, _vp, _i64, ctypes.c_float, _i32, ctypes.c_float,
+     _vp, _vp, _sz, _vp)
 
 
 class MoeError(RuntimeError):
@@ -730,6 +731,7 @@ def moe_expert_backward_mxfp8(dy, x, w1g_q, w1g_s, w1u_q, w1u_s, w2_q, w2_s, exp
 # ------------------------------------------------------------------ the layer around the block
 
 _TYPES = {torch.float32: 0, torch.bfloat16: 1}
+_CLIP_WORKSPACE = _lib.moe_clip_grad_norm_workspace_size()
 _SCORES = {"softmax": 0, "sigmoid": 1}
 # the current stream of a device as an integer, without a Stream object
 _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
@@ -986,36 +988,60 @@ def moe_clip_grad_norm(grads, max_norm, out=None, norm_type=2.0, eps=1e-6, norm_
         raise ValueError(f"max_norm must be None or >= 0, got {max_norm}")
     if max_norm is None and out is not None:
         raise ValueError("out is written when gradients are clipped: max_norm is None")
-    dev = grads[0].device if grads else None if norm_coef is None else norm_coef.device
-    if dev is None:
+    if not grads and norm_coef is None:
         raise ValueError("no gradients: pass norm_coef to say where the norm goes")
-    for i, g in enumerate(grads):
-        if g.dtype not in _TYPES or g.device != dev or not g.is_contiguous():
-            raise ValueError(f"grads[{i}] must be a contiguous float32 or bfloat16 tensor on {dev}")
+    dev = grads[0].device if grads else norm_coef.device
+    index, n = grads[0].get_device() if grads else dev.index, len(grads)
+    # a call may have hundreds of tensors: whole lists at a time, and a loop
+    # only to name the one that is wrong
+    Tensor = torch.Tensor
+    dtypes = [g.dtype for g in grads]
+    kinds = set(dtypes)
+    sizes = [g.numel() for g in grads]
+    if not kinds <= _TYPES.keys() or not all(map(Tensor.is_contiguous, grads)) or \
+            {g.get_device() for g in grads} - {index}:
+        for i, g in enumerate(grads):
+            if g.dtype not in _TYPES or g.get_device() != index or not g.is_contiguous():
+                raise ValueError(f"grads[{i}] must be a contiguous float32 or bfloat16 tensor "
+                                 f"on {dev}")
     if dev.type != "cuda":
         raise ValueError("grads must be CUDA tensors")
-    n = len(grads)
     outs = None
     if out is not None:
         out = list(out)
         if len(out) != n:
             raise ValueError(f"out holds {len(out)} tensors, grads {n}")
-        for i, (g, o) in enumerate(zip(grads, out)):
-            if o.dtype != g.dtype or o.device != dev or not o.is_contiguous() or \
-                    o.numel() != g.numel():
-                raise ValueError(f"out[{i}] must be as grads[{i}]: same type, device and size")
-        outs = (_vp * n)(*[o.data_ptr() for o in out])
+        if [o.dtype for o in out] != dtypes or [o.numel() for o in out] != sizes or \
+                not all(map(Tensor.is_contiguous, out)) or \
+                {o.get_device() for o in out} - {index}:
+            for i, o in enumerate(out):
+                if o.dtype != dtypes[i] or o.numel() != sizes[i] or not o.is_contiguous() or \
+                        o.get_device() != index:
+                    raise ValueError(f"out[{i}] must be as grads[{i}]: same type, device and size")
+        outs = array.array("Q", [o.data_ptr() for o in out])
     _fit(dev, (norm_coef, "norm_coef", torch.float32, 2))
-    if norm_coef is None:
-        norm_coef = torch.empty(2, dtype=torch.float32, device=dev)
-    ws, ws_bytes = _scratch(workspace, _lib.moe_clip_grad_norm_workspace_size(), dev)
-    _check(_on(dev, _lib.moe_clip_grad_norm, (_vp * n)(*[g.data_ptr() for g in grads]), outs,
-               (_i64 * n)(*[g.numel() for g in grads]),
-               (_i32 * n)(*[_TYPES[g.dtype] for g in grads]), n,
-               -1.0 if max_norm is None else max_norm, int(norm_type == math.inf), eps,
-               norm_coef.data_ptr(), _ptr(ws), ws_bytes, _raw_stream(stream, dev)),
+    if norm_coef is None and workspace is None:
+        # one allocation: the two results, then the workspace
+        norm_coef = torch.empty(4 + _CLIP_WORKSPACE // 4, dtype=torch.float32, device=dev)
+        result, ws_bytes = norm_coef.data_ptr(), _CLIP_WORKSPACE
+        ws_at = result + 16
+    else:
+        if norm_coef is None:
+            norm_coef = torch.empty(2, dtype=torch.float32, device=dev)
+        ws, ws_bytes = _scratch(workspace, _CLIP_WORKSPACE, dev)
+        result, ws_at = norm_coef.data_ptr(), _ptr(ws)
+    ptrs = array.array("Q", [g.data_ptr() for g in grads])
+    numels = array.array("q", sizes)
+    codes = array.array("i", [_TYPES[d] for d in (kinds if len(kinds) == 1 else dtypes)])
+    if len(kinds) == 1:
+        codes *= n
+    at = array.array.buffer_info
+    _check(_on(dev, _lib.moe_clip_grad_norm, at(ptrs)[0], None if outs is None else at(outs)[0],
+               at(numels)[0], at(codes)[0], n, -1.0 if max_norm is None else max_norm,
+               norm_type == math.inf, eps, result, ws_at, ws_bytes, _raw_stream(stream, dev)),
            "moe_clip_grad_norm")
-    return norm_coef[0:1], norm_coef[1:2]
+    flat = norm_coef.reshape(-1) if norm_coef.dim() != 1 else norm_coef
+    return flat[:1], flat[1:2]
 
 
 def moe_grad_norm(grads, norm_type=2.0, norm_coef=None, workspace=None, stream=None):

@@ -1,5 +1,18 @@
-// clip.cu - moe_clip_grad_norm: one norm over many gradients, and all of
-// them scaled by it.
+// clip.cu - moe_clip_grad_norm: one norm over many gradients, and all of them
+// scaled by it.
+//
+// Two launches: clip_norm_kernel reads every gradient and leaves one partial
+// result a CTA, clip_scale_kernel adds these up in every CTA, each for itself
+// (a few hundred values, one warp), and scales. Both walk the same items, 16 KB
+// of one tensor each, the second in the opposite order: what the first read
+// last is still in L2. The tensors' table travels in the kernels' parameters.
+// Up to 16 items (256 KB) are one launch of one cluster, clip_small_kernel,
+// which keeps them in registers between the norm and the scaling.
+//
+// Bound by HBM: a gradient is read twice and written once (12 bytes an element
+// in float), the second read from L2 as far as the 129 MB hold. Double
+// precision runs at 1/64 of float's rate here, so the long sums are kept as
+// pairs of floats (a sum and what its roundings lost).
 #include "common.cuh"
 #include "internal.h"
 
@@ -7,25 +20,31 @@ namespace moe {
 namespace {
 
 constexpr int kClipThreads = 256;
-constexpr int kClipChunk = 16384;          // elements of one work item
-constexpr int kClipTensors = 256;          // tensors of one launch's table
-constexpr int kClipMaxCtas = 2048;         // partial results in the workspace
+constexpr int kClipCtas = 4;               // of an SM: 3 to 5, 256 or 512 threads and items of 16
+                                           // or 32 KB measured within 5% of each other
+constexpr int kItemBytes = 16384;
+constexpr int kLoads = kItemBytes / 16 / kClipThreads;   // 16-byte words of a thread
+constexpr int kClipMaxCtas = 1024;         // partial results in the workspace
+constexpr int kSmallCtas = 8, kSmallItems = 2;   // the one cluster's
+constexpr int64_t kMaxNumel = static_cast<int64_t>(1) << 40;
 
+template <int N>
 struct ClipTable {
-  const void* src[kClipTensors];
-  void* dst[kClipTensors];
-  int64_t numel[kClipTensors];
-  int64_t chunk0[kClipTensors + 1];        // first work item of each tensor
-  uint8_t type[kClipTensors];
+  const void* src[N];
+  void* dst[N];
+  int64_t numel[N];
+  int item0[N + 1];                        // first item of each tensor
+  uint8_t type[N];
   int n;
 };
 
-// The tensor whose work items hold c.
-__device__ __forceinline__ int clip_find(const ClipTable& t, int64_t c) {
+// The tensor that item c belongs to.
+template <int N>
+__device__ __forceinline__ int clip_find(const ClipTable<N>& t, int c) {
   int lo = 0, hi = t.n;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (t.chunk0[mid] <= c)
+    if (t.item0[mid] <= c)
       lo = mid;
     else
       hi = mid;
@@ -33,89 +52,408 @@ __device__ __forceinline__ int clip_find(const ClipTable& t, int64_t c) {
   return lo;
 }
 
-__device__ __forceinline__ float clip_load(const ClipTable& t, int i, int64_t at) {
-  return t.type[i] == MOE_TYPE_F32
-             ? static_cast<const float*>(t.src[i])[at]
-             : __bfloat162float(static_cast<const __nv_bfloat16*>(t.src[i])[at]);
+// Elements before the first 16-byte boundary (all of a short tensor): they go
+// with the tensor's first item.
+__host__ __device__ __forceinline__ int64_t head_of(const void* p, int shift, int64_t numel) {
+  const int64_t head = ((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) >> shift;
+  return head < numel ? head : numel;
 }
+__host__ __device__ __forceinline__ int64_t items_of(const void* p, int shift, int64_t numel) {
+  const int64_t body = (numel - head_of(p, shift, numel)) << shift;
+  return body > kItemBytes ? (body + kItemBytes - 1) / kItemBytes : 1;
+}
+
+// A sum of floats and what its roundings lost. An infinite sum stays one.
+struct Sum {
+  float s, lost;
+  __device__ __forceinline__ void add(float x) {
+    const float t = s + x, b = t - s;
+    lost += (s - (t - b)) + (x - b);
+    s = t;
+  }
+  __device__ __forceinline__ double value() const {
+    return isfinite(s) ? static_cast<double>(s) + lost : static_cast<double>(s);
+  }
+};
 
 // The larger of two magnitudes as bit patterns: a NaN is above every number.
 __device__ __forceinline__ unsigned max_bits(unsigned m, float g) {
   return max(m, __float_as_uint(g) & 0x7fffffffu);
 }
 
-// Every CTA's part of the sum of squares (or of the largest magnitude, as
-// the value of its bits) into partial[blockIdx.x]; a later launch of the
-// same call (first = 0) adds to it, in the same order every time.
-__global__ void __launch_bounds__(kClipThreads)
-    clip_norm_kernel(const __grid_constant__ ClipTable t, int kind, int first,
-                     double* __restrict__ partial) {
-  __shared__ double sh[kClipThreads];
-  double sum = 0.0;
-  unsigned big = 0u;
-  const int64_t items = t.chunk0[t.n];
-  for (int64_t c = blockIdx.x; c < items; c += gridDim.x) {
-    const int i = clip_find(t, c);
-    const int64_t lo = (c - t.chunk0[i]) * kClipChunk;
-    const int64_t hi = min(t.numel[i], lo + kClipChunk);
-    float part = 0.0f;
-    for (int64_t at = lo + threadIdx.x; at < hi; at += kClipThreads) {
-      const float g = clip_load(t, i, at);
-      part = fmaf(g, g, part);
-      big = max_bits(big, g);
+__device__ __forceinline__ uint4 load_word(const void* p) {
+  uint4 q;
+  asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
+               : "l"(p)
+               : "memory");
+  return q;
+}
+
+// One thread's share of an item: kLoads words, all on their way at once.
+struct Words {
+  uint4 w[kLoads];
+  bool has[kLoads];
+};
+__device__ __forceinline__ Words load_words(const char* p, int words) {
+  Words r;
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const int at = threadIdx.x + i * kClipThreads;
+    r.has[i] = at < words;
+    r.w[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (r.has[i]) r.w[i] = load_word(p + static_cast<int64_t>(at) * 16);
+  }
+  return r;
+}
+
+// An item: its words, and the elements before (first item) and after (last
+// item) the tensor's words.
+struct Item {
+  const char* src;
+  char* dst;
+  int64_t body;              // byte offset of the words in the tensor
+  int words, head, tail;     // tail: elements after the words
+  int f32;
+};
+template <int N>
+__device__ __forceinline__ Item item_at(const ClipTable<N>& t, int c) {
+  const int i = clip_find(t, c);
+  Item it;
+  it.f32 = t.type[i] == MOE_TYPE_F32;
+  it.src = static_cast<const char*>(t.src[i]);
+  it.dst = static_cast<char*>(t.dst[i]);
+  const int shift = it.f32 ? 2 : 1;
+  const int64_t numel = t.numel[i], head = head_of(it.src, shift, numel);
+  const int k = c - t.item0[i];
+  const int64_t lo = static_cast<int64_t>(k) * kItemBytes, left = ((numel - head) << shift) - lo;
+  it.body = (head << shift) + lo;
+  it.words = static_cast<int>((left < kItemBytes ? left : kItemBytes) >> 4);
+  it.head = k == 0 ? static_cast<int>(head) : 0;
+  it.tail = left < kItemBytes ? static_cast<int>(left & 15) >> shift : 0;
+  return it;
+}
+
+__device__ __forceinline__ float element(const char* p, int f32, int64_t at) {
+  return f32 ? reinterpret_cast<const float*>(p)[at]
+             : __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p)[at]);
+}
+
+template <typename F>
+__device__ __forceinline__ void each(const uint4& q, int f32, F&& f) {
+  const unsigned w[4] = {q.x, q.y, q.z, q.w};
+  if (f32) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f(__uint_as_float(w[i]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f(__uint_as_float(w[i] << 16));
+      f(__uint_as_float(w[i] & 0xffff0000u));
     }
-    sum += part;
-  }
-  sh[threadIdx.x] = kind == 0 ? sum : static_cast<double>(big);
-  for (int o = kClipThreads / 2; o > 0; o >>= 1) {
-    __syncthreads();
-    if (threadIdx.x < o)
-      sh[threadIdx.x] = kind == 0 ? sh[threadIdx.x] + sh[threadIdx.x + o]
-                                  : fmax(sh[threadIdx.x], sh[threadIdx.x + o]);
-  }
-  if (threadIdx.x == 0) {
-    double v = sh[0];
-    if (!first) v = kind == 0 ? v + partial[blockIdx.x] : fmax(v, partial[blockIdx.x]);
-    partial[blockIdx.x] = v;
   }
 }
 
-__global__ void __launch_bounds__(32) clip_finish_kernel(const double* __restrict__ partial, int n,
-                                                         int kind, float max_norm, float eps,
-                                                         float* __restrict__ norm_coef) {
-  double v = 0.0;
-  for (int i = threadIdx.x; i < n; i += 32) v = kind == 0 ? v + partial[i] : fmax(v, partial[i]);
+// One thread's squares (kInf: largest magnitude) of an item.
+template <bool kInf>
+__device__ __forceinline__ void take_item(const Item& it, const Words& q, Sum* sum, unsigned* big) {
+  float part[4] = {};
+  int k = 0;
+  auto take = [&](float g) {
+    if (kInf)
+      *big = max_bits(*big, g);
+    else
+      part[k & 3] = fmaf(g, g, part[k & 3]);
+    ++k;
+  };
+#pragma unroll
+  for (int u = 0; u < kLoads; ++u) each(q.w[u], it.f32, take);
+  if (threadIdx.x < it.head) take(element(it.src, it.f32, threadIdx.x));
+  if (threadIdx.x < it.tail)
+    take(element(it.src + it.body + it.words * 16, it.f32, threadIdx.x));
+  if (!kInf) sum->add((part[0] + part[1]) + (part[2] + part[3]));
+}
+
+// The CTA's result from its threads', in thread 0; sh: one value a warp.
+template <bool kInf>
+__device__ __forceinline__ double cta_result(Sum sum, unsigned big, double* sh) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    const double x = __shfl_xor_sync(0xffffffffu, v, o);
-    v = kind == 0 ? v + x : fmax(v, x);
+    if (kInf) {
+      big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
+    } else {
+      const float s = __shfl_xor_sync(0xffffffffu, sum.s, o);
+      const float l = __shfl_xor_sync(0xffffffffu, sum.lost, o);
+      sum.add(s);
+      sum.lost += l;
+    }
   }
+  if (lane_id() == 0) sh[threadIdx.x >> 5] = kInf ? static_cast<double>(big) : sum.value();
+  __syncthreads();
+  double v = 0.0;
+  if (threadIdx.x == 0)
+#pragma unroll
+    for (int w = 0; w < kClipThreads / 32; ++w) v = kInf ? fmax(v, sh[w]) : v + sh[w];
+  return v;
+}
+
+// Every CTA's part of the sum of squares (kInf: of the largest magnitude, as
+// the value of its bits) into partial[blockIdx.x]; a later launch of the same
+// call (first = 0) adds to it, in the same order every time.
+template <int N, bool kInf>
+__global__ void __launch_bounds__(kClipThreads, kClipCtas)
+    clip_norm_kernel(const __grid_constant__ ClipTable<N> t, int first,
+                     double* __restrict__ partial) {
+  __shared__ double sh[kClipThreads / 32];
+  Sum sum = {0.0f, 0.0f};
+  unsigned big = 0u;
+  const int items = t.item0[t.n];
+  for (int c = blockIdx.x; c < items; c += gridDim.x) {
+    const Item it = item_at(t, c);
+    take_item<kInf>(it, load_words(it.src + it.body, it.words), &sum, &big);
+  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const double v = cta_result<kInf>(sum, big, sh);
   if (threadIdx.x == 0) {
-    const double norm = kind == 0 ? sqrt(v) : __uint_as_float(static_cast<unsigned>(v));
-    const double c = max_norm / (norm + eps);
-    norm_coef[0] = static_cast<float>(norm);
-    norm_coef[1] = max_norm < 0.0f || c >= 1.0 ? 1.0f : static_cast<float>(c);
+    const double old = first ? 0.0 : partial[blockIdx.x];
+    partial[blockIdx.x] = kInf ? fmax(old, v) : old + v;
   }
 }
 
-__global__ void __launch_bounds__(kClipThreads)
-    clip_scale_kernel(const __grid_constant__ ClipTable t, int in_place,
-                      const float* __restrict__ norm_coef) {
-  const float coef = norm_coef[1];
-  if (in_place && coef == 1.0f) return;
-  const int64_t items = t.chunk0[t.n];
-  for (int64_t c = blockIdx.x; c < items; c += gridDim.x) {
-    const int i = clip_find(t, c);
-    const int64_t lo = (c - t.chunk0[i]) * kClipChunk;
-    const int64_t hi = min(t.numel[i], lo + kClipChunk);
-    for (int64_t at = lo + threadIdx.x; at < hi; at += kClipThreads) {
-      const float g = clip_load(t, i, at) * coef;
-      if (t.type[i] == MOE_TYPE_F32)
-        static_cast<float*>(t.dst[i])[at] = g;
-      else
-        static_cast<__nv_bfloat16*>(t.dst[i])[at] = __float2bfloat16_rn(g);
+struct ClipHow {
+  const double* partial;
+  float* norm_coef;
+  int parts, inf, in_place;
+  float max_norm, eps;
+};
+
+// norm and coef from the whole sum of squares (or the largest magnitude's bits).
+__device__ __forceinline__ float2 norm_and_coef(const ClipHow& h, double s) {
+  float norm;
+  if (h.inf)
+    norm = __uint_as_float(static_cast<unsigned>(s));
+  else                       // a sum beyond float's range, but with a root in it
+    norm = s > 1e38 ? sqrtf(static_cast<float>(s * 0x1p-60)) * 0x1p30f
+                    : sqrtf(static_cast<float>(s));
+  const float c = h.max_norm / (norm + h.eps);
+  return make_float2(norm, h.max_norm < 0.0f || c >= 1.0f ? 1.0f : c);     // a NaN stays one
+}
+
+// The coefficient from the partial results, by the first warp, to every thread.
+__device__ __forceinline__ float clip_coef(const ClipHow& h, bool write) {
+  __shared__ float sh;
+  if (threadIdx.x < 32) {
+    double v[4] = {};
+    for (int i = threadIdx.x; i < h.parts; i += 128)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int j = i + 32 * u;
+        const double x = j < h.parts ? __ldcg(h.partial + j) : 0.0;
+        v[u] = h.inf ? fmax(v[u], x) : v[u] + x;
+      }
+    double s = h.inf ? fmax(fmax(v[0], v[1]), fmax(v[2], v[3])) : (v[0] + v[1]) + (v[2] + v[3]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const double x = __shfl_xor_sync(0xffffffffu, s, o);
+      s = h.inf ? fmax(s, x) : s + x;
+    }
+    if (threadIdx.x == 0) {
+      const float2 r = norm_and_coef(h, s);
+      sh = r.y;
+      if (write) {
+        h.norm_coef[0] = r.x;
+        h.norm_coef[1] = r.y;
+      }
     }
   }
+  __syncthreads();
+  return sh;
+}
+
+// An item times coef, to its tensor's destination.
+__device__ __forceinline__ void scale_item(const Item& it, const Words& q, float coef) {
+  auto put = [&](int64_t at, float g) {
+    if (it.f32)
+      reinterpret_cast<float*>(it.dst)[at] = g * coef;
+    else
+      reinterpret_cast<__nv_bfloat16*>(it.dst)[at] = __float2bfloat16_rn(g * coef);
+  };
+  const int shift = it.f32 ? 2 : 1;
+  const bool alike =
+      ((reinterpret_cast<uintptr_t>(it.dst) ^ reinterpret_cast<uintptr_t>(it.src)) & 15) == 0;
+#pragma unroll
+  for (int u = 0; u < kLoads; ++u) {
+    if (!q.has[u]) continue;
+    const int64_t at = it.body + (threadIdx.x + u * kClipThreads) * 16;
+    if (alike) {
+      float g[8];
+      int k = 0;
+      each(q.w[u], it.f32, [&](float x) { g[k++] = x * coef; });
+      uint4 w;
+      if (it.f32)
+        w = make_uint4(__float_as_uint(g[0]), __float_as_uint(g[1]), __float_as_uint(g[2]),
+                       __float_as_uint(g[3]));
+      else
+        w = make_uint4(pack_bf16x2(g[0], g[1]), pack_bf16x2(g[2], g[3]), pack_bf16x2(g[4], g[5]),
+                       pack_bf16x2(g[6], g[7]));
+      *reinterpret_cast<uint4*>(it.dst + at) = w;
+    } else {
+      int64_t e = at >> shift;                     // another alignment: element by element
+      each(q.w[u], it.f32, [&](float x) { put(e++, x); });
+    }
+  }
+  if (threadIdx.x < it.head) put(threadIdx.x, element(it.src, it.f32, threadIdx.x));
+  if (threadIdx.x < it.tail) {
+    const int64_t at = ((it.body + it.words * 16) >> shift) + threadIdx.x;
+    put(at, element(it.src, it.f32, at));
+  }
+}
+
+template <int N>
+__global__ void __launch_bounds__(kClipThreads, kClipCtas)
+    clip_scale_kernel(const __grid_constant__ ClipTable<N> t, const __grid_constant__ ClipHow h) {
+  const int items = t.item0[t.n];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const float coef = clip_coef(h, blockIdx.x == 0);
+  if (h.in_place && coef == 1.0f) return;
+  for (int c = items - 1 - static_cast<int>(blockIdx.x); c >= 0; c -= gridDim.x) {
+    const Item it = item_at(t, c);
+    scale_item(it, load_words(it.src + it.body, it.words), coef);
+  }
+}
+
+// The whole call by one cluster: every CTA keeps its items in registers while
+// the CTAs' sums meet.
+template <int N, bool kInf>
+__global__ void __launch_bounds__(kClipThreads, 1)
+    clip_small_kernel(const __grid_constant__ ClipTable<N> t, const __grid_constant__ ClipHow h) {
+  __shared__ double sh[kClipThreads / 32];
+  __shared__ double mine;
+  __shared__ float sh_coef;
+  const int items = t.item0[t.n];
+  Sum sum = {0.0f, 0.0f};
+  unsigned big = 0u;
+  Item it[kSmallItems];
+  Words q[kSmallItems];
+#pragma unroll
+  for (int i = 0; i < kSmallItems; ++i) {
+    const int c = blockIdx.x + i * gridDim.x;
+    it[i] = Item{};
+    if (c < items) it[i] = item_at(t, c);
+    q[i] = load_words(it[i].src + it[i].body, it[i].words);
+  }
+#pragma unroll
+  for (int i = 0; i < kSmallItems; ++i) take_item<kInf>(it[i], q[i], &sum, &big);
+  const double v = cta_result<kInf>(sum, big, sh);
+  if (threadIdx.x == 0) mine = v;
+  cluster_sync();
+  if (threadIdx.x == 0) {
+    double s = 0.0;
+    for (unsigned c = 0; c < gridDim.x; ++c) {
+      const double x = ld_cluster_f64(smem_u32(&mine), c);
+      s = kInf ? fmax(s, x) : s + x;
+    }
+    const float2 r = norm_and_coef(h, s);
+    sh_coef = r.y;
+    if (blockIdx.x == 0) {
+      h.norm_coef[0] = r.x;
+      h.norm_coef[1] = r.y;
+    }
+  }
+  cluster_sync();
+  const float coef = sh_coef;
+  if (h.in_place && coef == 1.0f) return;
+#pragma unroll
+  for (int i = 0; i < kSmallItems; ++i)
+    if (blockIdx.x + i * gridDim.x < items) scale_item(it[i], q[i], coef);
+}
+
+struct ClipCall {
+  const void* const* grads;
+  void* const* outs;
+  const int64_t* numels;
+  const int* types;
+  int64_t n;
+  float max_norm, eps;
+  int inf;
+  float* norm_coef;
+  double* partial;
+  cudaStream_t st;
+};
+
+// The next table of up to N tensors from i on, empty ones left out.
+template <int N>
+void fill_table(const ClipCall& c, int64_t* i, ClipTable<N>* t) {
+  int n = 0;
+  int64_t items = 0;
+  t->item0[0] = 0;
+  for (; *i < c.n && n < N; ++*i) {
+    const int64_t numel = c.numels[*i];
+    if (numel == 0) continue;
+    const int64_t more = items_of(c.grads[*i], c.types[*i] == MOE_TYPE_F32 ? 2 : 1, numel);
+    if (items + more > INT32_MAX) break;           // the next launch's
+    items += more;
+    t->src[n] = c.grads[*i];
+    t->dst[n] = c.outs ? c.outs[*i] : const_cast<void*>(c.grads[*i]);
+    t->numel[n] = numel;
+    t->type[n] = static_cast<uint8_t>(c.types[*i]);
+    t->item0[++n] = static_cast<int>(items);
+  }
+  t->n = n;
+}
+
+template <int N>
+cudaError_t clip(const ClipCall& c) {
+  ClipTable<N> t;
+  const int most = device_sm_count() * kClipCtas < kClipMaxCtas ? device_sm_count() * kClipCtas
+                                                                 : kClipMaxCtas;
+  int64_t i = 0;
+  fill_table(c, &i, &t);
+  const bool one = i >= c.n;                       // the whole call in one table
+  const int all = t.item0[t.n];
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.blockDim = dim3(kClipThreads);
+  cfg.stream = c.st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  ClipHow h = {c.partial, c.norm_coef, 0, c.inf, c.outs == nullptr, c.max_norm, c.eps};
+  if (one && all <= kSmallCtas * kSmallItems) {
+    const int ctas = all < kSmallCtas ? (all > 0 ? all : 1) : kSmallCtas;
+    cfg.gridDim = dim3(ctas);
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ctas;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    return c.inf ? cudaLaunchKernelEx(&cfg, clip_small_kernel<N, true>, t, h)
+                 : cudaLaunchKernelEx(&cfg, clip_small_kernel<N, false>, t, h);
+  }
+  // one partial result a CTA; with several tables each launch has them all
+  const int parts = h.parts = one && all < most ? all : most;
+  for (bool first = true;; first = false) {
+    if (c.inf)
+      clip_norm_kernel<N, true><<<parts, kClipThreads, 0, c.st>>>(t, first, c.partial);
+    else
+      clip_norm_kernel<N, false><<<parts, kClipThreads, 0, c.st>>>(t, first, c.partial);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    if (i >= c.n) break;
+    fill_table(c, &i, &t);
+  }
+  const bool norm_only = c.max_norm < 0.0f && !c.outs;
+  // comes up while the norm's last CTAs still run, and waits for all of them
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  if (!one) i = 0;
+  do {
+    if (!one) fill_table(c, &i, &t);
+    if (norm_only) t.n = t.item0[0] = 0;
+    const int ctas = t.item0[t.n] < most ? t.item0[t.n] : most;
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas > 0 ? ctas : 1));
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, clip_scale_kernel<N>, t, h);
+    if (e != cudaSuccess || norm_only) return e;
+    cfg.numAttrs = 0;
+  } while (i < c.n);
+  return cudaSuccess;
 }
 
 }  // namespace
@@ -137,7 +475,7 @@ moe_status moe_clip_grad_norm(const void* const* grads, void* const* outs, const
     return MOE_ERR_INVALID_ARG;
   if (n_tensors > 0 && (!grads || !numels || !types)) return MOE_ERR_INVALID_ARG;
   for (int64_t i = 0; i < n_tensors; ++i) {
-    if (numels[i] < 0 || numels[i] > (static_cast<int64_t>(1) << 48) ||
+    if (numels[i] < 0 || numels[i] > kMaxNumel ||
         (types[i] != MOE_TYPE_F32 && types[i] != MOE_TYPE_BF16))
       return MOE_ERR_INVALID_ARG;
     if (numels[i] == 0) continue;
@@ -149,37 +487,14 @@ moe_status moe_clip_grad_norm(const void* const* grads, void* const* outs, const
   if (!workspace || ws_bytes < moe_clip_grad_norm_workspace_size() ||
       (reinterpret_cast<uintptr_t>(workspace) & 15))
     return MOE_ERR_WORKSPACE;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  double* partial = static_cast<double*>(workspace);
-  ClipTable t;
-  const int cap = device_sm_count() * 8 < kClipMaxCtas ? device_sm_count() * 8 : kClipMaxCtas;
-  for (int pass = 0; pass < 2; ++pass) {
-    if (pass == 1 && max_norm < 0.0f && !outs) break;
-    int launches = 0;
-    int64_t i = 0;
-    do {
-      t.n = 0;
-      t.chunk0[0] = 0;
-      for (; i < n_tensors && t.n < kClipTensors; ++i) {
-        if (numels[i] == 0) continue;
-        t.src[t.n] = grads[i];
-        t.dst[t.n] = outs ? outs[i] : const_cast<void*>(grads[i]);
-        t.numel[t.n] = numels[i];
-        t.type[t.n] = static_cast<uint8_t>(types[i]);
-        t.chunk0[t.n + 1] = t.chunk0[t.n] + (numels[i] + kClipChunk - 1) / kClipChunk;
-        ++t.n;
-      }
-      // every norm launch has the whole grid, so that all partials are written
-      if (pass == 0)
-        clip_norm_kernel<<<cap, kClipThreads, 0, st>>>(t, norm_kind, launches == 0, partial);
-      else if (t.n > 0)
-        clip_scale_kernel<<<cap, kClipThreads, 0, st>>>(t, outs == nullptr, norm_coef);
-      ++launches;
-    } while (i < n_tensors);
-    if (pass == 0)
-      clip_finish_kernel<<<1, 32, 0, st>>>(partial, cap, norm_kind, max_norm, eps, norm_coef);
-  }
-  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  const ClipCall c = {grads, outs, numels,   types,     n_tensors, max_norm,
+                      eps,   norm_kind, norm_coef, static_cast<double*>(workspace),
+                      static_cast<cudaStream_t>(stream)};
+  // the smallest table that holds them: its bytes go with every launch
+  const cudaError_t e = n_tensors <= 8     ? clip<8>(c)
+                        : n_tensors <= 100 ? clip<100>(c)
+                                           : clip<960>(c);
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -300,13 +300,21 @@ __device__ __forceinline__ uint32_t mapa_shared(uint32_t addr, uint32_t rank) {
   return r;
 }
 
-// A 32-bit word of the shared memory of the CTA of cluster rank `rank`, at the
+// A 32-bit word (and a double) of the shared memory of the CTA of cluster rank `rank`, at the
 // offset of this CTA's shared-memory address `addr`.
 __device__ __forceinline__ int ld_cluster_s32(uint32_t addr, uint32_t rank) {
   uint32_t at;
   int v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
   asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ double ld_cluster_f64(uint32_t addr, uint32_t rank) {
+  uint32_t at;
+  double v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(at) : "memory");
   return v;
 }
 
