@@ -473,7 +473,7 @@ struct GateShape {
   static constexpr int kMost = W * C < 32 ? W * C : 32;        // the largest k
   static constexpr int kPicks = kMost + 1;                     // and the first one left out
   static constexpr int kSlots = (kMost + W - 1) / W;           // k over W lanes
-  static constexpr int kCtas = C > 16 ? 2 : C > 8 ? 3 : 4;     // of an SM, by registers
+  static constexpr int kCtas = C > 16 ? 2 : 4;                 // of an SM, by registers
 };
 
 // ------------------------------------------------------------------ forward
@@ -779,6 +779,7 @@ __global__ void __launch_bounds__((GateShape<W, C>::kWarps * 32), (GateShape<W, 
   } else {
     __shared__ int is_last;
     int* total = scratch + 64;
+    asm volatile("griddepcontrol.wait;" ::: "memory");         // gate_zero_kernel's zeros
     for (int e = threadIdx.x; e < p.E; e += blockDim.x)
       if (hist[e]) atomicAdd(total + e, hist[e]);
     __threadfence();
@@ -809,13 +810,19 @@ __global__ void __launch_bounds__((GateShape<W, C>::kWarps * 32), (GateShape<W, 
   }
 }
 
+// Zeroes the ticket and the totals while gate_kernel already runs beside it.
+__global__ void __launch_bounds__(256) gate_zero_kernel(int32_t* scratch, int n) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  for (int i = threadIdx.x; i < n; i += blockDim.x) scratch[i] = 0;
+}
+
 // ------------------------------------------------------------------ backward
 
 // W lanes of C experts share a token, as forward. The slots' gradients go
 // through a row of shared memory, zero between tokens, to the lanes that own
 // their experts; every lane then writes its C columns.
 template <typename L, int W, int C>
-__global__ void __launch_bounds__((GateShape<W, C>::kWarps * 32), (GateShape<W, C>::kCtas))
+__global__ void __launch_bounds__((GateShape<W, C>::kWarps * 32), (C > 8 ? 2 : 4))
     gate_backward_kernel(const __grid_constant__ GateParams p, const float* __restrict__ dprobs,
                          const int32_t* __restrict__ ids, L* __restrict__ dlogits, int vec_out,
                          int* err) {
@@ -982,26 +989,29 @@ cudaError_t launch_gate(const GateParams& p, int32_t* ids, float* probs, int32_t
   const int64_t want = GateCtas{p.T}.operator()<W, C>();
   const size_t smem = static_cast<size_t>(G::kWarps) * p.E * sizeof(double) + p.E * sizeof(int);
   auto* kernel = p.bias || p.n_group > 1 ? gate_kernel<L, W, C, true> : gate_kernel<L, W, C, false>;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.blockDim = dim3(G::kWarps * 32);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
   if (want <= kMaxCluster) {
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3(static_cast<unsigned>(want));
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = static_cast<unsigned>(want);
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(want));
-    cfg.blockDim = dim3(G::kWarps * 32);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, p, ids, probs, counts, offsets, scratch, 1);
   }
-  cudaError_t e = cudaMemsetAsync(scratch, 0, gate_scratch_bytes(p.E), st);
+  gate_zero_kernel<<<1, 256, 0, st>>>(scratch, static_cast<int>(gate_scratch_bytes(p.E) / 4));
+  const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
+  // beside the zeroing; it waits for it before it counts
   const int64_t cap = static_cast<int64_t>(device_sm_count()) * G::kCtas;
-  kernel<<<static_cast<unsigned>(want < cap ? want : cap), G::kWarps * 32, smem, st>>>(
-      p, ids, probs, counts, offsets, scratch, 0);
-  return cudaGetLastError();
+  cfg.gridDim = dim3(static_cast<unsigned>(want < cap ? want : cap));
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p, ids, probs, counts, offsets, scratch, 0);
 }
 
 template <typename L, int W, int C>
