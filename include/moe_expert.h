@@ -638,8 +638,8 @@ void moe_norm_config_init(moe_norm_config* cfg);
  *  n       bf16 [T, H]   out
  *  rstd_y  float [T]     out with w_post, else not written (may be NULL)
  *  rstd_out float [T]    out with w_next, else not written (may be NULL)
- * Any H from 1 to 65536; with H % 8 == 0 and at most 16384 (8192 with a
- * float stream) rows are read once. T = 0 does nothing.
+ * Any H from 1 to 65536; rows with H % 8 == 0 and H <= 32768 (16384 with a
+ * float stream) are read once, others up to three times. T = 0 does nothing.
  * ------------------------------------------------------------------------ */
 moe_status moe_norm_residual(const void* x, const void* y, const void* w_post, const void* gate,
                              int64_t gate_rows, const void* w_next, int64_t T, int H,
@@ -671,8 +671,8 @@ moe_status moe_norm_residual(const void* x, const void* y, const void* w_post, c
  *          when accumulate_dw
  *  workspace >= moe_norm_residual_backward_workspace_size(T, H, gate_rows)
  *          bytes, 16-byte aligned
- * Same limits as moe_norm_residual. T = 0 writes zero weight gradients (or
- * leaves them when accumulating).
+ * Same H as moe_norm_residual; rows with H % 8 == 0 and H <= 8192 are read
+ * once. T = 0 writes zero weight gradients (or leaves them when accumulating).
  * ------------------------------------------------------------------------ */
 size_t moe_norm_residual_backward_workspace_size(int64_t T, int H, int64_t gate_rows);
 moe_status moe_norm_residual_backward(const void* d_out, const void* d_n, const void* out,
