@@ -3,22 +3,21 @@
 // memory.
 //
 // A group of threads (whole warps) walks a strip of consecutive rows, every
-// thread with 4 V fixed columns (V vectors of four, so that all accesses are
-// coalesced for float and for bf16): V = 2 forward, V = 4 backward, where the
-// registers of the pointers and counters would leave too few for the columns
-// of a thread with eight. What belongs to a column stays in its registers from
-// row to row: the weights, b w_post g as one factor, and the column sums of the
-// weight gradients. A row's tensors lie in one stage of the group's ring, which
-// its first thread fills with bulk copies up to three rows ahead; each is read
-// from HBM once. A CTA has as many groups as its threads hold, one CTA an SM,
-// so that short rows too have enough bytes on their way, and the groups'
-// column sums are added up in shared memory: the finishing kernel finds one
-// row of partial sums an SM.
+// thread with sixteen fixed columns: two vectors of eight in bf16, four of four
+// with a float stream, so that all accesses are 16 bytes and coalesced. What
+// belongs to a column stays in its registers from row to row: the weights,
+// b w_post g as one factor, and the column sums of the weight gradients. A
+// row's tensors lie in one stage of the group's ring, which its first thread
+// fills with bulk copies up to three rows ahead; each is read from HBM once. A
+// CTA has as many groups as 512 threads hold, one CTA an SM, so that short rows
+// too have enough bytes on their way, and the groups' column sums are added up
+// in shared memory: the finishing kernel finds one row of partial sums an SM.
 //
 // Bound by HBM, 8 bytes an element forward and 12 backward in bf16 (18 with a
 // float stream), where a row's instructions stay below its bytes' time: pairs
 // of columns go through the packed float instructions (fma.rn.f32x2), which
-// round each half as the single ones do.
+// round each half as the single ones do, and the backward's two means, of which
+// the second needs the first, come from one reduction of three sums.
 #include "norm.cuh"
 
 namespace moe {
@@ -27,10 +26,10 @@ int* device_error_word();
 
 namespace {
 
-constexpr int kSharedBytes = 216 * 1024;  // of the rings, and what lies behind them
+constexpr int kSharedBytes = 208 * 1024;  // of the rings, and what lies behind them
 constexpr int kMaxStages = 4;
-constexpr int kForwardVecs = 2, kBackwardVecs = 4;
-constexpr int ring_threads(int V) { return 2048 / V; }
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kCols = 16;                 // of a thread
 
 struct RingParams {
   NormParams n;
@@ -70,51 +69,107 @@ __device__ __forceinline__ float sum2(Pair a) {
   return f.x + f.y;
 }
 
-struct Four {
-  Pair p[2];
+// W columns, as floats and (bf16) as they are stored.
+template <int W>
+struct Vec {
+  Pair p[W / 2];
+};
+template <int W>
+struct Half {
+  unsigned u[W / 2];
 };
 
-__device__ __forceinline__ Pair widen(unsigned q) {
-  return pair(__uint_as_float(q << 16), __uint_as_float(q & 0xffff0000u));
+template <int W>
+__device__ __forceinline__ Vec<W> widen(const Half<W>& h) {
+  Vec<W> v;
+#pragma unroll
+  for (int i = 0; i < W / 2; ++i)
+    v.p[i] = pair(__uint_as_float(h.u[i] << 16), __uint_as_float(h.u[i] & 0xffff0000u));
+  return v;
 }
-__device__ __forceinline__ Four widen(uint2 q) { return Four{{widen(q.x), widen(q.y)}}; }
+template <int W>
+__device__ __forceinline__ Half<W> get_half(const unsigned char* p) {
+  if constexpr (W == 8) {
+    const uint4 q = *reinterpret_cast<const uint4*>(p);
+    return Half<W>{{q.x, q.y, q.z, q.w}};
+  } else {
+    const uint2 q = *reinterpret_cast<const uint2*>(p);
+    return Half<W>{{q.x, q.y}};
+  }
+}
 
-// Four elements in shared memory, and to global memory.
-template <typename T>
-__device__ __forceinline__ Four get4(const unsigned char* p) {
-  if constexpr (sizeof(T) == 4) {
-    const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(p);
-    return Four{{q.x, q.y}};
-  } else {
-    return widen(*reinterpret_cast<const uint2*>(p));
+// A vector of the stream as it is stored: floats (W = 4) or bf16.
+template <typename ST>
+struct Stream {
+  static constexpr int W = sizeof(ST) == 4 ? 4 : 8;
+  static constexpr int V = kCols / W;
+  ulonglong2 f;
+  Half<W> h;
+  static __device__ __forceinline__ Stream get(const unsigned char* p) {
+    Stream s;
+    if constexpr (W == 4)
+      s.f = *reinterpret_cast<const ulonglong2*>(p);
+    else
+      s.h = get_half<W>(p);
+    return s;
   }
+  __device__ __forceinline__ Vec<W> wide() const {
+    if constexpr (W == 4)
+      return Vec<W>{{f.x, f.y}};
+    else
+      return widen<W>(h);
+  }
+};
+
+template <int W>
+__device__ __forceinline__ void put_half(unsigned char* p, const Vec<W>& v) {
+  unsigned u[W / 2];
+#pragma unroll
+  for (int i = 0; i < W / 2; ++i) {
+    const float2 f = halves(v.p[i]);
+    u[i] = pack_bf16x2(f.x, f.y);
+  }
+  if constexpr (W == 8)
+    *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+  else
+    *reinterpret_cast<uint2*>(p) = make_uint2(u[0], u[1]);
 }
-template <typename T>
-__device__ __forceinline__ void put4(unsigned char* p, const Four& v) {
-  if constexpr (sizeof(T) == 4) {
+template <typename ST, int W>
+__device__ __forceinline__ void put_stream(unsigned char* p, const Vec<W>& v) {
+  if constexpr (sizeof(ST) == 4)
     *reinterpret_cast<ulonglong2*>(p) = make_ulonglong2(v.p[0], v.p[1]);
-  } else {
-    const float2 a = halves(v.p[0]), b = halves(v.p[1]);
-    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(b.x, b.y));
-  }
+  else
+    put_half<W>(p, v);
 }
 
 // ------------------------------------------------------------------ groups and rings
 
-// The sum of v over a group to each of its threads; warps: of the group. The
-// barrier in it also tells that the group has read what it had to.
-template <int kWarps>
-__device__ __forceinline__ float group_sum(float v, float* red, int warp, int bar, int group) {
+// The sums of N values over a group to each of its threads. The barrier in it
+// also tells that the group has read what it had to.
+template <int N>
+__device__ __forceinline__ void group_sum(float (&v)[N], float4* red, int warp, int bar, int group) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if (group == 32) return v;
-  if (lane_id() == 0) red[warp] = v;
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+  if (group == 32) {
+    __syncwarp();
+    return;
+  }
+  if (lane_id() == 0)
+    red[warp] = make_float4(v[0], N > 1 ? v[N > 1 ? 1 : 0] : 0.0f, N > 2 ? v[N > 2 ? 2 : 0] : 0.0f,
+                            0.0f);
   asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(group) : "memory");
   const int at = lane_id() & (kWarps - 1);
-  v = at < (group >> 5) ? red[at] : 0.0f;
+  float4 r = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (at < (group >> 5)) r = red[at];
+  v[0] = r.x;
+  if (N > 1) v[N > 1 ? 1 : 0] = r.y;
+  if (N > 2) v[N > 2 ? 2 : 0] = r.z;
 #pragma unroll
-  for (int o = kWarps / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+  for (int o = kWarps / 2; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
 }
 
 __device__ __forceinline__ void group_barrier(int bar, int group) {
@@ -131,7 +186,7 @@ struct Walk {
   int64_t lo, hi;
   unsigned char* ring;
   uint32_t full;               // mbarriers of its stages
-  int col0, step;              // columns col0 + v step .. + 3 are the thread's
+  int col0, step;              // columns col0 + v step .. + W - 1 are the thread's
   bool has[V];
 };
 
@@ -152,8 +207,8 @@ __device__ __forceinline__ Walk<V> walk_of(const RingParams& p, unsigned char* r
   }
   w.ring = ring_all + static_cast<size_t>(w.g) * p.r.stages * p.row_bytes;
   w.full = smem_u32(&full_all[w.g][0]);
-  w.col0 = 4 * w.tid;
-  w.step = 4 * p.r.group;
+  w.col0 = (kCols / V) * w.tid;
+  w.step = (kCols / V) * p.r.group;
 #pragma unroll
   for (int v = 0; v < V; ++v) w.has[v] = kFull || w.col0 + v * w.step < w.H;
   if (threadIdx.x == 0) *abort_wait = 0;
@@ -168,21 +223,34 @@ __device__ __forceinline__ Walk<V> walk_of(const RingParams& p, unsigned char* r
 // f[columns] *= weights[row + columns]
 template <int V>
 __device__ __forceinline__ void times(const RingParams& p, const Walk<V>& w, const void* weights,
-                                      int64_t row, Pair (&f)[2 * V]) {
+                                      int64_t row, Pair (&f)[kCols / 2]) {
+  constexpr int W = kCols / V;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     if (!w.has[v]) continue;
     const int64_t at = row + w.col0 + v * w.step;
-    Four m;
+    Vec<W> m;
     if (p.n.weights_f32) {
-      const float4 q = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(weights) + at));
-      m = Four{{pair(q.x, q.y), pair(q.z, q.w)}};
+#pragma unroll
+      for (int i = 0; i < W / 4; ++i) {
+        const float4 q = __ldg(
+            reinterpret_cast<const float4*>(static_cast<const float*>(weights) + at) + i);
+        m.p[2 * i] = pair(q.x, q.y);
+        m.p[2 * i + 1] = pair(q.z, q.w);
+      }
     } else {
-      m = widen(__ldg(
-          reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(weights) + at)));
+      Half<W> h;
+#pragma unroll
+      for (int i = 0; i < W / 4; ++i) {
+        const uint2 q = __ldg(
+            reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(weights) + at) + i);
+        h.u[2 * i] = q.x;
+        h.u[2 * i + 1] = q.y;
+      }
+      m = widen<W>(h);
     }
-    f[2 * v] = mul2(f[2 * v], m.p[0]);
-    f[2 * v + 1] = mul2(f[2 * v + 1], m.p[1]);
+#pragma unroll
+    for (int i = 0; i < W / 2; ++i) f[v * (W / 2) + i] = mul2(f[v * (W / 2) + i], m.p[i]);
   }
 }
 
@@ -190,28 +258,28 @@ __device__ __forceinline__ void times(const RingParams& p, const Walk<V>& w, con
 // reported, and the waits after it are given up at once.
 template <int V>
 __device__ __forceinline__ void wait_stage(const RingParams& p, const Walk<V>& w, int stage,
-                                           int parity, unsigned long long* limit,
-                                           int* abort_wait) {
-  if (!mbar_wait(w.full + 8 * stage, parity, *limit, abort_wait)) {
+                                           int parity, bool* gave_up, int* abort_wait) {
+  if (mbar_try_wait(w.full + 8 * stage, parity)) return;
+  if (!mbar_wait(w.full + 8 * stage, parity, *gave_up ? 0 : kDefaultWaitNs, abort_wait)) {
     report_error(p.err, kErrTimeout);
-    *limit = 0;
+    *gave_up = true;
   }
 }
 
 // ------------------------------------------------------------------ forward
 
-template <typename ST, bool kMany, bool kFull>
-__global__ void __launch_bounds__(ring_threads(kForwardVecs), 1)
+// kAll: with y, w_post and w_next.
+template <typename ST, bool kMany, bool kFull, bool kAll>
+__global__ void __launch_bounds__(kThreads, 1)
     norm_ring_kernel(const __grid_constant__ RingParams p) {
-  constexpr int V = kForwardVecs, kWarps = ring_threads(V) / 32;
+  constexpr int W = Stream<ST>::W, V = Stream<ST>::V, P = W / 2, kSize = sizeof(ST);
   extern __shared__ __align__(128) unsigned char ring_all[];
-  __shared__ float red_all[kMaxRingGroups][4][kWarps];
+  __shared__ float4 red_all[kMaxRingGroups][4][kWarps];
   __shared__ __align__(8) uint64_t full_all[kMaxRingGroups][kMaxStages];
   __shared__ int abort_wait;
   const Walk<V> w = walk_of<V, kFull>(p, ring_all, full_all, &abort_wait);
   const NormParams& q = p.n;
-  const bool branch = q.y, post = q.w_post, next = q.w_next;
-  constexpr int kSize = sizeof(ST);
+  const bool branch = kAll || q.y, post = kAll || q.w_post, next = kAll || q.w_next;
   const int wide = w.H * kSize, half = w.H * 2;
   auto issue = [&](int64_t t, int stage) {
     const uint32_t bar = w.full + 8 * stage, to = smem_u32(w.ring) + stage * p.row_bytes;
@@ -222,9 +290,9 @@ __global__ void __launch_bounds__(ring_threads(kForwardVecs), 1)
   if (w.tid == 0)
     for (int i = 0; i < p.r.stages && w.lo + i < w.hi; ++i) issue(w.lo + i, i);
 
-  Pair gw[2 * V], wn[2 * V];
+  Pair gw[kCols / 2], wn[kCols / 2];
 #pragma unroll
-  for (int i = 0; i < 2 * V; ++i) {
+  for (int i = 0; i < kCols / 2; ++i) {
     gw[i] = pair(q.b);
     wn[i] = pair(1.0f);
   }
@@ -233,47 +301,52 @@ __global__ void __launch_bounds__(ring_threads(kForwardVecs), 1)
     if (post) times(p, w, q.w_post, 0, gw);
     if (q.gate) times(p, w, q.gate, 0, gw);
   }
-  int64_t gate_row = -1, gate_end = w.lo;
+  int64_t gate_row = -1;
+  int to_gate = 0;                                 // rows until another gate row
   if (kMany && w.lo < w.hi) gate_row = w.lo / q.gate_span - 1;
-  unsigned long long limit = kDefaultWaitNs;
+  bool gave_up = false;
   int stage = 0, parity = 0, odd = 0;
   unsigned char* to_out = static_cast<unsigned char*>(p.o.stream) + (w.lo * w.H + w.col0) * kSize;
   unsigned char* to_n = reinterpret_cast<unsigned char*>(p.o.branch) + (w.lo * w.H + w.col0) * 2;
-  const unsigned char* row_x = w.ring + w.col0 * kSize;
-  const unsigned char* row_y = w.ring + wide + w.col0 * 2;
+  const int rows = static_cast<int>(w.hi - w.lo);
   const Pair a = pair(q.a);
-  for (int64_t t = w.lo; t < w.hi; ++t, to_out += wide, to_n += half) {
-    if (kMany && t == gate_end) {
+  for (int t = 0; t < rows; ++t, to_out += wide, to_n += half) {
+    if (kMany && to_gate-- == 0) {
       ++gate_row;
-      gate_end = (gate_row + 1) * q.gate_span;
+      to_gate = static_cast<int>((gate_row + 1) * q.gate_span - (w.lo + t)) - 1;
 #pragma unroll
-      for (int i = 0; i < 2 * V; ++i) gw[i] = pair(q.b);
+      for (int i = 0; i < kCols / 2; ++i) gw[i] = pair(q.b);
       if (post) times(p, w, q.w_post, 0, gw);
       times(p, w, q.gate, gate_row * w.H, gw);
     }
-    wait_stage(p, w, stage, parity, &limit, &abort_wait);
-    const int base = stage * p.row_bytes;
-    Four x[V], y[V];
+    wait_stage(p, w, stage, parity, &gave_up, &abort_wait);
+    const unsigned char* row_x = w.ring + (stage * p.row_bytes + w.col0 * kSize);
+    const unsigned char* row_y = w.ring + (stage * p.row_bytes + wide + w.col0 * 2);
+    Vec<W> x[V], y[V];
     Pair s = pair(0.0f);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       if (!w.has[v]) continue;
-      x[v] = get4<ST>(row_x + (base + v * w.step * kSize));
+      x[v] = Stream<ST>::get(row_x + v * w.step * kSize).wide();
       if (branch) {
-        y[v] = get4<__nv_bfloat16>(row_y + (base + v * w.step * 2));
-        s = fma2(y[v].p[0], y[v].p[0], s);
-        s = fma2(y[v].p[1], y[v].p[1], s);
+        y[v] = widen<W>(get_half<W>(row_y + v * w.step * 2));
+#pragma unroll
+        for (int h = 0; h < P; ++h) s = fma2(y[v].p[h], y[v].p[h], s);
       }
     }
     float ry = 1.0f;
     if (post) {
-      const float m = group_sum<kWarps>(sum2(s), red_all[w.g][odd], w.warp, w.g + 1, p.r.group);
-      ry = 1.0f / sqrtf(fmaf(m, q.inv_h, q.eps));
-      if (w.tid == 0 && p.o.rstd_y) p.o.rstd_y[t] = ry;
+      float m[1] = {sum2(s)};
+      group_sum(m, red_all[w.g][odd], w.warp, w.g + 1, p.r.group);
+      ry = 1.0f / sqrtf(fmaf(m[0], q.inv_h, q.eps));
+    } else {
+      group_barrier(w.g + 1, p.r.group);
     }
-    if (!post || p.r.group == 32) group_barrier(w.g + 1, p.r.group);
     // every thread has the row in registers: its stage takes another
-    if (w.tid == 0 && t + p.r.stages < w.hi) issue(t + p.r.stages, stage);
+    if (w.tid == 0) {
+      if (t + p.r.stages < rows) issue(w.lo + t + p.r.stages, stage);
+      if (post && p.o.rstd_y) p.o.rstd_y[w.lo + t] = ry;
+    }
     s = pair(0.0f);
     const Pair r = pair(ry);
 #pragma unroll
@@ -281,25 +354,25 @@ __global__ void __launch_bounds__(ring_threads(kForwardVecs), 1)
       if (!w.has[v]) continue;
       if (branch) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          x[v].p[h] = fma2(mul2(y[v].p[h], r), gw[2 * v + h], mul2(a, x[v].p[h]));
-        put4<ST>(to_out + v * w.step * kSize, x[v]);
+        for (int h = 0; h < P; ++h)
+          x[v].p[h] = fma2(mul2(y[v].p[h], r), gw[P * v + h], mul2(a, x[v].p[h]));
+        put_stream<ST, W>(to_out + v * w.step * kSize, x[v]);
       }
-      s = fma2(x[v].p[0], x[v].p[0], s);
-      s = fma2(x[v].p[1], x[v].p[1], s);
+#pragma unroll
+      for (int h = 0; h < P; ++h) s = fma2(x[v].p[h], x[v].p[h], s);
     }
     if (next) {
-      const float m =
-          group_sum<kWarps>(sum2(s), red_all[w.g][2 + odd], w.warp, w.g + 1, p.r.group);
-      const float ro = 1.0f / sqrtf(fmaf(m, q.inv_h, q.eps));
-      if (w.tid == 0 && p.o.rstd_out) p.o.rstd_out[t] = ro;
+      float m[1] = {sum2(s)};
+      group_sum(m, red_all[w.g][2 + odd], w.warp, w.g + 1, p.r.group);
+      const float ro = 1.0f / sqrtf(fmaf(m[0], q.inv_h, q.eps));
+      if (w.tid == 0 && p.o.rstd_out) p.o.rstd_out[w.lo + t] = ro;
       const Pair o = pair(ro);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         if (!w.has[v]) continue;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) x[v].p[h] = mul2(mul2(x[v].p[h], o), wn[2 * v + h]);
-        put4<__nv_bfloat16>(to_n + v * w.step * 2, x[v]);
+        for (int h = 0; h < P; ++h) x[v].p[h] = mul2(mul2(x[v].p[h], o), wn[P * v + h]);
+        put_half<W>(to_n + v * w.step * 2, x[v]);
       }
     }
     odd ^= 1;
@@ -312,25 +385,26 @@ __global__ void __launch_bounds__(ring_threads(kForwardVecs), 1)
 
 // ------------------------------------------------------------------ backward
 
-// With r = rstd_out, t = d_n out: dw_next += r t,
-//   D = d_out + r (d_n w_next - out (r^2 m(t w_next)));
-// with r = rstd_y, u = D y, gw = b g w_post: S += r u (dw_post = b g S and
-// dgate = b w_post S for one gate row; kMany keeps S for a row's tokens, and
-// its sum over rows times g in shared memory),
-//   dy = r (gw D - y (r^2 m(u gw))).
-// No product of three r: a row of 1e15 stays in float's range.
-template <typename ST, bool kMany, bool kFull>
-__global__ void __launch_bounds__(ring_threads(kBackwardVecs), 1)
+// With r = rstd_out: dw_next += r d_n out, and D = A + k out with
+//   A = d_out + r d_n w_next,  k = -r (r (r m(d_n w_next out))).
+// The gradient of y's norm needs m(gw D y), gw = b g w_post, which is
+// m(gw A y) + k m(gw out y): three sums of one pass over the row, one barrier.
+// With r = rstd_y: S += r D y (dw_post = b g S and dgate = b w_post S for one
+// gate row; kMany keeps S for a row's tokens, and its sum over rows times g in
+// shared memory), dy = r (gw D - y (r^2 m(gw D y))).
+// kAll: with d_out, d_n, y and w_post.
+template <typename ST, bool kMany, bool kFull, bool kAll>
+__global__ void __launch_bounds__(kThreads, 1)
     norm_ring_backward_kernel(const __grid_constant__ RingParams p) {
-  constexpr int V = kBackwardVecs, kWarps = ring_threads(V) / 32;
+  constexpr int W = Stream<ST>::W, V = Stream<ST>::V, P = W / 2, kSize = sizeof(ST);
   extern __shared__ __align__(128) unsigned char ring_all[];
-  __shared__ float red_all[kMaxRingGroups][4][kWarps];
+  __shared__ float4 red_all[kMaxRingGroups][2][kWarps];
   __shared__ __align__(8) uint64_t full_all[kMaxRingGroups][kMaxStages];
   __shared__ int abort_wait;
   const Walk<V> w = walk_of<V, kFull>(p, ring_all, full_all, &abort_wait);
   const NormParams& q = p.n;
-  const bool branch = q.y, post = q.w_post, next = q.d_n, has_d = q.x;
-  constexpr int kSize = sizeof(ST);
+  const bool branch = kAll || q.y, post = kAll || q.w_post, next = kAll || q.d_n,
+             has_d = kAll || q.x;
   // a stage: d_out, out, y, d_n, as far as there are any
   const int wide = w.H * kSize, half = w.H * 2;
   const int at_out = has_d ? wide : 0, at_y = at_out + (next ? wide : 0),
@@ -347,13 +421,18 @@ __global__ void __launch_bounds__(ring_threads(kBackwardVecs), 1)
   if (w.tid == 0)
     for (int i = 0; i < p.r.stages && w.lo + i < w.hi; ++i) issue(w.lo + i, i);
 
-  // kMany: the group's sum of g S, behind the rings
-  float* sum_w = reinterpret_cast<float*>(ring_all + static_cast<size_t>(p.r.groups) * p.r.stages *
-                                                         p.row_bytes) +
-                 w.g * w.H + w.col0;
-  Pair gw[2 * V], wn[2 * V], sum_s[2 * V], sum_n[2 * V];
+  // kMany: the group's sum of g S, behind the rings; the only group's is the
+  // CTA's partial sum itself
+  float* sum_w = nullptr;
+  if (kMany && p.o.part_post)
+    sum_w = (p.r.tail_bytes ? reinterpret_cast<float*>(ring_all + static_cast<size_t>(p.r.groups) *
+                                                                      p.r.stages * p.row_bytes) +
+                                  w.g * w.H
+                            : p.o.part_post + static_cast<int64_t>(blockIdx.x) * w.H) +
+            w.col0;
+  Pair gw[kCols / 2], wn[kCols / 2], sum_s[kCols / 2], sum_n[kCols / 2];
 #pragma unroll
-  for (int i = 0; i < 2 * V; ++i) {
+  for (int i = 0; i < kCols / 2; ++i) {
     gw[i] = pair(q.b);
     wn[i] = pair(1.0f);
     sum_s[i] = sum_n[i] = pair(0.0f);
@@ -362,155 +441,155 @@ __global__ void __launch_bounds__(ring_threads(kBackwardVecs), 1)
   if (kMany) {
 #pragma unroll
     for (int v = 0; v < V; ++v)
-      if (w.has[v])
-        *reinterpret_cast<float4*>(sum_w + v * w.step) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (w.has[v] && sum_w)
+#pragma unroll
+        for (int i = 0; i < W; i += 4)
+          *reinterpret_cast<float4*>(sum_w + v * w.step + i) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   } else {
     if (post) times(p, w, q.w_post, 0, gw);
     if (q.gate) times(p, w, q.gate, 0, gw);
   }
-  int64_t gate_row = -1, gate_end = w.lo;
+  int64_t gate_row = -1;
+  int to_gate = 0;                                 // rows until another gate row
   if (kMany && w.lo < w.hi) gate_row = w.lo / q.gate_span - 1;
-  unsigned long long limit = kDefaultWaitNs;
-  float next_ro = 0.0f, next_ry = 1.0f;
-  if (w.lo < w.hi) {
-    if (next) next_ro = q.rstd_out[w.lo];
-    if (post) next_ry = q.rstd_y[w.lo];
-  }
-  int stage = 0, parity = 0, odd = 0;
-  unsigned char* to_dx = static_cast<unsigned char*>(p.o.stream) + (w.lo * w.H + w.col0) * kSize;
-  unsigned char* to_dy = reinterpret_cast<unsigned char*>(p.o.branch) + (w.lo * w.H + w.col0) * 2;
-  const unsigned char* row_wide = w.ring + w.col0 * kSize;
-  const unsigned char* row_half = w.ring + w.col0 * 2;
+  bool gave_up = false;
+  int stage = 0, parity = 0;
+  const int rows = static_cast<int>(w.hi - w.lo);
   const Pair a = pair(branch ? q.a : 1.0f);
-  for (int64_t t = w.lo; t < w.hi; ++t, to_dx += wide, to_dy += half) {
-    const float ro = next_ro, ry = next_ry;
-    if (t + 1 < w.hi) {
-      if (next) next_ro = q.rstd_out[t + 1];
-      if (post) next_ry = q.rstd_y[t + 1];
+  float ro32 = 0.0f, ry32 = 1.0f;                  // of 32 rows, a lane each
+  for (int t = 0; t < rows; ++t) {
+    if ((t & 31) == 0) {
+      const int64_t at = min(w.lo + t + lane_id(), w.hi - 1);
+      if (next) ro32 = q.rstd_out[at];
+      if (post) ry32 = q.rstd_y[at];
     }
-    if (kMany && t == gate_end) {
+    const float ro = __shfl_sync(0xffffffffu, ro32, t & 31);
+    const float ry = __shfl_sync(0xffffffffu, ry32, t & 31);
+    if (kMany && to_gate == 0) {
       ++gate_row;
-      gate_end = (gate_row + 1) * q.gate_span;
+      to_gate = static_cast<int>((gate_row + 1) * q.gate_span - (w.lo + t));
 #pragma unroll
-      for (int i = 0; i < 2 * V; ++i) {
+      for (int i = 0; i < kCols / 2; ++i) {
         gw[i] = pair(q.b);
         sum_s[i] = pair(0.0f);
       }
       if (post) times(p, w, q.w_post, 0, gw);
       times(p, w, q.gate, gate_row * w.H, gw);
     }
-    wait_stage(p, w, stage, parity, &limit, &abort_wait);
-    const int base = stage * p.row_bytes;
-    Four d[V];
+    wait_stage(p, w, stage, parity, &gave_up, &abort_wait);
+    const unsigned char* row_wide = w.ring + (stage * p.row_bytes + w.col0 * kSize);
+    const unsigned char* row_half = w.ring + (stage * p.row_bytes + w.col0 * 2);
+    Vec<W> d[V];                                   // A, then D
+    Half<W> y[V];
+    Pair s0 = pair(0.0f), s1 = s0, s2 = s0;
+    const Pair r = pair(ro);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      if (!w.has[v]) continue;
+      if (has_d) d[v] = Stream<ST>::get(row_wide + v * w.step * kSize).wide();
+      if (next) {
+        const Vec<W> dn = widen<W>(get_half<W>(row_half + (at_dn + v * w.step * 2)));
+        const Vec<W> o = Stream<ST>::get(row_wide + (at_out + v * w.step * kSize)).wide();
+#pragma unroll
+        for (int h = 0; h < P; ++h) {
+          const int i = P * v + h;
+          const Pair u = mul2(dn.p[h], wn[i]);
+          s0 = fma2(u, o.p[h], s0);
+          sum_n[i] = fma2(mul2(dn.p[h], o.p[h]), r, sum_n[i]);
+          d[v].p[h] = has_d ? fma2(u, r, d[v].p[h]) : mul2(u, r);
+        }
+      }
+      if (branch) {
+        y[v] = get_half<W>(row_half + (at_y + v * w.step * 2));
+        if (post) {
+          const Vec<W> f = widen<W>(y[v]);
+          Vec<W> o;
+          if (next) o = Stream<ST>::get(row_wide + (at_out + v * w.step * kSize)).wide();
+#pragma unroll
+          for (int h = 0; h < P; ++h) {
+            const Pair u = mul2(f.p[h], gw[P * v + h]);
+            s1 = fma2(u, d[v].p[h], s1);
+            if (next) s2 = fma2(u, o.p[h], s2);
+          }
+        }
+      }
+    }
+    float m[3] = {sum2(s0), sum2(s1), sum2(s2)};
+    if (post || next) group_sum(m, red_all[w.g][t & 1], w.warp, w.g + 1, p.r.group);
+    const float k0 = next ? -ro * (ro * (ro * (m[0] * q.inv_h))) : 0.0f;
+    const Pair k = pair(k0), l = pair(-ry * (ry * (fmaf(k0, m[2], m[1]) * q.inv_h)));
+    const Pair e = pair(ry);
     if (next) {
-      Pair s = pair(0.0f);
-      const Pair r = pair(ro);
+      // out once more: registers to keep it would be spilled, and with this much
+      // shared memory L1 is too small to spill to
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         if (!w.has[v]) continue;
-        const Four f = get4<__nv_bfloat16>(row_half + (base + at_dn + v * w.step * 2));
-        const Four out = get4<ST>(row_wide + (base + at_out + v * w.step * kSize));
+        const Vec<W> o = Stream<ST>::get(row_wide + (at_out + v * w.step * kSize)).wide();
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const Pair u = mul2(f.p[h], out.p[h]);
-          s = fma2(u, wn[2 * v + h], s);
-          sum_n[2 * v + h] = fma2(u, r, sum_n[2 * v + h]);
-        }
-      }
-      const float m = group_sum<kWarps>(sum2(s), red_all[w.g][odd], w.warp, w.g + 1, p.r.group);
-      const Pair k = pair(-ro * (ro * (m * q.inv_h)));
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        if (!w.has[v]) continue;
-        // read again: shared memory is cheaper here than registers
-        const Four f = get4<__nv_bfloat16>(row_half + (base + at_dn + v * w.step * 2));
-        const Four out = get4<ST>(row_wide + (base + at_out + v * w.step * kSize));
-        Four e = {{0, 0}};
-        if (has_d) e = get4<ST>(row_wide + (base + v * w.step * kSize));
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          d[v].p[h] = fma2(r, fma2(k, out.p[h], mul2(f.p[h], wn[2 * v + h])), e.p[h]);
-      }
-    } else {
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (w.has[v]) d[v] = get4<ST>(row_wide + (base + v * w.step * kSize));
-    }
-    uint2 y[V];
-    Pair s = pair(0.0f);
-    const Pair r = pair(ry);
-    if (branch) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        if (!w.has[v]) continue;
-        y[v] = *reinterpret_cast<const uint2*>(row_half + (base + at_y + v * w.step * 2));
-        const Four f = widen(y[v]);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const Pair u = mul2(d[v].p[h], f.p[h]);
-          sum_s[2 * v + h] = fma2(u, r, sum_s[2 * v + h]);
-          s = fma2(u, gw[2 * v + h], s);
-        }
+        for (int h = 0; h < P; ++h) d[v].p[h] = fma2(k, o.p[h], d[v].p[h]);
       }
     }
-    float m = 0.0f;
-    if (post) m = group_sum<kWarps>(sum2(s), red_all[w.g][2 + odd], w.warp, w.g + 1, p.r.group);
-    if (!post || p.r.group == 32) group_barrier(w.g + 1, p.r.group);
     // every thread has the row in registers: its stage takes another
-    if (w.tid == 0 && t + p.r.stages < w.hi) issue(t + p.r.stages, stage);
-    const Pair k = pair(-ry * (ry * (m * q.inv_h)));
+    group_barrier(w.g + 1, p.r.group);
+    if (w.tid == 0 && t + p.r.stages < rows) issue(w.lo + t + p.r.stages, stage);
+    const int64_t first_col = (w.lo + t) * w.H + w.col0;
+    unsigned char* to_dx = static_cast<unsigned char*>(p.o.stream) + first_col * kSize;
+    unsigned char* to_dy = reinterpret_cast<unsigned char*>(p.o.branch) + first_col * 2;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       if (!w.has[v]) continue;
       if (branch) {
-        const Four f = widen(y[v]);
-        Four g;
+        const Vec<W> f = widen<W>(y[v]);
+        Vec<W> g;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          g.p[h] = mul2(gw[2 * v + h], d[v].p[h]);
-          if (post) g.p[h] = mul2(r, fma2(k, f.p[h], g.p[h]));
+        for (int h = 0; h < P; ++h) {
+          const int i = P * v + h;
+          sum_s[i] = fma2(mul2(d[v].p[h], f.p[h]), e, sum_s[i]);
+          g.p[h] = mul2(gw[i], d[v].p[h]);
+          if (post) g.p[h] = mul2(e, fma2(l, f.p[h], g.p[h]));
         }
-        put4<__nv_bfloat16>(to_dy + v * w.step * 2, g);
+        put_half<W>(to_dy + v * w.step * 2, g);
       }
 #pragma unroll
-      for (int h = 0; h < 2; ++h) d[v].p[h] = mul2(a, d[v].p[h]);
-      put4<ST>(to_dx + v * w.step * kSize, d[v]);
+      for (int h = 0; h < P; ++h) d[v].p[h] = mul2(a, d[v].p[h]);
+      put_stream<ST, W>(to_dx + v * w.step * kSize, d[v]);
     }
-    if (kMany && (t + 1 == gate_end || t + 1 == w.hi)) {
+    if (kMany && (--to_gate == 0 || t + 1 == rows)) {
       // S of the gate row: whole to dgate, else a piece (0: begun in an earlier
       // strip, 1: in this one); its share of dw_post stays
       const int64_t first = gate_row * q.gate_span;
-      const bool whole = first >= w.lo && t + 1 == gate_end;
+      const bool whole = first >= w.lo && to_gate == 0;
       const int64_t strip = static_cast<int64_t>(blockIdx.x) * p.r.groups + w.g;
       float* to = (whole ? p.o.dgate + gate_row * w.H
                          : p.o.part_gate + (strip * 2 + (first >= w.lo)) * w.H) +
                   w.col0;
-      Pair f[2 * V];
+      Pair f[kCols / 2];
 #pragma unroll
-      for (int i = 0; i < 2 * V; ++i) f[i] = sum_s[i];
+      for (int i = 0; i < kCols / 2; ++i) f[i] = sum_s[i];
       times(p, w, q.gate, gate_row * w.H, f);
+      auto add4 = [&](float* at, int i, bool old) {
+        const float2 lo = halves(f[i]), hi = halves(f[i + 1]);
+        float4 z = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (old) z = *reinterpret_cast<const float4*>(at);
+        *reinterpret_cast<float4*>(at) =
+            make_float4(z.x + lo.x, z.y + lo.y, z.z + hi.x, z.w + hi.y);
+      };
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        if (!w.has[v]) continue;
-        float4* at = reinterpret_cast<float4*>(sum_w + v * w.step);
-        const float2 lo = halves(f[2 * v]), hi = halves(f[2 * v + 1]);
-        const float4 z = *at;
-        *at = make_float4(z.x + lo.x, z.y + lo.y, z.z + hi.x, z.w + hi.y);
-      }
+      for (int v = 0; v < V; ++v)
+        if (w.has[v] && sum_w)
 #pragma unroll
-      for (int i = 0; i < 2 * V; ++i) f[i] = whole ? mul2(pair(q.b), sum_s[i]) : sum_s[i];
+          for (int i = 0; i < W; i += 4) add4(sum_w + v * w.step + i, P * v + i / 2, true);
+#pragma unroll
+      for (int i = 0; i < kCols / 2; ++i) f[i] = whole ? mul2(pair(q.b), sum_s[i]) : sum_s[i];
       if (whole && post) times(p, w, q.w_post, 0, f);
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        if (!w.has[v]) continue;
-        float4* at = reinterpret_cast<float4*>(to + v * w.step);
-        const float2 lo = halves(f[2 * v]), hi = halves(f[2 * v + 1]);
-        float4 z = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (whole && p.o.accumulate) z = *at;
-        *at = make_float4(z.x + lo.x, z.y + lo.y, z.z + hi.x, z.w + hi.y);
-      }
+      for (int v = 0; v < V; ++v)
+        if (w.has[v])
+#pragma unroll
+          for (int i = 0; i < W; i += 4)
+            add4(to + v * w.step + i, P * v + i / 2, whole && p.o.accumulate);
     }
-    odd ^= 1;
     if (++stage == p.r.stages) {
       stage = 0;
       parity ^= 1;
@@ -527,26 +606,29 @@ __global__ void __launch_bounds__(ring_threads(kBackwardVecs), 1)
       part[static_cast<int64_t>(blockIdx.x) * w.H + h] = z;
     }
   };
-  auto share = [&](const Pair (&sum)[2 * V]) {
+  auto share = [&](const Pair (&sum)[kCols / 2]) {
     float* all = reinterpret_cast<float*>(ring_all) + w.g * w.H + w.col0;
     __syncthreads();
 #pragma unroll
     for (int v = 0; v < V; ++v)
       if (w.has[v])
-        *reinterpret_cast<ulonglong2*>(all + v * w.step) =
-            make_ulonglong2(sum[2 * v], sum[2 * v + 1]);
+#pragma unroll
+        for (int i = 0; i < W; i += 4)
+          *reinterpret_cast<ulonglong2*>(all + v * w.step + i) =
+              make_ulonglong2(sum[P * v + i / 2], sum[P * v + i / 2 + 1]);
     return reinterpret_cast<const float*>(ring_all);
   };
-  if (p.o.part_post) add_up(kMany ? sum_w - w.g * w.H - w.col0 : share(sum_s), p.o.part_post);
+  if (kMany ? p.r.tail_bytes > 0 && sum_w : p.o.part_post != nullptr)
+    add_up(kMany ? sum_w - w.g * w.H - w.col0 : share(sum_s), p.o.part_post);
   if (p.o.part_next) add_up(share(sum_n), p.o.part_next);
 }
 
 // ------------------------------------------------------------------ launches
 
-// Threads that share a row of H, V vectors of four each; 0: more than a CTA has.
-int group_of(int H, int V) {
-  const int group = (H + 128 * V - 1) / (128 * V) * 32;
-  return H % 8 == 0 && group <= ring_threads(V) ? group : 0;
+// Threads that share a row; 0: more than a CTA has.
+int group_of(int H) {
+  const int group = (H + 32 * kCols - 1) / (32 * kCols) * 32;
+  return H % 8 == 0 && group <= kThreads ? group : 0;
 }
 
 template <typename K>
@@ -558,42 +640,49 @@ cudaError_t launch(K* kernel, const RingParams& p, size_t smem, cudaStream_t st)
   return cudaGetLastError();
 }
 
+template <typename ST, bool kFull, bool kAll>
+cudaError_t launch_of(const RingParams& p, bool backward, bool many, size_t smem, cudaStream_t st) {
+  auto* kernel = backward ? (many ? norm_ring_backward_kernel<ST, true, kFull, kAll>
+                                  : norm_ring_backward_kernel<ST, false, kFull, kAll>)
+                          : (many ? norm_ring_kernel<ST, true, kFull, kAll>
+                                  : norm_ring_kernel<ST, false, kFull, kAll>);
+  return launch(kernel, p, smem, st);
+}
+
+// Rows of a multiple of 512 with all the tensors are what layers have; any
+// other takes the kernels that look at each run.
 template <typename ST>
 cudaError_t launch_of(const RingParams& p, bool backward, bool many, size_t smem, cudaStream_t st) {
-  const bool full = p.n.H == 4 * (backward ? kBackwardVecs : kForwardVecs) * p.r.group;
-  auto* kernel =
-      backward ? (many ? (full ? norm_ring_backward_kernel<ST, true, true>
-                               : norm_ring_backward_kernel<ST, true, false>)
-                       : (full ? norm_ring_backward_kernel<ST, false, true>
-                               : norm_ring_backward_kernel<ST, false, false>))
-               : (many ? (full ? norm_ring_kernel<ST, true, true> : norm_ring_kernel<ST, true, false>)
-                       : (full ? norm_ring_kernel<ST, false, true>
-                               : norm_ring_kernel<ST, false, false>));
-  return launch(kernel, p, smem, st);
+  const NormParams& n = p.n;
+  const bool full = n.H == kCols * p.r.group;
+  const bool all = n.y && n.w_post && (backward ? n.x && n.d_n : n.w_next != nullptr);
+  return full ? (all ? launch_of<ST, true, true>(p, backward, many, smem, st)
+                     : launch_of<ST, true, false>(p, backward, many, smem, st))
+              : launch_of<ST, false, false>(p, backward, many, smem, st);
 }
 
 }  // namespace
 
 int most_ring_groups(int H) {
-  const int group = group_of(H, kBackwardVecs);
-  const int groups = group ? ring_threads(kBackwardVecs) / group : 0;
+  const int group = group_of(H);
+  const int groups = group ? kThreads / group : 0;
   return groups < kMaxRingGroups ? groups : kMaxRingGroups;
 }
 
 RingShape ring_shape(int64_t T, int H, int row_bytes, bool backward, bool many) {
   RingShape r = {};
-  const int V = backward ? kBackwardVecs : kForwardVecs;
-  r.group = group_of(H, V);
-  r.tail_bytes = backward && many ? H * static_cast<int>(sizeof(float)) : 0;
-  if (T == 0 || r.group == 0 || 2 * row_bytes + r.tail_bytes > kSharedBytes) return r;
+  r.group = group_of(H);
+  if (T == 0 || r.group == 0 || 2 * row_bytes > kSharedBytes) return r;
   const int sms = device_sm_count();
   // as many groups as there are threads and two stages of memory for, unless
   // the rows run out first
-  r.groups = ring_threads(V) / r.group;
+  r.groups = kThreads / r.group;
   if (r.groups > kMaxRingGroups) r.groups = kMaxRingGroups;
-  while (r.groups > 1 && (r.groups * (2 * row_bytes + r.tail_bytes) > kSharedBytes ||
+  const int tail = backward && many ? H * static_cast<int>(sizeof(float)) : 0;
+  while (r.groups > 1 && (r.groups * (2 * row_bytes + tail) > kSharedBytes ||
                           T <= static_cast<int64_t>(sms) * (r.groups - 1)))
     --r.groups;
+  r.tail_bytes = r.groups > 1 ? tail : 0;
   r.stages = (kSharedBytes / r.groups - r.tail_bytes) / row_bytes;
   if (r.stages > kMaxStages) r.stages = kMaxStages;
   const int64_t most = static_cast<int64_t>(sms) * r.groups;
