@@ -61,7 +61,9 @@ __device__ __forceinline__ unsigned seg_max_key(unsigned v) {
   return v;
 }
 
-// Unsigned keys in the order of the floats (-0.0 below +0.0), and back.
+// Unsigned keys in the order of the floats (-0.0 below +0.0), and back. Below
+// the lowest finite one's there is room for what is masked, and 0 for nothing.
+constexpr unsigned kLeastKey = 0x00800000u;
 __device__ __forceinline__ unsigned key_of(float v) {
   const int b = __float_as_int(v);
   return static_cast<unsigned>(b) ^ (static_cast<unsigned>(b >> 31) | 0x80000000u);
@@ -328,7 +330,7 @@ __device__ __noinline__ bool reorder(const GateParams& p, const L* row, Pick* pi
   }
   const unsigned next = __shfl_down_sync(kAll, key, 1);
   const float nl = __shfl_down_sync(kAll, l, 1), nb = __shfl_down_sync(kAll, b, 1);
-  const bool differ = lane + 1 < n && next != 0u && !(l == nl && b == nb) &&
+  const bool differ = lane + 1 < n && next >= kLeastKey && !(l == nl && b == nb) &&
                       !apart(float_of(key), float_of(next), abs_off, C * 0x1.2p-23f);
   const bool compute = __any_sync(kAll, differ);
   if (compute && soft && p.bias) return false;
@@ -401,8 +403,13 @@ __device__ __forceinline__ void slot_weights(const GateParams& p, const float (&
       sum += u[i];
     }
     sum = seg_sum<W>(sum);
-    // scores near the end of float's range: their ratios in double
-    if (__any_sync(kAll, sum < 1e-30f)) {
+    // scores near the end of float's range (masked slots alone are not): their
+    // ratios in double
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < S; ++i) m = fmaxf(m, l[i]);
+    m = __any_sync(kAll, sum < 1e-30f) ? seg_max<W>(m) : 0.0f;
+    if (__any_sync(kAll, sum < 1e-30f && m > -INFINITY)) {
       double total = 0.0;
 #pragma unroll
       for (int i = 0; i < S; ++i) total += sigmoid_in_double(l[i]);
@@ -559,10 +566,18 @@ __global__ void __launch_bounds__((GateShape<W, C>::kWarps * 32), (GateShape<W, 
           v[i + 3] += b.w;
         }
       }
+    }
+    bool masks = false;                                        // in any of the warp's tokens
+    if (!exact) {
       float least = l[0];
 #pragma unroll
       for (int i = 1; i < C; ++i) least = fminf(least, l[i]);
-      if (__any_sync(kAll, least == -INFINITY)) {
+      if (biased) {
+#pragma unroll
+        for (int i = 0; i < C; ++i) least = fminf(least, v[i]);
+      }
+      masks = __any_sync(kAll, least == -INFINITY);
+      if (kScored && masks) {
 #pragma unroll
         for (int i = 0; i < C; ++i)
           if (l[i] == -INFINITY) v[i] = -INFINITY;
@@ -572,6 +587,12 @@ __global__ void __launch_bounds__((GateShape<W, C>::kWarps * 32), (GateShape<W, 
 #pragma unroll
       for (int i = 0; i < C; ++i)
         key[i] = (key_of((biased ? v[i] : l[i]) + 0.0f) & ~(C - 1u)) | (C - 1u - i);   // one zero
+      if (masks) {
+        // what is masked ranks after every float, the lower expert first
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+          if ((biased ? v[i] : l[i]) == -INFINITY) key[i] = C * (W - sub) + (C - 1u - i);
+      }
     }
     // how far a score may be off (logits that rank by themselves: only by their key)
     const float off = soft ? inv * 0x1p-19f : 0x1p-21f;
@@ -606,8 +627,9 @@ __global__ void __launch_bounds__((GateShape<W, C>::kWarps * 32), (GateShape<W, 
         }
         const float g = p.group_topk == 2 && c != -INFINITY ? a + c : a;
         // topk_group rounds of the largest; groups of one score go together,
-        // and are then too close to be certain
-        unsigned gk = key_of(g + 0.0f), low = 0u, high = 0u;
+        // and are then too close to be certain (masked ones go by their index)
+        unsigned gk = g == -INFINITY ? W - (sub & ~(lanes - 1)) : key_of(g + 0.0f);
+        unsigned low = 0u, high = 0u;
         for (int j = 0; j <= p.topk_group; ++j) {
           low = high;
           high = seg_max_key<W>(gk);
@@ -616,7 +638,8 @@ __global__ void __launch_bounds__((GateShape<W, C>::kWarps * 32), (GateShape<W, 
         bool kept = gk == 0u;
         const int of = __popc(__ballot_sync(kAll, kept) & seg);
         open_set = of != p.topk_group * lanes ||
-                   (high != 0u && !apart(float_of(low), float_of(high), 4.0f * off, 0x1p-22f));
+                   (high >= kLeastKey &&
+                    !apart(float_of(low), float_of(high), 4.0f * off, 0x1p-22f));
         if (const unsigned opens = __ballot_sync(kAll, open_set)) {
           const unsigned right = settle_groups(opens);
           if (right) {
@@ -669,7 +692,7 @@ __global__ void __launch_bounds__((GateShape<W, C>::kWarps * 32), (GateShape<W, 
         for (int o = W / 2; o > 0; o >>= 1) kept |= __shfl_xor_sync(kAll, kept, o);
         low = -seg_max<W>(-low);
         high = seg_max<W>(high);
-        open_set = p.topk_group < p.n_group && !apart(low, high, 4.0f * off, 0x1p-22f);
+        open_set = high != -INFINITY && !apart(low, high, 4.0f * off, 0x1p-22f);
         if (const unsigned opens = __ballot_sync(kAll, open_set)) {
           const unsigned right = settle_groups(opens);
           if (right) {
@@ -711,7 +734,7 @@ __global__ void __launch_bounds__((GateShape<W, C>::kWarps * 32), (GateShape<W, 
       const float abs_off = biased ? 2.0f * off : 1e-43f;
       auto close = [&](int i, int j) {
         const unsigned ka = pick[i].key & ~(C - 1u), kb = pick[j].key & ~(C - 1u);
-        return kb != 0u && !apart(float_of(ka), float_of(kb), abs_off, C * 0x1.2p-23f);
+        return kb >= kLeastKey && !apart(float_of(ka), float_of(kb), abs_off, C * 0x1.2p-23f);
       };
       bool open_order = false, open_end = false;
       for (int j = sub; j < p.k; j += W)
