@@ -997,9 +997,9 @@ def moe_clip_grad_norm(grads, max_norm, out=None, norm_type=2.0, eps=1e-6, norm_
     Tensor = torch.Tensor
     dtypes = [g.dtype for g in grads]
     kinds = set(dtypes)
-    sizes = [g.numel() for g in grads]
+    sizes = list(map(Tensor.numel, grads))
     if not kinds <= _TYPES.keys() or not all(map(Tensor.is_contiguous, grads)) or \
-            {g.get_device() for g in grads} - {index}:
+            set(map(Tensor.get_device, grads)) - {index}:
         for i, g in enumerate(grads):
             if g.dtype not in _TYPES or g.get_device() != index or not g.is_contiguous():
                 raise ValueError(f"grads[{i}] must be a contiguous float32 or bfloat16 tensor "
@@ -1011,14 +1011,14 @@ def moe_clip_grad_norm(grads, max_norm, out=None, norm_type=2.0, eps=1e-6, norm_
         out = list(out)
         if len(out) != n:
             raise ValueError(f"out holds {len(out)} tensors, grads {n}")
-        if [o.dtype for o in out] != dtypes or [o.numel() for o in out] != sizes or \
+        if [o.dtype for o in out] != dtypes or list(map(Tensor.numel, out)) != sizes or \
                 not all(map(Tensor.is_contiguous, out)) or \
-                {o.get_device() for o in out} - {index}:
+                set(map(Tensor.get_device, out)) - {index}:
             for i, o in enumerate(out):
                 if o.dtype != dtypes[i] or o.numel() != sizes[i] or not o.is_contiguous() or \
                         o.get_device() != index:
                     raise ValueError(f"out[{i}] must be as grads[{i}]: same type, device and size")
-        outs = array.array("Q", [o.data_ptr() for o in out])
+        outs = array.array("Q", list(map(Tensor.data_ptr, out)))
     _fit(dev, (norm_coef, "norm_coef", torch.float32, 2))
     if norm_coef is None and workspace is None:
         # one allocation: the two results, then the workspace
@@ -1030,7 +1030,7 @@ def moe_clip_grad_norm(grads, max_norm, out=None, norm_type=2.0, eps=1e-6, norm_
             norm_coef = torch.empty(2, dtype=torch.float32, device=dev)
         ws, ws_bytes = _scratch(workspace, _CLIP_WORKSPACE, dev)
         result, ws_at = norm_coef.data_ptr(), _ptr(ws)
-    ptrs = array.array("Q", [g.data_ptr() for g in grads])
+    ptrs = array.array("Q", list(map(Tensor.data_ptr, grads)))
     numels = array.array("q", sizes)
     codes = array.array("i", [_TYPES[d] for d in (kinds if len(kinds) == 1 else dtypes)])
     if len(kinds) == 1:
