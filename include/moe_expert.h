@@ -638,7 +638,7 @@ void moe_norm_config_init(moe_norm_config* cfg);
  *  n       bf16 [T, H]   out
  *  rstd_y  float [T]     out with w_post, else not written (may be NULL)
  *  rstd_out float [T]    out with w_next, else not written (may be NULL)
- * Any H from 1 to 65536; rows with H % 8 == 0 and H <= 32768 (16384 with a
+ * T < 2^32. Any H from 1 to 65536; rows with H % 8 == 0 and H <= 32768 (16384 with a
  * float stream) are read once, others up to three times. T = 0 does nothing.
  * ------------------------------------------------------------------------ */
 moe_status moe_norm_residual(const void* x, const void* y, const void* w_post, const void* gate,

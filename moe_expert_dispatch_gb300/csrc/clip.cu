@@ -13,6 +13,11 @@
 // in float), the second read from L2 as far as the 129 MB hold. Double
 // precision runs at 1/64 of float's rate here, so the long sums are kept as
 // pairs of floats (a sum and what its roundings lost).
+//
+// 5.6 GB in float: 2.62 ms for its three passes over HBM (16.9 GB: 6.45 TB/s;
+// read once and written once it would be 1.66 ms). 50 MB: 25 us on the GPU. 300
+// packed bf16 tensors, 100 MB: 62 us. 45 thousand elements: 5.5 us, one launch.
+// One cooperative launch for both passes was slower: 28 us and 3.0 ms.
 #include "common.cuh"
 #include "internal.h"
 

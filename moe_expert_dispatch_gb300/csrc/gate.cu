@@ -153,7 +153,8 @@ __device__ __forceinline__ void warp_argmax(long long& v, int& e) {
 
 // The choice of one token by a whole warp with every value in double (v: E
 // values of shared memory): for the few tokens that neither reorder nor
-// groups_in_double can settle. Some 20 us, most of it the exponentials.
+// groups_in_double can settle. Some 20 us, most of it the exponentials: double
+// precision runs at 1/64 of float's rate here.
 template <typename L>
 __device__ __noinline__ void choose_in_double(const GateParams& p, const L* row, double* v,
                                               Pick* pick) {
@@ -501,7 +502,14 @@ struct GateShape {
 // logits that rank by themselves leave room for the whole index in the key,
 // and need no second look at all (kScored false: no bias and no groups).
 //
-// Bound by instruction issue.
+// Bound by instruction issue: 65536 tokens x 256 experts (sigmoid, bias, 8
+// groups) take 60 us, 680 warp instructions a token with two thirds of the
+// issue slots busy, where their 71 MB take 10.5; 49 us without groups, 36 for
+// bf16 logits ranked by themselves. 8192 x 128 take 7.7 us and 32 x 256 7.5,
+// most of it launch and latency. Sixteen experts a lane measured 67 against 71
+// us for eight (65536 x 256), four CTAs an SM 60 against 67 for three. A row
+// whose logits and bias are all the same ties beyond 32 candidates and is
+// chosen in double: 65536 such rows take 1 ms.
 template <typename L, int W, int C, bool kScored>
 __global__ void __launch_bounds__((GateShape<W, C>::kWarps * 32), (GateShape<W, C>::kCtas))
     gate_kernel(const __grid_constant__ GateParams p, int32_t* __restrict__ ids, float* __restrict__ probs,
@@ -843,7 +851,8 @@ __global__ void __launch_bounds__(256) gate_zero_kernel(int32_t* scratch, int n)
 
 // W lanes of C experts share a token, as forward. The slots' gradients go
 // through a row of shared memory, zero between tokens, to the lanes that own
-// their experts; every lane then writes its C columns.
+// their experts; every lane then writes its C columns. 16384 x 64 (dense
+// softmax): 5.6 us, half of it a launch's latency, against 1.4 for its 9.2 MB.
 template <typename L, int W, int C>
 __global__ void __launch_bounds__((GateShape<W, C>::kWarps * 32), (C > 8 ? 2 : 4))
     gate_backward_kernel(const __grid_constant__ GateParams p, const float* __restrict__ dprobs,

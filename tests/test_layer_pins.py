@@ -262,6 +262,7 @@ def test_entry_points_refuse_before_any_launch(m):
         ("norm: H = 0", INV, lambda: norm(H=0)),
         ("norm: H > 65536", UNS, lambda: norm(H=65537)),
         ("norm: T < 0", INV, lambda: norm(T=-1)),
+        ("norm: T past 2^32", INV, lambda: norm(T=1 << 32)),
         ("norm: eps", INV, lambda: norm(cfg=ncfg(eps=nan))),
         ("norm: negative eps", INV, lambda: norm(cfg=ncfg(eps=-1.0))),
         ("norm: residual scale", INV, lambda: norm(cfg=ncfg(a=inf))),
