@@ -3,6 +3,8 @@
 // points, and the kernels for rows that those of norm_ring.cu do not take.
 #include "norm.cuh"
 
+#include <type_traits>
+
 namespace moe {
 namespace {
 
@@ -214,162 +216,308 @@ __global__ void __launch_bounds__(1024)
 
 // ------------------------------------------------------------------ any H, any alignment
 
-// One CTA per row, three passes over it (the later two from L1/L2): lengths
-// that are no multiple of eight, and very long rows. 4096 x 4096: 70 us.
-template <typename ST, typename WT>
-__global__ void __launch_bounds__(kNormThreads)
+// V elements: one, or four through 8- or 16-byte words. Plain accesses: out may be
+// x, and dx may be d_out.
+template <typename E, int V>
+__device__ __forceinline__ void ldv(const void* p, int64_t i, float (&f)[V]) {
+  if constexpr (V == 1) {
+    f[0] = ld<E>(p, i);
+  } else if constexpr (sizeof(E) == 4) {
+    const float4 q = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+    f[0] = q.x;
+    f[1] = q.y;
+    f[2] = q.z;
+    f[3] = q.w;
+  } else {
+    const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p) + i);
+    unpack<4>(Raw<4>{q.x, q.y}, f);
+  }
+}
+template <typename E, int V>
+__device__ __forceinline__ void stv(E* p, const float (&f)[V]) {
+  if constexpr (V == 1)
+    st(p, f[0]);
+  else if constexpr (sizeof(E) == 4)
+    *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+  else
+    store_bf16<4>(p, f);
+}
+
+// The threads that share a row: a warp up to kWarpH elements, else the CTA; V
+// elements a thread at once.
+constexpr int kWarpH = 1024;
+template <bool kWarp, int V>
+struct RowGroup {
+  static constexpr int kThreads = kWarp ? 32 : kNormThreads;
+  static constexpr int kRows = kNormThreads / kThreads;      // of a CTA at once
+  static constexpr int kStep = kThreads * V;
+  static constexpr int kUnroll = V == 1 ? 4 : 1;       // of the loops along a row
+  int tid, h0;
+  int64_t first;
+  float* red;
+  __device__ __forceinline__ explicit RowGroup(float* shared)
+      : tid(threadIdx.x % kThreads),
+        h0(tid * V),
+        first(static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / kThreads),
+        red(shared) {}
+  __device__ __forceinline__ float sum(float v) const {
+    if (!kWarp) return cta_sum(v, red);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  }
+};
+
+// A warp or a CTA per row, three passes over it (the later two from L1/L2):
+// lengths that are no multiple of eight, and very long rows. 16384 x 333: 20 us
+// (a CTA per row: 63), 4096 x 4095: 84, 4096 x 10236: 103 (single elements: 250),
+// bound by the latency of the three passes.
+template <typename ST, typename WT, bool kWarp, int V>
+__global__ void __launch_bounds__(kNormThreads, V == 1 ? 6 : 8)
     norm_rows_kernel(NormParams p, ST* out, __nv_bfloat16* __restrict__ n, float* rstd_y,
                      float* rstd_out) {
+  using Group = RowGroup<kWarp, V>;
   __shared__ float red[kNormThreads / 32];
-  for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
+  const Group w(red);
+  for (int64_t t = w.first; t < p.T; t += static_cast<int64_t>(gridDim.x) * w.kRows) {
     const int64_t at = t * p.H;
     float ry = 1.0f;
     if (p.w_post) {
       float s = 0.0f;
-      for (int h = threadIdx.x; h < p.H; h += kNormThreads) {
-        const float v = ld<__nv_bfloat16>(p.y, at + h);
-        s = fmaf(v, v, s);
+#pragma unroll(Group::kUnroll)
+      for (int h = w.h0; h < p.H; h += w.kStep) {
+        float y[V];
+        ldv<__nv_bfloat16>(p.y, at + h, y);
+#pragma unroll
+        for (int i = 0; i < V; ++i) s = fmaf(y[i], y[i], s);
       }
-      ry = 1.0f / sqrtf(cta_sum(s, red) * p.inv_h + p.eps);
-      if (threadIdx.x == 0 && rstd_y) rstd_y[t] = ry;
+      ry = 1.0f / sqrtf(w.sum(s) * p.inv_h + p.eps);
+      if (w.tid == 0 && rstd_y) rstd_y[t] = ry;
     }
     const int64_t gat = p.gate ? t / p.gate_span * p.H : 0;
-    auto row = [&](int h) {
-      const float xv = ld<ST>(p.x, at + h);
-      if (!p.y) return xv;
-      float z = ld<__nv_bfloat16>(p.y, at + h);
-      if (p.w_post) z = z * ry * ld<WT>(p.w_post, h);
-      if (p.gate) z *= ld<WT>(p.gate, gat + h);
-      return fmaf(p.a, xv, p.b * z);
+    auto row = [&](int h, float (&o)[V]) {
+      ldv<ST>(p.x, at + h, o);
+      if (!p.y) return;
+      float z[V], f[V];
+      ldv<__nv_bfloat16>(p.y, at + h, z);
+      if (p.w_post) {
+        ldv<WT>(p.w_post, h, f);
+#pragma unroll
+        for (int i = 0; i < V; ++i) z[i] = z[i] * ry * f[i];
+      }
+      if (p.gate) {
+        ldv<WT>(p.gate, gat + h, f);
+#pragma unroll
+        for (int i = 0; i < V; ++i) z[i] *= f[i];
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) o[i] = fmaf(p.a, o[i], p.b * z[i]);
     };
     float ro = 1.0f;
     if (p.w_next) {
       float s = 0.0f;
-      for (int h = threadIdx.x; h < p.H; h += kNormThreads) {
-        const float o = row(h);
-        s = fmaf(o, o, s);
+#pragma unroll(Group::kUnroll)
+      for (int h = w.h0; h < p.H; h += w.kStep) {
+        float o[V];
+        row(h, o);
+#pragma unroll
+        for (int i = 0; i < V; ++i) s = fmaf(o[i], o[i], s);
       }
-      ro = 1.0f / sqrtf(cta_sum(s, red) * p.inv_h + p.eps);
-      if (threadIdx.x == 0 && rstd_out) rstd_out[t] = ro;
+      ro = 1.0f / sqrtf(w.sum(s) * p.inv_h + p.eps);
+      if (w.tid == 0 && rstd_out) rstd_out[t] = ro;
     }
-    for (int h = threadIdx.x; h < p.H; h += kNormThreads) {
-      const float o = row(h);                      // before out, which may be x, is written
-      if (out) st(out + at + h, o);
-      if (p.w_next) st(n + at + h, o * ro * ld<WT>(p.w_next, h));
+#pragma unroll(Group::kUnroll)
+    for (int h = w.h0; h < p.H; h += w.kStep) {
+      float o[V], f[V];
+      row(h, o);                                   // before out, which may be x, is written
+      if (out) stv<ST>(out + at + h, o);
+      if (p.w_next) {
+        ldv<WT>(p.w_next, h, f);
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[i] *= o[i] * ro;
+        stv<__nv_bfloat16>(n + at + h, f);
+      }
     }
   }
 }
 
-// D_t at column h, from the row's mean c = m(q * o).
-template <typename ST, typename WT>
-__device__ __forceinline__ float total_grad(const NormParams& p, int64_t at, int h, float ro,
-                                            float c) {
-  float d = p.x ? ld<ST>(p.x, at + h) : 0.0f;
+// D_t at the columns from h, from the row's mean c = m(q * o).
+template <typename ST, typename WT, int V>
+__device__ __forceinline__ void total_grad(const NormParams& p, int64_t at, int h, float ro,
+                                           float c, float (&d)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) d[i] = 0.0f;
+  if (p.x) ldv<ST>(p.x, at + h, d);
   if (p.d_n) {
-    const float q = ld<__nv_bfloat16>(p.d_n, at + h) * ld<WT>(p.w_next, h);
-    d = fmaf(ro, q - ld<ST>(p.out, at + h) * ro * c, d);
+    float q[V], f[V], o[V];
+    ldv<__nv_bfloat16>(p.d_n, at + h, q);
+    ldv<WT>(p.w_next, h, f);
+    ldv<ST>(p.out, at + h, o);
+#pragma unroll
+    for (int i = 0; i < V; ++i) d[i] = fmaf(ro, q[i] * f[i] - o[i] * ro * c, d[i]);
   }
-  return d;
 }
 
-// One CTA per row. kMean: the row's mean c, for the column sums that follow;
+// A warp or a CTA per row. kMean: the row's mean c, for the column sums that follow;
 // else dx and dy from it. Two launches around the column sums, because these
-// read d_out and dx may be d_out itself.
-template <typename ST, typename WT, bool kMean>
-__global__ void __launch_bounds__(kNormThreads)
+// read d_out and dx may be d_out itself. The three together: 16384 x 333 54 us
+// (a CTA per row: 100), 4096 x 10240 296 us (single elements: 630), of which the
+// four readings of the rows are the most.
+template <typename ST, typename WT, bool kMean, bool kWarp, int V>
+__global__ void __launch_bounds__(kNormThreads, V == 1 ? 5 : 1)
     norm_rows_backward_kernel(NormParams p, ST* dx, __nv_bfloat16* __restrict__ dy,
                               float* __restrict__ c_of) {
+  using Group = RowGroup<kWarp, V>;
   __shared__ float red[kNormThreads / 32];
-  for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
+  const Group w(red);
+  for (int64_t t = w.first; t < p.T; t += static_cast<int64_t>(gridDim.x) * w.kRows) {
     const int64_t at = t * p.H;
     const float ro = p.d_n ? p.rstd_out[t] : 0.0f;
     if (kMean) {
       float s = 0.0f;
       if (p.d_n)
-        for (int h = threadIdx.x; h < p.H; h += kNormThreads)
-          s = fmaf(ld<__nv_bfloat16>(p.d_n, at + h) * ld<WT>(p.w_next, h),
-                   ld<ST>(p.out, at + h) * ro, s);
-      s = cta_sum(s, red);
-      if (threadIdx.x == 0) c_of[t] = s * p.inv_h;
+#pragma unroll(Group::kUnroll)
+        for (int h = w.h0; h < p.H; h += w.kStep) {
+          float q[V], f[V], o[V];
+          ldv<__nv_bfloat16>(p.d_n, at + h, q);
+          ldv<WT>(p.w_next, h, f);
+          ldv<ST>(p.out, at + h, o);
+#pragma unroll
+          for (int i = 0; i < V; ++i) s = fmaf(q[i] * f[i], o[i] * ro, s);
+        }
+      s = w.sum(s);
+      if (w.tid == 0) c_of[t] = s * p.inv_h;
       continue;
     }
     const float c = c_of[t];
     const int64_t gat = p.gate ? t / p.gate_span * p.H : 0;
     const float ry = p.y && p.w_post ? p.rstd_y[t] : 1.0f;
-    auto grad_z = [&](int h) {                     // of the normalised y, times w_post
-      float q = p.b * total_grad<ST, WT>(p, at, h, ro, c);
-      if (p.gate) q *= ld<WT>(p.gate, gat + h);
-      if (p.w_post) q *= ld<WT>(p.w_post, h);
-      return q;
+    auto grad_z = [&](int h, float (&q)[V]) {      // of the normalised y, times w_post, from D
+      float f[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) q[i] *= p.b;
+      if (p.gate) {
+        ldv<WT>(p.gate, gat + h, f);
+#pragma unroll
+        for (int i = 0; i < V; ++i) q[i] *= f[i];
+      }
+      if (p.w_post) {
+        ldv<WT>(p.w_post, h, f);
+#pragma unroll
+        for (int i = 0; i < V; ++i) q[i] *= f[i];
+      }
     };
     float m = 0.0f;
     if (p.y && p.w_post) {
       float s = 0.0f;
-      for (int h = threadIdx.x; h < p.H; h += kNormThreads)
-        s = fmaf(grad_z(h), ld<__nv_bfloat16>(p.y, at + h) * ry, s);
-      m = cta_sum(s, red) * p.inv_h;
-    }
-    for (int h = threadIdx.x; h < p.H; h += kNormThreads) {
-      const float d = total_grad<ST, WT>(p, at, h, ro, c);
-      if (p.y) {
-        float q = grad_z(h);
-        if (p.w_post) q = ry * (q - ld<__nv_bfloat16>(p.y, at + h) * ry * m);
-        st(dy + at + h, q);
+#pragma unroll(Group::kUnroll)
+      for (int h = w.h0; h < p.H; h += w.kStep) {
+        float q[V], y[V];
+        ldv<__nv_bfloat16>(p.y, at + h, y);
+        total_grad<ST, WT>(p, at, h, ro, c, q);
+        grad_z(h, q);
+#pragma unroll
+        for (int i = 0; i < V; ++i) s = fmaf(q[i], y[i] * ry, s);
       }
-      st(dx + at + h, p.y ? p.a * d : d);          // last: dx may be d_out
+      m = w.sum(s) * p.inv_h;
+    }
+#pragma unroll(Group::kUnroll)
+    for (int h = w.h0; h < p.H; h += w.kStep) {
+      float d[V];
+      total_grad<ST, WT>(p, at, h, ro, c, d);
+      if (p.y) {
+        float q[V], y[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) q[i] = d[i];
+        grad_z(h, q);
+        if (p.w_post) {
+          ldv<__nv_bfloat16>(p.y, at + h, y);
+#pragma unroll
+          for (int i = 0; i < V; ++i) q[i] = ry * (q[i] - y[i] * ry * m);
+        }
+        stv<__nv_bfloat16>(dy + at + h, q);
+#pragma unroll
+        for (int i = 0; i < V; ++i) d[i] *= p.a;
+      }
+      stv<ST>(dx + at + h, d);                     // last: dx may be d_out
     }
   }
 }
 
-// Column sums of a strip of rows (blockIdx.y), one column per thread: dw_next
+// Column sums of a strip of rows (blockIdx.y), V columns per thread: dw_next
 // and dw_post into part[strip], and S = sum D yh of every gate row: straight
 // to dgate where the strip holds all of the row's tokens, else into one of
 // the strip's two pieces (0: the row began in an earlier strip, 1: in this
 // one). All without b, and with one gate row without it, as the fast kernel.
-template <typename ST, typename WT>
+template <typename ST, typename WT, int V>
 __global__ void __launch_bounds__(128)
     norm_cols_backward_kernel(NormParams p, const float* __restrict__ c_of,
                               float* __restrict__ part_post, float* __restrict__ part_next,
                               float* __restrict__ part_gate, int one_gate,
                               float* __restrict__ dgate, int accumulate) {
-  const int h = blockIdx.x * 128 + threadIdx.x;
+  const int h = (blockIdx.x * 128 + threadIdx.x) * V;
   if (h >= p.H) return;
   const int64_t strip = blockIdx.y;
   const int64_t lo = strip_row(p.T, gridDim.y, strip), hi = strip_row(p.T, gridDim.y, strip + 1);
-  const float wp = p.w_post ? ld<WT>(p.w_post, h) : 1.0f;
-  float sum_post = 0.0f, sum_next = 0.0f, s = 0.0f, g = 1.0f;
-  int64_t first = 0;                               // the current gate row's first token
-  for (int64_t t = lo; t < hi; ++t) {
-    if (p.gate && !one_gate && (t == lo || t % p.gate_span == 0)) {
-      first = t / p.gate_span * p.gate_span;
-      g = ld<WT>(p.gate, t / p.gate_span * p.H + h);
-      s = 0.0f;
-    }
-    const float ro = p.d_n ? p.rstd_out[t] : 0.0f;
-    if (p.y) {
-      const float d = total_grad<ST, WT>(p, t * p.H, h, ro, c_of[t]);
-      const float yh = ld<__nv_bfloat16>(p.y, t * p.H + h) * (p.w_post ? p.rstd_y[t] : 1.0f);
-      sum_post = fmaf(g * d, yh, sum_post);
-      s = fmaf(d, yh, s);
-    }
-    if (p.d_n)
-      sum_next = fmaf(ld<__nv_bfloat16>(p.d_n, t * p.H + h), ld<ST>(p.out, t * p.H + h) * ro,
-                      sum_next);
-    if (p.gate && !one_gate && (t + 1 == hi || (t + 1) % p.gate_span == 0)) {
-      if (first >= lo && first + p.gate_span <= hi) {
-        float* to = dgate + t / p.gate_span * p.H + h;
-        *to = accumulate ? *to + s * wp * p.b : s * wp * p.b;
-      } else {
-        part_gate[(strip * 2 + (first >= lo)) * p.H + h] = s;
+  float sum_post[V] = {}, sum_next[V] = {};
+  const bool many = p.gate && !one_gate;
+  // the gate row of the token, and the token after its last one
+  int64_t r = many ? lo / p.gate_span : 0, end = many ? (r + 1) * p.gate_span : hi;
+  for (int64_t t0 = lo; t0 < hi;) {
+    const int64_t stop = min(hi, end);
+    float s[V] = {};
+#pragma unroll 4
+    for (int64_t t = t0; t < stop; ++t) {
+      const float ro = p.d_n ? p.rstd_out[t] : 0.0f;
+      if (p.y) {
+        const float ry = p.w_post ? p.rstd_y[t] : 1.0f;
+        float d[V], y[V];
+        ldv<__nv_bfloat16>(p.y, t * p.H + h, y);
+        total_grad<ST, WT>(p, t * p.H, h, ro, c_of[t], d);
+#pragma unroll
+        for (int i = 0; i < V; ++i) s[i] = fmaf(d[i], y[i] * ry, s[i]);
+      }
+      if (p.d_n) {
+        float q[V], o[V];
+        ldv<__nv_bfloat16>(p.d_n, t * p.H + h, q);
+        ldv<ST>(p.out, t * p.H + h, o);
+#pragma unroll
+        for (int i = 0; i < V; ++i) sum_next[i] = fmaf(q[i], o[i] * ro, sum_next[i]);
       }
     }
+    if (many) {
+      float g[V];
+      ldv<WT>(p.gate, r * p.H + h, g);
+#pragma unroll
+      for (int i = 0; i < V; ++i) sum_post[i] = fmaf(g[i], s[i], sum_post[i]);
+      const int64_t first = end - p.gate_span;
+      if (first >= lo && end <= hi) {
+        float* to = dgate + r * p.H + h;
+        float old[V] = {}, wp[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) wp[i] = 1.0f;
+        if (accumulate) ldv<float>(to, 0, old);
+        if (p.w_post) ldv<WT>(p.w_post, h, wp);
+#pragma unroll
+        for (int i = 0; i < V; ++i) old[i] += s[i] * wp[i] * p.b;
+        stv<float>(to, old);
+      } else {
+        stv<float>(part_gate + (strip * 2 + (first >= lo)) * p.H + h, s);
+      }
+      ++r;
+      end += p.gate_span;
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) sum_post[i] += s[i];
+    }
+    t0 = stop;
   }
-  if (part_post) part_post[strip * p.H + h] = sum_post;
-  if (part_next) part_next[strip * p.H + h] = sum_next;
+  if (part_post) stv<float>(part_post + strip * p.H + h, sum_post);
+  if (part_next) stv<float>(part_next + strip * p.H + h, sum_next);
 }
 
 // The partial sums, in order: 128 columns a CTA, its warps taking the parts in
-// turn. blockIdx.y 0: dw_post, 1: dw_next, 2 + r: gate row r, from the pieces of
+// turn. blockIdx.y 0: dw_post, 1: dw_next, beyond: a gate row, from the pieces of
 // the strips that share it. Bound by latency: 5 us, of which two are hidden by
 // its launch while the last rows are worked on.
 struct FinishParams {
@@ -381,6 +529,12 @@ struct FinishParams {
   float b;
 };
 
+// Gate rows, or strips' ends, that the kernel looks at.
+__host__ __device__ __forceinline__ int64_t finish_gates(const FinishParams& p) {
+  if (!p.dgate) return 0;
+  return !p.one_gate && p.strips > 0 && p.strips - 1 < p.gate_rows ? p.strips - 1 : p.gate_rows;
+}
+
 __global__ void __launch_bounds__(256) norm_finish_kernel(const __grid_constant__ FinishParams p) {
   constexpr int kWarps = 8, kLoads = 10;
   __shared__ float4 sh[kWarps][32];
@@ -388,18 +542,24 @@ __global__ void __launch_bounds__(256) norm_finish_kernel(const __grid_constant_
   const int h = blockIdx.x * 128 + lane * 4;       // the lane's four columns
   const bool vec = p.H % 4 == 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  for (int64_t what = blockIdx.y; what < 2 + p.gate_rows; what += gridDim.y) {
+  // one gate row: its sum is the one behind dw_post. Several: those that lie
+  // across strips (the others are written by their strips), found from the rows
+  // or, if there are fewer, from the strips' ends: a row counts at its first one
+  const bool across = !p.one_gate && p.strips > 0, by_end = across && p.strips - 1 < p.gate_rows;
+  for (int64_t what = blockIdx.y; what < 2 + finish_gates(p); what += gridDim.y) {
     const bool of_gate = what >= 2;
-    const int64_t r = what - 2;
     if (!of_gate && !(what == 0 ? p.dw_post : p.dw_next)) continue;
-    // one gate row: its sum is the one behind dw_post
     const bool pieces = of_gate && !p.one_gate;
     const float* part = what == 1 ? p.part_next : pieces ? p.part_gate : p.part_post;
+    int64_t r = what - 2;
     int i0 = 0, i1 = p.parts;
-    if (pieces && p.strips > 0) {
+    if (of_gate && across) {
+      const int64_t end = by_end ? strip_row(p.T, p.strips, what - 1) : 0;
+      if (by_end) r = (end - 1) / p.gate_span;
       i0 = static_cast<int>(strip_of(p.T, p.strips, r * p.gate_span));
+      if (by_end && i0 != what - 2) continue;
       i1 = static_cast<int>(strip_of(p.T, p.strips, (r + 1) * p.gate_span - 1)) + 1;
-      if (i1 - i0 == 1) continue;                  // written by its strip
+      if (i1 - i0 == 1) continue;
     }
     float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     for (int i = i0 + w; i < i1; i += kWarps * kLoads) {
@@ -471,10 +631,29 @@ int rows_grid(int64_t T) {
   return static_cast<int>(T < most ? T : most);
 }
 
+// Bytes of the gate in a row of the ring: a token's own.
+int token_gate_bytes(const NormParams& p) {
+  return p.gate && p.gate_span == 1 && p.T > 1 ? p.H * (p.weights_f32 ? 4 : 2) : 0;
+}
+
 // Threads of a forward CTA that hold a row in V vectors each (0: too long).
 int forward_threads(int H, int W, int V) {
   const int threads = (H / W + 32 * V - 1) / (32 * V) * 32;
   return threads <= 1024 ? threads : 0;
+}
+
+// f(kWarp, V) of the kernels that take any length of a row.
+template <typename F>
+void with_rows_of(int H, F f) {
+  using std::integral_constant;
+  if (H <= kWarpH && H % 4 == 0)
+    f(std::true_type(), integral_constant<int, 4>());
+  else if (H <= kWarpH)
+    f(std::true_type(), integral_constant<int, 1>());
+  else if (H % 4 == 0)
+    f(std::false_type(), integral_constant<int, 4>());
+  else
+    f(std::false_type(), integral_constant<int, 1>());
 }
 
 template <typename ST, typename WT>
@@ -483,7 +662,7 @@ cudaError_t forward(const NormParams& p, void* out, void* n, float* rstd_y, floa
   // up to one row an SM the kernel without a ring is shorter (1 x 7168: 3.8
   // against 4.4 us); beyond, rows through shared memory (4096 x 4096: 31
   // against 37 us)
-  const int row_bytes = p.H * static_cast<int>(sizeof(ST) + (p.y ? 2 : 0));
+  const int row_bytes = p.H * static_cast<int>(sizeof(ST) + (p.y ? 2 : 0)) + token_gate_bytes(p);
   const RingShape r = ring_shape(p.T, p.H, row_bytes, false, false);
   if (r.groups > 0 && p.T > device_sm_count()) {
     RingOut ro = {};
@@ -510,7 +689,12 @@ cudaError_t forward(const NormParams& p, void* out, void* n, float* rstd_y, floa
         p, o, nn, rstd_y, rstd_out);
     return cudaGetLastError();
   }
-  norm_rows_kernel<ST, WT><<<rows_grid(p.T), kNormThreads, 0, s>>>(p, o, nn, rstd_y, rstd_out);
+  with_rows_of(p.H, [&](auto warp, auto width) {
+    constexpr bool kWarp = decltype(warp)::value;
+    constexpr int V = decltype(width)::value;
+    norm_rows_kernel<ST, WT, kWarp, V>
+        <<<rows_grid(kWarp ? (p.T + 7) / 8 : p.T), kNormThreads, 0, s>>>(p, o, nn, rstd_y, rstd_out);
+  });
   return cudaGetLastError();
 }
 
@@ -522,14 +706,16 @@ struct NormGrads {
 };
 
 int row_bytes_of(const NormParams& p, int stream_size) {
-  return p.H * ((p.x ? stream_size : 0) + (p.d_n ? stream_size + 2 : 0) + (p.y ? 2 : 0));
+  return p.H * ((p.x ? stream_size : 0) + (p.d_n ? stream_size + 2 : 0) + (p.y ? 2 : 0)) +
+         token_gate_bytes(p);
 }
 
 template <typename ST, typename WT>
 cudaError_t backward(const NormParams& p, const NormGrads& g, void* ws, cudaStream_t s) {
   const bool one_gate = p.gate && p.T > 0 && p.gate_span == p.T;
   const int row_bytes = row_bytes_of(p, sizeof(ST));
-  RingShape b = ring_shape(p.T, p.H, row_bytes, true, p.gate && !one_gate);
+  RingShape b = ring_shape(p.T, p.H, row_bytes, true,
+                           p.gate && !one_gate && p.gate_span > 1);
   if (b.groups == 0) {
     const int64_t most = static_cast<int64_t>(device_sm_count()) * 2;
     b.strips = b.ctas = static_cast<int>(p.T < most ? p.T : most);
@@ -552,14 +738,22 @@ cudaError_t backward(const NormParams& p, const NormGrads& g, void* ws, cudaStre
     o.accumulate = g.accumulate;
     e = launch_norm_ring(p, b, o, sizeof(ST) == 4, true, row_bytes, s);
   } else if (p.T > 0) {
-    const unsigned cols = static_cast<unsigned>((p.H + 127) / 128);
-    norm_rows_backward_kernel<ST, WT, true><<<rows_grid(p.T), kNormThreads, 0, s>>>(
-        p, static_cast<ST*>(g.dx), static_cast<__nv_bfloat16*>(g.dy), c_of);
-    if (part_post || part_next || g.dgate)
-      norm_cols_backward_kernel<ST, WT><<<dim3(cols, b.strips), 128, 0, s>>>(
-          p, c_of, part_post, part_next, part_gate, one_gate, g.dgate, g.accumulate);
-    norm_rows_backward_kernel<ST, WT, false><<<rows_grid(p.T), kNormThreads, 0, s>>>(
-        p, static_cast<ST*>(g.dx), static_cast<__nv_bfloat16*>(g.dy), c_of);
+    ST* dx = static_cast<ST*>(g.dx);
+    __nv_bfloat16* dy = static_cast<__nv_bfloat16*>(g.dy);
+    with_rows_of(p.H, [&](auto warp, auto width) {
+      constexpr bool kWarp = decltype(warp)::value;
+      constexpr int V = decltype(width)::value;
+      const int rows = rows_grid(kWarp ? (p.T + 7) / 8 : p.T);
+      norm_rows_backward_kernel<ST, WT, true, kWarp, V><<<rows, kNormThreads, 0, s>>>(p, dx, dy,
+                                                                                    c_of);
+      if (part_post || part_next || g.dgate) {
+        const unsigned cols = static_cast<unsigned>((p.H + 128 * V - 1) / (128 * V));
+        norm_cols_backward_kernel<ST, WT, V><<<dim3(cols, b.strips), 128, 0, s>>>(
+            p, c_of, part_post, part_next, part_gate, one_gate, g.dgate, g.accumulate);
+      }
+      norm_rows_backward_kernel<ST, WT, false, kWarp, V><<<rows, kNormThreads, 0, s>>>(p, dx, dy,
+                                                                                     c_of);
+    });
     e = cudaGetLastError();
   }
   if (e != cudaSuccess || !(g.dw_post || g.dw_next || g.dgate)) return e;
@@ -567,7 +761,9 @@ cudaError_t backward(const NormParams& p, const NormGrads& g, void* ws, cudaStre
                     p.w_post,  p.gate,      p.T,       p.gate_span, g.dgate ? g.gate_rows : 0,
                     p.H,       b.ctas,      b.strips,  one_gate,  g.accumulate, sizeof(WT) == 4,
                     p.b};
-  const int64_t want = 2 + f.gate_rows;
+  // a row for each token (and with fewer tokens than strips, none across them)
+  if (p.T > 0 && p.gate_span == 1 && !one_gate) f.dgate = nullptr;
+  const int64_t want = 2 + finish_gates(f);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   // its CTAs may come up while the last rows are still worked on; they wait

@@ -31,6 +31,11 @@ constexpr int kMaxStages = 4;
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kCols = 16;                 // of a thread
 
+// How tokens share gate rows: one row (or none), whose factors stay in
+// registers; several rows of several tokens each, loaded as a strip comes to
+// them; a row for each token, which comes through the ring.
+enum Gate { kOneGate, kManyGates, kTokenGates };
+
 struct RingParams {
   NormParams n;
   RingOut o;
@@ -254,6 +259,20 @@ __device__ __forceinline__ void times(const RingParams& p, const Walk<V>& w, con
   }
 }
 
+// A gate row's vector in shared memory.
+template <int W>
+__device__ __forceinline__ Vec<W> gate_of(const RingParams& p, const unsigned char* row, int col) {
+  if (!p.n.weights_f32) return widen<W>(get_half<W>(row + col * 2));
+  Vec<W> v;
+#pragma unroll
+  for (int i = 0; i < W / 4; ++i) {
+    const ulonglong2 q = reinterpret_cast<const ulonglong2*>(row + col * 4)[i];
+    v.p[2 * i] = q.x;
+    v.p[2 * i + 1] = q.y;
+  }
+  return v;
+}
+
 // Waits for a stage. No wait as long as the limit is legitimate: it is
 // reported, and the waits after it are given up at once.
 template <int V>
@@ -271,7 +290,7 @@ __device__ __forceinline__ void wait_stage(const RingParams& p, const Walk<V>& w
 // kAll: with y, w_post and w_next. 4096 x 4096 in bf16 takes 24 us alone and 27
 // with inputs from HBM (134 MB: 5.0 TB/s), of which 4 are launch and the first
 // rows' way; 16384 x 7168 151 us (6.2 TB/s).
-template <typename ST, bool kMany, bool kFull, bool kAll>
+template <typename ST, int kGate, bool kFull, bool kAll>
 __global__ void __launch_bounds__(kThreads, 1)
     norm_ring_kernel(const __grid_constant__ RingParams p) {
   constexpr int W = Stream<ST>::W, V = Stream<ST>::V, P = W / 2, kSize = sizeof(ST);
@@ -282,12 +301,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Walk<V> w = walk_of<V, kFull>(p, ring_all, full_all, &abort_wait);
   const NormParams& q = p.n;
   const bool branch = kAll || q.y, post = kAll || q.w_post, next = kAll || q.w_next;
+  constexpr bool kMany = kGate == kManyGates, kToken = kGate == kTokenGates;
   const int wide = w.H * kSize, half = w.H * 2;
+  const int at_g = wide + half, gate_bytes = q.weights_f32 ? w.H * 4 : half;
   auto issue = [&](int64_t t, int stage) {
     const uint32_t bar = w.full + 8 * stage, to = smem_u32(w.ring) + stage * p.row_bytes;
     mbar_arrive_expect_tx(bar, p.row_bytes);
     bulk_copy_g2s(to, static_cast<const ST*>(q.x) + t * w.H, wide, bar);
     if (branch) bulk_copy_g2s(to + wide, q.y + t * w.H, half, bar);
+    if (kToken)
+      bulk_copy_g2s(to + at_g, static_cast<const char*>(q.gate) + t * gate_bytes, gate_bytes, bar);
   };
   if (w.tid == 0)
     for (int i = 0; i < p.r.stages && w.lo + i < w.hi; ++i) issue(w.lo + i, i);
@@ -301,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (next) times(p, w, q.w_next, 0, wn);
   if (!kMany) {
     if (post) times(p, w, q.w_post, 0, gw);
-    if (q.gate) times(p, w, q.gate, 0, gw);
+    if (kGate == kOneGate && q.gate) times(p, w, q.gate, 0, gw);
   }
   int64_t gate_row = -1;
   int to_gate = 0;                                 // rows until another gate row
@@ -334,6 +357,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         y[v] = widen<W>(get_half<W>(row_y + v * w.step * 2));
 #pragma unroll
         for (int h = 0; h < P; ++h) s = fma2(y[v].p[h], y[v].p[h], s);
+        if (kToken) {
+          const Vec<W> g = gate_of<W>(p, w.ring + stage * p.row_bytes + at_g, w.col0 + v * w.step);
+#pragma unroll
+          for (int h = 0; h < P; ++h) y[v].p[h] = mul2(y[v].p[h], g.p[h]);
+        }
       }
     }
     float ry = 1.0f;
@@ -391,14 +419,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 //   A = d_out + r d_n w_next,  k = -r (r (r m(d_n w_next out))).
 // The gradient of y's norm needs m(gw D y), gw = b g w_post, which is
 // m(gw A y) + k m(gw out y): three sums of one pass over the row, one barrier.
-// With r = rstd_y: S += r D y (dw_post = b g S and dgate = b w_post S for one
-// gate row; kMany keeps S for a row's tokens, and its sum over rows times g in
-// shared memory), dy = r (gw D - y (r^2 m(gw D y))).
+// With r = rstd_y: S += r D y, and dy = r (gw D - y (r^2 m(gw D y))). One gate
+// row: dw_post = b g S and dgate = b w_post S; kManyGates keeps S for a row's
+// tokens, and its sum over rows times g in shared memory; kTokenGates sums g
+// times it and writes dgate at once (16384 x 2048 in bf16: 107 us at a floor of 89;
+// by kManyGates' way of leaving a row 409).
 // kAll: with d_out, d_n, y and w_post. 16384 x 7168 with a float stream takes
 // 331 us (2.1 GB: 6.4 TB/s, 94% of a copy's rate), in bf16 229 us (6.2 TB/s);
 // 4083 x 2048 in bf16 with three gate rows 32 us (3.1 TB/s), of which some 9 are
 // launches, the first rows' way and the strips' sums.
-template <typename ST, bool kMany, bool kFull, bool kAll>
+template <typename ST, int kGate, bool kFull, bool kAll>
 __global__ void __launch_bounds__(kThreads, 1)
     norm_ring_backward_kernel(const __grid_constant__ RingParams p) {
   constexpr int W = Stream<ST>::W, V = Stream<ST>::V, P = W / 2, kSize = sizeof(ST);
@@ -410,10 +440,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const NormParams& q = p.n;
   const bool branch = kAll || q.y, post = kAll || q.w_post, next = kAll || q.d_n,
              has_d = kAll || q.x;
+  constexpr bool kMany = kGate == kManyGates, kToken = kGate == kTokenGates;
   // a stage: d_out, out, y, d_n, as far as there are any
   const int wide = w.H * kSize, half = w.H * 2;
   const int at_out = has_d ? wide : 0, at_y = at_out + (next ? wide : 0),
-            at_dn = at_y + (branch ? half : 0);
+            at_dn = at_y + (branch ? half : 0), at_g = at_dn + (next ? half : 0);
+  const int gate_bytes = q.weights_f32 ? w.H * 4 : half;
   auto issue = [&](int64_t t, int stage) {
     const uint32_t bar = w.full + 8 * stage, to = smem_u32(w.ring) + stage * p.row_bytes;
     const int64_t at = t * w.H;
@@ -422,19 +454,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (next) bulk_copy_g2s(to + at_out, static_cast<const ST*>(q.out) + at, wide, bar);
     if (branch) bulk_copy_g2s(to + at_y, q.y + at, half, bar);
     if (next) bulk_copy_g2s(to + at_dn, q.d_n + at, half, bar);
+    if (kToken)
+      bulk_copy_g2s(to + at_g, static_cast<const char*>(q.gate) + t * gate_bytes, gate_bytes, bar);
   };
   if (w.tid == 0)
     for (int i = 0; i < p.r.stages && w.lo + i < w.hi; ++i) issue(w.lo + i, i);
 
   // kMany: the group's sum of g S, behind the rings; the only group's is the
   // CTA's partial sum itself
-  float* sum_w = nullptr;
-  if (kMany && p.o.part_post)
-    sum_w = (p.r.tail_bytes ? reinterpret_cast<float*>(ring_all + static_cast<size_t>(p.r.groups) *
-                                                                      p.r.stages * p.row_bytes) +
-                                  w.g * w.H
-                            : p.o.part_post + static_cast<int64_t>(blockIdx.x) * w.H) +
-            w.col0;
+  auto sum_of_groups = [&]() {
+    return p.r.tail_bytes ? reinterpret_cast<float*>(ring_all + static_cast<size_t>(p.r.groups) *
+                                                                    p.r.stages * p.row_bytes)
+                          : p.o.part_post + static_cast<int64_t>(blockIdx.x) * w.H;
+  };
+  const bool keep_w = kMany && p.o.part_post;
   Pair gw[kCols / 2], wn[kCols / 2], sum_s[kCols / 2], sum_n[kCols / 2];
 #pragma unroll
   for (int i = 0; i < kCols / 2; ++i) {
@@ -444,15 +477,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (next) times(p, w, q.w_next, 0, wn);
   if (kMany) {
+    float* sum_w = keep_w ? sum_of_groups() + (p.r.tail_bytes ? w.g * w.H : 0) + w.col0 : nullptr;
 #pragma unroll
     for (int v = 0; v < V; ++v)
-      if (w.has[v] && sum_w)
+      if (w.has[v] && keep_w)
 #pragma unroll
         for (int i = 0; i < W; i += 4)
           *reinterpret_cast<float4*>(sum_w + v * w.step + i) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   } else {
     if (post) times(p, w, q.w_post, 0, gw);
-    if (q.gate) times(p, w, q.gate, 0, gw);
+    if (kGate == kOneGate && q.gate) times(p, w, q.gate, 0, gw);
   }
   int64_t gate_row = -1;
   int to_gate = 0;                                 // rows until another gate row
@@ -507,8 +541,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (branch) {
         y[v] = get_half<W>(row_half + (at_y + v * w.step * 2));
         if (post) {
-          const Vec<W> f = widen<W>(y[v]);
-          Vec<W> o;
+          Vec<W> f = widen<W>(y[v]), o;
+          if (kToken) {
+            const Vec<W> g = gate_of<W>(p, w.ring + stage * p.row_bytes + at_g,
+                                        w.col0 + v * w.step);
+#pragma unroll
+            for (int h = 0; h < P; ++h) f.p[h] = mul2(f.p[h], g.p[h]);
+          }
           if (next) o = Stream<ST>::get(row_wide + (at_out + v * w.step * kSize)).wide();
 #pragma unroll
           for (int h = 0; h < P; ++h) {
@@ -535,9 +574,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int h = 0; h < P; ++h) d[v].p[h] = fma2(k, o.p[h], d[v].p[h]);
       }
     }
-    // every thread has the row in registers: its stage takes another
-    group_barrier(w.g + 1, p.r.group);
-    if (w.tid == 0 && t + p.r.stages < rows) issue(w.lo + t + p.r.stages, stage);
+    // every thread has the row in registers: its stage takes another (after the
+    // gate's row has been read too)
+    auto refill = [&]() {
+      group_barrier(w.g + 1, p.r.group);
+      if (w.tid == 0 && t + p.r.stages < rows) issue(w.lo + t + p.r.stages, stage);
+    };
+    if (!kToken) refill();
     const int64_t first_col = (w.lo + t) * w.H + w.col0;
     unsigned char* to_dx = static_cast<unsigned char*>(p.o.stream) + first_col * kSize;
     unsigned char* to_dy = reinterpret_cast<unsigned char*>(p.o.branch) + first_col * 2;
@@ -546,20 +589,42 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!w.has[v]) continue;
       if (branch) {
         const Vec<W> f = widen<W>(y[v]);
-        Vec<W> g;
+        Vec<W> g, z;
+        if (kToken)
+          z = gate_of<W>(p, w.ring + stage * p.row_bytes + at_g, w.col0 + v * w.step);
 #pragma unroll
         for (int h = 0; h < P; ++h) {
           const int i = P * v + h;
-          sum_s[i] = fma2(mul2(d[v].p[h], f.p[h]), e, sum_s[i]);
+          Pair u = mul2(d[v].p[h], f.p[h]);        // D y
           g.p[h] = mul2(gw[i], d[v].p[h]);
+          if (kToken) {
+            u = mul2(u, e);
+            sum_s[i] = fma2(u, z.p[h], sum_s[i]);
+            g.p[h] = mul2(g.p[h], z.p[h]);
+            z.p[h] = mul2(u, gw[i]);               // this token's dgate
+          } else {
+            sum_s[i] = fma2(u, e, sum_s[i]);
+          }
           if (post) g.p[h] = mul2(e, fma2(l, f.p[h], g.p[h]));
         }
         put_half<W>(to_dy + v * w.step * 2, g);
+        if (kToken) {
+          float* to = p.o.dgate + first_col + v * w.step;
+#pragma unroll
+          for (int i = 0; i < W; i += 4) {
+            const float2 lo = halves(z.p[i / 2]), hi = halves(z.p[i / 2 + 1]);
+            float4 old = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (p.o.accumulate) old = *reinterpret_cast<const float4*>(to + i);
+            *reinterpret_cast<float4*>(to + i) =
+                make_float4(old.x + lo.x, old.y + lo.y, old.z + hi.x, old.w + hi.y);
+          }
+        }
       }
 #pragma unroll
       for (int h = 0; h < P; ++h) d[v].p[h] = mul2(a, d[v].p[h]);
       put_stream<ST, W>(to_dx + v * w.step * kSize, d[v]);
     }
+    if (kToken) refill();
     if (kMany && (--to_gate == 0 || t + 1 == rows)) {
       // S of the gate row: whole to dgate, else a piece (0: begun in an earlier
       // strip, 1: in this one); its share of dw_post stays
@@ -580,9 +645,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         *reinterpret_cast<float4*>(at) =
             make_float4(z.x + lo.x, z.y + lo.y, z.z + hi.x, z.w + hi.y);
       };
+      float* sum_w = keep_w ? sum_of_groups() + (p.r.tail_bytes ? w.g * w.H : 0) + w.col0 : nullptr;
 #pragma unroll
       for (int v = 0; v < V; ++v)
-        if (w.has[v] && sum_w)
+        if (w.has[v] && keep_w)
 #pragma unroll
           for (int i = 0; i < W; i += 4) add4(sum_w + v * w.step + i, P * v + i / 2, true);
 #pragma unroll
@@ -623,8 +689,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               make_ulonglong2(sum[P * v + i / 2], sum[P * v + i / 2 + 1]);
     return reinterpret_cast<const float*>(ring_all);
   };
-  if (kMany ? p.r.tail_bytes > 0 && sum_w : p.o.part_post != nullptr)
-    add_up(kMany ? sum_w - w.g * w.H - w.col0 : share(sum_s), p.o.part_post);
+  if (p.o.part_post && !(kMany && p.r.tail_bytes == 0))
+    add_up(kMany ? sum_of_groups() : share(sum_s), p.o.part_post);
   if (p.o.part_next) add_up(share(sum_n), p.o.part_next);
 }
 
@@ -646,24 +712,31 @@ cudaError_t launch(K* kernel, const RingParams& p, size_t smem, cudaStream_t st)
 }
 
 template <typename ST, bool kFull, bool kAll>
-cudaError_t launch_of(const RingParams& p, bool backward, bool many, size_t smem, cudaStream_t st) {
-  auto* kernel = backward ? (many ? norm_ring_backward_kernel<ST, true, kFull, kAll>
-                                  : norm_ring_backward_kernel<ST, false, kFull, kAll>)
-                          : (many ? norm_ring_kernel<ST, true, kFull, kAll>
-                                  : norm_ring_kernel<ST, false, kFull, kAll>);
+cudaError_t launch_of(const RingParams& p, bool backward, int gate, size_t smem, cudaStream_t st) {
+  auto* kernel =
+      backward ? (gate == kTokenGates  ? norm_ring_backward_kernel<ST, kTokenGates, kFull, kAll>
+                  : gate == kManyGates ? norm_ring_backward_kernel<ST, kManyGates, kFull, kAll>
+                                       : norm_ring_backward_kernel<ST, kOneGate, kFull, kAll>)
+               : (gate == kTokenGates  ? norm_ring_kernel<ST, kTokenGates, kFull, kAll>
+                  : gate == kManyGates ? norm_ring_kernel<ST, kManyGates, kFull, kAll>
+                                       : norm_ring_kernel<ST, kOneGate, kFull, kAll>);
   return launch(kernel, p, smem, st);
 }
 
 // Rows of a multiple of 512 with all the tensors are what layers have; any
 // other takes the kernels that look at each run.
 template <typename ST>
-cudaError_t launch_of(const RingParams& p, bool backward, bool many, size_t smem, cudaStream_t st) {
+cudaError_t launch_of(const RingParams& p, bool backward, size_t smem, cudaStream_t st) {
   const NormParams& n = p.n;
+  const int gate = !n.gate || n.gate_span == n.T ? kOneGate
+                   : n.gate_span == 1            ? kTokenGates
+                                                 : kManyGates;
   const bool full = n.H == kCols * p.r.group;
   const bool all = n.y && n.w_post && (backward ? n.x && n.d_n : n.w_next != nullptr);
-  return full ? (all ? launch_of<ST, true, true>(p, backward, many, smem, st)
-                     : launch_of<ST, true, false>(p, backward, many, smem, st))
-              : launch_of<ST, false, false>(p, backward, many, smem, st);
+  return full ? (all ? launch_of<ST, true, true>(p, backward, gate, smem, st)
+                     : launch_of<ST, true, false>(p, backward, gate, smem, st))
+              : (all ? launch_of<ST, false, true>(p, backward, gate, smem, st)
+                     : launch_of<ST, false, false>(p, backward, gate, smem, st));
 }
 
 }  // namespace
@@ -699,12 +772,11 @@ RingShape ring_shape(int64_t T, int H, int row_bytes, bool backward, bool many) 
 cudaError_t launch_norm_ring(const NormParams& n, const RingShape& r, const RingOut& o,
                              bool stream_f32, bool backward, int row_bytes, cudaStream_t st) {
   const RingParams p = {n, o, r, row_bytes, device_error_word()};
-  const bool many = n.gate && n.gate_span < n.T;
   const size_t rings = static_cast<size_t>(r.groups) * (r.stages * row_bytes + r.tail_bytes);
   const size_t sums = backward ? static_cast<size_t>(r.groups) * n.H * sizeof(float) : 0;
   const size_t smem = rings > sums ? rings : sums;
-  return stream_f32 ? launch_of<float>(p, backward, many, smem, st)
-                    : launch_of<__nv_bfloat16>(p, backward, many, smem, st);
+  return stream_f32 ? launch_of<float>(p, backward, smem, st)
+                    : launch_of<__nv_bfloat16>(p, backward, smem, st);
 }
 
 }  // namespace moe
