@@ -772,6 +772,19 @@ def _raw_stream(stream, dev):
     return stream.cuda_stream
 
 
+def _elsewhere(stream):
+    """Whether the call is for another stream than its device's current one."""
+    return stream is not None and stream != torch.cuda.current_stream(stream.device)
+
+
+def _within(stream, fn, args):
+    """fn(**args) with stream current, so that what it allocates is stream's: memory
+    of another one's pool may still be in use there, and would go back to it
+    while the kernels run."""
+    with torch.cuda.stream(stream):
+        return fn(**args)
+
+
 def _scratch(workspace, need, dev):
     """(the given workspace or a new one, its bytes); None where none is needed."""
     if workspace is not None:
@@ -811,6 +824,8 @@ def moe_route_gate(logits: torch.Tensor, k: int, bias=None, score="softmax", n_g
     renormalised over the chosen and scaled: (expert_ids int32 [T, k], probs
     float32 [T, k], counts int32 [E], offsets int32 [E+1]) of float32 or
     bfloat16 logits [T, E]."""
+    if _elsewhere(stream):
+        return _within(stream, moe_route_gate, locals())
     lt = _typed(logits, "logits")
     T, E = logits.shape
     dev = logits.device
@@ -838,6 +853,8 @@ def moe_route_gate_backward(dprobs, logits, expert_ids, bias=None, score="softma
                             renormalise=True, scale=1.0, dlogits=None, stream=None):
     """dlogits [T, E], of the logits' type, of moe_route_gate's weights for the
     choice expert_ids that it made; bias, score, renormalise and scale as there."""
+    if _elsewhere(stream):
+        return _within(stream, moe_route_gate_backward, locals())
     lt = _typed(logits, "logits")
     T, E = logits.shape
     k = expert_ids.shape[1]
@@ -889,6 +906,8 @@ def moe_norm_residual(x, y=None, w_post=None, gate=None, w_next=None, eps=1e-6,
     / rows consecutive tokens to a row) it is 1, without w_next n is left out.
     Without y it is the norm alone, of x. Returns dict(out, n, rstd_y,
     rstd_out), None where nothing was computed; out may be x itself."""
+    if _elsewhere(stream):
+        return _within(stream, moe_norm_residual, locals())
     st = _typed(x, "x")
     T, H = x.shape
     dev = x.device
@@ -929,6 +948,8 @@ def moe_norm_residual_backward(d_out, d_n, out, y=None, w_post=None, gate=None, 
     forward's. Returns dict(dx, dy, dw_post, dgate, dw_next), the last three in
     float32 and, with accumulate_dw, added to what the given tensors hold; None
     where there is no such input. dx may be d_out itself."""
+    if _elsewhere(stream):
+        return _within(stream, moe_norm_residual_backward, locals())
     st = _typed(out, "out")
     T, H = out.shape
     dev = out.device
@@ -981,6 +1002,8 @@ def moe_clip_grad_norm(grads, max_norm, out=None, norm_type=2.0, eps=1e-6, norm_
     or into the tensors of the list out (same types and sizes). norm_type is 2.0
     or math.inf; max_norm None computes the norm alone. Returns (norm, coef), two
     float32 tensors of one element; nothing is read back to the host."""
+    if _elsewhere(stream):
+        return _within(stream, moe_clip_grad_norm, locals())
     grads = list(grads)
     if norm_type not in (2.0, math.inf):
         raise ValueError(f"norm_type must be 2.0 or inf, got {norm_type}")

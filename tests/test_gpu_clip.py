@@ -2,7 +2,7 @@
 
 Tolerances, in half steps of float32 (H = 2^-24 relative): squares are summed
 in float over runs of at most 128 terms (128 H of the sum, half of that in its
-root) and in double beyond; norm and coef are rounded once (H each), a scaled
+root) and as pairs of floats, which lose next to nothing, beyond; norm and coef are rounded once (H each), a scaled
 gradient once more, and bfloat16 results by half a step, 2^-8."""
 import math
 

@@ -174,6 +174,58 @@ def test_gate_many_tokens_and_repeats():
                                atol=0)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_gate_masks_of_the_types_lowest_value(dtype):
+    # masked with finfo.min instead of -inf: real numbers, that are chosen where the
+    # others run out, and with a weight of zero unless all of a row's are such
+    E, k, low = 48, 8, torch.finfo(dtype).min
+    logits = _logits(120, E, dtype)
+    logits[40:80, 5:] = low                        # fewer open experts than k
+    logits[80:, :] = low
+    logits[100:, 7] = -math.inf
+    for score in ("softmax", "sigmoid"):
+        for b in (None, _bias(E)):
+            for groups in ({}, dict(n_group=6, topk_group=2, group_topk=2)):
+                how = dict(score=score, **groups)
+                rid, rw, rc, _ = orc.route_gate(logits.float().numpy(), k,
+                                                bias=None if b is None else b.numpy(), **how)
+                ids, w, counts, _ = m.moe_route_gate(dev(logits), k, bias=dev(b), **how)
+                assert np.array_equal(ids.cpu().numpy(), rid)
+                assert np.array_equal(counts.cpu().numpy(), rc)
+                # among themselves the masked are equal: the others' spread counts
+                tol = _units(torch.where(logits == low, torch.zeros_like(logits), logits), k)
+                assert np.all(np.abs(w.cpu().numpy() - rw) <= tol * np.abs(rw) + TINY)
+
+
+def test_gate_past_two_to_the_31_elements():
+    T, E, k, last = (1 << 21) + 77, 1024, 4, 100
+    logits = torch.empty((T, E), dtype=torch.bfloat16, device="cuda").normal_()
+    ids, w, counts, offsets = m.moe_route_gate(logits, k)
+    assert m.moe_get_error() == 0 and int(counts.sum()) == int(offsets[-1]) == T * k
+    tail = logits[-last:].clone()
+    tid, tw, _, _ = m.moe_route_gate(tail, k)
+    assert torch.equal(ids[-last:], tid) and torch.equal(w[-last:], tw)
+    assert torch.equal(counts, torch.bincount(ids.reshape(-1), minlength=E).to(torch.int32))
+    dp = torch.empty((T, k), device="cuda").normal_()
+    got = m.moe_route_gate_backward(dp, logits, ids)
+    assert torch.equal(got[-last:], m.moe_route_gate_backward(dp[-last:].clone(), tail, tid))
+
+
+def test_gate_allocates_on_the_stream_that_it_runs_on():
+    logits = dev(_logits(70001, 64))
+    want = m.moe_route_gate(logits, 6)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = []
+    for _ in range(8):                             # workspaces and results of the side stream
+        got.append(m.moe_route_gate(logits, 6, stream=side))
+        torch.full((1 << 20,), -1, dtype=torch.int32, device="cuda")
+    side.synchronize()
+    for g in got:
+        for x, y in zip(g, want):
+            assert torch.equal(x, y)
+
+
 def test_gate_zero_tokens():
     ids, w, counts, offsets = m.moe_route_gate(dev(torch.zeros((0, 12))), 3)
     assert ids.shape == (0, 3) and w.shape == (0, 3)

@@ -6,7 +6,8 @@ non-negative terms is off by at most the length of its longest chain of
 additions, here at most width / 256 + 16 terms a thread and lane (64 lanes at
 least share a row), and its root by half of that; what a result multiplies
 and adds up takes some 8 roundings more. C = 24 + width / 64 half steps
-bound all of that, of the sum of the terms' magnitudes. A column sum over T
+bound all of that, of the sum of the terms' magnitudes (up to 1024 elements
+32 lanes may share a row: width / 32 + 5 terms, fewer than C). A column sum over T
 tokens adds at most T half steps. bfloat16 results add half a step, 2^-8;
 bfloat16 reads are exact."""
 import numpy as np
@@ -154,6 +155,35 @@ def test_norm_gate_rows_across_strips():
     for T, rows in ((1000, 4), (1216, 304), (912, 456), (2000, 1000), (700, 7), (305, 305)):
         v, d_out, d_n = _inputs(T, 136, "bf16", "f32", True, rows, True, seed=T)
         _check(v, d_out, d_n, a=1.0, b=0.5)
+
+
+@pytest.mark.parametrize("T,W", [(1, 512), (151, 512), (2500, 512), (700, 1024), (333, 264),
+                                 (170, 2304), (160, 1364), (90, 8192), (40, 10240), (500, 45)])
+@pytest.mark.parametrize("stream,weights", [("bf16", "bf16"), ("f32", "f32"), ("bf16", "f32")])
+def test_norm_gate_row_for_each_token(T, W, stream, weights):
+    v, d_out, d_n = _inputs(T, W, stream, weights, True, T, True, seed=3)
+    _check(v, d_out, d_n, a=0.5, b=2.0)
+    v, d_out, d_n = _inputs(T, W, stream, weights, False, T, False, seed=4)
+    d = {key: dev(t) for key, t in v.items()}
+    got = m.moe_norm_residual(**d)
+    back = dict(y=d["y"], gate=d["gate"])
+    one = m.moe_norm_residual_backward(dev(d_out), None, got["out"], **back)
+    two = m.moe_norm_residual_backward(dev(d_out), None, got["out"], **back,
+                                       dgate=torch.ones((T, W), device="cuda"),
+                                       accumulate_dw=True)
+    assert torch.equal(two["dgate"], one["dgate"] + 1.0)
+    want = orc.norm_residual_backward(_np(d_out), None, _np(got["out"]), y=_np(v["y"]),
+                                      gate=_np(v["gate"]))
+    _near(one["dgate"], want["dgate"], np.abs(want["dgate"]), 24, "dgate")
+    _near(one["dy"], want["dy"], np.abs(want["dy"]), 24, "dy")
+
+
+@pytest.mark.parametrize("W", [36, 1020, 1021, 1028, 8200, 16388, 20001])
+@pytest.mark.parametrize("rows", [0, 1, 6, 30])
+def test_norm_lengths_that_the_ring_does_not_take(W, rows):
+    for stream, weights in (("bf16", "f32"), ("f32", "bf16")):
+        v, d_out, d_n = _inputs(30, W, stream, weights, True, rows, True, seed=5)
+        _check(v, d_out, d_n, a=1.5, b=0.5)
 
 
 def test_norm_zero_rows_and_large_values():
