@@ -160,26 +160,44 @@ __device__ __noinline__ void choose_in_double(const GateParams& p, const L* row,
                                               Pick* pick) {
   const int lane = lane_id();
   const int size = p.E / p.n_group;
+  const bool soft = p.score == MOE_SCORE_SOFTMAX;
+  const bool scored = p.bias != nullptr || p.n_group > 1;      // else the logits' own order
+  // one exponential for all experts where their logits are the same (of a router
+  // whose weights are still zero, say)
+  float m = -INFINITY, least = INFINITY;
+  int open = 0;
+  for (int e = lane; e < p.E; e += 32) {
+    const float l = clean(load_logit(row + e));
+    m = fmaxf(m, l);
+    if (l == -INFINITY) continue;
+    least = fminf(least, l);
+    ++open;
+  }
+  m = seg_max<32>(m);
+  const bool level = -seg_max<32>(-least) >= m;
   double inv = 1.0, top = 0.0;
-  if (p.score == MOE_SCORE_SOFTMAX) {
-    float m = -INFINITY;
-    for (int e = lane; e < p.E; e += 32) m = fmaxf(m, clean(load_logit(row + e)));
-    m = seg_max<32>(m);
+  if (soft && scored) {
     top = m == -INFINITY ? 0.0 : static_cast<double>(m);
-    double sum = 0.0;
+    double sum = open;
+    if (!level) {
+      sum = 0.0;
 #pragma unroll 4
-    for (int e = lane; e < p.E; e += 32) sum += exp(clean(load_logit(row + e)) - top);
+      for (int e = lane; e < p.E; e += 32) sum += exp(clean(load_logit(row + e)) - top);
+    }
     sum = seg_sum<32>(sum);
     inv = sum > 0.0 ? 1.0 / sum : 0.0;
   }
+  auto score = [&](float l) {
+    const double ex = exp(soft ? l - top : -static_cast<double>(l));
+    return soft ? ex * inv : 1.0 / (1.0 + ex);
+  };
+  const double same = scored && level ? score(m) : 0.0;
   __syncwarp();
 #pragma unroll 4
   for (int e = lane; e < p.E; e += 32) {
     const float l = clean(load_logit(row + e));
     const float b = p.bias ? clean(__ldg(p.bias + e)) : 0.0f;
-    const double ex = exp(p.score == MOE_SCORE_SOFTMAX ? l - top : -static_cast<double>(l));
-    const double s = p.score == MOE_SCORE_SOFTMAX ? ex * inv : 1.0 / (1.0 + ex);
-    v[e] = l == -INFINITY || b == -INFINITY ? -INFINITY : s + b;
+    v[e] = l == -INFINITY || b == -INFINITY ? -INFINITY : (scored && !level ? score(l) : same) + b;
   }
   __syncwarp();
   unsigned kept = kAll;
@@ -509,7 +527,8 @@ struct GateShape {
 // most of it launch and latency. Sixteen experts a lane measured 67 against 71
 // us for eight (65536 x 256), four CTAs an SM 60 against 67 for three. A row
 // whose logits and bias are all the same ties beyond 32 candidates and is
-// chosen in double: 65536 such rows take 1 ms.
+// left to choose_in_double: 65536 such rows take 0.35 ms (1 to 1.45 ms with an
+// exponential for each expert).
 template <typename L, int W, int C, bool kScored>
 __global__ void __launch_bounds__((GateShape<W, C>::kWarps * 32), (GateShape<W, C>::kCtas))
     gate_kernel(const __grid_constant__ GateParams p, int32_t* __restrict__ ids, float* __restrict__ probs,
