@@ -4,8 +4,8 @@
 // Two launches: clip_norm_kernel reads every gradient and leaves one partial
 // result a CTA, clip_scale_kernel adds these up in every CTA, each for itself
 // (a few hundred values, one warp), and scales. Both walk the same items, 16 KB
-// of one tensor each, the second in the opposite order: what the first read
-// last is still in L2. The tensors' table travels in the kernels' parameters.
+// of one tensor each in short runs, the second in the opposite order: what the
+// first read last is still in L2. The tensors' table travels in the kernels' parameters.
 // Up to 16 items (256 KB) are one launch of one cluster, clip_small_kernel,
 // which keeps them in registers between the norm and the scaling.
 //
@@ -14,10 +14,12 @@
 // precision runs at 1/64 of float's rate here, so the long sums are kept as
 // pairs of floats (a sum and what its roundings lost).
 //
-// 5.6 GB in float: 2.62 ms for its three passes over HBM (16.9 GB: 6.45 TB/s;
-// read once and written once it would be 1.66 ms). 50 MB: 25 us on the GPU. 300
-// packed bf16 tensors, 100 MB: 62 us. 45 thousand elements: 5.5 us, one launch.
+// 5.6 GB in float: 2.60 ms for its three passes over HBM (16.9 GB: 6.5 TB/s;
+// read once and written once it would be 1.66 ms). 50 MB: 24 us on the GPU. 300
+// packed bf16 tensors, 100 MB: 59 us. 45 thousand elements: 4.9 us, one launch.
 // One cooperative launch for both passes was slower: 28 us and 3.0 ms.
+#include <type_traits>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -121,22 +123,56 @@ struct Item {
   int words, head, tail;     // tail: elements after the words
   int f32;
 };
-template <int N>
-__device__ __forceinline__ Item item_at(const ClipTable<N>& t, int c) {
-  const int i = clip_find(t, c);
-  Item it;
-  it.f32 = t.type[i] == MOE_TYPE_F32;
-  it.src = static_cast<const char*>(t.src[i]);
-  it.dst = static_cast<char*>(t.dst[i]);
-  const int shift = it.f32 ? 2 : 1;
-  const int64_t numel = t.numel[i], head = head_of(it.src, shift, numel);
-  const int k = c - t.item0[i];
-  const int64_t lo = static_cast<int64_t>(k) * kItemBytes, left = ((numel - head) << shift) - lo;
-  it.body = (head << shift) + lo;
-  it.words = static_cast<int>((left < kItemBytes ? left : kItemBytes) >> 4);
-  it.head = k == 0 ? static_cast<int>(head) : 0;
-  it.tail = left < kItemBytes ? static_cast<int>(left & 15) >> shift : 0;
-  return it;
+// The tensor of a run of items: looked up once, then followed to its neighbours.
+struct Tensor {
+  const char* src;
+  char* dst;
+  int64_t bytes;             // after the head
+  int item0, item1, i;       // its items; its place in the table
+  int head, f32;
+  template <int N>
+  __device__ __forceinline__ void load(const ClipTable<N>& t, int at) {
+    i = at;
+    src = static_cast<const char*>(t.src[i]);
+    dst = static_cast<char*>(t.dst[i]);
+    f32 = t.type[i] == MOE_TYPE_F32;
+    const int shift = f32 ? 2 : 1;
+    head = static_cast<int>(head_of(src, shift, t.numel[i]));
+    bytes = (t.numel[i] - head) << shift;
+    item0 = t.item0[i];
+    item1 = t.item0[i + 1];
+  }
+  template <int N>
+  __device__ __forceinline__ Item item(const ClipTable<N>& t, int c) {
+    if (c >= item1) load(t, i + 1);
+    if (c < item0) load(t, i - 1);
+    Item it;
+    it.src = src;
+    it.dst = dst;
+    it.f32 = f32;
+    const int shift = f32 ? 2 : 1;
+    const int64_t lo = static_cast<int64_t>(c - item0) * kItemBytes, left = bytes - lo;
+    it.body = (head << shift) + lo;
+    it.words = static_cast<int>((left < kItemBytes ? left : kItemBytes) >> 4);
+    it.head = c == item0 ? head : 0;
+    it.tail = left < kItemBytes ? static_cast<int>(left & 15) >> shift : 0;
+    return it;
+  }
+};
+// Items go to the CTAs in waves of kRun for each: a run of neighbours, which
+// share a tensor for the most part, while the CTAs stay close together (a search
+// for every item: 1.6 GB in 100 bf16 tensors 848 us against 747; one run a CTA:
+// 5.6 GB 2.65 against 2.60 ms). The last wave's are as long as one another or one
+// longer.
+constexpr int kRun = 8;
+struct Run {
+  int c0, c1;
+};
+__device__ __forceinline__ Run run_of(int items, int64_t base) {
+  const int64_t wave = static_cast<int64_t>(gridDim.x) * kRun;
+  const int64_t n = items - base < wave ? items - base : wave;
+  return Run{static_cast<int>(base + n * blockIdx.x / gridDim.x),
+             static_cast<int>(base + n * (blockIdx.x + 1) / gridDim.x)};
 }
 
 __device__ __forceinline__ float element(const char* p, int f32, int64_t at) {
@@ -144,15 +180,14 @@ __device__ __forceinline__ float element(const char* p, int f32, int64_t at) {
              : __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p)[at]);
 }
 
-template <typename F>
-__device__ __forceinline__ void each(const uint4& q, int f32, F&& f) {
+template <bool kF32, typename F>
+__device__ __forceinline__ void each(const uint4& q, F&& f) {
   const unsigned w[4] = {q.x, q.y, q.z, q.w};
-  if (f32) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f(__uint_as_float(w[i]));
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 4; ++i) {
+    if (kF32) {
+      f(__uint_as_float(w[i]));
+    } else {
       f(__uint_as_float(w[i] << 16));
       f(__uint_as_float(w[i] & 0xffff0000u));
     }
@@ -163,19 +198,25 @@ __device__ __forceinline__ void each(const uint4& q, int f32, F&& f) {
 template <bool kInf>
 __device__ __forceinline__ void take_item(const Item& it, const Words& q, Sum* sum, unsigned* big) {
   float part[4] = {};
-  int k = 0;
-  auto take = [&](float g) {
+  auto take = [&](float g, int k) {
     if (kInf)
       *big = max_bits(*big, g);
     else
-      part[k & 3] = fmaf(g, g, part[k & 3]);
-    ++k;
+      part[k] = fmaf(g, g, part[k]);
   };
+  auto take_words = [&](auto f32) {
+    int k = 0;
 #pragma unroll
-  for (int u = 0; u < kLoads; ++u) each(q.w[u], it.f32, take);
-  if (threadIdx.x < it.head) take(element(it.src, it.f32, threadIdx.x));
+    for (int u = 0; u < kLoads; ++u)
+      each<decltype(f32)::value>(q.w[u], [&](float g) { take(g, k++ & 3); });
+  };
+  if (it.f32)
+    take_words(std::true_type());
+  else
+    take_words(std::false_type());
+  if (threadIdx.x < it.head) take(element(it.src, it.f32, threadIdx.x), 0);
   if (threadIdx.x < it.tail)
-    take(element(it.src + it.body + it.words * 16, it.f32, threadIdx.x));
+    take(element(it.src + it.body + it.words * 16, it.f32, threadIdx.x), 1);
   if (!kInf) sum->add((part[0] + part[1]) + (part[2] + part[3]));
 }
 
@@ -213,9 +254,16 @@ __global__ void __launch_bounds__(kClipThreads, kClipCtas)
   Sum sum = {0.0f, 0.0f};
   unsigned big = 0u;
   const int items = t.item0[t.n];
-  for (int c = blockIdx.x; c < items; c += gridDim.x) {
-    const Item it = item_at(t, c);
-    take_item<kInf>(it, load_words(it.src + it.body, it.words), &sum, &big);
+  const int64_t wave = static_cast<int64_t>(gridDim.x) * kRun;
+  for (int64_t base = 0; base < items; base += wave) {
+    const Run r = run_of(items, base);
+    if (r.c0 == r.c1) break;
+    Tensor tensor;
+    tensor.load(t, clip_find(t, r.c0));
+    for (int c = r.c0; c < r.c1; ++c) {
+      const Item it = tensor.item(t, c);
+      take_item<kInf>(it, load_words(it.src + it.body, it.words), &sum, &big);
+    }
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const double v = cta_result<kInf>(sum, big, sh);
@@ -276,14 +324,17 @@ __device__ __forceinline__ float clip_coef(const ClipHow& h, bool write) {
 }
 
 // An item times coef, to its tensor's destination.
+template <bool kF32>
 __device__ __forceinline__ void scale_item(const Item& it, const Words& q, float coef) {
+  using E = std::conditional_t<kF32, float, __nv_bfloat16>;
+  E* dst = reinterpret_cast<E*>(it.dst);
   auto put = [&](int64_t at, float g) {
-    if (it.f32)
-      reinterpret_cast<float*>(it.dst)[at] = g * coef;
+    if constexpr (kF32)
+      dst[at] = g * coef;
     else
-      reinterpret_cast<__nv_bfloat16*>(it.dst)[at] = __float2bfloat16_rn(g * coef);
+      dst[at] = __float2bfloat16_rn(g * coef);
   };
-  const int shift = it.f32 ? 2 : 1;
+  constexpr int kShift = kF32 ? 2 : 1;
   const bool alike =
       ((reinterpret_cast<uintptr_t>(it.dst) ^ reinterpret_cast<uintptr_t>(it.src)) & 15) == 0;
 #pragma unroll
@@ -293,9 +344,9 @@ __device__ __forceinline__ void scale_item(const Item& it, const Words& q, float
     if (alike) {
       float g[8];
       int k = 0;
-      each(q.w[u], it.f32, [&](float x) { g[k++] = x * coef; });
+      each<kF32>(q.w[u], [&](float x) { g[k++] = x * coef; });
       uint4 w;
-      if (it.f32)
+      if (kF32)
         w = make_uint4(__float_as_uint(g[0]), __float_as_uint(g[1]), __float_as_uint(g[2]),
                        __float_as_uint(g[3]));
       else
@@ -303,15 +354,21 @@ __device__ __forceinline__ void scale_item(const Item& it, const Words& q, float
                        pack_bf16x2(g[6], g[7]));
       *reinterpret_cast<uint4*>(it.dst + at) = w;
     } else {
-      int64_t e = at >> shift;                     // another alignment: element by element
-      each(q.w[u], it.f32, [&](float x) { put(e++, x); });
+      int64_t e = at >> kShift;                    // another alignment: element by element
+      each<kF32>(q.w[u], [&](float x) { put(e++, x); });
     }
   }
-  if (threadIdx.x < it.head) put(threadIdx.x, element(it.src, it.f32, threadIdx.x));
+  if (threadIdx.x < it.head) put(threadIdx.x, element(it.src, kF32, threadIdx.x));
   if (threadIdx.x < it.tail) {
-    const int64_t at = ((it.body + it.words * 16) >> shift) + threadIdx.x;
-    put(at, element(it.src, it.f32, at));
+    const int64_t at = ((it.body + it.words * 16) >> kShift) + threadIdx.x;
+    put(at, element(it.src, kF32, at));
   }
+}
+__device__ __forceinline__ void scale_item(const Item& it, const Words& q, float coef) {
+  if (it.f32)
+    scale_item<true>(it, q, coef);
+  else
+    scale_item<false>(it, q, coef);
 }
 
 template <int N>
@@ -321,9 +378,16 @@ __global__ void __launch_bounds__(kClipThreads, kClipCtas)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const float coef = clip_coef(h, blockIdx.x == 0);
   if (h.in_place && coef == 1.0f) return;
-  for (int c = items - 1 - static_cast<int>(blockIdx.x); c >= 0; c -= gridDim.x) {
-    const Item it = item_at(t, c);
-    scale_item(it, load_words(it.src + it.body, it.words), coef);
+  const int64_t wave = static_cast<int64_t>(gridDim.x) * kRun;
+  for (int64_t base = (items - 1) / wave * wave; base >= 0 && items > 0; base -= wave) {
+    const Run r = run_of(items, base);
+    if (r.c0 == r.c1) continue;
+    Tensor tensor;
+    tensor.load(t, clip_find(t, r.c1 - 1));
+    for (int c = r.c1 - 1; c >= r.c0; --c) {
+      const Item it = tensor.item(t, c);
+      scale_item(it, load_words(it.src + it.body, it.words), coef);
+    }
   }
 }
 
@@ -344,7 +408,11 @@ __global__ void __launch_bounds__(kClipThreads, 1)
   for (int i = 0; i < kSmallItems; ++i) {
     const int c = blockIdx.x + i * gridDim.x;
     it[i] = Item{};
-    if (c < items) it[i] = item_at(t, c);
+    if (c < items) {
+      Tensor tensor;
+      tensor.load(t, clip_find(t, c));
+      it[i] = tensor.item(t, c);
+    }
     q[i] = load_words(it[i].src + it[i].body, it[i].words);
   }
 #pragma unroll
