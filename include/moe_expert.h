@@ -671,8 +671,10 @@ moe_status moe_norm_residual(const void* x, const void* y, const void* w_post, c
  *          when accumulate_dw
  *  workspace >= moe_norm_residual_backward_workspace_size(T, H, gate_rows)
  *          bytes, 16-byte aligned
- * Same H as moe_norm_residual; rows with H % 8 == 0 and H <= 8192 are read
- * once. T = 0 writes zero weight gradients (or leaves them when accumulating).
+ * Same H as moe_norm_residual; rows with H % 8 == 0 and H <= 8192 (6656 with a
+ * float stream and a gate row for each token) are read once, others up to four
+ * times. A wait inside the kernels that hits its limit reports MOE_ERR_TIMEOUT
+ * (moe_get_error), here and in the forward. T = 0 writes zero weight gradients (or leaves them when accumulating).
  * ------------------------------------------------------------------------ */
 size_t moe_norm_residual_backward_workspace_size(int64_t T, int H, int64_t gate_rows);
 moe_status moe_norm_residual_backward(const void* d_out, const void* d_n, const void* out,

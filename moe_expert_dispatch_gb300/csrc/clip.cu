@@ -14,7 +14,7 @@
 // precision runs at 1/64 of float's rate here, so the long sums are kept as
 // pairs of floats (a sum and what its roundings lost).
 //
-// 5.6 GB in float: 2.50 ms for its three passes over HBM (16.9 GB: 6.75 TB/s;
+// 5.6 GB in float: 2.48 to 2.50 ms for its three passes over HBM (16.9 GB: 6.8 TB/s;
 // read once and written once it would be 1.66 ms). 50 MB: 21 us on the GPU. 300
 // packed bf16 tensors, 100 MB: 51 us. 45 thousand elements: 5 us, one launch.
 // One cooperative launch for both passes was slower: 28 us and 3.0 ms.
