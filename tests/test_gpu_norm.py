@@ -178,6 +178,25 @@ def test_norm_gate_row_for_each_token(T, W, stream, weights):
     _near(one["dy"], want["dy"], np.abs(want["dy"]), 24, "dy")
 
 
+@pytest.mark.parametrize("T,W,rows", [(2000, 136, 1000), (2001, 512, 667), (5000, 512, 2500),
+                                      (1212, 333, 404), (999, 2048, 27)])
+def test_norm_gate_rows_accumulate_and_repeat(T, W, rows):
+    # rows inside strips and across them are each added to once, in the same order every time
+    v, d_out, d_n = _inputs(T, W, "bf16", "bf16", True, rows, True, seed=6)
+    d = {key: dev(t) for key, t in v.items()}
+    f = m.moe_norm_residual(**d)
+    rest = dict(y=d["y"], w_post=d["w_post"], gate=d["gate"], w_next=d["w_next"],
+                rstd_y=f["rstd_y"], rstd_out=f["rstd_out"])
+    one = m.moe_norm_residual_backward(dev(d_out), dev(d_n), f["out"], **rest)
+    sums = {key: torch.full_like(one[key], 2.0) for key in ("dw_post", "dgate", "dw_next")}
+    two = m.moe_norm_residual_backward(dev(d_out), dev(d_n), f["out"], **rest,
+                                       accumulate_dw=True, **sums)
+    for key in ("dx", "dy"):
+        assert torch.equal(two[key], one[key]), key
+    for key in sums:
+        assert torch.equal(two[key], one[key] + 2.0), key
+
+
 @pytest.mark.parametrize("W", [36, 1020, 1021, 1028, 8200, 16388, 20001])
 @pytest.mark.parametrize("rows", [0, 1, 6, 30])
 def test_norm_lengths_that_the_ring_does_not_take(W, rows):
