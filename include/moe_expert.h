@@ -705,8 +705,10 @@ moe_status moe_norm_residual_backward(const void* d_out, const void* d_n, const 
  *  workspace >= moe_clip_grad_norm_workspace_size() bytes, 16-byte aligned;
  *           every call overwrites what it uses
  * n_tensors <= 1048576, numels[i] <= 2^40. Squares are summed in float over
- * runs of at most 32 and to twice its precision beyond: elements between 1e-18
- * and 1e18 in magnitude count in full.
+ * runs of at most 34, in chains of at most nine that two more additions join,
+ * and to twice float's precision and in double's range beyond: elements between
+ * 1e-18 and 1e18 in magnitude count in full, however many there are, and norm
+ * is off by at most seven half steps of float (7 * 2^-24 of it).
  * No tensors, or only empty ones: norm = 0, coef = min(1, max_norm / eps).
  * ------------------------------------------------------------------------ */
 size_t moe_clip_grad_norm_workspace_size(void);

@@ -12,7 +12,8 @@
 // Bound by HBM: a gradient is read twice and written once (12 bytes an element
 // in float), the second read from L2 as far as the 129 MB hold. Double
 // precision runs at 1/64 of float's rate here, so the long sums are kept as
-// pairs of floats (a sum and what its roundings lost).
+// pairs of floats (a sum and what its roundings lost), and only sums that would
+// leave float's range go on in double.
 //
 // 5.6 GB in float: 2.48 to 2.50 ms for its three passes over HBM (16.9 GB: 6.8 TB/s;
 // read once and written once it would be 1.66 ms). 50 MB: 21 us on the GPU. 300
@@ -70,16 +71,27 @@ __host__ __device__ __forceinline__ int64_t items_of(const void* p, int shift, i
   return body > kItemBytes ? (body + kItemBytes - 1) / kItemBytes : 1;
 }
 
-// A sum of floats and what its roundings lost. An infinite sum stays one.
+// A sum of squares: a float, what its roundings lost (Knuth's two-sum), and in
+// double what would leave float's range, which no usual gradient comes near: a
+// share of an item adds less than kFar to it, so that s stays finite unless a
+// square is not. An infinite sum stays one, a NaN too.
+constexpr float kFar = 1e38f;
 struct Sum {
   float s, lost;
+  double far;
   __device__ __forceinline__ void add(float x) {
     const float t = s + x, b = t - s;
     lost += (s - (t - b)) + (x - b);
     s = t;
   }
+  __device__ __forceinline__ void settle() {
+    if (!(s > kFar)) return;
+    far += s;
+    if (isinf(s)) lost = 0.0f;
+    s = 0.0f;
+  }
   __device__ __forceinline__ double value() const {
-    return isfinite(s) ? static_cast<double>(s) + lost : static_cast<double>(s);
+    return (isfinite(s) ? static_cast<double>(s) + lost : static_cast<double>(s)) + far;
   }
 };
 
@@ -210,24 +222,36 @@ __device__ __forceinline__ void take_item(const Item& it, const Words& q, Sum* s
   if (threadIdx.x < it.head) take(element(it.src, it.f32, threadIdx.x), 0);
   if (threadIdx.x < it.tail)
     take(element(it.src + it.body + it.words * 16, it.f32, threadIdx.x), 1);
-  if (!kInf) sum->add((part[0] + part[1]) + (part[2] + part[3]));
+  if (!kInf) {
+    sum->add((part[0] + part[1]) + (part[2] + part[3]));
+    sum->settle();
+  }
 }
 
 // The CTA's result from its threads', in thread 0; sh: one value a warp.
 template <bool kInf>
 __device__ __forceinline__ double cta_result(Sum sum, unsigned big, double* sh) {
+  double all = 0.0;
+  if (kInf) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    if (kInf) {
-      big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
-    } else {
+    for (int o = 16; o > 0; o >>= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
+    all = static_cast<double>(big);
+  } else if (__any_sync(0xffffffffu, sum.s > kFar / 32 || sum.far != 0.0)) {
+    // 32 lanes together may leave float's range
+    all = sum.value();
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+  } else {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
       const float s = __shfl_xor_sync(0xffffffffu, sum.s, o);
       const float l = __shfl_xor_sync(0xffffffffu, sum.lost, o);
       sum.add(s);
       sum.lost += l;
     }
+    all = sum.value();
   }
-  if (lane_id() == 0) sh[threadIdx.x >> 5] = kInf ? static_cast<double>(big) : sum.value();
+  if (lane_id() == 0) sh[threadIdx.x >> 5] = all;
   __syncthreads();
   double v = 0.0;
   if (threadIdx.x == 0)
@@ -244,7 +268,7 @@ __global__ void __launch_bounds__(kClipThreads, kClipCtas)
     clip_norm_kernel(const __grid_constant__ ClipTable<N> t, int first,
                      double* __restrict__ partial) {
   __shared__ double sh[kClipThreads / 32];
-  Sum sum = {0.0f, 0.0f};
+  Sum sum = {0.0f, 0.0f, 0.0};
   unsigned big = 0u;
   const int items = t.item0[t.n];
   const int64_t wave = static_cast<int64_t>(gridDim.x) * kRun;
@@ -395,7 +419,7 @@ __global__ void __launch_bounds__(kClipThreads, 1)
   __shared__ double mine;
   __shared__ float sh_coef;
   const int items = t.item0[t.n];
-  Sum sum = {0.0f, 0.0f};
+  Sum sum = {0.0f, 0.0f, 0.0};
   unsigned big = 0u;
   Item it[kSmallItems];
   Words q[kSmallItems];

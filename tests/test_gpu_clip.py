@@ -181,3 +181,56 @@ def test_clip_refusals():
     with pytest.raises(m.MoeError) as e:
         m.moe_clip_grad_norm([g], 1.0, eps=-1.0)
     assert e.value.status == 1
+
+
+# A thread's share of an item: four chains of nine squares at most, added up by two more
+# additions, and to twice float's precision from there: 11 half steps of the sum and one to
+# round it, half of that in the root, and the root's own.
+ROOT = 7 * H32
+
+
+@pytest.mark.parametrize("sizes", [[1000], [65536], [1 << 20, 12345], [50_000_011]])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_clip_norm_within_the_roundings_of_a_share(sizes, dtype):
+    grads = _grads(sizes, dtype)
+    want = math.sqrt(math.fsum(float(g.double().square().sum()) for g in grads))
+    assert abs(m.moe_grad_norm(grads).item() - want) <= ROOT * want
+
+
+@pytest.mark.parametrize("n", [4096, 8192, 65536, 131072, 60_000_011])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_clip_counts_the_ends_of_its_range_in_full(n, dtype):
+    # one item, one cluster's items, two launches; every element as large or as small as stated
+    for size in (1e18, 1e-18):
+        g = torch.full((n,), size, dtype=dtype, device="cuda")
+        value = g[0].double().item()
+        out = torch.empty_like(g)
+        norm, coef = m.moe_clip_grad_norm([g], value, out=[out], eps=0.0)
+        assert abs(norm.item() / (value * math.sqrt(n)) - 1) <= ROOT
+        assert abs(coef.item() * math.sqrt(n) - 1) <= ROOT + H32
+        half = BF if dtype == torch.bfloat16 else 0.0
+        ends = out[[0, n // 2, n - 1]].double() * (math.sqrt(n) / value)
+        assert torch.all((ends - 1).abs() <= ROOT + 2 * H32 + half)
+        assert torch.all(out == out[0])
+
+
+def test_clip_mixes_small_gradients_with_the_largest():
+    # the sum leaves float's range and comes back to what is small beside it
+    n = 40_000_000
+    large = torch.full((n,), 1e18, device="cuda")
+    usual = _grads([100_000], seed=5)[0] * 1e15
+    want = math.sqrt(n * large[0].double().item() ** 2 + float(usual.double().square().sum()))
+    for grads in ([large, usual], [usual, large], [usual[:1000], large, usual[1000:]]):
+        assert abs(m.moe_grad_norm(grads).item() - want) <= ROOT * want
+
+
+@pytest.mark.parametrize("n", [8192, 60_000_011])
+def test_clip_infinities_and_nan_among_the_largest(n):
+    for at in (0, n // 2, n - 1):
+        g = torch.full((n,), 1e18, device="cuda")
+        g[at] = math.inf
+        norm, coef = m.moe_clip_grad_norm([g], 1.0, out=[torch.empty_like(g)])
+        assert norm.item() == math.inf and coef.item() == 0.0
+        g[n // 3] = math.nan
+        norm, coef = m.moe_clip_grad_norm([g], 1.0, out=[torch.empty_like(g)])
+        assert math.isnan(norm.item()) and math.isnan(coef.item())
