@@ -92,6 +92,26 @@ __device__ __forceinline__ bool apart(float x, float y, float abs_off, float rel
   return y == -INFINITY ? x != -INFINITY : x - y > abs_off + (fabsf(x) + fabsf(y)) * rel_off;
 }
 
+// Half of a group's score, which stays in float's range, from the group's best
+// two values (the second -inf: one counts), and half of what these measure: a
+// sum of opposite signs is as far off as they are, not as it is itself.
+struct GroupScore {
+  float half, size;
+};
+__device__ __forceinline__ GroupScore group_score(float best, float next) {
+  GroupScore r = {0.5f * best, best == -INFINITY ? 0.0f : 0.5f * fabsf(best)};
+  if (next != -INFINITY) {
+    r.half = fmaf(0.5f, next, r.half);
+    r.size = fmaf(0.5f, fabsf(next), r.size);
+  }
+  return r;
+}
+// How far half of a score may be off: both values by off and 2^-24 of
+// themselves, their sum by 2^-24 of it, and what compares it by as much again.
+__device__ __forceinline__ float group_off(float size, float off) {
+  return fmaf(size, 0x1p-22f, off);
+}
+
 // Batcher's odd-even merge sort, descending, over registers: a[kLo .. kLo + kN).
 template <int kLo, int kN, int kStep, int N>
 __device__ __forceinline__ void merge_desc(unsigned (&a)[N]) {
@@ -273,17 +293,18 @@ __device__ __noinline__ unsigned groups_in_double(const GateParams& p, const L* 
       a = fmaxf(a, x);
     }
   const bool two = p.group_topk == 2 && c != -INFINITY;
-  const float g = two ? a + c : a;
+  const GroupScore mine_of = group_score(a, two ? c : -INFINITY);
+  const float g = mine_of.half, may_be = group_off(mine_of.size, off);
   int rank = 0;
   for (int j = 0; j < p.n_group; ++j) {
     const float o = __shfl_sync(kAll, g, j);
     rank += o > g || (o == g && j < lane);
   }
   const bool in = lane < p.n_group && rank < p.topk_group;
-  const float low = -seg_max<32>(in ? -g : -INFINITY);
-  const float high = seg_max<32>(in || lane >= p.n_group ? -INFINITY : g);
-  const bool open = lane < p.n_group && !(in ? apart(g, high, 4.0f * off, 0x1p-22f)
-                                             : apart(low, g, 4.0f * off, 0x1p-22f));
+  // certain: above whatever those outside may be, or below whatever those inside may be
+  const float low = -seg_max<32>(in ? may_be - g : -INFINITY);
+  const float high = seg_max<32>(in || lane >= p.n_group ? -INFINITY : g + may_be);
+  const bool open = lane < p.n_group && !(in ? g - may_be > high : g + may_be < low);
   const unsigned opens = __ballot_sync(kAll, open);
   unsigned kept = __ballot_sync(kAll, in && !open);
   const float least = two ? c : a;                 // what a group's best may be level with
@@ -514,7 +535,7 @@ struct GateShape {
 // score in float is off by at most 2^-21 of the largest score (ex2.approx
 // and rcp.approx within 2^-22 and 2^-23, and s (1 - s) <= 1/4), a choice
 // value by 2^-24 of itself more, and its key by the C - 1 units that its low
-// bits hold. Only tokens with two neighbours in the order closer than that
+// bits hold; a group's score as group_off says. Only tokens with two neighbours in the order closer than that
 // (some 0.3% with scores of 256 experts) are looked at again: for ties and
 // most others in the order of the candidates alone (reorder). bf16
 // logits that rank by themselves leave room for the whole index in the key,
@@ -652,7 +673,8 @@ __global__ void __launch_bounds__((GateShape<W, C>::kWarps * 32), (GateShape<W, 
           c = fmaxf(fminf(a, oa), fmaxf(c, oc));
           a = fmaxf(a, oa);
         }
-        const float g = p.group_topk == 2 && c != -INFINITY ? a + c : a;
+        const GroupScore score = group_score(a, p.group_topk == 2 ? c : -INFINITY);
+        const float g = score.half;
         // topk_group rounds of the largest; groups of one score go together,
         // and are then too close to be certain (masked ones go by their index)
         unsigned gk = g == -INFINITY ? W - (sub & ~(lanes - 1)) : key_of(g + 0.0f);
@@ -664,9 +686,10 @@ __global__ void __launch_bounds__((GateShape<W, C>::kWarps * 32), (GateShape<W, 
         }
         bool kept = gk == 0u;
         const int of = __popc(__ballot_sync(kAll, kept) & seg);
+        const float size_most = __uint_as_float(seg_max_key<W>(__float_as_uint(score.size)));
         open_set = of != p.topk_group * lanes ||
                    (high >= kLeastKey &&
-                    !apart(float_of(low), float_of(high), 4.0f * off, 0x1p-22f));
+                    !(float_of(low) - float_of(high) > 2.0f * group_off(size_most, off)));
         if (const unsigned opens = __ballot_sync(kAll, open_set)) {
           const unsigned right = settle_groups(opens);
           if (right) {
@@ -683,7 +706,7 @@ __global__ void __launch_bounds__((GateShape<W, C>::kWarps * 32), (GateShape<W, 
         float* row_v = reinterpret_cast<float*>(sh_v + static_cast<size_t>(w) * p.E);
         float* score = sh_group[w][tok];
         unsigned kept = 0u;
-        float low = INFINITY, high = -INFINITY;
+        float low = INFINITY, high = -INFINITY, size_most = 0.0f;
         for (int q = 0; q < G::kTokens; ++q) {                 // the warp's tokens in turn
           __syncwarp();
           if (tok == q) {
@@ -692,6 +715,7 @@ __global__ void __launch_bounds__((GateShape<W, C>::kWarps * 32), (GateShape<W, 
               if (e0 + i < p.E) row_v[e0 + i] = v[i];
           }
           __syncwarp();
+          unsigned most = 0u;
           if (lane < p.n_group) {
             float a = -INFINITY, c = -INFINITY;
             for (int i = 0, at = lane % size; i < size; ++i, at = at + 1 == size ? 0 : at + 1) {
@@ -699,8 +723,12 @@ __global__ void __launch_bounds__((GateShape<W, C>::kWarps * 32), (GateShape<W, 
               c = fmaxf(c, fminf(a, x));
               a = fmaxf(a, x);
             }
-            sh_group[w][q][lane] = p.group_topk == 2 && c != -INFINITY ? a + c : a;
+            const GroupScore r = group_score(a, p.group_topk == 2 ? c : -INFINITY);
+            sh_group[w][q][lane] = r.half;
+            most = __float_as_uint(r.size);
           }
+          most = __reduce_max_sync(kAll, most);
+          if (tok == q) size_most = __uint_as_float(most);
         }
         __syncwarp();
         for (int g = sub; g < p.n_group; g += W) {
@@ -719,7 +747,7 @@ __global__ void __launch_bounds__((GateShape<W, C>::kWarps * 32), (GateShape<W, 
         for (int o = W / 2; o > 0; o >>= 1) kept |= __shfl_xor_sync(kAll, kept, o);
         low = -seg_max<W>(-low);
         high = seg_max<W>(high);
-        open_set = high != -INFINITY && !apart(low, high, 4.0f * off, 0x1p-22f);
+        open_set = high != -INFINITY && !(low - high > 2.0f * group_off(size_most, off));
         if (const unsigned opens = __ballot_sync(kAll, open_set)) {
           const unsigned right = settle_groups(opens);
           if (right) {

@@ -310,3 +310,44 @@ def test_gate_refusals():
         m.moe_route_gate(logits.double(), 2)
     with pytest.raises(ValueError, match="shape"):
         m.moe_route_gate(logits, 2, bias=dev(torch.zeros(7)))
+
+
+def _opposite_biases(E, n_group, B):
+    """In every group +B, -B and, below these, -2 B: the two best sum to their scores alone."""
+    size = E // n_group
+    rng = np.random.default_rng(E + n_group)
+    rows = np.full((n_group, size), -2.0 * B, np.float32)
+    for row in rows:
+        first, second = rng.choice(size, 2, replace=False)
+        row[first], row[second] = B, -B
+    return torch.from_numpy(rows.reshape(-1))
+
+
+# groups that whole lanes hold, groups that lie across them, both with one and many tokens a warp
+@pytest.mark.parametrize("E,k,n_group,topk_group", [(64, 6, 4, 2), (256, 8, 8, 4), (256, 8, 16, 3),
+                                                    (512, 8, 32, 9), (8, 2, 4, 2), (48, 6, 8, 3),
+                                                    (64, 6, 32, 9), (72, 5, 12, 4)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_gate_groups_whose_two_best_cancel(E, k, n_group, topk_group, score):
+    for i, B in enumerate((100.0, 1000.0, 10000.0)):
+        bias = _opposite_biases(E, n_group, B)
+        for sd in (1e-4, 1e-2):
+            logits = 0.3 + _logits(300, E, sd=sd, seed=i)
+            _check(logits, k, bias=bias, score=score, n_group=n_group, topk_group=topk_group,
+                   group_topk=2, backward=False)
+
+
+@pytest.mark.parametrize("E", [8, 64, 256])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_gate_groups_whose_sum_leaves_the_range_of_float(E, score):
+    # a sum of two beyond float's range is not a masked group's, nor all such sums alike
+    size = E // 4
+    for pairs in (((-math.inf, -math.inf), (-3e38, -3e38), (-2e38, -2e38), (-2.5e38, -2.5e38)),
+                  ((-math.inf, -math.inf), (-3e38, -3e38), (-math.inf, -math.inf), (-2e38, -3e38)),
+                  ((3e38, 3e38), (3.2e38, 2.9e38), (3.3e38, 2e38), (2e38, 1e38)),
+                  ((3e38, -3e38), (2e38, -2e38), (0.1, 0.1), (-3e38, -1e38))):
+        bias = torch.full((4, size), -math.inf)
+        bias[:, :2] = torch.tensor(pairs)
+        for topk_group in (1, 2, 3):
+            _check(_logits(70, E), 2, bias=bias.reshape(-1), score=score, n_group=4,
+                   topk_group=topk_group, group_topk=2, backward=False)
