@@ -421,6 +421,7 @@ __device__ __forceinline__ void slot_weights(const GateParams& p, const float (&
     return;
   }
   float sum = 0.0f;
+  bool low = false;
   if (p.score == MOE_SCORE_SOFTMAX) {
     float m = -INFINITY;
 #pragma unroll
@@ -443,25 +444,26 @@ __device__ __forceinline__ void slot_weights(const GateParams& p, const float (&
       sum += u[i];
     }
     sum = seg_sum<W>(sum);
-    // scores near the end of float's range (masked slots alone are not): their
-    // ratios in double
+    // a token whose scores lie near the end of float's range (masked slots alone
+    // do not): their ratios in double, and no other token's of the warp
     float m = -INFINITY;
 #pragma unroll
     for (int i = 0; i < S; ++i) m = fmaxf(m, l[i]);
     m = __any_sync(kAll, sum < 1e-30f) ? seg_max<W>(m) : 0.0f;
-    if (__any_sync(kAll, sum < 1e-30f && m > -INFINITY)) {
+    low = sum < 1e-30f && m > -INFINITY;
+    if (__any_sync(kAll, low)) {
       double total = 0.0;
 #pragma unroll
-      for (int i = 0; i < S; ++i) total += sigmoid_in_double(l[i]);
+      for (int i = 0; i < S; ++i) total += low ? sigmoid_in_double(l[i]) : 0.0;
       total = seg_sum<W>(total);
 #pragma unroll
-      for (int i = 0; i < S; ++i) u[i] = share_in_double(l[i], total);
-      return;
+      for (int i = 0; i < S; ++i)
+        if (low) u[i] = share_in_double(l[i], total);
     }
   }
 #pragma unroll
   for (int i = 0; i < S; ++i)
-    if (W * i < p.k) u[i] = sum > 0.0f ? __fdividef(u[i], sum) : 0.0f;
+    if (W * i < p.k && !low) u[i] = sum > 0.0f ? __fdividef(u[i], sum) : 0.0f;
 }
 
 // The softmax's largest logit (0 for a row of -inf) and the reciprocal of

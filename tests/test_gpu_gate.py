@@ -351,3 +351,24 @@ def test_gate_groups_whose_sum_leaves_the_range_of_float(E, score):
         for topk_group in (1, 2, 3):
             _check(_logits(70, E), 2, bias=bias.reshape(-1), score=score, n_group=4,
                    topk_group=topk_group, group_topk=2, backward=False)
+
+
+@pytest.mark.parametrize("E,k", [(8, 4), (24, 6), (64, 6), (100, 8), (256, 8)])
+@pytest.mark.parametrize("renormalise", [True, False])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_gate_token_alone_and_among_others(E, k, renormalise, score):
+    # rows masked with the type's lowest value, and rows of scores below float's range, beside
+    # rows of any other kind: the others' bits do not depend on their neighbours
+    logits = _logits(67, E)
+    logits[5::7] = torch.finfo(torch.float32).min
+    logits[9::11] -= 120.0
+    logits, dp = dev(logits), dev(_logits(67, k, seed=1))
+    how = dict(score=score, renormalise=renormalise, scale=2.5)
+    ids, w, _, _ = m.moe_route_gate(logits, k, **how)
+    grad = m.moe_route_gate_backward(dp, logits, ids, **how)
+    for t in range(67):
+        alone = m.moe_route_gate(logits[t:t + 1].clone(), k, **how)
+        assert torch.equal(alone[0][0], ids[t]) and torch.equal(alone[1][0], w[t]), t
+        one = m.moe_route_gate_backward(dp[t:t + 1].clone(), logits[t:t + 1].clone(), alone[0],
+                                        **how)
+        assert torch.equal(one[0], grad[t]), t
