@@ -702,25 +702,35 @@ int group_of(int H) {
   return H % 8 == 0 && group <= kThreads ? group : 0;
 }
 
-template <typename K>
-cudaError_t launch(K* kernel, const RingParams& p, size_t smem, cudaStream_t st) {
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(smem));
-  if (e != cudaSuccess) return e;
-  kernel<<<p.r.ctas, p.r.groups * p.r.group, smem, st>>>(p);
+// A call's shared memory follows from its rows, types and gate; the kernel's limit
+// is set once per device, to the most of any call, and never lowered: a call
+// from another thread may lie between its setting and this launch.
+template <void (*kKernel)(RingParams)>
+cudaError_t launch(const RingParams& p, size_t smem, cudaStream_t st) {
+  static bool configured[kMaxDevices] = {};
+  const int d = current_device();
+  if (d < 0 || d >= kMaxDevices) return cudaErrorInvalidDevice;
+  if (!configured[d]) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedBytes);
+    if (e != cudaSuccess) return e;
+    configured[d] = true;
+  }
+  kKernel<<<p.r.ctas, p.r.groups * p.r.group, smem, st>>>(p);
   return cudaGetLastError();
+}
+
+template <typename ST, int kGate, bool kFull, bool kAll>
+cudaError_t launch_of(const RingParams& p, bool backward, size_t smem, cudaStream_t st) {
+  return backward ? launch<norm_ring_backward_kernel<ST, kGate, kFull, kAll>>(p, smem, st)
+                  : launch<norm_ring_kernel<ST, kGate, kFull, kAll>>(p, smem, st);
 }
 
 template <typename ST, bool kFull, bool kAll>
 cudaError_t launch_of(const RingParams& p, bool backward, int gate, size_t smem, cudaStream_t st) {
-  auto* kernel =
-      backward ? (gate == kTokenGates  ? norm_ring_backward_kernel<ST, kTokenGates, kFull, kAll>
-                  : gate == kManyGates ? norm_ring_backward_kernel<ST, kManyGates, kFull, kAll>
-                                       : norm_ring_backward_kernel<ST, kOneGate, kFull, kAll>)
-               : (gate == kTokenGates  ? norm_ring_kernel<ST, kTokenGates, kFull, kAll>
-                  : gate == kManyGates ? norm_ring_kernel<ST, kManyGates, kFull, kAll>
-                                       : norm_ring_kernel<ST, kOneGate, kFull, kAll>);
-  return launch(kernel, p, smem, st);
+  return gate == kTokenGates  ? launch_of<ST, kTokenGates, kFull, kAll>(p, backward, smem, st)
+         : gate == kManyGates ? launch_of<ST, kManyGates, kFull, kAll>(p, backward, smem, st)
+                              : launch_of<ST, kOneGate, kFull, kAll>(p, backward, smem, st);
 }
 
 // Rows of a multiple of 512 with all the tensors are what layers have; any

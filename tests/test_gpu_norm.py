@@ -345,3 +345,53 @@ def test_norm_refusals():
         with pytest.raises(m.MoeError) as e:
             call()
         assert e.value.status == 1
+
+
+def test_norm_of_two_lengths_from_two_threads():
+    # rows of 512 and of 7168 share their kernels and differ in the shared memory that these
+    # launch with; the library's own calls, back to back, so that the threads' launches mix
+    import threading
+    cases, wrong = [], []
+    for W in (512, 7168):
+        v, d_out, d_n = _inputs(160, W, "bf16", "bf16", True, 1, True)
+        d = {key: dev(t) for key, t in v.items()}
+        do, dn = dev(d_out), dev(d_n)
+        f = m.moe_norm_residual(**d)
+        rest = {key: d[key] for key in ("y", "w_post", "gate", "w_next")}
+        g = m.moe_norm_residual_backward(do, dn, f["out"], **rest, rstd_y=f["rstd_y"],
+                                         rstd_out=f["rstd_out"])
+        got_f = {key: torch.zeros_like(t) for key, t in f.items()}
+        got_g = {key: torch.zeros_like(t) for key, t in g.items()}
+        need = m._lib.moe_norm_residual_backward_workspace_size(160, W, 1)
+        ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+        stream = torch.cuda.Stream()
+        at = lambda t: t.data_ptr()                # noqa: E731
+        w = (at(d["w_post"]), at(d["gate"]), 1, at(d["w_next"]))
+        there = (at(d["x"]), at(d["y"]), *w, 160, W, None, *map(at, got_f.values()),
+                 stream.cuda_stream)
+        back = (at(do), at(dn), at(f["out"]), at(d["y"]), *w, at(f["rstd_y"]), at(f["rstd_out"]),
+                160, W, None, *map(at, got_g.values()), 0, at(ws), need, stream.cuda_stream)
+        cases.append((there, back, stream, (f, got_f), (g, got_g), (d, do, dn, ws)))
+    torch.cuda.synchronize()
+    start = threading.Barrier(2)
+
+    def work(there, back):
+        torch.cuda.current_stream()                # the thread's device
+        start.wait()
+        for i in range(20000):
+            status = (m._lib.moe_norm_residual(*there), m._lib.moe_norm_residual_backward(*back))
+            if status != (0, 0):
+                wrong.append((i, status))
+                return
+
+    threads = [threading.Thread(target=work, args=c[:2]) for c in cases]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not wrong, wrong
+    for case in cases:
+        for want, got in case[3:5]:
+            for key in want:
+                assert torch.equal(want[key], got[key]), key
