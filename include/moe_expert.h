@@ -673,8 +673,12 @@ moe_status moe_norm_residual(const void* x, const void* y, const void* w_post, c
  *          bytes, 16-byte aligned
  * Same H as moe_norm_residual; rows with H % 8 == 0 and H <= 8192 (6656 with a
  * float stream and a gate row for each token) are read once, others up to four
- * times. A wait inside the kernels that hits its limit reports MOE_ERR_TIMEOUT
- * (moe_get_error), here and in the forward. T = 0 writes zero weight gradients (or leaves them when accumulating).
+ * times. A wait inside the kernels that hits its limit (2 s) reports
+ * MOE_ERR_TIMEOUT (moe_get_error), here and in the forward: the CTA waits, once
+ * more with a limit, for the copies that it has under way and starts no others;
+ * the call's outputs are then no results, and what accumulate_dw was to add to
+ * is spoilt. T = 0 writes zero weight gradients (or leaves them when
+ * accumulating).
  * ------------------------------------------------------------------------ */
 size_t moe_norm_residual_backward_workspace_size(int64_t T, int H, int64_t gate_rows);
 moe_status moe_norm_residual_backward(const void* d_out, const void* d_n, const void* out,

@@ -20,6 +20,8 @@
 // the second needs the first, come from one reduction of three sums.
 #include "norm.cuh"
 
+#include <stdlib.h>
+
 namespace moe {
 
 int* device_error_word();
@@ -42,6 +44,9 @@ struct RingParams {
   RingShape r;
   int row_bytes;
   int* err;
+#ifdef MOE_DEBUG
+  bool give_up;                            // every wait is given up
+#endif
 };
 
 // ------------------------------------------------------------------ pairs of floats
@@ -195,10 +200,16 @@ struct Walk {
   bool has[V];
 };
 
+// Waits that were given up: in the CTA, and in each group (1; 2: and its copies
+// were waited for).
+struct GaveUp {
+  int cta, group[kMaxRingGroups];
+};
+
 // kFull: every thread has all its columns.
 template <int V, bool kFull>
 __device__ __forceinline__ Walk<V> walk_of(const RingParams& p, unsigned char* ring_all,
-                                           uint64_t (*full_all)[kMaxStages], int* abort_wait) {
+                                           uint64_t (*full_all)[kMaxStages], GaveUp* gave_up) {
   Walk<V> w;
   w.g = threadIdx.x / p.r.group;
   w.tid = threadIdx.x - w.g * p.r.group;
@@ -216,8 +227,9 @@ __device__ __forceinline__ Walk<V> walk_of(const RingParams& p, unsigned char* r
   w.step = (kCols / V) * p.r.group;
 #pragma unroll
   for (int v = 0; v < V; ++v) w.has[v] = kFull || w.col0 + v * w.step < w.H;
-  if (threadIdx.x == 0) *abort_wait = 0;
+  if (threadIdx.x == 0) gave_up->cta = 0;
   if (w.tid == 0) {
+    gave_up->group[w.g] = 0;
     for (int i = 0; i < p.r.stages; ++i) mbar_init(w.full + 8 * i, 1);
     fence_mbar_init();
   }
@@ -273,16 +285,54 @@ __device__ __forceinline__ Vec<W> gate_of(const RingParams& p, const unsigned ch
   return v;
 }
 
-// Waits for a stage. No wait as long as the limit is legitimate: it is
-// reported, and the waits after it are given up at once.
+// Waits for a stage. No wait as long as the limit is legitimate: it is reported,
+// and what the thread computes from there on is no result, but it keeps to the
+// group's barriers to the last one. Its own later waits and the CTA's others
+// are given up with it, each after the few microseconds that a try_wait lasts.
 template <int V>
 __device__ __forceinline__ void wait_stage(const RingParams& p, const Walk<V>& w, int stage,
-                                           int parity, bool* gave_up, int* abort_wait) {
-  if (mbar_try_wait(w.full + 8 * stage, parity)) return;
-  if (!mbar_wait(w.full + 8 * stage, parity, *gave_up ? 0 : kDefaultWaitNs, abort_wait)) {
-    report_error(p.err, kErrTimeout);
-    *gave_up = true;
+                                           int parity, bool* gave_up, GaveUp* all) {
+  const uint32_t bar = w.full + 8 * stage;
+  volatile int *cta = &all->cta, *group = &all->group[w.g];
+#ifdef MOE_DEBUG
+  const bool unseen = p.give_up;           // whether or not the copies have come
+#else
+  const bool unseen = false;
+#endif
+  if (!unseen && mbar_try_wait(bar, parity)) return;
+  if (!unseen && mbar_wait(bar, parity, *gave_up ? 0 : kDefaultWaitNs, cta)) return;
+  report_error(p.err, kErrTimeout);
+  *cta = 1;
+  if (*group == 0) *group = 1;
+  *gave_up = true;
+}
+
+// Waits, once more with a limit, for the copies of a group that are still on their
+// way: from the row of this stage on, of which `left` are to come.
+__device__ __noinline__ void drain(uint32_t full, int stages, int left, int stage, int parity) {
+  const unsigned long long t0 = global_timer_ns();
+  for (int i = 0; i < stages && i < left; ++i) {
+    while (!mbar_try_wait(full + 8 * stage, parity))
+      if (global_timer_ns() - t0 > kDefaultWaitNs) return;
+    if (++stage == stages) {
+      stage = 0;
+      parity ^= 1;
+    }
   }
+}
+
+// Whether the group's first thread may fill a stage again, behind the barrier that
+// the group came to with that stage's row. Once a wait was given up it fills
+// none: it has waited for what was on its way, and nothing is when the CTA ends.
+template <int V>
+__device__ __forceinline__ bool may_refill(const RingParams& p, const Walk<V>& w, int left,
+                                           int stage, int parity, GaveUp* all) {
+  const int was = *static_cast<volatile int*>(&all->group[w.g]);
+  if (was == 1) {
+    drain(w.full, p.r.stages, left, stage, parity);
+    all->group[w.g] = 2;
+  }
+  return was == 0;
 }
 
 // ------------------------------------------------------------------ forward
@@ -297,8 +347,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(128) unsigned char ring_all[];
   __shared__ float4 red_all[kMaxRingGroups][4][kWarps];
   __shared__ __align__(8) uint64_t full_all[kMaxRingGroups][kMaxStages];
-  __shared__ int abort_wait;
-  const Walk<V> w = walk_of<V, kFull>(p, ring_all, full_all, &abort_wait);
+  __shared__ GaveUp gave_up_all;
+  const Walk<V> w = walk_of<V, kFull>(p, ring_all, full_all, &gave_up_all);
   const NormParams& q = p.n;
   const bool branch = kAll || q.y, post = kAll || q.w_post, next = kAll || q.w_next;
   constexpr bool kMany = kGate == kManyGates, kToken = kGate == kTokenGates;
@@ -344,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (post) times(p, w, q.w_post, 0, gw);
       times(p, w, q.gate, gate_row * w.H, gw);
     }
-    wait_stage(p, w, stage, parity, &gave_up, &abort_wait);
+    wait_stage(p, w, stage, parity, &gave_up, &gave_up_all);
     const unsigned char* row_x = w.ring + (stage * p.row_bytes + w.col0 * kSize);
     const unsigned char* row_y = w.ring + (stage * p.row_bytes + wide + w.col0 * 2);
     Vec<W> x[V], y[V];
@@ -374,7 +424,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // every thread has the row in registers: its stage takes another
     if (w.tid == 0) {
-      if (t + p.r.stages < rows) issue(w.lo + t + p.r.stages, stage);
+      if (may_refill(p, w, rows - t, stage, parity, &gave_up_all) && t + p.r.stages < rows)
+        issue(w.lo + t + p.r.stages, stage);
       if (post && p.o.rstd_y) p.o.rstd_y[w.lo + t] = ry;
     }
     s = pair(0.0f);
@@ -435,8 +486,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(128) unsigned char ring_all[];
   __shared__ float4 red_all[kMaxRingGroups][2][kWarps];
   __shared__ __align__(8) uint64_t full_all[kMaxRingGroups][kMaxStages];
-  __shared__ int abort_wait;
-  const Walk<V> w = walk_of<V, kFull>(p, ring_all, full_all, &abort_wait);
+  __shared__ GaveUp gave_up_all;
+  const Walk<V> w = walk_of<V, kFull>(p, ring_all, full_all, &gave_up_all);
   const NormParams& q = p.n;
   const bool branch = kAll || q.y, post = kAll || q.w_post, next = kAll || q.d_n,
              has_d = kAll || q.x;
@@ -515,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (post) times(p, w, q.w_post, 0, gw);
       times(p, w, q.gate, gate_row * w.H, gw);
     }
-    wait_stage(p, w, stage, parity, &gave_up, &abort_wait);
+    wait_stage(p, w, stage, parity, &gave_up, &gave_up_all);
     const unsigned char* row_wide = w.ring + (stage * p.row_bytes + w.col0 * kSize);
     const unsigned char* row_half = w.ring + (stage * p.row_bytes + w.col0 * 2);
     Vec<W> d[V];                                   // A, then D
@@ -578,7 +629,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // gate's row has been read too)
     auto refill = [&]() {
       group_barrier(w.g + 1, p.r.group);
-      if (w.tid == 0 && t + p.r.stages < rows) issue(w.lo + t + p.r.stages, stage);
+      if (w.tid == 0 && may_refill(p, w, rows - t, stage, parity, &gave_up_all) &&
+          t + p.r.stages < rows)
+        issue(w.lo + t + p.r.stages, stage);
     };
     if (!kToken) refill();
     const int64_t first_col = (w.lo + t) * w.H + w.col0;
@@ -668,6 +721,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // with a wait given up there are no sums, and perhaps a copy that never came to
+  // where they would lie
+  __syncthreads();
+  if (gave_up_all.cta) return;
   // the groups' sums, in order
   auto add_up = [&](const float* all, float* part) {
     __syncthreads();
@@ -781,7 +838,11 @@ RingShape ring_shape(int64_t T, int H, int row_bytes, bool backward, bool many) 
 
 cudaError_t launch_norm_ring(const NormParams& n, const RingShape& r, const RingOut& o,
                              bool stream_f32, bool backward, int row_bytes, cudaStream_t st) {
-  const RingParams p = {n, o, r, row_bytes, device_error_word()};
+  RingParams p = {n, o, r, row_bytes, device_error_word()};
+#ifdef MOE_DEBUG
+  // for tests of what a wait given up leaves behind
+  p.give_up = getenv("MOE_GB300_GIVE_UP_WAITS") != nullptr;
+#endif
   const size_t rings = static_cast<size_t>(r.groups) * (r.stages * row_bytes + r.tail_bytes);
   const size_t sums = backward ? static_cast<size_t>(r.groups) * n.H * sizeof(float) : 0;
   const size_t smem = rings > sums ? rings : sums;

@@ -10,6 +10,10 @@ bound all of that, of the sum of the terms' magnitudes (up to 1024 elements
 32 lanes may share a row: width / 32 + 5 terms, fewer than C). A column sum over T
 tokens adds at most T half steps. bfloat16 results add half a step, 2^-8;
 bfloat16 reads are exact."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -395,3 +399,49 @@ def test_norm_of_two_lengths_from_two_threads():
         for want, got in case[3:5]:
             for key in want:
                 assert torch.equal(want[key], got[key]), key
+
+
+# groups of one warp and of several, one group a CTA and many, every form of the gate, rows
+# whose last threads have no columns, forms without the first reduction
+LATE = [(5000, 512, True, 0), (2000, 1024, True, 20), (700, 4096, True, 700), (160, 2048, True, 1),
+        (3000, 1096, False, 0), (1500, 7168, True, 1), (1500, 2048, False, 1500)]
+
+
+def _late(T, W, post, rows):
+    """Calls that give their waits up, each followed by one that is right."""
+    for stream in ("f32", "bf16"):
+        v, d_out, d_n = _inputs(T, W, stream, "bf16", post, rows, True)
+        d, do, dn = {key: dev(t) for key, t in v.items()}, dev(d_out), dev(d_n)
+        f = m.moe_norm_residual(**d)
+        rest = dict(**{key: d[key] for key in ("y", "w_post", "gate", "w_next")},
+                    rstd_y=f["rstd_y"], rstd_out=f["rstd_out"])
+        g = m.moe_norm_residual_backward(do, dn, f["out"], **rest)
+        assert m.moe_get_error() == 0
+        for _ in range(3):
+            os.environ["MOE_GB300_GIVE_UP_WAITS"] = "1"
+            m.moe_norm_residual(**d)
+            assert m.moe_get_error() == 5
+            m.moe_norm_residual_backward(do, dn, f["out"], **rest)
+            assert m.moe_get_error() == 5
+            del os.environ["MOE_GB300_GIVE_UP_WAITS"]
+            f2 = m.moe_norm_residual(**d)
+            g2 = m.moe_norm_residual_backward(do, dn, f["out"], **rest)
+            assert m.moe_get_error() == 0
+            for a, b in ((f, f2), (g, g2)):
+                for key in a:
+                    assert a[key] is None or torch.equal(a[key], b[key]), key
+
+
+def test_norm_wait_timeout_reports_and_recovers():
+    # the library's waits last microseconds of their two seconds: the debug build gives them up
+    # where the environment says so
+    if not m.DEBUG:
+        code = "import test_gpu_norm as t; [t._late(*c) for c in t.LATE]; print('late ok')"
+        here = os.path.dirname(os.path.abspath(__file__))
+        path = os.pathsep.join([os.path.dirname(here), here])
+        r = subprocess.run([sys.executable, "-c", code], cwd=here, capture_output=True, text=True,
+                           timeout=300, env=dict(os.environ, MOE_GB300_DEBUG="1", PYTHONPATH=path))
+        assert r.returncode == 0 and "late ok" in r.stdout, r.stdout[-2000:] + r.stderr[-4000:]
+        return
+    for case in LATE:
+        _late(*case)
