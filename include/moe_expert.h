@@ -695,14 +695,16 @@ moe_status moe_norm_residual_backward(const void* d_out, const void* d_n, const 
  * by it: with norm = sqrt(sum of all g^2) (norm_kind 0) or max |g| (1),
  *   coef = min(1, max_norm / (norm + eps)),   g <- g * coef
  * A NaN among the gradients gives norm = coef = NaN, an infinity norm = inf
- * and coef = 0 (so that finite gradients become 0 and infinite ones NaN).
- * With max_norm < 0 only the norm is computed (coef = 1).
+ * and coef = 0 (so that finite gradients become 0 and infinite ones NaN; with
+ * max_norm = inf the quotient, and coef, is NaN). With max_norm < 0 only the norm
+ * is computed (coef = 1).
  *
  *  grads    HOST array of n_tensors device pointers, each aligned to its
  *           element; the arrays are read before the call returns
  *  outs     HOST array of n_tensors device pointers of the same types, or
  *           NULL: in place. In place nothing is written when coef = 1; out of
- *           place every element is. outs[i] is grads[i] or overlaps no input.
+ *           place every element is. outs[i] is grads[i] or overlaps no input,
+ *           no two outputs overlap, and so no two gradients clipped in place.
  *  numels   HOST array of element counts (>= 0; 0 allows a null pointer)
  *  types    HOST array of moe_type
  *  norm_coef float [2] device memory   out: norm, coef

@@ -905,7 +905,8 @@ def moe_norm_residual(x, y=None, w_post=None, gate=None, w_next=None, eps=1e-6,
     Without w_post y enters as it is, without gate (of [H], or [rows, H] with T
     / rows consecutive tokens to a row) it is 1, without w_next n is left out.
     Without y it is the norm alone, of x. Returns dict(out, n, rstd_y,
-    rstd_out), None where nothing was computed; out may be x itself."""
+    rstd_out), None where nothing was computed; out may be x itself. All
+    tensors of [T, H], [rows, H] and [H] start on 16 bytes."""
     if _elsewhere(stream):
         return _within(stream, moe_norm_residual, locals())
     st = _typed(x, "x")
@@ -947,7 +948,8 @@ def moe_norm_residual_backward(d_out, d_n, out, y=None, w_post=None, gate=None, 
     x where y is None); y, the weights, rstd_y, rstd_out and the scalars are the
     forward's. Returns dict(dx, dy, dw_post, dgate, dw_next), the last three in
     float32 and, with accumulate_dw, added to what the given tensors hold; None
-    where there is no such input. dx may be d_out itself."""
+    where there is no such input. dx may be d_out itself. All tensors of [T, H],
+    [rows, H] and [H] start on 16 bytes."""
     if _elsewhere(stream):
         return _within(stream, moe_norm_residual_backward, locals())
     st = _typed(out, "out")

@@ -15,10 +15,10 @@
 // pairs of floats (a sum and what its roundings lost), and only sums that would
 // leave float's range go on in double.
 //
-// 5.6 GB in float: 2.48 to 2.50 ms for its three passes over HBM (16.9 GB: 6.8 TB/s;
-// read once and written once it would be 1.66 ms). 50 MB: 21 us on the GPU. 300
-// packed bf16 tensors, 100 MB: 51 us. 45 thousand elements: 5 us, one launch.
-// One cooperative launch for both passes was slower: 28 us and 3.0 ms.
+// 5.6 GB in float: 2.47 to 2.53 ms for its three passes over HBM (16.9 GB: 6.8 TB/s;
+// read once and written once it would be 1.66 ms). 50 MB: 22 us on the GPU. 300
+// packed bf16 tensors, 100 MB: 50 to 52 us. 45 thousand elements: 5 us, one launch.
+// One cooperative launch for both passes was slower: 28 us (50 MB) and 3.0 ms.
 #include <type_traits>
 
 #include "common.cuh"
@@ -101,7 +101,7 @@ __device__ __forceinline__ unsigned max_bits(unsigned m, float g) {
 }
 
 // One thread's share of an item: kLoads words, all on their way at once; from L2
-// alone (50 MB 20.5 us, with L1's way 24).
+// alone, since no word is read twice by an SM (by L1's way the same within 1%).
 struct Words {
   uint4 w[kLoads];
   bool has[kLoads];
@@ -369,8 +369,8 @@ __device__ __forceinline__ void scale_item(const Item& it, const Words& q, float
       else
         w = make_uint4(pack_bf16x2(g[0], g[1]), pack_bf16x2(g[2], g[3]), pack_bf16x2(g[4], g[5]),
                        pack_bf16x2(g[6], g[7]));
-      // first to leave L2: what is still to be read there stays (100 MB 47 us
-      // against 55, 5.6 GB 2.50 ms against 2.60)
+      // first to leave L2: what is still to be read there stays (50 MB 21.4 us
+      // against 22.7, 100 MB 50.4 against 51.2, 5.6 GB the same)
       __stcs(reinterpret_cast<uint4*>(it.dst + at), w);
     } else {
       int64_t e = at >> kShift;                    // another alignment: element by element
@@ -582,7 +582,9 @@ moe_status moe_clip_grad_norm(const void* const* grads, void* const* outs, const
   const ClipCall c = {grads, outs, numels,   types,     n_tensors, max_norm,
                       eps,   norm_kind, norm_coef, static_cast<double*>(workspace),
                       static_cast<cudaStream_t>(stream)};
-  // the smallest table that holds them: its bytes go with every launch
+  // a table that holds them: its bytes go with every launch. 300 tensors in three
+  // tables of 100 take 78 us for 50 (100 MB); the small tables spare the launches
+  // of few tensors some 28 KB of parameters (0.1 to 0.2 us of 4.7)
   const cudaError_t e = n_tensors <= 8     ? clip<8>(c)
                         : n_tensors <= 100 ? clip<100>(c)
                                            : clip<960>(c);

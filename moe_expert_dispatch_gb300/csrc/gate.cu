@@ -537,21 +537,29 @@ struct GateShape {
 // score in float is off by at most 2^-21 of the largest score (ex2.approx
 // and rcp.approx within 2^-22 and 2^-23, and s (1 - s) <= 1/4), a choice
 // value by 2^-24 of itself more, and its key by the C - 1 units that its low
-// bits hold; a group's score as group_off says. Only tokens with two neighbours in the order closer than that
-// (some 0.3% with scores of 256 experts) are looked at again: for ties and
-// most others in the order of the candidates alone (reorder). bf16
-// logits that rank by themselves leave room for the whole index in the key,
-// and need no second look at all (kScored false: no bias and no groups).
+// bits hold; a group's score as group_off says. Only tokens with two
+// neighbours in the order closer than that (some 0.3% with scores of 256
+// experts) are looked at again: for ties and most others in the order of the
+// candidates alone (reorder). bf16 logits that rank by themselves leave room
+// for the whole index in the key, and need no second look at all (kScored
+// false: no bias and no groups).
 //
 // Bound by instruction issue: 65536 tokens x 256 experts (sigmoid, bias, 8
-// groups) take 60 us, 680 warp instructions a token with two thirds of the
-// issue slots busy, where their 71 MB take 10.5; 49 us without groups, 36 for
-// bf16 logits ranked by themselves. 8192 x 128 take 7.7 us and 32 x 256 7.5,
-// most of it launch and latency. Sixteen experts a lane measured 67 against 71
-// us for eight (65536 x 256), four CTAs an SM 60 against 67 for three. A row
-// whose logits and bias are all the same ties beyond 32 candidates and is
-// left to choose_in_double: 65536 such rows take 0.35 ms (1 to 1.45 ms with an
-// exponential for each expert).
+// groups) take 62 us, 690 warp instructions a token with two thirds of the
+// issue slots busy, where their 71 MB take 10.5; 50 us without groups, 36 for
+// bf16 logits ranked by themselves. 8192 x 128 take 7.6 us and 32 x 256 7.7,
+// most of it launch and latency. Four CTAs an SM measured 60 against 67 for
+// three.
+//
+// The bound on a score is absolute, so that scores far below the largest look
+// closer than they are, and the time then depends on the values. 65536 x 256,
+// k 8, where 50 to 70 us are usual: softmax scores with a bias of zeros and
+// logits of a spread of 5 141 us, of 7 274 (reorder needs the row's sum there, and
+// leaves them to choose_in_double); sigmoid scores with a bias of zeros and logits
+// around -12 103 us, around -15 344, around +12 (scores that are all 1 in
+// float) 994; groups without a bias and logits around -12 109. Rows whose logits
+// and bias are all the same tie beyond 32 candidates: 342 to 364 us. A bias whose
+// values differ keeps saturated scores apart (50 us).
 template <typename L, int W, int C, bool kScored>
 __global__ void __launch_bounds__((GateShape<W, C>::kWarps * 32), (GateShape<W, C>::kCtas))
     gate_kernel(const __grid_constant__ GateParams p, int32_t* __restrict__ ids, float* __restrict__ probs,
@@ -901,7 +909,9 @@ __global__ void __launch_bounds__(256) gate_zero_kernel(int32_t* scratch, int n)
 // W lanes of C experts share a token, as forward. The slots' gradients go
 // through a row of shared memory, zero between tokens, to the lanes that own
 // their experts; every lane then writes its C columns. 16384 x 64 (dense
-// softmax): 5.6 us, half of it a launch's latency, against 1.4 for its 9.2 MB.
+// softmax): 6.0 us, half of it a launch's latency, against 1.4 for its 9.2 MB.
+// 65536 x 256: 54 us dense, 43 where only the chosen have a gradient (71 MB
+// written and read, 10.5).
 template <typename L, int W, int C>
 __global__ void __launch_bounds__((GateShape<W, C>::kWarps * 32), (C > 8 ? 2 : 4))
     gate_backward_kernel(const __grid_constant__ GateParams p, const float* __restrict__ dprobs,
@@ -1112,7 +1122,10 @@ cudaError_t launch_gate_backward(const GateParams& p, const float* dprobs, const
 
 // Calls f with the lanes per token and the experts per lane that hold E. Most
 // instructions are a token's, not an expert's, and a warp issues them once for
-// all its tokens: sixteen experts a lane where there are that many to hold.
+// all its tokens: sixteen experts a lane where there are that many to hold
+// (65536 x 256: 63 us, with eight 72). Where latency counts eight are the shorter
+// way (32 x 256: 7.3 us, with eight 6.0; the gradient 3.7 against 2.9): the shape
+// goes by E alone.
 template <typename F>
 auto with_shape(int E, F&& f) {
   if (E <= 8) return f.template operator()<1, 8>();

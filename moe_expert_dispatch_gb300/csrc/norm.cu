@@ -118,9 +118,9 @@ __device__ __forceinline__ float cta_sum_once(float v, float* red) {
 // One CTA per row, the whole row in its registers: V vectors of W elements a
 // thread (16-byte loads of the stream, coalesced for both types), loaded
 // before the first of the two reductions, so that x and y are read once. For
-// few rows (1 x 7168: 3.7 us, a launch and two reductions; the ring kernel 4.4)
-// and for rows longer than the ring kernels take (4096 x 4096 by this kernel:
-// 37 us, bound by the latency between its reductions).
+// few rows (1 x 7168: 3.1 us, a launch and two reductions; the ring kernel 3.4)
+// and for rows longer than the ring kernels take (4096 x 10240: 74 us, bound by
+// the latency between its reductions; their bytes take 49).
 template <typename ST, typename WT, int V>
 __global__ void __launch_bounds__(1024)
     norm_forward_kernel(NormParams p, ST* out, __nv_bfloat16* __restrict__ n, float* rstd_y,
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(1024)
   }
 }
 
-// ------------------------------------------------------------------ any H, any alignment
+// ------------------------------------------------------------------ any H
 
 // V elements: one, or four through 8- or 16-byte words. Plain accesses: out may be
 // x, and dx may be d_out.
@@ -659,9 +659,11 @@ void with_rows_of(int H, F f) {
 template <typename ST, typename WT>
 cudaError_t forward(const NormParams& p, void* out, void* n, float* rstd_y, float* rstd_out,
                     cudaStream_t s) {
-  // up to one row an SM the kernel without a ring is shorter (1 x 7168: 3.8
-  // against 4.4 us); beyond, rows through shared memory (4096 x 4096: 31
-  // against 37 us)
+  // up to one row an SM the kernel without a ring is shorter (152 x 7168: 3.4
+  // against 3.7 us); beyond, rows through shared memory (300 x 7168: 5.2 against
+  // 5.8, 4096 x 4096 in bf16: 23.4 against 28.9). Not for every shape between:
+  // 300 x 2048 3.5 against 3.0, 600 x 7168 7.8 against 6.9, 4096 x 4096 with a
+  // float stream 36.9 against 35.6
   const int row_bytes = p.H * static_cast<int>(sizeof(ST) + (p.y ? 2 : 0)) + token_gate_bytes(p);
   const RingShape r = ring_shape(p.T, p.H, row_bytes, false, false);
   if (r.groups > 0 && p.T > device_sm_count()) {
@@ -676,8 +678,9 @@ cudaError_t forward(const NormParams& p, void* out, void* n, float* rstd_y, floa
   ST* o = static_cast<ST*>(out);
   __nv_bfloat16* nn = static_cast<__nv_bfloat16*>(n);
   if (p.H % 8 == 0 && forward_threads(p.H, W, 4)) {
-    // few rows: every element a thread of its own, for the shortest way
-    // through a row; many: more loads in flight a thread
+    // few rows: every vector a thread of its own, for the shortest way through a
+    // row (1 x 7168: 3.1 us, with two vectors a thread 3.5, with four 5.0); many:
+    // more loads in flight a thread (4096 x 16384: 115 with four, 135 with two)
     const int nvec = p.H / W;
     int V = p.T <= device_sm_count() * 2 || nvec < 256 ? 1 : nvec < 512 ? 2 : 4;
     while (!forward_threads(p.H, W, V)) V *= 2;

@@ -337,9 +337,11 @@ __device__ __forceinline__ bool may_refill(const RingParams& p, const Walk<V>& w
 
 // ------------------------------------------------------------------ forward
 
-// kAll: with y, w_post and w_next. 4096 x 4096 in bf16 takes 24 us alone and 27
-// with inputs from HBM (134 MB: 5.0 TB/s), of which 4 are launch and the first
-// rows' way; 16384 x 7168 151 us (6.2 TB/s).
+// kAll: with y, w_post and w_next. 4096 x 4096 in bf16 takes 23.5 us where L2 has
+// some of it, and 26.7 (134 MB: 5.0 TB/s), of which 4 are launch and the first
+// rows' way; 16384 x 7168 145 us (6.5 TB/s), with a float stream 247 (5.7 TB/s).
+// Other forms: 16384 x 7168 in bf16 without w_post 164 us (5.7 TB/s), the norm
+// alone 97 (4.8 TB/s).
 template <typename ST, int kGate, bool kFull, bool kAll>
 __global__ void __launch_bounds__(kThreads, 1)
     norm_ring_kernel(const __grid_constant__ RingParams p) {
@@ -473,12 +475,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 // With r = rstd_y: S += r D y, and dy = r (gw D - y (r^2 m(gw D y))). One gate
 // row: dw_post = b g S and dgate = b w_post S; kManyGates keeps S for a row's
 // tokens, and its sum over rows times g in shared memory; kTokenGates sums g
-// times it and writes dgate at once (16384 x 2048 in bf16: 107 us at a floor of 89;
+// times it and writes dgate at once (16384 x 2048 in bf16: 105 us at a floor of 89;
 // by kManyGates' way of leaving a row 409).
 // kAll: with d_out, d_n, y and w_post. 16384 x 7168 with a float stream takes
-// 331 us (2.1 GB: 6.4 TB/s, 94% of a copy's rate), in bf16 229 us (6.2 TB/s);
-// 4083 x 2048 in bf16 with three gate rows 32 us (3.1 TB/s), of which some 9 are
-// launches, the first rows' way and the strips' sums.
+// 327 us (2.1 GB: 6.5 TB/s, 95% of a copy's rate), in bf16 242 us (5.8 TB/s);
+// 4083 x 2048 in bf16 with three gate rows 32.9 us (3.1 TB/s), of which some 9 are
+// launches, the first rows' way and the strips' sums. Other forms choose at run
+// time and spill more: 16384 x 7168 in bf16 without w_post and gate 371 us (y is
+// read and summed up for a gradient that nobody takes: 10 of its 12 bytes an
+// element are needed, 173 us), the norm alone 318 (138); with a float stream 421
+// (277) and 260 (242).
 template <typename ST, int kGate, bool kFull, bool kAll>
 __global__ void __launch_bounds__(kThreads, 1)
     norm_ring_backward_kernel(const __grid_constant__ RingParams p) {
