@@ -723,6 +723,187 @@ moe_status moe_clip_grad_norm(const void* const* grads, void* const* outs, const
                               float eps, float* norm_coef, void* workspace, size_t ws_bytes,
                               void* stream);
 
+/* ------------------------------------------------------------------------
+ * The dense half of a layer: the gated feed-forward block that every token
+ * takes (a shared expert beside the routed ones, a dense layer), low-rank
+ * adapters of many requests beside a projection, and dropout of the branch.
+ * The pages stop at the routed experts; the formulas are stated here in
+ * full. All of them are deterministic: the same inputs give the same bits.
+ * ------------------------------------------------------------------------ */
+
+/* act(z): silu z / (1 + e^-z); gelu z Phi(z); gelu_tanh z (1 + tanh(sqrt(2/pi)
+ * (z + 0.044715 z^3))) / 2; relu max(z, 0) with derivative 0 at 0. */
+typedef enum moe_act {
+  MOE_ACT_SILU = 0,
+  MOE_ACT_GELU = 1,
+  MOE_ACT_GELU_TANH = 2,
+  MOE_ACT_RELU = 3
+} moe_act;
+
+/* ------------------------------------------------------------------------
+ * moe_gated_ffn - the block of one dense expert over every token:
+ *   A_g = x W_gate, A_u = x W_up (float),  h = bf16(act(A_g) * A_u),
+ *   y = bf16(add + h W_down)               (add NULL: 0)
+ * Both projections, the activation and the product are one kernel, W_down
+ * and the addition a second one.
+ *
+ *  x       bf16 [T, H];  w_gate, w_up  bf16 [H, F];  w_down  bf16 [F, H]
+ *  add     bf16 [T, H] or NULL: what the result joins (the routed experts' y)
+ *  act     a moe_act
+ *  y       bf16 [T, H]   out; may be add itself
+ *  a_gate, a_up  bf16 [T, F]  out, both or neither: A_g and A_u for the backward
+ *  workspace >= moe_gated_ffn_workspace_size(T, H, F) bytes, 16-byte aligned
+ * Any T >= 0 below 2^31 - 1024; H % 8 == 0 and F % 8 == 0, each at most 2^30
+ * (else MOE_ERR_UNSUPPORTED). Every pointer starts on 16 bytes; y, a_gate, a_up
+ * and the workspace overlap nothing else of the call (y: add alone, and then
+ * as a whole). T = 0 does nothing. A wait inside the kernels that
+ * hits its limit (2 s) reports MOE_ERR_TIMEOUT, here and in the backward; the
+ * call's outputs are then no results.
+ * ------------------------------------------------------------------------ */
+size_t moe_gated_ffn_workspace_size(int64_t T, int H, int F);
+moe_status moe_gated_ffn(const void* x, const void* w_gate, const void* w_up, const void* w_down,
+                         const void* add, int64_t T, int H, int F, int act, void* y, void* a_gate,
+                         void* a_up, void* workspace, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * moe_gated_ffn_backward - the gradients of moe_gated_ffn:
+ *   dh   = dy W_down^T (float),            h = bf16(act(A_g) A_u) once more,
+ *   dA_g = bf16(dh A_u act'(A_g)),         dA_u = bf16(dh act(A_g)),
+ *   dx   = bf16(add + dA_g W_gate^T + dA_u W_up^T)          (add NULL: 0)
+ *   dW_down = h^T dy,  dW_gate = x^T dA_g,  dW_up = x^T dA_u (float sums)
+ *
+ *  dy      bf16 [T, H];  x, the weights and act: the forward's
+ *  a_gate, a_up  bf16 [T, F] as the forward wrote them
+ *  add     bf16 [T, H] or NULL: the gradient that reaches x by other ways
+ *  dx      bf16 [T, H]   out; may be add itself
+ *  dw_gate, dw_up [H, F], dw_down [F, H]  out, of dw_type (a moe_type), all
+ *          three or, for frozen weights, none; in float they are added to
+ *          what is there when accumulate_dw
+ *  workspace >= moe_gated_ffn_backward_workspace_size(T, H, F) bytes
+ * Sizes and overlaps as moe_gated_ffn; accumulate_dw with bf16 gradients is
+ * MOE_ERR_UNSUPPORTED. T = 0 writes zero weight gradients (or leaves them when
+ * accumulating).
+ * ------------------------------------------------------------------------ */
+size_t moe_gated_ffn_backward_workspace_size(int64_t T, int H, int F);
+moe_status moe_gated_ffn_backward(const void* dy, const void* x, const void* w_gate,
+                                  const void* w_up, const void* w_down, const void* a_gate,
+                                  const void* a_up, const void* add, int64_t T, int H, int F,
+                                  int act, void* dx, void* dw_gate, void* dw_up, void* dw_down,
+                                  int dw_type, int accumulate_dw, void* workspace, size_t ws_bytes,
+                                  void* stream);
+
+/* ------------------------------------------------------------------------
+ * moe_lora_plan - the rows of a batch in the order of their adapters. One
+ * plan serves every projection and layer that the batch goes through.
+ *
+ *  adapter_ids int32 [T]      row t's adapter, 0..n-1, or -1: none
+ *  order       int32 [T]      out: the rows by adapter, each adapter's in their
+ *                             own order; rows without an adapter come last
+ *  offsets     int32 [n + 1]  out: adapter a has order[offsets[a]] up to
+ *                             order[offsets[a + 1]]; from offsets[n] on: none
+ * An id outside [-1, n) counts as none and raises MOE_ERR_BAD_EXPERT_ID. One
+ * launch, no workspace. 1 <= n <= 1024, T < 2^31; T = 0 gives zero offsets.
+ * ------------------------------------------------------------------------ */
+moe_status moe_lora_plan(const int32_t* adapter_ids, int64_t T, int n, int32_t* order,
+                         int32_t* offsets, void* stream);
+
+/* ------------------------------------------------------------------------
+ * moe_lora - low-rank adapters beside a shared projection: with a = the
+ * row's adapter,
+ *   v_t = A_a x_t (float),   out_t = bf16(base_t + s_a B_a^T v_t)
+ * A row without an adapter has v_t = 0 and out_t = base_t. v enters the second
+ * product as the sum of two bf16 numbers (16 bits of it).
+ *
+ *  x       bf16 [T, H]
+ *  a       bf16 [n, r, H], b  bf16 [n, r, N]: both with the rank ahead of the
+ *          width, so that a row of either is contiguous
+ *  adapter_ids, order, offsets: as moe_lora_plan took and wrote them. A row
+ *          number outside [0, T) or offsets that do not grow from 0 to at most T
+ *          are never followed; the result is then none, and
+ *          MOE_ERR_BAD_EXPERT_ID is raised
+ *  scales  float [n] or NULL: s_a, or 1
+ *  base    bf16 [T, N] or NULL (0): the projection's result
+ *  out     bf16 [T, N]   out; may be base itself
+ *  v       float [T, r]  out: what the backward needs
+ * 1 <= r <= 128, H % 8 == 0 and N % 8 == 0 (else MOE_ERR_UNSUPPORTED), 1 <= n <=
+ * 1024, T < 2^31 - 1024. Pointers start on 16 bytes; out and v overlap nothing
+ * else of the call (out: base alone, and then as a whole). T = 0 does nothing.
+ * ------------------------------------------------------------------------ */
+moe_status moe_lora(const void* x, const void* a, const void* b, const int32_t* adapter_ids,
+                    const int32_t* order, const int32_t* offsets, const float* scales,
+                    const void* base, int64_t T, int H, int N, int n, int r, void* out, float* v,
+                    void* stream);
+
+/* ------------------------------------------------------------------------
+ * moe_lora_backward - the gradients of moe_lora (that of base is dy itself):
+ *   dv_t = s_a B_a dy_t (float),   dx_t = bf16(base_t + A_a^T dv_t)
+ *   dA_a = sum_t dv_t x_t^T,       dB_a = s_a sum_t v_t dy_t^T (float)
+ * over the rows t of adapter a. dv and v enter the products as the sum of two
+ * bf16 numbers.
+ *
+ *  dy      bf16 [T, N];  x, a, b, order, offsets, scales: the forward's
+ *  v       float [T, r] as the forward wrote it
+ *  base    bf16 [T, H] or NULL: the gradient that reaches x by the projection
+ *  dx      bf16 [T, H]   out; may be base itself
+ *  da      float [n, r, H], db  float [n, r, N]   out; added to what is there
+ *          when accumulate. An adapter without rows gets 0 (or is left)
+ *  workspace >= moe_lora_backward_workspace_size(T, r) bytes, 16-byte aligned
+ * Limits as moe_lora. T = 0 writes zero gradients (or leaves them).
+ * ------------------------------------------------------------------------ */
+size_t moe_lora_backward_workspace_size(int64_t T, int r);
+moe_status moe_lora_backward(const void* dy, const void* x, const float* v, const void* a,
+                             const void* b, const int32_t* order, const int32_t* offsets,
+                             const float* scales, const void* base, int64_t T, int H, int N, int n,
+                             int r, void* dx, float* da, float* db, int accumulate,
+                             void* workspace, size_t ws_bytes, void* stream);
+
+/* Scalars and types of dropout. moe_dropout_config_init() fills the defaults:
+ * p 0.1, both scales 1, a bf16 stream and a bf16 branch; a NULL pointer means
+ * the defaults. */
+typedef struct moe_dropout_config {
+  float p;               /* probability to drop, in [0, 1): the threshold below
+                            is min(65535, p * 65536 rounded to nearest, even)   */
+  float residual_scale;  /* a: factor of the residual stream                   */
+  float branch_scale;    /* b: factor of the branch                            */
+  int stream_type;       /* moe_type of x, out, d_out and dx                   */
+  int branch_type;       /* moe_type of y and dy                               */
+} moe_dropout_config;
+
+void moe_dropout_config_init(moe_dropout_config* cfg);
+
+/* ------------------------------------------------------------------------
+ * moe_dropout_residual - dropout of a branch and its scaled residual, with a
+ * mask that is never stored:
+ *   out_i = a x_i + f m_i y_i   (x NULL: f m_i y_i),   f = b / (1 - t / 65536)
+ * in float, rounded once. m_i = [u_i >= t], t the threshold of p, u_i the 16-bit
+ * number of element i: Philox 4x32 of ten rounds gives eight of them a block, at
+ * counter (i / 8 in two words, draw in two words, low words first) under the key
+ * seed (two words); element i has half i % 2 (0 the low one) of word i % 8 / 2.
+ * What is dropped is 0 whatever y holds there (NaN too).
+ *
+ *  y       [numel] of the branch's type, x and out [numel] of the stream's; out
+ *          may be x itself, or y where the types are one
+ *  rng     int64 [2], DEVICE memory: seed and draw. It is read when the kernel
+ *          runs, so that a graph replayed with another draw drops others. Two
+ *          calls with one seed and draw drop the same elements.
+ * Pointers aligned to their element (with all of them on 16 bytes eight elements
+ * go at once). numel < 2^40; 0 does nothing.
+ * ------------------------------------------------------------------------ */
+moe_status moe_dropout_residual(const void* y, const void* x, int64_t numel, const int64_t* rng,
+                                const moe_dropout_config* cfg, void* out, void* stream);
+
+/* ------------------------------------------------------------------------
+ * moe_dropout_residual_backward - its gradients, by the same mask:
+ *   dy_i = f m_i d_out_i,   dx_i = a d_out_i
+ *  dx      [numel] of the stream's type, or NULL (no residual, or a = 1, where
+ *          it is d_out); may be d_out itself
+ *  dy      [numel] of the branch's type   out; may be d_out where the types are
+ *          one and dx is NULL
+ * ------------------------------------------------------------------------ */
+moe_status moe_dropout_residual_backward(const void* d_out, int64_t numel, const int64_t* rng,
+                                         const moe_dropout_config* cfg, void* dx, void* dy,
+                                         void* stream);
+
 #ifdef __cplusplus
 }
 #endif

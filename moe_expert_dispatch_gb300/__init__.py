@@ -65,6 +65,12 @@ class moe_norm_config(ctypes.Structure):
                 ("weight_type", ctypes.c_int)]
 
 
+class moe_dropout_config(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_float), ("residual_scale", ctypes.c_float),
+                ("branch_scale", ctypes.c_float), ("stream_type", ctypes.c_int),
+                ("branch_type", ctypes.c_int)]
+
+
 STEP_EVENTS = 5       # forward: start, routing, fc1+SwiGLU, fc2, unpermute
 BWD_STEP_EVENTS = 7   # backward: start, dO+dprobs, dH, dXp, dX, dW1, dW2
 # MXFP8 backward: start, dO + quantise, dH, quantise dA, dXp, dX, quantise x and h, dW1, dW2
@@ -131,6 +137,24 @@ _sig("moe_norm_residual_backward", _i32, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp
 _sig("moe_clip_grad_norm_workspace_size", _sz)
 _sig("moe_clip_grad_norm", _i32, _vp, _vp, _vp, _vp, _i64, ctypes.c_float, _i32, ctypes.c_float,
      _vp, _vp, _sz, _vp)
+
+_sig("moe_gated_ffn_workspace_size", _sz, _i64, _i32, _i32)
+_sig("moe_gated_ffn", _i32, _vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _vp, _vp, _vp, _vp,
+     _sz, _vp)
+_sig("moe_gated_ffn_backward_workspace_size", _sz, _i64, _i32, _i32)
+_sig("moe_gated_ffn_backward", _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32,
+     _i32, _vp, _vp, _vp, _vp, _i32, _i32, _vp, _sz, _vp)
+_sig("moe_lora_plan", _i32, _vp, _i64, _i32, _vp, _vp, _vp)
+_sig("moe_lora", _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i32, _vp,
+     _vp, _vp)
+_sig("moe_lora_backward_workspace_size", _sz, _i64, _i32)
+_sig("moe_lora_backward", _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32,
+     _i32, _i32, _vp, _vp, _vp, _i32, _vp, _sz, _vp)
+_sig("moe_dropout_config_init", None, ctypes.POINTER(moe_dropout_config))
+_sig("moe_dropout_residual", _i32, _vp, _vp, _i64, _vp, ctypes.POINTER(moe_dropout_config), _vp,
+     _vp)
+_sig("moe_dropout_residual_backward", _i32, _vp, _i64, _vp, ctypes.POINTER(moe_dropout_config),
+     _vp, _vp, _vp)
 
 
 class MoeError(RuntimeError):
@@ -1073,3 +1097,263 @@ def moe_grad_norm(grads, norm_type=2.0, norm_coef=None, workspace=None, stream=N
     """The norm alone of a list of gradients: a float32 tensor of one element."""
     return moe_clip_grad_norm(grads, None, norm_type=norm_type, norm_coef=norm_coef,
                               workspace=workspace, stream=stream)[0]
+
+
+_ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}
+
+
+def _act(act):
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {sorted(_ACTS)}, got {act!r}")
+    return _ACTS[act]
+
+
+def _made(t, shape, dtype, dev):
+    """The given output, or a new one."""
+    return torch.empty(shape, dtype=dtype, device=dev) if t is None else t
+
+
+def _ffn_weights(dev, H, w_gate, w_up, w_down):
+    """F, of w_gate and w_up [H, F] and w_down [F, H]."""
+    bf16 = torch.bfloat16
+    _fit(dev, (w_gate, "w_gate", bf16, 0), (w_up, "w_up", bf16, 0), (w_down, "w_down", bf16, 0))
+    if w_gate.dim() != 2:
+        raise ValueError(f"w_gate must have shape [{H}, F], got {list(w_gate.shape)}")
+    F = w_gate.shape[1]
+    _shaped(w_gate, "w_gate", H, F)
+    _shaped(w_up, "w_up", H, F)
+    _shaped(w_down, "w_down", F, H)
+    return F
+
+
+def moe_gated_ffn(x, w_gate, w_up, w_down, act="silu", add=None, save_for_backward=False, y=None,
+                  a_gate=None, a_up=None, workspace=None, stream=None):
+    """The gated feed-forward block of a dense layer or a shared expert over
+    x bf16 [T, H]: y = add + (act(x w_gate) * (x w_up)) w_down, with w_gate and
+    w_up bf16 [H, F], w_down bf16 [F, H], act "silu", "gelu", "gelu_tanh" or
+    "relu", and add bf16 [T, H] (the routed experts' result) or None. Returns
+    dict(y, a_gate, a_up); a_gate = x w_gate and a_up = x w_up (bf16 [T, F]) are
+    kept with save_for_backward, else None. y may be add itself. H and F are
+    multiples of 8, tensors start on 16 bytes."""
+    if _elsewhere(stream):
+        return _within(stream, moe_gated_ffn, locals())
+    bf16 = torch.bfloat16
+    T, H = x.shape
+    dev = x.device
+    _fit(dev, (x, "x", bf16, 0))
+    F = _ffn_weights(dev, H, w_gate, w_up, w_down)
+    _shaped(add, "add", T, H)
+    if save_for_backward:
+        a_gate, a_up = _made(a_gate, (T, F), bf16, dev), _made(a_up, (T, F), bf16, dev)
+    else:
+        a_gate = a_up = None
+    y = _made(y, (T, H), bf16, dev)
+    _fit(dev, (add, "add", bf16, 0), (y, "y", bf16, T * H), (a_gate, "a_gate", bf16, T * F),
+         (a_up, "a_up", bf16, T * F))
+    ws, ws_bytes = _scratch(workspace, _lib.moe_gated_ffn_workspace_size(T, H, F), dev)
+    _check(_on(dev, _lib.moe_gated_ffn, x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(),
+               w_down.data_ptr(), _ptr(add), T, H, F, _act(act), y.data_ptr(), _ptr(a_gate),
+               _ptr(a_up), _ptr(ws), ws_bytes, _raw_stream(stream, dev)), "moe_gated_ffn")
+    return dict(y=y, a_gate=a_gate, a_up=a_up)
+
+
+def moe_gated_ffn_backward(dy, x, w_gate, w_up, w_down, a_gate, a_up, act="silu", add=None,
+                           weight_grads=True, dw_dtype=torch.bfloat16, dx=None, dw_gate=None,
+                           dw_up=None, dw_down=None, accumulate_dw=False, workspace=None,
+                           stream=None):
+    """Gradients of moe_gated_ffn from dy bf16 [T, H]; x, the weights, act, a_gate
+    and a_up are the forward's, add (bf16 [T, H] or None) what reaches x by other
+    ways and joins dx. Returns dict(dx, dw_gate, dw_up, dw_down): the weight
+    gradients in the type of those given, else in dw_dtype (torch.bfloat16 or
+    torch.float32); in float32 they are added to what is there with accumulate_dw;
+    None without weight_grads (frozen weights). dx may be add itself."""
+    if _elsewhere(stream):
+        return _within(stream, moe_gated_ffn_backward, locals())
+    bf16 = torch.bfloat16
+    T, H = x.shape
+    dev = x.device
+    _fit(dev, (x, "x", bf16, 0), (dy, "dy", bf16, 0), (add, "add", bf16, 0),
+         (a_gate, "a_gate", bf16, 0), (a_up, "a_up", bf16, 0))
+    F = _ffn_weights(dev, H, w_gate, w_up, w_down)
+    _shaped(dy, "dy", T, H)
+    _shaped(add, "add", T, H)
+    _shaped(a_gate, "a_gate", T, F)
+    _shaped(a_up, "a_up", T, F)
+    dx = _made(dx, (T, H), bf16, dev)
+    wt = 0
+    if weight_grads:
+        given = [t for t in (dw_gate, dw_up, dw_down) if t is not None]
+        if accumulate_dw and len(given) != 3:
+            raise ValueError("accumulate_dw adds to dw_gate, dw_up and dw_down: pass them")
+        dt = given[0].dtype if given else dw_dtype
+        if dt not in _TYPES:
+            raise ValueError(f"weight gradients must be torch.float32 or torch.bfloat16, got {dt}")
+        wt = _TYPES[dt]
+        dw_gate, dw_up = _made(dw_gate, (H, F), dt, dev), _made(dw_up, (H, F), dt, dev)
+        dw_down = _made(dw_down, (F, H), dt, dev)
+        _fit(dev, (dw_gate, "dw_gate", dt, H * F), (dw_up, "dw_up", dt, H * F),
+             (dw_down, "dw_down", dt, H * F))
+    else:
+        dw_gate = dw_up = dw_down = None
+    _fit(dev, (dx, "dx", bf16, T * H))
+    ws, ws_bytes = _scratch(workspace, _lib.moe_gated_ffn_backward_workspace_size(T, H, F), dev)
+    _check(_on(dev, _lib.moe_gated_ffn_backward, dy.data_ptr(), x.data_ptr(), w_gate.data_ptr(),
+               w_up.data_ptr(), w_down.data_ptr(), a_gate.data_ptr(), a_up.data_ptr(), _ptr(add),
+               T, H, F, _act(act), dx.data_ptr(), _ptr(dw_gate), _ptr(dw_up), _ptr(dw_down), wt,
+               bool(accumulate_dw), _ptr(ws), ws_bytes, _raw_stream(stream, dev)),
+           "moe_gated_ffn_backward")
+    return dict(dx=dx, dw_gate=dw_gate, dw_up=dw_up, dw_down=dw_down)
+
+
+def moe_lora_plan(adapter_ids, n, order=None, offsets=None, stream=None):
+    """The rows of a batch by adapter: (order int32 [T], offsets int32 [n + 1]) of
+    adapter_ids int32 [T], -1 for a row without one. Adapter a has the rows
+    order[offsets[a]:offsets[a + 1]] in their own order; those without one come
+    last. One plan serves every projection and layer of the batch."""
+    if _elsewhere(stream):
+        return _within(stream, moe_lora_plan, locals())
+    dev = adapter_ids.device
+    if adapter_ids.dim() != 1:
+        raise ValueError(f"adapter_ids must have shape [T], got {list(adapter_ids.shape)}")
+    T = adapter_ids.shape[0]
+    order = _made(order, (T,), torch.int32, dev)
+    offsets = _made(offsets, (max(n, 0) + 1,), torch.int32, dev)
+    _fit(dev, (adapter_ids, "adapter_ids", torch.int32, 0), (order, "order", torch.int32, T),
+         (offsets, "offsets", torch.int32, n + 1))
+    _check(_on(dev, _lib.moe_lora_plan, adapter_ids.data_ptr(), T, n, order.data_ptr(),
+               offsets.data_ptr(), _raw_stream(stream, dev)), "moe_lora_plan")
+    return order, offsets
+
+
+def _lora_operands(dev, T, a, b, adapter_ids, plan, scales):
+    """(n, r, H, N, order, offsets) of a [n, r, H] and b [n, r, N]."""
+    if a.dim() != 3 or b.dim() != 3 or a.shape[:2] != b.shape[:2]:
+        raise ValueError("a and b must have shapes [n, r, H] and [n, r, N], got "
+                         f"{list(a.shape)} and {list(b.shape)}")
+    n, r, H = a.shape
+    _fit(dev, (a, "a", torch.bfloat16, 0), (b, "b", torch.bfloat16, 0),
+         (adapter_ids, "adapter_ids", torch.int32, 0), (scales, "scales", torch.float32, 0))
+    _shaped(adapter_ids, "adapter_ids", T)
+    _shaped(scales, "scales", n)
+    order, offsets = moe_lora_plan(adapter_ids, n) if plan is None else plan
+    _fit(dev, (order, "order", torch.int32, 0), (offsets, "offsets", torch.int32, 0))
+    _shaped(order, "order", T)
+    _shaped(offsets, "offsets", n + 1)
+    return n, r, H, b.shape[2], order, offsets
+
+
+def moe_lora(x, a, b, adapter_ids, plan=None, scales=None, base=None, out=None, v=None,
+             stream=None):
+    """Low-rank adapters beside a shared projection: for row t with adapter i =
+    adapter_ids[t], v_t = a[i] x_t and out_t = base_t + scales[i] * b[i]^T v_t. x
+    bf16 [T, H], a bf16 [n, r, H], b bf16 [n, r, N] (rank first in both),
+    adapter_ids int32 [T] with -1 for a row without one, plan what moe_lora_plan
+    gives for them (made here when None), scales float32 [n] or None (1), base
+    bf16 [T, N] (the projection's result) or None (0). Returns dict(out bf16 [T,
+    N], v float32 [T, r]), v for the backward. out may be base itself. r is 1 to
+    128, H and N are multiples of 8, tensors start on 16 bytes."""
+    if _elsewhere(stream):
+        return _within(stream, moe_lora, locals())
+    bf16 = torch.bfloat16
+    T, H = x.shape
+    dev = x.device
+    n, r, ha, N, order, offsets = _lora_operands(dev, T, a, b, adapter_ids, plan, scales)
+    if ha != H:
+        raise ValueError(f"a must have shape [n, r, {H}], got {list(a.shape)}")
+    _shaped(base, "base", T, N)
+    out, v = _made(out, (T, N), bf16, dev), _made(v, (T, r), torch.float32, dev)
+    _fit(dev, (x, "x", bf16, 0), (base, "base", bf16, 0), (out, "out", bf16, T * N),
+         (v, "v", torch.float32, T * r))
+    _check(_on(dev, _lib.moe_lora, x.data_ptr(), a.data_ptr(), b.data_ptr(),
+               adapter_ids.data_ptr(), order.data_ptr(), offsets.data_ptr(), _ptr(scales),
+               _ptr(base), T, H, N, n, r, out.data_ptr(), v.data_ptr(), _raw_stream(stream, dev)),
+           "moe_lora")
+    return dict(out=out, v=v)
+
+
+def moe_lora_backward(dy, x, v, a, b, adapter_ids, plan=None, scales=None, base=None, dx=None,
+                      da=None, db=None, accumulate=False, workspace=None, stream=None):
+    """Gradients of moe_lora from dy bf16 [T, N]: dict(dx bf16 [T, H], da float32
+    [n, r, H], db float32 [n, r, N]). x, v, a, b, adapter_ids, plan and scales are
+    the forward's; base (bf16 [T, H] or None) is what reaches x by the projection
+    and joins dx. With accumulate da and db are added to what the given tensors
+    hold. dx may be base itself. base's own gradient in the forward is dy."""
+    if _elsewhere(stream):
+        return _within(stream, moe_lora_backward, locals())
+    bf16, f32 = torch.bfloat16, torch.float32
+    T, H = x.shape
+    dev = x.device
+    n, r, ha, N, order, offsets = _lora_operands(dev, T, a, b, adapter_ids, plan, scales)
+    if ha != H:
+        raise ValueError(f"a must have shape [n, r, {H}], got {list(a.shape)}")
+    if accumulate and (da is None or db is None):
+        raise ValueError("accumulate adds to da and db: pass them")
+    _shaped(dy, "dy", T, N)
+    _shaped(v, "v", T, r)
+    _shaped(base, "base", T, H)
+    dx = _made(dx, (T, H), bf16, dev)
+    da, db = _made(da, (n, r, H), f32, dev), _made(db, (n, r, N), f32, dev)
+    _fit(dev, (x, "x", bf16, 0), (dy, "dy", bf16, 0), (v, "v", f32, 0), (base, "base", bf16, 0),
+         (dx, "dx", bf16, T * H), (da, "da", f32, n * r * H), (db, "db", f32, n * r * N))
+    ws, ws_bytes = _scratch(workspace, _lib.moe_lora_backward_workspace_size(T, r), dev)
+    _check(_on(dev, _lib.moe_lora_backward, dy.data_ptr(), x.data_ptr(), v.data_ptr(),
+               a.data_ptr(), b.data_ptr(), order.data_ptr(), offsets.data_ptr(), _ptr(scales),
+               _ptr(base), T, H, N, n, r, dx.data_ptr(), da.data_ptr(), db.data_ptr(),
+               bool(accumulate), _ptr(ws), ws_bytes, _raw_stream(stream, dev)),
+           "moe_lora_backward")
+    return dict(dx=dx, da=da, db=db)
+
+
+def _rng(rng, dev):
+    _fit(dev, (rng, "rng", torch.int64, 2))
+    _shaped(rng, "rng", 2)
+    return rng.data_ptr()
+
+
+def moe_dropout_residual(y, rng, p, x=None, residual_scale=1.0, branch_scale=1.0, out=None,
+                         stream=None):
+    """Dropout of a branch and the scaled residual it joins: out = residual_scale
+    * x + branch_scale / (1 - p) * mask * y, the mask made anew wherever it is
+    needed from rng, an int64 [2] CUDA tensor of seed and draw that the kernel
+    reads (add to rng[1] between steps: a captured graph then drops others at
+    every replay). y is float32 or bfloat16 of any shape; x has that shape and
+    the result's type, without x there is no residual and the result has y's
+    type (or out's). p, in [0, 1), is taken to the nearest 1/65536 and the factor
+    is that one's. out may be x itself."""
+    if _elsewhere(stream):
+        return _within(stream, moe_dropout_residual, locals())
+    bt = _typed(y, "y")
+    dev = y.device
+    _shaped(x, "x", *y.shape)
+    out = _made(out, y.shape, (y if x is None else x).dtype, dev)
+    st = _typed(out, "out")
+    _fit(dev, (y, "y", y.dtype, 0), (x, "x", out.dtype, 0), (out, "out", out.dtype, y.numel()))
+    _check(_on(dev, _lib.moe_dropout_residual, y.data_ptr(), _ptr(x), y.numel(), _rng(rng, dev),
+               moe_dropout_config(p, residual_scale, branch_scale, st, bt), out.data_ptr(),
+               _raw_stream(stream, dev)), "moe_dropout_residual")
+    return out
+
+
+def moe_dropout_residual_backward(d_out, rng, p, residual=True, residual_scale=1.0,
+                                  branch_scale=1.0, dx=None, dy=None, branch_dtype=torch.bfloat16,
+                                  stream=None):
+    """Gradients of moe_dropout_residual by the same rng, p and scales: dict(dx,
+    dy), dy of dy's type or branch_dtype, dx of d_out's type, or None without a
+    residual. dx may be d_out itself."""
+    if _elsewhere(stream):
+        return _within(stream, moe_dropout_residual_backward, locals())
+    st = _typed(d_out, "d_out")
+    dev = d_out.device
+    if dy is None:
+        dy = torch.empty(d_out.shape, dtype=branch_dtype, device=dev)
+    bt = _typed(dy, "dy")
+    if not residual:
+        dx = None
+    elif dx is None:
+        dx = torch.empty_like(d_out)
+    _fit(dev, (d_out, "d_out", d_out.dtype, 0), (dx, "dx", d_out.dtype, d_out.numel()),
+         (dy, "dy", dy.dtype, d_out.numel()))
+    _check(_on(dev, _lib.moe_dropout_residual_backward, d_out.data_ptr(), d_out.numel(),
+               _rng(rng, dev), moe_dropout_config(p, residual_scale, branch_scale, st, bt),
+               _ptr(dx), dy.data_ptr(), _raw_stream(stream, dev)), "moe_dropout_residual_backward")
+    return dict(dx=dx, dy=dy)

@@ -5,3 +5,4 @@ reference arm may import this package; the CUDA library never does.
 """
 from .moe_oracle import *  # noqa: F401,F403
 from .layer_oracle import *  # noqa: F401,F403
+from .dense_oracle import *  # noqa: F401,F403

@@ -1,0 +1,276 @@
+"""Low-rank adapters on the GPU against the float64 oracle.
+
+Small integers: every sum is an integer below 2^24 (and v one that two bf16
+numbers hold), so v, da, db and the roundings of out and dx have to be equal.
+Gaussian values: v is a float sum (2^-23 of its terms a chain of 64, float
+additions beyond); out and dx lie within 2^-8 of themselves and 2^-15 of the sum
+of their terms (v to 16 bits, the sums' own roundings); da and db within 2^-15
+of theirs."""
+import numpy as np
+import pytest
+import torch
+
+import oracle as orc
+
+pytestmark = pytest.mark.gpu
+m = pytest.importorskip("moe_expert_dispatch_gb300")
+
+BF = torch.bfloat16
+
+
+def _np(t):
+    return t.detach().double().cpu().numpy()
+
+
+def _ids(T, n, kind, rng):
+    if kind == "mixed":
+        return rng.integers(-1, n, T)
+    if kind == "none":
+        return np.full(T, -1)
+    if kind == "one":
+        return np.full(T, n - 1)
+    ids = np.sort(rng.integers(0, n, T))           # runs, some adapters without a row
+    return rng.permutation(n)[ids]
+
+
+def _draw(T, H, N, n, r, kind, seed, integers):
+    rng = np.random.default_rng(seed)
+
+    def make(*shape, sd=1.0, low=-2, high=3):
+        v = rng.integers(low, high, shape).astype(np.float64) if integers \
+            else rng.standard_normal(shape) * sd
+        return torch.from_numpy(v.astype(np.float32)).to(BF).cuda()
+
+    # integers: A sparse enough that v stays below 2^16
+    v = dict(x=make(T, H), a=make(n, r, H, sd=H ** -0.5), b=make(n, r, N, sd=r ** -0.5))
+    scales = rng.choice([0.5, 1.0, 2.0, -4.0], n) if integers else rng.uniform(0.5, 2.0, n)
+    return (v, torch.from_numpy(_ids(T, n, kind, rng).astype(np.int32)).cuda(),
+            torch.from_numpy(scales.astype(np.float32)).cuda(), make(T, N), make(T, H), make(T, N))
+
+
+CASES = [(1, 64, 64, 1, 1, "one"), (1, 4096, 4096, 8, 16, "mixed"), (2, 8, 8, 3, 4, "mixed"),
+         (5, 200, 72, 4, 13, "mixed"), (33, 512, 1000, 7, 16, "mixed"),
+         (64, 264, 520, 70, 64, "mixed"), (128, 64, 136, 5, 32, "runs"),
+         (129, 72, 328, 3, 16, "runs"), (200, 136, 264, 2, 17, "mixed"),
+         (300, 520, 128, 9, 33, "runs"), (257, 128, 512, 4, 100, "mixed"),
+         (400, 256, 200, 40, 128, "runs"), (500, 64, 64, 3, 8, "none"),
+         (700, 328, 392, 1, 48, "one"), (1500, 200, 136, 6, 16, "mixed")]
+
+
+@pytest.mark.parametrize("T,n,kind", [(0, 3, "mixed"), (1, 1, "one"), (31, 5, "mixed"),
+                                      (33, 5, "runs"), (1000, 1, "none"), (1024, 1024, "mixed"),
+                                      (1025, 7, "mixed"), (20000, 33, "mixed")])
+def test_lora_plan(T, n, kind):
+    ids = _ids(T, n, kind, np.random.default_rng(T))
+    order, offsets = m.moe_lora_plan(torch.from_numpy(ids.astype(np.int32)).cuda(), n)
+    want = orc.lora_plan(ids.tolist(), n)
+    assert np.array_equal(order.cpu().numpy(), want[0])
+    assert np.array_equal(offsets.cpu().numpy(), want[1])
+    assert m.moe_get_error() == 0
+
+
+@pytest.mark.parametrize("T,H,N,n,r,kind", CASES)
+def test_lora_integers(T, H, N, n, r, kind):
+    v, ids, scales, base, dbase, dy = _draw(T, H, N, n, r, kind, T + r, True)
+    n64 = {k: _np(t) for k, t in v.items()}
+    rows = ids.cpu().numpy()
+    plan = m.moe_lora_plan(ids, n)
+    for s, bs, db_ in ((None, None, None), (scales, base, dbase)):
+        s64 = None if s is None else _np(s)
+        ref, rv = orc.lora(**n64, ids=rows, scales=s64, base=None if bs is None else _np(bs))
+        got = m.moe_lora(**v, adapter_ids=ids, plan=plan, scales=s, base=bs)
+        assert np.array_equal(_np(got["v"]), rv)
+        assert torch.equal(got["out"].cpu(), torch.from_numpy(ref).float().to(BF))
+        want = orc.lora_backward(_np(dy), n64["x"], rv, n64["a"], n64["b"], rows, s64,
+                                 None if db_ is None else _np(db_))
+        back = m.moe_lora_backward(dy, v["x"], got["v"], v["a"], v["b"], ids, plan=plan, scales=s,
+                                   base=db_)
+        assert m.moe_get_error() == 0
+        assert np.abs(want["dv"]).max(initial=0) < 2 ** 16       # two bf16 numbers hold it
+        assert torch.equal(back["dx"].cpu(), torch.from_numpy(want["dx"]).float().to(BF))
+        for key in ("da", "db"):
+            assert np.abs(want[key]).max() < 2 ** 24
+            assert np.array_equal(_np(back[key]), want[key]), key
+        more = {k: torch.full_like(back[k], 2.0) for k in ("da", "db")}
+        m.moe_lora_backward(dy, v["x"], got["v"], v["a"], v["b"], ids, scales=s, base=db_, **more,
+                            accumulate=True)
+        for key in more:
+            assert np.array_equal(_np(more[key]), want[key] + 2.0), key
+
+
+@pytest.mark.parametrize("T,H,N,n,r,kind", [(3, 1000, 264, 4, 16, "mixed"),
+                                            (100, 512, 328, 6, 24, "mixed"),
+                                            (400, 1032, 200, 3, 64, "runs"),
+                                            (900, 136, 520, 5, 128, "mixed")])
+def test_lora_gaussian(T, H, N, n, r, kind):
+    v, ids, scales, base, dbase, dy = _draw(T, H, N, n, r, kind, T, False)
+    n64, rows, s64 = {k: _np(t) for k, t in v.items()}, ids.cpu().numpy(), _np(scales)
+    size = {k: np.abs(t) for k, t in n64.items()}
+    got = m.moe_lora(**v, adapter_ids=ids, scales=scales, base=base)
+    ref, rv = orc.lora(**n64, ids=rows, scales=s64, base=_np(base))
+    terms, vt = orc.lora(**size, ids=rows, scales=np.abs(s64), base=np.abs(_np(base)))
+    assert (np.abs(_np(got["v"]) - rv) <= 2.0 ** -17 * vt).all()
+    err = np.abs(_np(got["out"]) - ref)
+    assert (err <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -15 * terms).all()
+    kept = _np(got["v"])
+    back = m.moe_lora_backward(dy, v["x"], got["v"], v["a"], v["b"], ids, scales=scales,
+                               base=dbase)
+    want = orc.lora_backward(_np(dy), n64["x"], kept, n64["a"], n64["b"], rows, s64, _np(dbase))
+    t = orc.lora_backward(np.abs(_np(dy)), size["x"], np.abs(kept), size["a"], size["b"], rows,
+                          s64, np.abs(_np(dbase)))
+    assert (np.abs(_np(back["dx"]) - want["dx"])
+            <= 2.0 ** -8 * np.abs(want["dx"]) + 2.0 ** -15 * t["dx"]).all()
+    for key in ("da", "db"):
+        assert (np.abs(_np(back[key]) - want[key]) <= 2.0 ** -15 * t[key]).all(), key
+    assert m.moe_get_error() == 0
+
+
+def test_lora_gradient_against_differences():
+    """The slope of the float64 forward along a random direction of each input: exact
+    but for the roundings of v (2^-16) and of dx (2^-8, averaged over its elements)."""
+    T, H, N, n, r = 150, 64, 72, 3, 8
+    v, ids, scales, _, _, dy = _draw(T, H, N, n, r, "mixed", 2, False)
+    n64, rows, s64 = {k: _np(t) for k, t in v.items()}, ids.cpu().numpy(), _np(scales)
+    f = m.moe_lora(**v, adapter_ids=ids, scales=scales)
+    got = m.moe_lora_backward(dy, v["x"], f["v"], v["a"], v["b"], ids, scales=scales)
+    rng = np.random.default_rng(1)
+    for key, name in (("x", "dx"), ("a", "da"), ("b", "db")):
+        u = rng.standard_normal(n64[key].shape)
+
+        def loss(e):
+            p = dict(n64, **{key: n64[key] + e * u})
+            return float((orc.lora(**p, ids=rows, scales=s64)[0] * _np(dy)).sum())
+
+        slope, size = (loss(1e-5) - loss(-1e-5)) / 2e-5, np.linalg.norm(_np(got[name]))
+        assert abs(slope - float((_np(got[name]) * u).sum())) < 2.0 ** -6 * size, name
+
+
+@pytest.mark.parametrize("T", [20, 300])
+def test_lora_bad_ids_and_plans(T):
+    v, ids, scales, base, _, dy = _draw(T, 64, 72, 4, 8, "mixed", 3, True)
+    want = m.moe_lora(**v, adapter_ids=ids, base=base)["out"]
+    bad = ids.clone()
+    bad[3], bad[7] = 4, -2
+    order, offsets = m.moe_lora_plan(bad, 4)
+    assert m.moe_get_error() == 3
+    got = m.moe_lora(**v, adapter_ids=bad, plan=(order, offsets), base=base)["out"]
+    # those rows have no adapter, the others keep theirs
+    assert torch.equal(got[[3, 7]], base[[3, 7]])
+    rest = [t for t in range(T) if t not in (3, 7)]
+    assert torch.equal(got[rest], want[rest])
+    m.moe_get_error()
+    if T <= 128:
+        return
+    # rows and offsets outside the batch are reported and not followed
+    order, offsets = m.moe_lora_plan(ids, 4)
+    for where, value in ((0, T), (5, -1), (T - 1, 2 ** 31 - 1)):
+        o = order.clone()
+        o[where] = value
+        m.moe_lora(**v, adapter_ids=ids, plan=(o, offsets), base=base)
+        assert m.moe_get_error() == 3, (where, value)
+    for where, value in ((0, 1), (0, -5), (1, T + 9), (2, -1), (4, T + 1), (3, 2 ** 31 - 1)):
+        o = offsets.clone()
+        o[where] = value
+        f = m.moe_lora(**v, adapter_ids=ids, plan=(order, o), base=base)
+        assert m.moe_get_error() == 3, (where, value)
+        m.moe_lora_backward(dy, v["x"], f["v"], v["a"], v["b"], ids, plan=(order, o))
+        assert m.moe_get_error() == 3, (where, value)
+
+
+@pytest.mark.parametrize("T", [30, 400])
+def test_lora_in_place_apart_and_empty(T):
+    v, ids, scales, base, dbase, dy = _draw(T, 136, 200, 5, 16, "mixed", 4, True)
+    want = m.moe_lora(**v, adapter_ids=ids, scales=scales, base=base)
+    b2 = base.clone()
+    assert m.moe_lora(**v, adapter_ids=ids, scales=scales, base=b2, out=b2)["out"] is b2
+    assert torch.equal(b2, want["out"])
+    back = m.moe_lora_backward(dy, v["x"], want["v"], v["a"], v["b"], ids, base=dbase)
+    d2 = dbase.clone()
+    m.moe_lora_backward(dy, v["x"], want["v"], v["a"], v["b"], ids, base=d2, dx=d2)
+    assert torch.equal(d2, back["dx"])
+    # a row's NaN stays in its row, and with its adapter
+    x = v["x"].clone()
+    x[2] = float("nan")
+    got = m.moe_lora(x, v["a"], v["b"], ids, scales=scales, base=base)["out"]
+    rest = [t for t in range(T) if t != 2]
+    assert torch.equal(got[rest], want["out"][rest])
+    ids2 = ids.clone()
+    ids2[0], ids2[1] = -1, 3
+    a = v["a"].clone()
+    a[3] = float("inf")
+    got = m.moe_lora(v["x"], a, v["b"], ids2, base=base)["out"]
+    assert torch.equal(got[ids2 == -1], base[ids2 == -1])
+    assert torch.isfinite(got[ids2 != 3]).all() and not torch.isfinite(got[1]).all()
+    # around the outputs nothing is written
+    buf = torch.full((T * 200 + 4096,), 7.0, dtype=BF, device="cuda")
+    vb = torch.full((T * 16 + 4096,), 7.0, device="cuda")
+    m.moe_lora(**v, adapter_ids=ids, scales=scales, base=base,
+               out=buf[2048:2048 + T * 200].view(T, 200), v=vb[2048:2048 + T * 16].view(T, 16))
+    assert torch.equal(buf[2048:2048 + T * 200].view(T, 200), want["out"])
+    for t, k in ((buf, T * 200), (vb, T * 16)):
+        assert (t[:2048] == 7).all() and (t[2048 + k:] == 7).all()
+    # no rows
+    e, i0 = torch.empty(0, 136, dtype=BF, device="cuda"), ids[:0]
+    assert m.moe_lora(e, v["a"], v["b"], i0)["out"].shape == (0, 200)
+    z = m.moe_lora_backward(torch.empty(0, 200, dtype=BF, device="cuda"), e,
+                            torch.empty(0, 16, device="cuda"), v["a"], v["b"], i0)
+    assert (z["da"] == 0).all() and (z["db"] == 0).all()
+    assert m.moe_get_error() == 0
+
+
+@pytest.mark.parametrize("T", [30, 400])
+def test_lora_on_another_stream_and_in_a_graph(T):
+    v, ids, scales, base, dbase, dy = _draw(T, 256, 328, 5, 16, "mixed", 4, False)
+    want = m.moe_lora(**v, adapter_ids=ids, scales=scales, base=base)
+    back = m.moe_lora_backward(dy, v["x"], want["v"], v["a"], v["b"], ids, scales=scales,
+                               base=dbase)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = m.moe_lora(**v, adapter_ids=ids, scales=scales, base=base, stream=s)
+    s.synchronize()
+    assert torch.equal(got["out"], want["out"]) and torch.equal(got["v"], want["v"])
+    live = ids.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        plan = m.moe_lora_plan(live, 5)
+        f = m.moe_lora(**v, adapter_ids=live, plan=plan, scales=scales, base=base)
+        b = m.moe_lora_backward(dy, v["x"], f["v"], v["a"], v["b"], live, plan=plan,
+                                scales=scales, base=dbase)
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    for key in want:
+        assert torch.equal(f[key], want[key]), key
+    for key in back:
+        assert torch.equal(b[key], back[key]), key
+    live.copy_(ids.flip(0))                        # other adapters at the replay
+    g.replay()
+    again = m.moe_lora(**v, adapter_ids=live, scales=scales, base=base)
+    assert torch.equal(f["out"], again["out"])
+    assert m.moe_get_error() == 0
+
+
+def test_lora_refusals():
+    v, ids, scales, base, _, dy = _draw(10, 64, 72, 4, 8, "mixed", 3, True)
+    with pytest.raises(ValueError, match="adapter_ids"):
+        m.moe_lora(**v, adapter_ids=ids[:5])
+    with pytest.raises(ValueError, match="adapter_ids"):
+        m.moe_lora(**v, adapter_ids=ids.long())
+    with pytest.raises(ValueError, match="offsets"):
+        m.moe_lora(**v, adapter_ids=ids, plan=(ids, ids))
+    with pytest.raises(ValueError, match="a must"):
+        m.moe_lora(v["x"][:, :56].contiguous(), v["a"], v["b"], ids)
+    with pytest.raises(ValueError, match="scales"):
+        m.moe_lora(**v, adapter_ids=ids, scales=scales[:2])
+    with pytest.raises(ValueError, match="base"):
+        m.moe_lora(**v, adapter_ids=ids, base=base[:, :64].contiguous())
+    with pytest.raises(m.MoeError, match="unsupported"):
+        m.moe_lora(v["x"], torch.zeros(1, 200, 64, dtype=BF, device="cuda"),
+                   torch.zeros(1, 200, 72, dtype=BF, device="cuda"), ids)
+    with pytest.raises(m.MoeError, match="unsupported"):
+        m.moe_lora(v["x"], v["a"], v["b"][:, :, :70].contiguous(), ids)
+    f = m.moe_lora(**v, adapter_ids=ids)
+    with pytest.raises(ValueError, match="accumulate"):
+        m.moe_lora_backward(dy, v["x"], f["v"], v["a"], v["b"], ids, accumulate=True)
+    with pytest.raises(ValueError, match="v must"):
+        m.moe_lora_backward(dy, v["x"], f["v"][:, :4].contiguous(), v["a"], v["b"], ids)
