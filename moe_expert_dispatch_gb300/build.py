@@ -22,7 +22,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe_gb300.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["route.cu", "gemm_bf16.cu", "gemm_mxfp8.cu", "capi.cu", "counts_static.cu", "gate.cu",
-           "norm.cu", "norm_ring.cu", "clip.cu", "ffn.cu", "lora.cu", "dropout.cu"]
+           "norm.cu", "norm_ring.cu", "clip.cu", "ffn.cu", "ffn_rows.cu", "lora.cu", "dropout.cu"]
 
 
 def nvcc() -> str:

@@ -22,7 +22,9 @@
 // piece lies outside, left out). What the epilogues read besides the
 // accumulator (A_g and A_u, or add) arrives by TMA in pieces of 32 rows x 32
 // columns, one step ahead.
+#include "act.cuh"
 #include "common.cuh"
+#include "ffn.h"
 #include "internal.h"
 
 namespace moe {
@@ -109,44 +111,6 @@ __device__ __forceinline__ Tile decode(int t, const Args& p) {
   r.n = local / rows;
   r.m = g * p.group + local - r.n * rows;
   return r;
-}
-
-// ------------------------------------------------------------------ activations
-
-// act(z); all of them hand a NaN on.
-template <int kAct>
-__device__ __forceinline__ float act_f(float z) {
-  if (kAct == MOE_ACT_SILU) return silu_f(z);
-  if (kAct == MOE_ACT_GELU) return 0.5f * z * erfcf(-0.70710678118654752f * z);
-  if (kAct == MOE_ACT_GELU_TANH) {
-    // (1 + tanh u) / 2 = 1 / (1 + e^-2u); past |z| = 16 it is 0 or 1 in float
-    const float c = fminf(fmaxf(z, -16.0f), 16.0f);
-    return z * sigmoid_f(c * (1.5957691216057308f + 0.07135481282742977f * c * c));
-  }
-  return z <= 0.0f ? 0.0f : z;
-}
-
-// act(z) and act'(z).
-template <int kAct>
-__device__ __forceinline__ void act_both(float z, float& f, float& d) {
-  if (kAct == MOE_ACT_SILU) {
-    const float s = sigmoid_f(z);
-    f = z * s;
-    d = s * (1.0f + z * (1.0f - s));
-  } else if (kAct == MOE_ACT_GELU) {
-    const float c = 0.5f * erfcf(-0.70710678118654752f * z);
-    f = z * c;
-    d = c + z * 0.39894228040143268f * __expf(-0.5f * z * z);
-  } else if (kAct == MOE_ACT_GELU_TANH) {
-    const float c = fminf(fmaxf(z, -16.0f), 16.0f);
-    const float s = sigmoid_f(c * (1.5957691216057308f + 0.07135481282742977f * c * c));
-    f = z * s;
-    d = s + c * s * (1.0f - s) * (1.5957691216057308f + 0.21406443848228931f * c * c);
-    if (z != z) d = z;
-  } else {
-    f = z <= 0.0f ? 0.0f : z;
-    d = z <= 0.0f ? 0.0f : z > 0.0f ? 1.0f : z;
-  }
 }
 
 // 32 accumulator columns of A_g and A_u -> 16 words of h.
@@ -612,6 +576,11 @@ moe_status moe_gated_ffn(const void* x, const void* w_gate, const void* w_up, co
   if (!workspace || ws_bytes < moe_gated_ffn_workspace_size(T, H, F) || !aligned16(workspace))
     return MOE_ERR_WORKSPACE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (T <= kFewRows)
+    return ffn_few_rows(x, w_gate, w_up, w_down, add, static_cast<int>(T), H, F, act, y, a_gate,
+                        a_up, workspace, device_error_word(), st) == cudaSuccess
+               ? MOE_OK
+               : MOE_ERR_CUDA;
   Args p{};
   p.act = act;
   p.err = device_error_word();
