@@ -825,21 +825,24 @@ moe_status moe_lora_plan(const int32_t* adapter_ids, int64_t T, int n, int32_t* 
  *  base    bf16 [T, N] or NULL (0): the projection's result
  *  out     bf16 [T, N]   out; may be base itself
  *  v       float [T, r]  out: what the backward needs
+ *  workspace >= moe_lora_workspace_size(T, n, r) bytes, 16-byte aligned; 0 bytes,
+ *          and NULL allowed, for the few rows that need none
  * 1 <= r <= 128, H % 8 == 0 and N % 8 == 0 (else MOE_ERR_UNSUPPORTED), 1 <= n <=
  * 1024, T < 2^31 - 1024. Pointers start on 16 bytes; out and v overlap nothing
  * else of the call (out: base alone, and then as a whole). T = 0 does nothing.
  * ------------------------------------------------------------------------ */
+size_t moe_lora_workspace_size(int64_t T, int n, int r);
 moe_status moe_lora(const void* x, const void* a, const void* b, const int32_t* adapter_ids,
                     const int32_t* order, const int32_t* offsets, const float* scales,
                     const void* base, int64_t T, int H, int N, int n, int r, void* out, float* v,
-                    void* stream);
+                    void* workspace, size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
  * moe_lora_backward - the gradients of moe_lora (that of base is dy itself):
  *   dv_t = s_a B_a dy_t (float),   dx_t = bf16(base_t + A_a^T dv_t)
  *   dA_a = sum_t dv_t x_t^T,       dB_a = s_a sum_t v_t dy_t^T (float)
- * over the rows t of adapter a. dv and v enter the products as the sum of two
- * bf16 numbers.
+ * over the rows t of adapter a. dv enters dx as the sum of two bf16 numbers, dv and
+ * v enter the others as that of three (24 bits).
  *
  *  dy      bf16 [T, N];  x, a, b, order, offsets, scales: the forward's
  *  v       float [T, r] as the forward wrote it
@@ -847,10 +850,10 @@ moe_status moe_lora(const void* x, const void* a, const void* b, const int32_t* 
  *  dx      bf16 [T, H]   out; may be base itself
  *  da      float [n, r, H], db  float [n, r, N]   out; added to what is there
  *          when accumulate. An adapter without rows gets 0 (or is left)
- *  workspace >= moe_lora_backward_workspace_size(T, r) bytes, 16-byte aligned
+ *  workspace >= moe_lora_backward_workspace_size(T, n, r) bytes, 16-byte aligned
  * Limits as moe_lora. T = 0 writes zero gradients (or leaves them).
  * ------------------------------------------------------------------------ */
-size_t moe_lora_backward_workspace_size(int64_t T, int r);
+size_t moe_lora_backward_workspace_size(int64_t T, int n, int r);
 moe_status moe_lora_backward(const void* dy, const void* x, const float* v, const void* a,
                              const void* b, const int32_t* order, const int32_t* offsets,
                              const float* scales, const void* base, int64_t T, int H, int N, int n,

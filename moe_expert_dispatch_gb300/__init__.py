@@ -145,9 +145,10 @@ _sig("moe_gated_ffn_backward_workspace_size", _sz, _i64, _i32, _i32)
 _sig("moe_gated_ffn_backward", _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32,
      _i32, _vp, _vp, _vp, _vp, _i32, _i32, _vp, _sz, _vp)
 _sig("moe_lora_plan", _i32, _vp, _i64, _i32, _vp, _vp, _vp)
+_sig("moe_lora_workspace_size", _sz, _i64, _i32, _i32)
 _sig("moe_lora", _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i32, _vp,
-     _vp, _vp)
-_sig("moe_lora_backward_workspace_size", _sz, _i64, _i32)
+     _vp, _vp, _sz, _vp)
+_sig("moe_lora_backward_workspace_size", _sz, _i64, _i32, _i32)
 _sig("moe_lora_backward", _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32,
      _i32, _i32, _vp, _vp, _vp, _i32, _vp, _sz, _vp)
 _sig("moe_dropout_config_init", None, ctypes.POINTER(moe_dropout_config))
@@ -1103,9 +1104,23 @@ _ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}
 
 
 def _act(act):
-    if act not in _ACTS:
+    code = _ACTS.get(act)
+    if code is None:
         raise ValueError(f"act must be one of {sorted(_ACTS)}, got {act!r}")
-    return _ACTS[act]
+    return code
+
+
+def _all_fit(dev, *named):
+    """Checks (tensor or None, name, shape, dtype) on dev; the messages are made
+    only where something is wrong."""
+    index = dev.index
+    for t, name, shape, dtype in named:
+        if t is not None and (t.shape != shape or t.dtype is not dtype or t.get_device() != index
+                              or not t.is_contiguous()):
+            _cuda(t, name, dtype)
+            _shaped(t, name, *shape)
+            raise ValueError(f"{name} is on {t.device} but the call's first tensor on {dev}: "
+                             "all tensors of a call must share one device")
 
 
 def _made(t, shape, dtype, dev):
@@ -1113,17 +1128,18 @@ def _made(t, shape, dtype, dev):
     return torch.empty(shape, dtype=dtype, device=dev) if t is None else t
 
 
-def _ffn_weights(dev, H, w_gate, w_up, w_down):
-    """F, of w_gate and w_up [H, F] and w_down [F, H]."""
-    bf16 = torch.bfloat16
-    _fit(dev, (w_gate, "w_gate", bf16, 0), (w_up, "w_up", bf16, 0), (w_down, "w_down", bf16, 0))
-    if w_gate.dim() != 2:
-        raise ValueError(f"w_gate must have shape [{H}, F], got {list(w_gate.shape)}")
-    F = w_gate.shape[1]
-    _shaped(w_gate, "w_gate", H, F)
-    _shaped(w_up, "w_up", H, F)
-    _shaped(w_down, "w_down", F, H)
-    return F
+def _space(workspace, query, dev, *sizes):
+    """(the given workspace or a new one, its bytes)."""
+    if workspace is not None:
+        return _scratch(workspace, 0, dev)
+    return _scratch(None, query(*sizes), dev)
+
+
+def _matrix(t, name):
+    """The shape of a tensor that has to have two dimensions."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, got {list(t.shape)}")
+    return t.shape
 
 
 def moe_gated_ffn(x, w_gate, w_up, w_down, act="silu", add=None, save_for_backward=False, y=None,
@@ -1135,22 +1151,23 @@ def moe_gated_ffn(x, w_gate, w_up, w_down, act="silu", add=None, save_for_backwa
     dict(y, a_gate, a_up); a_gate = x w_gate and a_up = x w_up (bf16 [T, F]) are
     kept with save_for_backward, else None. y may be add itself. H and F are
     multiples of 8, tensors start on 16 bytes."""
-    if _elsewhere(stream):
+    if stream is not None and _elsewhere(stream):
         return _within(stream, moe_gated_ffn, locals())
-    bf16 = torch.bfloat16
-    T, H = x.shape
-    dev = x.device
-    _fit(dev, (x, "x", bf16, 0))
-    F = _ffn_weights(dev, H, w_gate, w_up, w_down)
-    _shaped(add, "add", T, H)
+    bf16, dev = torch.bfloat16, x.device
+    T, H = rows = _matrix(x, "x")
+    wide = _matrix(w_gate, "w_gate")
+    F = wide[1]
+    if y is None:
+        y = torch.empty(rows, dtype=bf16, device=dev)
     if save_for_backward:
         a_gate, a_up = _made(a_gate, (T, F), bf16, dev), _made(a_up, (T, F), bf16, dev)
     else:
         a_gate = a_up = None
-    y = _made(y, (T, H), bf16, dev)
-    _fit(dev, (add, "add", bf16, 0), (y, "y", bf16, T * H), (a_gate, "a_gate", bf16, T * F),
-         (a_up, "a_up", bf16, T * F))
-    ws, ws_bytes = _scratch(workspace, _lib.moe_gated_ffn_workspace_size(T, H, F), dev)
+    _all_fit(dev, (x, "x", rows, bf16), (w_gate, "w_gate", (H, F), bf16),
+             (w_up, "w_up", wide, bf16), (w_down, "w_down", (F, H), bf16),
+             (add, "add", rows, bf16), (y, "y", rows, bf16), (a_gate, "a_gate", (T, F), bf16),
+             (a_up, "a_up", (T, F), bf16))
+    ws, ws_bytes = _space(workspace, _lib.moe_gated_ffn_workspace_size, dev, T, H, F)
     _check(_on(dev, _lib.moe_gated_ffn, x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(),
                w_down.data_ptr(), _ptr(add), T, H, F, _act(act), y.data_ptr(), _ptr(a_gate),
                _ptr(a_up), _ptr(ws), ws_bytes, _raw_stream(stream, dev)), "moe_gated_ffn")
@@ -1167,20 +1184,14 @@ def moe_gated_ffn_backward(dy, x, w_gate, w_up, w_down, a_gate, a_up, act="silu"
     gradients in the type of those given, else in dw_dtype (torch.bfloat16 or
     torch.float32); in float32 they are added to what is there with accumulate_dw;
     None without weight_grads (frozen weights). dx may be add itself."""
-    if _elsewhere(stream):
+    if stream is not None and _elsewhere(stream):
         return _within(stream, moe_gated_ffn_backward, locals())
-    bf16 = torch.bfloat16
-    T, H = x.shape
-    dev = x.device
-    _fit(dev, (x, "x", bf16, 0), (dy, "dy", bf16, 0), (add, "add", bf16, 0),
-         (a_gate, "a_gate", bf16, 0), (a_up, "a_up", bf16, 0))
-    F = _ffn_weights(dev, H, w_gate, w_up, w_down)
-    _shaped(dy, "dy", T, H)
-    _shaped(add, "add", T, H)
-    _shaped(a_gate, "a_gate", T, F)
-    _shaped(a_up, "a_up", T, F)
-    dx = _made(dx, (T, H), bf16, dev)
-    wt = 0
+    bf16, dev = torch.bfloat16, x.device
+    T, H = rows = _matrix(x, "x")
+    F = _matrix(w_gate, "w_gate")[1]
+    if dx is None:
+        dx = torch.empty(rows, dtype=bf16, device=dev)
+    dt, wt = bf16, 0
     if weight_grads:
         given = [t for t in (dw_gate, dw_up, dw_down) if t is not None]
         if accumulate_dw and len(given) != 3:
@@ -1191,12 +1202,14 @@ def moe_gated_ffn_backward(dy, x, w_gate, w_up, w_down, a_gate, a_up, act="silu"
         wt = _TYPES[dt]
         dw_gate, dw_up = _made(dw_gate, (H, F), dt, dev), _made(dw_up, (H, F), dt, dev)
         dw_down = _made(dw_down, (F, H), dt, dev)
-        _fit(dev, (dw_gate, "dw_gate", dt, H * F), (dw_up, "dw_up", dt, H * F),
-             (dw_down, "dw_down", dt, H * F))
     else:
         dw_gate = dw_up = dw_down = None
-    _fit(dev, (dx, "dx", bf16, T * H))
-    ws, ws_bytes = _scratch(workspace, _lib.moe_gated_ffn_backward_workspace_size(T, H, F), dev)
+    _all_fit(dev, (x, "x", rows, bf16), (dy, "dy", rows, bf16), (w_gate, "w_gate", (H, F), bf16),
+             (w_up, "w_up", (H, F), bf16), (w_down, "w_down", (F, H), bf16),
+             (a_gate, "a_gate", (T, F), bf16), (a_up, "a_up", (T, F), bf16),
+             (add, "add", rows, bf16), (dx, "dx", rows, bf16), (dw_gate, "dw_gate", (H, F), dt),
+             (dw_up, "dw_up", (H, F), dt), (dw_down, "dw_down", (F, H), dt))
+    ws, ws_bytes = _space(workspace, _lib.moe_gated_ffn_backward_workspace_size, dev, T, H, F)
     _check(_on(dev, _lib.moe_gated_ffn_backward, dy.data_ptr(), x.data_ptr(), w_gate.data_ptr(),
                w_up.data_ptr(), w_down.data_ptr(), a_gate.data_ptr(), a_up.data_ptr(), _ptr(add),
                T, H, F, _act(act), dx.data_ptr(), _ptr(dw_gate), _ptr(dw_up), _ptr(dw_down), wt,
@@ -1210,16 +1223,16 @@ def moe_lora_plan(adapter_ids, n, order=None, offsets=None, stream=None):
     adapter_ids int32 [T], -1 for a row without one. Adapter a has the rows
     order[offsets[a]:offsets[a + 1]] in their own order; those without one come
     last. One plan serves every projection and layer of the batch."""
-    if _elsewhere(stream):
+    if stream is not None and _elsewhere(stream):
         return _within(stream, moe_lora_plan, locals())
     dev = adapter_ids.device
     if adapter_ids.dim() != 1:
         raise ValueError(f"adapter_ids must have shape [T], got {list(adapter_ids.shape)}")
-    T = adapter_ids.shape[0]
-    order = _made(order, (T,), torch.int32, dev)
-    offsets = _made(offsets, (max(n, 0) + 1,), torch.int32, dev)
-    _fit(dev, (adapter_ids, "adapter_ids", torch.int32, 0), (order, "order", torch.int32, T),
-         (offsets, "offsets", torch.int32, n + 1))
+    T, i32 = adapter_ids.shape[0], torch.int32
+    order = _made(order, (T,), i32, dev)
+    offsets = _made(offsets, (max(n, 0) + 1,), i32, dev)
+    _all_fit(dev, (adapter_ids, "adapter_ids", (T,), i32), (order, "order", (T,), i32),
+             (offsets, "offsets", (max(n, 0) + 1,), i32))
     _check(_on(dev, _lib.moe_lora_plan, adapter_ids.data_ptr(), T, n, order.data_ptr(),
                offsets.data_ptr(), _raw_stream(stream, dev)), "moe_lora_plan")
     return order, offsets
@@ -1227,23 +1240,23 @@ def moe_lora_plan(adapter_ids, n, order=None, offsets=None, stream=None):
 
 def _lora_operands(dev, T, a, b, adapter_ids, plan, scales):
     """(n, r, H, N, order, offsets) of a [n, r, H] and b [n, r, N]."""
-    if a.dim() != 3 or b.dim() != 3 or a.shape[:2] != b.shape[:2]:
+    if a.dim() != 3 or b.dim() != 3:
         raise ValueError("a and b must have shapes [n, r, H] and [n, r, N], got "
                          f"{list(a.shape)} and {list(b.shape)}")
     n, r, H = a.shape
-    _fit(dev, (a, "a", torch.bfloat16, 0), (b, "b", torch.bfloat16, 0),
-         (adapter_ids, "adapter_ids", torch.int32, 0), (scales, "scales", torch.float32, 0))
-    _shaped(adapter_ids, "adapter_ids", T)
-    _shaped(scales, "scales", n)
+    N, bf16, i32 = b.shape[2], torch.bfloat16, torch.int32
+    if b.shape != (n, r, N):
+        raise ValueError("a and b must have shapes [n, r, H] and [n, r, N], got "
+                         f"{list(a.shape)} and {list(b.shape)}")
+    _all_fit(dev, (a, "a", (n, r, H), bf16), (b, "b", (n, r, N), bf16),
+             (adapter_ids, "adapter_ids", (T,), i32), (scales, "scales", (n,), torch.float32))
     order, offsets = moe_lora_plan(adapter_ids, n) if plan is None else plan
-    _fit(dev, (order, "order", torch.int32, 0), (offsets, "offsets", torch.int32, 0))
-    _shaped(order, "order", T)
-    _shaped(offsets, "offsets", n + 1)
-    return n, r, H, b.shape[2], order, offsets
+    _all_fit(dev, (order, "order", (T,), i32), (offsets, "offsets", (n + 1,), i32))
+    return n, r, H, N, order, offsets
 
 
 def moe_lora(x, a, b, adapter_ids, plan=None, scales=None, base=None, out=None, v=None,
-             stream=None):
+             workspace=None, stream=None):
     """Low-rank adapters beside a shared projection: for row t with adapter i =
     adapter_ids[t], v_t = a[i] x_t and out_t = base_t + scales[i] * b[i]^T v_t. x
     bf16 [T, H], a bf16 [n, r, H], b bf16 [n, r, N] (rank first in both),
@@ -1252,22 +1265,24 @@ def moe_lora(x, a, b, adapter_ids, plan=None, scales=None, base=None, out=None, 
     bf16 [T, N] (the projection's result) or None (0). Returns dict(out bf16 [T,
     N], v float32 [T, r]), v for the backward. out may be base itself. r is 1 to
     128, H and N are multiples of 8, tensors start on 16 bytes."""
-    if _elsewhere(stream):
+    if stream is not None and _elsewhere(stream):
         return _within(stream, moe_lora, locals())
-    bf16 = torch.bfloat16
-    T, H = x.shape
-    dev = x.device
+    bf16, f32, dev = torch.bfloat16, torch.float32, x.device
+    T, H = rows = _matrix(x, "x")
     n, r, ha, N, order, offsets = _lora_operands(dev, T, a, b, adapter_ids, plan, scales)
     if ha != H:
         raise ValueError(f"a must have shape [n, r, {H}], got {list(a.shape)}")
-    _shaped(base, "base", T, N)
-    out, v = _made(out, (T, N), bf16, dev), _made(v, (T, r), torch.float32, dev)
-    _fit(dev, (x, "x", bf16, 0), (base, "base", bf16, 0), (out, "out", bf16, T * N),
-         (v, "v", torch.float32, T * r))
+    if out is None:
+        out = torch.empty((T, N), dtype=bf16, device=dev)
+    if v is None:
+        v = torch.empty((T, r), dtype=f32, device=dev)
+    _all_fit(dev, (x, "x", rows, bf16), (base, "base", (T, N), bf16), (out, "out", (T, N), bf16),
+             (v, "v", (T, r), f32))
+    ws, ws_bytes = _space(workspace, _lib.moe_lora_workspace_size, dev, T, n, r)
     _check(_on(dev, _lib.moe_lora, x.data_ptr(), a.data_ptr(), b.data_ptr(),
                adapter_ids.data_ptr(), order.data_ptr(), offsets.data_ptr(), _ptr(scales),
-               _ptr(base), T, H, N, n, r, out.data_ptr(), v.data_ptr(), _raw_stream(stream, dev)),
-           "moe_lora")
+               _ptr(base), T, H, N, n, r, out.data_ptr(), v.data_ptr(), _ptr(ws), ws_bytes,
+               _raw_stream(stream, dev)), "moe_lora")
     return dict(out=out, v=v)
 
 
@@ -1278,36 +1293,28 @@ def moe_lora_backward(dy, x, v, a, b, adapter_ids, plan=None, scales=None, base=
     the forward's; base (bf16 [T, H] or None) is what reaches x by the projection
     and joins dx. With accumulate da and db are added to what the given tensors
     hold. dx may be base itself. base's own gradient in the forward is dy."""
-    if _elsewhere(stream):
+    if stream is not None and _elsewhere(stream):
         return _within(stream, moe_lora_backward, locals())
-    bf16, f32 = torch.bfloat16, torch.float32
-    T, H = x.shape
-    dev = x.device
+    bf16, f32, dev = torch.bfloat16, torch.float32, x.device
+    T, H = rows = _matrix(x, "x")
     n, r, ha, N, order, offsets = _lora_operands(dev, T, a, b, adapter_ids, plan, scales)
     if ha != H:
         raise ValueError(f"a must have shape [n, r, {H}], got {list(a.shape)}")
     if accumulate and (da is None or db is None):
         raise ValueError("accumulate adds to da and db: pass them")
-    _shaped(dy, "dy", T, N)
-    _shaped(v, "v", T, r)
-    _shaped(base, "base", T, H)
     dx = _made(dx, (T, H), bf16, dev)
     da, db = _made(da, (n, r, H), f32, dev), _made(db, (n, r, N), f32, dev)
-    _fit(dev, (x, "x", bf16, 0), (dy, "dy", bf16, 0), (v, "v", f32, 0), (base, "base", bf16, 0),
-         (dx, "dx", bf16, T * H), (da, "da", f32, n * r * H), (db, "db", f32, n * r * N))
-    ws, ws_bytes = _scratch(workspace, _lib.moe_lora_backward_workspace_size(T, r), dev)
+    _all_fit(dev, (x, "x", rows, bf16), (dy, "dy", (T, N), bf16), (v, "v", (T, r), f32),
+             (base, "base", rows, bf16), (dx, "dx", rows, bf16), (da, "da", (n, r, H), f32),
+             (db, "db", (n, r, N), f32))
+    ws, ws_bytes = _scratch(workspace, 0 if workspace is not None else _on(
+        dev, _lib.moe_lora_backward_workspace_size, T, n, r), dev)
     _check(_on(dev, _lib.moe_lora_backward, dy.data_ptr(), x.data_ptr(), v.data_ptr(),
                a.data_ptr(), b.data_ptr(), order.data_ptr(), offsets.data_ptr(), _ptr(scales),
                _ptr(base), T, H, N, n, r, dx.data_ptr(), da.data_ptr(), db.data_ptr(),
                bool(accumulate), _ptr(ws), ws_bytes, _raw_stream(stream, dev)),
            "moe_lora_backward")
     return dict(dx=dx, da=da, db=db)
-
-
-def _rng(rng, dev):
-    _fit(dev, (rng, "rng", torch.int64, 2))
-    _shaped(rng, "rng", 2)
-    return rng.data_ptr()
 
 
 def moe_dropout_residual(y, rng, p, x=None, residual_scale=1.0, branch_scale=1.0, out=None,
@@ -1320,15 +1327,15 @@ def moe_dropout_residual(y, rng, p, x=None, residual_scale=1.0, branch_scale=1.0
     the result's type, without x there is no residual and the result has y's
     type (or out's). p, in [0, 1), is taken to the nearest 1/65536 and the factor
     is that one's. out may be x itself."""
-    if _elsewhere(stream):
+    if stream is not None and _elsewhere(stream):
         return _within(stream, moe_dropout_residual, locals())
-    bt = _typed(y, "y")
-    dev = y.device
-    _shaped(x, "x", *y.shape)
-    out = _made(out, y.shape, (y if x is None else x).dtype, dev)
+    bt, dev, shape = _typed(y, "y"), y.device, y.shape
+    if out is None:
+        out = torch.empty(shape, dtype=(y if x is None else x).dtype, device=dev)
     st = _typed(out, "out")
-    _fit(dev, (y, "y", y.dtype, 0), (x, "x", out.dtype, 0), (out, "out", out.dtype, y.numel()))
-    _check(_on(dev, _lib.moe_dropout_residual, y.data_ptr(), _ptr(x), y.numel(), _rng(rng, dev),
+    _all_fit(dev, (y, "y", shape, y.dtype), (x, "x", shape, out.dtype),
+             (out, "out", shape, out.dtype), (rng, "rng", (2,), torch.int64))
+    _check(_on(dev, _lib.moe_dropout_residual, y.data_ptr(), _ptr(x), y.numel(), rng.data_ptr(),
                moe_dropout_config(p, residual_scale, branch_scale, st, bt), out.data_ptr(),
                _raw_stream(stream, dev)), "moe_dropout_residual")
     return out
@@ -1340,20 +1347,19 @@ def moe_dropout_residual_backward(d_out, rng, p, residual=True, residual_scale=1
     """Gradients of moe_dropout_residual by the same rng, p and scales: dict(dx,
     dy), dy of dy's type or branch_dtype, dx of d_out's type, or None without a
     residual. dx may be d_out itself."""
-    if _elsewhere(stream):
+    if stream is not None and _elsewhere(stream):
         return _within(stream, moe_dropout_residual_backward, locals())
-    st = _typed(d_out, "d_out")
-    dev = d_out.device
+    st, dev, shape = _typed(d_out, "d_out"), d_out.device, d_out.shape
     if dy is None:
-        dy = torch.empty(d_out.shape, dtype=branch_dtype, device=dev)
+        dy = torch.empty(shape, dtype=branch_dtype, device=dev)
     bt = _typed(dy, "dy")
     if not residual:
         dx = None
     elif dx is None:
-        dx = torch.empty_like(d_out)
-    _fit(dev, (d_out, "d_out", d_out.dtype, 0), (dx, "dx", d_out.dtype, d_out.numel()),
-         (dy, "dy", dy.dtype, d_out.numel()))
+        dx = torch.empty(shape, dtype=d_out.dtype, device=dev)
+    _all_fit(dev, (d_out, "d_out", shape, d_out.dtype), (dx, "dx", shape, d_out.dtype),
+             (dy, "dy", shape, dy.dtype), (rng, "rng", (2,), torch.int64))
     _check(_on(dev, _lib.moe_dropout_residual_backward, d_out.data_ptr(), d_out.numel(),
-               _rng(rng, dev), moe_dropout_config(p, residual_scale, branch_scale, st, bt),
+               rng.data_ptr(), moe_dropout_config(p, residual_scale, branch_scale, st, bt),
                _ptr(dx), dy.data_ptr(), _raw_stream(stream, dev)), "moe_dropout_residual_backward")
     return dict(dx=dx, dy=dy)

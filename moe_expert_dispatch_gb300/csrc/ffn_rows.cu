@@ -68,14 +68,6 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr, uint32_t rank)
   return v;
 }
 
-__device__ __forceinline__ void grid_dependency_wait() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
-__device__ __forceinline__ void grid_dependents_launch() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
 __device__ __forceinline__ float act_any(int act, float z) {
   switch (act) {
     case MOE_ACT_SILU: return act_f<MOE_ACT_SILU>(z);
@@ -140,7 +132,7 @@ __global__ void __launch_bounds__(kThreads)
       const int first = min(S, kb1 - kb0);
       for (int i = 0; i < first; ++i) load_w(kb0 + i, i);
       grid_dependency_wait();
-      asm volatile("fence.proxy.async;" ::: "memory");
+      fence_proxy_async();
       for (int i = 0; i < first; ++i) load_x(kb0 + i, i);
       int stage = first == S ? 0 : first;
       uint32_t phase = first == S ? 1 : 0;

@@ -167,6 +167,10 @@ struct GroupedGemmArgs {
 // Encodes a 2D bf16 tensor map with the 128-byte swizzle (box inner = 64).
 bool make_tmap_bf16_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,
                        uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_outer);
+// The same of a contiguous [outer, mid, inner] tensor, with boxes of one outer index:
+// rows past mid are zeros, not the next matrix's.
+bool make_tmap_bf16_3d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t mid,
+                       uint64_t outer, uint32_t box_inner, uint32_t box_mid);
 
 // Output tensor maps of a grouped GEMM's epilogue: boxes of 32 rows x 64
 // bytes with the 64-byte swizzle (see make_out_tmap). Unused maps may repeat

@@ -3,22 +3,28 @@
 //
 // With A and B both stored rank-major ([n, r, H] and [n, r, N]), forward and
 // backward need three products only, each over the rows of one adapter:
-//   shrink  V[t, j]   = s sum_c in[t, c] P[j, c]      v from x, A; dv from dy, B
-//   expand  out[t, c] = base[t, c] + sum_j V[t, j] Q[j, c]   out from v, B; dx from dv, A
-//   grad    G[j, c]   = sum_t V[t, j] in[t, c]        dA from dv, x; dB from v, dy
-// The rank is at most 128 and the widths are thousands, so all three are bound
-// by the rows that they read and write. The products go through mma.sync
-// m16n8k16: a tile of 64 rows and one adapter's rank fills it as it is, where a
-// tcgen05 tile would be mostly padding, and its rate is far above what the
-// memory delivers.
+//   shrink  V[t, j]   = sum_c in[t, c] P[j, c]              v from x, A; dv from dy, B
+//   expand  out[t, c] = base[t, c] + sum_j s V[t, j] Q[j, c]   out from v, B; dx from dv, A
+//   grad    G[j, c]   = sum_t s V[t, j] in[t, c]            dA from dv, x; dB from v, dy
+// The widths are thousands and the rank is at most 128, so all three are bound by
+// the rows that they read and write; the products go through tcgen05.mma, which
+// leaves the SMs to move rows.
 //
-// V is float. Where it enters a product it is the sum of two bf16 numbers, 16
-// bits of its 24 (rounding to one would cost as much as rounding the result to
-// bf16 once more). Sums over long axes leave the tensor cores every 64 terms and
-// are added up in float registers, because the accumulation there truncates.
+// Rows are taken in the order of the plan, 128 of one adapter at a time (a unit).
+// A plan comes from the caller: every row number is checked against T before use.
 //
-// Rows are taken in the order of the plan, 64 of one adapter at a time. A plan
-// comes from the caller: every row number is checked against T before use.
+// V is float. Where it enters a product it is a sum of bf16 numbers: two of them
+// (16 bits) for expand, whose result is rounded to bf16, and three (24 bits) for
+// grad, whose result is float. The shrink kernel writes them as images: a unit's
+// [128, 64] or [128, 128] values of a part, in the swizzled order in which the
+// tensor cores read shared memory, so that one bulk copy brings a part, as a
+// K-major operand to expand and as an MN-major one to grad. Rows past the end of an
+// adapter are zeros there.
+//
+// The tensor cores add their products up in float but cut off what does not fit;
+// over thousands of terms that bias shows in float results. So shrink and grad
+// take their accumulators out of tensor memory every 64 terms and add them up in
+// float registers, which round.
 #include <string.h>
 
 #include "common.cuh"
@@ -30,33 +36,16 @@ int* device_error_word();
 
 namespace {
 
-constexpr int kRows = 64;           // rows of a block: one adapter's
+constexpr int kRows = 128;          // rows of a unit: one adapter's
 constexpr int kMaxAdapters = 1024;
 constexpr int kMaxRank = 128;
-
-// ------------------------------------------------------------------ mma.sync
-
-__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t* r) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-
-__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t* r) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-
-__device__ __forceinline__ void mma_bf16(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
+constexpr unsigned long long kDrainNs = 1000000000ull;
+constexpr int kAtom = kRows * 128;  // 16 KB: 128 rows x 64 columns of an image or a tile
+// 64-wide atoms of a part of an image, and bytes of a part
+template <int R>
+constexpr int atoms() { return R > 64 ? 2 : 1; }
+template <int R>
+constexpr int part_bytes() { return atoms<R>() * kAtom; }
 
 // 16 bytes global -> shared, or 16 zero bytes where ok is false (src is then
 // any valid address and nothing is read).
@@ -80,12 +69,30 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr, uint32_t rank) {
   return v;
 }
 
-// v = hi + lo in bf16, packed by pairs; what is not finite is in hi alone.
-__device__ __forceinline__ void split2(float v0, float v1, uint32_t& hi, uint32_t& lo) {
-  hi = pack_bf16x2(v0, v1);
-  const float h0 = __uint_as_float(hi << 16), h1 = __uint_as_float(hi & 0xFFFF0000u);
-  const float l0 = v0 - h0, l1 = v1 - h1;
-  lo = pack_bf16x2(fabsf(h0) < INFINITY ? l0 : 0.0f, fabsf(h1) < INFINITY ? l1 : 0.0f);
+// The next bf16 part of two values, packed; what is left of them stays. What is not
+// finite is in the first part alone.
+__device__ __forceinline__ uint32_t take_part(float& v0, float& v1) {
+  const uint32_t w = pack_bf16x2(v0, v1);
+  const float h0 = __uint_as_float(w << 16), h1 = __uint_as_float(w & 0xFFFF0000u);
+  v0 = fabsf(h0) < INFINITY ? v0 - h0 : 0.0f;
+  v1 = fabsf(h1) < INFINITY ? v1 - h1 : 0.0f;
+  return w;
+}
+
+__device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// R consecutive accumulator columns of this lane added to sum.
+template <int R>
+__device__ __forceinline__ void add_columns(uint32_t taddr, float* sum) {
+#pragma unroll
+  for (int c = 0; c < R; c += 16) {
+    uint32_t v[16];
+    tmem_ld_32x32b_x16(taddr + c, v);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) sum[c + i] += __uint_as_float(v[i]);
+  }
 }
 
 // ------------------------------------------------------------------ plan
@@ -116,13 +123,13 @@ __device__ __forceinline__ int plan_row(const Plan& p, int i) {
   return -1;
 }
 
-struct Block { int a, lo, rows; };   // adapter, first entry of the order, rows (0: none)
+struct Unit { int a, lo, rows; };   // adapter, first entry of the order, rows (0: none)
 
-// Block u of the batch: the adapters' blocks one after the other, those without an
-// adapter last. Called by a whole warp.
-__device__ __forceinline__ Block find_block(const Plan& p, int u) {
+// Unit u of the batch: the adapters' units one after the other, those of rows without
+// an adapter last. Called by a whole warp.
+__device__ __forceinline__ Unit find_unit(const Plan& p, int u) {
   const int lane = lane_id();
-  Block b = {-1, 0, 0};
+  Unit b = {-1, 0, 0};
   int before = 0;
   for (int a0 = 0; a0 <= p.n; a0 += 32) {
     int lo = 0, hi = 0;
@@ -223,443 +230,801 @@ __global__ void __launch_bounds__(1024, 1)
 
 // ------------------------------------------------------------------ shrink
 
-// x tile and P tile: rows of 64 columns (128 bytes), 16-byte chunk c of row i at c ^ (i & 7).
+// A cluster takes a unit, each of its CTAs a run of 64-wide k-blocks; the sums are
+// added over the cluster in the order of the ranks, and each CTA splits and writes
+// its share. Warps: 0 loads P by TMA, 1 issues the MMAs, then 4 (a quarter of the
+// accumulators' rows each) or 8 (and half of their columns) drain the accumulators,
+// and 4 gather the rows (cp.async, 128 bytes a row and k-block).
 template <int R>
 struct Shrink {
   static constexpr int kStages = 4;
-  static constexpr int kX = kRows * 128, kP = R * 128;
-  static constexpr int kStage = kX + kP;
-  static constexpr int kPartial = kRows * R * 4;
-  static constexpr int kBytes = kStages * kStage > kPartial ? kStages * kStage : kPartial;
+  static constexpr int kStage = kAtom + R * 128;
+  static constexpr int kAcc = R > 64 ? 2 : 4;       // accumulators in flight
+  static constexpr int kTmem = R <= 16 ? 64 : R <= 32 ? 128 : 256;
+  static constexpr int kRing = kStages * kStage;
+  static constexpr int kBytes = 1024 + (kRing > kRows * R * 4 ? kRing : kRows * R * 4);
+  static constexpr int kGroups = R > 32 ? 2 : 1;    // draining warps to a quarter of the rows
+  static constexpr int kOwn = R / kGroups;          // columns of such a warp
+  static constexpr int kThreads = 32 * (2 + 4 * kGroups + 4);
 };
 
-// A cluster of CTAs takes a block of rows, each CTA a run of 64-wide k-blocks;
-// their sums are added over the cluster in the order of the ranks. Four warps of
-// 16 rows each.
+struct ShrinkArgs {
+  const __nv_bfloat16* in;     // [T, K]
+  const float* scales;         // or NULL
+  float* V;                    // [T, r] or NULL: the sums, without the scale
+  uint8_t* img;                // images of s V
+  const float* kept;           // [T, r] or NULL: another V that is split as well
+  uint8_t* img_kept;
+  int parts;                   // of each image: 2 or 3
+  int K, r, split;
+  unsigned long long wait_ns;
+  Plan plan;
+};
+
 template <int R>
-__global__ void __launch_bounds__(128)
-    shrink_kernel(const __nv_bfloat16* __restrict__ in, const __nv_bfloat16* __restrict__ P,
-                  const float* __restrict__ scales, float* __restrict__ V, int K, int r, int split,
-                  Plan plan) {
+__global__ void __launch_bounds__(Shrink<R>::kThreads, R > 64 ? 1 : 2)
+    shrink_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ ShrinkArgs p) {
   using S = Shrink<R>;
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ uint8_t smem_raw[];
   __shared__ int rows[kRows];
+  __shared__ uint64_t full[S::kStages], empty[S::kStages], tfull[S::kAcc], tempty[S::kAcc];
+  __shared__ uint32_t tmem_at;
+  __shared__ int stop, zero;
+  uint8_t* ring = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t rank = cluster_ctarank();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const Block blk = find_block(plan, static_cast<int>(blockIdx.x / split));
-  if (tid < kRows) rows[tid] = tid < blk.rows ? plan_row(plan, blk.lo + tid) : -1;
-  __syncthreads();
-  if (blk.rows == 0 || blk.a == plan.n) {       // the whole cluster leaves together
-    if (rank == 0)
-      for (int i = tid; i < blk.rows * r; i += 128)
-        if (rows[i / r] >= 0) V[static_cast<int64_t>(rows[i / r]) * r + i % r] = 0.0f;
+  const int unit = static_cast<int>(blockIdx.x) / p.split;
+  const Unit u = find_unit(p.plan, unit);
+  if (tid < kRows) rows[tid] = tid < u.rows ? plan_row(p.plan, u.lo + tid) : -1;
+  grid_dependents_launch();
+  if (u.rows == 0 || u.a == p.plan.n) {         // the whole cluster leaves together
+    __syncthreads();
+    if (rank == 0 && p.V)
+      for (int i = tid; i < u.rows * p.r; i += S::kThreads)
+        if (rows[i / p.r] >= 0) p.V[static_cast<int64_t>(rows[i / p.r]) * p.r + i % p.r] = 0.0f;
     return;
   }
-  const int kblocks = (K + 63) / 64, per = (kblocks + split - 1) / split;
-  const int kb0 = static_cast<int>(rank) * per, kb1 = min(kblocks, kb0 + per);
-  const __nv_bfloat16* Pa = P + static_cast<int64_t>(blk.a) * r * K;
-  const uint32_t base = smem_u32(smem);
-  // this thread's chunk column and rows of the copies
-  const int ch = tid & 7, r0 = tid >> 3;
-  const __nv_bfloat16* src[4];
-  bool live[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int row = rows[r0 + 16 * i];
-    live[i] = row >= 0;
-    src[i] = in + static_cast<int64_t>(live[i] ? row : 0) * K + ch * 8;
-  }
-  auto load = [&](int kb, int s) {
-    const int col = kb * 64 + ch * 8;
-    const bool in_k = col < K;
-    const uint32_t sx = base + s * S::kStage, sp = sx + S::kX;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = r0 + 16 * i;
-      const bool ok = live[i] && in_k;
-      cp_async_16z(sx + row * 128 + ((ch ^ (row & 7)) << 4), ok ? src[i] + kb * 64 : in, ok);
+  if (tid == 0) {
+    for (int s = 0; s < S::kStages; ++s) {
+      mbar_init(smem_u32(&full[s]), 1 + 128);   // P's bytes, and a lane of the gathering warps each
+      mbar_init(smem_u32(&empty[s]), 1);
     }
-#pragma unroll
-    for (int i = 0; i < R / 16; ++i) {
-      const int j = r0 + 16 * i;
-      const bool ok = j < r && in_k;
-      cp_async_16z(sp + j * 128 + ((ch ^ (j & 7)) << 4),
-                   ok ? Pa + static_cast<int64_t>(j) * K + col : P, ok);
+    for (int a = 0; a < S::kAcc; ++a) {
+      mbar_init(smem_u32(&tfull[a]), 1);
+      mbar_init(smem_u32(&tempty[a]), 4 * S::kGroups);
     }
-  };
-  float sum[R / 8][4];
-#pragma unroll
-  for (int i = 0; i < R / 8; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) sum[i][j] = 0.0f;
-#pragma unroll
-  for (int s = 0; s < S::kStages - 1; ++s) {
-    if (kb0 + s < kb1) load(kb0 + s, s);
-    cp_commit();
+    stop = 0;
+    zero = 0;
+    fence_mbar_init();
   }
-  for (int kb = kb0; kb < kb1; ++kb) {
-    const int s = (kb - kb0) % S::kStages;
-    cp_wait<S::kStages - 2>();
-    __syncthreads();
-    if (kb + S::kStages - 1 < kb1) load(kb + S::kStages - 1, (s + S::kStages - 1) % S::kStages);
-    cp_commit();
-    const uint32_t sx = base + s * S::kStage, sp = sx + S::kX;
-    float acc[R / 8][4];
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&tmem_at), S::kTmem);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_at;
+  const int kblocks = (p.K + 63) / 64, per = (kblocks + p.split - 1) / p.split;
+  const int kb0 = min(kblocks, static_cast<int>(rank) * per), kb1 = min(kblocks, kb0 + per);
+  const int steps = kb1 - kb0;
+  volatile int* stopped = &stop;
+  bool ok = true;
+  float sum[S::kOwn];                            // of a draining warp's lane
+  const int j0 = ((warp - 2) >> 2) * S::kOwn;    // and its first column
 #pragma unroll
-    for (int i = 0; i < R / 8; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      uint32_t a[4];
-      const int row = warp * 16 + (lane & 15), ca = 2 * ks + (lane >> 4);
-      ldsm4(sx + row * 128 + ((ca ^ (row & 7)) << 4), a);
-#pragma unroll
-      for (int nt = 0; nt < R / 16; ++nt) {
-        uint32_t b[4];
-        const int j = nt * 16 + (lane & 7) + ((lane >> 4) << 3), cb = 2 * ks + ((lane >> 3) & 1);
-        ldsm4(sp + j * 128 + ((cb ^ (j & 7)) << 4), b);
-        mma_bf16(acc[2 * nt], a, b[0], b[1]);
-        mma_bf16(acc[2 * nt + 1], a, b[2], b[3]);
+  for (int j = 0; j < S::kOwn; ++j) sum[j] = 0.0f;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      for (int i = 0; i < steps; ++i) {
+        const int s = i % S::kStages;
+        ok = mbar_wait(smem_u32(&empty[s]), ((i / S::kStages) & 1) ^ 1, p.wait_ns, stopped);
+        if (!ok) break;
+        mbar_arrive_expect_tx(smem_u32(&full[s]), R * 128);
+        tma_load_3d(smem_u32(ring) + s * S::kStage + kAtom, &map_p, smem_u32(&full[s]),
+                    (kb0 + i) * 64, 0, u.a);
       }
     }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = idesc_bf16(128, R, false, false);
+      for (int i = 0; i < steps; ++i) {
+        const int s = i % S::kStages, a = i % S::kAcc;
+        ok = mbar_wait(smem_u32(&tempty[a]), ((i / S::kAcc) & 1) ^ 1, p.wait_ns, stopped) &&
+             mbar_wait(smem_u32(&full[s]), (i / S::kStages) & 1, p.wait_ns, stopped);
+        if (!ok) break;
+        fence_proxy_async_shared();              // the gathered rows came through the generic proxy
+        tc_fence_after();
+        const uint32_t sa = smem_u32(ring) + s * S::kStage;
+        const uint64_t ad = sdesc_sw128(sa, 16, 1024), bd = sdesc_sw128(sa + kAtom, 16, 1024);
 #pragma unroll
-    for (int i = 0; i < R / 8; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) sum[i][j] += acc[i][j];
-  }
-  cp_wait<0>();
-  __syncthreads();
-  // partial sums of the block, then each rank adds its share of the entries
-  float* part = reinterpret_cast<float*>(smem);
-#pragma unroll
-  for (int i = 0; i < R / 8; ++i) {
-    const int row = warp * 16 + (lane >> 2), c = i * 8 + (lane & 3) * 2;
-    part[row * R + c] = sum[i][0];
-    part[row * R + c + 1] = sum[i][1];
-    part[(row + 8) * R + c] = sum[i][2];
-    part[(row + 8) * R + c + 1] = sum[i][3];
-  }
-  const float f = scales ? __ldg(scales + blk.a) : 1.0f;
-  if (split > 1) cluster_sync();
-  else __syncthreads();
-  const int share = kRows * R / split;            // split divides it: a power of two up to 8
-  for (int i = tid; i < share; i += 128) {
-    const int e = static_cast<int>(rank) * share + i, row = e / R, j = e % R;
-    float v = 0.0f;
-    if (split > 1) {
-      for (int q = 0; q < split; ++q) v += ld_cluster_f32(base + e * 4, q);
-    } else {
-      v = part[e];
+        for (int ks = 0; ks < 4; ++ks)
+          umma_bf16(tmem + a * R, ad + ks * 2, bd + ks * 2, idesc, ks ? 1u : 0u);
+        umma_commit(smem_u32(&empty[s]));
+        umma_commit(smem_u32(&tfull[a]));
+      }
     }
-    if (j < r && rows[row] >= 0) V[static_cast<int64_t>(rows[row]) * r + j] = f * v;
+  } else if (warp < 2 + 4 * S::kGroups) {
+    const uint32_t taddr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + j0;
+    for (int i = 0; i < steps; ++i) {
+      const int a = i % S::kAcc;
+      const bool got = mbar_wait(smem_u32(&tfull[a]), (i / S::kAcc) & 1, p.wait_ns, stopped);
+      ok = __all_sync(0xffffffffu, got);
+      if (!ok) break;
+      tc_fence_after();
+      add_columns<S::kOwn>(taddr + a * R, sum);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&tempty[a]));
+    }
+  } else {
+    const int g = tid - (S::kThreads - 128), ch = g & 7, r0 = g >> 3;
+    const __nv_bfloat16* src[8];
+    bool live[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int row = rows[r0 + 16 * i];
+      live[i] = row >= 0;
+      src[i] = p.in + static_cast<int64_t>(live[i] ? row : 0) * p.K + ch * 8;
+    }
+    for (int i = 0; i < steps; ++i) {
+      const int s = i % S::kStages, k0 = (kb0 + i) * 64;
+      const bool got = mbar_wait(smem_u32(&empty[s]), ((i / S::kStages) & 1) ^ 1, p.wait_ns, stopped);
+      ok = __all_sync(0xffffffffu, got);
+      if (!ok) break;
+      const uint32_t sa = smem_u32(ring) + s * S::kStage;
+      const bool in_k = k0 + ch * 8 < p.K;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int row = r0 + 16 * j;
+        const bool here = live[j] && in_k;
+        cp_async_16z(sa + row * 128 + ((ch ^ (row & 7)) << 4), here ? src[j] + k0 : p.in, here);
+      }
+      cp_async_arrive_noinc(smem_u32(&full[s]));
+    }
+    cp_commit();
+    cp_wait<0>();
   }
-  if (split > 1) cluster_sync();                  // the others' sums have been read
+  if (!ok) {
+    stop = 1;
+    report_error(p.plan.err, kErrTimeout);
+    // what is under way lands (or is given up on) before the CTA goes on
+    if (warp == 0 && lane == 0)
+      for (int s = 0; s < S::kStages; ++s) mbar_wait(smem_u32(&full[s]), 0, kDrainNs / 8, &zero);
+  }
+  __syncthreads();                               // the ring has been read
+
+  // sums as [column][row]
+  float* part = reinterpret_cast<float*>(ring);
+  if (warp >= 2 && warp < 2 + 4 * S::kGroups) {
+    const int row = (warp & 3) * 32 + lane;
+#pragma unroll
+    for (int j = 0; j < S::kOwn; ++j) part[(j0 + j) * kRows + row] = sum[j];
+  }
+  if (p.split > 1) cluster_sync();
+  else __syncthreads();
+  const float f = p.scales ? __ldg(p.scales + u.a) : 1.0f;
+  const uint32_t part0 = smem_u32(part);
+  const int share = kRows * (R / 8) / p.split;    // eight columns of a row each
+  for (int i = tid; i < share; i += S::kThreads) {
+    const int e = static_cast<int>(rank) * share + i, row = e % kRows, c = e / kRows;
+    const int g = rows[row];
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int at = (c * 8 + j) * kRows + row;
+      v[j] = 0.0f;
+      if (p.split > 1) {
+        for (int q = 0; q < p.split; ++q) v[j] += ld_cluster_f32(part0 + at * 4, q);
+      } else {
+        v[j] = part[at];
+      }
+      if (g < 0 || c * 8 + j >= p.r) v[j] = 0.0f;
+      else if (p.V) p.V[static_cast<int64_t>(g) * p.r + c * 8 + j] = v[j];
+      v[j] *= f;
+    }
+    const int64_t at = static_cast<int64_t>(unit) * p.parts * part_bytes<R>() + (c >> 3) * kAtom +
+                       row * 128 + (((c & 7) ^ (row & 7)) << 4);
+    auto put = [&](uint8_t* img) {
+      for (int k = 0; k < p.parts; ++k) {
+        uint4 w;
+        w.x = take_part(v[0], v[1]);
+        w.y = take_part(v[2], v[3]);
+        w.z = take_part(v[4], v[5]);
+        w.w = take_part(v[6], v[7]);
+        *reinterpret_cast<uint4*>(img + at + k * part_bytes<R>()) = w;
+      }
+    };
+    put(p.img);
+    if (p.kept) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        v[j] = (g >= 0 && c * 8 + j < p.r)
+                   ? f * __ldg(p.kept + static_cast<int64_t>(g) * p.r + c * 8 + j)
+                   : 0.0f;
+      put(p.img_kept);
+    }
+  }
+  tc_fence_before();
+  if (p.split > 1) cluster_sync();               // the others have read this CTA's sums
+  else __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, S::kTmem);
+  }
 }
 
 // ------------------------------------------------------------------ expand
 
-constexpr int kCols = 128;          // columns of a tile: rows of 256 bytes
+// A CTA takes a unit and every gridDim.y-th tile of 128 columns. Warps: 0 loads the
+// image and Q, 1 issues the MMAs, 2 to 5 add base and store: 32 rows x 64 columns at a
+// time through shared memory, so that rows move in runs of 128 bytes, the next such
+// piece of base on its way and the ones after it asked into L2.
+constexpr int kCols = 128;
+constexpr int kPiece = 32 * 128;
+constexpr int kSlots = 2;
+constexpr int kExpandThreads = 192;
 
 template <int R>
 struct Expand {
-  static constexpr int kStages = R >= 128 ? 2 : 3;
-  static constexpr int kT = kRows * 256, kQ = R * 256;
-  static constexpr int kStage = kT + kQ;
-  static constexpr int kBytes = kStages * kStage;
+  static constexpr int kImg = 2 * part_bytes<R>();
+  static constexpr int kQ = 2 * R * 128;          // two boxes of 64 columns
+  static constexpr int kStages = 2;
+  static constexpr int kBytes = 1024 + kImg + kStages * kQ + 4 * kSlots * kPiece;
+};
+
+struct ExpandArgs {
+  const uint8_t* img;
+  int parts;                      // of the image; the first two are used
+  const __nv_bfloat16* base;      // or NULL
+  __nv_bfloat16* out;
+  int N;
+  unsigned long long wait_ns;
+  Plan plan;
 };
 
 template <int R>
-__global__ void __launch_bounds__(128)
-    expand_kernel(const float* __restrict__ V, const __nv_bfloat16* __restrict__ Q,
-                  const float* __restrict__ scales, const __nv_bfloat16* base, __nv_bfloat16* out,
-                  int N, int r, Plan plan) {
+__global__ void __launch_bounds__(kExpandThreads)
+    expand_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ ExpandArgs p) {
   using S = Expand<R>;
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ uint8_t smem_raw[];
   __shared__ int rows[kRows];
+  __shared__ uint64_t full[S::kStages], empty[S::kStages], tfull[2], tempty[2], image;
+  __shared__ uint32_t tmem_at;
+  __shared__ int stop, zero;
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const Block blk = find_block(plan, static_cast<int>(blockIdx.x));
-  if (blk.rows == 0) return;
-  const bool none = blk.a == plan.n;
-  if (none && base == out) return;                // base stays as it is
-  if (tid < kRows) rows[tid] = tid < blk.rows ? plan_row(plan, blk.lo + tid) : -1;
-  __syncthreads();
-  const uint32_t sb = smem_u32(smem);
-  const int tiles = (N + kCols - 1) / kCols;
-  const int t0 = blockIdx.y, dt = gridDim.y;
-  const __nv_bfloat16* Qa = Q + static_cast<int64_t>(none ? 0 : blk.a) * r * N;
-  // this lane's chunk and rows of its warp's part of a tile: two rows a step
-  const int ch = lane & 15, w0 = warp * 16 + (lane >> 4);
-  auto load = [&](int t, int s) {
-    const int col = t * kCols + ch * 8;
-    const bool in_n = col < N;
-    const uint32_t st = sb + s * S::kStage, sq = st + S::kT;
-    if (base) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int row = w0 + 2 * i, g = rows[row];
-        const bool ok = in_n && g >= 0;
-        cp_async_16z(st + row * 256 + ((ch ^ (row & 7)) << 4),
-                     ok ? base + static_cast<int64_t>(g) * N + col : base, ok);
-      }
-    }
-    if (!none) {
-#pragma unroll
-      for (int i = 0; i < R / 8; ++i) {
-        const int j = (tid >> 4) + 8 * i;
-        const bool ok = in_n && j < r;
-        cp_async_16z(sq + j * 256 + ((ch ^ (j & 7)) << 4),
-                     ok ? Qa + static_cast<int64_t>(j) * N + col : Q, ok);
-      }
-    }
-  };
-#pragma unroll
-  for (int s = 0; s < S::kStages - 1; ++s) {
-    if (t0 + s * dt < tiles) load(t0 + s * dt, s);
-    cp_commit();
+  const int unit = static_cast<int>(blockIdx.x);
+  const Unit u = find_unit(p.plan, unit);
+  const bool none = u.a == p.plan.n;
+  if (u.rows == 0 || (none && p.base == p.out)) {  // nothing, or base stays as it is
+    grid_dependency_wait();
+    return;
   }
-  // V of this warp's rows as the A operand, high and low parts
-  uint32_t hi[R / 16][4], lo[R / 16][4];
-  {
-    const float f = (scales && !none) ? __ldg(scales + blk.a) : 1.0f;
-    auto at = [&](int row, int j) {
-      const int g = rows[row];
-      return (!none && g >= 0 && j < r) ? f * __ldg(V + static_cast<int64_t>(g) * r + j) : 0.0f;
-    };
-#pragma unroll
-    for (int ks = 0; ks < R / 16; ++ks)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = warp * 16 + (lane >> 2) + (i & 1) * 8;
-        const int j = ks * 16 + (lane & 3) * 2 + (i >> 1) * 8;
-        split2(at(row, j), at(row, j + 1), hi[ks][i], lo[ks][i]);
-      }
-  }
-  int it = 0;
-  for (int t = t0; t < tiles; t += dt, ++it) {
-    const int s = it % S::kStages;
-    cp_wait<S::kStages - 2>();
+  if (tid < kRows) rows[tid] = tid < u.rows ? plan_row(p.plan, u.lo + tid) : -1;
+  const int tiles = (p.N + kCols - 1) / kCols;
+  if (none) {                                    // base as it is, or zeros
     __syncthreads();
-    if (t + (S::kStages - 1) * dt < tiles)
-      load(t + (S::kStages - 1) * dt, (s + S::kStages - 1) % S::kStages);
-    cp_commit();
-    uint8_t* st = smem + s * S::kStage;
-    const uint32_t sq = sb + s * S::kStage + S::kT;
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      float acc[8][4];
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
-      if (!none) {
-#pragma unroll
-        for (int ks = 0; ks < R / 16; ++ks)
-#pragma unroll
-          for (int nt = 0; nt < 4; ++nt) {
-            uint32_t b[4];
-            const int j = ks * 16 + (lane & 7) + ((lane >> 3) & 1) * 8;
-            const int c = half * 8 + nt * 2 + (lane >> 4);
-            ldsm4_t(sq + j * 256 + ((c ^ (j & 7)) << 4), b);
-            mma_bf16(acc[2 * nt], hi[ks], b[0], b[1]);
-            mma_bf16(acc[2 * nt + 1], hi[ks], b[2], b[3]);
-            mma_bf16(acc[2 * nt], lo[ks], b[0], b[1]);
-            mma_bf16(acc[2 * nt + 1], lo[ks], b[2], b[3]);
-          }
-      }
-#pragma unroll
-      for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int row = warp * 16 + (lane >> 2) + i * 8, c = half * 8 + nt;
-          uint32_t* w = reinterpret_cast<uint32_t*>(st + row * 256 + ((c ^ (row & 7)) << 4) +
-                                                    (lane & 3) * 4);
-          float v0 = acc[nt][2 * i], v1 = acc[nt][2 * i + 1];
-          if (base) {
-            const uint32_t o = *w;
-            v0 += __uint_as_float(o << 16);
-            v1 += __uint_as_float(o & 0xFFFF0000u);
-          }
-          *w = pack_bf16x2(v0, v1);
-        }
+    const int nv = p.N / 8;
+    for (int row = blockIdx.y; row < u.rows; row += gridDim.y) {
+      if (rows[row] < 0) continue;
+      const int64_t at = static_cast<int64_t>(rows[row]) * p.N;
+      for (int c = tid; c < nv; c += kExpandThreads)
+        reinterpret_cast<uint4*>(p.out + at)[c] =
+            p.base ? reinterpret_cast<const uint4*>(p.base + at)[c] : make_uint4(0, 0, 0, 0);
     }
-    __syncwarp();                                  // the warp's 16 rows are its own
-    const int col = t * kCols + ch * 8;
-    if (col < N) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int row = w0 + 2 * i, g = rows[row];
-        if (g >= 0)
-          __stcs(reinterpret_cast<uint4*>(out + static_cast<int64_t>(g) * N + col),
-                 *reinterpret_cast<const uint4*>(st + row * 256 + ((ch ^ (row & 7)) << 4)));
-      }
-    }
+    grid_dependency_wait();
+    return;
   }
-  cp_wait<0>();
+  if (tid == 0) {
+    for (int s = 0; s < S::kStages; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&empty[s]), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(smem_u32(&tfull[a]), 1);
+      mbar_init(smem_u32(&tempty[a]), 4);
+    }
+    mbar_init(smem_u32(&image), 1);
+    stop = 0;
+    zero = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&tmem_at), 256);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_at, img0 = smem_u32(smem), q0 = img0 + S::kImg;
+  const int t0 = blockIdx.y, dt = gridDim.y;
+  volatile int* stopped = &stop;
+  bool ok = true;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int i = 0;
+      if (t0 >= tiles) grid_dependency_wait();
+      for (int t = t0; t < tiles; t += dt, ++i) {
+        const int s = i % S::kStages;
+        ok = mbar_wait(smem_u32(&empty[s]), ((i / S::kStages) & 1) ^ 1, p.wait_ns, stopped);
+        if (!ok) break;
+        const uint32_t sq = q0 + s * S::kQ, bar = smem_u32(&full[s]);
+        mbar_arrive_expect_tx(bar, S::kQ);
+        tma_load_3d(sq, &map_q, bar, t * kCols, 0, u.a);
+        tma_load_3d(sq + R * 128, &map_q, bar, t * kCols + 64, 0, u.a);
+        if (i == 0) {                            // Q is there before the image is written
+          grid_dependency_wait();
+          fence_proxy_async();
+          mbar_arrive_expect_tx(smem_u32(&image), S::kImg);
+          const uint8_t* src = p.img + static_cast<int64_t>(unit) * p.parts * part_bytes<R>();
+          for (int k = 0; k < S::kImg / kAtom; ++k)
+            bulk_copy_g2s(img0 + k * kAtom, src + k * kAtom, kAtom, smem_u32(&image));
+        }
+      }
+      for (int k = i > S::kStages ? i - S::kStages : 0; k < i; ++k)
+        mbar_wait(smem_u32(&full[k % S::kStages]), (k / S::kStages) & 1, kDrainNs, &zero);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = idesc_bf16(128, kCols, false, true);
+      ok = t0 >= tiles || mbar_wait(smem_u32(&image), 0, p.wait_ns, stopped);
+      int i = 0;
+      for (int t = t0; t < tiles && ok; t += dt, ++i) {
+        const int s = i % S::kStages, a = i & 1;
+        ok = mbar_wait(smem_u32(&tempty[a]), ((i >> 1) & 1) ^ 1, p.wait_ns, stopped) &&
+             mbar_wait(smem_u32(&full[s]), (i / S::kStages) & 1, p.wait_ns, stopped);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t bd = sdesc_sw128(q0 + s * S::kQ, R * 128, 1024);
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int ks = 0; ks < R / 16; ++ks) {
+            const uint64_t ad = sdesc_sw128(img0 + k * part_bytes<R>() + (ks >> 2) * kAtom, 16, 1024);
+            umma_bf16(tmem + a * kCols, ad + (ks & 3) * 2, bd + ks * (2048 >> 4), idesc,
+                      (k | ks) ? 1u : 0u);
+          }
+        umma_commit(smem_u32(&empty[s]));
+        umma_commit(smem_u32(&tfull[a]));
+      }
+    }
+  } else {
+    const int q = warp & 3;
+    const uint32_t slot0 = smem_u32(smem) + S::kImg + S::kStages * S::kQ + q * kSlots * kPiece;
+    const int ch = lane & 7, w0 = q * 32 + (lane >> 3);
+    const int mine = rows[q * 32 + lane];        // this lane's row of the accumulator
+    const bool any = __any_sync(0xffffffffu, mine >= 0);
+    // the piece after (t, half): columns, or -1
+    auto next = [&](int t, int half) { return half == 0 ? t * kCols + 64 : (t + dt) * kCols; };
+    auto load = [&](int col, int slot) {
+      if (p.base && col < p.N) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int row = w0 + 4 * i, g = rows[row];
+          const bool here = g >= 0 && col + ch * 8 < p.N;
+          cp_async_16z(slot0 + slot * kPiece + (row & 31) * 128 + ((ch ^ (row & 7)) << 4),
+                       here ? p.base + static_cast<int64_t>(g) * p.N + col + ch * 8 : p.base, here);
+        }
+      }
+      cp_commit();
+    };
+    auto ask = [&](int col) {
+      if (p.base && mine >= 0 && col < p.N)
+        prefetch_l2(p.base + static_cast<int64_t>(mine) * p.N + col);
+    };
+    int i = 0, slot = 0;
+    if (t0 < tiles && any) {
+      load(t0 * kCols, 0);
+      ask(t0 * kCols + 64);
+      ask((t0 + dt) * kCols);
+      ask((t0 + dt) * kCols + 64);
+    }
+    for (int t = t0; t < tiles; t += dt, ++i) {
+      const int a = i & 1;
+      if (any) {
+        ask((t + 2 * dt) * kCols);
+        ask((t + 2 * dt) * kCols + 64);
+      }
+      const bool got = mbar_wait(smem_u32(&tfull[a]), (i >> 1) & 1, p.wait_ns, stopped);
+      ok = __all_sync(0xffffffffu, got);
+      if (!ok) break;
+      tc_fence_after();
+      if (any) {
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          const int col = t * kCols + half * 64;
+          if (col >= p.N) break;
+          load(next(t, half), slot ^ 1);
+          uint32_t v[64];
+          const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + a * kCols + half * 64;
+          tmem_ld_32x32b_x32(taddr, v);
+          tmem_ld_32x32b_x32(taddr + 32, v + 32);
+          tmem_ld_wait();
+          cp_wait<1>();                          // this piece of base
+          __syncwarp();
+          uint8_t* st = smem + S::kImg + S::kStages * S::kQ + (q * kSlots + slot) * kPiece;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            uint4* w = reinterpret_cast<uint4*>(st + lane * 128 + ((c ^ (lane & 7)) << 4));
+            float x[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(v[c * 8 + j]);
+            if (p.base) {
+              const uint4 o = *w;
+              const uint32_t b[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                x[2 * j] += lo_f(b[j]);
+                x[2 * j + 1] += hi_f(b[j]);
+              }
+            }
+            *w = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                            pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+          }
+          __syncwarp();
+          if (col + ch * 8 < p.N) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const int row = w0 + 4 * j, g = rows[row];
+              if (g >= 0)
+                __stcs(reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(g) * p.N + col + ch * 8),
+                       *reinterpret_cast<const uint4*>(st + (row & 31) * 128 +
+                                                       ((ch ^ (row & 7)) << 4)));
+            }
+          }
+          __syncwarp();                          // the slot may be filled again
+          slot ^= 1;
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&tempty[a]));
+    }
+    cp_wait<0>();
+  }
+  if (!ok) {
+    stop = 1;
+    report_error(p.plan.err, kErrTimeout);
+    if (warp == 1 && lane == 0 && t0 < tiles) mbar_wait(smem_u32(&image), 0, kDrainNs, &zero);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 256);
+  }
 }
 
 // ------------------------------------------------------------------ grad
 
+// Both gradients in one launch. Their work is a list of items: (tile of columns, 64
+// rows of one adapter), the rows running fastest. One CTA an SM takes an equal run of
+// items whatever the adapters' shares are; where a run ends inside an output, its sums
+// go to a slot of the CTA, and grad_finish_kernel adds the slots up in order.
+// Warps: 0 loads images, 1 issues the MMAs, then 8 draining warps (one for each 32
+// columns, or 32 columns and half of the rank) and 4 gathering rows of the input, each
+// row's columns of the tile in one run of 512 (256) bytes.
 struct GradJob {
-  const float* V;              // [T, r]
+  const uint8_t* img;          // three parts
   const __nv_bfloat16* in;     // [T, N]
-  const float* scales;         // or NULL
   float* G;                    // [n, r, N]
-  int N;
+  int N, tiles;
+};
+
+struct GradArgs {
+  GradJob job[2];
+  float* partial;              // [2 * CTAs][R][kTile]
+  int* chunks;                 // [n + 1]: 64-row chunks before each adapter, for the finish
+  int r, accumulate;
+  int units;                   // that the images have room for
+  unsigned long long wait_ns;
+  Plan plan;
 };
 
 template <int R>
 struct Grad {
+  static constexpr int kHalves = R > 64 ? 1 : 2;
+  static constexpr int kTile = 128 * kHalves;
+  static constexpr int kIn = kHalves * kAtom;                 // 64 rows of the tile's columns
+  static constexpr int kImg = 3 * part_bytes<R>() / 2;        // 64 rows of three parts
+  static constexpr int kStage = kIn + kImg;
   static constexpr int kStages = 3;
-  static constexpr int kIn = kRows * 256;
-  static constexpr int kVRow = R * 2 + 16;                  // padded: eight rows hit all banks
-  static constexpr int kV = 2 * kRows * kVRow;              // high and low parts
-  static constexpr int kRing = kStages * kIn + 2 * kV;
-  static constexpr int kPartial = R * kCols * 4;
-  static constexpr int kBytes = kRing > kPartial ? kRing : kPartial;
+  static constexpr int kDrain = 8;
+  static constexpr int kOwn = R > 64 ? 64 : R;                // ranks of a draining warp
+  static constexpr int kThreads = 32 * (2 + kDrain + 4);
+  static constexpr int kTmem = 2 * kHalves * R;
+  static constexpr int kBytes = 1024 + kStages * kStage;
 };
 
-// A cluster takes (adapter, 128 columns), each of its CTAs a run of the adapter's
-// 64-row chunks; eight warps of 16 columns and the whole rank each. blockIdx.z:
-// which of the two gradients.
+// What of the list CTA b has: items [first(b), first(b + 1)).
+__device__ __forceinline__ int64_t first_item(int64_t items, int ctas, int b) {
+  return items * b / ctas;
+}
+
+// A walk over items: tile, chunk within the tile, adapter.
+struct Walk {
+  int tile, c, a;
+  __device__ __forceinline__ void start(int64_t item, int total, int n, const int* chunks) {
+    tile = static_cast<int>(item / total);
+    c = static_cast<int>(item - static_cast<int64_t>(tile) * total);
+    int lo = 0, hi = n - 1;                      // the last adapter that begins at or before c
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (chunks[mid] <= c) lo = mid; else hi = mid - 1;
+    }
+    a = lo;
+  }
+  __device__ __forceinline__ void next(int total, const int* chunks) {
+    if (++c == total) {
+      ++tile;
+      c = 0;
+      a = 0;
+    }
+    while (chunks[a + 1] <= c) ++a;
+  }
+};
+
 template <int R>
-__global__ void __launch_bounds__(256)
-    grad_kernel(GradJob job0, GradJob job1, int r, int split, int accumulate, Plan plan) {
+__global__ void __launch_bounds__(Grad<R>::kThreads, 1)
+    grad_kernel(const __grid_constant__ GradArgs p) {
   using S = Grad<R>;
-  extern __shared__ __align__(128) uint8_t smem[];
-  const GradJob job = blockIdx.z ? job1 : job0;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ int chunks[kMaxAdapters + 1], units[kMaxAdapters + 1], begin[kMaxAdapters], end[kMaxAdapters];
+  __shared__ uint64_t full[S::kStages], empty[S::kStages], tfull[2], tempty[2];
+  __shared__ uint32_t tmem_at;
+  __shared__ int stop, zero;
+  uint8_t* ring = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t rank = cluster_ctarank();
-  const int tile = static_cast<int>(blockIdx.x / split), a = blockIdx.y;
-  if (tile * kCols >= job.N) return;               // the whole cluster
-  int lo, hi;
-  segment(plan, a, lo, hi);
-  const int chunks = (hi - lo + kRows - 1) / kRows, per = (chunks + split - 1) / split;
-  const int c0 = min(chunks, static_cast<int>(rank) * per), c1 = min(chunks, c0 + per);
-  const int N = job.N, col0 = tile * kCols;
-  const uint32_t sb = smem_u32(smem), sv = sb + S::kStages * S::kIn;
-  const float f = job.scales ? __ldg(job.scales + a) : 1.0f;
-  const int ch = tid & 15, w0 = tid >> 4;          // chunk and first row of the copies
-  const bool in_n = col0 + ch * 8 < N;
-  auto load = [&](int c, int s) {
+  const int n = p.plan.n, b = blockIdx.x, ctas = gridDim.x;
+  if (warp == 0) {
+    int c_sum = 0, u_sum = 0;
+    for (int a0 = 0; a0 < n; a0 += 32) {
+      int lo = 0, hi = 0;
+      if (a0 + lane < n) segment(p.plan, a0 + lane, lo, hi);
+      int c = (hi - lo + 63) >> 6, u = (hi - lo + kRows - 1) / kRows;
+      const int c_own = c, u_own = u;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = w0 + 16 * i, at = lo + c * kRows + row;
-      const int g = at < hi ? plan_row(plan, at) : -1;
-      const bool ok = in_n && g >= 0;
-      cp_async_16z(sb + s * S::kIn + row * 256 + ((ch ^ (row & 7)) << 4),
-                   ok ? job.in + static_cast<int64_t>(g) * N + col0 + ch * 8 : job.in, ok);
+      for (int d = 1; d < 32; d <<= 1) {
+        const int oc = __shfl_up_sync(0xffffffffu, c, d), ou = __shfl_up_sync(0xffffffffu, u, d);
+        if (lane >= d) {
+          c += oc;
+          u += ou;
+        }
+      }
+      if (a0 + lane < n) {
+        chunks[a0 + lane] = c_sum + c - c_own;
+        units[a0 + lane] = u_sum + u - u_own;
+        begin[a0 + lane] = lo;
+        end[a0 + lane] = hi;
+      }
+      c_sum += __shfl_sync(0xffffffffu, c, 31);
+      u_sum += __shfl_sync(0xffffffffu, u, 31);
     }
-  };
-  // V of a chunk: 64 x R values, R / 8 pairs a thread
-  float2 vr[R / 8];
-  auto load_v = [&](int c) {
-#pragma unroll
-    for (int i = 0; i < R / 8; ++i) {
-      const int e = (tid + 256 * i) * 2, row = e / R, j = e % R, at = lo + c * kRows + row;
-      const int g = at < hi ? plan_row(plan, at) : -1;
-      const float* src = job.V + static_cast<int64_t>(g < 0 ? 0 : g) * r + j;
-      vr[i].x = (g >= 0 && j < r) ? f * __ldg(src) : 0.0f;
-      vr[i].y = (g >= 0 && j + 1 < r) ? f * __ldg(src + 1) : 0.0f;
-    }
-  };
-  auto store_v = [&](int b) {
-#pragma unroll
-    for (int i = 0; i < R / 8; ++i) {
-      const int e = (tid + 256 * i) * 2, row = e / R, j = e % R;
-      uint32_t h, l;
-      split2(vr[i].x, vr[i].y, h, l);
-      uint8_t* p = smem + S::kStages * S::kIn + b * S::kV + row * S::kVRow + j * 2;
-      *reinterpret_cast<uint32_t*>(p) = h;
-      *reinterpret_cast<uint32_t*>(p + kRows * S::kVRow) = l;
-    }
-  };
-  float sum[R / 16][2][4];
-#pragma unroll
-  for (int m = 0; m < R / 16; ++m)
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) sum[m][i][j] = 0.0f;
-#pragma unroll
-  for (int s = 0; s < S::kStages - 1; ++s) {
-    if (c0 + s < c1) load(c0 + s, s);
-    cp_commit();
+    if (lane == 0) chunks[n] = c_sum;
   }
-  if (c0 < c1) {
-    load_v(c0);
-    store_v(0);
+  if (tid == 0) {
+    for (int s = 0; s < S::kStages; ++s) {
+      mbar_init(smem_u32(&full[s]), 1 + 128);
+      mbar_init(smem_u32(&empty[s]), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(smem_u32(&tfull[a]), 1);
+      mbar_init(smem_u32(&tempty[a]), S::kDrain);
+    }
+    stop = 0;
+    zero = 0;
+    fence_mbar_init();
   }
-  for (int c = c0; c < c1; ++c) {
-    const int it = c - c0, s = it % S::kStages, vb = it & 1;
-    cp_wait<S::kStages - 2>();
-    __syncthreads();
-    if (c + S::kStages - 1 < c1) load(c + S::kStages - 1, (s + S::kStages - 1) % S::kStages);
-    cp_commit();
-    if (c + 1 < c1) load_v(c + 1);
-    const uint32_t si = sb + s * S::kIn, sh = sv + vb * S::kV, sl = sh + kRows * S::kVRow;
-    float acc[R / 16][2][4];
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&tmem_at), S::kTmem < 32 ? 32 : S::kTmem);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_at;
+  const int total = chunks[n];
+  if (b == 0)
+    for (int a = tid; a <= n; a += S::kThreads) p.chunks[a] = chunks[a];
+  const int64_t items = static_cast<int64_t>(p.job[0].tiles + p.job[1].tiles) * total;
+  const int64_t i0 = first_item(items, ctas, b);
+  const int steps = static_cast<int>(first_item(items, ctas, b + 1) - i0);
+  volatile int* stopped = &stop;
+  bool ok = true;
+  Walk w = {0, 0, 0};
+  if (steps > 0) w.start(i0, total, n, chunks);
+  const int t0 = p.job[0].tiles;
+
+  if (steps == 0) {
+    // nothing of the list
+  } else if (warp == 0) {
+    if (lane == 0) {
+      for (int i = 0; i < steps; ++i) {
+        const int s = i % S::kStages;
+        ok = mbar_wait(smem_u32(&empty[s]), ((i / S::kStages) & 1) ^ 1, p.wait_ns, stopped);
+        if (!ok) break;
+        const uint32_t bar = smem_u32(&full[s]), dst = smem_u32(ring) + s * S::kStage + S::kIn;
+        const int c = w.c - chunks[w.a];         // chunk of the adapter: half a unit
+        const int unit = min(units[w.a] + (c >> 1), p.units - 1);   // offsets may overlap
+        const uint8_t* src = p.job[w.tile >= t0].img +
+                             static_cast<int64_t>(unit) * 3 * part_bytes<R>() +
+                             (c & 1) * (kAtom / 2);
+        mbar_arrive_expect_tx(bar, S::kImg);
 #pragma unroll
-    for (int m = 0; m < R / 16; ++m)
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[m][i][j] = 0.0f;
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      uint32_t b[4];
-      const int k = ks * 16 + (lane & 7) + ((lane >> 3) & 1) * 8, cc = warp * 2 + (lane >> 4);
-      ldsm4_t(si + k * 256 + ((cc ^ (k & 7)) << 4), b);
-      const int kv = ks * 16 + (lane & 7) + ((lane >> 4) << 3), mc = ((lane >> 3) & 1) * 16;
-#pragma unroll
-      for (int m = 0; m < R / 16; ++m) {
-        uint32_t h[4], l[4];
-        ldsm4_t(sh + kv * S::kVRow + m * 32 + mc, h);
-        ldsm4_t(sl + kv * S::kVRow + m * 32 + mc, l);
-        mma_bf16(acc[m][0], h, b[0], b[1]);
-        mma_bf16(acc[m][1], h, b[2], b[3]);
-        mma_bf16(acc[m][0], l, b[0], b[1]);
-        mma_bf16(acc[m][1], l, b[2], b[3]);
+        for (int k = 0; k < 3 * atoms<R>(); ++k)
+          bulk_copy_g2s(dst + k * (kAtom / 2), src + k * kAtom, kAtom / 2, bar);
+        if (i + 1 < steps) w.next(total, chunks);
       }
     }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = idesc_bf16(128, R, true, true);
+      for (int i = 0; i < steps; ++i) {
+        const int s = i % S::kStages, a = i & 1;
+        ok = mbar_wait(smem_u32(&tempty[a]), ((i >> 1) & 1) ^ 1, p.wait_ns, stopped) &&
+             mbar_wait(smem_u32(&full[s]), (i / S::kStages) & 1, p.wait_ns, stopped);
+        if (!ok) break;
+        fence_proxy_async_shared();
+        tc_fence_after();
+        const uint32_t si = smem_u32(ring) + s * S::kStage;
 #pragma unroll
-    for (int m = 0; m < R / 16; ++m)
+        for (int m = 0; m < S::kHalves; ++m) {
+          const uint64_t ad = sdesc_sw128(si + m * kAtom, kAtom / 2, 1024);
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+          for (int k = 0; k < 3; ++k) {
+            const uint64_t bd = sdesc_sw128(si + S::kIn + k * atoms<R>() * (kAtom / 2), kAtom / 2, 1024);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) sum[m][i][j] += acc[m][i][j];
-    if (c + 1 < c1) store_v(vb ^ 1);               // read by nobody until the next barrier
+            for (int ks = 0; ks < 4; ++ks)
+              umma_bf16(tmem + (a * S::kHalves + m) * R, ad + ks * (2048 >> 4),
+                        bd + ks * (2048 >> 4), idesc, (k | ks) ? 1u : 0u);
+          }
+        }
+        umma_commit(smem_u32(&empty[s]));
+        umma_commit(smem_u32(&tfull[a]));
+      }
+    }
+  } else if (warp < 2 + S::kDrain) {
+    const int m = S::kHalves == 2 ? (warp - 2) >> 2 : 0, q = warp & 3;
+    const int j0 = S::kHalves == 2 ? 0 : ((warp - 2) >> 2) * S::kOwn;
+    const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + m * R + j0;
+    const int in_tile = m * 128 + q * 32 + lane;
+    float sum[S::kOwn];
+#pragma unroll
+    for (int j = 0; j < S::kOwn; ++j) sum[j] = 0.0f;
+    bool from_first = w.c == chunks[w.a];        // the run began with its output's first chunk
+    bool first_run = true;
+    for (int i = 0; i < steps; ++i) {
+      const int a = i & 1;
+      const bool got = mbar_wait(smem_u32(&tfull[a]), (i >> 1) & 1, p.wait_ns, stopped);
+      ok = __all_sync(0xffffffffu, got);
+      if (!ok) break;
+      tc_fence_after();
+      add_columns<S::kOwn>(taddr + a * S::kHalves * R, sum);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&tempty[a]));
+      const bool last = w.c + 1 == chunks[w.a + 1];
+      if (last || i + 1 == steps) {              // the run's end
+        const GradJob& job = p.job[w.tile >= t0];
+        const int col = (w.tile >= t0 ? w.tile - t0 : w.tile) * S::kTile + in_tile;
+        if (last && from_first) {
+          if (col < job.N) {
+            float* at = job.G + (static_cast<int64_t>(w.a) * p.r + j0) * job.N + col;
+#pragma unroll
+            for (int j = 0; j < S::kOwn; ++j) {
+              if (j0 + j < p.r) *at = p.accumulate ? *at + sum[j] : sum[j];
+              at += job.N;
+            }
+          }
+        } else {
+          float* slot = p.partial + static_cast<int64_t>(2 * b + (first_run ? 0 : 1)) * R * S::kTile;
+#pragma unroll
+          for (int j = 0; j < S::kOwn; ++j) slot[(j0 + j) * S::kTile + in_tile] = sum[j];
+        }
+#pragma unroll
+        for (int j = 0; j < S::kOwn; ++j) sum[j] = 0.0f;
+        first_run = false;
+        from_first = true;
+      }
+      if (i + 1 < steps) w.next(total, chunks);
+    }
+  } else {
+    const int g = warp - 2 - S::kDrain;          // rows g, g + 4, ... of a chunk
+    constexpr int kVec = S::kTile / 8;           // 16-byte pieces of a row: 32 or 16
+    constexpr int kPer = 32 / kVec;              // rows of a warp's instruction
+    const int ch = lane % kVec, sub = lane / kVec;
+    auto row_of = [&](const Walk& x) {           // lane l: the chunk's row 4 l + g, or -1
+      const int at = begin[x.a] + (x.c - chunks[x.a]) * 64 + 4 * lane + g;
+      return (lane < 16 && at < end[x.a]) ? plan_row(p.plan, at) : -1;
+    };
+    int mine = row_of(w);
+    for (int i = 0; i < steps; ++i) {
+      const int s = i % S::kStages;
+      const GradJob& job = p.job[w.tile >= t0];
+      const int col = (w.tile >= t0 ? w.tile - t0 : w.tile) * S::kTile + ch * 8;
+      const bool in_n = col < job.N;
+      const int here = mine;
+      if (i + 1 < steps) {
+        w.next(total, chunks);
+        mine = row_of(w);
+      }
+      const bool got = mbar_wait(smem_u32(&empty[s]), ((i / S::kStages) & 1) ^ 1, p.wait_ns, stopped);
+      ok = __all_sync(0xffffffffu, got);
+      if (!ok) break;
+      const uint32_t dst = smem_u32(ring) + s * S::kStage + (ch >> 3) * (kAtom / 2);
+#pragma unroll
+      for (int j = 0; j < 16 / kPer; ++j) {
+        const int k = j * kPer + sub, row = 4 * k + g;
+        const int t = __shfl_sync(0xffffffffu, here, k);
+        const bool live = t >= 0 && in_n;
+        cp_async_16z(dst + row * 128 + (((ch & 7) ^ (row & 7)) << 4),
+                     live ? job.in + static_cast<int64_t>(t) * job.N + col : job.in, live);
+      }
+      cp_async_arrive_noinc(smem_u32(&full[s]));
+    }
+    cp_commit();
+    cp_wait<0>();
   }
-  cp_wait<0>();
+  if (!ok) {
+    stop = 1;
+    report_error(p.plan.err, kErrTimeout);
+    if (warp == 0 && lane == 0)
+      for (int s = 0; s < S::kStages; ++s) mbar_wait(smem_u32(&full[s]), 0, kDrainNs / 8, &zero);
+  }
+  tc_fence_before();
   __syncthreads();
-  float* part = reinterpret_cast<float*>(smem);
-#pragma unroll
-  for (int m = 0; m < R / 16; ++m)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int j = m * 16 + (lane >> 2), c = warp * 16 + i * 8 + (lane & 3) * 2;
-      part[j * kCols + c] = sum[m][i][0];
-      part[j * kCols + c + 1] = sum[m][i][1];
-      part[(j + 8) * kCols + c] = sum[m][i][2];
-      part[(j + 8) * kCols + c + 1] = sum[m][i][3];
-    }
-  if (split > 1) cluster_sync();
-  else __syncthreads();
-  const int share = R * kCols / split;
-  for (int i = tid; i < share; i += 256) {
-    const int e = static_cast<int>(rank) * share + i, j = e / kCols, c = e % kCols;
-    float v = 0.0f;
-    if (split > 1) {
-      for (int q = 0; q < split; ++q) v += ld_cluster_f32(sb + e * 4, q);
-    } else {
-      v = part[e];
-    }
-    if (j < r && col0 + c < N) {
-      float* g = job.G + (static_cast<int64_t>(a) * r + j) * N + col0 + c;
-      *g = accumulate ? *g + v : v;
-    }
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, S::kTmem < 32 ? 32 : S::kTmem);
   }
-  if (split > 1) cluster_sync();
+}
+
+// The outputs that more than one CTA added to, in the order of the CTAs, and those of
+// adapters without rows.
+template <int R>
+__global__ void __launch_bounds__(Grad<R>::kTile)
+    grad_finish_kernel(const __grid_constant__ GradArgs p, int ctas) {
+  using S = Grad<R>;
+  const int a = blockIdx.y, n = p.plan.n, tile = blockIdx.x, t0 = p.job[0].tiles;
+  const GradJob& job = p.job[tile >= t0];
+  const int col = (tile >= t0 ? tile - t0 : tile) * S::kTile + threadIdx.x;
+  const int total = p.chunks[n], c0 = p.chunks[a], c1 = p.chunks[a + 1];
+  float* g = job.G + static_cast<int64_t>(a) * p.r * job.N + col;
+  if (c0 == c1) {
+    if (col < job.N && !p.accumulate)
+      for (int j = 0; j < p.r; ++j) g[static_cast<int64_t>(j) * job.N] = 0.0f;
+    return;
+  }
+  const int64_t items = static_cast<int64_t>(t0 + p.job[1].tiles) * total;
+  const int64_t i0 = static_cast<int64_t>(tile) * total + c0, i1 = i0 + (c1 - c0);
+  // the CTA of an item: the last one that begins at or before it
+  auto owner = [&](int64_t i) {
+    int lo = 0, hi = ctas - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (first_item(items, ctas, mid) <= i) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+  };
+  const int b0 = owner(i0), b1 = owner(i1 - 1);
+  if (b0 == b1 || col >= job.N) return;
+  for (int j = 0; j < p.r; ++j) {
+    float v = 0.0f;
+    for (int b = b0; b <= b1; ++b) {
+      const int64_t first = first_item(items, ctas, b);
+      if (first == first_item(items, ctas, b + 1)) continue;      // a CTA without items
+      const int slot = 2 * b + (first >= i0 ? 0 : 1);
+      v += p.partial[(static_cast<int64_t>(slot) * R + j) * S::kTile + threadIdx.x];
+    }
+    float* at = g + static_cast<int64_t>(j) * job.N;
+    *at = p.accumulate ? *at + v : v;
+  }
 }
 
 // ------------------------------------------------------------------ few rows
@@ -795,9 +1160,10 @@ __global__ void __launch_bounds__(kFewThreads)
 
 // ------------------------------------------------------------------ host
 
+// A launch with clusters of `cluster` CTAs; beside: beside the kernel before it.
 template <typename... KArgs, typename... Args>
-cudaError_t launch_cluster(void (*kern)(KArgs...), dim3 grid, int threads, int smem, int cluster,
-                           bool* configured, cudaStream_t st, Args... args) {
+cudaError_t launch(void (*kern)(KArgs...), dim3 grid, int threads, int smem, int cluster,
+                   bool beside, bool* configured, cudaStream_t st, Args... args) {
   const int d = current_device();
   if (d < 0 || d >= kMaxDevices) return cudaErrorInvalidDevice;
   if (!configured[d]) {
@@ -806,7 +1172,7 @@ cudaError_t launch_cluster(void (*kern)(KArgs...), dim3 grid, int threads, int s
     configured[d] = true;
   }
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
@@ -815,55 +1181,62 @@ cudaError_t launch_cluster(void (*kern)(KArgs...), dim3 grid, int threads, int s
   attr[0].val.clusterDim.x = cluster;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = beside ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, KArgs(args)...);
 }
 
-// CTAs to a cluster: as many as leave each of them `least` steps of `steps`, while
-// `units` clusters do not fill the GPU four CTAs deep.
-int pick_split(int64_t units, int64_t steps, int least) {
-  int s = 1;
-  while (s < 8 && steps / (2 * s) >= least && units * s < 4 * device_sm_count()) s *= 2;
-  return s;
-}
-
-int64_t max_blocks(const Plan& p) { return (p.T + kRows - 1) / kRows + p.n; }
-
-template <int R>
-cudaError_t shrink(const __nv_bfloat16* in, const __nv_bfloat16* P, const float* scales, float* V,
-                   int K, int r, const Plan& plan, cudaStream_t st) {
-  static bool configured[kMaxDevices] = {};
-  const int64_t blocks = max_blocks(plan);
-  const int split = pick_split(blocks, (K + 63) / 64, 4);
-  return launch_cluster(shrink_kernel<R>, dim3(static_cast<unsigned>(blocks * split)), 128,
-                        Shrink<R>::kBytes, split, configured, st, in, P, scales, V, K, r, split,
-                        plan);
+int64_t max_units(int64_t T, int n) { return (T + kRows - 1) / kRows + n; }
+int rank_up(int r) { return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128; }
+size_t up256(size_t b) { return (b + 255) / 256 * 256; }
+size_t image_bytes(int64_t T, int n, int r, int parts) {
+  return static_cast<size_t>(max_units(T, n)) * parts * (r > 64 ? 2 : 1) * kAtom;
 }
 
 template <int R>
-cudaError_t expand(const float* V, const __nv_bfloat16* Q, const float* scales,
-                   const __nv_bfloat16* base, __nv_bfloat16* out, int N, int r, const Plan& plan,
-                   cudaStream_t st) {
+cudaError_t shrink(const __nv_bfloat16* P, ShrinkArgs p, cudaStream_t st) {
   static bool configured[kMaxDevices] = {};
-  const int64_t blocks = max_blocks(plan);
-  const int tiles = (N + kCols - 1) / kCols;
+  CUtensorMap map;
+  if (!make_tmap_bf16_3d(&map, P, p.K, p.r, p.plan.n, 64, R)) return cudaErrorInvalidValue;
+  const int64_t units = max_units(p.plan.T, p.plan.n);
+  const int kblocks = (p.K + 63) / 64;
+  // CTAs to a cluster: until two an SM are there, each with four k-blocks at least
+  p.split = 1;
+  while (p.split < 8 && kblocks / (2 * p.split) >= 4 && units * p.split < 2 * device_sm_count())
+    p.split *= 2;
+  p.wait_ns = kDefaultWaitNs;
+  return launch(shrink_kernel<R>, dim3(static_cast<unsigned>(units * p.split)), Shrink<R>::kThreads,
+                Shrink<R>::kBytes, p.split, false, configured, st, map, p);
+}
+
+template <int R>
+cudaError_t expand(const __nv_bfloat16* Q, int r, ExpandArgs p, cudaStream_t st) {
+  static bool configured[kMaxDevices] = {};
+  CUtensorMap map;
+  if (!make_tmap_bf16_3d(&map, Q, p.N, r, p.plan.n, 64, R)) return cudaErrorInvalidValue;
+  const int64_t units = max_units(p.plan.T, p.plan.n);
+  const int tiles = (p.N + kCols - 1) / kCols;
+  // CTAs to a unit: until two an SM are there, each with two tiles at least
   int split = 1;
-  while (2 * split <= tiles && tiles / (2 * split) >= 2 && blocks * split < 8 * device_sm_count())
-    split *= 2;
-  return launch_cluster(expand_kernel<R>, dim3(static_cast<unsigned>(blocks), split), 128,
-                        Expand<R>::kBytes, 1, configured, st, V, Q, scales, base, out, N, r, plan);
+  while (tiles / (2 * split) >= 2 && units * split < 2 * device_sm_count()) split *= 2;
+  p.wait_ns = kDefaultWaitNs;
+  return launch(expand_kernel<R>, dim3(static_cast<unsigned>(units), split), kExpandThreads,
+                Expand<R>::kBytes, 1, true, configured, st, map, p);
 }
 
 template <int R>
-cudaError_t grad(const GradJob& j0, const GradJob& j1, int r, int accumulate, const Plan& plan,
-                 cudaStream_t st) {
-  static bool configured[kMaxDevices] = {};
-  const int wide = j0.N > j1.N ? j0.N : j1.N;
-  const int tiles = (wide + kCols - 1) / kCols;
-  const int split = pick_split(static_cast<int64_t>(tiles) * plan.n, plan.T / plan.n / kRows, 2);
-  return launch_cluster(grad_kernel<R>, dim3(tiles * split, plan.n, 2), 256, Grad<R>::kBytes, split,
-                        configured, st, j0, j1, r, split, accumulate, plan);
+cudaError_t grad(GradArgs p, cudaStream_t st) {
+  static bool configured[kMaxDevices] = {}, configured_finish[kMaxDevices] = {};
+  for (GradJob& j : p.job) j.tiles = (j.N + Grad<R>::kTile - 1) / Grad<R>::kTile;
+  p.wait_ns = kDefaultWaitNs;
+  const int ctas = device_sm_count();
+  const cudaError_t e = launch(grad_kernel<R>, dim3(ctas), Grad<R>::kThreads, Grad<R>::kBytes, 1,
+                               false, configured, st, p);
+  if (e != cudaSuccess) return e;
+  return launch(grad_finish_kernel<R>, dim3(p.job[0].tiles + p.job[1].tiles, p.plan.n),
+                Grad<R>::kTile, 0, 1, false, configured_finish, st, p, ctas);
 }
 
 #define MOE_BY_RANK(r, call)       \
@@ -882,8 +1255,24 @@ moe_status check_sizes(int64_t T, int H, int N, int n, int r) {
 }
 
 // The rows that one cluster each takes without a plan: every row reads its adapter
-// whole, which 64 rows of a block share otherwise.
+// whole, which the rows of a unit share otherwise.
 bool few_rows(int64_t T, int r) { return T <= 128 && T * r <= 4096; }
+
+// What the backward has in its workspace.
+struct BwdLayout {
+  size_t dv, v, partial, chunks, total;
+};
+BwdLayout bwd_layout(int64_t T, int n, int r) {
+  BwdLayout L;
+  const size_t img = up256(image_bytes(T, n, r, 3));
+  L.dv = 0;
+  L.v = img;
+  L.partial = 2 * img;
+  const size_t tile = r > 64 ? 128 : 256;
+  L.chunks = L.partial + up256(static_cast<size_t>(2) * device_sm_count() * rank_up(r) * tile * 4);
+  L.total = L.chunks + up256((n + 1) * sizeof(int));
+  return L;
+}
 
 }  // namespace
 
@@ -914,10 +1303,15 @@ moe_status moe_lora_plan(const int32_t* adapter_ids, int64_t T, int n, int32_t* 
   return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
+size_t moe_lora_workspace_size(int64_t T, int n, int r) {
+  if (check_sizes(T, 8, 8, n, r) != MOE_OK || T == 0 || few_rows(T, r)) return 0;
+  return up256(image_bytes(T, n, r, 2));
+}
+
 moe_status moe_lora(const void* x, const void* a, const void* b, const int32_t* adapter_ids,
                     const int32_t* order, const int32_t* offsets, const float* scales,
                     const void* base, int64_t T, int H, int N, int n, int r, void* out, float* v,
-                    void* stream) {
+                    void* workspace, size_t ws_bytes, void* stream) {
   MOE_ENTRY_RANGE();
   const moe_status s = check_sizes(T, H, N, n, r);
   if (s != MOE_OK) return s;
@@ -933,22 +1327,40 @@ moe_status moe_lora(const void* x, const void* a, const void* b, const int32_t* 
   auto* ob = static_cast<__nv_bfloat16*>(out);
   if (few_rows(T, r)) {
     static bool configured[kMaxDevices] = {};
-    return launch_cluster(few_kernel, dim3(static_cast<unsigned>(T) * kFewCtas), kFewThreads, 0,
-                          kFewCtas, configured, st, xb, ab, bb, adapter_ids, scales, yb, ob, v, H,
-                          N, n, r, device_error_word()) == cudaSuccess
+    return launch(few_kernel, dim3(static_cast<unsigned>(T) * kFewCtas), kFewThreads, 0, kFewCtas,
+                  false, configured, st, xb, ab, bb, adapter_ids, scales, yb, ob, v, H, N, n, r,
+                  device_error_word()) == cudaSuccess
                ? MOE_OK
                : MOE_ERR_CUDA;
   }
+  if (!workspace || ws_bytes < moe_lora_workspace_size(T, n, r) || !aligned16(workspace))
+    return MOE_ERR_WORKSPACE;
   const Plan plan = {order, offsets, T, n, device_error_word()};
-  if (MOE_BY_RANK(r, shrink)(xb, ab, nullptr, v, H, r, plan, st) != cudaSuccess ||
-      MOE_BY_RANK(r, expand)(v, bb, scales, yb, ob, N, r, plan, st) != cudaSuccess)
+  ShrinkArgs sh{};
+  sh.in = xb;
+  sh.scales = scales;
+  sh.V = v;
+  sh.img = static_cast<uint8_t*>(workspace);
+  sh.parts = 2;
+  sh.K = H;
+  sh.r = r;
+  sh.plan = plan;
+  ExpandArgs ex{};
+  ex.img = sh.img;
+  ex.parts = 2;
+  ex.base = yb;
+  ex.out = ob;
+  ex.N = N;
+  ex.plan = plan;
+  if (MOE_BY_RANK(r, shrink)(ab, sh, st) != cudaSuccess ||
+      MOE_BY_RANK(r, expand)(bb, r, ex, st) != cudaSuccess)
     return MOE_ERR_CUDA;
   return MOE_OK;
 }
 
-size_t moe_lora_backward_workspace_size(int64_t T, int r) {
-  if (T < 0 || T > INT32_MAX - 1024 || r < 1 || r > kMaxRank) return 0;
-  return (static_cast<size_t>(T) * r * sizeof(float) + 255) / 256 * 256;
+size_t moe_lora_backward_workspace_size(int64_t T, int n, int r) {
+  if (check_sizes(T, 8, 8, n, r) != MOE_OK || T == 0) return 0;
+  return bwd_layout(T, n, r).total;
 }
 
 moe_status moe_lora_backward(const void* dy, const void* x, const float* v, const void* a,
@@ -972,19 +1384,41 @@ moe_status moe_lora_backward(const void* dy, const void* x, const float* v, cons
   if (!dy || !x || !v || !a || !b || !order || !offsets || !dx || !aligned16(dy) ||
       !aligned16(x) || !aligned16(a) || !aligned16(b) || !aligned16(base) || !aligned16(dx))
     return MOE_ERR_INVALID_ARG;
-  if (!workspace || ws_bytes < moe_lora_backward_workspace_size(T, r) || !aligned16(workspace))
-    return MOE_ERR_WORKSPACE;
+  const BwdLayout L = bwd_layout(T, n, r);
+  if (!workspace || ws_bytes < L.total || !aligned16(workspace)) return MOE_ERR_WORKSPACE;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
   const Plan plan = {order, offsets, T, n, device_error_word()};
   const auto* gb = static_cast<const __nv_bfloat16*>(dy);
   const auto* xb = static_cast<const __nv_bfloat16*>(x);
-  const auto* ab = static_cast<const __nv_bfloat16*>(a);
-  const auto* bb = static_cast<const __nv_bfloat16*>(b);
-  float* dv = static_cast<float*>(workspace);
-  const GradJob ja = {dv, xb, nullptr, da, H}, jb = {v, gb, scales, db, N};
-  if (MOE_BY_RANK(r, shrink)(gb, bb, scales, dv, N, r, plan, st) != cudaSuccess ||
-      MOE_BY_RANK(r, expand)(dv, ab, nullptr, static_cast<const __nv_bfloat16*>(base),
-                             static_cast<__nv_bfloat16*>(dx), H, r, plan, st) != cudaSuccess ||
-      MOE_BY_RANK(r, grad)(ja, jb, r, accumulate, plan, st) != cudaSuccess)
+  ShrinkArgs sh{};
+  sh.in = gb;
+  sh.scales = scales;
+  sh.img = ws + L.dv;
+  sh.kept = v;
+  sh.img_kept = ws + L.v;
+  sh.parts = 3;
+  sh.K = N;
+  sh.r = r;
+  sh.plan = plan;
+  ExpandArgs ex{};
+  ex.img = sh.img;
+  ex.parts = 3;
+  ex.base = static_cast<const __nv_bfloat16*>(base);
+  ex.out = static_cast<__nv_bfloat16*>(dx);
+  ex.N = H;
+  ex.plan = plan;
+  GradArgs gr{};
+  gr.job[0] = {ws + L.dv, xb, da, H, 0};
+  gr.job[1] = {ws + L.v, gb, db, N, 0};
+  gr.partial = reinterpret_cast<float*>(ws + L.partial);
+  gr.chunks = reinterpret_cast<int*>(ws + L.chunks);
+  gr.r = r;
+  gr.accumulate = accumulate;
+  gr.units = static_cast<int>(max_units(T, n));
+  gr.plan = plan;
+  if (MOE_BY_RANK(r, shrink)(static_cast<const __nv_bfloat16*>(b), sh, st) != cudaSuccess ||
+      MOE_BY_RANK(r, expand)(static_cast<const __nv_bfloat16*>(a), r, ex, st) != cudaSuccess ||
+      MOE_BY_RANK(r, grad)(gr, st) != cudaSuccess)
     return MOE_ERR_CUDA;
   return MOE_OK;
 }

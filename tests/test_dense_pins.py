@@ -157,8 +157,14 @@ def test_dense_workspace_sizes(m):
     for bad in ((-1, 64, 64), (4, 60, 64), (4, 64, 60), (4, 0, 64), (4, 64, -8)):
         assert L.moe_gated_ffn_workspace_size(*bad) == 0, bad
         assert L.moe_gated_ffn_backward_workspace_size(*bad) == 0, bad
-    assert L.moe_lora_backward_workspace_size(100, 16) == 6400
-    assert L.moe_lora_backward_workspace_size(100, 129) == 0
+    # images of units of 128 rows: 16 KB a part and 64 ranks; none for few rows
+    assert L.moe_lora_workspace_size(1000, 4, 16) == (8 + 4) * 2 * 16384
+    assert L.moe_lora_workspace_size(1000, 4, 128) == (8 + 4) * 2 * 32768
+    assert L.moe_lora_workspace_size(64, 4, 16) == 0
+    assert L.moe_lora_backward_workspace_size(1000, 4, 16) > 2 * (8 + 4) * 3 * 16384
+    for bad in ((100, 4, 129), (-1, 4, 16), (100, 0, 16), (100, 1025, 16), (100, 4, 0)):
+        assert L.moe_lora_workspace_size(*bad) == 0
+        assert L.moe_lora_backward_workspace_size(*bad) == 0
     c = m.moe_dropout_config()
     L.moe_dropout_config_init(c)
     assert abs(c.p - 0.1) < 1e-7 and c.residual_scale == 1.0 and c.branch_scale == 1.0
@@ -207,8 +213,8 @@ def test_dense_entry_points_refuse_before_any_launch(m):
         assert plan(**kw) == INV, kw
 
     def lora(x=P, a=P, b=P, ids=P, order=P, off=P, s=None, base=None, T=4, H=64, N=64, n=2, r=8,
-             out=P, v=P):
-        return L.moe_lora(x, a, b, ids, order, off, s, base, T, H, N, n, r, out, v, None)
+             out=P, v=P, ws=P, nb=BIG):
+        return L.moe_lora(x, a, b, ids, order, off, s, base, T, H, N, n, r, out, v, ws, nb, None)
 
     assert lora(T=0, x=None) == 0
     for kw in (dict(x=None), dict(a=None), dict(b=None), dict(ids=None), dict(order=None),
@@ -218,6 +224,9 @@ def test_dense_entry_points_refuse_before_any_launch(m):
         assert lora(**kw) == INV, kw
     for kw in (dict(H=60), dict(N=12), dict(r=129)):
         assert lora(**kw) == UNS, kw
+
+    for kw in (dict(ws=None), dict(nb=255), dict(ws=U)):
+        assert lora(T=500, **kw) == WS, kw
 
     def lora_b(dy=P, x=P, v=P, a=P, b=P, order=P, off=P, s=None, base=None, T=4, H=64, N=64, n=2,
                r=8, dx=P, da=P, db=P, acc=0, ws=P, nb=BIG):

@@ -168,7 +168,8 @@ def test_lora_bad_ids_and_plans(T):
         o[where] = value
         m.moe_lora(**v, adapter_ids=ids, plan=(o, offsets), base=base)
         assert m.moe_get_error() == 3, (where, value)
-    for where, value in ((0, 1), (0, -5), (1, T + 9), (2, -1), (4, T + 1), (3, 2 ** 31 - 1)):
+    for where, value in ((0, 1), (0, -5), (1, T + 9), (2, -1), (4, T + 1), (3, 2 ** 31 - 1),
+                         (1, T), (2, 0)):
         o = offsets.clone()
         o[where] = value
         f = m.moe_lora(**v, adapter_ids=ids, plan=(order, o), base=base)
@@ -266,7 +267,7 @@ def test_lora_refusals():
         m.moe_lora(**v, adapter_ids=ids, base=base[:, :64].contiguous())
     with pytest.raises(m.MoeError, match="unsupported"):
         m.moe_lora(v["x"], torch.zeros(1, 200, 64, dtype=BF, device="cuda"),
-                   torch.zeros(1, 200, 72, dtype=BF, device="cuda"), ids)
+                   torch.zeros(1, 200, 72, dtype=BF, device="cuda"), torch.zeros_like(ids))
     with pytest.raises(m.MoeError, match="unsupported"):
         m.moe_lora(v["x"], v["a"], v["b"][:, :, :70].contiguous(), ids)
     f = m.moe_lora(**v, adapter_ids=ids)
@@ -274,3 +275,4 @@ def test_lora_refusals():
         m.moe_lora_backward(dy, v["x"], f["v"], v["a"], v["b"], ids, accumulate=True)
     with pytest.raises(ValueError, match="v must"):
         m.moe_lora_backward(dy, v["x"], f["v"][:, :4].contiguous(), v["a"], v["b"], ids)
+    assert m.moe_get_error() == 0
