@@ -59,15 +59,6 @@ struct Args {
   unsigned long long wait_ns;
 };
 
-__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr, uint32_t rank) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(mapa_shared(addr, rank))
-               : "memory");
-  return v;
-}
-
 __device__ __forceinline__ float act_any(int act, float z) {
   switch (act) {
     case MOE_ACT_SILU: return act_f<MOE_ACT_SILU>(z);

@@ -63,6 +63,7 @@ __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr, uint32_t rank) {
   float v;
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(mapa_shared(addr, rank)) : "memory");
@@ -396,31 +397,50 @@ __global__ void __launch_bounds__(Shrink<R>::kThreads, R > 64 ? 1 : 2)
   }
   __syncthreads();                               // the ring has been read
 
-  // sums as [column][row]
+  // sums as [row][column], 16-byte piece c of row i at c ^ (i & kMix)
+  constexpr int kMix = R >= 32 ? 7 : 3;
   float* part = reinterpret_cast<float*>(ring);
   if (warp >= 2 && warp < 2 + 4 * S::kGroups) {
     const int row = (warp & 3) * 32 + lane;
 #pragma unroll
-    for (int j = 0; j < S::kOwn; ++j) part[(j0 + j) * kRows + row] = sum[j];
+    for (int j = 0; j < S::kOwn; j += 4)
+      *reinterpret_cast<float4*>(part + row * R + ((((j0 + j) >> 2) ^ (row & kMix)) << 2)) =
+          make_float4(sum[j], sum[j + 1], sum[j + 2], sum[j + 3]);
   }
   if (p.split > 1) cluster_sync();
   else __syncthreads();
   const float f = p.scales ? __ldg(p.scales + u.a) : 1.0f;
   const uint32_t part0 = smem_u32(part);
-  const int share = kRows * (R / 8) / p.split;    // eight columns of a row each
-  for (int i = tid; i < share; i += S::kThreads) {
-    const int e = static_cast<int>(rank) * share + i, row = e % kRows, c = e / kRows;
+  // eight columns of a row at a time, dealt out over the cluster
+  for (int e = static_cast<int>(rank) + p.split * tid; e < kRows * (R / 8);
+       e += p.split * S::kThreads) {
+    const int row = e % kRows, c = e / kRows;
     const int g = rows[row];
+    const uint32_t at0 = part0 + (row * R + (((2 * c) ^ (row & kMix)) << 2)) * 4;
+    const uint32_t at1 = part0 + (row * R + (((2 * c + 1) ^ (row & kMix)) << 2)) * 4;
     float v[8];
+    auto add_up = [&](uint32_t at, float* to) {
+      float4 a[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (q < p.split) a[q] = ld_cluster_f32x4(at, q);
+      to[0] = a[0].x;
+      to[1] = a[0].y;
+      to[2] = a[0].z;
+      to[3] = a[0].w;
+#pragma unroll
+      for (int q = 1; q < 8; ++q)
+        if (q < p.split) {
+          to[0] += a[q].x;
+          to[1] += a[q].y;
+          to[2] += a[q].z;
+          to[3] += a[q].w;
+        }
+    };
+    add_up(at0, v);
+    add_up(at1, v + 4);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int at = (c * 8 + j) * kRows + row;
-      v[j] = 0.0f;
-      if (p.split > 1) {
-        for (int q = 0; q < p.split; ++q) v[j] += ld_cluster_f32(part0 + at * 4, q);
-      } else {
-        v[j] = part[at];
-      }
       if (g < 0 || c * 8 + j >= p.r) v[j] = 0.0f;
       else if (p.V) p.V[static_cast<int64_t>(g) * p.r + c * 8 + j] = v[j];
       v[j] *= f;
@@ -458,21 +478,22 @@ __global__ void __launch_bounds__(Shrink<R>::kThreads, R > 64 ? 1 : 2)
 
 // ------------------------------------------------------------------ expand
 
-// A CTA takes a unit and every gridDim.y-th tile of 128 columns. Warps: 0 loads the
-// image and Q, 1 issues the MMAs, 2 to 5 add base and store: 32 rows x 64 columns at a
-// time through shared memory, so that rows move in runs of 128 bytes, the next such
-// piece of base on its way and the ones after it asked into L2.
-constexpr int kCols = 128;
+// A CTA takes a unit and every gridDim.y-th tile of 64 columns. Warps: 0 loads the
+// image and Q, 1 issues the MMAs, 2 to 5 finish every second tile and 6 to 9 the
+// others: base comes in by runs of 128 bytes a row, a tile ahead in registers, and goes
+// through 4 KB of shared memory a warp, in which each lane adds its row of the
+// accumulator, back into runs of 128 bytes.
+constexpr int kCols = 64;
 constexpr int kPiece = 32 * 128;
-constexpr int kSlots = 2;
-constexpr int kExpandThreads = 192;
+constexpr int kExpandThreads = 320;
+constexpr int kExpandAcc = 4;                     // accumulators: two to each half of the warps
 
 template <int R>
 struct Expand {
   static constexpr int kImg = 2 * part_bytes<R>();
-  static constexpr int kQ = 2 * R * 128;          // two boxes of 64 columns
-  static constexpr int kStages = 2;
-  static constexpr int kBytes = 1024 + kImg + kStages * kQ + 4 * kSlots * kPiece;
+  static constexpr int kQ = R * 128;
+  static constexpr int kStages = 3;
+  static constexpr int kBytes = 1024 + kImg + kStages * kQ + 8 * kPiece;
 };
 
 struct ExpandArgs {
@@ -486,12 +507,13 @@ struct ExpandArgs {
 };
 
 template <int R>
-__global__ void __launch_bounds__(kExpandThreads)
+__global__ void __launch_bounds__(kExpandThreads, R > 64 ? 1 : 2)
     expand_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ ExpandArgs p) {
   using S = Expand<R>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ int rows[kRows];
-  __shared__ uint64_t full[S::kStages], empty[S::kStages], tfull[2], tempty[2], image;
+  __shared__ uint64_t full[S::kStages], empty[S::kStages], tfull[kExpandAcc], tempty[kExpandAcc],
+      image;
   __shared__ uint32_t tmem_at;
   __shared__ int stop, zero;
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -505,7 +527,6 @@ __global__ void __launch_bounds__(kExpandThreads)
     return;
   }
   if (tid < kRows) rows[tid] = tid < u.rows ? plan_row(p.plan, u.lo + tid) : -1;
-  const int tiles = (p.N + kCols - 1) / kCols;
   if (none) {                                    // base as it is, or zeros
     __syncthreads();
     const int nv = p.N / 8;
@@ -519,12 +540,15 @@ __global__ void __launch_bounds__(kExpandThreads)
     grid_dependency_wait();
     return;
   }
+  const int tiles = (p.N + kCols - 1) / kCols;
+  const int t0 = blockIdx.y, dt = gridDim.y;
+  const int steps = t0 < tiles ? (tiles - t0 + dt - 1) / dt : 0;
   if (tid == 0) {
     for (int s = 0; s < S::kStages; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
       mbar_init(smem_u32(&empty[s]), 1);
     }
-    for (int a = 0; a < 2; ++a) {
+    for (int a = 0; a < kExpandAcc; ++a) {
       mbar_init(smem_u32(&tfull[a]), 1);
       mbar_init(smem_u32(&tempty[a]), 4);
     }
@@ -534,29 +558,26 @@ __global__ void __launch_bounds__(kExpandThreads)
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(&tmem_at), 256);
+    tmem_alloc(smem_u32(&tmem_at), kExpandAcc * kCols);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_at, img0 = smem_u32(smem), q0 = img0 + S::kImg;
-  const int t0 = blockIdx.y, dt = gridDim.y;
   volatile int* stopped = &stop;
   bool ok = true;
 
   if (warp == 0) {
     if (lane == 0) {
+      if (steps == 0) grid_dependency_wait();
       int i = 0;
-      if (t0 >= tiles) grid_dependency_wait();
-      for (int t = t0; t < tiles; t += dt, ++i) {
+      for (; i < steps; ++i) {
         const int s = i % S::kStages;
         ok = mbar_wait(smem_u32(&empty[s]), ((i / S::kStages) & 1) ^ 1, p.wait_ns, stopped);
         if (!ok) break;
-        const uint32_t sq = q0 + s * S::kQ, bar = smem_u32(&full[s]);
-        mbar_arrive_expect_tx(bar, S::kQ);
-        tma_load_3d(sq, &map_q, bar, t * kCols, 0, u.a);
-        tma_load_3d(sq + R * 128, &map_q, bar, t * kCols + 64, 0, u.a);
+        mbar_arrive_expect_tx(smem_u32(&full[s]), S::kQ);
+        tma_load_3d(q0 + s * S::kQ, &map_q, smem_u32(&full[s]), (t0 + i * dt) * kCols, 0, u.a);
         if (i == 0) {                            // Q is there before the image is written
           grid_dependency_wait();
           fence_proxy_async();
@@ -572,15 +593,14 @@ __global__ void __launch_bounds__(kExpandThreads)
   } else if (warp == 1) {
     if (lane == 0) {
       const uint32_t idesc = idesc_bf16(128, kCols, false, true);
-      ok = t0 >= tiles || mbar_wait(smem_u32(&image), 0, p.wait_ns, stopped);
-      int i = 0;
-      for (int t = t0; t < tiles && ok; t += dt, ++i) {
-        const int s = i % S::kStages, a = i & 1;
-        ok = mbar_wait(smem_u32(&tempty[a]), ((i >> 1) & 1) ^ 1, p.wait_ns, stopped) &&
+      ok = steps == 0 || mbar_wait(smem_u32(&image), 0, p.wait_ns, stopped);
+      for (int i = 0; i < steps && ok; ++i) {
+        const int s = i % S::kStages, a = i % kExpandAcc;
+        ok = mbar_wait(smem_u32(&tempty[a]), ((i / kExpandAcc) & 1) ^ 1, p.wait_ns, stopped) &&
              mbar_wait(smem_u32(&full[s]), (i / S::kStages) & 1, p.wait_ns, stopped);
         if (!ok) break;
         tc_fence_after();
-        const uint64_t bd = sdesc_sw128(q0 + s * S::kQ, R * 128, 1024);
+        const uint64_t bd = sdesc_sw128(q0 + s * S::kQ, S::kQ, 1024);
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -594,109 +614,80 @@ __global__ void __launch_bounds__(kExpandThreads)
       }
     }
   } else {
-    const int q = warp & 3;
-    const uint32_t slot0 = smem_u32(smem) + S::kImg + S::kStages * S::kQ + q * kSlots * kPiece;
-    const int ch = lane & 7, w0 = q * 32 + (lane >> 3);
-    const int mine = rows[q * 32 + lane];        // this lane's row of the accumulator
-    const bool any = __any_sync(0xffffffffu, mine >= 0);
-    // the piece after (t, half): columns, or -1
-    auto next = [&](int t, int half) { return half == 0 ? t * kCols + 64 : (t + dt) * kCols; };
-    auto load = [&](int col, int slot) {
-      if (p.base && col < p.N) {
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    uint8_t* st = smem + S::kImg + S::kStages * S::kQ + (warp - 2) * kPiece;
+    const int ch = lane & 7, r0 = lane >> 3;     // of the runs: rows r0, r0 + 4, ... of 32
+    int g[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int row = w0 + 4 * i, g = rows[row];
-          const bool here = g >= 0 && col + ch * 8 < p.N;
-          cp_async_16z(slot0 + slot * kPiece + (row & 31) * 128 + ((ch ^ (row & 7)) << 4),
-                       here ? p.base + static_cast<int64_t>(g) * p.N + col + ch * 8 : p.base, here);
-        }
-      }
-      cp_commit();
+    for (int j = 0; j < 8; ++j) g[j] = rows[q * 32 + r0 + 4 * j];
+    const bool any = __any_sync(0xffffffffu, rows[q * 32 + lane] >= 0);
+    uint4 next[8];
+    auto load = [&](int i) {                     // base of step i
+      const int col = (t0 + i * dt) * kCols + ch * 8;
+      const bool here = p.base && i < steps && col < p.N;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        next[j] = here && g[j] >= 0
+                      ? __ldcs(reinterpret_cast<const uint4*>(p.base + static_cast<int64_t>(g[j]) * p.N + col))
+                      : make_uint4(0, 0, 0, 0);
     };
-    auto ask = [&](int col) {
-      if (p.base && mine >= 0 && col < p.N)
-        prefetch_l2(p.base + static_cast<int64_t>(mine) * p.N + col);
-    };
-    int i = 0, slot = 0;
-    if (t0 < tiles && any) {
-      load(t0 * kCols, 0);
-      ask(t0 * kCols + 64);
-      ask((t0 + dt) * kCols);
-      ask((t0 + dt) * kCols + 64);
-    }
-    for (int t = t0; t < tiles; t += dt, ++i) {
-      const int a = i & 1;
-      if (any) {
-        ask((t + 2 * dt) * kCols);
-        ask((t + 2 * dt) * kCols + 64);
+    load(half);
+    for (int i = half; i < steps; i += 2) {
+      const int a = i % kExpandAcc;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int row = r0 + 4 * j;
+        *reinterpret_cast<uint4*>(st + row * 128 + ((ch ^ (row & 7)) << 4)) = next[j];
       }
-      const bool got = mbar_wait(smem_u32(&tfull[a]), (i >> 1) & 1, p.wait_ns, stopped);
+      __syncwarp();
+      load(i + 2);
+      const bool got = mbar_wait(smem_u32(&tfull[a]), (i / kExpandAcc) & 1, p.wait_ns, stopped);
       ok = __all_sync(0xffffffffu, got);
       if (!ok) break;
       tc_fence_after();
-      if (any) {
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          const int col = t * kCols + half * 64;
-          if (col >= p.N) break;
-          load(next(t, half), slot ^ 1);
-          uint32_t v[64];
-          const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + a * kCols + half * 64;
-          tmem_ld_32x32b_x32(taddr, v);
-          tmem_ld_32x32b_x32(taddr + 32, v + 32);
-          tmem_ld_wait();
-          cp_wait<1>();                          // this piece of base
-          __syncwarp();
-          uint8_t* st = smem + S::kImg + S::kStages * S::kQ + (q * kSlots + slot) * kPiece;
+      const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + a * kCols;
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            uint4* w = reinterpret_cast<uint4*>(st + lane * 128 + ((c ^ (lane & 7)) << 4));
-            float x[8];
+      for (int c0 = 0; c0 < 8; c0 += 2) {
+        uint32_t v[16];
+        tmem_ld_32x32b_x16(taddr + c0 * 8, v);
+        tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(v[c * 8 + j]);
-            if (p.base) {
-              const uint4 o = *w;
-              const uint32_t b[4] = {o.x, o.y, o.z, o.w};
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                x[2 * j] += lo_f(b[j]);
-                x[2 * j + 1] += hi_f(b[j]);
-              }
-            }
-            *w = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                            pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
-          }
-          __syncwarp();
-          if (col + ch * 8 < p.N) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const int row = w0 + 4 * j, g = rows[row];
-              if (g >= 0)
-                __stcs(reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(g) * p.N + col + ch * 8),
-                       *reinterpret_cast<const uint4*>(st + (row & 31) * 128 +
-                                                       ((ch ^ (row & 7)) << 4)));
-            }
-          }
-          __syncwarp();                          // the slot may be filled again
-          slot ^= 1;
+        for (int c = 0; c < 2; ++c) {
+          uint4* w = reinterpret_cast<uint4*>(st + lane * 128 + (((c0 + c) ^ (lane & 7)) << 4));
+          const uint4 o = *w;
+          const float* x = reinterpret_cast<const float*>(v + c * 8);
+          *w = make_uint4(pack_bf16x2(x[0] + lo_f(o.x), x[1] + hi_f(o.x)),
+                          pack_bf16x2(x[2] + lo_f(o.y), x[3] + hi_f(o.y)),
+                          pack_bf16x2(x[4] + lo_f(o.z), x[5] + hi_f(o.z)),
+                          pack_bf16x2(x[6] + lo_f(o.w), x[7] + hi_f(o.w)));
         }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&tempty[a]));
+      const int col = (t0 + i * dt) * kCols + ch * 8;
+      if (any && col < p.N) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int row = r0 + 4 * j;
+          if (g[j] >= 0)
+            __stcs(reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(g[j]) * p.N + col),
+                   *reinterpret_cast<const uint4*>(st + row * 128 + ((ch ^ (row & 7)) << 4)));
+        }
+      }
+      __syncwarp();                              // the piece may be filled again
     }
-    cp_wait<0>();
   }
   if (!ok) {
     stop = 1;
     report_error(p.plan.err, kErrTimeout);
-    if (warp == 1 && lane == 0 && t0 < tiles) mbar_wait(smem_u32(&image), 0, kDrainNs, &zero);
+    if (warp == 1 && lane == 0) mbar_wait(smem_u32(&image), 0, kDrainNs, &zero);
   }
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 256);
+    tmem_dealloc(tmem, kExpandAcc * kCols);
   }
 }
 
@@ -939,20 +930,28 @@ __global__ void __launch_bounds__(Grad<R>::kThreads, 1)
     constexpr int kVec = S::kTile / 8;           // 16-byte pieces of a row: 32 or 16
     constexpr int kPer = 32 / kVec;              // rows of a warp's instruction
     const int ch = lane % kVec, sub = lane / kVec;
-    auto row_of = [&](const Walk& x) {           // lane l: the chunk's row 4 l + g, or -1
+    // lane l: the chunk's row 4 l + g as the plan has it (checked when it is used, so
+    // that nothing waits for it before), -1 past the adapter
+    auto row_of = [&](const Walk& x) {
       const int at = begin[x.a] + (x.c - chunks[x.a]) * 64 + 4 * lane + g;
-      return (lane < 16 && at < end[x.a]) ? plan_row(p.plan, at) : -1;
+      return (lane < 16 && at < end[x.a]) ? __ldg(p.plan.order + at) : -1;
     };
     int mine = row_of(w);
+    bool inside = lane < 16 && begin[w.a] + (w.c - chunks[w.a]) * 64 + 4 * lane + g < end[w.a];
     for (int i = 0; i < steps; ++i) {
       const int s = i % S::kStages;
       const GradJob& job = p.job[w.tile >= t0];
       const int col = (w.tile >= t0 ? w.tile - t0 : w.tile) * S::kTile + ch * 8;
       const bool in_n = col < job.N;
-      const int here = mine;
+      int here = mine;
+      if (inside && (here < 0 || here >= p.plan.T)) {
+        report_error(p.plan.err, kErrBadId);
+        here = -1;
+      }
       if (i + 1 < steps) {
         w.next(total, chunks);
         mine = row_of(w);
+        inside = lane < 16 && begin[w.a] + (w.c - chunks[w.a]) * 64 + 4 * lane + g < end[w.a];
       }
       const bool got = mbar_wait(smem_u32(&empty[s]), ((i / S::kStages) & 1) ^ 1, p.wait_ns, stopped);
       ok = __all_sync(0xffffffffu, got);
@@ -986,7 +985,9 @@ __global__ void __launch_bounds__(Grad<R>::kThreads, 1)
 }
 
 // The outputs that more than one CTA added to, in the order of the CTAs, and those of
-// adapters without rows.
+// adapters without rows; kFinishRanks ranks of a tile to a CTA.
+constexpr int kFinishRanks = 8;
+
 template <int R>
 __global__ void __launch_bounds__(Grad<R>::kTile)
     grad_finish_kernel(const __grid_constant__ GradArgs p, int ctas) {
@@ -996,9 +997,11 @@ __global__ void __launch_bounds__(Grad<R>::kTile)
   const int col = (tile >= t0 ? tile - t0 : tile) * S::kTile + threadIdx.x;
   const int total = p.chunks[n], c0 = p.chunks[a], c1 = p.chunks[a + 1];
   float* g = job.G + static_cast<int64_t>(a) * p.r * job.N + col;
+  const int j0 = blockIdx.z * kFinishRanks, j1 = min(p.r, j0 + kFinishRanks);
+  if (col >= job.N) return;
   if (c0 == c1) {
-    if (col < job.N && !p.accumulate)
-      for (int j = 0; j < p.r; ++j) g[static_cast<int64_t>(j) * job.N] = 0.0f;
+    if (!p.accumulate)
+      for (int j = j0; j < j1; ++j) g[static_cast<int64_t>(j) * job.N] = 0.0f;
     return;
   }
   const int64_t items = static_cast<int64_t>(t0 + p.job[1].tiles) * total;
@@ -1013,33 +1016,42 @@ __global__ void __launch_bounds__(Grad<R>::kTile)
     return lo;
   };
   const int b0 = owner(i0), b1 = owner(i1 - 1);
-  if (b0 == b1 || col >= job.N) return;
-  for (int j = 0; j < p.r; ++j) {
-    float v = 0.0f;
-    for (int b = b0; b <= b1; ++b) {
-      const int64_t first = first_item(items, ctas, b);
-      if (first == first_item(items, ctas, b + 1)) continue;      // a CTA without items
-      const int slot = 2 * b + (first >= i0 ? 0 : 1);
-      v += p.partial[(static_cast<int64_t>(slot) * R + j) * S::kTile + threadIdx.x];
-    }
-    float* at = g + static_cast<int64_t>(j) * job.N;
-    *at = p.accumulate ? *at + v : v;
+  if (b0 == b1) return;
+  float v[kFinishRanks];
+#pragma unroll
+  for (int j = 0; j < kFinishRanks; ++j) v[j] = 0.0f;
+  for (int b = b0; b <= b1; ++b) {
+    const int64_t first = first_item(items, ctas, b);
+    if (first == first_item(items, ctas, b + 1)) continue;        // a CTA without items
+    const int slot = 2 * b + (first >= i0 ? 0 : 1);
+    const float* src = p.partial + (static_cast<int64_t>(slot) * R + j0) * S::kTile + threadIdx.x;
+#pragma unroll
+    for (int j = 0; j < kFinishRanks; ++j) v[j] += src[j * S::kTile];
   }
+#pragma unroll
+  for (int j = 0; j < kFinishRanks; ++j)
+    if (j0 + j < j1) {
+      float* at = g + static_cast<int64_t>(j0 + j) * job.N;
+      *at = p.accumulate ? *at + v[j] : v[j];
+    }
 }
 
 // ------------------------------------------------------------------ few rows
 
 constexpr int kFewCtas = 8;         // CTAs of a row's cluster
 constexpr int kFewThreads = 256;
+constexpr int kFewAhead = 44 * 1024;   // bytes of B that are fetched before v is known
 
 // One cluster a row: each CTA takes an eighth of H for v and, once the cluster has
-// added v up, an eighth of N for out. The first values of B are on their way
-// before v is known. No plan, one launch.
-__global__ void __launch_bounds__(kFewThreads)
+// added v up, an eighth of N for out. What the CTA needs of B is on its way into shared
+// memory (as much as kFewAhead holds) and base in registers before v is known. No plan,
+// one launch; what bounds it is the latency of three loads and two cluster barriers.
+__global__ void __launch_bounds__(kFewThreads, 4)
     few_kernel(const __nv_bfloat16* __restrict__ x, const __nv_bfloat16* __restrict__ A,
                const __nv_bfloat16* __restrict__ B, const int32_t* __restrict__ ids,
                const float* __restrict__ scales, const __nv_bfloat16* base, __nv_bfloat16* out,
                float* __restrict__ v, int H, int N, int n, int r, int* err) {
+  extern __shared__ uint4 ahead[];                // [ranks][vectors of this CTA]
   __shared__ float part[kMaxRank];                // this CTA's share of v
   __shared__ float whole[kMaxRank];
   __shared__ float red[kFewThreads * 8];
@@ -1054,54 +1066,77 @@ __global__ void __launch_bounds__(kFewThreads)
   const int h0 = min(hv, static_cast<int>(rank) * hper), h1 = min(hv, h0 + hper);
   const int nv = N / 8, nper = (nv + kFewCtas - 1) / kFewCtas;
   const int n0 = min(nv, static_cast<int>(rank) * nper), n1 = min(nv, n0 + nper);
-  const __nv_bfloat16* xr = x + t * H;
-  const __nv_bfloat16* Aa = A + static_cast<int64_t>(on ? id : 0) * r * H;
-  const __nv_bfloat16* Ba = B + static_cast<int64_t>(on ? id : 0) * r * N;
+  const int vecs = n1 - n0;
+  const uint4* xr = reinterpret_cast<const uint4*>(x + t * H);
+  const uint4* Aa = reinterpret_cast<const uint4*>(A + static_cast<int64_t>(on ? id : 0) * r * H);
+  const uint4* Ba = reinterpret_cast<const uint4*>(B + static_cast<int64_t>(on ? id : 0) * r * N);
   auto dot8 = [](const uint4& p, const uint4& q, float acc) {
     const uint32_t a[4] = {p.x, p.y, p.z, p.w}, b[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      acc = fmaf(__uint_as_float(a[i] << 16), __uint_as_float(b[i] << 16), acc);
-      acc = fmaf(__uint_as_float(a[i] & 0xFFFF0000u), __uint_as_float(b[i] & 0xFFFF0000u), acc);
+      acc = fmaf(lo_f(a[i]), lo_f(b[i]), acc);
+      acc = fmaf(hi_f(a[i]), hi_f(b[i]), acc);
     }
     return acc;
   };
-  // groups of threads share the rank where a CTA's columns are few
+  const int fetched = on && vecs > 0 ? min(r, kFewAhead / 16 / vecs) : 0;
+  if (on) {
+    // the ranks of a warp two at a time, so that their loads overlap
+    for (int j = warp; j < r; j += kFewThreads / 16) {
+      const int k = min(j + kFewThreads / 32, r - 1);
+      float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll 2
+      for (int h = h0 + lane; h < h1; h += 32) {
+        const uint4 xv = __ldg(xr + h);
+        const uint4 a0 = __ldg(Aa + static_cast<int64_t>(j) * hv + h);
+        const uint4 a1 = __ldg(Aa + static_cast<int64_t>(k) * hv + h);
+        s0 = dot8(xv, a0, s0);
+        s1 = dot8(xv, a1, s1);
+      }
+      if (j == warp) {                             // behind the first loads of A
+        for (int e = tid; e < fetched * vecs; e += kFewThreads)
+          cp_async_16(smem_u32(ahead + e), Ba + static_cast<int64_t>(e / vecs) * nv + n0 + e % vecs);
+        cp_commit();
+      }
+#pragma unroll
+      for (int d = 16; d; d >>= 1) {
+        s0 += __shfl_xor_sync(0xffffffffu, s0, d);
+        s1 += __shfl_xor_sync(0xffffffffu, s1, d);
+      }
+      if (lane == 0) {
+        part[j] = s0;
+        part[k] = s1;
+      }
+    }
+    if (warp >= r) {                               // warps without a rank fetch their share too
+      for (int e = tid; e < fetched * vecs; e += kFewThreads)
+        cp_async_16(smem_u32(ahead + e), Ba + static_cast<int64_t>(e / vecs) * nv + n0 + e % vecs);
+      cp_commit();
+    }
+  }
+  // groups of threads share the ranks where a CTA's columns are few
   int groups = 1;
-  while (groups < 32 && 2 * groups * (n1 - n0) <= kFewThreads) groups *= 2;
+  while (groups < 32 && 2 * groups * vecs <= kFewThreads) groups *= 2;
   const int width = kFewThreads / groups;          // threads of a group
   const int grp = tid / width, col = tid % width;
-  constexpr int kAhead = 8;
-  uint4 ahead[kAhead];
-  const bool early = on && n0 + col < n1;
-#pragma unroll
-  for (int i = 0; i < kAhead; ++i) {
-    const int j = grp + i * groups;
-    ahead[i] = (early && j < r)
-                   ? __ldg(reinterpret_cast<const uint4*>(Ba + static_cast<int64_t>(j) * N) + n0 + col)
-                   : make_uint4(0, 0, 0, 0);
-  }
+  uint4 first = make_uint4(0, 0, 0, 0);            // base of the first columns
+  if (base && grp == 0 && n0 + col < n1)
+    first = *(reinterpret_cast<const uint4*>(base + t * N) + n0 + col);
   if (on) {
-    for (int j = warp; j < r; j += kFewThreads / 32) {
-      float s = 0.0f;
-#pragma unroll 4
-      for (int h = h0 + lane; h < h1; h += 32)
-        s = dot8(__ldg(reinterpret_cast<const uint4*>(xr) + h),
-                 __ldg(reinterpret_cast<const uint4*>(Aa + static_cast<int64_t>(j) * H) + h), s);
-#pragma unroll
-      for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-      if (lane == 0) part[j] = s;
-    }
     cluster_sync();
     const float f = scales ? __ldg(scales + id) : 1.0f;
     for (int j = tid; j < r; j += kFewThreads) {
-      float s = 0.0f;
+      float s[kFewCtas];
 #pragma unroll
-      for (int q = 0; q < kFewCtas; ++q) s += ld_cluster_f32(smem_u32(part + j), q);
-      if (rank == 0) v[t * r + j] = s;
-      whole[j] = f * s;
+      for (int q = 0; q < kFewCtas; ++q) s[q] = ld_cluster_f32(smem_u32(part + j), q);
+      float sum = s[0];
+#pragma unroll
+      for (int q = 1; q < kFewCtas; ++q) sum += s[q];
+      if (rank == 0) v[t * r + j] = sum;
+      whole[j] = f * sum;
     }
-    cluster_sync();                                // part has been read, whole is there
+    cp_wait<0>();
+    cluster_sync();                                // part has been read; whole and B are there
   } else if (rank == 0) {
     for (int j = tid; j < r; j += kFewThreads) v[t * r + j] = 0.0f;
   }
@@ -1115,21 +1150,16 @@ __global__ void __launch_bounds__(kFewThreads)
       const uint32_t b[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        acc[2 * i] = fmaf(w, __uint_as_float(b[i] << 16), acc[2 * i]);
-        acc[2 * i + 1] = fmaf(w, __uint_as_float(b[i] & 0xFFFF0000u), acc[2 * i + 1]);
+        acc[2 * i] = fmaf(w, lo_f(b[i]), acc[2 * i]);
+        acc[2 * i + 1] = fmaf(w, hi_f(b[i]), acc[2 * i + 1]);
       }
     };
     if (on && live) {
-      int i0 = 0;
-      if (c0 == n0) {
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-          if (grp + i * groups < r) add(ahead[i], whole[grp + i * groups]);
-        i0 = kAhead;
-      }
-#pragma unroll 8
-      for (int j = grp + i0 * groups; j < r; j += groups)
-        add(__ldg(reinterpret_cast<const uint4*>(Ba + static_cast<int64_t>(j) * N) + c), whole[j]);
+      int j = grp;
+#pragma unroll 4
+      for (; j < fetched; j += groups) add(ahead[j * vecs + c - n0], whole[j]);
+#pragma unroll 4
+      for (; j < r; j += groups) add(__ldg(Ba + static_cast<int64_t>(j) * nv + c), whole[j]);
     }
     if (groups > 1) {
       __syncthreads();
@@ -1143,12 +1173,12 @@ __global__ void __launch_bounds__(kFewThreads)
     }
     if (grp == 0 && live) {
       if (base) {
-        const uint4 o = *(reinterpret_cast<const uint4*>(base + t * N) + c);
+        const uint4 o = c0 == n0 ? first : *(reinterpret_cast<const uint4*>(base + t * N) + c);
         const uint32_t b[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          acc[2 * i] += __uint_as_float(b[i] << 16);
-          acc[2 * i + 1] += __uint_as_float(b[i] & 0xFFFF0000u);
+          acc[2 * i] += lo_f(b[i]);
+          acc[2 * i + 1] += hi_f(b[i]);
         }
       }
       *(reinterpret_cast<uint4*>(out + t * N) + c) =
@@ -1202,10 +1232,11 @@ cudaError_t shrink(const __nv_bfloat16* P, ShrinkArgs p, cudaStream_t st) {
   if (!make_tmap_bf16_3d(&map, P, p.K, p.r, p.plan.n, 64, R)) return cudaErrorInvalidValue;
   const int64_t units = max_units(p.plan.T, p.plan.n);
   const int kblocks = (p.K + 63) / 64;
-  // CTAs to a cluster: until two an SM are there, each with four k-blocks at least
+  // CTAs to a cluster: as many as two an SM take at once, each with four k-blocks at least
   p.split = 1;
-  while (p.split < 8 && kblocks / (2 * p.split) >= 4 && units * p.split < 2 * device_sm_count())
-    p.split *= 2;
+  while (p.split < 8 && kblocks / (p.split + 1) >= 4 &&
+         units * (p.split + 1) <= 2 * device_sm_count())
+    ++p.split;
   p.wait_ns = kDefaultWaitNs;
   return launch(shrink_kernel<R>, dim3(static_cast<unsigned>(units * p.split)), Shrink<R>::kThreads,
                 Shrink<R>::kBytes, p.split, false, configured, st, map, p);
@@ -1218,9 +1249,9 @@ cudaError_t expand(const __nv_bfloat16* Q, int r, ExpandArgs p, cudaStream_t st)
   if (!make_tmap_bf16_3d(&map, Q, p.N, r, p.plan.n, 64, R)) return cudaErrorInvalidValue;
   const int64_t units = max_units(p.plan.T, p.plan.n);
   const int tiles = (p.N + kCols - 1) / kCols;
-  // CTAs to a unit: until two an SM are there, each with two tiles at least
+  // CTAs to a unit: as many as two an SM take at once, each with four tiles at least
   int split = 1;
-  while (tiles / (2 * split) >= 2 && units * split < 2 * device_sm_count()) split *= 2;
+  while (tiles / (split + 1) >= 4 && units * (split + 1) <= 2 * device_sm_count()) ++split;
   p.wait_ns = kDefaultWaitNs;
   return launch(expand_kernel<R>, dim3(static_cast<unsigned>(units), split), kExpandThreads,
                 Expand<R>::kBytes, 1, true, configured, st, map, p);
@@ -1235,7 +1266,7 @@ cudaError_t grad(GradArgs p, cudaStream_t st) {
   const cudaError_t e = launch(grad_kernel<R>, dim3(ctas), Grad<R>::kThreads, Grad<R>::kBytes, 1,
                                false, configured, st, p);
   if (e != cudaSuccess) return e;
-  return launch(grad_finish_kernel<R>, dim3(p.job[0].tiles + p.job[1].tiles, p.plan.n),
+  return launch(grad_finish_kernel<R>, dim3(p.job[0].tiles + p.job[1].tiles, p.plan.n, (p.r + kFinishRanks - 1) / kFinishRanks),
                 Grad<R>::kTile, 0, 1, false, configured_finish, st, p, ctas);
 }
 
@@ -1327,7 +1358,8 @@ moe_status moe_lora(const void* x, const void* a, const void* b, const int32_t* 
   auto* ob = static_cast<__nv_bfloat16*>(out);
   if (few_rows(T, r)) {
     static bool configured[kMaxDevices] = {};
-    return launch(few_kernel, dim3(static_cast<unsigned>(T) * kFewCtas), kFewThreads, 0, kFewCtas,
+    return launch(few_kernel, dim3(static_cast<unsigned>(T) * kFewCtas), kFewThreads,
+                  kFewAhead, kFewCtas,
                   false, configured, st, xb, ab, bb, adapter_ids, scales, yb, ob, v, H, N, n, r,
                   device_error_word()) == cudaSuccess
                ? MOE_OK
