@@ -15,16 +15,16 @@
 //
 // V is float. Where it enters a product it is a sum of bf16 numbers: two of them
 // (16 bits) for expand, whose result is rounded to bf16, and three (24 bits) for
-// grad, whose result is float. The shrink kernel writes them as images: a unit's
-// [128, 64] or [128, 128] values of a part, in the swizzled order in which the
-// tensor cores read shared memory, so that one bulk copy brings a part, as a
-// K-major operand to expand and as an MN-major one to grad. Rows past the end of an
-// adapter are zeros there.
+// grad, whose result is float. The shrink kernel writes them as images: the parts of
+// a unit's rows side by side, parts * R columns in atoms of 64 rows x 64 columns, in
+// the swizzled order in which the tensor cores read shared memory, so that bulk
+// copies bring them in, as a K-major operand to expand and as an MN-major one to
+// grad. Rows past the end of an adapter are zeros there.
 //
 // The tensor cores add their products up in float but cut off what does not fit;
 // over thousands of terms that bias shows in float results. So shrink and grad
-// take their accumulators out of tensor memory every 64 terms and add them up in
-// float registers, which round.
+// take their accumulators out of tensor memory every 128 or 64 terms and add them up
+// in float registers, which round.
 #include <string.h>
 
 #include "common.cuh"
@@ -41,11 +41,8 @@ constexpr int kMaxAdapters = 1024;
 constexpr int kMaxRank = 128;
 constexpr unsigned long long kDrainNs = 1000000000ull;
 constexpr int kAtom = kRows * 128;  // 16 KB: 128 rows x 64 columns of an image or a tile
-// 64-wide atoms of a part of an image, and bytes of a part
-template <int R>
-constexpr int atoms() { return R > 64 ? 2 : 1; }
-template <int R>
-constexpr int part_bytes() { return atoms<R>() * kAtom; }
+// 64-wide atoms of an image of so many parts
+__host__ __device__ constexpr int atoms(int parts, int R) { return (parts * R + 63) / 64; }
 
 // 16 bytes global -> shared, or 16 zero bytes where ok is false (src is then
 // any valid address and nothing is read).
@@ -235,7 +232,10 @@ __global__ void __launch_bounds__(1024, 1)
 // added over the cluster in the order of the ranks, and each CTA splits and writes
 // its share. Warps: 0 loads P by TMA, 1 issues the MMAs, then 4 (a quarter of the
 // accumulators' rows each) or 8 (and half of their columns) drain the accumulators,
-// and 4 gather the rows (cp.async, 128 bytes a row and k-block).
+// and 4 gather the rows (cp.async, 128 bytes a row and k-block) where warp 0 cannot load
+// them as a box.
+constexpr int kBlocks = 2;          // k-blocks that an accumulator takes up
+
 template <int R>
 struct Shrink {
   static constexpr int kStages = 4;
@@ -264,7 +264,8 @@ struct ShrinkArgs {
 
 template <int R>
 __global__ void __launch_bounds__(Shrink<R>::kThreads, R > 64 ? 1 : 2)
-    shrink_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ ShrinkArgs p) {
+    shrink_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_in,
+                  const __grid_constant__ ShrinkArgs p) {
   using S = Shrink<R>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ int rows[kRows];
@@ -306,6 +307,8 @@ __global__ void __launch_bounds__(Shrink<R>::kThreads, R > 64 ? 1 : 2)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // a full unit of rows that follow one another (a request's tokens) is a box
+  const bool box = __syncthreads_and(tid >= kRows || (rows[0] >= 0 && rows[tid] == rows[0] + tid));
   const uint32_t tmem = tmem_at;
   const int kblocks = (p.K + 63) / 64, per = (kblocks + p.split - 1) / p.split;
   const int kb0 = min(kblocks, static_cast<int>(rank) * per), kb1 = min(kblocks, kb0 + per);
@@ -323,7 +326,10 @@ __global__ void __launch_bounds__(Shrink<R>::kThreads, R > 64 ? 1 : 2)
         const int s = i % S::kStages;
         ok = mbar_wait(smem_u32(&empty[s]), ((i / S::kStages) & 1) ^ 1, p.wait_ns, stopped);
         if (!ok) break;
-        mbar_arrive_expect_tx(smem_u32(&full[s]), R * 128);
+        mbar_arrive_expect_tx(smem_u32(&full[s]), R * 128 + (box ? kAtom : 0));
+        if (box)
+          tma_load_2d(smem_u32(ring) + s * S::kStage, &map_in, smem_u32(&full[s]), (kb0 + i) * 64,
+                      rows[0]);
         tma_load_3d(smem_u32(ring) + s * S::kStage + kAtom, &map_p, smem_u32(&full[s]),
                     (kb0 + i) * 64, 0, u.a);
       }
@@ -332,8 +338,9 @@ __global__ void __launch_bounds__(Shrink<R>::kThreads, R > 64 ? 1 : 2)
     if (lane == 0) {
       const uint32_t idesc = idesc_bf16(128, R, false, false);
       for (int i = 0; i < steps; ++i) {
-        const int s = i % S::kStages, a = i % S::kAcc;
-        ok = mbar_wait(smem_u32(&tempty[a]), ((i / S::kAcc) & 1) ^ 1, p.wait_ns, stopped) &&
+        const int s = i % S::kStages, d = i / kBlocks, a = d % S::kAcc;
+        ok = (i % kBlocks || mbar_wait(smem_u32(&tempty[a]), ((d / S::kAcc) & 1) ^ 1, p.wait_ns,
+                                       stopped)) &&
              mbar_wait(smem_u32(&full[s]), (i / S::kStages) & 1, p.wait_ns, stopped);
         if (!ok) break;
         fence_proxy_async_shared();              // the gathered rows came through the generic proxy
@@ -342,16 +349,16 @@ __global__ void __launch_bounds__(Shrink<R>::kThreads, R > 64 ? 1 : 2)
         const uint64_t ad = sdesc_sw128(sa, 16, 1024), bd = sdesc_sw128(sa + kAtom, 16, 1024);
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
-          umma_bf16(tmem + a * R, ad + ks * 2, bd + ks * 2, idesc, ks ? 1u : 0u);
+          umma_bf16(tmem + a * R, ad + ks * 2, bd + ks * 2, idesc, (i % kBlocks || ks) ? 1u : 0u);
         umma_commit(smem_u32(&empty[s]));
-        umma_commit(smem_u32(&tfull[a]));
+        if (i % kBlocks == kBlocks - 1 || i + 1 == steps) umma_commit(smem_u32(&tfull[a]));
       }
     }
   } else if (warp < 2 + 4 * S::kGroups) {
     const uint32_t taddr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + j0;
-    for (int i = 0; i < steps; ++i) {
-      const int a = i % S::kAcc;
-      const bool got = mbar_wait(smem_u32(&tfull[a]), (i / S::kAcc) & 1, p.wait_ns, stopped);
+    for (int d = 0; d * kBlocks < steps; ++d) {
+      const int a = d % S::kAcc;
+      const bool got = mbar_wait(smem_u32(&tfull[a]), (d / S::kAcc) & 1, p.wait_ns, stopped);
       ok = __all_sync(0xffffffffu, got);
       if (!ok) break;
       tc_fence_after();
@@ -375,6 +382,10 @@ __global__ void __launch_bounds__(Shrink<R>::kThreads, R > 64 ? 1 : 2)
       const bool got = mbar_wait(smem_u32(&empty[s]), ((i / S::kStages) & 1) ^ 1, p.wait_ns, stopped);
       ok = __all_sync(0xffffffffu, got);
       if (!ok) break;
+      if (box) {
+        mbar_arrive(smem_u32(&full[s]));
+        continue;
+      }
       const uint32_t sa = smem_u32(ring) + s * S::kStage;
       const bool in_k = k0 + ch * 8 < p.K;
 #pragma unroll
@@ -414,7 +425,7 @@ __global__ void __launch_bounds__(Shrink<R>::kThreads, R > 64 ? 1 : 2)
   // eight columns of a row at a time, dealt out over the cluster
   for (int e = static_cast<int>(rank) + p.split * tid; e < kRows * (R / 8);
        e += p.split * S::kThreads) {
-    const int row = e % kRows, c = e / kRows;
+    const int row = e / (R / 8), c = e % (R / 8);
     const int g = rows[row];
     const uint32_t at0 = part0 + (row * R + (((2 * c) ^ (row & kMix)) << 2)) * 4;
     const uint32_t at1 = part0 + (row * R + (((2 * c + 1) ^ (row & kMix)) << 2)) * 4;
@@ -445,16 +456,17 @@ __global__ void __launch_bounds__(Shrink<R>::kThreads, R > 64 ? 1 : 2)
       else if (p.V) p.V[static_cast<int64_t>(g) * p.r + c * 8 + j] = v[j];
       v[j] *= f;
     }
-    const int64_t at = static_cast<int64_t>(unit) * p.parts * part_bytes<R>() + (c >> 3) * kAtom +
-                       row * 128 + (((c & 7) ^ (row & 7)) << 4);
+    const int64_t at = (static_cast<int64_t>(unit) * 2 + (row >> 6)) * atoms(p.parts, R) * (kAtom / 2) +
+                       (row & 63) * 128;
     auto put = [&](uint8_t* img) {
       for (int k = 0; k < p.parts; ++k) {
+        const int piece = k * (R / 8) + c;       // of 16 bytes, of the row
         uint4 w;
         w.x = take_part(v[0], v[1]);
         w.y = take_part(v[2], v[3]);
         w.z = take_part(v[4], v[5]);
         w.w = take_part(v[6], v[7]);
-        *reinterpret_cast<uint4*>(img + at + k * part_bytes<R>()) = w;
+        *reinterpret_cast<uint4*>(img + at + (piece >> 3) * (kAtom / 2) + (((piece & 7) ^ (row & 7)) << 4)) = w;
       }
     };
     put(p.img);
@@ -490,7 +502,7 @@ constexpr int kExpandAcc = 4;                     // accumulators: two to each h
 
 template <int R>
 struct Expand {
-  static constexpr int kImg = 2 * part_bytes<R>();
+  static constexpr int kImg = atoms(2, R) * kAtom;
   static constexpr int kQ = R * 128;
   static constexpr int kStages = 3;
   static constexpr int kBytes = 1024 + kImg + kStages * kQ + 8 * kPiece;
@@ -582,9 +594,12 @@ __global__ void __launch_bounds__(kExpandThreads, R > 64 ? 1 : 2)
           grid_dependency_wait();
           fence_proxy_async();
           mbar_arrive_expect_tx(smem_u32(&image), S::kImg);
-          const uint8_t* src = p.img + static_cast<int64_t>(unit) * p.parts * part_bytes<R>();
+          const uint8_t* src = p.img + static_cast<int64_t>(unit) * atoms(p.parts, R) * kAtom;
           for (int k = 0; k < S::kImg / kAtom; ++k)
-            bulk_copy_g2s(img0 + k * kAtom, src + k * kAtom, kAtom, smem_u32(&image));
+            for (int h = 0; h < 2; ++h)          // rows of the unit's halves
+              bulk_copy_g2s(img0 + k * kAtom + h * (kAtom / 2),
+                            src + (h * atoms(p.parts, R) + k) * (kAtom / 2), kAtom / 2,
+                            smem_u32(&image));
         }
       }
       for (int k = i > S::kStages ? i - S::kStages : 0; k < i; ++k)
@@ -605,9 +620,9 @@ __global__ void __launch_bounds__(kExpandThreads, R > 64 ? 1 : 2)
         for (int k = 0; k < 2; ++k)
 #pragma unroll
           for (int ks = 0; ks < R / 16; ++ks) {
-            const uint64_t ad = sdesc_sw128(img0 + k * part_bytes<R>() + (ks >> 2) * kAtom, 16, 1024);
-            umma_bf16(tmem + a * kCols, ad + (ks & 3) * 2, bd + ks * (2048 >> 4), idesc,
-                      (k | ks) ? 1u : 0u);
+            const int at = k * (R / 16) + ks;      // of the image's columns, in 16s
+            const uint64_t ad = sdesc_sw128(img0 + (at >> 2) * kAtom, 16, 1024) + (at & 3) * 2;
+            umma_bf16(tmem + a * kCols, ad, bd + ks * (2048 >> 4), idesc, (k | ks) ? 1u : 0u);
           }
         umma_commit(smem_u32(&empty[s]));
         umma_commit(smem_u32(&tfull[a]));
@@ -699,8 +714,11 @@ __global__ void __launch_bounds__(kExpandThreads, R > 64 ? 1 : 2)
 // go to a slot of the CTA, and grad_finish_kernel adds the slots up in order.
 // Warps: 0 loads images, 1 issues the MMAs, then 8 draining warps (one for each 32
 // columns, or 32 columns and half of the rank) and 4 gathering rows of the input, each
-// row's columns of the tile in one run of 512 (256) bytes.
+// row's columns of the tile in one run of 512 (256) bytes, where warp 0 cannot load the
+// 64 rows as boxes. The accumulators take up two chunks of an output; those of one half
+// of a tile are taken out while the other half's MMAs run.
 struct GradJob {
+  CUtensorMap map;             // of in: boxes of 64 columns x 64 rows
   const uint8_t* img;          // three parts
   const __nv_bfloat16* in;     // [T, N]
   float* G;                    // [n, r, N]
@@ -722,13 +740,13 @@ struct Grad {
   static constexpr int kHalves = R > 64 ? 1 : 2;
   static constexpr int kTile = 128 * kHalves;
   static constexpr int kIn = kHalves * kAtom;                 // 64 rows of the tile's columns
-  static constexpr int kImg = 3 * part_bytes<R>() / 2;        // 64 rows of three parts
+  static constexpr int kImg = atoms(3, R) * kAtom / 2;        // 64 rows of three parts
   static constexpr int kStage = kIn + kImg;
-  static constexpr int kStages = 3;
+  static constexpr int kStages = R <= 16 ? 5 : R <= 32 ? 4 : 3;
   static constexpr int kDrain = 8;
   static constexpr int kOwn = R > 64 ? 64 : R;                // ranks of a draining warp
   static constexpr int kThreads = 32 * (2 + kDrain + 4);
-  static constexpr int kTmem = 2 * kHalves * R;
+  static constexpr int kTmem = R <= 16 ? 128 : R <= 32 ? 256 : 512;   // kHalves * 3 R
   static constexpr int kBytes = 1024 + kStages * kStage;
 };
 
@@ -737,9 +755,10 @@ __device__ __forceinline__ int64_t first_item(int64_t items, int ctas, int b) {
   return items * b / ctas;
 }
 
-// A walk over items: tile, chunk within the tile, adapter.
+// A walk over items: tile, chunk c within the tile, adapter a with the chunks from c0 to
+// c1 (kept here: every role takes a step for every stage).
 struct Walk {
-  int tile, c, a;
+  int tile, c, a, c0, c1;
   __device__ __forceinline__ void start(int64_t item, int total, int n, const int* chunks) {
     tile = static_cast<int>(item / total);
     c = static_cast<int>(item - static_cast<int64_t>(tile) * total);
@@ -749,14 +768,22 @@ struct Walk {
       if (chunks[mid] <= c) lo = mid; else hi = mid - 1;
     }
     a = lo;
+    c0 = chunks[a];
+    c1 = chunks[a + 1];
   }
+  __device__ __forceinline__ bool last() const { return c + 1 == c1; }   // of its output
+  // Whether accumulators with so many chunks are full, or their output complete.
+  __device__ __forceinline__ bool ends_group(int held) const { return held == 2 || last(); }
   __device__ __forceinline__ void next(int total, const int* chunks) {
-    if (++c == total) {
+    if (++c < c1) return;
+    if (c == total) {
       ++tile;
       c = 0;
-      a = 0;
+      a = -1;
     }
-    while (chunks[a + 1] <= c) ++a;
+    do ++a; while (chunks[a + 1] <= c);          // adapters without rows have no chunk
+    c0 = chunks[a];
+    c1 = chunks[a + 1];
   }
 };
 
@@ -768,6 +795,7 @@ __global__ void __launch_bounds__(Grad<R>::kThreads, 1)
   __shared__ int chunks[kMaxAdapters + 1], units[kMaxAdapters + 1], begin[kMaxAdapters], end[kMaxAdapters];
   __shared__ uint64_t full[S::kStages], empty[S::kStages], tfull[2], tempty[2];
   __shared__ uint32_t tmem_at;
+  __shared__ int ends[S::kStages];               // whether the accumulators end with a stage
   __shared__ int stop, zero;
   uint8_t* ring = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -804,16 +832,16 @@ __global__ void __launch_bounds__(Grad<R>::kThreads, 1)
       mbar_init(smem_u32(&full[s]), 1 + 128);
       mbar_init(smem_u32(&empty[s]), 1);
     }
-    for (int a = 0; a < 2; ++a) {
-      mbar_init(smem_u32(&tfull[a]), 1);
-      mbar_init(smem_u32(&tempty[a]), S::kDrain);
+    for (int m = 0; m < S::kHalves; ++m) {
+      mbar_init(smem_u32(&tfull[m]), 1);
+      mbar_init(smem_u32(&tempty[m]), S::kDrain / S::kHalves);
     }
     stop = 0;
     zero = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(&tmem_at), S::kTmem < 32 ? 32 : S::kTmem);
+    tmem_alloc(smem_u32(&tmem_at), S::kTmem);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -828,79 +856,142 @@ __global__ void __launch_bounds__(Grad<R>::kThreads, 1)
   const int steps = static_cast<int>(first_item(items, ctas, b + 1) - i0);
   volatile int* stopped = &stop;
   bool ok = true;
-  Walk w = {0, 0, 0};
+  Walk w = {0, 0, 0, 0, 0};
   if (steps > 0) w.start(i0, total, n, chunks);
   const int t0 = p.job[0].tiles;
+
+  // a chunk's rows as the plan has them, two a lane (checked when they are used, so that
+  // nothing waits for them before); -1 past the adapter
+  auto plan_rows = [&](const Walk& x, int& o0, int& o1) {
+    const int at = begin[x.a] + (x.c - x.c0) * 64 + lane, past = end[x.a];
+    o0 = at < past ? __ldg(p.plan.order + at) : -1;
+    o1 = at + 32 < past ? __ldg(p.plan.order + at + 32) : -1;
+  };
+  // 64 rows that follow one another: the same answer in every warp
+  auto is_box = [&](int o0, int o1) {
+    const int first = __shfl_sync(0xffffffffu, o0, 0);
+    return __all_sync(0xffffffffu, first >= 0 && first <= p.plan.T - 64 && o0 == first + lane &&
+                                       o1 == first + 32 + lane);
+  };
 
   if (steps == 0) {
     // nothing of the list
   } else if (warp == 0) {
-    if (lane == 0) {
-      for (int i = 0; i < steps; ++i) {
-        const int s = i % S::kStages;
-        ok = mbar_wait(smem_u32(&empty[s]), ((i / S::kStages) & 1) ^ 1, p.wait_ns, stopped);
-        if (!ok) break;
-        const uint32_t bar = smem_u32(&full[s]), dst = smem_u32(ring) + s * S::kStage + S::kIn;
-        const int c = w.c - chunks[w.a];         // chunk of the adapter: half a unit
-        const int unit = min(units[w.a] + (c >> 1), p.units - 1);   // offsets may overlap
-        const uint8_t* src = p.job[w.tile >= t0].img +
-                             static_cast<int64_t>(unit) * 3 * part_bytes<R>() +
-                             (c & 1) * (kAtom / 2);
-        mbar_arrive_expect_tx(bar, S::kImg);
-#pragma unroll
-        for (int k = 0; k < 3 * atoms<R>(); ++k)
-          bulk_copy_g2s(dst + k * (kAtom / 2), src + k * kAtom, kAtom / 2, bar);
-        if (i + 1 < steps) w.next(total, chunks);
+    int o0, o1, held = 0;
+    plan_rows(w, o0, o1);
+    for (int i = 0; i < steps; ++i) {
+      const int s = i % S::kStages;
+      const Walk x = w;
+      const bool last = w.ends_group(++held) || i + 1 == steps;
+      if (last) held = 0;
+      const bool box = is_box(o0, o1);
+      const int row = __shfl_sync(0xffffffffu, o0, 0);
+      if (i + 1 < steps) {
+        w.next(total, chunks);
+        plan_rows(w, o0, o1);
       }
+      const bool got = mbar_wait(smem_u32(&empty[s]), ((i / S::kStages) & 1) ^ 1, p.wait_ns, stopped);
+      ok = __all_sync(0xffffffffu, got);
+      if (!ok) break;
+      const uint32_t bar = smem_u32(&full[s]), dst = smem_u32(ring) + s * S::kStage;
+      const bool second = x.tile >= t0;
+      const int col = (second ? x.tile - t0 : x.tile) * S::kTile;
+      if (lane == 0) {
+        ends[s] = last;
+        mbar_arrive_expect_tx(bar, S::kImg + (box ? S::kIn : 0));
+        const int c = x.c - x.c0;                // chunk of the adapter: half a unit
+        const int unit = min(units[x.a] + (c >> 1), p.units - 1);   // offsets may overlap
+        bulk_copy_g2s(dst + S::kIn,
+                      (second ? p.job[1].img : p.job[0].img) +
+                          (static_cast<int64_t>(unit) * 2 + (c & 1)) * S::kImg, S::kImg, bar);
+      }
+      __syncwarp();
+      if (box && lane < S::kTile / 64)           // a lane a box
+        tma_load_2d(dst + lane * (kAtom / 2), second ? &p.job[1].map : &p.job[0].map, bar,
+                    col + 64 * lane, row);
+      __syncwarp();
     }
   } else if (warp == 1) {
     if (lane == 0) {
-      const uint32_t idesc = idesc_bf16(128, R, true, true);
+      // the parts side by side are one N of 3 R, or of 256 and 128
+      constexpr int kN0 = 3 * R > 256 ? 256 : 3 * R, kN1 = 3 * R - kN0;
+      const uint32_t idesc0 = idesc_bf16(128, kN0, true, true);
+      const uint32_t idesc1 = idesc_bf16(128, kN1 > 0 ? kN1 : 16, true, true);
+      const uint64_t ad0 = sdesc_sw128(smem_u32(ring), kAtom / 2, 1024);
+      const uint64_t bd0 = sdesc_sw128(smem_u32(ring) + S::kIn, kAtom / 2, 1024);
+      uint32_t held = 0, turn = 0;               // the accumulators hold something; turns so far
+      int s = 0;
+      uint32_t phase = 0;
       for (int i = 0; i < steps; ++i) {
-        const int s = i % S::kStages, a = i & 1;
-        ok = mbar_wait(smem_u32(&tempty[a]), ((i >> 1) & 1) ^ 1, p.wait_ns, stopped) &&
-             mbar_wait(smem_u32(&full[s]), (i / S::kStages) & 1, p.wait_ns, stopped);
+        ok = mbar_wait(smem_u32(&full[s]), phase, p.wait_ns, stopped);
         if (!ok) break;
+        const bool last = ends[s] != 0;
         fence_proxy_async_shared();
         tc_fence_after();
-        const uint32_t si = smem_u32(ring) + s * S::kStage;
+        const uint64_t off = static_cast<uint64_t>(s) * (S::kStage >> 4);
 #pragma unroll
         for (int m = 0; m < S::kHalves; ++m) {
-          const uint64_t ad = sdesc_sw128(si + m * kAtom, kAtom / 2, 1024);
-#pragma unroll
-          for (int k = 0; k < 3; ++k) {
-            const uint64_t bd = sdesc_sw128(si + S::kIn + k * atoms<R>() * (kAtom / 2), kAtom / 2, 1024);
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              umma_bf16(tmem + (a * S::kHalves + m) * R, ad + ks * (2048 >> 4),
-                        bd + ks * (2048 >> 4), idesc, (k | ks) ? 1u : 0u);
+          if (held == 0) {                       // the half's last sums have been taken out
+            ok = mbar_wait(smem_u32(&tempty[m]), turn ^ 1, p.wait_ns, stopped);
+            if (!ok) break;
+            tc_fence_after();
           }
+          const uint64_t ad = ad0 + off + m * (kAtom >> 4), bd = bd0 + off;
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks) {
+            const uint32_t to = tmem + m * 3 * R, on = ks ? 1u : held;
+            umma_bf16(to, ad + ks * (2048 >> 4), bd + ks * (2048 >> 4), idesc0, on);
+            if (kN1 > 0)
+              umma_bf16(to + kN0, ad + ks * (2048 >> 4),
+                        bd + (kN0 / 64) * (kAtom / 2 >> 4) + ks * (2048 >> 4), idesc1, on);
+          }
+          if (last) umma_commit(smem_u32(&tfull[m]));
         }
+        if (!ok) break;
         umma_commit(smem_u32(&empty[s]));
-        umma_commit(smem_u32(&tfull[a]));
+        held = last ? 0 : 1;
+        turn ^= last ? 1 : 0;
+        if (++s == S::kStages) {
+          s = 0;
+          phase ^= 1;
+        }
       }
     }
   } else if (warp < 2 + S::kDrain) {
     const int m = S::kHalves == 2 ? (warp - 2) >> 2 : 0, q = warp & 3;
     const int j0 = S::kHalves == 2 ? 0 : ((warp - 2) >> 2) * S::kOwn;
-    const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + m * R + j0;
+    const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + m * 3 * R + j0;
     const int in_tile = m * 128 + q * 32 + lane;
     float sum[S::kOwn];
 #pragma unroll
     for (int j = 0; j < S::kOwn; ++j) sum[j] = 0.0f;
-    bool from_first = w.c == chunks[w.a];        // the run began with its output's first chunk
+    bool from_first = w.c == w.c0;               // the run began with its output's first chunk
     bool first_run = true;
+    int held = 0, d = 0;
     for (int i = 0; i < steps; ++i) {
-      const int a = i & 1;
-      const bool got = mbar_wait(smem_u32(&tfull[a]), (i >> 1) & 1, p.wait_ns, stopped);
-      ok = __all_sync(0xffffffffu, got);
-      if (!ok) break;
-      tc_fence_after();
-      add_columns<S::kOwn>(taddr + a * S::kHalves * R, sum);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&tempty[a]));
-      const bool last = w.c + 1 == chunks[w.a + 1];
+      const bool last = w.last();
+      if (w.ends_group(++held) || i + 1 == steps) {
+        const bool got = mbar_wait(smem_u32(&tfull[m]), d & 1, p.wait_ns, stopped);
+        ok = __all_sync(0xffffffffu, got);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int j = 0; j < S::kOwn; j += 16) {        // the smallest part first
+          uint32_t v0[16], v1[16], v2[16];
+          tmem_ld_32x32b_x16(taddr + j, v0);
+          tmem_ld_32x32b_x16(taddr + R + j, v1);
+          tmem_ld_32x32b_x16(taddr + 2 * R + j, v2);
+          tmem_ld_wait();
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            sum[j + k] += __uint_as_float(v0[k]) + (__uint_as_float(v1[k]) + __uint_as_float(v2[k]));
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&tempty[m]));
+        held = 0;
+        ++d;
+      }
       if (last || i + 1 == steps) {              // the run's end
         const GradJob& job = p.job[w.tile >= t0];
         const int col = (w.tile >= t0 ? w.tile - t0 : w.tile) * S::kTile + in_tile;
@@ -930,37 +1021,40 @@ __global__ void __launch_bounds__(Grad<R>::kThreads, 1)
     constexpr int kVec = S::kTile / 8;           // 16-byte pieces of a row: 32 or 16
     constexpr int kPer = 32 / kVec;              // rows of a warp's instruction
     const int ch = lane % kVec, sub = lane / kVec;
-    // lane l: the chunk's row 4 l + g as the plan has it (checked when it is used, so
-    // that nothing waits for it before), -1 past the adapter
-    auto row_of = [&](const Walk& x) {
-      const int at = begin[x.a] + (x.c - chunks[x.a]) * 64 + 4 * lane + g;
-      return (lane < 16 && at < end[x.a]) ? __ldg(p.plan.order + at) : -1;
-    };
-    int mine = row_of(w);
-    bool inside = lane < 16 && begin[w.a] + (w.c - chunks[w.a]) * 64 + 4 * lane + g < end[w.a];
+    int o0, o1;
+    plan_rows(w, o0, o1);
     for (int i = 0; i < steps; ++i) {
       const int s = i % S::kStages;
-      const GradJob& job = p.job[w.tile >= t0];
-      const int col = (w.tile >= t0 ? w.tile - t0 : w.tile) * S::kTile + ch * 8;
-      const bool in_n = col < job.N;
-      int here = mine;
-      if (inside && (here < 0 || here >= p.plan.T)) {
-        report_error(p.plan.err, kErrBadId);
-        here = -1;
-      }
+      const Walk x = w;
+      const bool box = is_box(o0, o1);
+      int h0 = o0, h1 = o1;
       if (i + 1 < steps) {
         w.next(total, chunks);
-        mine = row_of(w);
-        inside = lane < 16 && begin[w.a] + (w.c - chunks[w.a]) * 64 + 4 * lane + g < end[w.a];
+        plan_rows(w, o0, o1);
       }
       const bool got = mbar_wait(smem_u32(&empty[s]), ((i / S::kStages) & 1) ^ 1, p.wait_ns, stopped);
       ok = __all_sync(0xffffffffu, got);
       if (!ok) break;
+      if (box) {
+        mbar_arrive(smem_u32(&full[s]));
+        continue;
+      }
+      const int left = end[x.a] - begin[x.a] - (x.c - x.c0) * 64;   // rows of the adapter
+      if ((lane < left && (h0 < 0 || h0 >= p.plan.T)) ||
+          (lane + 32 < left && (h1 < 0 || h1 >= p.plan.T)))
+        report_error(p.plan.err, kErrBadId);
+      if (h0 >= p.plan.T) h0 = -1;
+      if (h1 >= p.plan.T) h1 = -1;
+      const GradJob& job = p.job[x.tile >= t0];
+      const int col = (x.tile >= t0 ? x.tile - t0 : x.tile) * S::kTile + ch * 8;
+      const bool in_n = col < job.N;
       const uint32_t dst = smem_u32(ring) + s * S::kStage + (ch >> 3) * (kAtom / 2);
 #pragma unroll
       for (int j = 0; j < 16 / kPer; ++j) {
-        const int k = j * kPer + sub, row = 4 * k + g;
-        const int t = __shfl_sync(0xffffffffu, here, k);
+        const int row = 4 * (j * kPer + sub) + g;
+        const int t_lo = __shfl_sync(0xffffffffu, h0, row & 31);
+        const int t_hi = __shfl_sync(0xffffffffu, h1, row & 31);
+        const int t = row < 32 ? t_lo : t_hi;
         const bool live = t >= 0 && in_n;
         cp_async_16z(dst + row * 128 + (((ch & 7) ^ (row & 7)) << 4),
                      live ? job.in + static_cast<int64_t>(t) * job.N + col : job.in, live);
@@ -980,7 +1074,7 @@ __global__ void __launch_bounds__(Grad<R>::kThreads, 1)
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, S::kTmem < 32 ? 32 : S::kTmem);
+    tmem_dealloc(tmem, S::kTmem);
   }
 }
 
@@ -1222,14 +1316,16 @@ int64_t max_units(int64_t T, int n) { return (T + kRows - 1) / kRows + n; }
 int rank_up(int r) { return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128; }
 size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 size_t image_bytes(int64_t T, int n, int r, int parts) {
-  return static_cast<size_t>(max_units(T, n)) * parts * (r > 64 ? 2 : 1) * kAtom;
+  return static_cast<size_t>(max_units(T, n)) * atoms(parts, rank_up(r)) * kAtom;
 }
 
 template <int R>
 cudaError_t shrink(const __nv_bfloat16* P, ShrinkArgs p, cudaStream_t st) {
   static bool configured[kMaxDevices] = {};
-  CUtensorMap map;
-  if (!make_tmap_bf16_3d(&map, P, p.K, p.r, p.plan.n, 64, R)) return cudaErrorInvalidValue;
+  CUtensorMap map, map_in;
+  if (!make_tmap_bf16_3d(&map, P, p.K, p.r, p.plan.n, 64, R) ||
+      !make_tmap_bf16_2d(&map_in, p.in, p.K, p.plan.T, static_cast<uint64_t>(p.K) * 2, 64, kRows))
+    return cudaErrorInvalidValue;
   const int64_t units = max_units(p.plan.T, p.plan.n);
   const int kblocks = (p.K + 63) / 64;
   // CTAs to a cluster: as many as two an SM take at once, each with four k-blocks at least
@@ -1239,7 +1335,7 @@ cudaError_t shrink(const __nv_bfloat16* P, ShrinkArgs p, cudaStream_t st) {
     ++p.split;
   p.wait_ns = kDefaultWaitNs;
   return launch(shrink_kernel<R>, dim3(static_cast<unsigned>(units * p.split)), Shrink<R>::kThreads,
-                Shrink<R>::kBytes, p.split, false, configured, st, map, p);
+                Shrink<R>::kBytes, p.split, false, configured, st, map, map_in, p);
 }
 
 template <int R>
@@ -1260,7 +1356,11 @@ cudaError_t expand(const __nv_bfloat16* Q, int r, ExpandArgs p, cudaStream_t st)
 template <int R>
 cudaError_t grad(GradArgs p, cudaStream_t st) {
   static bool configured[kMaxDevices] = {}, configured_finish[kMaxDevices] = {};
-  for (GradJob& j : p.job) j.tiles = (j.N + Grad<R>::kTile - 1) / Grad<R>::kTile;
+  for (GradJob& j : p.job) {
+    j.tiles = (j.N + Grad<R>::kTile - 1) / Grad<R>::kTile;
+    if (!make_tmap_bf16_2d(&j.map, j.in, j.N, p.plan.T, static_cast<uint64_t>(j.N) * 2, 64, 64))
+      return cudaErrorInvalidValue;
+  }
   p.wait_ns = kDefaultWaitNs;
   const int ctas = device_sm_count();
   const cudaError_t e = launch(grad_kernel<R>, dim3(ctas), Grad<R>::kThreads, Grad<R>::kBytes, 1,
@@ -1440,8 +1540,8 @@ moe_status moe_lora_backward(const void* dy, const void* x, const float* v, cons
   ex.N = H;
   ex.plan = plan;
   GradArgs gr{};
-  gr.job[0] = {ws + L.dv, xb, da, H, 0};
-  gr.job[1] = {ws + L.v, gb, db, N, 0};
+  gr.job[0] = {{}, ws + L.dv, xb, da, H, 0};
+  gr.job[1] = {{}, ws + L.v, gb, db, N, 0};
   gr.partial = reinterpret_cast<float*>(ws + L.partial);
   gr.chunks = reinterpret_cast<int*>(ws + L.chunks);
   gr.r = r;

@@ -157,11 +157,11 @@ def test_dense_workspace_sizes(m):
     for bad in ((-1, 64, 64), (4, 60, 64), (4, 64, 60), (4, 0, 64), (4, 64, -8)):
         assert L.moe_gated_ffn_workspace_size(*bad) == 0, bad
         assert L.moe_gated_ffn_backward_workspace_size(*bad) == 0, bad
-    # images of units of 128 rows: 16 KB a part and 64 ranks; none for few rows
-    assert L.moe_lora_workspace_size(1000, 4, 16) == (8 + 4) * 2 * 16384
-    assert L.moe_lora_workspace_size(1000, 4, 128) == (8 + 4) * 2 * 32768
+    # images of units of 128 rows, 16 KB to 64 columns of two parts; none for few rows
+    assert L.moe_lora_workspace_size(1000, 4, 16) == (8 + 4) * 16384
+    assert L.moe_lora_workspace_size(1000, 4, 128) == (8 + 4) * 4 * 16384
     assert L.moe_lora_workspace_size(64, 4, 16) == 0
-    assert L.moe_lora_backward_workspace_size(1000, 4, 16) > 2 * (8 + 4) * 3 * 16384
+    assert L.moe_lora_backward_workspace_size(1000, 4, 16) > 2 * (8 + 4) * 16384
     for bad in ((100, 4, 129), (-1, 4, 16), (100, 0, 16), (100, 1025, 16), (100, 4, 0)):
         assert L.moe_lora_workspace_size(*bad) == 0
         assert L.moe_lora_backward_workspace_size(*bad) == 0
