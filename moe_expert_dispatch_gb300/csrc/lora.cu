@@ -113,9 +113,8 @@ __device__ __forceinline__ void segment(const Plan& p, int a, int& lo, int& hi) 
   if (lo != l || hi != h || (a == 0 && l != 0)) report_error(p.err, kErrBadId);
 }
 
-// Row i of the order, or -1 (reported) where it is no row.
-__device__ __forceinline__ int plan_row(const Plan& p, int i) {
-  const int r = __ldg(p.order + i);
+// A row number of the order, or -1 (reported) where it is no row.
+__device__ __forceinline__ int checked_row(const Plan& p, int r) {
   if (r >= 0 && r < p.T) return r;
   report_error(p.err, kErrBadId);
   return -1;
@@ -238,7 +237,7 @@ constexpr int kBlocks = 2;          // k-blocks that an accumulator takes up
 
 template <int R>
 struct Shrink {
-  static constexpr int kStages = 4;
+  static constexpr int kStages = R <= 16 ? 6 : R <= 32 ? 5 : 4;   // two CTAs an SM up to 64
   static constexpr int kStage = kAtom + R * 128;
   static constexpr int kAcc = R > 64 ? 2 : 4;       // accumulators in flight
   static constexpr int kTmem = R <= 16 ? 64 : R <= 32 ? 128 : 256;
@@ -262,6 +261,25 @@ struct ShrinkArgs {
   Plan plan;
 };
 
+// Columns 8 c to 8 c + 7 of a row of V into the image of its unit, part by part.
+template <int R>
+__device__ __forceinline__ void put_parts(uint8_t* img, int unit, int row, int c, int parts, float* v) {
+  const int64_t at = (static_cast<int64_t>(unit) * 2 + (row >> 6)) * atoms(parts, R) * (kAtom / 2) +
+                     (row & 63) * 128;
+#pragma unroll
+  for (int k = 0; k < 3; ++k)
+    if (k < parts) {
+      const int piece = k * (R / 8) + c;         // of 16 bytes, of the row
+      uint4 w;
+      w.x = take_part(v[0], v[1]);
+      w.y = take_part(v[2], v[3]);
+      w.z = take_part(v[4], v[5]);
+      w.w = take_part(v[6], v[7]);
+      *reinterpret_cast<uint4*>(img + at + (piece >> 3) * (kAtom / 2) +
+                                (((piece & 7) ^ (row & 7)) << 4)) = w;
+    }
+}
+
 template <int R>
 __global__ void __launch_bounds__(Shrink<R>::kThreads, R > 64 ? 1 : 2)
     shrink_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_in,
@@ -278,9 +296,11 @@ __global__ void __launch_bounds__(Shrink<R>::kThreads, R > 64 ? 1 : 2)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int unit = static_cast<int>(blockIdx.x) / p.split;
   const Unit u = find_unit(p.plan, unit);
-  if (tid < kRows) rows[tid] = tid < u.rows ? plan_row(p.plan, u.lo + tid) : -1;
+  // on its way while the barriers are made
+  const int raw = tid < u.rows ? __ldg(p.plan.order + u.lo + tid) : 0;
   grid_dependents_launch();
   if (u.rows == 0 || u.a == p.plan.n) {         // the whole cluster leaves together
+    if (tid < kRows) rows[tid] = tid < u.rows ? checked_row(p.plan, raw) : -1;
     __syncthreads();
     if (rank == 0 && p.V)
       for (int i = tid; i < u.rows * p.r; i += S::kThreads)
@@ -304,6 +324,7 @@ __global__ void __launch_bounds__(Shrink<R>::kThreads, R > 64 ? 1 : 2)
     tmem_alloc(smem_u32(&tmem_at), S::kTmem);
     tmem_relinquish();
   }
+  if (tid < kRows) rows[tid] = tid < u.rows ? checked_row(p.plan, raw) : -1;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -313,6 +334,7 @@ __global__ void __launch_bounds__(Shrink<R>::kThreads, R > 64 ? 1 : 2)
   const int kblocks = (p.K + 63) / 64, per = (kblocks + p.split - 1) / p.split;
   const int kb0 = min(kblocks, static_cast<int>(rank) * per), kb1 = min(kblocks, kb0 + per);
   const int steps = kb1 - kb0;
+  const float f = p.scales ? __ldg(p.scales + u.a) : 1.0f;
   volatile int* stopped = &stop;
   bool ok = true;
   float sum[S::kOwn];                            // of a draining warp's lane
@@ -396,6 +418,20 @@ __global__ void __launch_bounds__(Shrink<R>::kThreads, R > 64 ? 1 : 2)
       }
       cp_async_arrive_noinc(smem_u32(&full[s]));
     }
+    // the other V, while the last rows come in
+    if (p.kept) {
+#pragma unroll 2
+      for (int e = static_cast<int>(rank) + p.split * g; e < kRows * (R / 8); e += p.split * 128) {
+        const int row = e / (R / 8), c = e % (R / 8), t = rows[row];
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          v[j] = (t >= 0 && c * 8 + j < p.r)
+                     ? f * __ldg(p.kept + static_cast<int64_t>(t) * p.r + c * 8 + j)
+                     : 0.0f;
+        put_parts<R>(p.img_kept, unit, row, c, p.parts, v);
+      }
+    }
     cp_commit();
     cp_wait<0>();
   }
@@ -420,7 +456,6 @@ __global__ void __launch_bounds__(Shrink<R>::kThreads, R > 64 ? 1 : 2)
   }
   if (p.split > 1) cluster_sync();
   else __syncthreads();
-  const float f = p.scales ? __ldg(p.scales + u.a) : 1.0f;
   const uint32_t part0 = smem_u32(part);
   // eight columns of a row at a time, dealt out over the cluster
   for (int e = static_cast<int>(rank) + p.split * tid; e < kRows * (R / 8);
@@ -429,55 +464,38 @@ __global__ void __launch_bounds__(Shrink<R>::kThreads, R > 64 ? 1 : 2)
     const int g = rows[row];
     const uint32_t at0 = part0 + (row * R + (((2 * c) ^ (row & kMix)) << 2)) * 4;
     const uint32_t at1 = part0 + (row * R + (((2 * c + 1) ^ (row & kMix)) << 2)) * 4;
-    float v[8];
-    auto add_up = [&](uint32_t at, float* to) {
-      float4 a[8];
+    float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int q = 0; q < 8; ++q)
-        if (q < p.split) a[q] = ld_cluster_f32x4(at, q);
-      to[0] = a[0].x;
-      to[1] = a[0].y;
-      to[2] = a[0].z;
-      to[3] = a[0].w;
+    for (int q0 = 0; q0 < 8; q0 += 4)
+      if (q0 < p.split) {
+        float4 a[4], b[4];
 #pragma unroll
-      for (int q = 1; q < 8; ++q)
-        if (q < p.split) {
-          to[0] += a[q].x;
-          to[1] += a[q].y;
-          to[2] += a[q].z;
-          to[3] += a[q].w;
+        for (int q = 0; q < 4; ++q) {            // all of them on their way at once
+          a[q] = b[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (q0 + q < p.split) {
+            a[q] = ld_cluster_f32x4(at0, q0 + q);
+            b[q] = ld_cluster_f32x4(at1, q0 + q);
+          }
         }
-    };
-    add_up(at0, v);
-    add_up(at1, v + 4);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          v[0] += a[q].x;
+          v[1] += a[q].y;
+          v[2] += a[q].z;
+          v[3] += a[q].w;
+          v[4] += b[q].x;
+          v[5] += b[q].y;
+          v[6] += b[q].z;
+          v[7] += b[q].w;
+        }
+      }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       if (g < 0 || c * 8 + j >= p.r) v[j] = 0.0f;
       else if (p.V) p.V[static_cast<int64_t>(g) * p.r + c * 8 + j] = v[j];
       v[j] *= f;
     }
-    const int64_t at = (static_cast<int64_t>(unit) * 2 + (row >> 6)) * atoms(p.parts, R) * (kAtom / 2) +
-                       (row & 63) * 128;
-    auto put = [&](uint8_t* img) {
-      for (int k = 0; k < p.parts; ++k) {
-        const int piece = k * (R / 8) + c;       // of 16 bytes, of the row
-        uint4 w;
-        w.x = take_part(v[0], v[1]);
-        w.y = take_part(v[2], v[3]);
-        w.z = take_part(v[4], v[5]);
-        w.w = take_part(v[6], v[7]);
-        *reinterpret_cast<uint4*>(img + at + (piece >> 3) * (kAtom / 2) + (((piece & 7) ^ (row & 7)) << 4)) = w;
-      }
-    };
-    put(p.img);
-    if (p.kept) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        v[j] = (g >= 0 && c * 8 + j < p.r)
-                   ? f * __ldg(p.kept + static_cast<int64_t>(g) * p.r + c * 8 + j)
-                   : 0.0f;
-      put(p.img_kept);
-    }
+    put_parts<R>(p.img, unit, row, c, p.parts, v);
   }
   tc_fence_before();
   if (p.split > 1) cluster_sync();               // the others have read this CTA's sums
@@ -538,7 +556,7 @@ __global__ void __launch_bounds__(kExpandThreads, R > 64 ? 1 : 2)
     grid_dependency_wait();
     return;
   }
-  if (tid < kRows) rows[tid] = tid < u.rows ? plan_row(p.plan, u.lo + tid) : -1;
+  if (tid < kRows) rows[tid] = tid < u.rows ? checked_row(p.plan, __ldg(p.plan.order + u.lo + tid)) : -1;
   if (none) {                                    // base as it is, or zeros
     __syncthreads();
     const int nv = p.N / 8;
@@ -801,6 +819,7 @@ __global__ void __launch_bounds__(Grad<R>::kThreads, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int n = p.plan.n, b = blockIdx.x, ctas = gridDim.x;
+  grid_dependents_launch();
   if (warp == 0) {
     int c_sum = 0, u_sum = 0;
     for (int a0 = 0; a0 < n; a0 += 32) {
@@ -1089,6 +1108,7 @@ __global__ void __launch_bounds__(Grad<R>::kTile)
   const int a = blockIdx.y, n = p.plan.n, tile = blockIdx.x, t0 = p.job[0].tiles;
   const GradJob& job = p.job[tile >= t0];
   const int col = (tile >= t0 ? tile - t0 : tile) * S::kTile + threadIdx.x;
+  grid_dependency_wait();
   const int total = p.chunks[n], c0 = p.chunks[a], c1 = p.chunks[a + 1];
   float* g = job.G + static_cast<int64_t>(a) * p.r * job.N + col;
   const int j0 = blockIdx.z * kFinishRanks, j1 = min(p.r, j0 + kFinishRanks);
@@ -1100,15 +1120,8 @@ __global__ void __launch_bounds__(Grad<R>::kTile)
   }
   const int64_t items = static_cast<int64_t>(t0 + p.job[1].tiles) * total;
   const int64_t i0 = static_cast<int64_t>(tile) * total + c0, i1 = i0 + (c1 - c0);
-  // the CTA of an item: the last one that begins at or before it
-  auto owner = [&](int64_t i) {
-    int lo = 0, hi = ctas - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (first_item(items, ctas, mid) <= i) lo = mid; else hi = mid - 1;
-    }
-    return lo;
-  };
+  // the CTA of an item, the last one that begins at or before it: items b / ctas <= i
+  auto owner = [&](int64_t i) { return static_cast<int>(((i + 1) * ctas - 1) / items); };
   const int b0 = owner(i0), b1 = owner(i1 - 1);
   if (b0 == b1) return;
   float v[kFinishRanks];
@@ -1367,7 +1380,7 @@ cudaError_t grad(GradArgs p, cudaStream_t st) {
                                false, configured, st, p);
   if (e != cudaSuccess) return e;
   return launch(grad_finish_kernel<R>, dim3(p.job[0].tiles + p.job[1].tiles, p.plan.n, (p.r + kFinishRanks - 1) / kFinishRanks),
-                Grad<R>::kTile, 0, 1, false, configured_finish, st, p, ctas);
+                Grad<R>::kTile, 0, 1, true, configured_finish, st, p, ctas);
 }
 
 #define MOE_BY_RANK(r, call)       \
