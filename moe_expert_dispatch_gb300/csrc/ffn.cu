@@ -654,28 +654,35 @@ moe_status moe_gated_ffn_backward(const void* dy, const void* x, const void* w_g
   p.act = act;
   p.err = device_error_word();
   p.wait_ns = kDefaultWaitNs;
-  // K-major B: one box of the columns that a CTA loads
-  const uint32_t box_h = narrow(T, F, 256, 1) ? 64 : 128, box_x = narrow(T, H, 256, 1) ? 64 : 128;
-  Maps mh{}, mx{}, m2{}, m1{};
-  if (!in_map(&mh.a[0], dy, H, T, kTileM) || !in_map(&mh.b[0], w_down, H, F, box_h) ||
-      !make_out_tmap(&mh.in[0], a_gate, F, T, rF, false) ||
-      !make_out_tmap(&mh.in[1], a_up, F, T, rF, false) ||
-      !make_out_tmap(&mh.out[0], h, F, T, rF, false) ||
-      !make_out_tmap(&mh.out[1], da_g, F, T, rF, false) ||
-      !make_out_tmap(&mh.out[2], da_u, F, T, rF, false) ||
-      !in_map(&mx.a[0], da_g, F, T, kTileM) || !in_map(&mx.a[1], da_u, F, T, kTileM) ||
-      !in_map(&mx.b[0], w_gate, F, H, box_x) || !in_map(&mx.b[1], w_up, F, H, box_x) ||
-      !make_out_tmap(&mx.out[0], dx, H, T, rH, false) ||
-      (add && !make_out_tmap(&mx.in[0], add, H, T, rH, false)))
-    return MOE_ERR_CUDA;
-  Args ph = p, px = p;
-  ph.kb = ph.kb0 = up_div(H, BK);
-  px.kb0 = up_div(F, BK);
-  px.kb = 2 * px.kb0;
-  px.add = add != nullptr;
-  if (launch<Op::GatedBwd>(mh, ph, T, F, 1, st) != cudaSuccess ||
-      launch<Op::InGrad>(mx, px, T, H, 1, st) != cudaSuccess)
-    return MOE_ERR_CUDA;
+  Maps m2{}, m1{};
+  if (T <= kFewRows) {
+    if (ffn_few_rows_backward(dy, w_gate, w_up, w_down, a_gate, a_up, add, static_cast<int>(T), H,
+                              F, act, dx, h, da_g, da_u, p.err, st) != cudaSuccess)
+      return MOE_ERR_CUDA;
+  } else {
+    // K-major B: one box of the columns that a CTA loads
+    const uint32_t box_h = narrow(T, F, 256, 1) ? 64 : 128, box_x = narrow(T, H, 256, 1) ? 64 : 128;
+    Maps mh{}, mx{};
+    if (!in_map(&mh.a[0], dy, H, T, kTileM) || !in_map(&mh.b[0], w_down, H, F, box_h) ||
+        !make_out_tmap(&mh.in[0], a_gate, F, T, rF, false) ||
+        !make_out_tmap(&mh.in[1], a_up, F, T, rF, false) ||
+        !make_out_tmap(&mh.out[0], h, F, T, rF, false) ||
+        !make_out_tmap(&mh.out[1], da_g, F, T, rF, false) ||
+        !make_out_tmap(&mh.out[2], da_u, F, T, rF, false) ||
+        !in_map(&mx.a[0], da_g, F, T, kTileM) || !in_map(&mx.a[1], da_u, F, T, kTileM) ||
+        !in_map(&mx.b[0], w_gate, F, H, box_x) || !in_map(&mx.b[1], w_up, F, H, box_x) ||
+        !make_out_tmap(&mx.out[0], dx, H, T, rH, false) ||
+        (add && !make_out_tmap(&mx.in[0], add, H, T, rH, false)))
+      return MOE_ERR_CUDA;
+    Args ph = p, px = p;
+    ph.kb = ph.kb0 = up_div(H, BK);
+    px.kb0 = up_div(F, BK);
+    px.kb = 2 * px.kb0;
+    px.add = add != nullptr;
+    if (launch<Op::GatedBwd>(mh, ph, T, F, 1, st) != cudaSuccess ||
+        launch<Op::InGrad>(mx, px, T, H, 1, st) != cudaSuccess)
+      return MOE_ERR_CUDA;
+  }
   if (!dw_gate) return MOE_OK;
   const uint64_t z = f32 ? 4 : 2;
   if (!in_map(&m2.a[0], h, F, T, BK) || !in_map(&m2.b[0], dy, H, T, BK) ||

@@ -7,7 +7,7 @@
 
 namespace moe {
 
-// Rows up to which the block's forward takes the form of ffn_rows.cu.
+// Rows up to which the block takes the form of ffn_rows.cu.
 constexpr int kFewRows = 128;
 
 // h [T, F] and, where a_gate is given, A_g and A_u; then y = bf16(add + h W_down).
@@ -15,5 +15,11 @@ constexpr int kFewRows = 128;
 cudaError_t ffn_few_rows(const void* x, const void* w_gate, const void* w_up, const void* w_down,
                          const void* add, int T, int H, int F, int act, void* y, void* a_gate,
                          void* a_up, void* h, int* err, cudaStream_t st);
+
+// h, dA_g and dA_u [T, F], then dx = bf16(add + dA_g W_gate^T + dA_u W_up^T).
+cudaError_t ffn_few_rows_backward(const void* dy, const void* w_gate, const void* w_up,
+                                  const void* w_down, const void* a_gate, const void* a_up,
+                                  const void* add, int T, int H, int F, int act, void* dx, void* h,
+                                  void* da_gate, void* da_up, int* err, cudaStream_t st);
 
 }  // namespace moe

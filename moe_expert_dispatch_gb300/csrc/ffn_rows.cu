@@ -1,19 +1,22 @@
-// ffn_rows.cu - the forward of the gated feed-forward block for few rows (a
-// decoding step): both products bound by reading the weights once.
+// ffn_rows.cu - the gated feed-forward block for few rows (a decoding step, a short
+// batch): its products with the weights, all bound by reading those once.
 //
-// The roles of the operands are exchanged: 128 columns of the weights are the M of
-// a tile and the tokens its N (16 to 128), so that a tile is full of weights however
-// few the tokens are. In the first product the 128 are 64 columns of W_gate and the
-// same 64 of W_up, and the tile ends with A_g and A_u of 64 columns of h.
+//   Gated     h from x, W_gate and W_up        Down    y from h and W_down
+//   GatedBwd  h, dA_g, dA_u from dy, W_down    InGrad  dx from dA_g, dA_u, W_gate, W_up
+//
+// The roles of the operands are exchanged: 128 columns of the result are the M of a
+// tile and the tokens its N (16 to 128), so that a tile is full of weights however
+// few the tokens are. Of a Gated tile the 128 are 64 columns of W_gate and the same
+// 64 of W_up, and it ends with A_g and A_u of 64 columns of h.
 //
 // The weights arrive by TMA, 64 of K at a time (16 KB), into a ring that keeps 100
 // KB of loads under way in each of two CTAs an SM: 30 MB over the GPU, where the
 // memory's rate times its latency asks for about 8. K is split over the CTAs of a
 // cluster (up to 8) so that narrow layers fill the GPU too; the cluster adds its
 // sums up through shared memory in the order of the ranks, each CTA finishing every
-// C-th token, and no sum depends on timing. The second product is launched while the
-// first runs (programmatic dependent launch): its rings fill with W_down before it
-// waits for h.
+// C-th token, and no sum depends on timing. The second product of a pass is launched
+// while the first runs (programmatic dependent launch): its rings fill with weights
+// before it waits for the first one's results.
 #include "act.cuh"
 #include "common.cuh"
 #include "ffn.h"
@@ -40,21 +43,27 @@ struct Smem {
   int zero;
 };
 
+enum class Op { Gated, Down, GatedBwd, InGrad };
+// weights with the columns of the result contiguous (MN-major), or with K (K-major)
+constexpr bool w_mn(Op op) { return op == Op::Gated || op == Op::Down; }
+
 struct Maps {
-  CUtensorMap w[2], x;
+  CUtensorMap w[2], x[2];
 };
 
 struct Args {
   int T, tn;             // rows, and rounded up to the MMA's N
-  int N, kb;             // columns of the result, k-blocks
+  int N, kb0, kb;        // columns of the result; k-blocks of the first operands, of both
   int split;             // CTAs of a cluster
   int stages;
   int tmem_cols;
   int act;
   const __nv_bfloat16* add;
-  __nv_bfloat16* out;    // h or y
-  __nv_bfloat16* a_gate;
+  __nv_bfloat16* out;    // h, y, h again or dx
+  __nv_bfloat16* a_gate; // Gated: A_g and A_u where they are kept; GatedBwd: as they were kept
   __nv_bfloat16* a_up;
+  __nv_bfloat16* da_gate;
+  __nv_bfloat16* da_up;
   int* err;
   unsigned long long wait_ns;
 };
@@ -68,8 +77,27 @@ __device__ __forceinline__ float act_any(int act, float z) {
   }
 }
 
-// A cluster takes one tile of weight columns, each of its CTAs a run of k-blocks.
-template <bool kGated>
+__device__ __forceinline__ void act_both_any(int act, float z, float& f, float& d) {
+  switch (act) {
+    case MOE_ACT_SILU: act_both<MOE_ACT_SILU>(z, f, d); break;
+    case MOE_ACT_GELU: act_both<MOE_ACT_GELU>(z, f, d); break;
+    case MOE_ACT_GELU_TANH: act_both<MOE_ACT_GELU_TANH>(z, f, d); break;
+    default: act_both<MOE_ACT_RELU>(z, f, d); break;
+  }
+}
+
+__device__ __forceinline__ float4 bf16x4(const __nv_bfloat16* p) {
+  const uint2 w = *reinterpret_cast<const uint2*>(p);
+  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u),
+                     __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u));
+}
+
+__device__ __forceinline__ void put_bf16x4(__nv_bfloat16* p, float a, float b, float c, float d) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(a, b), pack_bf16x2(c, d));
+}
+
+// A cluster takes one tile of columns, each of its CTAs a run of k-blocks.
+template <Op op>
 __global__ void __launch_bounds__(kThreads)
     rows_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args p) {
   extern __shared__ uint8_t smem_raw[];
@@ -78,6 +106,7 @@ __global__ void __launch_bounds__(kThreads)
   Smem* sm = reinterpret_cast<Smem*>(ring + kRingBytes);
   const int warp = threadIdx.x >> 5, lane = lane_id();
   const uint32_t rank = cluster_ctarank();
+  constexpr bool kGated = op == Op::Gated, kMn = w_mn(op);
   const int tile = static_cast<int>(blockIdx.x) / p.split;
   const int n0 = tile * (kGated ? 64 : 128);
   const int per = (p.kb + p.split - 1) / p.split;
@@ -103,7 +132,7 @@ __global__ void __launch_bounds__(kThreads)
   tc_fence_after();
   const uint32_t tmem = sm->tmem_base;
   volatile int* abort_flag = &sm->abort;
-  if (kGated) grid_dependents_launch();
+  if (kGated || op == Op::GatedBwd) grid_dependents_launch();
 
   if (warp == 0) {
     if (lane == 0) {
@@ -112,12 +141,20 @@ __global__ void __launch_bounds__(kThreads)
       auto load_w = [&](int kb, int s) {
         const uint32_t bar = smem_u32(&sm->full[s]), sa = ring0 + s * stage_bytes;
         mbar_arrive_expect_tx(bar, stage_bytes);
-        tma_load_2d_hint(sa, &maps.w[0], bar, n0, kb * BK, pol);
-        tma_load_2d_hint(sa + kBox, &maps.w[kGated ? 1 : 0], bar, kGated ? n0 : n0 + 64, kb * BK,
-                         pol);
+        if (kMn) {
+          tma_load_2d_hint(sa, &maps.w[0], bar, n0, kb * BK, pol);
+          tma_load_2d_hint(sa + kBox, &maps.w[kGated ? 1 : 0], bar, kGated ? n0 : n0 + 64, kb * BK,
+                           pol);
+        } else {
+          const bool second = op == Op::InGrad && kb >= p.kb0;
+          tma_load_2d_hint(sa, &maps.w[second ? 1 : 0], bar, (second ? kb - p.kb0 : kb) * BK, n0,
+                           pol);
+        }
       };
       auto load_x = [&](int kb, int s) {
-        tma_load_2d(ring0 + s * stage_bytes + kWBytes, &maps.x, smem_u32(&sm->full[s]), kb * BK, 0);
+        const bool second = op == Op::InGrad && kb >= p.kb0;
+        tma_load_2d(ring0 + s * stage_bytes + kWBytes, &maps.x[second ? 1 : 0],
+                    smem_u32(&sm->full[s]), (second ? kb - p.kb0 : kb) * BK, 0);
       };
       // weights fill the ring before the rows are there
       const int first = min(S, kb1 - kb0);
@@ -152,8 +189,8 @@ __global__ void __launch_bounds__(kThreads)
     }
   } else if (warp == 1) {
     if (lane == 0) {
-      // weights: MN-major atoms of 64 columns, 8 KB apart; rows of x: K-major
-      const uint32_t idesc = idesc_bf16(128, p.tn, true, false);
+      // weights: MN-major atoms of 64 columns, 8 KB apart, or K-major like the rows
+      const uint32_t idesc = idesc_bf16(128, p.tn, kMn, false);
       const uint32_t ring0 = smem_u32(ring);
       int stage = 0;
       uint32_t phase = 0;
@@ -165,10 +202,11 @@ __global__ void __launch_bounds__(kThreads)
         }
         tc_fence_after();
         const uint32_t sa = ring0 + stage * stage_bytes;
-        const uint64_t ad = sdesc_sw128(sa, kBox, 1024), bd = sdesc_sw128(sa + kWBytes, 16, 1024);
+        const uint64_t ad = sdesc_sw128(sa, kMn ? kBox : 16, 1024);
+        const uint64_t bd = sdesc_sw128(sa + kWBytes, 16, 1024);
 #pragma unroll
         for (int ks = 0; ks < BK / 16; ++ks)
-          umma_bf16(tmem, ad + ks * (2048 >> 4), bd + ks * (32 >> 4), idesc,
+          umma_bf16(tmem, ad + ks * (kMn ? 2048 >> 4 : 32 >> 4), bd + ks * (32 >> 4), idesc,
                     (kb > kb0 || ks) ? 1u : 0u);
         umma_commit(smem_u32(&sm->empty[stage]));
         if (++stage == S) {
@@ -230,31 +268,39 @@ __global__ void __launch_bounds__(kThreads)
       const int col = n0 + (lane & 15) * 4;
       const int64_t at = static_cast<int64_t>(t) * p.N + col;
       const bool up = lane >= 16;
-      if (p.a_gate && col < p.N)
-        *reinterpret_cast<uint2*>((up ? p.a_up : p.a_gate) + at) =
-            make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+      if (p.a_gate && col < p.N) put_bf16x4((up ? p.a_up : p.a_gate) + at, s.x, s.y, s.z, s.w);
       const float ux = __shfl_down_sync(0xffffffffu, s.x, 16);
       const float uy = __shfl_down_sync(0xffffffffu, s.y, 16);
       const float uz = __shfl_down_sync(0xffffffffu, s.z, 16);
       const float uw = __shfl_down_sync(0xffffffffu, s.w, 16);
       if (!up && col < p.N)
-        *reinterpret_cast<uint2*>(p.out + at) =
-            make_uint2(pack_bf16x2(act_any(p.act, s.x) * ux, act_any(p.act, s.y) * uy),
-                       pack_bf16x2(act_any(p.act, s.z) * uz, act_any(p.act, s.w) * uw));
+        put_bf16x4(p.out + at, act_any(p.act, s.x) * ux, act_any(p.act, s.y) * uy,
+                   act_any(p.act, s.z) * uz, act_any(p.act, s.w) * uw);
+      continue;
+    }
+    const int col = n0 + lane * 4;
+    if (col >= p.N) continue;
+    const int64_t at = static_cast<int64_t>(t) * p.N + col;
+    if (op == Op::GatedBwd) {
+      const float4 g = bf16x4(p.a_gate + at), u = bf16x4(p.a_up + at);
+      float4 f, d;
+      act_both_any(p.act, g.x, f.x, d.x);
+      act_both_any(p.act, g.y, f.y, d.y);
+      act_both_any(p.act, g.z, f.z, d.z);
+      act_both_any(p.act, g.w, f.w, d.w);
+      put_bf16x4(p.out + at, f.x * u.x, f.y * u.y, f.z * u.z, f.w * u.w);
+      put_bf16x4(p.da_gate + at, s.x * u.x * d.x, s.y * u.y * d.y, s.z * u.z * d.z,
+                 s.w * u.w * d.w);
+      put_bf16x4(p.da_up + at, s.x * f.x, s.y * f.y, s.z * f.z, s.w * f.w);
     } else {
-      const int col = n0 + lane * 4;
-      if (col < p.N) {
-        const int64_t at = static_cast<int64_t>(t) * p.N + col;
-        if (p.add) {
-          const uint2 a = *reinterpret_cast<const uint2*>(p.add + at);
-          s.x += __uint_as_float(a.x << 16);
-          s.y += __uint_as_float(a.x & 0xFFFF0000u);
-          s.z += __uint_as_float(a.y << 16);
-          s.w += __uint_as_float(a.y & 0xFFFF0000u);
-        }
-        *reinterpret_cast<uint2*>(p.out + at) =
-            make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+      if (p.add) {
+        const float4 a = bf16x4(p.add + at);
+        s.x += a.x;
+        s.y += a.y;
+        s.z += a.z;
+        s.w += a.w;
       }
+      put_bf16x4(p.out + at, s.x, s.y, s.z, s.w);
     }
   }
   if (p.split > 1) cluster_sync();               // the others have read this CTA's sums
@@ -275,9 +321,9 @@ int pick_split(int tiles, int kb) {
   return s;
 }
 
-template <bool kGated>
+template <Op op>
 cudaError_t launch(const Maps& maps, Args p, cudaStream_t st) {
-  auto kern = rows_kernel<kGated>;
+  auto kern = rows_kernel<op>;
   static bool configured[kMaxDevices] = {};
   const int d = current_device();
   if (d < 0 || d >= kMaxDevices) return cudaErrorInvalidDevice;
@@ -291,7 +337,7 @@ cudaError_t launch(const Maps& maps, Args p, cudaStream_t st) {
   p.tmem_cols = p.tn <= 32 ? 32 : p.tn <= 64 ? 64 : 128;
   const int stage_bytes = kWBytes + p.tn * BK * 2;
   p.stages = kRingBytes / stage_bytes < kMaxStages ? kRingBytes / stage_bytes : kMaxStages;
-  const int cols = kGated ? 64 : 128, tiles = (p.N + cols - 1) / cols;
+  const int cols = op == Op::Gated ? 64 : 128, tiles = (p.N + cols - 1) / cols;
   p.split = pick_split(tiles, p.kb);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
@@ -306,8 +352,12 @@ cudaError_t launch(const Maps& maps, Args p, cudaStream_t st) {
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = kGated ? 1 : 2;
+  cfg.numAttrs = op == Op::Down || op == Op::InGrad ? 2 : 1;   // those run beside the one before
   return cudaLaunchKernelEx(&cfg, kern, maps, p);
+}
+
+bool rows_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint32_t box_outer) {
+  return make_tmap_bf16_2d(m, base, inner, outer, inner * 2, BK, box_outer);
 }
 
 }  // namespace
@@ -315,33 +365,61 @@ cudaError_t launch(const Maps& maps, Args p, cudaStream_t st) {
 cudaError_t ffn_few_rows(const void* x, const void* w_gate, const void* w_up, const void* w_down,
                          const void* add, int T, int H, int F, int act, void* y, void* a_gate,
                          void* a_up, void* h, int* err, cudaStream_t st) {
-  Maps m1, m2;
+  Maps m1{}, m2{};
   const uint32_t rows = static_cast<uint32_t>((T + 15) / 16 * 16);
-  const uint64_t rF = static_cast<uint64_t>(F) * 2, rH = static_cast<uint64_t>(H) * 2;
-  if (!make_tmap_bf16_2d(&m1.w[0], w_gate, F, H, rF, 64, BK) ||
-      !make_tmap_bf16_2d(&m1.w[1], w_up, F, H, rF, 64, BK) ||
-      !make_tmap_bf16_2d(&m1.x, x, H, T, rH, BK, rows) ||
-      !make_tmap_bf16_2d(&m2.w[0], w_down, H, F, rH, 64, BK) ||
-      !make_tmap_bf16_2d(&m2.x, h, F, T, rF, BK, rows))
+  if (!rows_map(&m1.w[0], w_gate, F, H, BK) || !rows_map(&m1.w[1], w_up, F, H, BK) ||
+      !rows_map(&m1.x[0], x, H, T, rows) || !rows_map(&m2.w[0], w_down, H, F, BK) ||
+      !rows_map(&m2.x[0], h, F, T, rows))
     return cudaErrorInvalidValue;
-  m2.w[1] = m2.w[0];
   Args p{};
   p.T = T;
   p.N = F;
-  p.kb = (H + BK - 1) / BK;
+  p.kb = p.kb0 = (H + BK - 1) / BK;
   p.act = act;
   p.out = static_cast<__nv_bfloat16*>(h);
   p.a_gate = static_cast<__nv_bfloat16*>(a_gate);
   p.a_up = static_cast<__nv_bfloat16*>(a_up);
   p.err = err;
   p.wait_ns = kDefaultWaitNs;
-  const cudaError_t e = launch<true>(m1, p, st);
+  const cudaError_t e = launch<Op::Gated>(m1, p, st);
   if (e != cudaSuccess) return e;
   p.N = H;
-  p.kb = (F + BK - 1) / BK;
+  p.kb = p.kb0 = (F + BK - 1) / BK;
   p.add = static_cast<const __nv_bfloat16*>(add);
   p.out = static_cast<__nv_bfloat16*>(y);
-  return launch<false>(m2, p, st);
+  return launch<Op::Down>(m2, p, st);
+}
+
+cudaError_t ffn_few_rows_backward(const void* dy, const void* w_gate, const void* w_up,
+                                  const void* w_down, const void* a_gate, const void* a_up,
+                                  const void* add, int T, int H, int F, int act, void* dx, void* h,
+                                  void* da_gate, void* da_up, int* err, cudaStream_t st) {
+  Maps m1{}, m2{};
+  const uint32_t rows = static_cast<uint32_t>((T + 15) / 16 * 16);
+  if (!rows_map(&m1.w[0], w_down, H, F, 128) || !rows_map(&m1.x[0], dy, H, T, rows) ||
+      !rows_map(&m2.w[0], w_gate, F, H, 128) || !rows_map(&m2.w[1], w_up, F, H, 128) ||
+      !rows_map(&m2.x[0], da_gate, F, T, rows) || !rows_map(&m2.x[1], da_up, F, T, rows))
+    return cudaErrorInvalidValue;
+  Args p{};
+  p.T = T;
+  p.N = F;
+  p.kb = p.kb0 = (H + BK - 1) / BK;
+  p.act = act;
+  p.out = static_cast<__nv_bfloat16*>(h);
+  p.a_gate = static_cast<__nv_bfloat16*>(const_cast<void*>(a_gate));
+  p.a_up = static_cast<__nv_bfloat16*>(const_cast<void*>(a_up));
+  p.da_gate = static_cast<__nv_bfloat16*>(da_gate);
+  p.da_up = static_cast<__nv_bfloat16*>(da_up);
+  p.err = err;
+  p.wait_ns = kDefaultWaitNs;
+  const cudaError_t e = launch<Op::GatedBwd>(m1, p, st);
+  if (e != cudaSuccess) return e;
+  p.N = H;
+  p.kb0 = (F + BK - 1) / BK;
+  p.kb = 2 * p.kb0;
+  p.add = static_cast<const __nv_bfloat16*>(add);
+  p.out = static_cast<__nv_bfloat16*>(dx);
+  return launch<Op::InGrad>(m2, p, st);
 }
 
 }  // namespace moe
