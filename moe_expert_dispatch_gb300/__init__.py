@@ -1129,10 +1129,10 @@ def _made(t, shape, dtype, dev):
 
 
 def _space(workspace, query, dev, *sizes):
-    """(the given workspace or a new one, its bytes)."""
+    """(the given workspace or a new one, its bytes); the size may go by the device."""
     if workspace is not None:
         return _scratch(workspace, 0, dev)
-    return _scratch(None, query(*sizes), dev)
+    return _scratch(None, _on(dev, query, *sizes), dev)
 
 
 def _matrix(t, name):
@@ -1307,8 +1307,7 @@ def moe_lora_backward(dy, x, v, a, b, adapter_ids, plan=None, scales=None, base=
     _all_fit(dev, (x, "x", rows, bf16), (dy, "dy", (T, N), bf16), (v, "v", (T, r), f32),
              (base, "base", rows, bf16), (dx, "dx", rows, bf16), (da, "da", (n, r, H), f32),
              (db, "db", (n, r, N), f32))
-    ws, ws_bytes = _scratch(workspace, 0 if workspace is not None else _on(
-        dev, _lib.moe_lora_backward_workspace_size, T, n, r), dev)
+    ws, ws_bytes = _space(workspace, _lib.moe_lora_backward_workspace_size, dev, T, n, r)
     _check(_on(dev, _lib.moe_lora_backward, dy.data_ptr(), x.data_ptr(), v.data_ptr(),
                a.data_ptr(), b.data_ptr(), order.data_ptr(), offsets.data_ptr(), _ptr(scales),
                _ptr(base), T, H, N, n, r, dx.data_ptr(), da.data_ptr(), db.data_ptr(),

@@ -5,23 +5,29 @@
 //   Gated     [A_g | A_u] = x [W_gate | W_up],  h = bf16(act(A_g) A_u)
 //   Down      y = bf16(add + h W_down)
 //   GatedBwd  dh = dy W_down^T; h, dA_g, dA_u from it and the kept A_g, A_u
-//   InGrad    dx = bf16(add + dA_g W_gate^T + dA_u W_up^T), one accumulator
-//   WGrad     dW_down = h^T dy, and [dW_gate | dW_up] = x^T [dA_g | dA_u]
+//   Joint     dx = bf16(add + dA_g W_gate^T + dA_u W_up^T), one accumulator, and
+//             dW_down = h^T dy, dW_gate = x^T dA_g, dW_up = x^T dA_u: nothing of
+//             these waits for another, so their tiles are one launch
 //
-// One kernel body serves the five. A cluster of two CTAs shares a tile of 256
-// rows and kBN columns (tcgen05.mma.cta_group::2): each CTA loads its own 128
-// rows of A and half of the tile's columns of B, the leader issues the MMAs,
-// and each CTA finishes its own 128 rows. Of a Gated tile one CTA loads columns
-// of W_gate and the other the same columns of W_up, so that the accumulator
-// holds A_g and A_u of a row in one lane. Warps: 0 the TMA producer, 1 the MMA
-// issuer, 2 to 5 the epilogue; two accumulators, so that the epilogue of a tile
-// runs beside the MMAs of the next.
+// One kernel body serves the four. A cluster of two CTAs shares a tile of 256
+// rows and 256 columns (tcgen05.mma.cta_group::2): each CTA loads its own 128
+// rows of A and half of the tile's columns of B, the leader issues the MMAs, and
+// each CTA finishes its own 128 rows. Of a Gated tile one CTA loads columns of
+// W_gate and the other the same columns of W_up, so that the accumulator holds A_g
+// and A_u of a row in one lane. Warps: 0 the TMA producer, 1 the MMA issuer, 2 to 9
+// the epilogue (two to a quarter of the rows, taking turns at 32 columns); two
+// accumulators, so that the epilogue of a tile runs beside the MMAs of the next.
 //
 // Nothing is padded: rows and columns past the matrices are the zeros that TMA
-// fills in, they add nothing, and the stores are clipped (or, where a whole
-// piece lies outside, left out). What the epilogues read besides the
-// accumulator (A_g and A_u, or add) arrives by TMA in pieces of 32 rows x 32
-// columns, one step ahead.
+// fills in, they add nothing, and the stores are clipped (or, where a whole piece
+// lies outside, left out). What the epilogues read besides the accumulator (A_g and
+// A_u, or add) arrives by TMA in pieces of 32 rows x 32 columns, a step ahead.
+//
+// Where a product has fewer tiles than the GPU has room for clusters and a long K
+// (short batches), K is split: the parts of a tile leave their accumulators as they
+// are, in float, and a small kernel adds them up in their order and does what the
+// epilogue would have done. The split is chosen from the sizes alone, so that the
+// same call gives the same bits.
 #include "act.cuh"
 #include "common.cuh"
 #include "ffn.h"
@@ -33,39 +39,37 @@ int* device_error_word();
 
 namespace {
 
-enum class Op { Gated, Down, GatedBwd, InGrad, WGradB16, WGradF32 };
+enum class Op { Gated, Down, GatedBwd, Joint };
+// What a tile of Joint is; Main is the product of the other three, and dx.
+enum Kind { kNone = -1, kMain = 0, kDwDown = 1, kDwGate = 2, kDwUp = 3 };
 
 constexpr int BK = 64;                         // k-block: 128 bytes of bf16
+constexpr int BN = 256;                        // columns of an accumulator
 constexpr int kABytes = kTileM * BK * 2;       // 16 KB: this CTA's rows of A
 constexpr int kBox = 64 * BK * 2;              // 8 KB: 64 columns x 64 of K
-constexpr int kStageBytes = 2 * kABytes;       // A and up to 128 columns of B
-constexpr int kThreads = 192;
+constexpr int kStageBytes = 2 * kABytes;       // A and 128 columns of B
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kPieceBytes = 32 * 64;           // 32 rows x 64 bytes, 64-byte swizzle
+constexpr int kSlots = 2;                      // pieces on their way out, of a warp
 constexpr unsigned long long kDrainNs = 1000000000ull;
 constexpr unsigned long long kPairDrainNs = 50000000ull;
+constexpr int kMaxSplit = 8;
 
-// pieces that a warp reads for 32 columns, out slots per warp, ring depth: what
-// 227 KB hold
+// pieces that a warp reads for 32 columns, and the ring depth that 227 KB leave
 template <Op op>
-constexpr int loads() { return op == Op::GatedBwd ? 2 : (op == Op::Down || op == Op::InGrad) ? 1 : 0; }
+constexpr int loads() { return op == Op::GatedBwd ? 2 : op == Op::Gated ? 0 : 1; }
 template <Op op>
-constexpr int out_slots() { return loads<op>() == 1 ? 2 : 3; }
-template <Op op>
-constexpr int stages() { return loads<op>() == 2 ? 5 : 6; }
+constexpr int stages() { return loads<op>() ? 5 : 6; }
 constexpr int kMaxStages = 6;
-
-template <Op op>
-constexpr bool a_mn() { return op == Op::WGradB16 || op == Op::WGradF32; }
-template <Op op>
-constexpr bool b_mn() { return op != Op::GatedBwd && op != Op::InGrad; }
 
 struct Smem {
   uint64_t full[kMaxStages];
   uint64_t empty[kMaxStages];
   uint64_t tfull[2];
   uint64_t tempty[2];
-  uint64_t in[4][2];
+  uint64_t in[kEpiWarps];
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
@@ -73,7 +77,7 @@ struct Smem {
 };
 
 template <Op op>
-constexpr int pieces_bytes() { return 4 * (out_slots<op>() + 2 * loads<op>()) * kPieceBytes; }
+constexpr int pieces_bytes() { return kEpiWarps * (kSlots + loads<op>()) * kPieceBytes; }
 template <Op op>
 constexpr size_t smem_bytes() {
   return 1024 + static_cast<size_t>(stages<op>()) * kStageBytes + pieces_bytes<op>() + sizeof(Smem);
@@ -81,36 +85,86 @@ constexpr size_t smem_bytes() {
 static_assert(smem_bytes<Op::Gated>() <= 232448 && smem_bytes<Op::Down>() <= 232448 &&
               smem_bytes<Op::GatedBwd>() <= 232448, "shared memory of one CTA");
 
+// Operands by kind: Main a[0], b[0] (a[1], b[1]: W_up, or dA_u with W_up), the
+// weight gradients from [2] on.
 struct Maps {
-  CUtensorMap a[2], b[2], out[3], in[2];
+  CUtensorMap a[4], b[5];
+  CUtensorMap out[4], in[2], part;
+};
+
+struct Grid {
+  int M, N;          // rows and columns of the result
+  int mt, nt;        // tiles
+  int group;         // row tiles that one column tile is walked over
 };
 
 struct Args {
-  int M, N;          // rows and (per output) columns of the result
-  int mt, nt;        // tiles; nt of both outputs of a WGrad together
-  int nt0;           // WGrad: tiles of the first output
-  int kb0, kb;       // k-blocks of the first pair of operands, and of both
-  int group;         // row tiles that one column tile is walked over
-  int act;           // Gated, GatedBwd
-  int keep;          // Gated: A_g and A_u are stored
-  int add;           // Down, InGrad: in[0] is added
-  int accumulate;    // WGradF32
+  Grid main, down, gate;       // Joint: dW_down; dW_gate and dW_up
+  int kb0, kb;                 // Main: k-blocks of the first pair of operands, and of both
+  int kb_rows;                 // weight gradients: k-blocks (of rows)
+  int split, per;              // Main: parts of K, k-blocks of a part
+  int units;                   // of Main: tiles times parts
+  int dw_units;                // tiles of the weight gradients
+  int skip;                    // their rounds that clusters with a unit of Main stay out of
+  int act;
+  int keep;                    // Gated: A_g and A_u are stored
+  int add;                     // Down, Joint: in[0] is added
+  int f32, accumulate;         // weight gradients
   int* err;
   unsigned long long wait_ns;
 };
 
-struct Tile { int m, n; };
+struct Unit {
+  int kind, m, n, part, kb0, kb1;
+};
 
 // Column tiles follow one another over groups of row tiles: a group's rows of A
 // stay in L2 while the columns of B stream by once a group.
-__device__ __forceinline__ Tile decode(int t, const Args& p) {
-  const int per = p.group * p.nt;
-  const int g = t / per, local = t - g * per;
-  const int rows = min(p.group, p.mt - g * p.group);
-  Tile r;
-  r.n = local / rows;
-  r.m = g * p.group + local - r.n * rows;
-  return r;
+__device__ __forceinline__ void place(int t, const Grid& g, Unit& u) {
+  const int per = g.group * g.nt;
+  const int i = t / per, local = t - i * per;
+  const int rows = min(g.group, g.mt - i * g.group);
+  u.n = local / rows;
+  u.m = i * g.group + local - u.n * rows;
+}
+
+// The i-th unit of a cluster. Units of Main go round the clusters. Weight gradients
+// follow: where Main has fewer units than there are clusters, those with one join in
+// when the others have done as much.
+template <Op op>
+__device__ __forceinline__ Unit unit_at(int i, const Args& p, int cluster, int clusters) {
+  Unit u = {kNone, 0, 0, 0, 0, 0};
+  int t = cluster + i * clusters;
+  if (t < p.units) {
+    const int tiles = p.main.mt * p.main.nt;
+    u.kind = kMain;
+    u.part = t / tiles;
+    place(t - u.part * tiles, p.main, u);
+    u.kb0 = min(p.kb, u.part * p.per);
+    u.kb1 = min(p.kb, u.kb0 + p.per);
+    return u;
+  }
+  if (op != Op::Joint) return u;
+  const int mine = p.units / clusters + (cluster < p.units % clusters ? 1 : 0);
+  const int r = i - mine;
+  if (p.units < clusters) {
+    const int rest = clusters - p.units;
+    if (cluster >= p.units && r < p.skip) t = r * rest + cluster - p.units;
+    else t = p.skip * rest + (cluster >= p.units ? r - p.skip : r) * clusters + cluster;
+  } else {
+    t = r * clusters + (cluster + clusters - p.units % clusters) % clusters;
+  }
+  if (t >= p.dw_units) return u;
+  const int down = p.down.mt * p.down.nt, gate = p.gate.mt * p.gate.nt;
+  u.kb1 = p.kb_rows;
+  if (t < down) {
+    u.kind = kDwDown;
+    place(t, p.down, u);
+  } else {
+    u.kind = t - down < gate ? kDwGate : kDwUp;
+    place(t - down - (u.kind == kDwUp ? gate : 0), p.gate, u);
+  }
+  return u;
 }
 
 // 32 accumulator columns of A_g and A_u -> 16 words of h.
@@ -125,13 +179,13 @@ __device__ __forceinline__ void gated_words(const uint32_t* g, const uint32_t* u
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// 32 columns of dh and the kept A_g, A_u (16 words each) -> dA_g over g, dA_u over u,
+// 2 n columns of dh and the kept A_g, A_u (n words each) -> dA_g over g, dA_u over u,
 // and h.
-template <int kAct>
+template <int kAct, int n>
 __device__ __forceinline__ void gated_bwd_words(const uint32_t* dh, uint32_t* g, uint32_t* u,
                                                 uint32_t* h) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
+  for (int i = 0; i < n; ++i) {
     float f0, f1, d0, d1;
     act_both<kAct>(lo_f(g[i]), f0, d0);
     act_both<kAct>(hi_f(g[i]), f1, d1);
@@ -143,26 +197,32 @@ __device__ __forceinline__ void gated_bwd_words(const uint32_t* dh, uint32_t* g,
   }
 }
 
+template <int n>
+__device__ __forceinline__ void gated_bwd_any(int act, const uint32_t* dh, uint32_t* g, uint32_t* u,
+                                              uint32_t* h) {
+  switch (act) {
+    case MOE_ACT_SILU: gated_bwd_words<MOE_ACT_SILU, n>(dh, g, u, h); break;
+    case MOE_ACT_GELU: gated_bwd_words<MOE_ACT_GELU, n>(dh, g, u, h); break;
+    case MOE_ACT_GELU_TANH: gated_bwd_words<MOE_ACT_GELU_TANH, n>(dh, g, u, h); break;
+    default: gated_bwd_words<MOE_ACT_RELU, n>(dh, g, u, h); break;
+  }
+}
+
 // ------------------------------------------------------------------ the kernel
 
-template <Op op, int kBN>
+template <Op op>
 __global__ void __launch_bounds__(kThreads, 1)
     dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args p) {
   extern __shared__ uint8_t smem_raw[];
-  constexpr bool kAmn = a_mn<op>(), kBmn = b_mn<op>();
-  constexpr bool kWGrad = op == Op::WGradB16 || op == Op::WGradF32;
-  constexpr int S = stages<op>(), kLoads = loads<op>(), kSlots = out_slots<op>();
-  constexpr int kHalfN = kBN / 2;              // columns of B that a CTA loads
-  constexpr int kOutN = op == Op::Gated ? kBN / 2 : kBN;   // columns of the result in a tile
+  constexpr int S = stages<op>(), kLoads = loads<op>();
   uint8_t* ring = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* pieces = ring + S * kStageBytes;
   Smem* sm = reinterpret_cast<Smem*>(pieces + pieces_bytes<op>());
   const int warp = threadIdx.x >> 5, lane = lane_id();
   const uint32_t rank = cluster_ctarank();
-  const int walk0 = static_cast<int>(blockIdx.x >> 1);
-  const int step = static_cast<int>(gridDim.x >> 1);
-  const int total = p.mt * p.nt;
+  const int cluster = static_cast<int>(blockIdx.x >> 1);
+  const int clusters = static_cast<int>(gridDim.x >> 1);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -171,9 +231,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(smem_u32(&sm->tfull[a]), 1);
-      mbar_init(smem_u32(&sm->tempty[a]), 8);   // the epilogue warps of both CTAs
-      for (int q = 0; q < 4; ++q) mbar_init(smem_u32(&sm->in[q][a]), 1);
+      mbar_init(smem_u32(&sm->tempty[a]), 2 * kEpiWarps);   // the epilogue warps of both CTAs
     }
+    for (int e = 0; e < kEpiWarps; ++e) mbar_init(smem_u32(&sm->in[e]), 1);
     mbar_init(smem_u32(&sm->drain), 1);
     sm->abort = 0;
     sm->zero = 0;
@@ -189,6 +249,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem_base = sm->tmem_base;
   volatile int* abort_flag = &sm->abort;
+  grid_dependency_wait();    // Joint and Down run beside the launch before them
+  grid_dependents_launch();
 
   if (warp == 0) {
     // ---------------------------------------------------------- producer
@@ -198,13 +260,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       const uint64_t pol = l2_policy_evict_normal();
       const uint32_t ring0 = smem_u32(ring);
-      for (int t = walk0; t < total && ok; t += step) {
-        const Tile tl = decode(t, p);
-        const int m0 = (2 * tl.m + static_cast<int>(rank)) * kTileM;
-        const bool second = kWGrad && tl.n >= p.nt0;        // WGrad: the second output
-        int n0 = (kWGrad && second ? tl.n - p.nt0 : tl.n) * kOutN;
-        if (op != Op::Gated) n0 += static_cast<int>(rank) * kHalfN;
-        for (int kb = 0; kb < p.kb; ++kb) {
+      fence_proxy_async();
+      for (int i = 0; ok; ++i) {
+        const Unit u = unit_at<op>(i, p, cluster, clusters);
+        if (u.kind == kNone) break;
+        const bool wgrad = op == Op::Joint && u.kind != kMain;
+        const int m0 = (2 * u.m + static_cast<int>(rank)) * kTileM;
+        const int n0 = op == Op::Gated ? u.n * (BN / 2)
+                                       : u.n * BN + static_cast<int>(rank) * (BN / 2);
+        for (int kb = u.kb0; kb < u.kb1; ++kb) {
           const uint32_t full = smem_u32(&sm->full[stage]);
           if (!mbar_wait(smem_u32(&sm->empty[stage]), phase ^ 1, p.wait_ns, abort_flag)) {
             ok = false;
@@ -213,24 +277,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t sa = ring0 + stage * kStageBytes, sb = sa + kABytes;
           // both CTAs' copies complete on the leader's barrier
           const uint32_t full_l = mapa_shared(full, 0);
-          if (rank == 0) mbar_arrive_expect_tx(full, 2 * (kABytes + kHalfN * BK * 2));
-          const bool part1 = op == Op::InGrad && kb >= p.kb0;
-          const int k0 = (part1 ? kb - p.kb0 : kb) * BK;
-          const CUtensorMap* ma = &maps.a[part1 ? 1 : 0];
-          const CUtensorMap* mb =
-              &maps.b[(op == Op::Gated ? rank == 1 : op == Op::InGrad ? part1 : second) ? 1 : 0];
-          if (kAmn) {
-            tma_load_2d_pair(sa, ma, full_l, m0, k0, pol);
-            tma_load_2d_pair(sa + kBox, ma, full_l, m0 + 64, k0, pol);
+          if (rank == 0) mbar_arrive_expect_tx(full, 2 * kStageBytes);
+          if (wgrad) {                         // both operands MN-major: boxes of 64 columns
+            const CUtensorMap* ma = &maps.a[u.kind == kDwDown ? 2 : 3];
+            const CUtensorMap* mb = &maps.b[1 + u.kind];
+            tma_load_2d_pair(sa, ma, full_l, m0, kb * BK, pol);
+            tma_load_2d_pair(sa + kBox, ma, full_l, m0 + 64, kb * BK, pol);
+            tma_load_2d_pair(sb, mb, full_l, n0, kb * BK, pol);
+            tma_load_2d_pair(sb + kBox, mb, full_l, n0 + 64, kb * BK, pol);
           } else {
-            tma_load_2d_pair(sa, ma, full_l, k0, m0, pol);
-          }
-          if (kBmn) {
-#pragma unroll
-            for (int j = 0; j < kHalfN / 64; ++j)
-              tma_load_2d_pair(sb + j * kBox, mb, full_l, n0 + 64 * j, k0, pol);
-          } else {
-            tma_load_2d_pair(sb, mb, full_l, k0, n0, pol);
+            const int second = op == Op::Joint && kb >= p.kb0 ? 1 : 0;
+            const int k0 = (second ? kb - p.kb0 : kb) * BK;
+            tma_load_2d_pair(sa, &maps.a[second], full_l, k0, m0, pol);
+            if (op == Op::Gated || op == Op::Down) {
+              const CUtensorMap* mb = &maps.b[op == Op::Gated ? rank : 0];
+              tma_load_2d_pair(sb, mb, full_l, n0, k0, pol);
+              tma_load_2d_pair(sb + kBox, mb, full_l, n0 + 64, k0, pol);
+            } else {
+              tma_load_2d_pair(sb, &maps.b[second], full_l, k0, n0, pol);
+            }
           }
           ++fills;
           if (++stage == S) {
@@ -253,25 +318,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer
     if (lane == 0 && rank == 0) {
-      const uint32_t idesc = idesc_bf16(2 * kTileM, kBN, kAmn, kBmn);
-      const uint32_t ring0 = smem_u32(ring);
+      constexpr bool kBmnMain = op == Op::Gated || op == Op::Down;
       // K-major, 128-byte swizzle: groups of 8 rows 1 KB apart, 32 bytes a step of K = 16.
       // MN-major: atoms of 64 columns 8 KB apart, groups of 8 of K 1 KB apart, 2 KB a step
-      const uint64_t ad0 = sdesc_sw128(ring0, kAmn ? kBox : 16, 1024);
-      const uint64_t bd0 = sdesc_sw128(ring0 + kABytes, kBmn ? kBox : 16, 1024);
-      constexpr uint64_t kAStep = kAmn ? (2048 >> 4) : (32 >> 4);
-      constexpr uint64_t kBStep = kBmn ? (2048 >> 4) : (32 >> 4);
+      const uint32_t ring0 = smem_u32(ring);
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true, issued = false;
-      for (int t = walk0; t < total && ok; t += step) {
+      for (int i = 0; ok; ++i) {
+        const Unit u = unit_at<op>(i, p, cluster, clusters);
+        if (u.kind == kNone) break;
+        const bool wgrad = op == Op::Joint && u.kind != kMain, bmn = kBmnMain || wgrad;
+        const uint32_t idesc = idesc_bf16(2 * kTileM, BN, wgrad, bmn);
+        const uint64_t ad0 = sdesc_sw128(ring0, wgrad ? kBox : 16, 1024);
+        const uint64_t bd0 = sdesc_sw128(ring0 + kABytes, bmn ? kBox : 16, 1024);
+        const uint64_t a_step = wgrad ? 2048 >> 4 : 32 >> 4, b_step = bmn ? 2048 >> 4 : 32 >> 4;
         if (!mbar_wait(smem_u32(&sm->tempty[acc]), acc_phase ^ 1, p.wait_ns, abort_flag)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t d = tmem_base + acc * 256;
-        for (int kb = 0; kb < p.kb; ++kb) {
+        const uint32_t d = tmem_base + acc * BN;
+        for (int kb = u.kb0; kb < u.kb1; ++kb) {
           if (!mbar_wait(smem_u32(&sm->full[stage]), phase, p.wait_ns, abort_flag)) {
             ok = false;
             break;
@@ -280,8 +348,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t off = static_cast<uint64_t>(stage) * (kStageBytes >> 4);
 #pragma unroll
           for (int ks = 0; ks < BK / 16; ++ks)
-            umma_bf16_pair(d, ad0 + off + ks * kAStep, bd0 + off + ks * kBStep, idesc,
-                           (kb | ks) ? 1u : 0u);
+            umma_bf16_pair(d, ad0 + off + ks * a_step, bd0 + off + ks * b_step, idesc,
+                           (kb > u.kb0 || ks) ? 1u : 0u);
           umma_commit_pair_mc(smem_u32(&sm->empty[stage]), 0x3);   // the slot, in both CTAs
           issued = true;
           if (++stage == S) {
@@ -305,9 +373,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ---------------------------------------------------------- epilogue
-    const int q = warp & 3;                    // TMEM lane quadrant of this warp
-    const uint32_t out0 = smem_u32(pieces) + q * kSlots * kPieceBytes;
-    const uint32_t in0 = smem_u32(pieces) + 4 * kSlots * kPieceBytes + q * 2 * kLoads * kPieceBytes;
+    const int e = warp - 2, q = warp & 3;      // q: TMEM lane quadrant of this warp
+    const int c_first = (e >> 2) * 32;         // its first columns; the next are 64 on
+    const uint32_t out0 = smem_u32(pieces) + e * (kSlots + kLoads) * kPieceBytes;
+    const uint32_t in0 = out0 + kSlots * kPieceBytes;
+    const uint32_t in_bar = smem_u32(&sm->in[e]);
     const uint32_t my_row = lane * 64, sw = (lane >> 1) & 3;
     int npiece = 0;
     uint32_t n_asked = 0, n_got = 0;           // steps of 32 columns asked for, and waited for
@@ -330,6 +400,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ++npiece;
     };
+    auto put_rounded = [&](const uint32_t* v, const CUtensorMap* map, int x, int y) {
+      uint32_t w[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        w[i] = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+      put(w, map, x, y, false);
+    };
     auto get = [&](uint32_t slot, uint32_t* w) {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
@@ -338,29 +415,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                      : "r"(slot + my_row + ((j ^ sw) << 4))
                      : "memory");
     };
-    const bool reads = kLoads == 2 || (kLoads == 1 && p.add != 0);
-    auto ask = [&](int x, int y) {             // the pieces of the next 32 columns
+    auto ask = [&](int x, int y) {             // the pieces of 32 columns
       if (lane == 0) {
-        const int b = n_asked & 1;
-        const uint32_t bar = smem_u32(&sm->in[q][b]);
-        mbar_arrive_expect_tx(bar, kLoads * kPieceBytes);
+        mbar_arrive_expect_tx(in_bar, kLoads * kPieceBytes);
 #pragma unroll
         for (int i = 0; i < kLoads; ++i)
-          tma_load_2d(in0 + (b * kLoads + i) * kPieceBytes, &maps.in[i], bar, x, y);
+          tma_load_2d(in0 + i * kPieceBytes, &maps.in[i], in_bar, x, y);
       }
       ++n_asked;
     };
+    if (lane == 0) fence_proxy_async();
     int acc = 0;
     uint32_t acc_phase = 0;
     const uint32_t tempty0 = mapa_shared(smem_u32(&sm->tempty[0]), 0);
     bool ok = true;
-    for (int t = walk0; t < total && ok; t += step) {
-      const Tile tl = decode(t, p);
-      const bool second = kWGrad && tl.n >= p.nt0;
-      const int n0 = (second ? tl.n - p.nt0 : tl.n) * kOutN;
-      const int y = (2 * tl.m + static_cast<int>(rank)) * kTileM + q * 32;
-      const int cols = y < p.M ? min(kOutN, p.N - n0) : 0;     // 0: nothing of this warp's
-      if (reads && cols > 0) ask(n0, y);
+    for (int i = 0; ok; ++i) {
+      const Unit u = unit_at<op>(i, p, cluster, clusters);
+      if (u.kind == kNone) break;
+      const bool main = op != Op::Joint || u.kind == kMain;
+      const Grid& g = main ? p.main : u.kind == kDwDown ? p.down : p.gate;
+      const bool part = main && p.split > 1;   // the accumulator leaves as it is
+      const bool reads = !part && (kLoads == 2 || (kLoads == 1 && main && p.add != 0));
+      const int y = (2 * u.m + static_cast<int>(rank)) * kTileM + q * 32;
+      const int width = op == Op::Gated && !part ? BN / 2 : BN;
+      const int n0 = u.n * width;
+      const int cols = y >= g.M ? 0 : part ? BN : min(width, g.N - n0);   // 0: nothing to finish
+      if (reads && c_first < cols) ask(n0 + c_first, y);
       const bool got = mbar_wait(smem_u32(&sm->tfull[acc]), acc_phase, p.wait_ns, abort_flag);
       // tcgen05.ld is warp-collective: the whole warp goes on or stops together
       if (!__all_sync(0xffffffffu, got)) {
@@ -369,15 +449,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       tc_fence_after();
-      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * 256;
+      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * BN;
 #pragma unroll 1
-      for (int c = 0; c < cols; c += 32) {
-        uint32_t v[32], g[16], u[16];
+      for (int c = c_first; c < cols; c += 64) {
+        uint32_t v[32], a[16], b[16];
         if (reads) {
-          if (c + 32 < cols) ask(n0 + c + 32, y);
-          const int b = n_got & 1;
-          const bool here = mbar_wait(smem_u32(&sm->in[q][b]), (n_got >> 1) & 1, p.wait_ns,
-                                      abort_flag);
+          const bool here = mbar_wait(in_bar, n_got & 1, p.wait_ns, abort_flag);
           if (!__all_sync(0xffffffffu, here)) {
             sm->abort = 1;
             if (lane == 0) report_error(p.err, kErrTimeout);
@@ -385,13 +462,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           ++n_got;
-          get(in0 + b * kLoads * kPieceBytes, g);
-          if (kLoads == 2) get(in0 + (b * kLoads + 1) * kPieceBytes, u);
+          get(in0, a);
+          if (kLoads == 2) get(in0 + kPieceBytes, b);
+          __syncwarp();                        // read before they are asked for again
+          if (c + 64 < cols) ask(n0 + c + 64, y);
         }
         tmem_ld_32x32b_x32(taddr + c, v);
-        if (op == Op::Gated) {
+        if (part) {
+          tmem_ld_wait();
+          const int py = y + u.part * p.main.mt * 2 * kTileM;
+          put(v, &maps.part, n0 + c, py, false);
+          put(v + 16, &maps.part, n0 + c + 16, py, false);
+        } else if (op == Op::Gated) {
           uint32_t up[32], w[16];
-          tmem_ld_32x32b_x32(taddr + kBN / 2 + c, up);
+          tmem_ld_32x32b_x32(taddr + BN / 2 + c, up);
           tmem_ld_wait();
           switch (p.act) {
             case MOE_ACT_SILU: gated_words<MOE_ACT_SILU>(v, up, w); break;
@@ -401,47 +485,30 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           put(w, &maps.out[0], n0 + c, y, false);
           if (p.keep) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              w[i] = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-            put(w, &maps.out[1], n0 + c, y, false);
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              w[i] = pack_bf16x2(__uint_as_float(up[2 * i]), __uint_as_float(up[2 * i + 1]));
-            put(w, &maps.out[2], n0 + c, y, false);
+            put_rounded(v, &maps.out[1], n0 + c, y);
+            put_rounded(up, &maps.out[2], n0 + c, y);
           }
         } else if (op == Op::GatedBwd) {
           uint32_t h[16];
           tmem_ld_wait();
-          switch (p.act) {
-            case MOE_ACT_SILU: gated_bwd_words<MOE_ACT_SILU>(v, g, u, h); break;
-            case MOE_ACT_GELU: gated_bwd_words<MOE_ACT_GELU>(v, g, u, h); break;
-            case MOE_ACT_GELU_TANH: gated_bwd_words<MOE_ACT_GELU_TANH>(v, g, u, h); break;
-            default: gated_bwd_words<MOE_ACT_RELU>(v, g, u, h); break;
-          }
+          gated_bwd_any<16>(p.act, v, a, b, h);
           put(h, &maps.out[0], n0 + c, y, false);
-          put(g, &maps.out[1], n0 + c, y, false);
-          put(u, &maps.out[2], n0 + c, y, false);
-        } else if (op == Op::WGradF32) {
+          put(a, &maps.out[1], n0 + c, y, false);
+          put(b, &maps.out[2], n0 + c, y, false);
+        } else if (!main && p.f32) {
           tmem_ld_wait();
-          const CUtensorMap* map = &maps.out[second ? 1 : 0];
-          put(v, map, n0 + c, y, p.accumulate != 0);
-          if (c + 16 < cols) put(v + 16, map, n0 + c + 16, y, p.accumulate != 0);
+          put(v, &maps.out[u.kind], n0 + c, y, p.accumulate != 0);
+          if (c + 16 < cols) put(v + 16, &maps.out[u.kind], n0 + c + 16, y, p.accumulate != 0);
         } else {
-          uint32_t w[16];
           tmem_ld_wait();
+          if (reads)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float a = __uint_as_float(v[2 * i]), b = __uint_as_float(v[2 * i + 1]);
-            if (reads) {
-              a += lo_f(g[i]);
-              b += hi_f(g[i]);
+            for (int j = 0; j < 16; ++j) {
+              v[2 * j] = __float_as_uint(__uint_as_float(v[2 * j]) + lo_f(a[j]));
+              v[2 * j + 1] = __float_as_uint(__uint_as_float(v[2 * j + 1]) + hi_f(a[j]));
             }
-            w[i] = pack_bf16x2(a, b);
-          }
-          put(w, &maps.out[second ? 1 : 0], n0 + c, y, false);
+          put_rounded(v, &maps.out[u.kind], n0 + c, y);
         }
-        __syncwarp();       // this step's pieces are read before they are asked for again
       }
       if (!ok) break;
       tc_fence_before();
@@ -451,8 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (acc == 0) acc_phase ^= 1;
     }
     // what was asked for lands, and every store has been made, before the CTA exits
-    for (; n_got != n_asked; ++n_got)
-      mbar_wait(smem_u32(&sm->in[q][n_got & 1]), (n_got >> 1) & 1, kDrainNs, &sm->zero);
+    if (n_got != n_asked) mbar_wait(in_bar, n_got & 1, kDrainNs, &sm->zero);
     if (lane == 0) bulk_wait_group_all();
   }
 
@@ -467,66 +533,229 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <Op op, int kBN>
-cudaError_t launch_bn(const Maps& maps, const Args& p, cudaStream_t st) {
-  auto kern = dense_gemm_kernel<op, kBN>;
+// ------------------------------------------------------------------ parts of K added up
+
+struct FinishArgs {
+  const float* part;           // [split][mpad][ncols]
+  int64_t mpad;
+  int ncols, split, N, act;
+  int64_t T;
+  const __nv_bfloat16 *in0, *in1;     // add, or A_g and A_u
+  __nv_bfloat16 *out0, *out1, *out2;  // the epilogue's outputs
+};
+
+__device__ __forceinline__ void add_parts(const FinishArgs& p, int64_t at, float* v) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+  for (int s = 0; s < p.split; ++s) {
+    const float4* q = reinterpret_cast<const float4*>(p.part + s * p.mpad * p.ncols + at);
+    const float4 a = __ldcs(q), b = __ldcs(q + 1);
+    v[0] += a.x;
+    v[1] += a.y;
+    v[2] += a.z;
+    v[3] += a.w;
+    v[4] += b.x;
+    v[5] += b.y;
+    v[6] += b.z;
+    v[7] += b.w;
+  }
+}
+
+__device__ __forceinline__ uint4 rounded(const float* v) {
+  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                    pack_bf16x2(v[6], v[7]));
+}
+
+__device__ __forceinline__ float act_any(int act, float z) {
+  switch (act) {
+    case MOE_ACT_SILU: return act_f<MOE_ACT_SILU>(z);
+    case MOE_ACT_GELU: return act_f<MOE_ACT_GELU>(z);
+    case MOE_ACT_GELU_TANH: return act_f<MOE_ACT_GELU_TANH>(z);
+    default: return act_f<MOE_ACT_RELU>(z);
+  }
+}
+
+// Eight columns of a row a thread: the parts in their order, then what the epilogue of
+// op does with a whole sum (Joint: dx).
+template <Op op>
+__global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ FinishArgs p) {
+  grid_dependency_wait();
+  const int vecs = p.N / 8;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= p.T * vecs) return;
+  const int64_t t = i / vecs;
+  const int c = static_cast<int>(i - t * vecs) * 8;
+  const int64_t to = t * p.N + c;
+  float v[8];
+  if (op == Op::Gated) {
+    float up[8];
+    const int64_t at = t * p.ncols + c / (BN / 2) * BN + c % (BN / 2);
+    add_parts(p, at, v);
+    add_parts(p, at + BN / 2, up);
+    if (p.out1) {
+      *reinterpret_cast<uint4*>(p.out1 + to) = rounded(v);
+      *reinterpret_cast<uint4*>(p.out2 + to) = rounded(up);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = act_any(p.act, v[j]) * up[j];
+    *reinterpret_cast<uint4*>(p.out0 + to) = rounded(v);
+    return;
+  }
+  add_parts(p, t * p.ncols + c, v);
+  if (op == Op::GatedBwd) {
+    const uint4 a = *reinterpret_cast<const uint4*>(p.in0 + to);
+    const uint4 b = *reinterpret_cast<const uint4*>(p.in1 + to);
+    uint32_t g[4] = {a.x, a.y, a.z, a.w}, u[4] = {b.x, b.y, b.z, b.w}, h[4], dh[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dh[j] = __float_as_uint(v[j]);
+    gated_bwd_any<4>(p.act, dh, g, u, h);
+    *reinterpret_cast<uint4*>(p.out0 + to) = make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4*>(p.out1 + to) = make_uint4(g[0], g[1], g[2], g[3]);
+    *reinterpret_cast<uint4*>(p.out2 + to) = make_uint4(u[0], u[1], u[2], u[3]);
+    return;
+  }
+  if (p.in0) {
+    const uint4 a = *reinterpret_cast<const uint4*>(p.in0 + to);
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] += lo_f(w[j]);
+      v[2 * j + 1] += hi_f(w[j]);
+    }
+  }
+  *reinterpret_cast<uint4*>(p.out0 + to) = rounded(v);
+}
+
+// ------------------------------------------------------------------ host
+
+int up_div(int64_t a, int b) { return static_cast<int>((a + b - 1) / b); }
+
+Grid make_grid(int64_t M, int N, int cols) {
+  Grid g;
+  g.M = static_cast<int>(M);
+  g.N = N;
+  g.mt = up_div(M, 2 * kTileM);
+  g.nt = up_div(N, cols);
+  g.group = g.mt < 16 ? g.mt : 16;
+  return g;
+}
+
+int clusters() { return device_sm_count() > 1 ? device_sm_count() / 2 : 1; }
+
+// Parts of K for a product alone in its launch: as many as the clusters that its tiles
+// leave idle, each with 8 k-blocks at least (half of what a tile's start and end cost).
+int pick_split(const Grid& g, int kb) {
+  const int64_t tiles = static_cast<int64_t>(g.mt) * g.nt;
+  int s = 1;
+  while (s < kMaxSplit && tiles * (s + 1) <= clusters() && kb / (s + 1) >= 8) ++s;
+  return s;
+}
+
+// Parts of K of dx beside the weight gradients: so that none of its units lasts longer
+// than an equal share of the launch. A tile costs its k-blocks and about 8 more.
+constexpr int kTileCost = 8;
+int pick_split_joint(const Grid& g, int kb, int64_t dw_units, int kb_rows) {
+  if (dw_units == 0) return pick_split(g, kb);
+  const int64_t tiles = static_cast<int64_t>(g.mt) * g.nt;
+  const int64_t share = (tiles * (kb + kTileCost) + dw_units * (kb_rows + kTileCost)) / clusters();
+  int s = 1;
+  while (s < kMaxSplit && kb / s + kTileCost > share && kb / (s + 1) >= 8) ++s;
+  return s;
+}
+
+void set_main(Args& p, const Grid& g, int kb0, int kb, int split) {
+  p.main = g;
+  p.kb0 = kb0;
+  p.kb = kb;
+  p.split = split;
+  p.per = up_div(kb, split);
+  p.units = g.mt * g.nt * split;
+}
+
+size_t part_bytes(const Grid& g, int split) {
+  return split > 1 ? static_cast<size_t>(split) * g.mt * 2 * kTileM * g.nt * BN * sizeof(float) : 0;
+}
+
+bool part_map(CUtensorMap* m, void* base, const Grid& g, int split) {
+  if (split <= 1) return true;
+  const uint64_t cols = static_cast<uint64_t>(g.nt) * BN;
+  return make_out_tmap(m, base, cols, static_cast<uint64_t>(split) * g.mt * 2 * kTileM, cols * 4,
+                       true);
+}
+
+// beside: beside the launch before it, as far as its waits let it.
+template <typename K, typename A, typename... B>
+cudaError_t launch_beside(K kern, dim3 grid, int threads, size_t smem, int cluster, cudaStream_t st,
+                          const A& a, const B&... b) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, a, b...);
+}
+
+template <Op op>
+cudaError_t launch(const Maps& maps, const Args& p, cudaStream_t st) {
+  auto kern = dense_gemm_kernel<op>;
   static bool configured[kMaxDevices] = {};
   static int max_pairs[kMaxDevices] = {};       // clusters of two that fit at once
   const int d = current_device();
   if (d < 0 || d >= kMaxDevices) return cudaErrorInvalidDevice;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem_bytes<op>();
-  cfg.stream = st;
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   if (!configured[d]) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(smem_bytes<op>()));
     if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
     cfg.gridDim = dim3(2 * kMaxDevices);        // any even size: the query asks how many fit
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem_bytes<op>();
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
     e = cudaOccupancyMaxActiveClusters(&max_pairs[d], kern, &cfg);
     if (e != cudaSuccess) return e;
     if (max_pairs[d] < 1) return cudaErrorInvalidConfiguration;
     configured[d] = true;
   }
-  const int64_t total = static_cast<int64_t>(p.mt) * p.nt;
-  cfg.gridDim = dim3(2 * static_cast<int>(total < max_pairs[d] ? total : max_pairs[d]));
-  return cudaLaunchKernelEx(&cfg, kern, maps, p);
-}
-
-int up_div(int64_t a, int b) { return static_cast<int>((a + b - 1) / b); }
-
-// Tiles of a [M, N] result with tiles of 256 x bn, N columns in each of n_out outputs.
-void set_tiles(Args& p, int64_t M, int N, int bn, int n_out) {
-  p.M = static_cast<int>(M);
-  p.N = N;
-  p.mt = up_div(M, 2 * kTileM);
-  p.nt0 = up_div(N, bn);
-  p.nt = n_out * p.nt0;
-  p.group = p.mt < 16 ? p.mt : 16;
-}
-
-// Tiles half as wide where whole ones (of bn columns) would leave clusters without one.
-bool narrow(int64_t M, int N, int bn, int n_out) {
-  return static_cast<int64_t>(up_div(M, 2 * kTileM)) * up_div(N, bn) * n_out <
-         device_sm_count() / 2;
+  const int64_t units = static_cast<int64_t>(p.units) + p.dw_units;
+  const int n = static_cast<int>(units < max_pairs[d] ? units : max_pairs[d]);
+  if (n == 0) return cudaSuccess;
+  return launch_beside(kern, dim3(2 * n), kThreads, smem_bytes<op>(), 2, st, maps, p);
 }
 
 template <Op op>
-cudaError_t launch(Maps& maps, Args& p, int64_t M, int N, int n_out, cudaStream_t st) {
-  constexpr int bn = op == Op::Gated ? 128 : 256;
-  if (narrow(M, N, bn, n_out)) {
-    set_tiles(p, M, N, bn / 2, n_out);
-    return launch_bn<op, 128>(maps, p, st);
-  }
-  set_tiles(p, M, N, bn, n_out);
-  return launch_bn<op, 256>(maps, p, st);
+cudaError_t finish(const Args& p, const float* part, int64_t T, const void* in0, const void* in1,
+                   void* out0, void* out1, void* out2, cudaStream_t st) {
+  if (p.split <= 1) return cudaSuccess;
+  FinishArgs f;
+  f.part = part;
+  f.mpad = static_cast<int64_t>(p.main.mt) * 2 * kTileM;
+  f.ncols = p.main.nt * BN;
+  f.split = p.split;
+  f.N = p.main.N;
+  f.act = p.act;
+  f.T = T;
+  f.in0 = static_cast<const __nv_bfloat16*>(in0);
+  f.in1 = static_cast<const __nv_bfloat16*>(in1);
+  f.out0 = static_cast<__nv_bfloat16*>(out0);
+  f.out1 = static_cast<__nv_bfloat16*>(out1);
+  f.out2 = static_cast<__nv_bfloat16*>(out2);
+  const int64_t ctas = (T * (f.N / 8) + 255) / 256;
+  return launch_beside(finish_kernel<op>, dim3(static_cast<unsigned>(ctas)), 256, 0, 1, st, f);
 }
 
 bool in_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint32_t box_outer) {
@@ -543,9 +772,55 @@ moe_status check_sizes(int64_t T, int H, int F, int act) {
   return (H % 8 || F % 8) ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
 
-// mt * nt stays below 2^31 where the tensors fit in memory at all; refuse the rest
+// Units stay below 2^30 where the tensors fit in memory at all; refuse the rest.
 bool tiles_fit(int64_t M, int N) {
-  return static_cast<int64_t>(up_div(M, 2 * kTileM)) * up_div(N, 64) * 2 < INT32_MAX;
+  return static_cast<int64_t>(up_div(M, 2 * kTileM)) * up_div(N, BN / 2) < (1 << 26);
+}
+
+// The forward's workspace: h, then the parts of whichever product is being split.
+struct FwdPlan {
+  Grid gated, down;
+  int s_gated, s_down;
+  size_t part, total;
+};
+FwdPlan fwd_plan(int64_t T, int H, int F) {
+  FwdPlan f;
+  f.gated = make_grid(T, F, BN / 2);
+  f.down = make_grid(T, H, BN);
+  const bool few = T <= kFewRows;
+  f.s_gated = few ? 1 : pick_split(f.gated, up_div(H, BK));
+  f.s_down = few ? 1 : pick_split(f.down, up_div(F, BK));
+  f.part = up256(static_cast<size_t>(T) * F * 2);
+  const size_t a = part_bytes(f.gated, f.s_gated), b = part_bytes(f.down, f.s_down);
+  f.total = f.part + up256(a > b ? a : b);
+  return f;
+}
+
+// The backward's: h, dA_g, dA_u, then the parts.
+struct BwdPlan {
+  Grid dh, dx, down, gate;
+  int s_dh, s_dx, kb_rows;
+  int64_t dw_units;
+  size_t each, part, total;
+};
+BwdPlan bwd_plan(int64_t T, int H, int F, bool dw) {
+  BwdPlan b;
+  b.dh = make_grid(T, F, BN);
+  b.dx = make_grid(T, H, BN);
+  b.down = make_grid(F, H, BN);
+  b.gate = make_grid(H, F, BN);
+  b.kb_rows = up_div(T, BK);
+  b.dw_units = dw ? static_cast<int64_t>(b.down.mt) * b.down.nt +
+                        2 * static_cast<int64_t>(b.gate.mt) * b.gate.nt
+                  : 0;
+  const bool few = T <= kFewRows;
+  b.s_dh = few ? 1 : pick_split(b.dh, up_div(H, BK));
+  b.s_dx = few ? 1 : pick_split_joint(b.dx, 2 * up_div(F, BK), b.dw_units, b.kb_rows);
+  b.each = up256(static_cast<size_t>(T) * F * 2);
+  b.part = 3 * b.each;
+  const size_t x = part_bytes(b.dh, b.s_dh), y = part_bytes(b.dx, b.s_dx);
+  b.total = b.part + up256(x > y ? x : y);
+  return b;
 }
 
 }  // namespace
@@ -557,8 +832,8 @@ using namespace moe;
 extern "C" {
 
 size_t moe_gated_ffn_workspace_size(int64_t T, int H, int F) {
-  if (check_sizes(T, H, F, 0) != MOE_OK) return 0;
-  return up256(static_cast<size_t>(T) * F * 2);
+  if (check_sizes(T, H, F, 0) != MOE_OK || !tiles_fit(T, F) || !tiles_fit(T, H)) return 0;
+  return fwd_plan(T, H, F).total;
 }
 
 moe_status moe_gated_ffn(const void* x, const void* w_gate, const void* w_up, const void* w_down,
@@ -573,42 +848,49 @@ moe_status moe_gated_ffn(const void* x, const void* w_gate, const void* w_up, co
       !aligned16(add) || !aligned16(y) || !aligned16(a_gate) || !aligned16(a_up) ||
       !tiles_fit(T, F) || !tiles_fit(T, H))
     return MOE_ERR_INVALID_ARG;
-  if (!workspace || ws_bytes < moe_gated_ffn_workspace_size(T, H, F) || !aligned16(workspace))
-    return MOE_ERR_WORKSPACE;
+  const FwdPlan f = fwd_plan(T, H, F);
+  if (!workspace || ws_bytes < f.total || !aligned16(workspace)) return MOE_ERR_WORKSPACE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (T <= kFewRows)
     return ffn_few_rows(x, w_gate, w_up, w_down, add, static_cast<int>(T), H, F, act, y, a_gate,
                         a_up, workspace, device_error_word(), st) == cudaSuccess
                ? MOE_OK
                : MOE_ERR_CUDA;
-  Args p{};
-  p.act = act;
-  p.err = device_error_word();
-  p.wait_ns = kDefaultWaitNs;
+  float* part = reinterpret_cast<float*>(static_cast<char*>(workspace) + f.part);
+  Args p1{};
+  p1.act = act;
+  p1.err = device_error_word();
+  p1.wait_ns = kDefaultWaitNs;
+  Args p2 = p1;
+  p1.keep = a_gate != nullptr;
+  p2.add = add != nullptr;
+  set_main(p1, f.gated, up_div(H, BK), up_div(H, BK), f.s_gated);
+  set_main(p2, f.down, up_div(F, BK), up_div(F, BK), f.s_down);
   Maps m1{}, m2{};
   const uint64_t rF = static_cast<uint64_t>(F) * 2, rH = static_cast<uint64_t>(H) * 2;
   if (!in_map(&m1.a[0], x, H, T, kTileM) || !in_map(&m1.b[0], w_gate, F, H, BK) ||
       !in_map(&m1.b[1], w_up, F, H, BK) || !make_out_tmap(&m1.out[0], workspace, F, T, rF, false) ||
       (a_gate && (!make_out_tmap(&m1.out[1], a_gate, F, T, rF, false) ||
                   !make_out_tmap(&m1.out[2], a_up, F, T, rF, false))) ||
+      !part_map(&m1.part, part, f.gated, f.s_gated) ||
       !in_map(&m2.a[0], workspace, F, T, kTileM) || !in_map(&m2.b[0], w_down, H, F, BK) ||
       !make_out_tmap(&m2.out[0], y, H, T, rH, false) ||
-      (add && !make_out_tmap(&m2.in[0], add, H, T, rH, false)))
+      (add && !make_out_tmap(&m2.in[0], add, H, T, rH, false)) ||
+      !part_map(&m2.part, part, f.down, f.s_down))
     return MOE_ERR_CUDA;
-  Args p1 = p, p2 = p;
-  p1.keep = a_gate != nullptr;
-  p1.kb = p1.kb0 = up_div(H, BK);
-  p2.add = add != nullptr;
-  p2.kb = p2.kb0 = up_div(F, BK);
-  if (launch<Op::Gated>(m1, p1, T, F, 1, st) != cudaSuccess ||
-      launch<Op::Down>(m2, p2, T, H, 1, st) != cudaSuccess)
+  if (launch<Op::Gated>(m1, p1, st) != cudaSuccess ||
+      finish<Op::Gated>(p1, part, T, nullptr, nullptr, workspace, a_gate, a_up, st) != cudaSuccess ||
+      launch<Op::Down>(m2, p2, st) != cudaSuccess ||
+      finish<Op::Down>(p2, part, T, add, nullptr, y, nullptr, nullptr, st) != cudaSuccess)
     return MOE_ERR_CUDA;
   return MOE_OK;
 }
 
 size_t moe_gated_ffn_backward_workspace_size(int64_t T, int H, int F) {
-  if (check_sizes(T, H, F, 0) != MOE_OK) return 0;
-  return 3 * up256(static_cast<size_t>(T) * F * 2);
+  if (check_sizes(T, H, F, 0) != MOE_OK || !tiles_fit(T, F) || !tiles_fit(T, H)) return 0;
+  // dx alone is split the more, for want of weight gradients beside it
+  const size_t a = bwd_plan(T, H, F, true).total, b = bwd_plan(T, H, F, false).total;
+  return a > b ? a : b;
 }
 
 moe_status moe_gated_ffn_backward(const void* dy, const void* x, const void* w_gate,
@@ -645,63 +927,65 @@ moe_status moe_gated_ffn_backward(const void* dy, const void* x, const void* w_g
   if (!workspace || ws_bytes < moe_gated_ffn_backward_workspace_size(T, H, F) ||
       !aligned16(workspace))
     return MOE_ERR_WORKSPACE;
-  const size_t each = up256(static_cast<size_t>(T) * F * 2);
-  void* h = workspace;
-  void* da_g = static_cast<char*>(workspace) + each;
-  void* da_u = static_cast<char*>(workspace) + 2 * each;
+  const BwdPlan b = bwd_plan(T, H, F, dw_gate != nullptr);
+  char* ws = static_cast<char*>(workspace);
+  void *h = ws, *da_g = ws + b.each, *da_u = ws + 2 * b.each;
+  float* part = reinterpret_cast<float*>(ws + b.part);
   const uint64_t rF = static_cast<uint64_t>(F) * 2, rH = static_cast<uint64_t>(H) * 2;
-  Args p{};
-  p.act = act;
-  p.err = device_error_word();
-  p.wait_ns = kDefaultWaitNs;
-  Maps m2{}, m1{};
+  Args ph{};
+  ph.act = act;
+  ph.err = device_error_word();
+  ph.wait_ns = kDefaultWaitNs;
+  Args pj = ph;
+  Maps mh{}, mj{};
   if (T <= kFewRows) {
     if (ffn_few_rows_backward(dy, w_gate, w_up, w_down, a_gate, a_up, add, static_cast<int>(T), H,
-                              F, act, dx, h, da_g, da_u, p.err, st) != cudaSuccess)
+                              F, act, dx, h, da_g, da_u, ph.err, st) != cudaSuccess)
       return MOE_ERR_CUDA;
+    pj.split = 1;
   } else {
-    // K-major B: one box of the columns that a CTA loads
-    const uint32_t box_h = narrow(T, F, 256, 1) ? 64 : 128, box_x = narrow(T, H, 256, 1) ? 64 : 128;
-    Maps mh{}, mx{};
-    if (!in_map(&mh.a[0], dy, H, T, kTileM) || !in_map(&mh.b[0], w_down, H, F, box_h) ||
+    set_main(ph, b.dh, up_div(H, BK), up_div(H, BK), b.s_dh);
+    set_main(pj, b.dx, up_div(F, BK), 2 * up_div(F, BK), b.s_dx);
+    pj.add = add != nullptr;
+    if (!in_map(&mh.a[0], dy, H, T, kTileM) || !in_map(&mh.b[0], w_down, H, F, 128) ||
         !make_out_tmap(&mh.in[0], a_gate, F, T, rF, false) ||
         !make_out_tmap(&mh.in[1], a_up, F, T, rF, false) ||
         !make_out_tmap(&mh.out[0], h, F, T, rF, false) ||
         !make_out_tmap(&mh.out[1], da_g, F, T, rF, false) ||
         !make_out_tmap(&mh.out[2], da_u, F, T, rF, false) ||
-        !in_map(&mx.a[0], da_g, F, T, kTileM) || !in_map(&mx.a[1], da_u, F, T, kTileM) ||
-        !in_map(&mx.b[0], w_gate, F, H, box_x) || !in_map(&mx.b[1], w_up, F, H, box_x) ||
-        !make_out_tmap(&mx.out[0], dx, H, T, rH, false) ||
-        (add && !make_out_tmap(&mx.in[0], add, H, T, rH, false)))
+        !part_map(&mh.part, part, b.dh, b.s_dh) ||
+        !in_map(&mj.a[0], da_g, F, T, kTileM) || !in_map(&mj.a[1], da_u, F, T, kTileM) ||
+        !in_map(&mj.b[0], w_gate, F, H, 128) || !in_map(&mj.b[1], w_up, F, H, 128) ||
+        !make_out_tmap(&mj.out[kMain], dx, H, T, rH, false) ||
+        (add && !make_out_tmap(&mj.in[0], add, H, T, rH, false)) ||
+        !part_map(&mj.part, part, b.dx, b.s_dx))
       return MOE_ERR_CUDA;
-    Args ph = p, px = p;
-    ph.kb = ph.kb0 = up_div(H, BK);
-    px.kb0 = up_div(F, BK);
-    px.kb = 2 * px.kb0;
-    px.add = add != nullptr;
-    if (launch<Op::GatedBwd>(mh, ph, T, F, 1, st) != cudaSuccess ||
-        launch<Op::InGrad>(mx, px, T, H, 1, st) != cudaSuccess)
+    if (launch<Op::GatedBwd>(mh, ph, st) != cudaSuccess ||
+        finish<Op::GatedBwd>(ph, part, T, a_gate, a_up, h, da_g, da_u, st) != cudaSuccess)
       return MOE_ERR_CUDA;
   }
-  if (!dw_gate) return MOE_OK;
-  const uint64_t z = f32 ? 4 : 2;
-  if (!in_map(&m2.a[0], h, F, T, BK) || !in_map(&m2.b[0], dy, H, T, BK) ||
-      !make_out_tmap(&m2.out[0], dw_down, H, F, static_cast<uint64_t>(H) * z, f32) ||
-      !in_map(&m1.a[0], x, H, T, BK) || !in_map(&m1.b[0], da_g, F, T, BK) ||
-      !in_map(&m1.b[1], da_u, F, T, BK) ||
-      !make_out_tmap(&m1.out[0], dw_gate, F, H, static_cast<uint64_t>(F) * z, f32) ||
-      !make_out_tmap(&m1.out[1], dw_up, F, H, static_cast<uint64_t>(F) * z, f32))
+  if (dw_gate) {
+    const uint64_t z = f32 ? 4 : 2;
+    if (!in_map(&mj.a[2], h, F, T, BK) || !in_map(&mj.b[1 + kDwDown], dy, H, T, BK) ||
+        !make_out_tmap(&mj.out[kDwDown], dw_down, H, F, static_cast<uint64_t>(H) * z, f32) ||
+        !in_map(&mj.a[3], x, H, T, BK) || !in_map(&mj.b[1 + kDwGate], da_g, F, T, BK) ||
+        !in_map(&mj.b[1 + kDwUp], da_u, F, T, BK) ||
+        !make_out_tmap(&mj.out[kDwGate], dw_gate, F, H, static_cast<uint64_t>(F) * z, f32) ||
+        !make_out_tmap(&mj.out[kDwUp], dw_up, F, H, static_cast<uint64_t>(F) * z, f32))
+      return MOE_ERR_CUDA;
+    pj.down = b.down;
+    pj.gate = b.gate;
+    pj.dw_units = static_cast<int>(b.dw_units);
+    pj.kb_rows = b.kb_rows;
+    pj.f32 = f32;
+    pj.accumulate = accumulate_dw;
+    // as many rounds as the gradient tiles that take as long as a unit of dx
+    pj.skip = pj.units > 0 ? (pj.per + kTileCost) / (b.kb_rows + kTileCost) : 0;
+  }
+  if (launch<Op::Joint>(mj, pj, st) != cudaSuccess ||
+      finish<Op::Joint>(pj, part, T, add, nullptr, dx, nullptr, nullptr, st) != cudaSuccess)
     return MOE_ERR_CUDA;
-  Args pw = p;
-  pw.kb = pw.kb0 = up_div(T, BK);
-  pw.accumulate = accumulate_dw;
-  Args pw1 = pw;
-  const cudaError_t e2 = f32 ? launch<Op::WGradF32>(m2, pw, F, H, 1, st)
-                             : launch<Op::WGradB16>(m2, pw, F, H, 1, st);
-  if (e2 != cudaSuccess) return MOE_ERR_CUDA;
-  const cudaError_t e1 = f32 ? launch<Op::WGradF32>(m1, pw1, H, F, 2, st)
-                             : launch<Op::WGradB16>(m1, pw1, H, F, 2, st);
-  return e1 == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return MOE_OK;
 }
 
 }  // extern "C"

@@ -23,7 +23,9 @@ ACTS = ["silu", "gelu", "gelu_tanh", "relu"]
 # one tile, tails of every tile dimension, a K shorter than a block and not a multiple of it
 SHAPES = [(1, 8, 8), (1, 64, 64), (2, 2048, 768), (3, 72, 136), (16, 512, 1024), (17, 128, 64),
           (33, 1000, 328), (64, 264, 2056), (65, 64, 520), (127, 256, 384), (129, 136, 72),
-          (256, 128, 640), (257, 200, 1000), (300, 1000, 328), (513, 512, 1032)]
+          (256, 128, 640), (257, 200, 1000), (300, 1000, 328), (513, 512, 1032),
+          # few tiles of a long K: its parts in several clusters
+          (130, 4096, 136), (200, 1104, 2056), (513, 1032, 1544), (140, 72, 4104)]
 
 
 def _np(t):
@@ -120,7 +122,7 @@ def _gauss(T, H, F, seed):
 
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("T,H,F", [(1, 128, 256), (5, 72, 200), (40, 520, 392), (150, 256, 328),
-                                   (300, 200, 264)])
+                                   (300, 200, 264), (180, 1096, 1544)])
 def test_ffn_gaussian(T, H, F, act):
     v, add, dy = _gauss(T, H, F, T + H)
     n = {k: _np(t) for k, t in v.items()}
