@@ -57,11 +57,14 @@ constexpr unsigned long long kDrainNs = 1000000000ull;
 constexpr unsigned long long kPairDrainNs = 50000000ull;
 constexpr int kMaxSplit = 8;
 
-// pieces that a warp reads for 32 columns, and the ring depth that 227 KB leave
+// Pieces that a warp reads for 32 columns: one goes out again in its own place, two have
+// places beside those of the pieces that go out. The ring depth that 227 KB leave.
 template <Op op>
 constexpr int loads() { return op == Op::GatedBwd ? 2 : op == Op::Gated ? 0 : 1; }
 template <Op op>
-constexpr int stages() { return loads<op>() ? 5 : 6; }
+constexpr int in_slots() { return op == Op::GatedBwd ? 2 : 0; }
+template <Op op>
+constexpr int stages() { return op == Op::GatedBwd ? 5 : 6; }
 constexpr int kMaxStages = 6;
 
 struct Smem {
@@ -77,7 +80,7 @@ struct Smem {
 };
 
 template <Op op>
-constexpr int pieces_bytes() { return kEpiWarps * (kSlots + loads<op>()) * kPieceBytes; }
+constexpr int pieces_bytes() { return kEpiWarps * (kSlots + in_slots<op>()) * kPieceBytes; }
 template <Op op>
 constexpr size_t smem_bytes() {
   return 1024 + static_cast<size_t>(stages<op>()) * kStageBytes + pieces_bytes<op>() + sizeof(Smem);
@@ -375,8 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------------------------------------------------- epilogue
     const int e = warp - 2, q = warp & 3;      // q: TMEM lane quadrant of this warp
     const int c_first = (e >> 2) * 32;         // its first columns; the next are 64 on
-    const uint32_t out0 = smem_u32(pieces) + e * (kSlots + kLoads) * kPieceBytes;
-    const uint32_t in0 = out0 + kSlots * kPieceBytes;
+    const uint32_t out0 = smem_u32(pieces) + e * (kSlots + in_slots<op>()) * kPieceBytes;
     const uint32_t in_bar = smem_u32(&sm->in[e]);
     const uint32_t my_row = lane * 64, sw = (lane >> 1) & 3;
     int npiece = 0;
@@ -415,12 +417,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                      : "r"(slot + my_row + ((j ^ sw) << 4))
                      : "memory");
     };
-    auto ask = [&](int x, int y) {             // the pieces of 32 columns
+    // the pieces of 32 columns: two into places of their own, one into the place from
+    // which piece k will go out, once the one before it there has been read
+    auto in_place = [&](int k) {
+      return out0 + (kLoads == 2 ? kSlots : k % kSlots) * kPieceBytes;
+    };
+    auto ask = [&](int x, int y, int k) {
       if (lane == 0) {
+        if (kLoads == 1) bulk_wait_group_read<0>();
         mbar_arrive_expect_tx(in_bar, kLoads * kPieceBytes);
 #pragma unroll
         for (int i = 0; i < kLoads; ++i)
-          tma_load_2d(in0 + i * kPieceBytes, &maps.in[i], in_bar, x, y);
+          tma_load_2d(in_place(k) + i * kPieceBytes, &maps.in[i], in_bar, x, y);
       }
       ++n_asked;
     };
@@ -440,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int width = op == Op::Gated && !part ? BN / 2 : BN;
       const int n0 = u.n * width;
       const int cols = y >= g.M ? 0 : part ? BN : min(width, g.N - n0);   // 0: nothing to finish
-      if (reads && c_first < cols) ask(n0 + c_first, y);
+      if (reads && c_first < cols) ask(n0 + c_first, y, npiece);
       const bool got = mbar_wait(smem_u32(&sm->tfull[acc]), acc_phase, p.wait_ns, abort_flag);
       // tcgen05.ld is warp-collective: the whole warp goes on or stops together
       if (!__all_sync(0xffffffffu, got)) {
@@ -462,10 +470,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           ++n_got;
-          get(in0, a);
-          if (kLoads == 2) get(in0 + kPieceBytes, b);
-          __syncwarp();                        // read before they are asked for again
-          if (c + 64 < cols) ask(n0 + c + 64, y);
+          get(in_place(npiece), a);
+          if (kLoads == 2) get(in_place(npiece) + kPieceBytes, b);
+          __syncwarp();                        // read before the place is filled again
+          if (c + 64 < cols) ask(n0 + c + 64, y, npiece + 1);
         }
         tmem_ld_32x32b_x32(taddr + c, v);
         if (part) {
