@@ -763,6 +763,10 @@ _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+# the current device: what has a CUDA tensor in hand needs no look at the initialisation
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _fit(dev, *named):
     """Checks (tensor or None, name, dtype, least number of elements) on dev:
     these calls are short, so one pass looks at everything and the messages
@@ -778,7 +782,7 @@ def _fit(dev, *named):
 
 def _on(dev, fn, *args):
     """fn(*args) with dev current."""
-    if dev.index == torch.cuda.current_device():
+    if dev.index == _current_device():
         return fn(*args)
     with torch.cuda.device(dev):
         return fn(*args)
@@ -1100,6 +1104,7 @@ def moe_grad_norm(grads, norm_type=2.0, norm_coef=None, workspace=None, stream=N
                               workspace=workspace, stream=stream)[0]
 
 
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 _ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}
 
 
@@ -1115,12 +1120,13 @@ def _all_fit(dev, *named):
     only where something is wrong."""
     index = dev.index
     for t, name, shape, dtype in named:
-        if t is not None and (t.shape != shape or t.dtype is not dtype or t.get_device() != index
-                              or not t.is_contiguous()):
-            _cuda(t, name, dtype)
-            _shaped(t, name, *shape)
-            raise ValueError(f"{name} is on {t.device} but the call's first tensor on {dev}: "
-                             "all tensors of a call must share one device")
+        if t is None or (t.dtype is dtype and t.shape == shape and t.is_contiguous()
+                         and t.get_device() == index):
+            continue
+        _cuda(t, name, dtype)
+        _shaped(t, name, *shape)
+        raise ValueError(f"{name} is on {t.device} but the call's first tensor on {dev}: "
+                         "all tensors of a call must share one device")
 
 
 def _made(t, shape, dtype, dev):
@@ -1153,25 +1159,31 @@ def moe_gated_ffn(x, w_gate, w_up, w_down, act="silu", add=None, save_for_backwa
     multiples of 8, tensors start on 16 bytes."""
     if stream is not None and _elsewhere(stream):
         return _within(stream, moe_gated_ffn, locals())
-    bf16, dev = torch.bfloat16, x.device
+    bf16, dev = _BF16, x.device
     T, H = rows = _matrix(x, "x")
-    wide = _matrix(w_gate, "w_gate")
-    F = wide[1]
+    F = _matrix(w_gate, "w_gate")[1]
     if y is None:
         y = torch.empty(rows, dtype=bf16, device=dev)
     if save_for_backward:
         a_gate, a_up = _made(a_gate, (T, F), bf16, dev), _made(a_up, (T, F), bf16, dev)
+        _all_fit(dev, (a_gate, "a_gate", (T, F), bf16), (a_up, "a_up", (T, F), bf16))
     else:
         a_gate = a_up = None
     _all_fit(dev, (x, "x", rows, bf16), (w_gate, "w_gate", (H, F), bf16),
-             (w_up, "w_up", wide, bf16), (w_down, "w_down", (F, H), bf16),
-             (add, "add", rows, bf16), (y, "y", rows, bf16), (a_gate, "a_gate", (T, F), bf16),
-             (a_up, "a_up", (T, F), bf16))
-    ws, ws_bytes = _space(workspace, _lib.moe_gated_ffn_workspace_size, dev, T, H, F)
+             (w_up, "w_up", (H, F), bf16), (w_down, "w_down", (F, H), bf16), (y, "y", rows, bf16))
+    if add is not None:
+        _all_fit(dev, (add, "add", rows, bf16))
+    code = _act(act)
+    if workspace is None:
+        ws_bytes = _on(dev, _lib.moe_gated_ffn_workspace_size, T, H, F)
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+    else:
+        _, ws_bytes = _scratch(workspace, 0, dev)
     _check(_on(dev, _lib.moe_gated_ffn, x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(),
-               w_down.data_ptr(), _ptr(add), T, H, F, _act(act), y.data_ptr(), _ptr(a_gate),
-               _ptr(a_up), _ptr(ws), ws_bytes, _raw_stream(stream, dev)), "moe_gated_ffn")
-    return dict(y=y, a_gate=a_gate, a_up=a_up)
+               w_down.data_ptr(), _ptr(add), T, H, F, code, y.data_ptr(), _ptr(a_gate),
+               _ptr(a_up), workspace.data_ptr(), ws_bytes, _raw_stream(stream, dev)),
+           "moe_gated_ffn")
+    return {"y": y, "a_gate": a_gate, "a_up": a_up}
 
 
 def moe_gated_ffn_backward(dy, x, w_gate, w_up, w_down, a_gate, a_up, act="silu", add=None,
@@ -1238,21 +1250,14 @@ def moe_lora_plan(adapter_ids, n, order=None, offsets=None, stream=None):
     return order, offsets
 
 
-def _lora_operands(dev, T, a, b, adapter_ids, plan, scales):
-    """(n, r, H, N, order, offsets) of a [n, r, H] and b [n, r, N]."""
-    if a.dim() != 3 or b.dim() != 3:
+def _lora_shapes(x, a, b):
+    """(T, H, N, n, r) of x [T, H], a [n, r, H] and b [n, r, N]."""
+    T, H = _matrix(x, "x")
+    if a.dim() != 3 or b.dim() != 3 or a.shape[:2] != b.shape[:2]:
         raise ValueError("a and b must have shapes [n, r, H] and [n, r, N], got "
                          f"{list(a.shape)} and {list(b.shape)}")
-    n, r, H = a.shape
-    N, bf16, i32 = b.shape[2], torch.bfloat16, torch.int32
-    if b.shape != (n, r, N):
-        raise ValueError("a and b must have shapes [n, r, H] and [n, r, N], got "
-                         f"{list(a.shape)} and {list(b.shape)}")
-    _all_fit(dev, (a, "a", (n, r, H), bf16), (b, "b", (n, r, N), bf16),
-             (adapter_ids, "adapter_ids", (T,), i32), (scales, "scales", (n,), torch.float32))
-    order, offsets = moe_lora_plan(adapter_ids, n) if plan is None else plan
-    _all_fit(dev, (order, "order", (T,), i32), (offsets, "offsets", (n + 1,), i32))
-    return n, r, H, N, order, offsets
+    n, r, N = b.shape
+    return T, H, N, n, r
 
 
 def moe_lora(x, a, b, adapter_ids, plan=None, scales=None, base=None, out=None, v=None,
@@ -1267,23 +1272,23 @@ def moe_lora(x, a, b, adapter_ids, plan=None, scales=None, base=None, out=None, 
     128, H and N are multiples of 8, tensors start on 16 bytes."""
     if stream is not None and _elsewhere(stream):
         return _within(stream, moe_lora, locals())
-    bf16, f32, dev = torch.bfloat16, torch.float32, x.device
-    T, H = rows = _matrix(x, "x")
-    n, r, ha, N, order, offsets = _lora_operands(dev, T, a, b, adapter_ids, plan, scales)
-    if ha != H:
-        raise ValueError(f"a must have shape [n, r, {H}], got {list(a.shape)}")
+    bf16, f32, i32, dev = _BF16, _F32, _I32, x.device
+    T, H, N, n, r = _lora_shapes(x, a, b)
     if out is None:
         out = torch.empty((T, N), dtype=bf16, device=dev)
     if v is None:
         v = torch.empty((T, r), dtype=f32, device=dev)
-    _all_fit(dev, (x, "x", rows, bf16), (base, "base", (T, N), bf16), (out, "out", (T, N), bf16),
-             (v, "v", (T, r), f32))
+    _all_fit(dev, (x, "x", (T, H), bf16), (a, "a", (n, r, H), bf16), (b, "b", (n, r, N), bf16),
+             (adapter_ids, "adapter_ids", (T,), i32), (scales, "scales", (n,), f32),
+             (base, "base", (T, N), bf16), (out, "out", (T, N), bf16), (v, "v", (T, r), f32))
+    order, offsets = moe_lora_plan(adapter_ids, n) if plan is None else plan
+    _all_fit(dev, (order, "order", (T,), i32), (offsets, "offsets", (n + 1,), i32))
     ws, ws_bytes = _space(workspace, _lib.moe_lora_workspace_size, dev, T, n, r)
     _check(_on(dev, _lib.moe_lora, x.data_ptr(), a.data_ptr(), b.data_ptr(),
                adapter_ids.data_ptr(), order.data_ptr(), offsets.data_ptr(), _ptr(scales),
                _ptr(base), T, H, N, n, r, out.data_ptr(), v.data_ptr(), _ptr(ws), ws_bytes,
                _raw_stream(stream, dev)), "moe_lora")
-    return dict(out=out, v=v)
+    return {"out": out, "v": v}
 
 
 def moe_lora_backward(dy, x, v, a, b, adapter_ids, plan=None, scales=None, base=None, dx=None,
@@ -1296,17 +1301,17 @@ def moe_lora_backward(dy, x, v, a, b, adapter_ids, plan=None, scales=None, base=
     if stream is not None and _elsewhere(stream):
         return _within(stream, moe_lora_backward, locals())
     bf16, f32, dev = torch.bfloat16, torch.float32, x.device
-    T, H = rows = _matrix(x, "x")
-    n, r, ha, N, order, offsets = _lora_operands(dev, T, a, b, adapter_ids, plan, scales)
-    if ha != H:
-        raise ValueError(f"a must have shape [n, r, {H}], got {list(a.shape)}")
+    T, H, N, n, r = _lora_shapes(x, a, b)
     if accumulate and (da is None or db is None):
         raise ValueError("accumulate adds to da and db: pass them")
     dx = _made(dx, (T, H), bf16, dev)
     da, db = _made(da, (n, r, H), f32, dev), _made(db, (n, r, N), f32, dev)
-    _all_fit(dev, (x, "x", rows, bf16), (dy, "dy", (T, N), bf16), (v, "v", (T, r), f32),
-             (base, "base", rows, bf16), (dx, "dx", rows, bf16), (da, "da", (n, r, H), f32),
-             (db, "db", (n, r, N), f32))
+    _all_fit(dev, (x, "x", (T, H), bf16), (a, "a", (n, r, H), bf16), (b, "b", (n, r, N), bf16),
+             (adapter_ids, "adapter_ids", (T,), _I32), (scales, "scales", (n,), f32),
+             (dy, "dy", (T, N), bf16), (v, "v", (T, r), f32), (base, "base", (T, H), bf16),
+             (dx, "dx", (T, H), bf16), (da, "da", (n, r, H), f32), (db, "db", (n, r, N), f32))
+    order, offsets = moe_lora_plan(adapter_ids, n) if plan is None else plan
+    _all_fit(dev, (order, "order", (T,), _I32), (offsets, "offsets", (n + 1,), _I32))
     ws, ws_bytes = _space(workspace, _lib.moe_lora_backward_workspace_size, dev, T, n, r)
     _check(_on(dev, _lib.moe_lora_backward, dy.data_ptr(), x.data_ptr(), v.data_ptr(),
                a.data_ptr(), b.data_ptr(), order.data_ptr(), offsets.data_ptr(), _ptr(scales),
