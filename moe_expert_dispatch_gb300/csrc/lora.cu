@@ -298,7 +298,6 @@ __global__ void __launch_bounds__(Shrink<R>::kThreads, R > 64 ? 1 : 2)
   const Unit u = find_unit(p.plan, unit);
   // on its way while the barriers are made
   const int raw = tid < u.rows ? __ldg(p.plan.order + u.lo + tid) : 0;
-  grid_dependents_launch();
   if (u.rows == 0 || u.a == p.plan.n) {         // the whole cluster leaves together
     if (tid < kRows) rows[tid] = tid < u.rows ? checked_row(p.plan, raw) : -1;
     __syncthreads();
@@ -552,10 +551,7 @@ __global__ void __launch_bounds__(kExpandThreads, R > 64 ? 1 : 2)
   const int unit = static_cast<int>(blockIdx.x);
   const Unit u = find_unit(p.plan, unit);
   const bool none = u.a == p.plan.n;
-  if (u.rows == 0 || (none && p.base == p.out)) {  // nothing, or base stays as it is
-    grid_dependency_wait();
-    return;
-  }
+  if (u.rows == 0 || (none && p.base == p.out)) return;   // nothing, or base stays as it is
   if (tid < kRows) rows[tid] = tid < u.rows ? checked_row(p.plan, __ldg(p.plan.order + u.lo + tid)) : -1;
   if (none) {                                    // base as it is, or zeros
     __syncthreads();
@@ -567,7 +563,6 @@ __global__ void __launch_bounds__(kExpandThreads, R > 64 ? 1 : 2)
         reinterpret_cast<uint4*>(p.out + at)[c] =
             p.base ? reinterpret_cast<const uint4*>(p.base + at)[c] : make_uint4(0, 0, 0, 0);
     }
-    grid_dependency_wait();
     return;
   }
   const int tiles = (p.N + kCols - 1) / kCols;
@@ -600,7 +595,6 @@ __global__ void __launch_bounds__(kExpandThreads, R > 64 ? 1 : 2)
 
   if (warp == 0) {
     if (lane == 0) {
-      if (steps == 0) grid_dependency_wait();
       int i = 0;
       for (; i < steps; ++i) {
         const int s = i % S::kStages;
@@ -608,9 +602,7 @@ __global__ void __launch_bounds__(kExpandThreads, R > 64 ? 1 : 2)
         if (!ok) break;
         mbar_arrive_expect_tx(smem_u32(&full[s]), S::kQ);
         tma_load_3d(q0 + s * S::kQ, &map_q, smem_u32(&full[s]), (t0 + i * dt) * kCols, 0, u.a);
-        if (i == 0) {                            // Q is there before the image is written
-          grid_dependency_wait();
-          fence_proxy_async();
+        if (i == 0) {
           mbar_arrive_expect_tx(smem_u32(&image), S::kImg);
           const uint8_t* src = p.img + static_cast<int64_t>(unit) * atoms(p.parts, R) * kAtom;
           for (int k = 0; k < S::kImg / kAtom; ++k)
@@ -1363,7 +1355,7 @@ cudaError_t expand(const __nv_bfloat16* Q, int r, ExpandArgs p, cudaStream_t st)
   while (tiles / (split + 1) >= 4 && units * (split + 1) <= 2 * device_sm_count()) ++split;
   p.wait_ns = kDefaultWaitNs;
   return launch(expand_kernel<R>, dim3(static_cast<unsigned>(units), split), kExpandThreads,
-                Expand<R>::kBytes, 1, true, configured, st, map, p);
+                Expand<R>::kBytes, 1, false, configured, st, map, p);
 }
 
 template <int R>
