@@ -95,10 +95,22 @@ struct Maps {
   CUtensorMap out[4], in[2], part;
 };
 
+// n / d for n below 2^31 by a product and a shift (Granlund and Montgomery: "Division by
+// invariant integers using multiplication", 1994): a tile's place takes four divisions,
+// which the hardware has to go through step by step.
+struct Divisor {
+  uint32_t d, m, l;
+};
+
+__device__ __forceinline__ int quotient(int n, const Divisor& v) {
+  return static_cast<int>((__umulhi(static_cast<uint32_t>(n), v.m) + static_cast<uint32_t>(n)) >> v.l);
+}
+
 struct Grid {
   int M, N;          // rows and columns of the result
   int mt, nt;        // tiles
   int group;         // row tiles that one column tile is walked over
+  Divisor per, whole, last;    // tiles of a group; row tiles of a whole one, of the last
 };
 
 struct Args {
@@ -107,6 +119,8 @@ struct Args {
   int kb_rows;                 // weight gradients: k-blocks (of rows)
   int split, per;              // Main: parts of K, k-blocks of a part
   int units;                   // of Main: tiles times parts
+  Divisor tiles;               // of Main
+  int rounds, rest;            // units = rounds * clusters + rest
   int dw_units;                // tiles of the weight gradients
   int skip;                    // their rounds that clusters with a unit of Main stay out of
   int act;
@@ -118,20 +132,19 @@ struct Args {
 };
 
 struct Unit {
-  int kind, m, n, part, kb0, kb1;
+  int kind, m, n, part, kb0, kb1;              // tiles below 2^26, parts up to kMaxSplit
 };
 
 // Column tiles follow one another over groups of row tiles: a group's rows of A
 // stay in L2 while the columns of B stream by once a group.
 __device__ __forceinline__ void place(int t, const Grid& g, Unit& u) {
-  const int per = g.group * g.nt;
-  const int i = t / per, local = t - i * per;
-  const int rows = min(g.group, g.mt - i * g.group);
-  u.n = local / rows;
-  u.m = i * g.group + local - u.n * rows;
+  const int i = quotient(t, g.per), local = t - i * static_cast<int>(g.per.d);
+  const Divisor& rows = (i + 1) * g.group <= g.mt ? g.whole : g.last;
+  u.n = quotient(local, rows);
+  u.m = i * g.group + local - u.n * static_cast<int>(rows.d);
 }
 
-// The i-th unit of a cluster. Units of Main go round the clusters. Weight gradients
+// The i-th unit of a cluster (its tile and part). Units of Main go round the clusters. Weight gradients
 // follow: where Main has fewer units than there are clusters, those with one join in
 // when the others have done as much.
 template <Op op>
@@ -139,27 +152,22 @@ __device__ __forceinline__ Unit unit_at(int i, const Args& p, int cluster, int c
   Unit u = {kNone, 0, 0, 0, 0, 0};
   int t = cluster + i * clusters;
   if (t < p.units) {
-    const int tiles = p.main.mt * p.main.nt;
     u.kind = kMain;
-    u.part = t / tiles;
-    place(t - u.part * tiles, p.main, u);
-    u.kb0 = min(p.kb, u.part * p.per);
-    u.kb1 = min(p.kb, u.kb0 + p.per);
+    u.part = quotient(t, p.tiles);
+    place(t - u.part * static_cast<int>(p.tiles.d), p.main, u);
     return u;
   }
   if (op != Op::Joint) return u;
-  const int mine = p.units / clusters + (cluster < p.units % clusters ? 1 : 0);
-  const int r = i - mine;
+  const int r = i - p.rounds - (cluster < p.rest ? 1 : 0);
   if (p.units < clusters) {
     const int rest = clusters - p.units;
     if (cluster >= p.units && r < p.skip) t = r * rest + cluster - p.units;
     else t = p.skip * rest + (cluster >= p.units ? r - p.skip : r) * clusters + cluster;
   } else {
-    t = r * clusters + (cluster + clusters - p.units % clusters) % clusters;
+    t = r * clusters + cluster - p.rest + (cluster < p.rest ? clusters : 0);
   }
   if (t >= p.dw_units) return u;
   const int down = p.down.mt * p.down.nt, gate = p.gate.mt * p.gate.nt;
-  u.kb1 = p.kb_rows;
   if (t < down) {
     u.kind = kDwDown;
     place(t, p.down, u);
@@ -169,6 +177,33 @@ __device__ __forceinline__ Unit unit_at(int i, const Args& p, int cluster, int c
   }
   return u;
 }
+
+// The units of a cluster in turn, for a whole warp: 32 of them are worked out at once,
+// one a lane, and dealt out by shuffles: worked out one by one they took half the time
+// of a weight gradient over few rows.
+template <Op op>
+struct Units {
+  const Args& p;
+  int cluster, clusters;
+  uint32_t where, what;        // row tile and kind + 1; column tile and part
+  __device__ __forceinline__ Unit get(int i) {
+    if ((i & 31) == 0) {
+      const Unit u = unit_at<op>(i + lane_id(), p, cluster, clusters);
+      where = static_cast<uint32_t>(u.m) | static_cast<uint32_t>(u.kind + 1) << 28;
+      what = static_cast<uint32_t>(u.n) | static_cast<uint32_t>(u.part) << 28;
+    }
+    const uint32_t a = __shfl_sync(0xffffffffu, where, i & 31);
+    const uint32_t b = __shfl_sync(0xffffffffu, what, i & 31);
+    Unit u;
+    u.kind = static_cast<int>(a >> 28) - 1;
+    u.m = static_cast<int>(a & 0xFFFFFFFu);
+    u.n = static_cast<int>(b & 0xFFFFFFFu);
+    u.part = static_cast<int>(b >> 28);
+    u.kb0 = u.kind == kMain ? min(p.kb, u.part * p.per) : 0;
+    u.kb1 = u.kind == kMain ? min(p.kb, u.kb0 + p.per) : p.kb_rows;
+    return u;
+  }
+};
 
 // 32 accumulator columns of A_g and A_u -> 16 words of h.
 template <int kAct>
@@ -254,19 +289,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = &sm->abort;
   grid_dependency_wait();    // Joint and Down run beside the launch before them
   grid_dependents_launch();
+  Units<op> units = {p, cluster, clusters, 0, 0};
 
   if (warp == 0) {
     // ---------------------------------------------------------- producer
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0, fills = 0;
-      bool ok = true;
-      const uint64_t pol = l2_policy_evict_normal();
-      const uint32_t ring0 = smem_u32(ring);
-      fence_proxy_async();
-      for (int i = 0; ok; ++i) {
-        const Unit u = unit_at<op>(i, p, cluster, clusters);
-        if (u.kind == kNone) break;
+    int stage = 0;
+    uint32_t phase = 0, fills = 0;
+    bool ok = true;
+    const uint64_t pol = l2_policy_evict_normal();
+    const uint32_t ring0 = smem_u32(ring);
+    if (lane == 0) fence_proxy_async();
+    for (int i = 0; __shfl_sync(0xffffffffu, ok, 0); ++i) {
+      const Unit u = units.get(i);
+      if (u.kind == kNone) break;
+      if (lane == 0) {
         const bool wgrad = op == Op::Joint && u.kind != kMain;
         const int m0 = (2 * u.m + static_cast<int>(rank)) * kTileM;
         const int n0 = op == Op::Gated ? u.n * (BN / 2)
@@ -307,6 +343,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
+    }
+    if (lane == 0) {
       if (!ok) {
         sm->abort = 1;
         report_error(p.err, kErrTimeout);
@@ -320,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       constexpr bool kBmnMain = op == Op::Gated || op == Op::Down;
       // K-major, 128-byte swizzle: groups of 8 rows 1 KB apart, 32 bytes a step of K = 16.
       // MN-major: atoms of 64 columns 8 KB apart, groups of 8 of K 1 KB apart, 2 KB a step
@@ -328,9 +366,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true, issued = false;
-      for (int i = 0; ok; ++i) {
-        const Unit u = unit_at<op>(i, p, cluster, clusters);
+      for (int i = 0; __shfl_sync(0xffffffffu, ok, 0); ++i) {
+        const Unit u = units.get(i);
         if (u.kind == kNone) break;
+        if (lane != 0) continue;
         const bool wgrad = op == Op::Joint && u.kind != kMain, bmn = kBmnMain || wgrad;
         const uint32_t idesc = idesc_bf16(2 * kTileM, BN, wgrad, bmn);
         const uint64_t ad0 = sdesc_sw128(ring0, wgrad ? kBox : 16, 1024);
@@ -338,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t a_step = wgrad ? 2048 >> 4 : 32 >> 4, b_step = bmn ? 2048 >> 4 : 32 >> 4;
         if (!mbar_wait(smem_u32(&sm->tempty[acc]), acc_phase ^ 1, p.wait_ns, abort_flag)) {
           ok = false;
-          break;
+          continue;
         }
         tc_fence_after();
         const uint32_t d = tmem_base + acc * BN;
@@ -360,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             phase ^= 1;
           }
         }
-        if (!ok) break;
+        if (!ok) continue;
         umma_commit_pair_mc(smem_u32(&sm->tfull[acc]), 0x3);       // both CTAs' epilogues
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1;
@@ -369,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         sm->abort = 1;
         report_error(p.err, kErrTimeout);
       }
-      if (issued) {
+      if (issued) {                            // of lane 0 alone
         umma_commit_pair_mc(smem_u32(&sm->drain), 0x1);
         mbar_wait(smem_u32(&sm->drain), 0, kDrainNs, &sm->zero);
       }
@@ -438,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tempty0 = mapa_shared(smem_u32(&sm->tempty[0]), 0);
     bool ok = true;
     for (int i = 0; ok; ++i) {
-      const Unit u = unit_at<op>(i, p, cluster, clusters);
+      const Unit u = units.get(i);
       if (u.kind == kNone) break;
       const bool main = op != Op::Joint || u.kind == kMain;
       const Grid& g = main ? p.main : u.kind == kDwDown ? p.down : p.gate;
@@ -638,6 +677,13 @@ __global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ Fin
 
 int up_div(int64_t a, int b) { return static_cast<int>((a + b - 1) / b); }
 
+Divisor divisor(int64_t d) {
+  Divisor v = {static_cast<uint32_t>(d), 0, 0};
+  while ((1ull << v.l) < v.d) ++v.l;
+  v.m = static_cast<uint32_t>(((1ull << 32) * ((1ull << v.l) - v.d)) / (v.d ? v.d : 1) + 1);
+  return v;
+}
+
 Grid make_grid(int64_t M, int N, int cols) {
   Grid g;
   g.M = static_cast<int>(M);
@@ -645,6 +691,9 @@ Grid make_grid(int64_t M, int N, int cols) {
   g.mt = up_div(M, 2 * kTileM);
   g.nt = up_div(N, cols);
   g.group = g.mt < 16 ? g.mt : 16;
+  g.per = divisor(static_cast<int64_t>(g.group) * g.nt);
+  g.whole = divisor(g.group);
+  g.last = divisor(g.group > 0 ? (g.mt - 1) % g.group + 1 : 0);
   return g;
 }
 
@@ -678,6 +727,7 @@ void set_main(Args& p, const Grid& g, int kb0, int kb, int split) {
   p.split = split;
   p.per = up_div(kb, split);
   p.units = g.mt * g.nt * split;
+  p.tiles = divisor(static_cast<int64_t>(g.mt) * g.nt);
 }
 
 size_t part_bytes(const Grid& g, int split) {
@@ -713,7 +763,7 @@ cudaError_t launch_beside(K kern, dim3 grid, int threads, size_t smem, int clust
 }
 
 template <Op op>
-cudaError_t launch(const Maps& maps, const Args& p, cudaStream_t st) {
+cudaError_t launch(const Maps& maps, Args p, cudaStream_t st) {
   auto kern = dense_gemm_kernel<op>;
   static bool configured[kMaxDevices] = {};
   static int max_pairs[kMaxDevices] = {};       // clusters of two that fit at once
@@ -742,6 +792,8 @@ cudaError_t launch(const Maps& maps, const Args& p, cudaStream_t st) {
   const int64_t units = static_cast<int64_t>(p.units) + p.dw_units;
   const int n = static_cast<int>(units < max_pairs[d] ? units : max_pairs[d]);
   if (n == 0) return cudaSuccess;
+  p.rounds = p.units / n;
+  p.rest = p.units % n;
   return launch_beside(kern, dim3(2 * n), kThreads, smem_bytes<op>(), 2, st, maps, p);
 }
 

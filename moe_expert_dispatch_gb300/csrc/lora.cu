@@ -659,32 +659,36 @@ __global__ void __launch_bounds__(kExpandThreads, R > 64 ? 1 : 2)
     load(half);
     for (int i = half; i < steps; i += 2) {
       const int a = i % kExpandAcc;
+      if (any) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int row = r0 + 4 * j;
-        *reinterpret_cast<uint4*>(st + row * 128 + ((ch ^ (row & 7)) << 4)) = next[j];
+        for (int j = 0; j < 8; ++j) {
+          const int row = r0 + 4 * j;
+          *reinterpret_cast<uint4*>(st + row * 128 + ((ch ^ (row & 7)) << 4)) = next[j];
+        }
+        __syncwarp();
+        load(i + 2);
       }
-      __syncwarp();
-      load(i + 2);
       const bool got = mbar_wait(smem_u32(&tfull[a]), (i / kExpandAcc) & 1, p.wait_ns, stopped);
       ok = __all_sync(0xffffffffu, got);
       if (!ok) break;
       tc_fence_after();
       const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + a * kCols;
+      if (any) {                                 // else no row of the quarter is there
 #pragma unroll
-      for (int c0 = 0; c0 < 8; c0 += 2) {
-        uint32_t v[16];
-        tmem_ld_32x32b_x16(taddr + c0 * 8, v);
-        tmem_ld_wait();
+        for (int c0 = 0; c0 < 8; c0 += 2) {
+          uint32_t v[16];
+          tmem_ld_32x32b_x16(taddr + c0 * 8, v);
+          tmem_ld_wait();
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint4* w = reinterpret_cast<uint4*>(st + lane * 128 + (((c0 + c) ^ (lane & 7)) << 4));
-          const uint4 o = *w;
-          const float* x = reinterpret_cast<const float*>(v + c * 8);
-          *w = make_uint4(pack_bf16x2(x[0] + lo_f(o.x), x[1] + hi_f(o.x)),
-                          pack_bf16x2(x[2] + lo_f(o.y), x[3] + hi_f(o.y)),
-                          pack_bf16x2(x[4] + lo_f(o.z), x[5] + hi_f(o.z)),
-                          pack_bf16x2(x[6] + lo_f(o.w), x[7] + hi_f(o.w)));
+          for (int c = 0; c < 2; ++c) {
+            uint4* w = reinterpret_cast<uint4*>(st + lane * 128 + (((c0 + c) ^ (lane & 7)) << 4));
+            const uint4 o = *w;
+            const float* x = reinterpret_cast<const float*>(v + c * 8);
+            *w = make_uint4(pack_bf16x2(x[0] + lo_f(o.x), x[1] + hi_f(o.x)),
+                            pack_bf16x2(x[2] + lo_f(o.y), x[3] + hi_f(o.y)),
+                            pack_bf16x2(x[4] + lo_f(o.z), x[5] + hi_f(o.z)),
+                            pack_bf16x2(x[6] + lo_f(o.w), x[7] + hi_f(o.w)));
+          }
         }
       }
       tc_fence_before();
@@ -1392,7 +1396,7 @@ moe_status check_sizes(int64_t T, int H, int N, int n, int r) {
 
 // The rows that one cluster each takes without a plan: every row reads its adapter
 // whole, which the rows of a unit share otherwise.
-bool few_rows(int64_t T, int r) { return T <= 128 && T * r <= 4096; }
+bool few_rows(int64_t T, int r) { return T <= 256 && T * r <= 8192; }
 
 // What the backward has in its workspace.
 struct BwdLayout {
