@@ -756,7 +756,7 @@ typedef enum moe_act {
  * Any T >= 0 below 2^31 - 1024; H % 8 == 0 and F % 8 == 0, each at most 2^30
  * (else MOE_ERR_UNSUPPORTED). Every pointer starts on 16 bytes; y, a_gate, a_up
  * and the workspace overlap nothing else of the call (y: add alone, and then
- * as a whole). T = 0 does nothing. A wait inside the kernels that
+ * as a whole, add being no other argument). T = 0 does nothing. A wait inside the kernels that
  * hits its limit (2 s) reports MOE_ERR_TIMEOUT, here and in the backward; the
  * call's outputs are then no results.
  * ------------------------------------------------------------------------ */
@@ -780,7 +780,8 @@ moe_status moe_gated_ffn(const void* x, const void* w_gate, const void* w_up, co
  *          three or, for frozen weights, none; in float they are added to
  *          what is there when accumulate_dw
  *  workspace >= moe_gated_ffn_backward_workspace_size(T, H, F) bytes
- * Sizes and overlaps as moe_gated_ffn; accumulate_dw with bf16 gradients is
+ * Sizes and overlaps as moe_gated_ffn (dx is neither dy nor x: MOE_ERR_INVALID_ARG);
+ * accumulate_dw with bf16 gradients is
  * MOE_ERR_UNSUPPORTED. T = 0 writes zero weight gradients (or leaves them when
  * accumulating).
  * ------------------------------------------------------------------------ */
@@ -828,8 +829,10 @@ moe_status moe_lora_plan(const int32_t* adapter_ids, int64_t T, int n, int32_t* 
  *  workspace >= moe_lora_workspace_size(T, n, r) bytes, 16-byte aligned; 0 bytes,
  *          and NULL allowed, for the few rows that need none
  * 1 <= r <= 128, H % 8 == 0 and N % 8 == 0 (else MOE_ERR_UNSUPPORTED), 1 <= n <=
- * 1024, T < 2^31 - 1024. Pointers start on 16 bytes; out and v overlap nothing
- * else of the call (out: base alone, and then as a whole). T = 0 does nothing.
+ * 1024, T < 2^31 - 1024. Pointers start on 16 bytes (v and the int32 arrays on
+ * 4); out and v overlap nothing else of the call (out: base alone, and then as a
+ * whole, base being no other argument). The plan is that of adapter_ids. T = 0 does
+ * nothing. Waits as moe_gated_ffn's.
  * ------------------------------------------------------------------------ */
 size_t moe_lora_workspace_size(int64_t T, int n, int r);
 moe_status moe_lora(const void* x, const void* a, const void* b, const int32_t* adapter_ids,
@@ -851,7 +854,8 @@ moe_status moe_lora(const void* x, const void* a, const void* b, const int32_t* 
  *  da      float [n, r, H], db  float [n, r, N]   out; added to what is there
  *          when accumulate. An adapter without rows gets 0 (or is left)
  *  workspace >= moe_lora_backward_workspace_size(T, n, r) bytes, 16-byte aligned
- * Limits as moe_lora. T = 0 writes zero gradients (or leaves them).
+ * Limits and overlaps as moe_lora (dx is neither dy nor x: MOE_ERR_INVALID_ARG).
+ * T = 0 writes zero gradients (or leaves them).
  * ------------------------------------------------------------------------ */
 size_t moe_lora_backward_workspace_size(int64_t T, int n, int r);
 moe_status moe_lora_backward(const void* dy, const void* x, const float* v, const void* a,

@@ -977,7 +977,7 @@ moe_status moe_gated_ffn_backward(const void* dy, const void* x, const void* w_g
                ? MOE_OK
                : MOE_ERR_CUDA;
   }
-  if (!dy || !x || !w_gate || !w_up || !w_down || !a_gate || !a_up || !dx)
+  if (!dy || !x || !w_gate || !w_up || !w_down || !a_gate || !a_up || !dx || dx == dy || dx == x)
     return MOE_ERR_INVALID_ARG;
   if (!aligned16(dy) || !aligned16(x) || !aligned16(w_gate) || !aligned16(w_up) ||
       !aligned16(w_down) || !aligned16(a_gate) || !aligned16(a_up) || !aligned16(add) ||

@@ -490,9 +490,12 @@ __global__ void __launch_bounds__(Shrink<R>::kThreads, R > 64 ? 1 : 2)
       }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      if (g < 0 || c * 8 + j >= p.r) v[j] = 0.0f;
-      else if (p.V) p.V[static_cast<int64_t>(g) * p.r + c * 8 + j] = v[j];
-      v[j] *= f;
+      if (g < 0 || c * 8 + j >= p.r) {
+        v[j] = 0.0f;                             // whatever the scale is
+      } else {
+        if (p.V) p.V[static_cast<int64_t>(g) * p.r + c * 8 + j] = v[j];
+        v[j] *= f;
+      }
     }
     put_parts<R>(p.img, unit, row, c, p.parts, v);
   }
@@ -1522,7 +1525,8 @@ moe_status moe_lora_backward(const void* dy, const void* x, const float* v, cons
                ? MOE_OK
                : MOE_ERR_CUDA;
   }
-  if (!dy || !x || !v || !a || !b || !order || !offsets || !dx || !aligned16(dy) ||
+  if (!dy || !x || !v || !a || !b || !order || !offsets || !dx || dx == dy || dx == x ||
+      !aligned16(dy) ||
       !aligned16(x) || !aligned16(a) || !aligned16(b) || !aligned16(base) || !aligned16(dx))
     return MOE_ERR_INVALID_ARG;
   const BwdLayout L = bwd_layout(T, n, r);

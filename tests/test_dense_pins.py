@@ -2,6 +2,7 @@
 hand-worked values, torch and finite differences, and the host-side checks of
 the entry points, which answer before any launch."""
 import ctypes
+import functools
 import math
 
 import numpy as np
@@ -144,6 +145,7 @@ def m():
 
 P = ctypes.c_void_p(1 << 20)             # fake, aligned addresses that no check reads
 U = ctypes.c_void_p((1 << 20) + 2)
+Q, R = ctypes.c_void_p(1 << 21), ctypes.c_void_p(1 << 22)
 INV, UNS, WS = 1, 2, 4
 BIG = 1 << 40
 
@@ -198,9 +200,11 @@ def test_dense_entry_points_refuse_before_any_launch(m):
     for kw in (dict(dy=None), dict(x=None), dict(wg=None), dict(wu=None), dict(wd=None),
                dict(ag=None), dict(au=None), dict(dx=None), dict(dg=None), dict(du=None),
                dict(dd=None), dict(dt=2), dict(act=9), dict(T=-2), dict(dy=U), dict(dx=U),
-               dict(add=U), dict(dg=U), dict(dd=U), dict(ag=U)):
-        assert ffn_b(**kw) == INV, kw
+               dict(add=U), dict(dg=U), dict(dd=U), dict(ag=U), dict(dx=Q, dy=Q),
+               dict(dx=Q, x=Q)):
+        assert ffn_b(**dict(dict(dx=R), **kw)) == INV, kw
     assert ffn_b(H=60) == UNS and ffn_b(acc=1) == UNS
+    ffn_b = functools.partial(ffn_b, dx=R)
     assert ffn_b(T=0, acc=1, dt=0) == 0 and ffn_b(T=0, dg=None, du=None, dd=None) == 0
     for kw in (dict(ws=None), dict(n=3 * 512 - 1), dict(ws=U)):
         assert ffn_b(**kw) == WS, kw
@@ -236,11 +240,12 @@ def test_dense_entry_points_refuse_before_any_launch(m):
     assert lora_b(T=0, acc=1) == 0
     for kw in (dict(dy=None), dict(x=None), dict(v=None), dict(a=None), dict(b=None),
                dict(order=None), dict(off=None), dict(dx=None), dict(da=None), dict(db=None),
-               dict(dy=U), dict(base=U), dict(da=U), dict(db=U), dict(n=0), dict(r=0)):
-        assert lora_b(**kw) == INV, kw
+               dict(dy=U), dict(base=U), dict(da=U), dict(db=U), dict(n=0), dict(r=0),
+               dict(dx=Q, dy=Q), dict(dx=Q, x=Q)):
+        assert lora_b(**dict(dict(dx=R), **kw)) == INV, kw
     assert lora_b(r=129) == UNS and lora_b(H=4) == UNS
     for kw in (dict(ws=None), dict(nb=255), dict(ws=U)):
-        assert lora_b(**kw) == WS, kw
+        assert lora_b(dx=R, **kw) == WS, kw
 
     def drop(y=P, x=None, k=10, rng=P, p=0.1, a=1.0, b=1.0, st=1, bt=1, out=P):
         return L.moe_dropout_residual(y, x, k, rng, m.moe_dropout_config(p, a, b, st, bt), out,

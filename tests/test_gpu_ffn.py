@@ -321,6 +321,34 @@ def test_ffn_on_another_stream_and_in_a_graph(T):
     assert m.moe_get_error() == 0
 
 
+@pytest.mark.parametrize("T,H,F", [(300000, 8, 8192), (90, 2048, 264)])
+def test_ffn_far_rows_and_repeats(T, H, F):
+    # h and the gradients of 2.4e9 elements, rows by their own formula; the same bits again
+    x = torch.zeros(T, H, dtype=BF, device="cuda")
+    x[:, 3] = (torch.arange(T, device="cuda") % 5 - 2).to(BF)
+    wg, wu = (torch.zeros(H, F, dtype=BF, device="cuda") for _ in range(2))
+    wd = torch.zeros(F, H, dtype=BF, device="cuda")
+    wg[3], wu[3] = 1.0, 2.0
+    wd[F - 1, 1] = 1.0
+    got = m.moe_gated_ffn(x, wg, wu, wd, act="relu", save_for_backward=True)
+    xs = x[:, 3].float()
+    h = xs.clamp(min=0) * 2 * xs
+    assert torch.equal(got["y"][:, 1].float(), h) and torch.equal(got["a_up"][:, F - 1].float(), 2 * xs)
+    assert torch.equal(m.moe_gated_ffn(x, wg, wu, wd, act="relu")["y"], got["y"])
+    dy = torch.zeros(T, H, dtype=BF, device="cuda")
+    dy[:, 1] = 1.0
+    back = [m.moe_gated_ffn_backward(dy, x, wg, wu, wd, got["a_gate"], got["a_up"], act="relu",
+                                     dw_dtype=torch.float32) for _ in range(2)]
+    on = (xs > 0).float()
+    # dA_g = 2 x [x > 0], dA_u = x [x > 0], in the last column alone
+    assert torch.equal(back[0]["dx"][:, 3].float(), 4 * xs * on)
+    assert back[0]["dw_down"][F - 1, 1] == h.double().sum()
+    assert back[0]["dw_up"][3, F - 1] == (xs * xs * on).double().sum()
+    for key in back[0]:
+        assert torch.equal(back[0][key], back[1][key]), key
+    assert m.moe_get_error() == 0
+
+
 def test_ffn_two_streams_at_once():
     H, F = 512, 1024
     runs = []

@@ -54,7 +54,10 @@ CASES = [(1, 64, 64, 1, 1, "one"), (1, 4096, 4096, 8, 16, "mixed"), (2, 8, 8, 3,
          (129, 72, 328, 3, 16, "runs"), (200, 136, 264, 2, 17, "mixed"),
          (300, 520, 128, 9, 33, "runs"), (257, 128, 512, 4, 100, "mixed"),
          (400, 256, 200, 40, 128, "runs"), (500, 64, 64, 3, 8, "none"),
-         (700, 328, 392, 1, 48, "one"), (1500, 200, 136, 6, 16, "mixed")]
+         (700, 328, 392, 1, 48, "one"), (1500, 200, 136, 6, 16, "mixed"),
+         # whole units of rows that follow one another, and few rows up to their bound
+         (900, 264, 392, 2, 64, "runs"), (600, 136, 200, 1, 128, "one"), (700, 72, 64, 1, 32, "one"),
+         (256, 72, 2056, 9, 32, "mixed"), (129, 1000, 72, 300, 2, "mixed")]
 
 
 @pytest.mark.parametrize("T,n,kind", [(0, 3, "mixed"), (1, 1, "one"), (31, 5, "mixed"),
@@ -122,6 +125,72 @@ def test_lora_gaussian(T, H, N, n, r, kind):
             <= 2.0 ** -8 * np.abs(want["dx"]) + 2.0 ** -15 * t["dx"]).all()
     for key in ("da", "db"):
         assert (np.abs(_np(back[key]) - want[key]) <= 2.0 ** -15 * t[key]).all(), key
+    assert m.moe_get_error() == 0
+
+
+def test_lora_scales_that_are_not_finite():
+    # an infinite scale makes its own adapter's rows infinite or NaN, and nothing else
+    for T, r in ((20, 5), (400, 20)):
+        v, ids, scales, base, _, dy = _draw(T, 64, 72, 4, r, "mixed", 3, True)
+        want = m.moe_lora(**v, adapter_ids=ids, scales=scales, base=base)
+        bad = scales.clone()
+        bad[2] = float("inf")
+        got = m.moe_lora(**v, adapter_ids=ids, scales=bad, base=base)
+        rest = ids != 2
+        assert torch.equal(got["out"][rest], want["out"][rest])
+        live = (want["out"] != base) & (ids == 2)[:, None]
+        assert not torch.isfinite(got["out"][live]).any()
+        a = m.moe_lora_backward(dy, v["x"], want["v"], v["a"], v["b"], ids, scales=scales)
+        b = m.moe_lora_backward(dy, v["x"], want["v"], v["a"], v["b"], ids, scales=bad)
+        keep = [0, 1, 3]
+        assert torch.equal(a["dx"][rest], b["dx"][rest])
+        assert torch.equal(a["da"][keep], b["da"][keep]) and torch.equal(a["db"][keep], b["db"][keep])
+
+
+def test_lora_two_streams_at_once():
+    runs = []
+    for T, r in ((200, 16), (1000, 64)):
+        v, ids, scales, base, dbase, dy = _draw(T, 264, 328, 5, r, "mixed", T, False)
+        runs.append((v, dict(adapter_ids=ids, scales=scales), base, dy, torch.cuda.Stream()))
+
+    def both(v, how, base, dy, stream):
+        f = m.moe_lora(**v, **how, base=base, stream=stream)
+        b = m.moe_lora_backward(dy, v["x"], f["v"], v["a"], v["b"], **how, stream=stream)
+        return [f["out"], f["v"], b["dx"], b["da"], b["db"]]
+
+    want = [both(*r[:4], None) for r in runs]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(8):
+        for i, r in enumerate(runs):
+            got[i].append(both(*r))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for g in got[i]:
+            assert all(torch.equal(p, q) for p, q in zip(g, want[i]))
+    assert m.moe_get_error() == 0
+
+
+def test_lora_past_two_to_the_31_elements():
+    # x of 2.2e9 elements: rows far out, in runs and one by one
+    T, H, N, n, r = 270000, 8192, 64, 3, 4
+    x = torch.zeros(T, H, dtype=BF, device="cuda")
+    x[:, 5] = (torch.arange(T, device="cuda") % 7 - 3).to(BF)
+    a = torch.zeros(n, r, H, dtype=BF, device="cuda")
+    a[:, 1, 5] = torch.tensor([1.0, 2.0, 3.0], device="cuda").to(BF)
+    b = torch.zeros(n, r, N, dtype=BF, device="cuda")
+    b[:, 1] = 1.0
+    for ids in (torch.arange(T, device="cuda") * n // T, torch.arange(T, device="cuda") % n):
+        got = m.moe_lora(x, a, b, ids.to(torch.int32))
+        want = x[:, 5].float() * (ids + 1)
+        assert torch.equal(got["v"][:, 1], want) and torch.equal(got["out"][:, 63].float(), want)
+        dy = torch.zeros(T, N, dtype=BF, device="cuda")
+        dy[:, 0] = 1.0
+        back = m.moe_lora_backward(dy, x, got["v"], a, b, ids.to(torch.int32))
+        assert torch.equal(back["dx"][:, 5].float(), (ids + 1).float())
+        sums = torch.zeros(n, device="cuda").index_add_(0, ids, x[:, 5].float())
+        assert torch.equal(back["da"][:, 1, 5], sums)
+        assert torch.equal(back["db"][:, 1, 0], sums * torch.tensor([1.0, 2.0, 3.0], device="cuda"))
     assert m.moe_get_error() == 0
 
 
