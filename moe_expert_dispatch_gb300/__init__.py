@@ -1253,11 +1253,12 @@ def moe_lora_plan(adapter_ids, n, order=None, offsets=None, stream=None):
 def _lora_shapes(x, a, b):
     """(T, H, N, n, r) of x [T, H], a [n, r, H] and b [n, r, N]."""
     T, H = _matrix(x, "x")
-    if a.dim() != 3 or b.dim() != 3 or a.shape[:2] != b.shape[:2]:
-        raise ValueError("a and b must have shapes [n, r, H] and [n, r, N], got "
-                         f"{list(a.shape)} and {list(b.shape)}")
-    n, r, N = b.shape
-    return T, H, N, n, r
+    if a.dim() == 3 and b.dim() == 3:
+        n, r, N = b.shape
+        if a.shape == (n, r, H):
+            return T, H, N, n, r
+    raise ValueError(f"a and b must have shapes [n, r, {H}] and [n, r, N], got "
+                     f"{list(a.shape)} and {list(b.shape)}")
 
 
 def moe_lora(x, a, b, adapter_ids, plan=None, scales=None, base=None, out=None, v=None,
@@ -1283,7 +1284,7 @@ def moe_lora(x, a, b, adapter_ids, plan=None, scales=None, base=None, out=None, 
              (base, "base", (T, N), bf16), (out, "out", (T, N), bf16), (v, "v", (T, r), f32))
     order, offsets = moe_lora_plan(adapter_ids, n) if plan is None else plan
     _all_fit(dev, (order, "order", (T,), i32), (offsets, "offsets", (n + 1,), i32))
-    ws, ws_bytes = _space(workspace, _lib.moe_lora_workspace_size, dev, T, n, r)
+    ws, ws_bytes = _scratch(workspace, _lib.moe_lora_workspace_size(T, n, r), dev)
     _check(_on(dev, _lib.moe_lora, x.data_ptr(), a.data_ptr(), b.data_ptr(),
                adapter_ids.data_ptr(), order.data_ptr(), offsets.data_ptr(), _ptr(scales),
                _ptr(base), T, H, N, n, r, out.data_ptr(), v.data_ptr(), _ptr(ws), ws_bytes,

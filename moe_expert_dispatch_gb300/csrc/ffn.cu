@@ -684,13 +684,20 @@ Divisor divisor(int64_t d) {
   return v;
 }
 
-Grid make_grid(int64_t M, int N, int cols) {
+// Tiles of an [M, N] result whose rows of A are kb k-blocks long. The clusters that run
+// at one time take a patch of tiles and move through K together, so that the squarest
+// patch reads least (8 row tiles by 9 or 10); where the rows of A of 16 row tiles fit in
+// half of L2, they stay there and the columns of B are what the patch has to spare.
+// Measured on 4096 x 14336 under the power cap: the gradients of 8192 rows 3740 us, by
+// 16 throughout 3784; the forward of 4096 rows 888 us, by 8 throughout 892.
+Grid make_grid(int64_t M, int N, int cols, int kb) {
   Grid g;
+  const int most = kb < 128 ? 16 : 8;          // 16 times 32 KB a k-block
   g.M = static_cast<int>(M);
   g.N = N;
   g.mt = up_div(M, 2 * kTileM);
   g.nt = up_div(N, cols);
-  g.group = g.mt < 16 ? g.mt : 16;
+  g.group = g.mt < most ? g.mt : most;
   g.per = divisor(static_cast<int64_t>(g.group) * g.nt);
   g.whole = divisor(g.group);
   g.last = divisor(g.group > 0 ? (g.mt - 1) % g.group + 1 : 0);
@@ -845,8 +852,8 @@ struct FwdPlan {
 };
 FwdPlan fwd_plan(int64_t T, int H, int F) {
   FwdPlan f;
-  f.gated = make_grid(T, F, BN / 2);
-  f.down = make_grid(T, H, BN);
+  f.gated = make_grid(T, F, BN / 2, up_div(H, BK));
+  f.down = make_grid(T, H, BN, up_div(F, BK));
   const bool few = T <= kFewRows;
   f.s_gated = few ? 1 : pick_split(f.gated, up_div(H, BK));
   f.s_down = few ? 1 : pick_split(f.down, up_div(F, BK));
@@ -865,11 +872,11 @@ struct BwdPlan {
 };
 BwdPlan bwd_plan(int64_t T, int H, int F, bool dw) {
   BwdPlan b;
-  b.dh = make_grid(T, F, BN);
-  b.dx = make_grid(T, H, BN);
-  b.down = make_grid(F, H, BN);
-  b.gate = make_grid(H, F, BN);
   b.kb_rows = up_div(T, BK);
+  b.dh = make_grid(T, F, BN, up_div(H, BK));
+  b.dx = make_grid(T, H, BN, 2 * up_div(F, BK));
+  b.down = make_grid(F, H, BN, b.kb_rows);
+  b.gate = make_grid(H, F, BN, b.kb_rows);
   b.dw_units = dw ? static_cast<int64_t>(b.down.mt) * b.down.nt +
                         2 * static_cast<int64_t>(b.gate.mt) * b.gate.nt
                   : 0;

@@ -328,7 +328,7 @@ def test_lora_refusals():
         m.moe_lora(**v, adapter_ids=ids.long())
     with pytest.raises(ValueError, match="offsets"):
         m.moe_lora(**v, adapter_ids=ids, plan=(ids, ids))
-    with pytest.raises(ValueError, match="a must"):
+    with pytest.raises(ValueError, match="a and b must"):
         m.moe_lora(v["x"][:, :56].contiguous(), v["a"], v["b"], ids)
     with pytest.raises(ValueError, match="scales"):
         m.moe_lora(**v, adapter_ids=ids, scales=scales[:2])
