@@ -828,8 +828,8 @@ moe_status moe_lora_plan(const int32_t* adapter_ids, int64_t T, int n, int32_t* 
  *  v       float [T, r]  out: what the backward needs
  *  workspace >= moe_lora_workspace_size(T, n, r) bytes, 16-byte aligned; 0 bytes,
  *          and NULL allowed, for the few rows that need none
- * 1 <= r <= 128, H % 8 == 0 and N % 8 == 0 (else MOE_ERR_UNSUPPORTED), 1 <= n <=
- * 1024, T < 2^31 - 1024. Pointers start on 16 bytes (v and the int32 arrays on
+ * 1 <= r <= 128, H % 8 == 0, N % 8 == 0 and T <= 2^27 (else MOE_ERR_UNSUPPORTED),
+ * 1 <= n <= 1024. Pointers start on 16 bytes (v and the int32 arrays on
  * 4); out and v overlap nothing else of the call (out: base alone, and then as a
  * whole, base being no other argument). The plan is that of adapter_ids. T = 0 does
  * nothing. Waits as moe_gated_ffn's.
@@ -894,7 +894,8 @@ void moe_dropout_config_init(moe_dropout_config* cfg);
  *          runs, so that a graph replayed with another draw drops others. Two
  *          calls with one seed and draw drop the same elements.
  * Pointers aligned to their element (with all of them on 16 bytes eight elements
- * go at once). numel < 2^40; 0 does nothing.
+ * go at once). numel < 2^40; 0 does nothing. A factor f that is not finite, and out
+ * over a y of another type, is MOE_ERR_INVALID_ARG.
  * ------------------------------------------------------------------------ */
 moe_status moe_dropout_residual(const void* y, const void* x, int64_t numel, const int64_t* rng,
                                 const moe_dropout_config* cfg, void* out, void* stream);
@@ -905,7 +906,7 @@ moe_status moe_dropout_residual(const void* y, const void* x, int64_t numel, con
  *  dx      [numel] of the stream's type, or NULL (no residual, or a = 1, where
  *          it is d_out); may be d_out itself
  *  dy      [numel] of the branch's type   out; may be d_out where the types are
- *          one and dx is NULL
+ *          one and dx is NULL (else, and for dy over dx, MOE_ERR_INVALID_ARG)
  * ------------------------------------------------------------------------ */
 moe_status moe_dropout_residual_backward(const void* d_out, int64_t numel, const int64_t* rng,
                                          const moe_dropout_config* cfg, void* dx, void* dy,

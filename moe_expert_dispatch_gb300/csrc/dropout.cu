@@ -206,7 +206,7 @@ moe_status prepare(int64_t numel, const int64_t* rng, const moe_dropout_config& 
   p.threshold = static_cast<uint32_t>(t) << 16;
   p.a = c.residual_scale;
   p.f = static_cast<float>(c.branch_scale / (1.0 - t / 65536.0));
-  return MOE_OK;
+  return isfinite(p.f) ? MOE_OK : MOE_ERR_INVALID_ARG;   // inf * 0 where y is 0
 }
 
 }  // namespace
@@ -237,7 +237,7 @@ moe_status moe_dropout_residual(const void* y, const void* x, int64_t numel, con
   const moe_status s = prepare(numel, rng, c, p);
   if (s != MOE_OK || numel == 0) return s;
   if (!y || !out || !aligned(y, width(c.branch_type)) || !aligned(x, width(c.stream_type)) ||
-      !aligned(out, width(c.stream_type)))
+      !aligned(out, width(c.stream_type)) || (out == y && c.stream_type != c.branch_type))
     return MOE_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e =
@@ -257,7 +257,8 @@ moe_status moe_dropout_residual_backward(const void* d_out, int64_t numel, const
   const moe_status s = prepare(numel, rng, c, p);
   if (s != MOE_OK || numel == 0) return s;
   if (!d_out || !dy || !aligned(d_out, width(c.stream_type)) || !aligned(dx, width(c.stream_type)) ||
-      !aligned(dy, width(c.branch_type)))
+      !aligned(dy, width(c.branch_type)) || dy == dx ||
+      (dy == d_out && (dx || c.stream_type != c.branch_type)))
     return MOE_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e =

@@ -39,6 +39,9 @@ namespace {
 constexpr int kRows = 128;          // rows of a unit: one adapter's
 constexpr int kMaxAdapters = 1024;
 constexpr int kMaxRank = 128;
+// Offsets that overlap can name every row 512 times: with so many rows the sums of
+// units and chunks stay below 2^31 whatever a plan holds.
+constexpr int64_t kMaxRows = 1 << 27;
 constexpr unsigned long long kDrainNs = 1000000000ull;
 constexpr int kAtom = kRows * 128;  // 16 KB: 128 rows x 64 columns of an image or a tile
 // 64-wide atoms of an image of so many parts
@@ -59,7 +62,6 @@ template <int N>
 __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-
 
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr, uint32_t rank) {
   float v;
@@ -1394,7 +1396,7 @@ moe_status check_sizes(int64_t T, int H, int N, int n, int r) {
   if (T < 0 || T > INT32_MAX - 1024 || H <= 0 || N <= 0 || H > (1 << 30) || N > (1 << 30) ||
       n < 1 || n > kMaxAdapters || r < 1)
     return MOE_ERR_INVALID_ARG;
-  return (H % 8 || N % 8 || r > kMaxRank) ? MOE_ERR_UNSUPPORTED : MOE_OK;
+  return (H % 8 || N % 8 || r > kMaxRank || T > kMaxRows) ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
 
 // The rows that one cluster each takes without a plan: every row reads its adapter

@@ -267,6 +267,34 @@ def test_dense_entry_points_refuse_before_any_launch(m):
         assert drop_b(**kw) == INV, kw
 
 
+def test_dense_entry_points_refuse_what_would_overlap_or_overflow(m):
+    if torch.cuda.is_available():
+        pytest.skip("host-only: the cases carry fake device addresses")
+    L = m._lib
+
+    def drop(y=P, x=None, numel=64, out=Q, p=0.5, b=1.0, st=0, bt=1):
+        return L.moe_dropout_residual(y, x, numel, R, m.moe_dropout_config(p, 1.0, b, st, bt), out,
+                                      None)
+
+    def drop_b(d_out=P, numel=64, dx=None, dy=Q, st=0, bt=1):
+        return L.moe_dropout_residual_backward(d_out, numel, R,
+                                               m.moe_dropout_config(0.5, 1.0, 1.0, st, bt), dx, dy,
+                                               None)
+
+    assert drop(out=P) == INV and drop_b(dy=P) == INV
+    assert drop_b(dy=P, dx=Q, bt=0) == INV and drop_b(dx=Q, dy=Q, bt=0) == INV
+    # the factor is rounded to float: 3e38 / (1 - 1/2) is past its range
+    assert drop(b=3e38) == INV and drop(b=-3e38) == INV and drop(b=3e38, numel=0) == INV
+
+    T = 2 ** 27
+    assert m._lib.moe_lora_workspace_size(T, 3, 4) > 0
+    assert m._lib.moe_lora_workspace_size(T + 1, 3, 4) == 0
+    assert m._lib.moe_lora_backward_workspace_size(T + 1, 3, 4) == 0
+    assert L.moe_lora(P, P, P, P, P, P, None, None, T + 1, 8, 8, 3, 4, P, P, P, BIG, None) == UNS
+    assert L.moe_lora_backward(P, P, P, P, P, P, P, None, None, T + 1, 8, 8, 3, 4, R, P, P, 0, P,
+                               BIG, None) == UNS
+
+
 def test_dense_binding_refuses_before_the_library(m):
     bf = torch.bfloat16
     x, w, wd = torch.zeros(4, 16, dtype=bf), torch.zeros(16, 8, dtype=bf), torch.zeros(8, 16, dtype=bf)
