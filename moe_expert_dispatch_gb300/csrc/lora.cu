@@ -156,31 +156,46 @@ __device__ __forceinline__ Unit find_unit(const Plan& p, int u) {
   return b;
 }
 
-// Stable counting sort by adapter in one CTA: each of 32 warps counts a run of
-// rows, one scan over adapters and warps gives every run its places, and each warp
-// then deals its rows out.
+// Stable counting sort by adapter in one cluster: each warp counts a run of rows, one
+// scan over adapters, CTAs and warps gives every run its places, and each warp then
+// deals its rows out, 32 at a time: which of them share an adapter comes from a ballot
+// for each bit of the id. Eight loads of a lane are under way at once; what bounds it is
+// the ballots' issue, which eight CTAs share.
+constexpr int kIdLoads = 8;
+constexpr int kPlanCtas = 8;
+// Rows up to which one CTA sorts alone, spared the cluster's two barriers. 64 rows of 8
+// adapters take 2.8 us so and 4.2 by eight CTAs, 4096 5.0 both ways; 65536 of 64 47 and 10.
+constexpr int64_t kPlanRows = 4096;
+
+// The ids of rows t, t + 32, ... below t1 as they are.
+__device__ __forceinline__ void plan_keys(const int32_t* ids, int64_t t, int64_t t1, int* key) {
+#pragma unroll
+  for (int i = 0; i < kIdLoads; ++i) key[i] = t + 32 * i < t1 ? __ldg(ids + t + 32 * i) : -1;
+}
+
 __global__ void __launch_bounds__(1024, 1)
     plan_kernel(const int32_t* ids, int64_t T64, int n, int32_t* order, int32_t* offsets, int* err) {
   extern __shared__ int plan_smem[];
   const int keys = n + 1, T = static_cast<int>(T64);
-  int* place = plan_smem;                       // [32][keys]
-  int* total = place + 32 * keys;               // [keys + 1]
+  int* place = plan_smem;                       // [32][keys]: of a warp, before it in the CTA
+  int* count = place + 32 * keys;               // [keys]: the CTA's
+  const int rank = static_cast<int>(cluster_ctarank()), ctas = static_cast<int>(gridDim.x);
+  int* total = ctas > 1 ? count + keys : count; // [keys]: of all CTAs, then where they begin
   const int warp = threadIdx.x >> 5, lane = lane_id();
   for (int i = threadIdx.x; i < 32 * keys; i += 1024) place[i] = 0;
   __syncthreads();
-  const int64_t run = (T64 + 1023) / 1024 * 32;             // rows of a warp, a multiple of 32
-  const int64_t t0 = warp * run, t1 = min(t0 + run, T64);
+  const int64_t run = (T64 + 1024 * ctas - 1) / (1024 * ctas) * 32;   // rows of a warp
+  const int64_t t0 = (rank * 32 + warp) * run, t1 = min(t0 + run, T64);
   int* mine = place + warp * keys;
-  for (int64_t t = t0 + lane; t - lane < t1; t += 32) {
-    int key = -1;
-    if (t < t1) {
-      key = ids[t];
-      if (key < -1 || key >= n) report_error(err, kErrBadId);
-      if (key < 0 || key >= n) key = n;
+  for (int64_t t = t0 + lane; t - lane < t1; t += 32 * kIdLoads) {
+    int key[kIdLoads];
+    plan_keys(ids, t, t1, key);
+#pragma unroll
+    for (int i = 0; i < kIdLoads; ++i) {
+      if (t + 32 * i >= t1) break;
+      if (key[i] < -1 || key[i] >= n) report_error(err, kErrBadId);
+      atomicAdd(mine + (key[i] < 0 || key[i] >= n ? n : key[i]), 1);   // counts: no order
     }
-    const unsigned same = __match_any_sync(0xffffffffu, key);
-    if (key >= 0 && lane == __ffs(same) - 1) mine[key] += __popc(same);
-    __syncwarp();
   }
   __syncthreads();
   for (int k = threadIdx.x; k < keys; k += 1024) {
@@ -190,9 +205,24 @@ __global__ void __launch_bounds__(1024, 1)
       place[w * keys + k] = sum;
       sum += c;
     }
-    total[k] = sum;
+    count[k] = sum;
   }
-  __syncthreads();
+  if (ctas > 1) {
+    cluster_sync();
+    for (int k = threadIdx.x; k < keys; k += 1024) {
+      int sum = 0, before = 0;                   // over the CTAs, and those before this one
+      for (int q = 0; q < ctas; ++q) {
+        const int c = __float_as_int(ld_cluster_f32(smem_u32(count + k), q));
+        if (q < rank) before += c;
+        sum += c;
+      }
+      total[k] = sum;
+      for (int w = 0; w < 32; ++w) place[w * keys + k] += before;
+    }
+    cluster_sync();                              // the others have read this CTA's counts
+  } else {
+    __syncthreads();
+  }
   if (warp == 0) {
     int before = 0;
     for (int k0 = 0; k0 < keys; k0 += 32) {
@@ -205,25 +235,35 @@ __global__ void __launch_bounds__(1024, 1)
       }
       if (k0 + lane < keys) {
         total[k0 + lane] = before + sum - c;
-        offsets[k0 + lane] = before + sum - c;   // keys = n + 1 offsets: the last is where none begin
+        // keys = n + 1 offsets: the last is where none begin
+        if (rank == 0) offsets[k0 + lane] = before + sum - c;
       }
       before += __shfl_sync(0xffffffffu, sum, 31);
     }
   }
   __syncthreads();
-  for (int64_t t = t0 + lane; t - lane < t1; t += 32) {
-    int key = -1;
-    if (t < t1) {
-      key = ids[t];
-      if (key < 0 || key >= n) key = n;
+  const int bits = 32 - __clz(n);                // of the keys 0 to n
+  for (int64_t t = t0 + lane; t - lane < t1; t += 32 * kIdLoads) {
+    int key[kIdLoads];
+    plan_keys(ids, t, t1, key);
+#pragma unroll
+    for (int i = 0; i < kIdLoads; ++i) {
+      if (t - lane + 32 * i >= t1) break;        // the whole warp
+      const bool row = t + 32 * i < t1;
+      const int k = key[i] < 0 || key[i] >= n ? n : key[i];
+      unsigned same = __ballot_sync(0xffffffffu, row);
+      for (int b = 0; b < bits; ++b) {
+        const bool set = (k >> b) & 1;
+        const unsigned m = __ballot_sync(0xffffffffu, set);
+        same &= set ? m : ~m;
+      }
+      int at = T;
+      if (row) at = total[k] + mine[k] + __popc(same & ((1u << lane) - 1));
+      __syncwarp();
+      if (at < T) order[at] = static_cast<int32_t>(t + 32 * i);
+      if (row && lane == __ffs(same) - 1) mine[k] += __popc(same);
+      __syncwarp();
     }
-    const unsigned same = __match_any_sync(0xffffffffu, key);
-    int at = 0;
-    if (key >= 0) at = total[key] + mine[key] + __popc(same & ((1u << lane) - 1));
-    if (key >= 0 && at < T) order[at] = static_cast<int32_t>(t);
-    __syncwarp();
-    if (key >= 0 && lane == __ffs(same) - 1) mine[key] += __popc(same);
-    __syncwarp();
   }
 }
 
@@ -233,8 +273,11 @@ __global__ void __launch_bounds__(1024, 1)
 // added over the cluster in the order of the ranks, and each CTA splits and writes
 // its share. Warps: 0 loads P by TMA, 1 issues the MMAs, then 4 (a quarter of the
 // accumulators' rows each) or 8 (and half of their columns) drain the accumulators,
-// and 4 gather the rows (cp.async, 128 bytes a row and k-block) where warp 0 cannot load
-// them as a box.
+// and 4 gather the rows (cp.async, 128 bytes a row and k-block). Boxes by TMA where the
+// rows follow one another were no faster (16384 rows of 4096, r = 64: 164 us the whole
+// backward both ways). Bound by the rows: 8192 of 4096, r = 16, take 19.5 us, 3.4 TB/s,
+// 16384 with r = 64 and the images of both V 37 us, 4.0 TB/s; what is missing to the
+// memory's rate is the start and end of CTAs that live for 30 k-blocks or fewer.
 constexpr int kBlocks = 2;          // k-blocks that an accumulator takes up
 
 template <int R>
@@ -284,8 +327,7 @@ __device__ __forceinline__ void put_parts(uint8_t* img, int unit, int row, int c
 
 template <int R>
 __global__ void __launch_bounds__(Shrink<R>::kThreads, R > 64 ? 1 : 2)
-    shrink_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_in,
-                  const __grid_constant__ ShrinkArgs p) {
+    shrink_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ ShrinkArgs p) {
   using S = Shrink<R>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ int rows[kRows];
@@ -329,8 +371,6 @@ __global__ void __launch_bounds__(Shrink<R>::kThreads, R > 64 ? 1 : 2)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  // a full unit of rows that follow one another (a request's tokens) is a box
-  const bool box = __syncthreads_and(tid >= kRows || (rows[0] >= 0 && rows[tid] == rows[0] + tid));
   const uint32_t tmem = tmem_at;
   const int kblocks = (p.K + 63) / 64, per = (kblocks + p.split - 1) / p.split;
   const int kb0 = min(kblocks, static_cast<int>(rank) * per), kb1 = min(kblocks, kb0 + per);
@@ -349,10 +389,7 @@ __global__ void __launch_bounds__(Shrink<R>::kThreads, R > 64 ? 1 : 2)
         const int s = i % S::kStages;
         ok = mbar_wait(smem_u32(&empty[s]), ((i / S::kStages) & 1) ^ 1, p.wait_ns, stopped);
         if (!ok) break;
-        mbar_arrive_expect_tx(smem_u32(&full[s]), R * 128 + (box ? kAtom : 0));
-        if (box)
-          tma_load_2d(smem_u32(ring) + s * S::kStage, &map_in, smem_u32(&full[s]), (kb0 + i) * 64,
-                      rows[0]);
+        mbar_arrive_expect_tx(smem_u32(&full[s]), R * 128);
         tma_load_3d(smem_u32(ring) + s * S::kStage + kAtom, &map_p, smem_u32(&full[s]),
                     (kb0 + i) * 64, 0, u.a);
       }
@@ -405,10 +442,6 @@ __global__ void __launch_bounds__(Shrink<R>::kThreads, R > 64 ? 1 : 2)
       const bool got = mbar_wait(smem_u32(&empty[s]), ((i / S::kStages) & 1) ^ 1, p.wait_ns, stopped);
       ok = __all_sync(0xffffffffu, got);
       if (!ok) break;
-      if (box) {
-        mbar_arrive(smem_u32(&full[s]));
-        continue;
-      }
       const uint32_t sa = smem_u32(ring) + s * S::kStage;
       const bool in_k = k0 + ch * 8 < p.K;
 #pragma unroll
@@ -516,7 +549,10 @@ __global__ void __launch_bounds__(Shrink<R>::kThreads, R > 64 ? 1 : 2)
 // image and Q, 1 issues the MMAs, 2 to 5 finish every second tile and 6 to 9 the
 // others: base comes in by runs of 128 bytes a row, a tile ahead in registers, and goes
 // through 4 KB of shared memory a warp, in which each lane adds its row of the
-// accumulator, back into runs of 128 bytes.
+// accumulator, back into runs of 128 bytes. Bound by base and out: 8192 rows of 4096, r =
+// 16, take 30 us, 4.4 TB/s; 16384, r = 64, 52 us, 5.2 TB/s. Launched beside the shrink
+// kernel (as far as its results let it) both were slower, 58 us against 51 for the 8192:
+// its CTAs take the room in which shrink's next ones start.
 constexpr int kCols = 64;
 constexpr int kPiece = 32 * 128;
 constexpr int kExpandThreads = 320;
@@ -735,7 +771,10 @@ __global__ void __launch_bounds__(kExpandThreads, R > 64 ? 1 : 2)
 // columns, or 32 columns and half of the rank) and 4 gathering rows of the input, each
 // row's columns of the tile in one run of 512 (256) bytes, where warp 0 cannot load the
 // 64 rows as boxes. The accumulators take up two chunks of an output; those of one half
-// of a tile are taken out while the other half's MMAs run.
+// of a tile are taken out while the other half's MMAs run. Bound by the input's rows, and
+// by what one warp issues for a stage: 16384 rows of twice 4096, r = 64, take 62 us, 4.8
+// TB/s, and the finish 9; with the rows gathered by cp.async throughout the whole backward
+// takes 191 us instead of 164.
 struct GradJob {
   CUtensorMap map;             // of in: boxes of 64 columns x 64 rows
   const uint8_t* img;          // three parts
@@ -1153,7 +1192,8 @@ constexpr int kFewAhead = 44 * 1024;   // bytes of B that are fetched before v i
 // One cluster a row: each CTA takes an eighth of H for v and, once the cluster has
 // added v up, an eighth of N for out. What the CTA needs of B is on its way into shared
 // memory (as much as kFewAhead holds) and base in registers before v is known. No plan,
-// one launch; what bounds it is the latency of three loads and two cluster barriers.
+// one launch; what bounds it is the latency of three loads and two cluster barriers: one
+// row takes 4.1 us, 64 rows of as many adapters (23 MB) 8.1, 2.8 TB/s.
 __global__ void __launch_bounds__(kFewThreads, 4)
     few_kernel(const __nv_bfloat16* __restrict__ x, const __nv_bfloat16* __restrict__ A,
                const __nv_bfloat16* __restrict__ B, const int32_t* __restrict__ ids,
@@ -1327,6 +1367,7 @@ cudaError_t launch(void (*kern)(KArgs...), dim3 grid, int threads, int smem, int
 }
 
 int64_t max_units(int64_t T, int n) { return (T + kRows - 1) / kRows + n; }
+// The kernels' R: 8192 rows with r = 16 take 51 us by R = 16 and 54 by 32.
 int rank_up(int r) { return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128; }
 size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 size_t image_bytes(int64_t T, int n, int r, int parts) {
@@ -1336,20 +1377,19 @@ size_t image_bytes(int64_t T, int n, int r, int parts) {
 template <int R>
 cudaError_t shrink(const __nv_bfloat16* P, ShrinkArgs p, cudaStream_t st) {
   static bool configured[kMaxDevices] = {};
-  CUtensorMap map, map_in;
-  if (!make_tmap_bf16_3d(&map, P, p.K, p.r, p.plan.n, 64, R) ||
-      !make_tmap_bf16_2d(&map_in, p.in, p.K, p.plan.T, static_cast<uint64_t>(p.K) * 2, 64, kRows))
-    return cudaErrorInvalidValue;
+  CUtensorMap map;
+  if (!make_tmap_bf16_3d(&map, P, p.K, p.r, p.plan.n, 64, R)) return cudaErrorInvalidValue;
   const int64_t units = max_units(p.plan.T, p.plan.n);
   const int kblocks = (p.K + 63) / 64;
   // CTAs to a cluster: as many as two an SM take at once, each with four k-blocks at least
+  // (300 rows of 16 adapters, 4096 x 4096: the call takes 18 us, 38 with one CTA a unit)
   p.split = 1;
   while (p.split < 8 && kblocks / (p.split + 1) >= 4 &&
          units * (p.split + 1) <= 2 * device_sm_count())
     ++p.split;
   p.wait_ns = kDefaultWaitNs;
   return launch(shrink_kernel<R>, dim3(static_cast<unsigned>(units * p.split)), Shrink<R>::kThreads,
-                Shrink<R>::kBytes, p.split, false, configured, st, map, map_in, p);
+                Shrink<R>::kBytes, p.split, false, configured, st, map, p);
 }
 
 template <int R>
@@ -1359,7 +1399,8 @@ cudaError_t expand(const __nv_bfloat16* Q, int r, ExpandArgs p, cudaStream_t st)
   if (!make_tmap_bf16_3d(&map, Q, p.N, r, p.plan.n, 64, R)) return cudaErrorInvalidValue;
   const int64_t units = max_units(p.plan.T, p.plan.n);
   const int tiles = (p.N + kCols - 1) / kCols;
-  // CTAs to a unit: as many as two an SM take at once, each with four tiles at least
+  // CTAs to a unit: as many as two an SM take at once, each with four tiles at least (the
+  // same 300 rows: 18 us, 53 with one CTA a unit)
   int split = 1;
   while (tiles / (split + 1) >= 4 && units * (split + 1) <= 2 * device_sm_count()) ++split;
   p.wait_ns = kDefaultWaitNs;
@@ -1400,7 +1441,9 @@ moe_status check_sizes(int64_t T, int H, int N, int n, int r) {
 }
 
 // The rows that one cluster each takes without a plan: every row reads its adapter
-// whole, which the rows of a unit share otherwise.
+// whole, which the rows of a unit share otherwise. Measured with 32 adapters over 4096 x
+// 4096, by clusters and by units: r = 16, 128 rows 11 and 21 us, 256 19 and 21, 512 34 and
+// 21; r = 64, 128 rows 20 and 32, 256 36 and 33.
 bool few_rows(int64_t T, int r) { return T <= 256 && T * r <= 8192; }
 
 // What the backward has in its workspace.
@@ -1436,16 +1479,18 @@ moe_status moe_lora_plan(const int32_t* adapter_ids, int64_t T, int n, int32_t* 
   static bool configured[kMaxDevices] = {};
   const int d = current_device();
   if (d < 0 || d >= kMaxDevices) return MOE_ERR_CUDA;
-  auto bytes = [](int keys) { return (33 * keys + 1) * static_cast<int>(sizeof(int)); };
-  if (!configured[d]) {
-    if (cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             bytes(kMaxAdapters + 1)) != cudaSuccess)
-      return MOE_ERR_CUDA;
-    configured[d] = true;
-  }
-  plan_kernel<<<1, 1024, bytes(n + 1), static_cast<cudaStream_t>(stream)>>>(
-      adapter_ids, T, n, order, offsets, device_error_word());
-  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  auto bytes = [](int keys) { return 34 * keys * static_cast<int>(sizeof(int)); };
+  if (!configured[d] &&
+      cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           bytes(kMaxAdapters + 1)) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  configured[d] = true;
+  const int ctas = T <= kPlanRows ? 1 : kPlanCtas;
+  return launch(plan_kernel, dim3(ctas), 1024, bytes(n + 1), ctas, false, configured,
+                static_cast<cudaStream_t>(stream), adapter_ids, T, n, order, offsets,
+                device_error_word()) == cudaSuccess
+             ? MOE_OK
+             : MOE_ERR_CUDA;
 }
 
 size_t moe_lora_workspace_size(int64_t T, int n, int r) {

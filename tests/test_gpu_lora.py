@@ -64,6 +64,19 @@ CASES = [(1, 64, 64, 1, 1, "one"), (1, 4096, 4096, 8, 16, "mixed"), (2, 8, 8, 3,
                                       (33, 5, "runs"), (1000, 1, "none"), (1024, 1024, "mixed"),
                                       (1025, 7, "mixed"), (20000, 33, "mixed")])
 def test_lora_plan(T, n, kind):
+    _check_plan(T, n, kind)
+
+
+# on both sides of where a cluster takes the rows, runs that end inside a CTA's share, one
+# key alone and every key
+@pytest.mark.parametrize("T,n,kind", [(4096, 1024, "mixed"), (4097, 1024, "mixed"),
+                                      (4097, 1, "none"), (8191, 3, "runs"), (70001, 1, "one"),
+                                      (65600, 1000, "mixed"), (100003, 64, "runs")])
+def test_lora_plan_of_many_rows(T, n, kind):
+    _check_plan(T, n, kind)
+
+
+def _check_plan(T, n, kind):
     ids = _ids(T, n, kind, np.random.default_rng(T))
     order, offsets = m.moe_lora_plan(torch.from_numpy(ids.astype(np.int32)).cuda(), n)
     want = orc.lora_plan(ids.tolist(), n)
