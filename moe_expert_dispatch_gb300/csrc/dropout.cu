@@ -159,6 +159,7 @@ bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p
 template <typename TIn, typename TOut, bool kRes, bool kDx>
 cudaError_t launch_typed(const void* in, const void* res, void* out, void* dx, const DropArgs& p,
                          cudaStream_t st) {
+  // 16 bytes at a time: 16.8 M elements of bf16 take 12.4 us so, one by one 48
   const bool wide = aligned(in, 16) && aligned(res, 16) && aligned(out, 16) && aligned(dx, 16);
   const int64_t ctas = ((p.numel + 7) / 8 + kThreads - 1) / kThreads;
   // One wave of CTAs that step through the tensor spares the others their start (seed and

@@ -707,7 +707,9 @@ Grid make_grid(int64_t M, int N, int cols, int kb) {
 int clusters() { return device_sm_count() > 1 ? device_sm_count() / 2 : 1; }
 
 // Parts of K for a product alone in its launch: as many as the clusters that its tiles
-// leave idle, each with 8 k-blocks at least (half of what a tile's start and end cost).
+// leave idle, each with 8 k-blocks at least (what a tile's start and end cost). Measured,
+// split and not: the forward of 4096 x 14336, 160 rows 80 and 114 us, 512 rows 113 and
+// 135, 1024 198 both ways; dh of 2048 x 768 in the gradients of 256 rows, 24 and 33.
 int pick_split(const Grid& g, int kb) {
   const int64_t tiles = static_cast<int64_t>(g.mt) * g.nt;
   int s = 1;
@@ -715,16 +717,36 @@ int pick_split(const Grid& g, int kb) {
   return s;
 }
 
-// Parts of K of dx beside the weight gradients: so that none of its units lasts longer
-// than an equal share of the launch. A tile costs its k-blocks and about 8 more.
+// Parts of K of dx beside the weight gradients, by what the launch would take in k-blocks
+// of a cluster: a tile costs its own and some 8 more; the clusters without a unit of dx
+// take gradient tiles meanwhile, as unit_at deals them out, and all of them the rest. The
+// kernel that adds the parts up costs about 9, and their way out and in again one for
+// three parts. Measured, split and not: 160 rows of 1024 x 8192 58 and 115 us, 512 rows
+// of 2048 x 8192 100 and 111; not worth it where the gradients are the most of it or a
+// split needs another round, 256 rows of 2048 x 768 27 and 24, 2048 of 512 x 2048 45 and 39.
 constexpr int kTileCost = 8;
 int pick_split_joint(const Grid& g, int kb, int64_t dw_units, int kb_rows) {
   if (dw_units == 0) return pick_split(g, kb);
-  const int64_t tiles = static_cast<int64_t>(g.mt) * g.nt;
-  const int64_t share = (tiles * (kb + kTileCost) + dw_units * (kb_rows + kTileCost)) / clusters();
-  int s = 1;
-  while (s < kMaxSplit && kb / s + kTileCost > share && kb / (s + 1) >= 8) ++s;
-  return s;
+  const int64_t tiles = static_cast<int64_t>(g.mt) * g.nt, all = clusters(), dw = kb_rows + kTileCost;
+  int best = 1;
+  int64_t least = 0;
+  for (int s = 1; s <= kMaxSplit && (s == 1 || (kb / s >= 8 && tiles * s < all)); ++s) {
+    const int64_t own = up_div(kb, s) + kTileCost, idle = all - tiles * s;
+    int64_t cost;
+    if (idle <= 0) {
+      cost = (tiles * own + dw_units * dw) / all;
+    } else {
+      const int64_t left = dw_units - idle * (own / dw), rounds = (dw_units + idle - 1) / idle;
+      if (left > 0) cost = own + (left + all - 1) / all * dw;
+      else cost = own > rounds * dw ? own : rounds * dw;
+    }
+    if (s > 1) cost += 9 + tiles * s / 3;
+    if (s == 1 || cost < least) {
+      best = s;
+      least = cost;
+    }
+  }
+  return best;
 }
 
 void set_main(Args& p, const Grid& g, int kb0, int kb, int split) {
@@ -1046,7 +1068,8 @@ moe_status moe_gated_ffn_backward(const void* dy, const void* x, const void* w_g
     pj.kb_rows = b.kb_rows;
     pj.f32 = f32;
     pj.accumulate = accumulate_dw;
-    // as many rounds as the gradient tiles that take as long as a unit of dx
+    // as many rounds as the gradient tiles that take as long as a unit of dx (the
+    // gradients of 300 rows of 4096 x 14336: 253 us, with everyone in every round 304)
     pj.skip = pj.units > 0 ? (pj.per + kTileCost) / (b.kb_rows + kTileCost) : 0;
   }
   if (launch<Op::Joint>(mj, pj, st) != cudaSuccess ||
