@@ -156,6 +156,20 @@ __device__ __forceinline__ Unit find_unit(const Plan& p, int u) {
   return b;
 }
 
+// The units of a batch, those of rows without an adapter where none is set. Called by a
+// whole warp.
+__device__ __forceinline__ int count_units(const Plan& p, bool none) {
+  int sum = 0;
+  for (int a = lane_id(); a < p.n + (none ? 1 : 0); a += 32) {
+    int lo, hi;
+    segment(p, a, lo, hi);
+    sum += (hi - lo + kRows - 1) / kRows;
+  }
+#pragma unroll
+  for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  return sum;
+}
+
 // Stable counting sort by adapter in one cluster: each warp counts a run of rows, one
 // scan over adapters, CTAs and warps gives every run its places, and each warp then
 // deals its rows out, 32 at a time: which of them share an adapter comes from a ballot
@@ -545,14 +559,19 @@ __global__ void __launch_bounds__(Shrink<R>::kThreads, R > 64 ? 1 : 2)
 
 // ------------------------------------------------------------------ expand
 
-// A CTA takes a unit and every gridDim.y-th tile of 64 columns. Warps: 0 loads the
-// image and Q, 1 issues the MMAs, 2 to 5 finish every second tile and 6 to 9 the
-// others: base comes in by runs of 128 bytes a row, a tile ahead in registers, and goes
-// through 4 KB of shared memory a warp, in which each lane adds its row of the
-// accumulator, back into runs of 128 bytes. Bound by base and out: 8192 rows of 4096, r =
-// 16, take 30 us, 4.4 TB/s; 16384, r = 64, 52 us, 5.2 TB/s. Launched beside the shrink
-// kernel (as far as its results let it) both were slower, 58 us against 51 for the 8192:
-// its CTAs take the room in which shrink's next ones start.
+// The work is a list of items (unit, tile of 64 columns), the tiles running fastest, of
+// which two CTAs an SM (one for more than 64 ranks) take equal runs, however many units
+// the plan has; warp 0 prepares the next unit of a run while the last one's tiles are
+// finished. CTAs dealt out by the number of units that there may be took 258 us instead of
+// 160 for 16384 mixed rows of 32 adapters, 4096 x 6144 (one CTA a unit: half of the GPU),
+// 51 and 48 for 8192 rows of 16, and 24.0 and 25.5 for 700 of 32.
+// Warps: 0 loads the image and Q, 1 issues the MMAs, 2 to 5 finish every second tile and 6
+// to 9 the others: base comes in by runs of 128 bytes a row, a tile ahead in registers,
+// and goes through 4 KB of shared memory a warp, in which each lane adds its row of the
+// accumulator, back into runs of 128 bytes. Bound by base and out, and by the instructions
+// of that way: 8192 rows of 4096, r = 16, take 28 us, 4.8 TB/s; 16384, r = 64, 50 us, 5.4
+// TB/s. Launched beside the shrink kernel (as far as its results let it) both were slower,
+// 58 us against 51 for the 8192: its CTAs take the room in which shrink's next ones start.
 constexpr int kCols = 64;
 constexpr int kPiece = 32 * 128;
 constexpr int kExpandThreads = 320;
@@ -566,12 +585,21 @@ struct Expand {
   static constexpr int kBytes = 1024 + kImg + kStages * kQ + 8 * kPiece;
 };
 
+// Where the items of CTA b of all begin. Tensors that fit in memory have fewer than 2^32.
+__device__ __forceinline__ uint32_t items_begin(uint32_t items, uint32_t all, uint32_t b) {
+  return items / all * b + min(b, items % all);
+}
+
+// What a CTA does of one unit: steps tiles from t0 on.
+struct Part { int unit, a, rows, t0, steps; };
+
 struct ExpandArgs {
   const uint8_t* img;
   int parts;                      // of the image; the first two are used
   const __nv_bfloat16* base;      // or NULL
   __nv_bfloat16* out;
   int N;
+  int units;                      // that the images have room for
   unsigned long long wait_ns;
   Plan plan;
 };
@@ -581,7 +609,9 @@ __global__ void __launch_bounds__(kExpandThreads, R > 64 ? 1 : 2)
     expand_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ ExpandArgs p) {
   using S = Expand<R>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ int rows[kRows];
+  __shared__ int rows_of[2][kRows];               // of this part and of the next
+  __shared__ Part parts[2];
+  __shared__ uint32_t at, past;                   // items that no part has yet
   __shared__ uint64_t full[S::kStages], empty[S::kStages], tfull[kExpandAcc], tempty[kExpandAcc],
       image;
   __shared__ uint32_t tmem_at;
@@ -589,27 +619,36 @@ __global__ void __launch_bounds__(kExpandThreads, R > 64 ? 1 : 2)
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int unit = static_cast<int>(blockIdx.x);
-  const Unit u = find_unit(p.plan, unit);
-  const bool none = u.a == p.plan.n;
-  if (u.rows == 0 || (none && p.base == p.out)) return;   // nothing, or base stays as it is
-  if (tid < kRows) rows[tid] = tid < u.rows ? checked_row(p.plan, __ldg(p.plan.order + u.lo + tid)) : -1;
-  if (none) {                                    // base as it is, or zeros
-    __syncthreads();
-    const int nv = p.N / 8;
-    for (int row = blockIdx.y; row < u.rows; row += gridDim.y) {
-      if (rows[row] < 0) continue;
-      const int64_t at = static_cast<int64_t>(rows[row]) * p.N;
-      for (int c = tid; c < nv; c += kExpandThreads)
-        reinterpret_cast<uint4*>(p.out + at)[c] =
-            p.base ? reinterpret_cast<const uint4*>(p.base + at)[c] : make_uint4(0, 0, 0, 0);
+  const uint32_t tiles = (p.N + kCols - 1) / kCols;
+  // the next part, by warp 0; no steps: there is none
+  auto prepare = [&](int k) {
+    if (at >= past) {
+      if (lane == 0) parts[k].steps = 0;
+      return;
     }
-    return;
+    const uint32_t unit = at / tiles, t0 = at - unit * tiles, steps = min(tiles - t0, past - at);
+    const Unit u = find_unit(p.plan, static_cast<int>(unit));
+#pragma unroll
+    for (int r = 0; r < kRows; r += 32)
+      rows_of[k][r + lane] =
+          r + lane < u.rows ? checked_row(p.plan, __ldg(p.plan.order + u.lo + r + lane)) : -1;
+    __syncwarp();
+    if (lane == 0) {
+      parts[k] = {static_cast<int>(unit), u.a, u.rows, static_cast<int>(t0), static_cast<int>(steps)};
+      at += steps;
+    }
+  };
+  if (warp == 0) {
+    // in place the rows without an adapter stay as they are; the plan's offsets may overlap
+    const uint32_t items = min(count_units(p.plan, p.base != p.out), p.units) * tiles;
+    if (lane == 0) {
+      at = items_begin(items, gridDim.x, blockIdx.x);
+      past = items_begin(items, gridDim.x, blockIdx.x + 1);
+    }
+    __syncwarp();
+    prepare(0);
   }
-  const int tiles = (p.N + kCols - 1) / kCols;
-  const int t0 = blockIdx.y, dt = gridDim.y;
-  const int steps = t0 < tiles ? (tiles - t0 + dt - 1) / dt : 0;
-  if (tid == 0) {
+  if (tid == 64) {
     for (int s = 0; s < S::kStages; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
       mbar_init(smem_u32(&empty[s]), 1);
@@ -634,127 +673,161 @@ __global__ void __launch_bounds__(kExpandThreads, R > 64 ? 1 : 2)
   volatile int* stopped = &stop;
   bool ok = true;
 
-  if (warp == 0) {
-    if (lane == 0) {
-      int i = 0;
-      for (; i < steps; ++i) {
-        const int s = i % S::kStages;
-        ok = mbar_wait(smem_u32(&empty[s]), ((i / S::kStages) & 1) ^ 1, p.wait_ns, stopped);
-        if (!ok) break;
-        mbar_arrive_expect_tx(smem_u32(&full[s]), S::kQ);
-        tma_load_3d(q0 + s * S::kQ, &map_q, smem_u32(&full[s]), (t0 + i * dt) * kCols, 0, u.a);
-        if (i == 0) {
-          mbar_arrive_expect_tx(smem_u32(&image), S::kImg);
-          const uint8_t* src = p.img + static_cast<int64_t>(unit) * atoms(p.parts, R) * kAtom;
-          for (int k = 0; k < S::kImg / kAtom; ++k)
-            for (int h = 0; h < 2; ++h)          // rows of the unit's halves
-              bulk_copy_g2s(img0 + k * kAtom + h * (kAtom / 2),
-                            src + (h * atoms(p.parts, R) + k) * (kAtom / 2), kAtom / 2,
-                            smem_u32(&image));
+  int before = 0;                                // steps of the units before, and their number
+  for (uint32_t turn = 0, units = 0; parts[turn & 1].steps > 0; ++turn) {
+    const int* rows = rows_of[turn & 1];
+    const Part& u = parts[turn & 1];
+    const int steps = u.steps, t0 = u.t0;
+    if (u.a == p.plan.n) {                       // base as it is, or zeros
+      for (int i = warp; i < u.rows; i += kExpandThreads / 32) {
+        if (rows[i] < 0) continue;
+        const int64_t at = static_cast<int64_t>(rows[i]) * (p.N / 8);
+        for (int e = lane; e < steps * (kCols / 8); e += 32) {
+          const int c = t0 * (kCols / 8) + e;
+          if (c < p.N / 8)
+            reinterpret_cast<uint4*>(p.out)[at + c] =
+                p.base ? reinterpret_cast<const uint4*>(p.base)[at + c] : make_uint4(0, 0, 0, 0);
         }
       }
-      for (int k = i > S::kStages ? i - S::kStages : 0; k < i; ++k)
-        mbar_wait(smem_u32(&full[k % S::kStages]), (k / S::kStages) & 1, kDrainNs, &zero);
-    }
-  } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t idesc = idesc_bf16(128, kCols, false, true);
-      ok = steps == 0 || mbar_wait(smem_u32(&image), 0, p.wait_ns, stopped);
-      for (int i = 0; i < steps && ok; ++i) {
-        const int s = i % S::kStages, a = i % kExpandAcc;
-        ok = mbar_wait(smem_u32(&tempty[a]), ((i / kExpandAcc) & 1) ^ 1, p.wait_ns, stopped) &&
-             mbar_wait(smem_u32(&full[s]), (i / S::kStages) & 1, p.wait_ns, stopped);
+    } else if (warp == 0) {
+      if (lane == 0) {
+        int i = before;
+        for (; i < before + steps; ++i) {
+          const int s = i % S::kStages;
+          ok = mbar_wait(smem_u32(&empty[s]), ((i / S::kStages) & 1) ^ 1, p.wait_ns, stopped);
+          if (!ok) break;
+          mbar_arrive_expect_tx(smem_u32(&full[s]), S::kQ);
+          tma_load_3d(q0 + s * S::kQ, &map_q, smem_u32(&full[s]), (t0 + i - before) * kCols, 0, u.a);
+          if (i == before) {                     // the last unit's MMAs have read their image
+            mbar_arrive_expect_tx(smem_u32(&image), S::kImg);
+            const uint8_t* src = p.img + static_cast<int64_t>(u.unit) * atoms(p.parts, R) * kAtom;
+            for (int k = 0; k < S::kImg / kAtom; ++k)
+              for (int h = 0; h < 2; ++h)        // rows of the unit's halves
+                bulk_copy_g2s(img0 + k * kAtom + h * (kAtom / 2),
+                              src + (h * atoms(p.parts, R) + k) * (kAtom / 2), kAtom / 2,
+                              smem_u32(&image));
+          }
+        }
+        for (int k = i > S::kStages ? i - S::kStages : 0; k < i; ++k)
+          mbar_wait(smem_u32(&full[k % S::kStages]), (k / S::kStages) & 1, kDrainNs, &zero);
+      }
+    } else if (warp == 1) {
+      if (lane == 0) {
+        const uint32_t idesc = idesc_bf16(128, kCols, false, true);
+        ok = mbar_wait(smem_u32(&image), units & 1, p.wait_ns, stopped);
+        for (int i = before; i < before + steps && ok; ++i) {
+          const int s = i % S::kStages, a = i % kExpandAcc;
+          ok = mbar_wait(smem_u32(&tempty[a]), ((i / kExpandAcc) & 1) ^ 1, p.wait_ns, stopped) &&
+               mbar_wait(smem_u32(&full[s]), (i / S::kStages) & 1, p.wait_ns, stopped);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t bd = sdesc_sw128(q0 + s * S::kQ, S::kQ, 1024);
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int ks = 0; ks < R / 16; ++ks) {
+              const int at = k * (R / 16) + ks;  // of the image's columns, in 16s
+              const uint64_t ad = sdesc_sw128(img0 + (at >> 2) * kAtom, 16, 1024) + (at & 3) * 2;
+              umma_bf16(tmem + a * kCols, ad, bd + ks * (2048 >> 4), idesc, (k | ks) ? 1u : 0u);
+            }
+          umma_commit(smem_u32(&empty[s]));
+          umma_commit(smem_u32(&tfull[a]));
+        }
+      }
+    } else {
+      const int q = warp & 3, half = (warp - 2) >> 2;
+      uint8_t* st = smem + S::kImg + S::kStages * S::kQ + (warp - 2) * kPiece;
+      const int ch = lane & 7, r0 = lane >> 3;   // of the runs: rows r0, r0 + 4, ... of 32
+      const int end = before + steps, first = before + ((half ^ before) & 1);
+      // rows and a bit for each that is there; where its run begins is one product away
+      uint32_t g[8], here = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int row = rows[q * 32 + r0 + 4 * j];
+        g[j] = row < 0 ? 0 : row;
+        here |= row < 0 ? 0 : 1u << j;
+      }
+      const uint32_t pitch = static_cast<uint32_t>(p.N) * 2;
+      auto at = [&](int j) { return static_cast<uint64_t>(g[j]) * pitch; };
+      const bool any = __any_sync(0xffffffffu, rows[q * 32 + lane] >= 0);
+      uint4 next[8];
+      auto load = [&](int i) {                   // base of step i
+        const int col = (t0 + i - before) * kCols + ch * 8;
+        const uint8_t* src = reinterpret_cast<const uint8_t*>(p.base) + static_cast<int64_t>(col) * 2;
+        const uint32_t on = p.base && i < end && col < p.N ? here : 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          next[j] = on & (1u << j) ? __ldcs(reinterpret_cast<const uint4*>(src + at(j)))
+                                   : make_uint4(0, 0, 0, 0);
+      };
+      load(first);
+      for (int i = first; i < end; i += 2) {
+        const int a = i % kExpandAcc;
+        if (any) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int row = r0 + 4 * j;
+            *reinterpret_cast<uint4*>(st + row * 128 + ((ch ^ (row & 7)) << 4)) = next[j];
+          }
+          __syncwarp();
+          load(i + 2);
+        }
+        const bool got = mbar_wait(smem_u32(&tfull[a]), (i / kExpandAcc) & 1, p.wait_ns, stopped);
+        ok = __all_sync(0xffffffffu, got);
         if (!ok) break;
         tc_fence_after();
-        const uint64_t bd = sdesc_sw128(q0 + s * S::kQ, S::kQ, 1024);
+        const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + a * kCols;
+        if (any) {                               // else no row of the quarter is there
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
+          for (int c0 = 0; c0 < 8; c0 += 2) {
+            uint32_t v[16];
+            tmem_ld_32x32b_x16(taddr + c0 * 8, v);
+            tmem_ld_wait();
 #pragma unroll
-          for (int ks = 0; ks < R / 16; ++ks) {
-            const int at = k * (R / 16) + ks;      // of the image's columns, in 16s
-            const uint64_t ad = sdesc_sw128(img0 + (at >> 2) * kAtom, 16, 1024) + (at & 3) * 2;
-            umma_bf16(tmem + a * kCols, ad, bd + ks * (2048 >> 4), idesc, (k | ks) ? 1u : 0u);
+            for (int c = 0; c < 2; ++c) {
+              uint4* w = reinterpret_cast<uint4*>(st + lane * 128 + (((c0 + c) ^ (lane & 7)) << 4));
+              const uint4 o = *w;
+              const float* x = reinterpret_cast<const float*>(v + c * 8);
+              *w = make_uint4(pack_bf16x2(x[0] + lo_f(o.x), x[1] + hi_f(o.x)),
+                              pack_bf16x2(x[2] + lo_f(o.y), x[3] + hi_f(o.y)),
+                              pack_bf16x2(x[4] + lo_f(o.z), x[5] + hi_f(o.z)),
+                              pack_bf16x2(x[6] + lo_f(o.w), x[7] + hi_f(o.w)));
+            }
           }
-        umma_commit(smem_u32(&empty[s]));
-        umma_commit(smem_u32(&tfull[a]));
-      }
-    }
-  } else {
-    const int q = warp & 3, half = (warp - 2) >> 2;
-    uint8_t* st = smem + S::kImg + S::kStages * S::kQ + (warp - 2) * kPiece;
-    const int ch = lane & 7, r0 = lane >> 3;     // of the runs: rows r0, r0 + 4, ... of 32
-    int g[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) g[j] = rows[q * 32 + r0 + 4 * j];
-    const bool any = __any_sync(0xffffffffu, rows[q * 32 + lane] >= 0);
-    uint4 next[8];
-    auto load = [&](int i) {                     // base of step i
-      const int col = (t0 + i * dt) * kCols + ch * 8;
-      const bool here = p.base && i < steps && col < p.N;
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        next[j] = here && g[j] >= 0
-                      ? __ldcs(reinterpret_cast<const uint4*>(p.base + static_cast<int64_t>(g[j]) * p.N + col))
-                      : make_uint4(0, 0, 0, 0);
-    };
-    load(half);
-    for (int i = half; i < steps; i += 2) {
-      const int a = i % kExpandAcc;
-      if (any) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int row = r0 + 4 * j;
-          *reinterpret_cast<uint4*>(st + row * 128 + ((ch ^ (row & 7)) << 4)) = next[j];
         }
+        tc_fence_before();
         __syncwarp();
-        load(i + 2);
-      }
-      const bool got = mbar_wait(smem_u32(&tfull[a]), (i / kExpandAcc) & 1, p.wait_ns, stopped);
-      ok = __all_sync(0xffffffffu, got);
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + a * kCols;
-      if (any) {                                 // else no row of the quarter is there
+        if (lane == 0) mbar_arrive(smem_u32(&tempty[a]));
+        const int col = (t0 + i - before) * kCols + ch * 8;
+        uint8_t* to = reinterpret_cast<uint8_t*>(p.out) + static_cast<int64_t>(col) * 2;
+        if (any && col < p.N) {
 #pragma unroll
-        for (int c0 = 0; c0 < 8; c0 += 2) {
-          uint32_t v[16];
-          tmem_ld_32x32b_x16(taddr + c0 * 8, v);
-          tmem_ld_wait();
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint4* w = reinterpret_cast<uint4*>(st + lane * 128 + (((c0 + c) ^ (lane & 7)) << 4));
-            const uint4 o = *w;
-            const float* x = reinterpret_cast<const float*>(v + c * 8);
-            *w = make_uint4(pack_bf16x2(x[0] + lo_f(o.x), x[1] + hi_f(o.x)),
-                            pack_bf16x2(x[2] + lo_f(o.y), x[3] + hi_f(o.y)),
-                            pack_bf16x2(x[4] + lo_f(o.z), x[5] + hi_f(o.z)),
-                            pack_bf16x2(x[6] + lo_f(o.w), x[7] + hi_f(o.w)));
+          for (int j = 0; j < 8; ++j) {
+            const int row = r0 + 4 * j;
+            if (here & (1u << j))
+              __stcs(reinterpret_cast<uint4*>(to + at(j)),
+                     *reinterpret_cast<const uint4*>(st + row * 128 + ((ch ^ (row & 7)) << 4)));
           }
         }
+        __syncwarp();                            // the piece may be filled again
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&tempty[a]));
-      const int col = (t0 + i * dt) * kCols + ch * 8;
-      if (any && col < p.N) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int row = r0 + 4 * j;
-          if (g[j] >= 0)
-            __stcs(reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(g[j]) * p.N + col),
-                   *reinterpret_cast<const uint4*>(st + row * 128 + ((ch ^ (row & 7)) << 4)));
-        }
-      }
-      __syncwarp();                              // the piece may be filled again
     }
+    if (warp == 0) {
+      __syncwarp();
+      prepare((turn + 1) & 1);
+    }
+    if (u.a != p.plan.n) {
+      before += steps;
+      ++units;
+    }
+    if (!ok) {
+      stop = 1;
+      report_error(p.plan.err, kErrTimeout);
+      if (warp == 1 && lane == 0) mbar_wait(smem_u32(&image), (units - 1) & 1, kDrainNs, &zero);
+    }
+    tc_fence_before();
+    if (__syncthreads_or(!ok)) break;            // every tile of the part has been finished
   }
-  if (!ok) {
-    stop = 1;
-    report_error(p.plan.err, kErrTimeout);
-    if (warp == 1 && lane == 0) mbar_wait(smem_u32(&image), 0, kDrainNs, &zero);
-  }
-  tc_fence_before();
-  __syncthreads();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, kExpandAcc * kCols);
@@ -1397,14 +1470,9 @@ cudaError_t expand(const __nv_bfloat16* Q, int r, ExpandArgs p, cudaStream_t st)
   static bool configured[kMaxDevices] = {};
   CUtensorMap map;
   if (!make_tmap_bf16_3d(&map, Q, p.N, r, p.plan.n, 64, R)) return cudaErrorInvalidValue;
-  const int64_t units = max_units(p.plan.T, p.plan.n);
-  const int tiles = (p.N + kCols - 1) / kCols;
-  // CTAs to a unit: as many as two an SM take at once, each with four tiles at least (the
-  // same 300 rows: 18 us, 53 with one CTA a unit)
-  int split = 1;
-  while (tiles / (split + 1) >= 4 && units * (split + 1) <= 2 * device_sm_count()) ++split;
+  p.units = static_cast<int>(max_units(p.plan.T, p.plan.n));
   p.wait_ns = kDefaultWaitNs;
-  return launch(expand_kernel<R>, dim3(static_cast<unsigned>(units), split), kExpandThreads,
+  return launch(expand_kernel<R>, dim3(device_sm_count() * (R > 64 ? 1 : 2)), kExpandThreads,
                 Expand<R>::kBytes, 1, false, configured, st, map, p);
 }
 

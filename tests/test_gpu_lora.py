@@ -114,6 +114,31 @@ def test_lora_integers(T, H, N, n, r, kind):
             assert np.array_equal(_np(more[key]), want[key] + 2.0), key
 
 
+# more units of rows than CTAs, and few enough that a CTA's run goes over two of them: by
+# adapters, at their ends and where the rows without one begin
+@pytest.mark.parametrize("T,H,N,n,r,kind", [(40000, 16, 136, 3, 4, "mixed"),
+                                            (22000, 32, 2056, 20, 8, "mixed"),
+                                            (20000, 64, 1032, 5, 100, "mixed"),
+                                            (21000, 8, 1544, 300, 5, "runs"),
+                                            (30000, 16, 520, 2, 16, "none")])
+def test_lora_many_units(T, H, N, n, r, kind):
+    v, ids, scales, base, _, _ = _draw(T, H, N, n, r, kind, T + r, True)
+    rows = ids.cpu().numpy()
+    plan = m.moe_lora_plan(ids, n)
+    n64 = {k: _np(t) for k, t in v.items()}
+    for bs in (base, None):
+        ref, rv = orc.lora(**n64, ids=rows, scales=_np(scales), base=None if bs is None else _np(bs))
+        want = torch.from_numpy(ref).float().to(BF)
+        out = torch.full((T, N), float("nan"), dtype=BF, device="cuda")
+        got = m.moe_lora(**v, adapter_ids=ids, plan=plan, scales=scales, base=bs, out=out)
+        assert np.array_equal(_np(got["v"]), rv) and torch.equal(out.cpu(), want)
+    held = base.clone()
+    m.moe_lora(**v, adapter_ids=ids, plan=plan, scales=scales, base=held, out=held)
+    want = orc.lora(**n64, ids=rows, scales=_np(scales), base=_np(base))[0]
+    assert torch.equal(held.cpu(), torch.from_numpy(want).float().to(BF))
+    assert m.moe_get_error() == 0
+
+
 @pytest.mark.parametrize("T,H,N,n,r,kind", [(3, 1000, 264, 4, 16, "mixed"),
                                             (100, 512, 328, 6, 24, "mixed"),
                                             (400, 1032, 200, 3, 64, "runs"),
