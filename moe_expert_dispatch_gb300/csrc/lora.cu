@@ -1508,11 +1508,17 @@ moe_status check_sizes(int64_t T, int H, int N, int n, int r) {
   return (H % 8 || N % 8 || r > kMaxRank || T > kMaxRows) ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
 
-// The rows that one cluster each takes without a plan: every row reads its adapter
-// whole, which the rows of a unit share otherwise. Measured with 32 adapters over 4096 x
-// 4096, by clusters and by units: r = 16, 128 rows 11 and 21 us, 256 19 and 21, 512 34 and
-// 21; r = 64, 128 rows 20 and 32, 256 36 and 33.
-bool few_rows(int64_t T, int r) { return T <= 256 && T * r <= 8192; }
+// Whether one cluster takes each row, without a plan: every row then reads its adapter
+// whole, which the rows of a unit share otherwise, but a unit costs as much for one row as
+// for 128. In units of 2 ns at 4096 x 4096 a row takes 25 + r, the two launches 6000 + 100
+// r and a unit 135, and there is one to an adapter at least. Measured by clusters and by
+// units: r = 16 and 32 adapters, 128 rows 11 and 22 us, 256 20 and 23, 512 35 and 23; 128
+// adapters, 512 rows 36 and 46, 1024 68 and 48; 512 adapters, 1024 rows 76 and 146, 4096
+// 289 and 166; r = 64 and 32 adapters, 128 rows 20 and 34, 256 36 and 34; and of 4096 x
+// 14336 with r = 16, 128 adapters, 512 rows 52 and 87, 1024 98 and 93.
+bool few_rows(int64_t T, int n, int r) {
+  return T * (25 + r) <= 6000 + 100 * r + 135 * (T < n ? T : n);
+}
 
 // What the backward has in its workspace.
 struct BwdLayout {
@@ -1562,7 +1568,7 @@ moe_status moe_lora_plan(const int32_t* adapter_ids, int64_t T, int n, int32_t* 
 }
 
 size_t moe_lora_workspace_size(int64_t T, int n, int r) {
-  if (check_sizes(T, 8, 8, n, r) != MOE_OK || T == 0 || few_rows(T, r)) return 0;
+  if (check_sizes(T, 8, 8, n, r) != MOE_OK || T == 0 || few_rows(T, n, r)) return 0;
   return up256(image_bytes(T, n, r, 2));
 }
 
@@ -1583,7 +1589,7 @@ moe_status moe_lora(const void* x, const void* a, const void* b, const int32_t* 
   const auto* bb = static_cast<const __nv_bfloat16*>(b);
   const auto* yb = static_cast<const __nv_bfloat16*>(base);
   auto* ob = static_cast<__nv_bfloat16*>(out);
-  if (few_rows(T, r)) {
+  if (few_rows(T, n, r)) {
     static bool configured[kMaxDevices] = {};
     return launch(few_kernel, dim3(static_cast<unsigned>(T) * kFewCtas), kFewThreads,
                   kFewAhead, kFewCtas,

@@ -57,7 +57,10 @@ CASES = [(1, 64, 64, 1, 1, "one"), (1, 4096, 4096, 8, 16, "mixed"), (2, 8, 8, 3,
          (700, 328, 392, 1, 48, "one"), (1500, 200, 136, 6, 16, "mixed"),
          # whole units of rows that follow one another, and few rows up to their bound
          (900, 264, 392, 2, 64, "runs"), (600, 136, 200, 1, 128, "one"), (700, 72, 64, 1, 32, "one"),
-         (256, 72, 2056, 9, 32, "mixed"), (129, 1000, 72, 300, 2, "mixed")]
+         (256, 72, 2056, 9, 32, "mixed"), (129, 1000, 72, 300, 2, "mixed"),
+         # many adapters of a few rows each, and as few as units still take
+         (500, 72, 136, 200, 8, "mixed"), (900, 64, 72, 500, 5, "runs"),
+         (700, 136, 64, 60, 64, "mixed"), (150, 64, 328, 1, 128, "one")]
 
 
 @pytest.mark.parametrize("T,n,kind", [(0, 3, "mixed"), (1, 1, "one"), (31, 5, "mixed"),
