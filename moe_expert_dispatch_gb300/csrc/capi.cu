@@ -354,17 +354,17 @@ bool make_tmap_scale_rows(CUtensorMap* map, const void* base, uint64_t bytes) {
 }
 
 bool make_out_tmap(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,
-                   uint64_t row_stride_bytes, bool f32) {
+                   uint64_t row_stride_bytes, bool f32, bool wide) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t dims[2] = {inner, outer};
   const cuuint64_t strides[1] = {row_stride_bytes};
-  const cuuint32_t box[2] = {f32 ? 16u : 32u, 32u};   // one epilogue warp's 32 rows
+  const cuuint32_t box[2] = {(f32 ? 16u : 32u) * (wide ? 2 : 1), 32u};   // one epilogue warp's 32 rows
   const cuuint32_t estr[2] = {1, 1};
   return fn(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
             const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+            wide ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace moe

@@ -86,7 +86,8 @@ constexpr size_t smem_bytes() {
   return 1024 + static_cast<size_t>(stages<op>()) * kStageBytes + pieces_bytes<op>() + sizeof(Smem);
 }
 static_assert(smem_bytes<Op::Gated>() <= 232448 && smem_bytes<Op::Down>() <= 232448 &&
-              smem_bytes<Op::GatedBwd>() <= 232448, "shared memory of one CTA");
+              smem_bytes<Op::GatedBwd>() <= 232448 && smem_bytes<Op::Joint>() <= 232448,
+              "shared memory of one CTA");
 
 // Operands by kind: Main a[0], b[0] (a[1], b[1]: W_up, or dA_u with W_up), the
 // weight gradients from [2] on.
@@ -441,6 +442,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ++npiece;
     };
+    // The same of 128 bytes a row, by both slots: chunk j of row r at chunk j ^ (r & 7).
+    // Weight gradients, which follow all other pieces of a cluster, leave so: with few
+    // rows they are bound by these stores (the gradients of 64 rows of 4096 x 14336 take
+    // 161 us, by pieces of 64 bytes a row 168; two such places and a stage less 161).
+    auto put_wide = [&](const uint32_t* w, const CUtensorMap* map, int x, int y, bool add) {
+      if (lane == 0) bulk_wait_group_read<0>();
+      __syncwarp();
+      const uint32_t slot = out0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(slot + lane * 128 +
+                                                                     ((j ^ (lane & 7)) << 4)),
+                     "r"(w[4 * j]), "r"(w[4 * j + 1]), "r"(w[4 * j + 2]), "r"(w[4 * j + 3])
+                     : "memory");
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) {
+        if (add) tma_reduce_add_2d(map, slot, x, y);
+        else tma_store_2d(map, slot, x, y);
+        bulk_commit_group();
+      }
+    };
     auto put_rounded = [&](const uint32_t* v, const CUtensorMap* map, int x, int y) {
       uint32_t w[16];
 #pragma unroll
@@ -497,8 +520,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_after();
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * BN;
+      if (op == Op::Joint && !main) {
+        const int wide = p.f32 ? 32 : 64;      // columns of a piece
 #pragma unroll 1
-      for (int c = c_first; c < cols; c += 64) {
+        for (int c = (e >> 2) * wide; c < cols; c += 2 * wide) {
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(taddr + c, v);
+          if (!p.f32) {
+            uint32_t more[32];
+            tmem_ld_32x32b_x32(taddr + c + 32, more);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              v[j] = pack_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+              more[j] = pack_bf16x2(__uint_as_float(more[2 * j]), __uint_as_float(more[2 * j + 1]));
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[16 + j] = more[j];
+          } else {
+            tmem_ld_wait();
+          }
+          put_wide(v, &maps.out[u.kind], n0 + c, y, p.accumulate != 0);
+        }
+      }
+#pragma unroll 1
+      for (int c = op == Op::Joint && !main ? cols : c_first; c < cols; c += 64) {
         uint32_t v[32], a[16], b[16];
         if (reads) {
           const bool here = mbar_wait(in_bar, n_got & 1, p.wait_ns, abort_flag);
@@ -542,10 +588,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           put(h, &maps.out[0], n0 + c, y, false);
           put(a, &maps.out[1], n0 + c, y, false);
           put(b, &maps.out[2], n0 + c, y, false);
-        } else if (!main && p.f32) {
-          tmem_ld_wait();
-          put(v, &maps.out[u.kind], n0 + c, y, p.accumulate != 0);
-          if (c + 16 < cols) put(v + 16, &maps.out[u.kind], n0 + c + 16, y, p.accumulate != 0);
         } else {
           tmem_ld_wait();
           if (reads)
@@ -554,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               v[2 * j] = __float_as_uint(__uint_as_float(v[2 * j]) + lo_f(a[j]));
               v[2 * j + 1] = __float_as_uint(__uint_as_float(v[2 * j + 1]) + hi_f(a[j]));
             }
-          put_rounded(v, &maps.out[u.kind], n0 + c, y);
+          put_rounded(v, &maps.out[kMain], n0 + c, y);
         }
       }
       if (!ok) break;
@@ -1056,11 +1098,13 @@ moe_status moe_gated_ffn_backward(const void* dy, const void* x, const void* w_g
   if (dw_gate) {
     const uint64_t z = f32 ? 4 : 2;
     if (!in_map(&mj.a[2], h, F, T, BK) || !in_map(&mj.b[1 + kDwDown], dy, H, T, BK) ||
-        !make_out_tmap(&mj.out[kDwDown], dw_down, H, F, static_cast<uint64_t>(H) * z, f32) ||
+        !make_out_tmap(&mj.out[kDwDown], dw_down, H, F, static_cast<uint64_t>(H) * z, f32,
+                       true) ||
         !in_map(&mj.a[3], x, H, T, BK) || !in_map(&mj.b[1 + kDwGate], da_g, F, T, BK) ||
         !in_map(&mj.b[1 + kDwUp], da_u, F, T, BK) ||
-        !make_out_tmap(&mj.out[kDwGate], dw_gate, F, H, static_cast<uint64_t>(F) * z, f32) ||
-        !make_out_tmap(&mj.out[kDwUp], dw_up, F, H, static_cast<uint64_t>(F) * z, f32))
+        !make_out_tmap(&mj.out[kDwGate], dw_gate, F, H, static_cast<uint64_t>(F) * z, f32,
+                       true) ||
+        !make_out_tmap(&mj.out[kDwUp], dw_up, F, H, static_cast<uint64_t>(F) * z, f32, true))
       return MOE_ERR_CUDA;
     pj.down = b.down;
     pj.gate = b.gate;

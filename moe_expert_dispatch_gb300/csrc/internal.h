@@ -179,9 +179,9 @@ struct GemmOut {
   CUtensorMap map[3];
 };
 // A 2D output map over a row-major [outer, inner] tensor of bf16 (f32 = false)
-// or float elements.
+// or float elements; wide: boxes of 128 bytes a row, with the 128-byte swizzle.
 bool make_out_tmap(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,
-                   uint64_t row_stride_bytes, bool f32);
+                   uint64_t row_stride_bytes, bool f32, bool wide = false);
 
 // fc1: out = bf16(silu(A W_gate) * (A W_up)), A rows tiled per expert.
 // Outputs: h (map 0) and, with save_g, A_g and A_u as blocks (save_g, save_u).
