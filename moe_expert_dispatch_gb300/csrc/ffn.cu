@@ -763,9 +763,10 @@ int pick_split(const Grid& g, int kb) {
 // of a cluster: a tile costs its own and some 8 more; the clusters without a unit of dx
 // take gradient tiles meanwhile, as unit_at deals them out, and all of them the rest. The
 // kernel that adds the parts up costs about 9, and their way out and in again one for
-// three parts. Measured, split and not: 160 rows of 1024 x 8192 58 and 115 us, 512 rows
-// of 2048 x 8192 100 and 111; not worth it where the gradients are the most of it or a
-// split needs another round, 256 rows of 2048 x 768 27 and 24, 2048 of 512 x 2048 45 and 39.
+// three parts. Measured, split and not: 160 rows of 1024 x 8192 50 and 98 us, 1024 rows 96
+// and 111, 512 rows of 2048 x 8192 100 and 110; not worth it where the gradients are the
+// most of it or a split needs another round, 256 rows of 2048 x 768 27 (in two) and 25,
+// 2048 of 512 x 2048 45 (in two) and 40.
 constexpr int kTileCost = 8;
 int pick_split_joint(const Grid& g, int kb, int64_t dw_units, int kb_rows) {
   if (dw_units == 0) return pick_split(g, kb);

@@ -571,7 +571,7 @@ __global__ void __launch_bounds__(Shrink<R>::kThreads, R > 64 ? 1 : 2)
 // accumulator, back into runs of 128 bytes. Bound by base and out, and by the instructions
 // of that way: 8192 rows of 4096, r = 16, take 28 us, 4.8 TB/s; 16384, r = 64, 50 us, 5.4
 // TB/s. Launched beside the shrink kernel (as far as its results let it) both were slower,
-// 58 us against 51 for the 8192: its CTAs take the room in which shrink's next ones start.
+// the 8192 53 us in all against 49: its CTAs take the room in which shrink's next ones start.
 constexpr int kCols = 64;
 constexpr int kPiece = 32 * 128;
 constexpr int kExpandThreads = 320;
