@@ -821,7 +821,8 @@ moe_status moe_lora_plan(const int32_t* adapter_ids, int64_t T, int n, int32_t* 
  *  adapter_ids, order, offsets: as moe_lora_plan took and wrote them. A row
  *          number outside [0, T) or offsets that do not grow from 0 to at most T
  *          are never followed; the result is then none, and
- *          MOE_ERR_BAD_EXPERT_ID is raised
+ *          MOE_ERR_BAD_EXPERT_ID is raised. Few rows (those without a workspace)
+ *          go by adapter_ids alone
  *  scales  float [n] or NULL: s_a, or 1
  *  base    bf16 [T, N] or NULL (0): the projection's result
  *  out     bf16 [T, N]   out; may be base itself

@@ -60,7 +60,11 @@ CASES = [(1, 64, 64, 1, 1, "one"), (1, 4096, 4096, 8, 16, "mixed"), (2, 8, 8, 3,
          (256, 72, 2056, 9, 32, "mixed"), (129, 1000, 72, 300, 2, "mixed"),
          # many adapters of a few rows each, and as few as units still take
          (500, 72, 136, 200, 8, "mixed"), (900, 64, 72, 500, 5, "runs"),
-         (700, 136, 64, 60, 64, "mixed"), (150, 64, 328, 1, 128, "one")]
+         (700, 136, 64, 60, 64, "mixed"), (150, 64, 328, 1, 128, "one"),
+         # few rows of long and short widths, of one adapter, of many and of none
+         (64, 264, 520, 2, 13, "runs"), (65, 264, 520, 2, 13, "runs"), (66, 72, 64, 1, 1, "one"),
+         (67, 4096, 8, 3, 16, "mixed"), (100, 136, 72, 3, 128, "mixed"), (90, 8, 4104, 80, 5, "mixed"),
+         (99, 64, 2056, 4, 33, "none")]
 
 
 @pytest.mark.parametrize("T,n,kind", [(0, 3, "mixed"), (1, 1, "one"), (31, 5, "mixed"),
@@ -286,6 +290,21 @@ def test_lora_bad_ids_and_plans(T):
         assert m.moe_get_error() == 3, (where, value)
         m.moe_lora_backward(dy, v["x"], f["v"], v["a"], v["b"], ids, plan=(order, o))
         assert m.moe_get_error() == 3, (where, value)
+
+
+def test_lora_few_rows_go_by_their_ids():
+    T = 100                                        # the plan is not read: nothing of it counts
+    v, ids, scales, base, _, _ = _draw(T, 64, 72, 4, 8, "mixed", 3, True)
+    order, offsets = m.moe_lora_plan(ids, 4)
+    want = m.moe_lora(**v, adapter_ids=ids, plan=(order, offsets), base=base)
+    for where, value in ((0, T), (5, -1), (T - 1, 2 ** 31 - 1)):
+        o = order.clone()
+        o[where] = value
+        f = offsets.clone()
+        f[where % 5] = value
+        got = m.moe_lora(**v, adapter_ids=ids, plan=(o, f), base=base)
+        assert m.moe_get_error() == 0, (where, value)
+        assert torch.equal(got["out"], want["out"]) and torch.equal(got["v"], want["v"])
 
 
 @pytest.mark.parametrize("T", [30, 400])
