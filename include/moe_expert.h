@@ -771,6 +771,9 @@ moe_status moe_gated_ffn(const void* x, const void* w_gate, const void* w_up, co
  *   dA_g = bf16(dh A_u act'(A_g)),         dA_u = bf16(dh act(A_g)),
  *   dx   = bf16(add + dA_g W_gate^T + dA_u W_up^T)          (add NULL: 0)
  *   dW_down = h^T dy,  dW_gate = x^T dA_g,  dW_up = x^T dA_u (float sums)
+ * The tensor cores cut off what does not fit in their float sums. The weight
+ * gradients' are therefore taken out every 512 rows (8192 for bf16 gradients) and
+ * added up in float, which rounds: a run of 512 rows of one sign loses 2^-20 of itself.
  *
  *  dy      bf16 [T, H];  x, the weights and act: the forward's
  *  a_gate, a_up  bf16 [T, F] as the forward wrote them

@@ -16,7 +16,8 @@
 // W_gate and the other the same columns of W_up, so that the accumulator holds A_g
 // and A_u of a row in one lane. Warps: 0 the TMA producer, 1 the MMA issuer, 2 to 9
 // the epilogue (two to a quarter of the rows, taking turns at 32 columns); two
-// accumulators, so that the epilogue of a tile runs beside the MMAs of the next.
+// accumulators, so that the epilogue of a tile runs beside the MMAs of the next (or of
+// the next run of rows of a weight gradient).
 //
 // Nothing is padded: rows and columns past the matrices are the zeros that TMA
 // fills in, they add nothing, and the stores are clipped (or, where a whole piece
@@ -56,6 +57,15 @@ constexpr int kSlots = 2;                      // pieces on their way out, of a 
 constexpr unsigned long long kDrainNs = 1000000000ull;
 constexpr unsigned long long kPairDrainNs = 50000000ull;
 constexpr int kMaxSplit = 8;
+// The tensor cores cut off what does not fit in their float sums, so that a long sum of
+// one sign ends too small: by 2^-20.1 of itself over 512 rows, 2^-14.8 over 8192, 2^-13.6
+// over 16384. A weight gradient sums over the rows; its accumulators are therefore taken out
+// every so many k-blocks and added up in registers, which round. In float every 512 rows,
+// in bf16 every 8192, where 2^-14.8 is far below its rounding. The float gradients of 8192
+// rows of 4096 x 14336 take 3743 us so (every 256 rows some 4100) and 3555 to 3680 by one
+// accumulator, those of 1024 rows 508 and 480, of 2048 rows of 2048 x 768 45 and 43.
+constexpr int kRunF32 = 8;
+constexpr int kRunBf16 = 128;
 
 // Pieces that a warp reads for 32 columns: one goes out again in its own place, two have
 // places beside those of the pieces that go out. The ring depth that 227 KB leave.
@@ -128,6 +138,7 @@ struct Args {
   int keep;                    // Gated: A_g and A_u are stored
   int add;                     // Down, Joint: in[0] is added
   int f32, accumulate;         // weight gradients
+  int run;                     // their k-blocks to an accumulator
   int* err;
   unsigned long long wait_ns;
 };
@@ -249,7 +260,10 @@ __device__ __forceinline__ void gated_bwd_any(int act, const uint32_t* dh, uint3
 
 // ------------------------------------------------------------------ the kernel
 
-template <Op op>
+// kRuns (of Joint): the rows of a weight gradient are more than one run of k-blocks. A
+// kernel of its own, because the 128 sums of a thread take all registers: in one kernel for
+// both, the gradients of 256 rows of 2048 x 768 took 25 us instead of 23.6.
+template <Op op, bool kRuns>
 __global__ void __launch_bounds__(kThreads, 1)
     dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args p) {
   extern __shared__ uint8_t smem_raw[];
@@ -376,34 +390,39 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t ad0 = sdesc_sw128(ring0, wgrad ? kBox : 16, 1024);
         const uint64_t bd0 = sdesc_sw128(ring0 + kABytes, bmn ? kBox : 16, 1024);
         const uint64_t a_step = wgrad ? 2048 >> 4 : 32 >> 4, b_step = bmn ? 2048 >> 4 : 32 >> 4;
-        if (!mbar_wait(smem_u32(&sm->tempty[acc]), acc_phase ^ 1, p.wait_ns, abort_flag)) {
-          ok = false;
-          continue;
-        }
-        tc_fence_after();
-        const uint32_t d = tmem_base + acc * BN;
-        for (int kb = u.kb0; kb < u.kb1; ++kb) {
-          if (!mbar_wait(smem_u32(&sm->full[stage]), phase, p.wait_ns, abort_flag)) {
+        // an accumulator takes up a unit's k-blocks, a weight gradient's by runs
+        for (int kb = u.kb0; ok;) {
+          const int first = kb, end = kRuns && wgrad ? min(kb + p.run, u.kb1) : u.kb1;
+          if (!mbar_wait(smem_u32(&sm->tempty[acc]), acc_phase ^ 1, p.wait_ns, abort_flag)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint64_t off = static_cast<uint64_t>(stage) * (kStageBytes >> 4);
+          const uint32_t d = tmem_base + acc * BN;
+          for (; kb < end; ++kb) {
+            if (!mbar_wait(smem_u32(&sm->full[stage]), phase, p.wait_ns, abort_flag)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t off = static_cast<uint64_t>(stage) * (kStageBytes >> 4);
 #pragma unroll
-          for (int ks = 0; ks < BK / 16; ++ks)
-            umma_bf16_pair(d, ad0 + off + ks * a_step, bd0 + off + ks * b_step, idesc,
-                           (kb > u.kb0 || ks) ? 1u : 0u);
-          umma_commit_pair_mc(smem_u32(&sm->empty[stage]), 0x3);   // the slot, in both CTAs
-          issued = true;
-          if (++stage == S) {
-            stage = 0;
-            phase ^= 1;
+            for (int ks = 0; ks < BK / 16; ++ks)
+              umma_bf16_pair(d, ad0 + off + ks * a_step, bd0 + off + ks * b_step, idesc,
+                             (kb > first || ks) ? 1u : 0u);
+            umma_commit_pair_mc(smem_u32(&sm->empty[stage]), 0x3);   // the slot, in both CTAs
+            issued = true;
+            if (++stage == S) {
+              stage = 0;
+              phase ^= 1;
+            }
           }
+          if (!ok) break;
+          umma_commit_pair_mc(smem_u32(&sm->tfull[acc]), 0x3);       // both CTAs' epilogues
+          acc ^= 1;
+          if (acc == 0) acc_phase ^= 1;
+          if (kb >= u.kb1) break;
         }
-        if (!ok) continue;
-        umma_commit_pair_mc(smem_u32(&sm->tfull[acc]), 0x3);       // both CTAs' epilogues
-        acc ^= 1;
-        if (acc == 0) acc_phase ^= 1;
       }
       if (!ok) {
         sm->abort = 1;
@@ -499,6 +518,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t acc_phase = 0;
     const uint32_t tempty0 = mapa_shared(smem_u32(&sm->tempty[0]), 0);
     bool ok = true;
+    // the next accumulator is full: tcgen05.ld is warp-collective, so the whole warp goes on
+    // or stops together
+    auto wait_full = [&]() {
+      const bool got = mbar_wait(smem_u32(&sm->tfull[acc]), acc_phase, p.wait_ns, abort_flag);
+      if (!__all_sync(0xffffffffu, got)) {
+        sm->abort = 1;
+        if (lane == 0) report_error(p.err, kErrTimeout);
+        return false;
+      }
+      tc_fence_after();
+      return true;
+    };
+    // and may be filled again
+    auto hand_back = [&]() {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(tempty0 + acc * static_cast<uint32_t>(sizeof(uint64_t)));
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1;
+    };
     for (int i = 0; ok; ++i) {
       const Unit u = units.get(i);
       if (u.kind == kNone) break;
@@ -510,17 +549,55 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int width = op == Op::Gated && !part ? BN / 2 : BN;
       const int n0 = u.n * width;
       const int cols = y >= g.M ? 0 : part ? BN : min(width, g.N - n0);   // 0: nothing to finish
-      if (reads && c_first < cols) ask(n0 + c_first, y, npiece);
-      const bool got = mbar_wait(smem_u32(&sm->tfull[acc]), acc_phase, p.wait_ns, abort_flag);
-      // tcgen05.ld is warp-collective: the whole warp goes on or stops together
-      if (!__all_sync(0xffffffffu, got)) {
-        sm->abort = 1;
-        if (lane == 0) report_error(p.err, kErrTimeout);
-        break;
+      if (kRuns && !main) {
+        // one run of k-blocks after another: columns c0 to c0 + 63 and the same 128 on,
+        // those past the matrix too
+        const int c0 = (e >> 2) * 64;
+        float sum[128];
+#pragma unroll
+        for (int j = 0; j < 128; ++j) sum[j] = 0.0f;
+        for (int kb = u.kb0; kb < u.kb1; kb += p.run) {
+          ok = wait_full();
+          if (!ok) break;
+          const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * BN + c0;
+#pragma unroll
+          for (int j = 0; j < 128; j += 32) {
+            uint32_t v[16], w[16];
+            tmem_ld_32x32b_x16(taddr + j / 64 * 128 + j % 64, v);
+            tmem_ld_32x32b_x16(taddr + j / 64 * 128 + j % 64 + 16, w);
+            tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) sum[j + k] += __uint_as_float(v[k]);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) sum[j + 16 + k] += __uint_as_float(w[k]);
+          }
+          hand_back();
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int c = c0 + i * 128;
+          uint32_t w[32];
+          if (p.f32) {
+#pragma unroll
+            for (int j = 0; j < 64; j += 32) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k) w[k] = __float_as_uint(sum[i * 64 + j + k]);
+              if (c + j < cols) put_wide(w, &maps.out[u.kind], n0 + c + j, y, p.accumulate != 0);
+            }
+          } else if (c < cols) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              w[k] = pack_bf16x2(sum[i * 64 + 2 * k], sum[i * 64 + 2 * k + 1]);
+            put_wide(w, &maps.out[u.kind], n0 + c, y, p.accumulate != 0);
+          }
+        }
+        continue;
       }
-      tc_fence_after();
+      if (reads && c_first < cols) ask(n0 + c_first, y, npiece);
+      if (!wait_full()) break;
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * BN;
-      if (op == Op::Joint && !main) {
+      if (op == Op::Joint && !kRuns && !main) {
         const int wide = p.f32 ? 32 : 64;      // columns of a piece
 #pragma unroll 1
         for (int c = (e >> 2) * wide; c < cols; c += 2 * wide) {
@@ -544,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
 #pragma unroll 1
-      for (int c = op == Op::Joint && !main ? cols : c_first; c < cols; c += 64) {
+      for (int c = op == Op::Joint && !kRuns && !main ? cols : c_first; c < cols; c += 64) {
         uint32_t v[32], a[16], b[16];
         if (reads) {
           const bool here = mbar_wait(in_bar, n_got & 1, p.wait_ns, abort_flag);
@@ -600,11 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) break;
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(tempty0 + acc * static_cast<uint32_t>(sizeof(uint64_t)));
-      acc ^= 1;
-      if (acc == 0) acc_phase ^= 1;
+      hand_back();
     }
     // what was asked for lands, and every store has been made, before the CTA exits
     if (n_got != n_asked) mbar_wait(in_bar, n_got & 1, kDrainNs, &sm->zero);
@@ -834,9 +907,9 @@ cudaError_t launch_beside(K kern, dim3 grid, int threads, size_t smem, int clust
   return cudaLaunchKernelEx(&cfg, kern, a, b...);
 }
 
-template <Op op>
+template <Op op, bool kRuns = false>
 cudaError_t launch(const Maps& maps, Args p, cudaStream_t st) {
-  auto kern = dense_gemm_kernel<op>;
+  auto kern = dense_gemm_kernel<op, kRuns>;
   static bool configured[kMaxDevices] = {};
   static int max_pairs[kMaxDevices] = {};       // clusters of two that fit at once
   const int d = current_device();
@@ -1112,12 +1185,14 @@ moe_status moe_gated_ffn_backward(const void* dy, const void* x, const void* w_g
     pj.dw_units = static_cast<int>(b.dw_units);
     pj.kb_rows = b.kb_rows;
     pj.f32 = f32;
+    pj.run = f32 ? kRunF32 : kRunBf16;
     pj.accumulate = accumulate_dw;
     // as many rounds as the gradient tiles that take as long as a unit of dx (the
     // gradients of 300 rows of 4096 x 14336: 253 us, with everyone in every round 304)
     pj.skip = pj.units > 0 ? (pj.per + kTileCost) / (b.kb_rows + kTileCost) : 0;
   }
-  if (launch<Op::Joint>(mj, pj, st) != cudaSuccess ||
+  const bool runs = dw_gate && b.kb_rows > pj.run;
+  if ((runs ? launch<Op::Joint, true>(mj, pj, st) : launch<Op::Joint>(mj, pj, st)) != cudaSuccess ||
       finish<Op::Joint>(pj, part, T, add, nullptr, dx, nullptr, nullptr, st) != cudaSuccess)
     return MOE_ERR_CUDA;
   return MOE_OK;

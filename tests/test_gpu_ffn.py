@@ -367,6 +367,68 @@ def test_ffn_two_streams_at_once():
     assert m.moe_get_error() == 0
 
 
+def _known_grads(T, H, F, positive, dtype, seed=0):
+    """The weight gradients beside their float64 values and the sums of their terms'
+    magnitudes, on inputs that leave no rounding before the sums: A_g = 1 through relu, so
+    that h = A_u; a selection as W_down, so that dh is columns of dy and dA_u = dh; dA_g =
+    bf16(dh A_u), of an exact product."""
+    g = torch.Generator(device="cuda").manual_seed(T + seed)
+
+    def rnd(*s):
+        v = torch.randn(s, generator=g, device="cuda")
+        return (v.abs() if positive else v).to(BF)
+
+    x, dy, up = rnd(T, H), rnd(T, H), rnd(T, F)
+    col = torch.arange(F, device="cuda") % H
+    wd = torch.zeros(F, H, dtype=BF, device="cuda")
+    wd[torch.arange(F), col] = 1.0
+    w = torch.zeros(H, F, dtype=BF, device="cuda")
+    args = (dy, x, w, w, wd, torch.ones_like(up), up)
+    got = m.moe_gated_ffn_backward(*args, act="relu", dw_dtype=dtype)
+    dh = dy[:, col]
+    pairs = dict(dw_down=(up, dy), dw_gate=(x, (dh.float() * up.float()).to(BF)), dw_up=(x, dh))
+    for key, (p, q) in pairs.items():
+        ref = p.double().t() @ q.double()
+        yield key, got[key], ref, p.double().abs().t() @ q.double().abs(), args
+
+
+@pytest.mark.parametrize("T,H,F", [(8192, 256, 392), (12001, 72, 264), (16384, 264, 128)])
+@pytest.mark.parametrize("positive", [True, False])
+def test_ffn_float_gradients_of_many_rows(T, H, F, positive):
+    """A run of 512 rows is 32 sums of 16 products and what is there; each may cut off 17
+    numbers below 2^-23 of the partial sum, on the average half of the last one: 32 * 17 / 2 *
+    2^-23 < 2^-14.9 of the terms. The additions of at most 32 runs round by 2^-24 each, 2^-19.
+    What is cut off is half of the most that it can be in the mean: 2^-15.9 of the sums. (One
+    accumulator over 8192 rows of positive numbers is off by 2^-14.7, over 16384 by 2^-13.5,
+    all of it in the mean.)"""
+    for key, got, ref, terms, args in _known_grads(T, H, F, positive, torch.float32):
+        err = got.double() - ref
+        assert (err.abs() <= (2.0 ** -14.9 + 2.0 ** -19) * terms).all(), key
+        mean = (err * ref.sign()).sum().abs()
+        assert mean <= (2.0 ** -15.9 + 2.0 ** -19) * (ref.abs() if positive else terms).sum(), key
+    # a second pass adds the same again: x + x is exact
+    one = m.moe_gated_ffn_backward(*args, act="relu", dw_dtype=torch.float32)
+    more = {k: one[k].clone() for k in ("dw_gate", "dw_up", "dw_down")}
+    m.moe_gated_ffn_backward(*args, act="relu", **more, accumulate_dw=True)
+    for key in more:
+        assert torch.equal(more[key], 2 * one[key]), key
+    assert m.moe_get_error() == 0
+
+
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+def test_ffn_gradients_of_a_million_rows(dtype):
+    """By runs of 512 rows as above (2^-14.9 of the terms), with 2^11 roundings of sums that
+    grow to the last one (2^-24 / 2 each on the average: 2^-14); in bf16 by runs of 8192 rows,
+    512 such sums (2^-10.9), 2^7 roundings, and half a step of bf16 (2^-8 of the result). One
+    accumulator over a million rows loses more than 2^-8."""
+    T = 1000003
+    for key, got, ref, terms, _ in _known_grads(T, 64, 40, True, dtype):
+        own = 2.0 ** -10.9 + 2.0 ** -18 if dtype == BF else 2.0 ** -14.9 + 2.0 ** -14
+        half = 2.0 ** -8 if dtype == BF else 2.0 ** -24
+        assert ((got.double() - ref).abs() <= half * ref.abs() + (1 + half) * own * terms).all(), key
+    assert m.moe_get_error() == 0
+
+
 def test_ffn_refusals():
     x, w, wd = (torch.zeros(s, dtype=BF, device="cuda") for s in ((4, 64), (64, 32), (32, 64)))
     with pytest.raises(m.MoeError, match="unsupported"):
