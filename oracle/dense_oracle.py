@@ -15,6 +15,13 @@ _erf = np.vectorize(math.erf, otypes=[np.float64])
 _erfc = np.vectorize(math.erfc, otypes=[np.float64])
 
 
+def _tanh_share(z, sign=1.0):
+    """(1 + sign tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 as a logistic function, which
+    keeps its tail where 1 + tanh would cancel."""
+    with np.errstate(over="ignore"):
+        return 1.0 / (1.0 + np.exp(-sign * math.sqrt(8.0 / math.pi) * (z + 0.044715 * z ** 3)))
+
+
 def act(z, kind):
     """act(z) in float64."""
     z = np.asarray(z, dtype=np.float64)
@@ -24,7 +31,7 @@ def act(z, kind):
     if kind == "gelu":
         return z * 0.5 * _erfc(-z / math.sqrt(2.0))
     if kind == "gelu_tanh":
-        return 0.5 * z * (1.0 + np.tanh(math.sqrt(2.0 / math.pi) * (z + 0.044715 * z ** 3)))
+        return z * _tanh_share(z)
     return np.maximum(z, 0.0)
 
 
@@ -38,9 +45,8 @@ def act_grad(z, kind):
     if kind == "gelu":
         return 0.5 * _erfc(-z / math.sqrt(2.0)) + z * np.exp(-0.5 * z * z) / math.sqrt(2 * math.pi)
     if kind == "gelu_tanh":
-        k = math.sqrt(2.0 / math.pi)
-        t = np.tanh(k * (z + 0.044715 * z ** 3))
-        return 0.5 * (1.0 + t) + 0.5 * z * (1.0 - t * t) * k * (1.0 + 3 * 0.044715 * z * z)
+        s, inner = _tanh_share(z), math.sqrt(8.0 / math.pi) * (1.0 + 3 * 0.044715 * z * z)
+        return s + z * s * _tanh_share(z, -1.0) * inner
     return (z > 0.0).astype(np.float64)
 
 

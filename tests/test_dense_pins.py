@@ -33,6 +33,28 @@ def test_activations_are_torchs(kind):
                                atol=1e-14)
 
 
+def test_gelu_tanh_far_out():
+    # (1 + tanh u) / 2 in 180 digits, where doubles would cancel: -9.5 gives 7.4e-34 of it
+    from decimal import Decimal, localcontext
+
+    with localcontext() as c:
+        c.prec = 180
+        k = (Decimal(2) / Decimal("3.14159265358979323846264338327950288419716939937510582097494459")).sqrt()
+
+        def f(z):
+            e = (2 * k * (z + Decimal("0.044715") * z ** 3)).exp()
+            return z * (1 + (e - 1) / (e + 1)) / 2
+
+        for v in (-12.0, -9.5, -6.0, -1.0, 0.5, 3.0, 9.0):
+            z, d = Decimal(v), Decimal("1e-30")
+            got = orc.act(np.array([v]), "gelu_tanh")[0], orc.act_grad(np.array([v]), "gelu_tanh")[0]
+            for have, want in zip(got, (f(z), (f(z + d) - f(z - d)) / (2 * d))):
+                assert abs(have - float(want)) <= 1e-11 * abs(float(want)), (v, have, float(want))
+    far = np.array([-3e4, -1e3, 1e3, 3e4])
+    assert orc.act(far, "gelu_tanh").tolist() == [0.0, 0.0, 1e3, 3e4]
+    assert orc.act_grad(far, "gelu_tanh").tolist() == [0.0, 0.0, 1.0, 1.0]
+
+
 def test_ffn_by_hand():
     # one token, two hidden units: A_g = (1, -2), A_u = (3, 5); relu keeps the first
     x, wg, wu = np.array([[1.0, 2.0]]), np.array([[1.0, 0.0], [0.0, -1.0]]), np.array([[1.0, 1.0],
