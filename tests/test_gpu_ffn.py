@@ -367,6 +367,52 @@ def test_ffn_two_streams_at_once():
     assert m.moe_get_error() == 0
 
 
+# by few rows, by tiles, and by tiles whose K is split
+@pytest.mark.parametrize("T,H", [(1, 176), (300, 176), (140, 1096)])
+@pytest.mark.parametrize("act", ACTS)
+def test_ffn_far_activations_in_each_form(act, T, H):
+    """Gates from -3e4 to 3e4 with unit matrices around them, so that y is h, dx is dA_g or
+    dA_u, and dW_down against rows of the unit matrix is h again; A_u = 1. Each is off by a
+    bf16 rounding (2^-8) beside the float formula's own error, 2^-14 of each of its terms: the
+    exponential's argument (up to 88, by four roundings of 2^-24) and its 2 + 1.2 * 88 ulps;
+    erfc's argument (by two, which erfc multiplies by up to 13^2) and a few ulps; a quotient of
+    two ulps. What is below 2^-118 may be cut to zero (a quotient by more than 2^126 is)."""
+    z = torch.cat([torch.linspace(-40, 40, 161), torch.tensor([-3e4, 3e4, 1e-30, 0.0, -0.0, -88.0,
+                                                               88.0, -1e3, 1e3])])
+    z = torch.cat([z, torch.zeros(H - z.numel())]).to(BF)
+    z64 = z.double().numpy()
+    eye, zero = torch.eye(H).to(BF), torch.zeros(H, H, dtype=BF)
+    x = torch.zeros(T, H, dtype=BF)
+    x[:, 0] = 1.0
+    wg, wu = zero.clone(), zero.clone()
+    wg[0], wu[0] = z, 1.0
+    got = m.moe_gated_ffn(dev(x), dev(wg), dev(wu), dev(eye), act=act, save_for_backward=True)
+    assert torch.equal(got["a_gate"].cpu(), z.expand(T, H)) and (got["a_up"] == 1).all()
+    f, d = orc.act(z64, act), orc.act_grad(z64, act)
+    slack = 2.0 ** -8 * np.abs(f) + 2.0 ** -14 * np.abs(f) + 2.0 ** -118
+
+    def holds(t, want, bound, what):
+        err = np.abs(_np(t) - want)
+        assert (err <= bound).all(), (what, z64[np.argwhere(err > bound)[0][-1]])
+
+    holds(got["y"], f, slack, "y")
+    one = torch.ones(T, H, dtype=BF)
+    kept = dict(a_gate=got["a_gate"], a_up=got["a_up"], act=act, weight_grads=False)
+    du = m.moe_gated_ffn_backward(dev(one), dev(x), dev(zero), dev(eye), dev(eye), **kept)["dx"]
+    holds(du, f, slack, "dA_u")
+    dg = m.moe_gated_ffn_backward(dev(one), dev(x), dev(eye), dev(zero), dev(eye), **kept)["dx"]
+    # act' is f / z and a second term that may cancel it
+    first = np.where(z64 == 0, 0.5, f / np.where(z64 == 0, 1.0, z64))
+    terms = np.abs(first) + np.abs(d - first)
+    holds(dg, d, 2.0 ** -8 * np.abs(d) + 2.0 ** -14 * terms + 2.0 ** -118, "dA_g")
+    rows = torch.zeros(T, H, dtype=BF)
+    rows[torch.arange(min(T, H)), torch.arange(min(T, H))] = 1.0
+    kept.update(weight_grads=True, dw_dtype=torch.float32)
+    back = m.moe_gated_ffn_backward(dev(rows), dev(x), dev(zero), dev(zero), dev(eye), **kept)
+    holds(back["dw_down"].t()[:min(T, H)], f, slack, "h")
+    assert m.moe_get_error() == 0
+
+
 def _known_grads(T, H, F, positive, dtype, seed=0):
     """The weight gradients beside their float64 values and the sums of their terms'
     magnitudes, on inputs that leave no rounding before the sums: A_g = 1 through relu, so
