@@ -2,8 +2,8 @@
 
 Small integers: every sum is an integer below 2^24 (and v one that two bf16
 numbers hold), so v, da, db and the roundings of out and dx have to be equal.
-Gaussian values: v is a float sum (2^-23 of its terms a chain of 64, float
-additions beyond); out and dx lie within 2^-8 of themselves and 2^-15 of the sum
+Gaussian values: v is a float sum (chains of 128 terms, float additions
+beyond); out and dx lie within 2^-8 of themselves and 2^-15 of the sum
 of their terms (v to 16 bits, the sums' own roundings); da and db within 2^-15
 of theirs."""
 import numpy as np
@@ -378,6 +378,90 @@ def test_lora_on_another_stream_and_in_a_graph(T):
     again = m.moe_lora(**v, adapter_ids=live, scales=scales, base=base)
     assert torch.equal(f["out"], again["out"])
     assert m.moe_get_error() == 0
+
+
+@pytest.mark.parametrize("T,H,N,n,r", [(20, 64, 72, 3, 16), (200, 264, 280, 3, 32),
+                                       (150, 200, 192, 70, 13), (300, 328, 392, 2, 64),
+                                       (300, 328, 392, 2, 128)])
+def test_lora_gradients_hold_24_bits(T, H, N, n, r):
+    """v and dv of 24 bits, each alone in its sum, come through as they are; two bf16 numbers
+    would hold less than 18 of them. dv = B dy has three terms, digits below 2^7 times 2^16,
+    2^8 and 1; further columns of dy, and those of x, are one a row, so that da[:, t] = dv_t
+    and db[:, 8 + t] = v_t for adapter ids[t]."""
+    rng = np.random.default_rng(T + r)
+    ids, t = rng.integers(0, n, T), np.arange(T)
+    x, dy = np.zeros((T, H)), np.zeros((T, N))
+    x[t, t], dy[t, 8 + t] = 1.0, 1.0
+    dy[:, :3] = rng.integers(-127, 128, (T, 3)) * 2.0 ** np.array([16, 8, 0])
+    a, b = np.zeros((n, r, H)), np.zeros((n, r, N))
+    b[:, :, :3] = rng.choice([-1.0, 1.0], (n, r, 3))
+    dv = np.einsum("tc,tjc->tj", dy[:, :3], b[ids][:, :, :3])
+    assert np.abs(dv).max() < 2 ** 23 and (np.abs(dv) % 2 == 1).any()
+    v = torch.from_numpy(rng.standard_normal((T, r)).astype(np.float32)).cuda()
+    scales = torch.tensor(rng.choice([0.5, 1.0, -2.0], n).astype(np.float32)).cuda()
+
+    def put(q):
+        p = torch.from_numpy(q.astype(np.float32)).to(BF).cuda()
+        assert np.array_equal(_np(p), q)
+        return p
+
+    got = m.moe_lora_backward(put(dy), put(x), v, put(a), put(b),
+                              torch.from_numpy(ids.astype(np.int32)).cuda(), scales=scales)
+    assert m.moe_get_error() == 0
+    s = _np(scales)[ids][:, None]
+    da, db = np.zeros((n, r, H)), np.zeros((n, r, N))
+    da[ids[t], :, t] = (s * dv)[t]
+    db[ids[t], :, 8 + t] = (s * _np(v))[t]
+    assert np.array_equal(_np(got["da"]), da)
+    assert np.array_equal(_np(got["db"])[:, :, 8:], db[:, :, 8:])
+
+
+# One accumulator over the whole of these sums, 1024 additions of positive numbers, ends
+# 2^-13.5 too small, all of it in the mean. A run of 128 terms is 8 additions of 16 products
+# to what is there, each of which may cut off 17 numbers below 2^-23 of the partial sum, on
+# the average half of the last one: 8 * 17 / 2 * 2^-23 < 2^-16.9. The 160 runs at most are
+# added up in float, 2^-24 of sums that are half of the last one on the average: 2^-17.6.
+# What is cut off is half of that in the mean. Together 2^-16.2, in the mean 2^-16.8.
+SUM, MEAN = 2.0 ** -16.2, 2.0 ** -16.8
+
+
+def _holds(got, ref, limit, mean, what):
+    err = got.double() - ref
+    assert (err.abs() <= limit * ref).all(), (what, float((err.abs() / ref).max()))
+    assert err.sum().abs() <= mean * ref.sum(), (what, float(err.sum() / ref.sum()))
+
+
+def _positive(*shape, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(sum(shape) + seed)
+    return torch.randn(shape, generator=g, device="cuda").abs().to(BF)
+
+
+@pytest.mark.parametrize("T,H,r", [(300, 16384, 16), (300, 16392, 30), (200, 16384, 64),
+                                   (400, 16384, 128)])
+def test_lora_long_sums_of_v(T, H, r):
+    x, a, b = _positive(T, H), _positive(2, r, H), _positive(2, r, 64)
+    ids = (torch.arange(T, device="cuda") % 2).to(torch.int32)
+    got = m.moe_lora(x, a, b, ids)
+    assert m.moe_get_error() == 0
+    for i in range(2):
+        _holds(got["v"][ids == i], x[ids == i].double() @ a[i].double().t(), SUM, MEAN, "v")
+
+
+@pytest.mark.parametrize("T,H,N,r", [(16384, 64, 72, 16), (20000, 72, 264, 32),
+                                     (16400, 136, 64, 50), (16384, 64, 64, 128)])
+def test_lora_long_sums_of_gradients(T, H, N, r):
+    # runs of rows and single rows; dv = B dy is itself such a sum, of at most 264 terms
+    x, a, dy, b = _positive(T, H), _positive(1, r, H), _positive(T, N), _positive(1, r, N)
+    v = torch.rand(T, r, generator=torch.Generator(device="cuda").manual_seed(T), device="cuda")
+    some = torch.zeros(T, dtype=torch.int32, device="cuda")
+    some[::9] = -1
+    for ids in (torch.zeros_like(some), some):
+        got = m.moe_lora_backward(dy, x, v, a, b, ids)
+        assert m.moe_get_error() == 0
+        on = ids == 0
+        X, D, V = x[on].double(), dy[on].double(), v[on].double()
+        _holds(got["db"][0], V.t() @ D, SUM, MEAN, "db")
+        _holds(got["da"][0], (D @ b[0].double().t()).t() @ X, 2 * SUM, 2 * MEAN, "da")
 
 
 def test_lora_refusals():
