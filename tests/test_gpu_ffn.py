@@ -413,6 +413,58 @@ def test_ffn_far_activations_in_each_form(act, T, H):
     assert m.moe_get_error() == 0
 
 
+# past the few rows: tiles of one part of K, and of several; columns that end inside a piece
+TILED = [(300, 136, 72), (200, 136, 4104), (140, 1096, 1096), (513, 1032, 1544)]
+
+
+@pytest.mark.parametrize("T,H,F", TILED)
+def test_ffn_in_place_by_tiles(T, H, F):
+    v, a, dy = _ints(T, H, F, T + 5)
+    ref = orc.gated_ffn(**v, kind="relu", add=a)
+    d = {k: dev(_bf(t)) for k, t in v.items()}
+    y = dev(_bf(a))
+    assert m.moe_gated_ffn(**d, act="relu", add=y, y=y)["y"] is y
+    _equal(y, ref["y"], "y in place")
+    kept = dict(a_gate=dev(_bf(ref["a_gate"])), a_up=dev(_bf(ref["a_up"])), act="relu")
+    want = orc.gated_ffn_backward(dy, **v, a_gate=ref["a_gate"], a_up=ref["a_up"], kind="relu",
+                                  add=a)
+    for weights in (True, False):
+        dx = dev(_bf(a))
+        got = m.moe_gated_ffn_backward(dev(_bf(dy)), **d, **kept, add=dx, dx=dx,
+                                       weight_grads=weights)
+        assert got["dx"] is dx
+        _equal(dx, want["dx"], "dx in place")
+        if weights:
+            for key in ("dw_gate", "dw_up", "dw_down"):
+                _equal(got[key], want[key], key)
+    assert m.moe_get_error() == 0
+
+
+@pytest.mark.parametrize("T,H,F", TILED)
+def test_ffn_rows_keep_to_themselves_by_tiles(T, H, F):
+    v, add, dy = _gauss(T, H, F, 1)
+    w = {k: dev(t) for k, t in v.items()}
+    add = dev(add)
+    clean = m.moe_gated_ffn(**w, add=add, save_for_backward=True)
+    bad = v["x"].clone()
+    bad[13, 5], bad[44, 7], bad[T - 1] = float("nan"), float("inf"), float("nan")
+    got = m.moe_gated_ffn(**dict(w, x=dev(bad)), add=add, save_for_backward=True)
+    rest = [t for t in range(T) if t not in (13, 44, T - 1)]
+    for key in ("y", "a_gate", "a_up"):
+        assert torch.equal(got[key][rest], clean[key][rest]), key
+        assert got[key][13].isnan().all() and got[key][T - 1].isnan().all()
+        assert not got[key][44].isfinite().all()
+    bad = dy.clone()
+    bad[13], bad[T - 1] = float("nan"), float("inf")
+    for weights in (True, False):
+        a, b = (m.moe_gated_ffn_backward(dev(t), **w, a_gate=clean["a_gate"], a_up=clean["a_up"],
+                                         add=add, weight_grads=weights)["dx"] for t in (dy, bad))
+        rest = [t for t in range(T) if t not in (13, T - 1)]
+        assert torch.equal(a[rest], b[rest])
+        assert b[13].isnan().all() and not b[T - 1].isfinite().all()
+    assert m.moe_get_error() == 0
+
+
 def _known_grads(T, H, F, positive, dtype, seed=0):
     """The weight gradients beside their float64 values and the sums of their terms'
     magnitudes, on inputs that leave no rounding before the sums: A_g = 1 through relu, so
