@@ -413,6 +413,28 @@ def test_ffn_far_activations_in_each_form(act, T, H):
     assert m.moe_get_error() == 0
 
 
+# shapes whose lists of tiles end in a way that SHAPES do not: units of dx on some of the
+# clusters and gradient tiles past the rounds that those stay out of (the first three),
+# several units a cluster with several column tiles (the last)
+@pytest.mark.parametrize("T,H,F", [(140, 1032, 2056), (300, 1000, 2728), (1500, 520, 1544),
+                                   (4700, 1096, 648)])
+def test_ffn_walks_over_tiles(T, H, F):
+    v, a, dy = _ints(T, H, F, T + F)
+    ref = orc.gated_ffn(**v, kind="relu", add=a)
+    d, add, got = _forward(v, a, "relu", save_for_backward=True)
+    for key in ("y", "a_gate", "a_up"):
+        _equal(got[key], ref[key], key)
+    want = orc.gated_ffn_backward(dy, **v, a_gate=ref["a_gate"], a_up=ref["a_up"], kind="relu",
+                                  add=a)
+    for dt in (BF, torch.float32):
+        back = m.moe_gated_ffn_backward(dev(_bf(dy)), **d, a_gate=got["a_gate"], a_up=got["a_up"],
+                                        act="relu", add=add, dw_dtype=dt)
+        for key in back:
+            assert np.abs(want[key]).max() < 2 ** 24
+            _equal(back[key], want[key], key)
+    assert m.moe_get_error() == 0
+
+
 # past the few rows: tiles of one part of K, and of several; columns that end inside a piece
 TILED = [(300, 136, 72), (200, 136, 4104), (140, 1096, 1096), (513, 1032, 1544)]
 
