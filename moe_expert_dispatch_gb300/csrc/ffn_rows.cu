@@ -319,6 +319,8 @@ __global__ void __launch_bounds__(kThreads)
 
 constexpr size_t kSmemBytes = 1024 + kRingBytes + sizeof(Smem);
 static_assert(2 * (kSmemBytes + 1024) <= 233472, "two CTAs an SM");
+static_assert(kFewRows * 128 * sizeof(float) <= kRingBytes, "the sums take the ring's place");
+static_assert(kFewRows <= 128, "columns of tensor memory");
 
 // CTAs to a cluster: as many as two an SM take, each with a k-block at least.
 int pick_split(int tiles, int kb) {
