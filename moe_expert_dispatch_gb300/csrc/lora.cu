@@ -1511,13 +1511,20 @@ moe_status check_sizes(int64_t T, int H, int N, int n, int r) {
 // Whether one cluster takes each row, without a plan: every row then reads its adapter
 // whole, which the rows of a unit share otherwise, but a unit costs as much for one row as
 // for 128. In units of 2 ns at 4096 x 4096 a row takes 25 + r, the two launches 6000 + 100
-// r and a unit 135, and there is one to an adapter at least. Measured by clusters and by
-// units: r = 16 and 32 adapters, 128 rows 11 and 22 us, 256 20 and 23, 512 35 and 23; 128
-// adapters, 512 rows 36 and 46, 1024 68 and 48; 512 adapters, 1024 rows 76 and 146, 4096
-// 289 and 166; r = 64 and 32 adapters, 128 rows 20 and 34, 256 36 and 34; and of 4096 x
-// 14336 with r = 16, 128 adapters, 512 rows 52 and 87, 1024 98 and 93.
+// r and a unit 135, one at least to an adapter in use. How many are is known on the device
+// alone: all of up to 32 are taken to be, and of more some half. By clusters and by units,
+// with every adapter in use: r = 16 and 32 adapters, 128 rows 11 and 22 us, 256 20 and 23,
+// 512 35 and 23; 128 adapters, 512 rows 36 and 47, 1024 68 and 47; 512 adapters, 512 rows 41
+// and 160, 1024 75 and 145, 1800 129 and 161; 1024 adapters, 1800 rows 131 and 280; r = 64
+// and 32 adapters, 128 rows 20 and 34, 256 36 and 34; of 4096 x 14336 with r = 16, 128
+// adapters, 512 rows 52 and 87, 1024 98 and 93. With one or 16 in use, r = 16: of 16, 256
+// rows 19 and 15 to 19; of 256, 512 rows 36 and 41 to 46, 1000 66 and 41 to 47; of 512, 1000
+// rows 66 and 45 to 54, 1800 116 and 51 to 55; of 1024, 1800 rows 116 and 89 to 104, 4096
+// 278 and 95 to 99; r = 64, of 512, 512 rows 66 and 52 to 58, 1000 124 and 49 to 60. (Every
+// adapter taken to be in use sent 1800 rows of one among 512 to the clusters.)
 bool few_rows(int64_t T, int n, int r) {
-  return T * (25 + r) <= 6000 + 100 * r + 135 * (T < n ? T : n);
+  const int64_t likely = n <= 32 ? n : 16 + n / 2;
+  return T * (25 + r) <= 6000 + 100 * r + 135 * (T < likely ? T : likely);
 }
 
 // What the backward has in its workspace.

@@ -172,6 +172,18 @@ INV, UNS, WS = 1, 2, 4
 BIG = 1 << 40
 
 
+def test_lora_takes_rows_one_by_one_as_measured(m):
+    # no workspace: a cluster a row. With every slot in use the first of each pair is faster
+    # so; the second is faster by units when one or 16 of the slots are in use
+    size = m._lib.moe_lora_workspace_size
+    for T, n, r in ((128, 32, 16), (256, 32, 16), (512, 512, 16), (1000, 512, 16), (64, 1024, 64),
+                    (1800, 1024, 16)):
+        assert size(T, n, r) == 0, (T, n, r)
+    for T, n, r in ((512, 16, 16), (512, 32, 16), (1000, 256, 16), (1800, 512, 16), (4096, 1024, 16),
+                    (1000, 512, 64), (600, 256, 64)):
+        assert size(T, n, r) > 0, (T, n, r)
+
+
 def test_dense_workspace_sizes(m):
     L = m._lib
     assert L.moe_gated_ffn_workspace_size(3, 64, 40) == 256

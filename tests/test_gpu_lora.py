@@ -146,6 +146,28 @@ def test_lora_many_units(T, H, N, n, r, kind):
     assert m.moe_get_error() == 0
 
 
+# slots of which one or a few are in use, on both sides of where units take the rows
+@pytest.mark.parametrize("T,H,N,n,r,used", [(40, 72, 64, 1024, 16, 1), (300, 200, 136, 512, 8, 3),
+                                            (1000, 136, 72, 256, 16, 1), (1900, 64, 200, 512, 16, 16),
+                                            (900, 264, 72, 1024, 64, 2), (1, 64, 64, 1000, 128, 1)])
+def test_lora_slots_that_are_not_in_use(T, H, N, n, r, used):
+    v, _, scales, base, _, dy = _draw(T, H, N, n, r, "mixed", T + r, True)
+    rng = np.random.default_rng(n)
+    rows = rng.choice(rng.choice(n, used, replace=False), T)
+    ids = torch.from_numpy(rows.astype(np.int32)).cuda()
+    n64, s64 = {k: _np(t) for k, t in v.items()}, _np(scales)
+    got = m.moe_lora(**v, adapter_ids=ids, scales=scales, base=base)
+    ref, rv = orc.lora(**n64, ids=rows, scales=s64, base=_np(base))
+    assert np.array_equal(_np(got["v"]), rv)
+    assert torch.equal(got["out"].cpu(), torch.from_numpy(ref).float().to(BF))
+    back = m.moe_lora_backward(dy, v["x"], got["v"], v["a"], v["b"], ids, scales=scales)
+    want = orc.lora_backward(_np(dy), n64["x"], rv, n64["a"], n64["b"], rows, s64)
+    assert torch.equal(back["dx"].cpu(), torch.from_numpy(want["dx"]).float().to(BF))
+    for key in ("da", "db"):
+        assert np.abs(want[key]).max() < 2 ** 24 and np.array_equal(_np(back[key]), want[key]), key
+    assert m.moe_get_error() == 0
+
+
 @pytest.mark.parametrize("T,H,N,n,r,kind", [(3, 1000, 264, 4, 16, "mixed"),
                                             (100, 512, 328, 6, 24, "mixed"),
                                             (400, 1032, 200, 3, 64, "runs"),
