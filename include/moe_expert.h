@@ -812,7 +812,9 @@ moe_status moe_lora_plan(const int32_t* adapter_ids, int64_t T, int n, int32_t* 
                          int32_t* offsets, void* stream);
 
 /* ------------------------------------------------------------------------
- * moe_lora - low-rank adapters beside a shared projection: with a = the
+ * moe_lora - low-rank adapters beside a shared projection, whose result the
+ * caller brings as base (moe_gated_ffn applies its activation inside, so that
+ * adapters go beside the whole block, not beside W_gate or W_up): with a = the
  * row's adapter,
  *   v_t = A_a x_t (float),   out_t = bf16(base_t + s_a B_a^T v_t)
  * A row without an adapter has v_t = 0 and out_t = base_t. v enters the second
@@ -831,7 +833,8 @@ moe_status moe_lora_plan(const int32_t* adapter_ids, int64_t T, int n, int32_t* 
  *  out     bf16 [T, N]   out; may be base itself
  *  v       float [T, r]  out: what the backward needs
  *  workspace >= moe_lora_workspace_size(T, n, r) bytes, 16-byte aligned; 0 bytes,
- *          and NULL allowed, for the few rows that need none
+ *          and NULL allowed, for the few rows that need none. It has room for
+ *          T / 128 + n units of 16 to 64 KB, whether adapters have rows or not
  * 1 <= r <= 128, H % 8 == 0, N % 8 == 0 and T <= 2^27 (else MOE_ERR_UNSUPPORTED),
  * 1 <= n <= 1024. Pointers start on 16 bytes (v and the int32 arrays on
  * 4); out and v overlap nothing else of the call (out: base alone, and then as a
@@ -857,7 +860,9 @@ moe_status moe_lora(const void* x, const void* a, const void* b, const int32_t* 
  *  dx      bf16 [T, H]   out; may be base itself
  *  da      float [n, r, H], db  float [n, r, N]   out; added to what is there
  *          when accumulate. An adapter without rows gets 0 (or is left)
- *  workspace >= moe_lora_backward_workspace_size(T, n, r) bytes, 16-byte aligned
+ *  workspace >= moe_lora_backward_workspace_size(T, n, r) bytes, 16-byte aligned:
+ *          twice T / 128 + n units of 16 to 96 KB (200 MB for n = 1024, r = 128,
+ *          however few the rows), and 5 to 20 MB of sums
  * Limits and overlaps as moe_lora (dx is neither dy nor x: MOE_ERR_INVALID_ARG).
  * T = 0 writes zero gradients (or leaves them).
  * ------------------------------------------------------------------------ */
