@@ -487,6 +487,35 @@ def test_ffn_rows_keep_to_themselves_by_tiles(T, H, F):
     assert m.moe_get_error() == 0
 
 
+# runs of rows that end with a single block of 64, or one row, in either type
+@pytest.mark.parametrize("T,H,F", [(8193, 72, 136), (16448, 8, 296), (577, 264, 72)])
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+def test_ffn_gradients_of_runs_and_a_rest(T, H, F, dtype):
+    v, _, dy = _ints(T, H, F, T, False)
+    fwd = orc.gated_ffn(**v, kind="relu")
+    want = orc.gated_ffn_backward(dy, **v, a_gate=fwd["a_gate"], a_up=fwd["a_up"], kind="relu")
+    d = {k: dev(_bf(t)) for k, t in v.items()}
+    args = dict(a_gate=dev(_bf(fwd["a_gate"])), a_up=dev(_bf(fwd["a_up"])), act="relu")
+    got = m.moe_gated_ffn_backward(dev(_bf(dy)), **d, **args, dw_dtype=dtype)
+    for key in got:
+        assert np.abs(want[key]).max() < 2 ** 24
+        _equal(got[key], want[key], key)
+    # the same in a graph, beside a call on another stream
+    s, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    dyb = dev(_bf(dy))
+    with torch.cuda.graph(g):
+        again = m.moe_gated_ffn_backward(dyb, **d, **args, dw_dtype=dtype)
+    for t in again.values():
+        t.zero_()
+    torch.cuda.synchronize()
+    g.replay()
+    beside = m.moe_gated_ffn_backward(dyb, **d, **args, dw_dtype=dtype, stream=s)
+    torch.cuda.synchronize()
+    for key in got:
+        assert torch.equal(again[key], got[key]) and torch.equal(beside[key], got[key]), key
+    assert m.moe_get_error() == 0
+
+
 def _known_grads(T, H, F, positive, dtype, seed=0):
     """The weight gradients beside their float64 values and the sums of their terms'
     magnitudes, on inputs that leave no rounding before the sums: A_g = 1 through relu, so
